@@ -24,6 +24,11 @@ __all__ = [
     "ssd_backward_workspace_bytes", "ssd_chunked_backward", "SSDBackwardPlan",
     "ssd_trapezoidal_backward", "ssd_trapezoidal_backward_workspace_bytes",
     "workspace_status", "wait_selftest", "STATUS", "VARIANTS",
+    "gated_recurrence_forward", "gated_recurrence_backward", "gated_recurrence_step",
+    "GatedRecurrencePlan", "GatedRecurrenceBackwardPlan", "GatedRecurrenceStepPlan",
+    "GATED_RECURRENCE_CHUNK", "group_norm_forward", "group_norm_backward", "GroupNormPlan",
+    "GroupNormBackwardPlan", "embedding_forward", "embedding_backward", "EmbeddingPlan",
+    "EmbeddingBackwardPlan",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -114,6 +119,7 @@ def load_library(path: Optional[str] = None):
     lib.ssd_wait_selftest.argtypes = [_VP, ctypes.c_size_t, ctypes.c_uint64, _VP]
     lib.ssd_abi_version.restype = ctypes.c_int32
     lib.ssd_abi_version.argtypes = []
+    lm_ops._declare(lib)
     if path is None:
         _LIB = lib
     return lib
@@ -624,3 +630,11 @@ def workspace_status(workspace: torch.Tensor, stream=None):
     st = load_library().ssd_workspace_status(_ptr(workspace), _stream_handle(stream),
                                              ctypes.byref(detail))
     return STATUS.get(int(st), str(st)), int(detail.value)
+
+
+from . import lm_ops  # noqa: E402  (uses the helpers above)
+from .lm_ops import (  # noqa: E402,F401
+    GATED_RECURRENCE_CHUNK, EmbeddingBackwardPlan, EmbeddingPlan, GatedRecurrenceBackwardPlan,
+    GatedRecurrencePlan, GatedRecurrenceStepPlan, GroupNormBackwardPlan, GroupNormPlan,
+    embedding_backward, embedding_forward, gated_recurrence_backward, gated_recurrence_forward,
+    gated_recurrence_step, group_norm_backward, group_norm_forward)

@@ -375,6 +375,144 @@ ssd_status selective_scan_forward_noalloc(const float* u, const float* delta, co
                                           float* y, int64_t batch, int64_t seqlen,
                                           int64_t d_model, int64_t d_state, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Operators around a scan in a recurrent language model: an elementwise gated recurrence, a
+ * channels-last group norm with an activation, and the token embedding.
+ * Activations are io_dtype (f32 or bf16), parameters, states, statistics and the gradients of
+ * parameters and states are f32.  Where a shape carries strides, they count elements and the last
+ * axis is contiguous, so an input can be a slice of a wider projection; outputs are contiguous and
+ * must not overlap inputs.  Pointers need only their element's alignment unless stated (rows
+ * that start on 16-byte boundaries take wider loads).  A size of zero where one is allowed
+ * launches only what defines the outputs.  All sums and states are held in fp32.
+ * ------------------------------------------------------------------------------------------ */
+
+/* Steps between the states that gated_recurrence_forward keeps for the backward pass. */
+#define GATED_RECURRENCE_CHUNK 64
+
+typedef struct gated_recurrence_shape {
+  int64_t batch;            /* b >= 0 */
+  int64_t seqlen;           /* T >= 0 */
+  int64_t d_model;          /* D >= 1 */
+  int64_t x_stride[2];      /* of the batch axis and the step axis, >= 0 */
+  int64_t gate_a_stride[2];
+  int64_t gate_x_stride[2];
+  int64_t dy_stride[2];     /* gated_recurrence_backward only */
+  float c;                  /* scale of the decay exponent, > 0 and finite */
+  int32_t io_dtype;         /* ssd_dtype of x, the gates, y, dy and their gradients */
+} gated_recurrence_shape;
+
+/*
+ * Bytes of device workspace (256-byte aligned, the first 256 bytes zero before the first call) that
+ * gated_recurrence_forward (backward = 0) or gated_recurrence_backward (backward = 1) needs; 0 if
+ * the shape is invalid or not supported.
+ */
+size_t gated_recurrence_workspace_bytes(const gated_recurrence_shape* shape, int32_t backward);
+
+/*
+ * Gated linear recurrence, elementwise per channel d:
+ *   r = sigmoid(gate_a[b,t,d]);  i = sigmoid(gate_x[b,t,d]);  a = exp(-c softplus(decay[d]) r)
+ *   h_t = a h_{t-1} + sqrt(1 - a^2) i x[b,t,d];   y[b,t,d] = h_t;   h_{-1} = init_state[b,d]
+ * x, gate_a, gate_x [batch, seqlen, d_model] strided, y contiguous, all io_dtype; decay [d_model],
+ * init_state (NULL = zeros), final_state (NULL = not written) [batch, d_model] f32.
+ * states: NULL, or f32 [batch, ceil(seqlen / GATED_RECURRENCE_CHUNK), d_model] that receives the
+ * state before steps 0, 64, 128, ... for gated_recurrence_backward.  y may be NULL.
+ * 1 - a^2 is formed without cancellation, so channels that hardly decay keep their precision.
+ * Asynchronous on `stream`; INVALID_ARG / UNSUPPORTED / WORKSPACE leave every output untouched.
+ */
+ssd_status gated_recurrence_forward(const gated_recurrence_shape* shape, const void* x,
+                                    const void* gate_a, const void* gate_x, const float* decay,
+                                    const float* init_state, void* y, float* final_state,
+                                    float* states, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/*
+ * Reverse mode of gated_recurrence_forward for the loss <dy, y> + <dfinal, final_state>:
+ *   dx, dgate_a, dgate_x [batch, seqlen, d_model] io_dtype contiguous, ddecay [d_model] f32 (summed
+ *   over batch and steps in a fixed order: the same bits every run), dinit [batch, d_model] f32
+ *   (may be NULL).
+ * dy strided io_dtype, dfinal [batch, d_model] f32 (NULL = zero).  states: what the forward kept,
+ * or NULL (the call then recomputes them in its workspace, one more pass over x and the gates).
+ * Where a gate is so closed that 1 - a^2 is zero in fp32, the gradients through it are zero (their
+ * limit).
+ */
+ssd_status gated_recurrence_backward(const gated_recurrence_shape* shape, const void* x,
+                                     const void* gate_a, const void* gate_x, const float* decay,
+                                     const float* init_state, const float* states, const void* dy,
+                                     const float* dfinal, void* dx, void* dgate_a, void* dgate_x,
+                                     float* ddecay, float* dinit, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/*
+ * One step of the recurrence for every sequence of a batch (serving): shape->seqlen must be 1 and
+ * the step strides are ignored.  state [batch, d_model] f32 is read (NULL = zeros), state_out
+ * receives the new state and may be the same buffer as state.  y [batch, d_model] io_dtype.
+ */
+ssd_status gated_recurrence_step(const gated_recurrence_shape* shape, const void* x,
+                                 const void* gate_a, const void* gate_x, const float* decay,
+                                 const float* state, void* y, float* state_out, void* stream);
+
+typedef enum ssd_activation { SSD_ACT_NONE = 0, SSD_ACT_SILU = 1 } ssd_activation;
+
+typedef struct group_norm_shape {
+  int64_t batch;        /* N >= 0: samples with statistics of their own              */
+  int64_t rows;         /* S >= 0: positions of a sample (1 for a norm per token)     */
+  int64_t channels;     /* C >= 1                                                    */
+  int64_t groups;       /* G >= 1, divides C                                         */
+  int64_t x_stride[2];  /* of the sample axis and the position axis, >= 0            */
+  int64_t dy_stride[2]; /* group_norm_backward only                                  */
+  float eps;            /* >= 0 and finite                                           */
+  int32_t activation;   /* ssd_activation                                            */
+  int32_t io_dtype;     /* ssd_dtype of x, y, dy and dx                              */
+} group_norm_shape;
+
+/* Bytes of device workspace of group_norm_forward (backward = 0) or group_norm_backward
+ * (backward = 1), under the rules of gated_recurrence_workspace_bytes. */
+size_t group_norm_workspace_bytes(const group_norm_shape* shape, int32_t backward);
+
+/*
+ * Group norm with an activation, channels last: over the rows * channels / groups values of sample
+ * n and group g, mean and (biased) variance, rstd = 1 / sqrt(var + eps), and
+ *   y[n,s,c] = act((x[n,s,c] - mean) rstd weight[c] + bias[c])
+ * x [batch, rows, channels] strided, y contiguous, io_dtype; weight (NULL = ones), bias (NULL =
+ * zeros) [channels] f32; mean, rstd [batch, groups] f32 (both or neither NULL).  The variance is
+ * summed around the mean, not as a difference of squares.
+ */
+ssd_status group_norm_forward(const group_norm_shape* shape, const void* x, const float* weight,
+                              const float* bias, void* y, float* mean, float* rstd,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Reverse mode of group_norm_forward for <dy, y>: dx io_dtype contiguous; dweight, dbias [channels]
+ * f32 (either may be NULL; summed in a fixed order).  mean and rstd are what the forward wrote.
+ */
+ssd_status group_norm_backward(const group_norm_shape* shape, const void* x, const void* dy,
+                               const float* mean, const float* rstd, const float* weight,
+                               const float* bias, void* dx, float* dweight, float* dbias,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Token embedding: out[i,:] = scale * table[ids[i],:] for i < n; an id outside [0, vocab) is padding
+ * and gives a row of zeros.  ids int32 or int64 (ids_bits 32 or 64), table [vocab, dim] and out
+ * [n, dim] io_dtype contiguous; the product is formed in fp32 and rounded once.
+ */
+ssd_status embedding_forward(const void* ids, int32_t ids_bits, int64_t n, const void* table,
+                             int64_t vocab, int64_t dim, int32_t io_dtype, float scale, void* out,
+                             void* stream);
+
+/* Bytes of device workspace of embedding_backward (0 if the sizes are invalid or unsupported). */
+size_t embedding_backward_workspace_bytes(int64_t n, int64_t vocab, int64_t dim);
+
+/*
+ * Gradient of embedding_forward with respect to its table: every row of dtable [vocab, dim] f32 is
+ * written, dtable[v,:] = scale * sum over the tokens with id v of dout[i,:] (zeros for an id that
+ * does not occur; padding ids contribute nothing).  Tokens are sorted by id on the device and
+ * summed in an order that depends only on the ids, so the same inputs give the same bits.
+ */
+ssd_status embedding_backward(const void* ids, int32_t ids_bits, int64_t n, const void* dout,
+                              int64_t vocab, int64_t dim, int32_t io_dtype, float scale,
+                              float* dtable, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
 /*
  * Reads (and clears) the device-side error word of a workspace after synchronising `stream`.
  * Returns SSD_OK, or SSD_ERR_TIMEOUT if a device wait of an earlier call on this workspace gave
