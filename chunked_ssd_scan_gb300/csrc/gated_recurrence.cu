@@ -7,7 +7,15 @@
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
+#include <initializer_list>
+#include <map>
+#include <mutex>
+#include <utility>
+
 #include "common.cuh"
+#include "fp_helpers.cuh"
+#include "lookback.cuh"
 
 namespace ssd {
 namespace {
@@ -22,6 +30,11 @@ struct RecParams {
   int64_t batch, T, D, nch;
   int64_t xs[2], as[2], gs[2], ds[2];
   float c;
+  int64_t ntile;     // tiles in time
+  uint32_t tiles;    // tiles in all
+  uint32_t* ticket;  // NULL where the order of the tiles does not matter
+  uint64_t* words;
+  WsHeader* hdr;
 };
 
 __device__ __forceinline__ float softplus(float d) { return fmaxf(d, 0.f) + log1pf(expf(-fabsf(d))); }
@@ -43,25 +56,320 @@ __device__ __forceinline__ Gates gates(float ga, float gx, float rate) {
 }
 __device__ __forceinline__ float decayed(const Gates& g, float h, float b) { return h + fmaf(g.w, h, b); }
 
-// One thread per (sequence, channel), the steps in order.
-template <typename T>
-__global__ void rec_forward_kernel(RecParams p) {
-  const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (id >= p.batch * p.D) return;
-  const int64_t b = id / p.D, d = id % p.D;
-  const float rate = p.c * softplus(p.decay[d]);
-  const T* x = static_cast<const T*>(p.x) + b * p.xs[0] + d;
-  const T* ga = static_cast<const T*>(p.ga) + b * p.as[0] + d;
-  const T* gx = static_cast<const T*>(p.gx) + b * p.gs[0] + d;
-  T* y = p.y ? static_cast<T*>(p.y) + b * p.T * p.D + d : nullptr;
-  float h = p.init ? p.init[id] : 0.f;
-  for (int64_t t = 0; t < p.T; ++t) {
-    if (p.states_out && t % kChunk == 0) p.states_out[(b * p.nch + t / kChunk) * p.D + d] = h;
-    const Gates g = gates(ld_f32(ga + t * p.as[1]), ld_f32(gx + t * p.gs[1]), rate);
-    h = decayed(g, h, g.m * g.i * ld_f32(x + t * p.xs[1]));
-    if (y) st_from_f32(y + t * p.D, h);
+// ------------------------------------------------------------------------------------------------
+// Forward.
+//
+// The work is cut into tiles of kSteps steps by one 128-byte row of channels.  A block takes tiles
+// by ticket, time-major, so a tile only ever waits for tiles with smaller tickets, which blocks
+// hold that are running: every wait ends.  A warp owns SPW consecutive steps of the tile and loads
+// them for itself (cp.async, the next tile's rows in flight while this one is computed), forms w and
+// b = m i x once, in registers, and composes its steps into one map; the maps of the block's
+// warps and, by look-back, of earlier tiles give the state before the warp's first step, and a
+// second walk over the registers writes y.  Every input byte is read once.
+// ------------------------------------------------------------------------------------------------
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kRowBytes = 128;
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float sqrt_approx(float x) {
+  float y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float2 dup(float v) { return make_float2(v, v); }
+// 1 / (1 + e^-v); e^-v = inf gives 0
+__device__ __forceinline__ float2 sigmoid2(float2 v) {
+  const float2 t = fp::mul2(v, dup(-kLog2e));
+  const float2 d = make_float2(1.f + fp::ex2_approx(t.x), 1.f + fp::ex2_approx(t.y));
+  return make_float2(rcp_approx(d.x), rcp_approx(d.y));
+}
+// expm1(l) for l <= 0.  Above -1/4 the Taylor polynomial of degree 6, whose remainder l^6 / 5040 is
+// 5e-8 of the value; below, 2^x - 1, whose error 2^-22 is at most 1e-6 of the value.  `far` is false
+// where no channel of the warp can leave the polynomial's range (l >= -rate).
+constexpr float kNear = 0.25f;
+__device__ __forceinline__ float2 expm1_neg2(float2 l, bool far) {
+  float2 q = fp::fma2(l, dup(1.f / 720), dup(1.f / 120));
+  q = fp::fma2(q, l, dup(1.f / 24));
+  q = fp::fma2(q, l, dup(1.f / 6));
+  q = fp::fma2(q, l, dup(0.5f));
+  float2 w = fp::fma2(fp::mul2(q, l), l, l);
+  if (far) {
+    if (l.x < -kNear) w.x = fp::ex2_approx(l.x * kLog2e) - 1.f;
+    if (l.y < -kNear) w.y = fp::ex2_approx(l.y * kLog2e) - 1.f;
   }
-  if (p.final_state) p.final_state[id] = h;
+  return w;
+}
+struct Gates2 {
+  float2 r, i, w, m;
+};
+__device__ __forceinline__ Gates2 gates2(float2 ga, float2 gx, float2 rate, bool far) {
+  Gates2 g;
+  g.r = sigmoid2(ga);
+  g.i = sigmoid2(gx);
+  g.w = expm1_neg2(fp::mul2(fp::mul2(rate, g.r), dup(-1.f)), far);
+  const float2 s = fp::fma2(g.w, dup(-1.f), dup(-2.f));   // -(2 + w)
+  const float2 u = fp::mul2(g.w, s);                      // 1 - a^2
+  g.m = make_float2(sqrt_approx(u.x), sqrt_approx(u.y));
+  return g;
+}
+
+// Rows of one array for the calling warp: `rows` rows from step t0 on (rows at or past T become
+// zeros, as do channels at or past D), kRowBytes each.  ALIGN is what every row start is known to be
+// aligned to: 16 (one copy per 16 bytes), 4, or 2 (odd bf16 rows, through registers).
+template <typename T, int ROWS, int ALIGN>
+__device__ __forceinline__ void load_rows(unsigned char* dst, const T* src, int64_t row_stride, int64_t t0,
+                                          int64_t Tlen, int64_t ch_left, int lane) {
+  constexpr int kPer = ALIGN == 2 ? 4 : ALIGN;         // bytes a lane moves at a time
+  constexpr int kLanes = kRowBytes / kPer;             // lanes a row takes
+  constexpr int kRowsAtOnce = 32 / kLanes < 1 ? 1 : 32 / kLanes;
+  const int64_t bytes_left = ch_left * (int64_t)sizeof(T);
+#pragma unroll
+  for (int r0 = 0; r0 < ROWS; r0 += kRowsAtOnce) {
+    const int r = r0 + lane / kLanes, at = lane % kLanes * kPer;
+    if (ROWS % kRowsAtOnce != 0 && r >= ROWS) continue;
+    int64_t n = t0 + r < Tlen ? bytes_left - at : 0;
+    n = n < 0 ? 0 : n > kPer ? kPer : n;
+    const unsigned char* s =
+        reinterpret_cast<const unsigned char*>(n > 0 ? src + (t0 + r) * row_stride : src) + (n > 0 ? at : 0);
+    unsigned char* d = dst + r * kRowBytes + at;
+    if constexpr (ALIGN == 16) {
+      cp_async16(d, s, (int)n);
+    } else if constexpr (ALIGN == 4) {
+      if (n >= 4) cp_async4(d, s);
+      else if (n == 2) *reinterpret_cast<uint32_t*>(d) = *reinterpret_cast<const uint16_t*>(s);
+      else *reinterpret_cast<uint32_t*>(d) = 0u;
+    } else {
+      uint32_t v = 0;
+      if (n >= 2) v = *reinterpret_cast<const uint16_t*>(s);
+      if (n >= 4) v |= (uint32_t)*reinterpret_cast<const uint16_t*>(s + 2) << 16;
+      *reinterpret_cast<uint32_t*>(d) = v;
+    }
+  }
+}
+
+// The pair k of a lane's values in its warp's rows: for bf16 the lane's two channels of row k, for
+// f32 its one channel of rows 2k and 2k + 1.
+__device__ __forceinline__ float2 pair_at(const unsigned char* rows, int k, int lane, __nv_bfloat16) {
+  const uint32_t u = *reinterpret_cast<const uint32_t*>(rows + k * kRowBytes + lane * 4);
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+__device__ __forceinline__ float2 pair_at(const unsigned char* rows, int k, int lane, float) {
+  const float* f = reinterpret_cast<const float*>(rows + 2 * k * kRowBytes) + lane;
+  return make_float2(f[0], f[kRowBytes / 4]);
+}
+
+// Writes a lane's channels of one row; `n` of them are inside the array.
+template <int ALIGN>
+__device__ __forceinline__ void store_row(__nv_bfloat16* p, const float (&v)[2], int n) {
+  if (ALIGN >= 4 && n == 2) {
+    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v[0], v[1]);
+  } else {
+    if (n > 0) p[0] = __float2bfloat16_rn(v[0]);
+    if (n > 1) p[1] = __float2bfloat16_rn(v[1]);
+  }
+}
+template <int ALIGN>
+__device__ __forceinline__ void store_row(float* p, const float (&v)[1], int n) {
+  if (n > 0) p[0] = v[0];
+}
+
+template <typename T>
+struct Tile {
+  static constexpr int kCh = kRowBytes / (int)sizeof(T);   // channels of a tile
+  static constexpr int kCpl = kCh / 32;                    // channels of a lane
+};
+
+// Where a tile lies.  Tickets run over all columns of a time before the next time.
+struct Place {
+  int64_t b, c0, t0, ti, word;   // word: index of the tile's first look-back word
+};
+template <typename T, int STEPS, bool kReverse>
+__device__ __forceinline__ Place place(const RecParams& p, uint32_t ticket) {
+  constexpr int kCh = Tile<T>::kCh;
+  const uint32_t cols = (uint32_t)((p.D + kCh - 1) / kCh), all = cols * (uint32_t)p.batch;
+  const uint32_t k = ticket / all, col = ticket % all;
+  Place q;
+  q.ti = kReverse ? p.ntile - 1 - k : k;
+  q.b = col / cols;
+  q.c0 = (int64_t)(col % cols) * kCh;
+  q.t0 = q.ti * STEPS;
+  q.word = ((int64_t)col * p.ntile + q.ti) * kCh;
+  return q;
+}
+
+template <typename T, int SPW, int ALIGN, int MINB>
+__global__ void __launch_bounds__(kThreads, MINB) rec_forward_kernel(RecParams p) {
+  constexpr int kSteps = kWarps * SPW, kCh = Tile<T>::kCh, kCpl = Tile<T>::kCpl;
+  constexpr int kVals = SPW * kCpl, kWarpBytes = SPW * kRowBytes, kStage = 3 * kWarps * kWarpBytes;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ float2 maps[2][kWarps][kCh];   // (W, H) of every warp's steps
+  __shared__ float before[2][kCh];          // the state before the tile
+  __shared__ float rates[2][kCh];           // c softplus(decay) of the tile's channels
+  __shared__ uint32_t s_ticket;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int cl = lane * kCpl;
+  const T* src[3] = {static_cast<const T*>(p.x), static_cast<const T*>(p.ga), static_cast<const T*>(p.gx)};
+
+  auto load = [&](uint32_t ticket, int stage) {
+    if (ticket < p.tiles) {
+      const Place q = place<T, kSteps, false>(p, ticket);
+      const int64_t bs[3] = {p.xs[0], p.as[0], p.gs[0]}, ts[3] = {p.xs[1], p.as[1], p.gs[1]};
+#pragma unroll
+      for (int a = 0; a < 3; ++a)
+        load_rows<T, SPW, ALIGN>(smem + stage * kStage + (a * kWarps + warp) * kWarpBytes,
+                                 src[a] + q.b * bs[a] + q.c0, ts[a], q.t0 + warp * SPW, p.T, p.D - q.c0, lane);
+    }
+    cp_async_commit();
+  };
+  auto take = [&]() { return atomicAdd(p.ticket, 1u); };
+  auto set_rates = [&](uint32_t ticket, int slot) {   // by one warp
+    if (ticket >= p.tiles) return;
+    const Place q = place<T, kSteps, false>(p, ticket);
+#pragma unroll
+    for (int c = 0; c < kCpl; ++c)
+      rates[slot][cl + c] = q.c0 + cl + c < p.D ? p.c * softplus(p.decay[q.c0 + cl + c]) : 0.f;
+  };
+
+  uint32_t cur, nxt;
+  if (p.ticket) {
+    if (threadIdx.x == 0) s_ticket = take();
+    __syncthreads();
+    cur = s_ticket;
+    __syncthreads();
+    if (threadIdx.x == 0) s_ticket = take();
+    __syncthreads();
+    nxt = s_ticket;
+  } else {   // one tile in time: no order to keep
+    cur = blockIdx.x;
+    nxt = cur + gridDim.x;
+  }
+  load(cur, 0);
+  if (warp == 2) set_rates(cur, 0);
+  __syncthreads();
+  for (int it = 0; cur < p.tiles; ++it) {
+    load(nxt, (it + 1) & 1);
+    cp_async_wait<1>();
+    __syncwarp();
+    const Place q = place<T, kSteps, false>(p, cur);
+    const int nch = (int)min((int64_t)kCpl, max((int64_t)0, p.D - q.c0 - cl));
+    const float2 rate2 = make_float2(rates[it & 1][cl], rates[it & 1][cl + kCpl - 1]);
+    const bool far = __any_sync(0xffffffffu, fmaxf(rate2.x, rate2.y) > kNear);
+
+    const unsigned char* rows = smem + (it & 1) * kStage + warp * kWarpBytes;
+    float w[kVals], b[kVals];   // value s * kCpl + c: step s, channel c
+#pragma unroll
+    for (int k = 0; k < kVals / 2; ++k) {
+      const float2 x = pair_at(rows, k, lane, T());
+      const Gates2 g = gates2(pair_at(rows + kWarps * kWarpBytes, k, lane, T()),
+                              pair_at(rows + 2 * kWarps * kWarpBytes, k, lane, T()), rate2, far);
+      const float2 bv = fp::mul2(fp::mul2(g.m, g.i), x);
+      w[2 * k] = g.w.x, w[2 * k + 1] = g.w.y;
+      b[2 * k] = bv.x, b[2 * k + 1] = bv.y;
+    }
+    const int64_t steps_left = p.T - q.t0 - warp * SPW;
+    if (steps_left < SPW) {   // steps past the end change nothing
+#pragma unroll
+      for (int s = 0; s < SPW; ++s)
+        if (s >= steps_left) {
+#pragma unroll
+          for (int c = 0; c < kCpl; ++c) w[s * kCpl + c] = b[s * kCpl + c] = 0.f;
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < kCpl; ++c) {
+      float W = 0.f, H = 0.f;
+#pragma unroll
+      for (int s = 0; s < SPW; ++s) {
+        H = lookback::apply(w[s * kCpl + c], b[s * kCpl + c], H);
+        W = lookback::apply(w[s * kCpl + c], w[s * kCpl + c], W);
+      }
+      maps[it & 1][warp][cl + c] = make_float2(W, H);
+    }
+    __syncthreads();
+    uint32_t later = nxt + gridDim.x;
+    if (warp == 0) {
+      float W[kCpl], H[kCpl], h[kCpl];
+#pragma unroll
+      for (int c = 0; c < kCpl; ++c) {
+        W[c] = H[c] = 0.f;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+          const float2 m = maps[it & 1][k][cl + c];
+          H[c] = lookback::apply(m.x, m.y, H[c]);
+          W[c] = lookback::apply(m.x, m.x, W[c]);
+        }
+      }
+      uint64_t* words = p.words + q.word + cl;
+      const bool last = q.ti == p.ntile - 1;
+      uint64_t v[kCpl];
+      if (q.ti == 0) {
+#pragma unroll
+        for (int c = 0; c < kCpl; ++c) h[c] = p.init && c < nch ? p.init[q.b * p.D + q.c0 + cl + c] : 0.f;
+      } else {
+        if (!last) {
+#pragma unroll
+          for (int c = 0; c < kCpl; ++c) v[c] = lookback::word(W[c], H[c], lookback::kMap);
+          lookback::publish(words, v);
+        }
+        lookback::state_before<8>(words - kCh, -kCh, q.ti, h, p.hdr, 400);
+      }
+      if (!last) {
+#pragma unroll
+        for (int c = 0; c < kCpl; ++c)
+          v[c] = lookback::word(0.f, lookback::apply(W[c], H[c], h[c]), lookback::kInclusive);
+        lookback::publish(words, v);
+      }
+#pragma unroll
+      for (int c = 0; c < kCpl; ++c) before[it & 1][cl + c] = h[c];
+    } else if (warp == 1) {
+      if (p.ticket && lane == 0) s_ticket = take();
+    } else if (warp == 2) {
+      set_rates(nxt, (it + 1) & 1);
+    }
+    __syncthreads();
+    if (p.ticket) later = s_ticket;
+    float h[kCpl];
+#pragma unroll
+    for (int c = 0; c < kCpl; ++c) h[c] = before[it & 1][cl + c];
+    for (int k = 0; k < warp; ++k) {
+#pragma unroll
+      for (int c = 0; c < kCpl; ++c) {
+        const float2 m = maps[it & 1][k][cl + c];
+        h[c] = lookback::apply(m.x, m.y, h[c]);
+      }
+    }
+    if (p.states_out && warp * SPW % kChunk == 0 && steps_left > 0) {
+      const int64_t at = (q.b * p.nch + (q.t0 + warp * SPW) / kChunk) * p.D + q.c0 + cl;
+#pragma unroll
+      for (int c = 0; c < kCpl; ++c)
+        if (c < nch && SSD_INDEX_OK(p.hdr, at + c, p.batch * p.nch * p.D, 60)) p.states_out[at + c] = h[c];
+    }
+    const int64_t row0 = (q.b * p.T + q.t0 + warp * SPW) * p.D + q.c0 + cl;
+    T* y = static_cast<T*>(p.y);
+#pragma unroll
+    for (int s = 0; s < SPW; ++s) {
+#pragma unroll
+      for (int c = 0; c < kCpl; ++c) h[c] = lookback::apply(w[s * kCpl + c], b[s * kCpl + c], h[c]);
+      if (y && nch > 0 && s < steps_left &&
+          SSD_INDEX_OK(p.hdr, row0 + s * p.D + nch - 1, p.batch * p.T * p.D, 61))
+        store_row<ALIGN>(y + row0 + s * p.D, h, nch);
+    }
+    if (p.final_state && q.ti == p.ntile - 1 && warp == kWarps - 1) {
+      const int64_t at = q.b * p.D + q.c0 + cl;
+#pragma unroll
+      for (int c = 0; c < kCpl; ++c)
+        if (c < nch && SSD_INDEX_OK(p.hdr, at + c, p.batch * p.D, 62)) p.final_state[at + c] = h[c];
+    }
+    cur = nxt;
+    nxt = later;
+  }
+  cp_async_wait_all();
 }
 
 // One thread per (sequence, channel): chunks from the last to the first, each recomputed from the
@@ -132,6 +440,7 @@ __global__ void rec_step_kernel(RecParams p) {
   st_from_f32(static_cast<T*>(p.y) + id, h);
 }
 
+constexpr int64_t kMinTileSteps = 64;   // no kernel's tile is shorter
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
 
 ssd_status check_shape(const gated_recurrence_shape* s, bool backward) {
@@ -145,7 +454,10 @@ ssd_status check_shape(const gated_recurrence_shape* s, bool backward) {
   if (s->d_model > kMaxElems || s->batch > kMaxElems / s->d_model ||
       (s->batch > 0 && s->seqlen > kMaxElems / s->d_model / s->batch))
     return SSD_ERR_UNSUPPORTED;
-  if ((s->batch * s->d_model + 127) / 128 > 0x7fffffffLL) return SSD_ERR_UNSUPPORTED;
+  // blocks of the per-channel kernels, and tiles (tickets are 32 bits)
+  if ((s->batch * s->d_model + 127) / 128 > 0x7fffffffLL ||
+      s->batch * ((s->d_model + 31) / 32) * ((s->seqlen + kMinTileSteps - 1) / kMinTileSteps) > 0x7f000000LL)
+    return SSD_ERR_UNSUPPORTED;
   return SSD_OK;
 }
 
@@ -167,11 +479,16 @@ RecParams rec_params(const gated_recurrence_shape* s) {
 }
 
 struct RecLayout {
-  size_t states = 0, partial = 0, total = 0;
+  size_t scan = 0, states = 0, partial = 0, total = 0;   // scan: ticket, then look-back words
 };
 RecLayout rec_layout(const gated_recurrence_shape* s, bool backward) {
   RecLayout L;
   size_t off = sizeof(WsHeader);
+  L.scan = off;
+  const int64_t ntile = (s->seqlen + kMinTileSteps - 1) / kMinTileSteps;
+  if (ntile > 1)
+    off = align_up(off + kWsAlign + sizeof(uint64_t) * (size_t)(s->batch * ntile * align_up(s->d_model, 64)),
+                   kWsAlign);
   if (backward) {
     L.states = off;
     const int64_t nch = (s->seqlen + kChunk - 1) / kChunk;
@@ -189,11 +506,73 @@ cudaError_t set_rows(float* dst, const float* src, int64_t n, cudaStream_t st) {
              : cudaMemsetAsync(dst, 0, sizeof(float) * (size_t)n, st);
 }
 
-cudaError_t launch_forward(const RecParams& p, bool bf16, cudaStream_t st) {
-  const unsigned grid = (unsigned)((p.batch * p.D + 127) / 128);
-  if (bf16) rec_forward_kernel<__nv_bfloat16><<<grid, 128, 0, st>>>(p);
-  else rec_forward_kernel<float><<<grid, 128, 0, st>>>(p);
+constexpr int kSpwFwd = 8;   // steps a warp takes of a forward tile
+constexpr int64_t kTileSteps = kWarps * kSpwFwd;
+
+// Alignment that every row of the arrays is known to have: 16, 4 or (bf16) 2 bytes.
+int row_align(size_t e, std::initializer_list<std::pair<const void*, const int64_t*>> in,
+              std::initializer_list<const void*> out, int64_t D) {
+  uint64_t bits = 0;
+  for (const auto& a : in)
+    bits |= reinterpret_cast<uintptr_t>(a.first) | (uint64_t)(a.second[0] | a.second[1]) * e;
+  // an output row only needs its stores' 4 bytes
+  uint64_t obits = (uint64_t)D * e;
+  for (const void* o : out) obits |= reinterpret_cast<uintptr_t>(o);
+  if (obits % 4 != 0) return 2;
+  return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
+}
+
+// Blocks of `kernel` that the device holds at once (looked up once per kernel and device).
+template <typename K>
+cudaError_t resident_blocks(K* kernel, int threads, int smem, int* out) {
+  static std::mutex mu;
+  static std::map<std::pair<const void*, int>, int> known;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  const auto key = std::make_pair(reinterpret_cast<const void*>(kernel), dev);
+  const auto it = known.find(key);
+  if (it != known.end()) {
+    *out = it->second;
+    return cudaSuccess;
+  }
+  int sms = 0, per = 0;
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem);
+  if (e != cudaSuccess) return e;
+  *out = known[key] = sms * std::max(per, 1);
+  return cudaSuccess;
+}
+
+template <typename T, int ALIGN>
+cudaError_t launch_forward_as(RecParams p, cudaStream_t st) {
+  auto* kernel = rec_forward_kernel<T, kSpwFwd, ALIGN, 3>;
+  constexpr int kSmem = 2 * 3 * kWarps * kSpwFwd * kRowBytes;
+  int blocks = 0;
+  cudaError_t e = resident_blocks(kernel, kThreads, kSmem, &blocks);
+  if (e != cudaSuccess) return e;
+  if (p.ntile > 1) {   // tickets and look-back words start at zero
+    const size_t n = kWsAlign + sizeof(uint64_t) * (size_t)p.tiles * Tile<T>::kCh;
+    if ((e = cudaMemsetAsync(p.ticket, 0, n, st)) != cudaSuccess) return e;
+  } else {
+    p.ticket = nullptr;
+  }
+  kernel<<<(unsigned)std::min<int64_t>(blocks, p.tiles), kThreads, kSmem, st>>>(p);
   return cudaGetLastError();
+}
+
+cudaError_t launch_forward(RecParams p, bool bf16, cudaStream_t st) {
+  p.ntile = (p.T + kTileSteps - 1) / kTileSteps;
+  const int64_t ch = bf16 ? Tile<__nv_bfloat16>::kCh : Tile<float>::kCh;
+  p.tiles = (uint32_t)(p.batch * ((p.D + ch - 1) / ch) * p.ntile);
+  const int align = row_align(bf16 ? 2 : 4, {{p.x, p.xs}, {p.ga, p.as}, {p.gx, p.gs}}, {p.y}, p.D);
+  if (bf16)
+    return align == 16 ? launch_forward_as<__nv_bfloat16, 16>(p, st)
+         : align == 4 ? launch_forward_as<__nv_bfloat16, 4>(p, st)
+                      : launch_forward_as<__nv_bfloat16, 2>(p, st);
+  return align == 16 ? launch_forward_as<float, 16>(p, st) : launch_forward_as<float, 4>(p, st);
 }
 
 ssd_status done(cudaError_t e) { return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA; }
@@ -238,6 +617,10 @@ ssd_status gated_recurrence_forward(const gated_recurrence_shape* shape, const v
   p.y = y;
   p.final_state = final_state;
   p.states_out = states;
+  char* ws = static_cast<char*>(workspace);
+  p.hdr = reinterpret_cast<WsHeader*>(ws);
+  p.ticket = reinterpret_cast<uint32_t*>(ws + rec_layout(shape, false).scan);
+  p.words = reinterpret_cast<uint64_t*>(reinterpret_cast<char*>(p.ticket) + kWsAlign);
   return done(launch_forward(p, shape->io_dtype == SSD_BF16, st));
 }
 
@@ -276,6 +659,9 @@ ssd_status gated_recurrence_backward(const gated_recurrence_shape* shape, const 
   p.gx = gate_x;
   p.decay = decay;
   p.init = init_state;
+  p.hdr = reinterpret_cast<WsHeader*>(ws);
+  p.ticket = reinterpret_cast<uint32_t*>(ws + L.scan);
+  p.words = reinterpret_cast<uint64_t*>(ws + L.scan + kWsAlign);
   if (!states) {
     RecParams f = p;
     f.states_out = reinterpret_cast<float*>(ws + L.states);
