@@ -153,6 +153,15 @@ __device__ __forceinline__ void load_rows(unsigned char* dst, const T* src, int6
   }
 }
 
+template <typename T>
+struct Tile {
+  static constexpr int kCh = kRowBytes / (int)sizeof(T);   // channels of a tile
+  static constexpr int kCpl = kCh / 32;                    // channels of a lane
+};
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+
 // The pair k of a lane's values in its warp's rows: for bf16 the lane's two channels of row k, for
 // f32 its one channel of rows 2k and 2k + 1.
 __device__ __forceinline__ float2 pair_at(const unsigned char* rows, int k, int lane, __nv_bfloat16) {
@@ -162,6 +171,12 @@ __device__ __forceinline__ float2 pair_at(const unsigned char* rows, int k, int 
 __device__ __forceinline__ float2 pair_at(const unsigned char* rows, int k, int lane, float) {
   const float* f = reinterpret_cast<const float*>(rows + 2 * k * kRowBytes) + lane;
   return make_float2(f[0], f[kRowBytes / 4]);
+}
+
+// Channel c of a lane in row s.
+template <typename T>
+__device__ __forceinline__ float dy_at(const unsigned char* rows, int s, int lane, int c) {
+  return to_f32(*(reinterpret_cast<const T*>(rows + s * kRowBytes) + lane * Tile<T>::kCpl + c));
 }
 
 // Writes a lane's channels of one row; `n` of them are inside the array.
@@ -178,12 +193,6 @@ template <int ALIGN>
 __device__ __forceinline__ void store_row(float* p, const float (&v)[1], int n) {
   if (n > 0) p[0] = v[0];
 }
-
-template <typename T>
-struct Tile {
-  static constexpr int kCh = kRowBytes / (int)sizeof(T);   // channels of a tile
-  static constexpr int kCpl = kCh / 32;                    // channels of a lane
-};
 
 // Where a tile lies.  Tickets run over all columns of a time before the next time.
 struct Place {
@@ -372,58 +381,297 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_forward_kernel(RecParams p
   cp_async_wait_all();
 }
 
-// One thread per (sequence, channel): chunks from the last to the first, each recomputed from the
-// state before it.
-template <typename T>
-__global__ void rec_backward_kernel(RecParams p) {
-  const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (id >= p.batch * p.D) return;
-  const int64_t b = id / p.D, d = id % p.D;
-  const float rate = p.c * softplus(p.decay[d]);
-  const T* x = static_cast<const T*>(p.x) + b * p.xs[0] + d;
-  const T* ga = static_cast<const T*>(p.ga) + b * p.as[0] + d;
-  const T* gx = static_cast<const T*>(p.gx) + b * p.gs[0] + d;
-  const T* dy = static_cast<const T*>(p.dy) + b * p.ds[0] + d;
-  const int64_t o = b * p.T * p.D + d;
-  float carry = p.dfinal ? p.dfinal[id] : 0.f, sum = 0.f, comp = 0.f;
-  float prev[kChunk];
-  for (int64_t k = p.nch - 1; k >= 0; --k) {
-    const int64_t t0 = k * kChunk;
-    const int n = (int)min((int64_t)kChunk, p.T - t0);
-    float h = p.states_in[(b * p.nch + k) * p.D + d];
-    for (int j = 0; j < n; ++j) {
-      const int64_t t = t0 + j;
-      prev[j] = h;
-      const Gates g = gates(ld_f32(ga + t * p.as[1]), ld_f32(gx + t * p.gs[1]), rate);
-      h = decayed(g, h, g.m * g.i * ld_f32(x + t * p.xs[1]));
+// ------------------------------------------------------------------------------------------------
+// Backward.
+//
+// The same tiles, from the last to the first; a tile's state comes from the states that the forward
+// kept (one a tile), so only dL/dh is carried by look-back: C = a G, the gradient that a tile hands
+// to the step before it, maps to C + W C + Q over a tile with the same W as the forward's.  A warp
+// forms the forward maps of its steps, takes the state before them, walks them forward for
+//   mi = m i,  xi = mi x (1 - i),  kr = a (h_{t-1} - a i x / m) r,  r   (kept in registers)
+// and composes the reverse map; with C known a walk backwards gives G and writes
+//   dx = G mi, dgate_x = G xi, dgate_a = -rate G kr (1 - r)   and sums G kr for ddecay.
+// ddecay: one partial row per tile, added in tile order by rec_ddecay_kernel.
+// ------------------------------------------------------------------------------------------------
+constexpr int kSpwBwd = 8;
+static_assert(kWarps * kSpwBwd == kChunk, "a backward tile starts from one kept state");
+
+template <typename T, int ALIGN, int MINB, int STAGES>
+__global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(RecParams p) {
+  constexpr int SPW = kSpwBwd, kSteps = kWarps * SPW, kCh = Tile<T>::kCh, kCpl = Tile<T>::kCpl;
+  constexpr int kVals = SPW * kCpl, kWarpBytes = SPW * kRowBytes, kArray = kWarps * kWarpBytes;
+  constexpr int kStage = 4 * kArray;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ float2 maps[2][kWarps][kCh];   // forward (W, H) of every warp's steps
+  __shared__ float2 back[2][kWarps][kCh];   // reverse (W, Q)
+  __shared__ float after[2][kCh];           // C from the tile after
+  __shared__ float sums[2][kWarps][kCh];    // G kr over every warp's steps
+  __shared__ float rates[2][kCh], start[2][kCh];
+  __shared__ uint32_t s_ticket;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int cl = lane * kCpl;
+  const T* src[4] = {static_cast<const T*>(p.x), static_cast<const T*>(p.ga), static_cast<const T*>(p.gx),
+                     static_cast<const T*>(p.dy)};
+
+  auto load = [&](uint32_t ticket, int stage) {
+    if (ticket < p.tiles) {
+      const Place q = place<T, kSteps, true>(p, ticket);
+      const int64_t bs[4] = {p.xs[0], p.as[0], p.gs[0], p.ds[0]}, ts[4] = {p.xs[1], p.as[1], p.gs[1], p.ds[1]};
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+        load_rows<T, SPW, ALIGN>(smem + stage * kStage + a * kArray + warp * kWarpBytes,
+                                 src[a] + q.b * bs[a] + q.c0, ts[a], q.t0 + warp * SPW, p.T, p.D - q.c0, lane);
     }
-    for (int j = n - 1; j >= 0; --j) {
-      const int64_t t = t0 + j;
-      const Gates g = gates(ld_f32(ga + t * p.as[1]), ld_f32(gx + t * p.gs[1]), rate);
-      const float xv = ld_f32(x + t * p.xs[1]);
-      const float G = ld_f32(dy + t * p.ds[1]) + carry;
-      const float a = 1.f + g.w;
-      const float k1 = G * a * (prev[j] - (g.m > 0.f ? a * g.i * xv / g.m : 0.f));
-      const float mi = g.m * g.i;
-      st_from_f32(static_cast<T*>(p.dx) + o + t * p.D, G * mi);
-      st_from_f32(static_cast<T*>(p.dgx) + o + t * p.D, G * mi * xv * (1.f - g.i));
-      st_from_f32(static_cast<T*>(p.dga) + o + t * p.D, k1 * g.l * (1.f - g.r));
-      const float add = k1 * g.r - comp, s = sum + add;   // compensated sum over the steps
-      comp = (s - sum) - add;
-      sum = s;
-      carry = decayed(g, G, 0.f);
+    cp_async_commit();
+  };
+  auto take = [&]() { return atomicAdd(p.ticket, 1u); };
+  auto set_channels = [&](uint32_t ticket, int slot) {   // by one warp: rates and the kept state
+    if (ticket >= p.tiles) return;
+    const Place q = place<T, kSteps, true>(p, ticket);
+#pragma unroll
+    for (int c = 0; c < kCpl; ++c) {
+      const int64_t d = q.c0 + cl + c;
+      rates[slot][cl + c] = d < p.D ? p.c * softplus(p.decay[d]) : 0.f;
+      start[slot][cl + c] = d < p.D ? p.states_in[(q.b * p.nch + q.ti) * p.D + d] : 0.f;
     }
+  };
+
+  uint32_t cur, nxt;
+  if (p.ticket) {
+    if (threadIdx.x == 0) s_ticket = take();
+    __syncthreads();
+    cur = s_ticket;
+    __syncthreads();
+    if (threadIdx.x == 0) s_ticket = take();
+    __syncthreads();
+    nxt = s_ticket;
+  } else {
+    cur = blockIdx.x;
+    nxt = cur + gridDim.x;
   }
-  p.partial[id] = sum;
-  if (p.dinit) p.dinit[id] = carry;
+  load(cur, 0);
+  if (warp == 2) set_channels(cur, 0);
+  __syncthreads();
+  for (int it = 0; cur < p.tiles; ++it) {
+    const int slot = it & 1;
+    load(nxt, (it + 1) % STAGES);
+    cp_async_wait<1>();
+    __syncwarp();
+    const Place q = place<T, kSteps, true>(p, cur);
+    const int nch = (int)min((int64_t)kCpl, max((int64_t)0, p.D - q.c0 - cl));
+    const float2 rate2 = make_float2(rates[slot][cl], rates[slot][cl + kCpl - 1]);
+    const bool far = __any_sync(0xffffffffu, fmaxf(rate2.x, rate2.y) > kNear);
+    const int64_t steps_left = p.T - q.t0 - warp * SPW;
+
+    const unsigned char* rows = smem + (it % STAGES) * kStage + warp * kWarpBytes;
+    float w[kVals], mi[kVals], xi[kVals], kr[kVals], r[kVals];   // value s * kCpl + c
+    float b[kVals];
+#pragma unroll
+    for (int k = 0; k < kVals / 2; ++k) {
+      const float2 x = pair_at(rows, k, lane, T());
+      const Gates2 g = gates2(pair_at(rows + kArray, k, lane, T()), pair_at(rows + 2 * kArray, k, lane, T()),
+                              rate2, far);
+      const float2 m = fp::mul2(g.m, g.i), bv = fp::mul2(m, x);
+      const float2 ic = fp::fma2(g.i, dup(-1.f), dup(1.f));
+      const float2 xv = fp::mul2(bv, ic);
+      // a i x / m (0 where m is): what kr subtracts from h_{t-1}
+      const float2 ix = fp::mul2(g.i, x);
+      const float2 over = make_float2(g.m.x > 0.f ? rcp_approx(g.m.x) : 0.f, g.m.y > 0.f ? rcp_approx(g.m.y) : 0.f);
+      const float2 a = fp::fma2(g.w, dup(1.f), dup(1.f));
+      const float2 sub = fp::mul2(fp::mul2(a, ix), over);
+      w[2 * k] = g.w.x, w[2 * k + 1] = g.w.y;
+      b[2 * k] = bv.x, b[2 * k + 1] = bv.y;
+      mi[2 * k] = m.x, mi[2 * k + 1] = m.y;
+      xi[2 * k] = xv.x, xi[2 * k + 1] = xv.y;
+      kr[2 * k] = sub.x, kr[2 * k + 1] = sub.y;
+      r[2 * k] = g.r.x, r[2 * k + 1] = g.r.y;
+    }
+    if (steps_left < SPW) {   // steps past the end change nothing and hand nothing on
+#pragma unroll
+      for (int s = 0; s < SPW; ++s)
+        if (s >= steps_left) {
+#pragma unroll
+          for (int c = 0; c < kCpl; ++c) {
+            const int k = s * kCpl + c;
+            w[k] = b[k] = mi[k] = xi[k] = kr[k] = 0.f;
+          }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < kCpl; ++c) {
+      float W = 0.f, H = 0.f;
+#pragma unroll
+      for (int s = 0; s < SPW; ++s) {
+        H = lookback::apply(w[s * kCpl + c], b[s * kCpl + c], H);
+        W = lookback::apply(w[s * kCpl + c], w[s * kCpl + c], W);
+      }
+      maps[slot][warp][cl + c] = make_float2(W, H);
+    }
+    // reverse map of the warp's steps: dy + C enters a step, a (dy + C) leaves it
+    float Wq[kCpl], Q[kCpl];
+#pragma unroll
+    for (int c = 0; c < kCpl; ++c) Q[c] = 0.f;
+#pragma unroll
+    for (int s = SPW - 1; s >= 0; --s) {
+#pragma unroll
+      for (int c = 0; c < kCpl; ++c) {
+        const float G = dy_at<T>(rows + 3 * kArray, s, lane, c) + Q[c];
+        Q[c] = lookback::apply(w[s * kCpl + c], 0.f, G);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < kCpl; ++c) {
+      Wq[c] = maps[slot][warp][cl + c].x;
+      back[slot][warp][cl + c] = make_float2(Wq[c], Q[c]);
+    }
+    __syncthreads();
+    uint32_t later = nxt + gridDim.x;
+    if (warp == 0) {
+      float W[kCpl], H[kCpl], C[kCpl];
+#pragma unroll
+      for (int c = 0; c < kCpl; ++c) {
+        W[c] = H[c] = 0.f;
+#pragma unroll
+        for (int k = kWarps - 1; k >= 0; --k) {
+          const float2 m = back[slot][k][cl + c];
+          H[c] = lookback::apply(m.x, m.y, H[c]);
+          W[c] = lookback::apply(m.x, m.x, W[c]);
+        }
+      }
+      uint64_t* words = p.words + q.word + cl;
+      uint64_t v[kCpl];
+      if (q.ti == p.ntile - 1) {
+#pragma unroll
+        for (int c = 0; c < kCpl; ++c) C[c] = p.dfinal && c < nch ? p.dfinal[q.b * p.D + q.c0 + cl + c] : 0.f;
+      } else {
+        if (q.ti > 0) {
+#pragma unroll
+          for (int c = 0; c < kCpl; ++c) v[c] = lookback::word(W[c], H[c], lookback::kMap);
+          lookback::publish(words, v);
+        }
+        lookback::state_before<8>(words + kCh, kCh, p.ntile - 1 - q.ti, C, p.hdr, 401);
+      }
+      if (q.ti > 0) {
+#pragma unroll
+        for (int c = 0; c < kCpl; ++c)
+          v[c] = lookback::word(0.f, lookback::apply(W[c], H[c], C[c]), lookback::kInclusive);
+        lookback::publish(words, v);
+      }
+#pragma unroll
+      for (int c = 0; c < kCpl; ++c) after[slot][cl + c] = C[c];
+    } else if (warp == 1) {
+      if (p.ticket && lane == 0) s_ticket = take();
+    } else if (warp == 2) {
+      set_channels(nxt, slot ^ 1);
+    }
+    // the state before the warp's steps, and kr of every step (before C is needed)
+    {
+      float h[kCpl];
+#pragma unroll
+      for (int c = 0; c < kCpl; ++c) h[c] = start[slot][cl + c];
+      for (int k = 0; k < warp; ++k) {
+#pragma unroll
+        for (int c = 0; c < kCpl; ++c) {
+          const float2 m = maps[slot][k][cl + c];
+          h[c] = lookback::apply(m.x, m.y, h[c]);
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < SPW; ++s) {
+#pragma unroll
+        for (int c = 0; c < kCpl; ++c) {
+          const int k = s * kCpl + c;
+          const float a = 1.f + w[k];
+          const float prev = h[c];
+          h[c] = lookback::apply(w[k], b[k], prev);
+          kr[k] = s < steps_left ? a * (prev - kr[k]) * r[k] : 0.f;
+        }
+      }
+    }
+    __syncthreads();
+    if (p.ticket) later = s_ticket;
+    float C[kCpl], sum[kCpl];
+#pragma unroll
+    for (int c = 0; c < kCpl; ++c) {
+      C[c] = after[slot][cl + c];
+      sum[c] = 0.f;
+    }
+    for (int k = kWarps - 1; k > warp; --k) {
+#pragma unroll
+      for (int c = 0; c < kCpl; ++c) {
+        const float2 m = back[slot][k][cl + c];
+        C[c] = lookback::apply(m.x, m.y, C[c]);
+      }
+    }
+    const int64_t row0 = (q.b * p.T + q.t0 + warp * SPW) * p.D + q.c0 + cl;
+#pragma unroll
+    for (int s = SPW - 1; s >= 0; --s) {
+      float vx[kCpl], va[kCpl], vg[kCpl];
+#pragma unroll
+      for (int c = 0; c < kCpl; ++c) {
+        const int k = s * kCpl + c;
+        const float G = dy_at<T>(rows + 3 * kArray, s, lane, c) + C[c];
+        const float e = G * kr[k];
+        vx[c] = G * mi[k];
+        vg[c] = G * xi[k];
+        va[c] = -(c ? rate2.y : rate2.x) * e * (1.f - r[k]);
+        sum[c] += e;
+        C[c] = lookback::apply(w[k], 0.f, G);
+      }
+      if (nch > 0 && s < steps_left && SSD_INDEX_OK(p.hdr, row0 + s * p.D + nch - 1, p.batch * p.T * p.D, 63)) {
+        store_row<ALIGN>(static_cast<T*>(p.dx) + row0 + s * p.D, vx, nch);
+        store_row<ALIGN>(static_cast<T*>(p.dga) + row0 + s * p.D, va, nch);
+        store_row<ALIGN>(static_cast<T*>(p.dgx) + row0 + s * p.D, vg, nch);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < kCpl; ++c) sums[slot][warp][cl + c] = sum[c];
+    if (p.dinit && q.ti == 0 && warp == 0) {
+      const int64_t at = q.b * p.D + q.c0 + cl;
+#pragma unroll
+      for (int c = 0; c < kCpl; ++c)
+        if (c < nch && SSD_INDEX_OK(p.hdr, at + c, p.batch * p.D, 64)) p.dinit[at + c] = C[c];
+    }
+    __syncthreads();
+    if (warp == 3) {   // the tile's row of ddecay partials
+      const int64_t at = (q.b * p.nch + q.ti) * p.D + q.c0 + cl;
+#pragma unroll
+      for (int c = 0; c < kCpl; ++c) {
+        float v = 0.f;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) v += sums[slot][k][cl + c];
+        if (c < nch && SSD_INDEX_OK(p.hdr, at + c, p.batch * p.nch * p.D, 65)) p.partial[at + c] = v;
+      }
+    }
+    cur = nxt;
+    nxt = later;
+  }
+  cp_async_wait_all();
 }
 
-__global__ void rec_ddecay_kernel(RecParams p) {
-  const int64_t d = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (d >= p.D) return;
-  float s = 0.f;
-  for (int64_t b = 0; b < p.batch; ++b) s += p.partial[b * p.D + d];
-  p.ddecay[d] = -p.c * s / (1.f + expf(-p.decay[d]));
+// ddecay[d] = -c sigmoid(decay) * sum of the partial rows: a block takes 32 channels, its warps every
+// 32nd row each, joined in warp order.
+__global__ void __launch_bounds__(1024) rec_ddecay_kernel(RecParams p) {
+  __shared__ float part[32][33];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int64_t d = (int64_t)blockIdx.x * 32 + lane, rows = p.batch * p.nch;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (d < p.D) {
+    int64_t r = warp;
+    for (; r + 96 < rows; r += 128) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[k] += p.partial[(r + 32 * k) * p.D + d];
+    }
+    for (; r < rows; r += 32) s[0] += p.partial[r * p.D + d];
+  }
+  part[warp][lane] = (s[0] + s[1]) + (s[2] + s[3]);
+  __syncthreads();
+  if (warp == 0 && d < p.D) {
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v += part[k][lane];
+    p.ddecay[d] = -p.c * v / (1.f + expf(-p.decay[d]));
+  }
 }
 
 template <typename T>
@@ -494,7 +742,7 @@ RecLayout rec_layout(const gated_recurrence_shape* s, bool backward) {
     const int64_t nch = (s->seqlen + kChunk - 1) / kChunk;
     off = align_up(off + sizeof(float) * (size_t)(s->batch * nch * s->d_model), kWsAlign);
     L.partial = off;
-    off = align_up(off + sizeof(float) * (size_t)(s->batch * s->d_model), kWsAlign);
+    off = align_up(off + sizeof(float) * (size_t)(s->batch * nch * s->d_model), kWsAlign);
   }
   L.total = off;
   return L;
@@ -573,6 +821,38 @@ cudaError_t launch_forward(RecParams p, bool bf16, cudaStream_t st) {
          : align == 4 ? launch_forward_as<__nv_bfloat16, 4>(p, st)
                       : launch_forward_as<__nv_bfloat16, 2>(p, st);
   return align == 16 ? launch_forward_as<float, 16>(p, st) : launch_forward_as<float, 4>(p, st);
+}
+
+template <typename T, int ALIGN>
+cudaError_t launch_backward_as(RecParams p, cudaStream_t st) {
+  auto* kernel = rec_backward_kernel<T, ALIGN, 2, 2>;
+  constexpr int kSmem = 2 * 4 * kWarps * kSpwBwd * kRowBytes;
+  int blocks = 0;
+  cudaError_t e = resident_blocks(kernel, kThreads, kSmem, &blocks);
+  if (e != cudaSuccess) return e;
+  if (p.ntile > 1) {
+    const size_t n = kWsAlign + sizeof(uint64_t) * (size_t)p.tiles * Tile<T>::kCh;
+    if ((e = cudaMemsetAsync(p.ticket, 0, n, st)) != cudaSuccess) return e;
+  } else {
+    p.ticket = nullptr;
+  }
+  kernel<<<(unsigned)std::min<int64_t>(blocks, p.tiles), kThreads, kSmem, st>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  rec_ddecay_kernel<<<(unsigned)((p.D + 31) / 32), 1024, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_backward(RecParams p, bool bf16, cudaStream_t st) {
+  p.ntile = p.nch;
+  const int64_t ch = bf16 ? Tile<__nv_bfloat16>::kCh : Tile<float>::kCh;
+  p.tiles = (uint32_t)(p.batch * ((p.D + ch - 1) / ch) * p.ntile);
+  const int align = row_align(bf16 ? 2 : 4, {{p.x, p.xs}, {p.ga, p.as}, {p.gx, p.gs}, {p.dy, p.ds}},
+                              {p.dx, p.dga, p.dgx}, p.D);
+  if (bf16)
+    return align == 16 ? launch_backward_as<__nv_bfloat16, 16>(p, st)
+         : align == 4 ? launch_backward_as<__nv_bfloat16, 4>(p, st)
+                      : launch_backward_as<__nv_bfloat16, 2>(p, st);
+  return align == 16 ? launch_backward_as<float, 16>(p, st) : launch_backward_as<float, 4>(p, st);
 }
 
 ssd_status done(cudaError_t e) { return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA; }
@@ -677,12 +957,7 @@ ssd_status gated_recurrence_backward(const gated_recurrence_shape* shape, const 
   p.ddecay = ddecay;
   p.dinit = dinit;
   p.partial = reinterpret_cast<float*>(ws + L.partial);
-  const unsigned grid = (unsigned)((p.batch * p.D + 127) / 128);
-  if (bf16) rec_backward_kernel<__nv_bfloat16><<<grid, 128, 0, st>>>(p);
-  else rec_backward_kernel<float><<<grid, 128, 0, st>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return SSD_ERR_CUDA;
-  rec_ddecay_kernel<<<(unsigned)((p.D + 127) / 128), 128, 0, st>>>(p);
-  return done(cudaGetLastError());
+  return done(launch_backward(p, bf16, st));
 }
 
 ssd_status gated_recurrence_step(const gated_recurrence_shape* shape, const void* x,
