@@ -11,6 +11,7 @@
 #include <initializer_list>
 #include <map>
 #include <mutex>
+#include <type_traits>
 #include <utility>
 
 #include "common.cuh"
@@ -31,6 +32,7 @@ struct RecParams {
   int64_t xs[2], as[2], gs[2], ds[2];
   float c;
   int64_t ntile;     // tiles in time
+  uint32_t cols;     // tiles side by side in the channels of one sequence
   uint32_t tiles;    // tiles in all
   uint32_t* ticket;  // NULL where the order of the tiles does not matter
   uint64_t* words;
@@ -71,84 +73,80 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kRowBytes = 128;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kTiny = 4e-38f;   // above the smallest normal number (the approximations flush what is below)
 
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float sqrt_approx(float x) {
+__device__ __forceinline__ float rsqrt_approx(float x) {
   float y;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float2 dup(float v) { return make_float2(v, v); }
-// 1 / (1 + e^-v); e^-v = inf gives 0
-__device__ __forceinline__ float2 sigmoid2(float2 v) {
+// 1 + e^-v, the reciprocal of sigmoid(v); inf where e^-v is
+__device__ __forceinline__ float2 one_plus_exp2(float2 v) {
   const float2 t = fp::mul2(v, dup(-kLog2e));
-  const float2 d = make_float2(1.f + fp::ex2_approx(t.x), 1.f + fp::ex2_approx(t.y));
-  return make_float2(rcp_approx(d.x), rcp_approx(d.y));
+  return fp::add2(make_float2(fp::ex2_approx(t.x), fp::ex2_approx(t.y)), dup(1.f));
 }
+__device__ __forceinline__ float2 rcp2(float2 d) { return make_float2(rcp_approx(d.x), rcp_approx(d.y)); }
 // expm1(l) for l <= 0.  Above -1/4 the Taylor polynomial of degree 6, whose remainder l^6 / 5040 is
-// 5e-8 of the value; below, 2^x - 1, whose error 2^-22 is at most 1e-6 of the value.  `far` is false
+// 5e-8 of the value; below, 2^x - 1, whose error 2^-22 is at most 1e-6 of the value.  kFar = false
 // where no channel of the warp can leave the polynomial's range (l >= -rate).
 constexpr float kNear = 0.25f;
-__device__ __forceinline__ float2 expm1_neg2(float2 l, bool far) {
+template <bool kFar>
+__device__ __forceinline__ float2 expm1_neg2(float2 l) {
   float2 q = fp::fma2(l, dup(1.f / 720), dup(1.f / 120));
   q = fp::fma2(q, l, dup(1.f / 24));
   q = fp::fma2(q, l, dup(1.f / 6));
   q = fp::fma2(q, l, dup(0.5f));
   float2 w = fp::fma2(fp::mul2(q, l), l, l);
-  if (far) {
-    if (l.x < -kNear) w.x = fp::ex2_approx(l.x * kLog2e) - 1.f;
-    if (l.y < -kNear) w.y = fp::ex2_approx(l.y * kLog2e) - 1.f;
+  if (kFar) {
+    const float2 e = make_float2(fp::ex2_approx(l.x * kLog2e) - 1.f, fp::ex2_approx(l.y * kLog2e) - 1.f);
+    w.x = l.x < -kNear ? e.x : w.x;
+    w.y = l.y < -kNear ? e.y : w.y;
   }
   return w;
 }
-struct Gates2 {
-  float2 r, i, w, m;
-};
-__device__ __forceinline__ Gates2 gates2(float2 ga, float2 gx, float2 rate, bool far) {
-  Gates2 g;
-  g.r = sigmoid2(ga);
-  g.i = sigmoid2(gx);
-  g.w = expm1_neg2(fp::mul2(fp::mul2(rate, g.r), dup(-1.f)), far);
-  const float2 s = fp::fma2(g.w, dup(-1.f), dup(-2.f));   // -(2 + w)
-  const float2 u = fp::mul2(g.w, s);                      // 1 - a^2
-  g.m = make_float2(sqrt_approx(u.x), sqrt_approx(u.y));
-  return g;
-}
+// 1 - a^2 = -w (2 + w)
+__device__ __forceinline__ float2 one_minus_a2(float2 w) { return fp::mul2(w, fp::fma2(w, dup(-1.f), dup(-2.f))); }
 
-// Rows of one array for the calling warp: `rows` rows from step t0 on (rows at or past T become
-// zeros, as do channels at or past D), kRowBytes each.  ALIGN is what every row start is known to be
-// aligned to: 16 (one copy per 16 bytes), 4, or 2 (odd bf16 rows, through registers).
-template <typename T, int ROWS, int ALIGN>
-__device__ __forceinline__ void load_rows(unsigned char* dst, const T* src, int64_t row_stride, int64_t t0,
-                                          int64_t Tlen, int64_t ch_left, int lane) {
-  constexpr int kPer = ALIGN == 2 ? 4 : ALIGN;         // bytes a lane moves at a time
-  constexpr int kLanes = kRowBytes / kPer;             // lanes a row takes
-  constexpr int kRowsAtOnce = 32 / kLanes < 1 ? 1 : 32 / kLanes;
-  const int64_t bytes_left = ch_left * (int64_t)sizeof(T);
+// Rows of one array for the calling warp: ROWS rows from `src` (the warp's first row, the tile's first
+// channel) on, kRowBytes each; `rows` and `bytes` are how many rows and bytes of a row lie inside the
+// array, the rest becomes zeros.  ALIGN is what every row start is known to be aligned to: 16 (one
+// copy per 16 bytes), 4, or 2 (odd bf16 rows, through registers).
+template <int ROWS, int ALIGN>
+__device__ __forceinline__ void load_rows(unsigned char* dst, const unsigned char* src, int64_t pitch, int rows,
+                                          int bytes, int lane) {
+  constexpr int kPer = ALIGN == 2 ? 4 : ALIGN;   // bytes a lane moves at a time
+  constexpr int kLanes = kRowBytes / kPer;       // lanes a row takes: 8 or 32
+  constexpr int kAtOnce = 32 / kLanes;
+  static_assert(ROWS % kAtOnce == 0, "whole groups of rows");
+  const int r = lane / kLanes, at = lane % kLanes * kPer;
+  const unsigned char* s = src + r * pitch + at;
+  unsigned char* d = dst + r * kRowBytes + at;
+  if (ALIGN == 16 && rows >= ROWS && bytes >= kRowBytes) {
 #pragma unroll
-  for (int r0 = 0; r0 < ROWS; r0 += kRowsAtOnce) {
-    const int r = r0 + lane / kLanes, at = lane % kLanes * kPer;
-    if (ROWS % kRowsAtOnce != 0 && r >= ROWS) continue;
-    int64_t n = t0 + r < Tlen ? bytes_left - at : 0;
-    n = n < 0 ? 0 : n > kPer ? kPer : n;
-    const unsigned char* s =
-        reinterpret_cast<const unsigned char*>(n > 0 ? src + (t0 + r) * row_stride : src) + (n > 0 ? at : 0);
-    unsigned char* d = dst + r * kRowBytes + at;
+    for (int k = 0; k < ROWS / kAtOnce; ++k) cp_async16(d + k * kAtOnce * kRowBytes, s + k * kAtOnce * pitch, 16);
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < ROWS / kAtOnce; ++k) {
+    const int n = r + k * kAtOnce < rows ? min(max(bytes - at, 0), kPer) : 0;
+    const unsigned char* sk = n > 0 ? s + k * kAtOnce * pitch : src;
+    unsigned char* dk = d + k * kAtOnce * kRowBytes;
     if constexpr (ALIGN == 16) {
-      cp_async16(d, s, (int)n);
+      cp_async16(dk, sk, n);
     } else if constexpr (ALIGN == 4) {
-      if (n >= 4) cp_async4(d, s);
-      else if (n == 2) *reinterpret_cast<uint32_t*>(d) = *reinterpret_cast<const uint16_t*>(s);
-      else *reinterpret_cast<uint32_t*>(d) = 0u;
+      if (n == 4) cp_async4(dk, sk);
+      else *reinterpret_cast<uint32_t*>(dk) = 0u;   // the width is a multiple of 4 bytes
     } else {
       uint32_t v = 0;
-      if (n >= 2) v = *reinterpret_cast<const uint16_t*>(s);
-      if (n >= 4) v |= (uint32_t)*reinterpret_cast<const uint16_t*>(s + 2) << 16;
-      *reinterpret_cast<uint32_t*>(d) = v;
+      if (n >= 2) v = *reinterpret_cast<const uint16_t*>(sk);
+      if (n >= 4) v |= (uint32_t)*reinterpret_cast<const uint16_t*>(sk + 2) << 16;
+      *reinterpret_cast<uint32_t*>(dk) = v;
     }
   }
 }
@@ -158,9 +156,6 @@ struct Tile {
   static constexpr int kCh = kRowBytes / (int)sizeof(T);   // channels of a tile
   static constexpr int kCpl = kCh / 32;                    // channels of a lane
 };
-
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 
 // The pair k of a lane's values in its warp's rows: for bf16 the lane's two channels of row k, for
 // f32 its one channel of rows 2k and 2k + 1.
@@ -173,135 +168,168 @@ __device__ __forceinline__ float2 pair_at(const unsigned char* rows, int k, int 
   return make_float2(f[0], f[kRowBytes / 4]);
 }
 
-// Channel c of a lane in row s.
-template <typename T>
-__device__ __forceinline__ float dy_at(const unsigned char* rows, int s, int lane, int c) {
-  return to_f32(*(reinterpret_cast<const T*>(rows + s * kRowBytes) + lane * Tile<T>::kCpl + c));
-}
-
-// Writes a lane's channels of one row; `n` of them are inside the array.
+// Writes a lane's channels of one row; `n` >= 1 of them lie inside the array.
 template <int ALIGN>
 __device__ __forceinline__ void store_row(__nv_bfloat16* p, const float (&v)[2], int n) {
-  if (ALIGN >= 4 && n == 2) {
+  if (ALIGN >= 4) {   // the width is even: both lie inside
     *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v[0], v[1]);
   } else {
-    if (n > 0) p[0] = __float2bfloat16_rn(v[0]);
+    p[0] = __float2bfloat16_rn(v[0]);
     if (n > 1) p[1] = __float2bfloat16_rn(v[1]);
   }
 }
 template <int ALIGN>
-__device__ __forceinline__ void store_row(float* p, const float (&v)[1], int n) {
-  if (n > 0) p[0] = v[0];
+__device__ __forceinline__ void store_row(float* p, const float (&v)[2], int n) {
+  p[0] = v[0];
 }
 
 // Where a tile lies.  Tickets run over all columns of a time before the next time.
 struct Place {
-  int64_t b, c0, t0, ti, word;   // word: index of the tile's first look-back word
+  int64_t b, t0, word;   // word: index of the tile's first look-back word
+  int32_t c0, ti, left;  // left: channels inside the array
+  uint32_t tile;
 };
 template <typename T, int STEPS, bool kReverse>
-__device__ __forceinline__ Place place(const RecParams& p, uint32_t ticket) {
+__device__ __forceinline__ Place place(const RecParams& p, uint32_t tile) {
   constexpr int kCh = Tile<T>::kCh;
-  const uint32_t cols = (uint32_t)((p.D + kCh - 1) / kCh), all = cols * (uint32_t)p.batch;
-  const uint32_t k = ticket / all, col = ticket % all;
+  const uint32_t all = p.cols * (uint32_t)p.batch, k = tile / all, col = tile % all;
   Place q;
-  q.ti = kReverse ? p.ntile - 1 - k : k;
-  q.b = col / cols;
-  q.c0 = (int64_t)(col % cols) * kCh;
-  q.t0 = q.ti * STEPS;
+  q.tile = tile;
+  q.ti = (int32_t)(kReverse ? p.ntile - 1 - k : k);
+  q.b = col / p.cols;
+  q.c0 = (int32_t)(col % p.cols) * kCh;
+  q.left = (int32_t)min((int64_t)kCh, p.D - q.c0);
+  q.t0 = (int64_t)q.ti * STEPS;
   q.word = ((int64_t)col * p.ntile + q.ti) * kCh;
   return q;
 }
 
+// A lane's values over its warp's SPW steps, in pairs: for bf16 the two channels of a step, for f32 two
+// steps of one channel.
+template <typename T, int SPW>
+struct Walk {
+  static constexpr int kCpl = Tile<T>::kCpl, kPairs = SPW * kCpl / 2;
+  // f(value index, pair) for every pair in step order
+  static __device__ __forceinline__ void compose(const float2 (&w)[kPairs], const float2 (&b)[kPairs], float2& W,
+                                                 float2& H) {
+    W = H = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) {
+      if constexpr (kCpl == 2) {
+        H = lookback::apply(w[k], b[k], H);
+        W = lookback::apply(w[k], w[k], W);
+      } else {
+        H.x = lookback::apply(w[k].y, b[k].y, lookback::apply(w[k].x, b[k].x, H.x));
+        W.x = lookback::apply(w[k].y, w[k].y, lookback::apply(w[k].x, w[k].x, W.x));
+      }
+    }
+  }
+  // zeroes the pairs of steps from `steps` on
+  static __device__ __forceinline__ void cut(float2 (&v)[kPairs], int64_t steps) {
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) {
+      if constexpr (kCpl == 2) {
+        if (k >= steps) v[k] = make_float2(0.f, 0.f);
+      } else {
+        if (2 * k >= steps) v[k].x = 0.f;
+        if (2 * k + 1 >= steps) v[k].y = 0.f;
+      }
+    }
+  }
+};
+
 template <typename T, int SPW, int ALIGN, int MINB>
 __global__ void __launch_bounds__(kThreads, MINB) rec_forward_kernel(RecParams p) {
   constexpr int kSteps = kWarps * SPW, kCh = Tile<T>::kCh, kCpl = Tile<T>::kCpl;
-  constexpr int kVals = SPW * kCpl, kWarpBytes = SPW * kRowBytes, kStage = 3 * kWarps * kWarpBytes;
+  constexpr int kPairs = Walk<T, SPW>::kPairs, kWarpBytes = SPW * kRowBytes, kArray = kWarps * kWarpBytes;
+  constexpr int kStage = 3 * kArray;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ float2 maps[2][kWarps][kCh];   // (W, H) of every warp's steps
-  __shared__ float before[2][kCh];          // the state before the tile
-  __shared__ float rates[2][kCh];           // c softplus(decay) of the tile's channels
-  __shared__ uint32_t s_ticket;
+  __shared__ float2 maps[kWarps][kCh];      // (W, H) of every warp's steps
+  __shared__ float before[kWarps][kCh];     // the state before every warp's steps
+  __shared__ float rates[2][kCh];           // -c softplus(decay) of the tile's channels
+  __shared__ Place places[2];               // of the tile in hand and the one being loaded
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int cl = lane * kCpl;
-  const T* src[3] = {static_cast<const T*>(p.x), static_cast<const T*>(p.ga), static_cast<const T*>(p.gx)};
 
-  auto load = [&](uint32_t ticket, int stage) {
-    if (ticket < p.tiles) {
-      const Place q = place<T, kSteps, false>(p, ticket);
-      const int64_t bs[3] = {p.xs[0], p.as[0], p.gs[0]}, ts[3] = {p.xs[1], p.as[1], p.gs[1]};
-#pragma unroll
-      for (int a = 0; a < 3; ++a)
-        load_rows<T, SPW, ALIGN>(smem + stage * kStage + (a * kWarps + warp) * kWarpBytes,
-                                 src[a] + q.b * bs[a] + q.c0, ts[a], q.t0 + warp * SPW, p.T, p.D - q.c0, lane);
+  auto load = [&](const Place& q, int stage) {
+    if (q.tile < p.tiles) {
+      const int64_t t = q.t0 + warp * SPW;
+      const int rows = (int)min((int64_t)SPW, max((int64_t)0, p.T - t)), bytes = q.left * (int)sizeof(T);
+      unsigned char* d = smem + stage * kStage + warp * kWarpBytes;
+      // a warp whose rows all lie past the end reads nothing: its pointers are the array's start
+      auto at = [&](const void* base, const int64_t (&s)[2]) {
+        return static_cast<const unsigned char*>(base) +
+               (rows > 0 ? (q.b * s[0] + t * s[1] + q.c0) * (int64_t)sizeof(T) : 0);
+      };
+      load_rows<SPW, ALIGN>(d, at(p.x, p.xs), p.xs[1] * sizeof(T), rows, bytes, lane);
+      load_rows<SPW, ALIGN>(d + kArray, at(p.ga, p.as), p.as[1] * sizeof(T), rows, bytes, lane);
+      load_rows<SPW, ALIGN>(d + 2 * kArray, at(p.gx, p.gs), p.gs[1] * sizeof(T), rows, bytes, lane);
     }
     cp_async_commit();
   };
-  auto take = [&]() { return atomicAdd(p.ticket, 1u); };
-  auto set_rates = [&](uint32_t ticket, int slot) {   // by one warp
-    if (ticket >= p.tiles) return;
-    const Place q = place<T, kSteps, false>(p, ticket);
+  // by one warp: the next tile's place and its channels' rates
+  auto fetch = [&](uint32_t last, int slot) {
+    uint32_t tile = last + gridDim.x;
+    if (p.ticket) {
+      if (lane == 0) tile = atomicAdd(p.ticket, 1u);
+      tile = __shfl_sync(0xffffffffu, tile, 0);
+    }
+    const Place q = place<T, kSteps, false>(p, tile);
+    if (lane == 0) places[slot] = q;
+    if (tile < p.tiles) {
 #pragma unroll
-    for (int c = 0; c < kCpl; ++c)
-      rates[slot][cl + c] = q.c0 + cl + c < p.D ? p.c * softplus(p.decay[q.c0 + cl + c]) : 0.f;
+      for (int c = 0; c < kCpl; ++c)
+        rates[slot][cl + c] = cl + c < q.left ? -p.c * softplus(p.decay[q.c0 + cl + c]) : 0.f;
+    }
   };
 
-  uint32_t cur, nxt;
-  if (p.ticket) {
-    if (threadIdx.x == 0) s_ticket = take();
-    __syncthreads();
-    cur = s_ticket;
-    __syncthreads();
-    if (threadIdx.x == 0) s_ticket = take();
-    __syncthreads();
-    nxt = s_ticket;
-  } else {   // one tile in time: no order to keep
-    cur = blockIdx.x;
-    nxt = cur + gridDim.x;
+  if (warp == 0) {
+    fetch(blockIdx.x - gridDim.x, 0);
+    __syncwarp();
+    fetch(blockIdx.x, 1);
   }
-  load(cur, 0);
-  if (warp == 2) set_rates(cur, 0);
   __syncthreads();
-  for (int it = 0; cur < p.tiles; ++it) {
-    load(nxt, (it + 1) & 1);
+  load(places[0], 0);
+  for (int it = 0;; ++it) {
+    const int slot = it & 1;
+    const Place q = places[slot];
+    if (q.tile >= p.tiles) break;
+    load(places[slot ^ 1], slot ^ 1);
     cp_async_wait<1>();
     __syncwarp();
-    const Place q = place<T, kSteps, false>(p, cur);
-    const int nch = (int)min((int64_t)kCpl, max((int64_t)0, p.D - q.c0 - cl));
-    const float2 rate2 = make_float2(rates[it & 1][cl], rates[it & 1][cl + kCpl - 1]);
-    const bool far = __any_sync(0xffffffffu, fmaxf(rate2.x, rate2.y) > kNear);
+    const float2 rate = make_float2(rates[slot][cl], rates[slot][cl + kCpl - 1]);
+    const bool far = __any_sync(0xffffffffu, fminf(rate.x, rate.y) < -kNear);
+    const int64_t steps = p.T - q.t0 - warp * SPW;   // of this warp's that lie inside
 
-    const unsigned char* rows = smem + (it & 1) * kStage + warp * kWarpBytes;
-    float w[kVals], b[kVals];   // value s * kCpl + c: step s, channel c
+    const unsigned char* rows = smem + slot * kStage + warp * kWarpBytes;
+    float2 w[kPairs], b[kPairs];
+    auto coefficients = [&](auto far_c) {
 #pragma unroll
-    for (int k = 0; k < kVals / 2; ++k) {
-      const float2 x = pair_at(rows, k, lane, T());
-      const Gates2 g = gates2(pair_at(rows + kWarps * kWarpBytes, k, lane, T()),
-                              pair_at(rows + 2 * kWarps * kWarpBytes, k, lane, T()), rate2, far);
-      const float2 bv = fp::mul2(fp::mul2(g.m, g.i), x);
-      w[2 * k] = g.w.x, w[2 * k + 1] = g.w.y;
-      b[2 * k] = bv.x, b[2 * k + 1] = bv.y;
-    }
-    const int64_t steps_left = p.T - q.t0 - warp * SPW;
-    if (steps_left < SPW) {   // steps past the end change nothing
-#pragma unroll
-      for (int s = 0; s < SPW; ++s)
-        if (s >= steps_left) {
-#pragma unroll
-          for (int c = 0; c < kCpl; ++c) w[s * kCpl + c] = b[s * kCpl + c] = 0.f;
-        }
-    }
-#pragma unroll
-    for (int c = 0; c < kCpl; ++c) {
-      float W = 0.f, H = 0.f;
-#pragma unroll
-      for (int s = 0; s < SPW; ++s) {
-        H = lookback::apply(w[s * kCpl + c], b[s * kCpl + c], H);
-        W = lookback::apply(w[s * kCpl + c], w[s * kCpl + c], W);
+      for (int k = 0; k < kPairs; ++k) {
+        const float2 r = rcp2(one_plus_exp2(pair_at(rows + kArray, k, lane, T())));
+        w[k] = expm1_neg2<decltype(far_c)::value>(fp::mul2(rate, r));
+        // m i = sqrt(u) / d = u / sqrt(u d^2), u = 1 - a^2, d = 1 / i: one special function, not two.
+        // Where d^2 overflows (i < 2^-64), m i is taken as 0.
+        const float2 d = one_plus_exp2(pair_at(rows + 2 * kArray, k, lane, T()));
+        const float2 u = one_minus_a2(w[k]);
+        const float2 v = fp::mul2(fp::mul2(fp::add2(u, dup(kTiny)), d), d);   // never 0, nor 0 * inf
+        const float2 mi = fp::mul2(u, make_float2(rsqrt_approx(v.x), rsqrt_approx(v.y)));
+        b[k] = fp::mul2(mi, pair_at(rows, k, lane, T()));
       }
-      maps[it & 1][warp][cl + c] = make_float2(W, H);
+    };
+    if (far) coefficients(std::true_type());
+    else coefficients(std::false_type());
+    if (steps < SPW) {   // steps past the end change nothing
+      Walk<T, SPW>::cut(w, steps);
+      Walk<T, SPW>::cut(b, steps);
     }
-    __syncthreads();
-    uint32_t later = nxt + gridDim.x;
+    {
+      float2 W, H;
+      Walk<T, SPW>::compose(w, b, W, H);
+      maps[warp][cl] = make_float2(W.x, H.x);
+      if (kCpl == 2) maps[warp][cl + kCpl - 1] = make_float2(W.y, H.y);
+    }
+    __syncthreads();   // A: the warps' maps are there; everyone is done with this stage's rows
     if (warp == 0) {
       float W[kCpl], H[kCpl], h[kCpl];
 #pragma unroll
@@ -309,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_forward_kernel(RecParams p
         W[c] = H[c] = 0.f;
 #pragma unroll
         for (int k = 0; k < kWarps; ++k) {
-          const float2 m = maps[it & 1][k][cl + c];
+          const float2 m = maps[k][cl + c];
           H[c] = lookback::apply(m.x, m.y, H[c]);
           W[c] = lookback::apply(m.x, m.x, W[c]);
         }
@@ -319,14 +347,14 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_forward_kernel(RecParams p
       uint64_t v[kCpl];
       if (q.ti == 0) {
 #pragma unroll
-        for (int c = 0; c < kCpl; ++c) h[c] = p.init && c < nch ? p.init[q.b * p.D + q.c0 + cl + c] : 0.f;
+        for (int c = 0; c < kCpl; ++c) h[c] = p.init && cl + c < q.left ? p.init[q.b * p.D + q.c0 + cl + c] : 0.f;
       } else {
         if (!last) {
 #pragma unroll
           for (int c = 0; c < kCpl; ++c) v[c] = lookback::word(W[c], H[c], lookback::kMap);
           lookback::publish(words, v);
         }
-        lookback::state_before<8>(words - kCh, -kCh, q.ti, h, p.hdr, 400);
+        lookback::state_before<8 / kCpl>(words - kCh, -kCh, q.ti, h, p.hdr, 400);
       }
       if (!last) {
 #pragma unroll
@@ -335,48 +363,51 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_forward_kernel(RecParams p
         lookback::publish(words, v);
       }
 #pragma unroll
-      for (int c = 0; c < kCpl; ++c) before[it & 1][cl + c] = h[c];
-    } else if (warp == 1) {
-      if (p.ticket && lane == 0) s_ticket = take();
-    } else if (warp == 2) {
-      set_rates(nxt, (it + 1) & 1);
-    }
-    __syncthreads();
-    if (p.ticket) later = s_ticket;
-    float h[kCpl];
-#pragma unroll
-    for (int c = 0; c < kCpl; ++c) h[c] = before[it & 1][cl + c];
-    for (int k = 0; k < warp; ++k) {
-#pragma unroll
       for (int c = 0; c < kCpl; ++c) {
-        const float2 m = maps[it & 1][k][cl + c];
-        h[c] = lookback::apply(m.x, m.y, h[c]);
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+          before[k][cl + c] = h[c];
+          const float2 m = maps[k][cl + c];
+          h[c] = lookback::apply(m.x, m.y, h[c]);
+        }
+        if (p.final_state && last && cl + c < q.left) {
+          const int64_t at = q.b * p.D + q.c0 + cl + c;
+          if (SSD_INDEX_OK(p.hdr, at, p.batch * p.D, 62)) p.final_state[at] = h[c];
+        }
+      }
+    } else if (warp == 1) {
+      fetch(places[slot ^ 1].tile, slot);
+    }
+    __syncthreads();   // B: the states before the warps' steps are there, and the tile after the next
+    float2 h = make_float2(before[warp][cl], before[warp][cl + kCpl - 1]);
+    const int n = min(kCpl, max(0, q.left - cl));   // this lane's channels that lie inside
+    if (p.states_out && warp * SPW % kChunk == 0 && steps > 0) {
+      const int64_t at = (q.b * p.nch + (q.t0 + warp * SPW) / kChunk) * p.D + q.c0 + cl;
+      if (n > 0 && SSD_INDEX_OK(p.hdr, at + n - 1, p.batch * p.nch * p.D, 60)) {
+        p.states_out[at] = h.x;
+        if (n == 2) p.states_out[at + 1] = h.y;
       }
     }
-    if (p.states_out && warp * SPW % kChunk == 0 && steps_left > 0) {
-      const int64_t at = (q.b * p.nch + (q.t0 + warp * SPW) / kChunk) * p.D + q.c0 + cl;
-#pragma unroll
-      for (int c = 0; c < kCpl; ++c)
-        if (c < nch && SSD_INDEX_OK(p.hdr, at + c, p.batch * p.nch * p.D, 60)) p.states_out[at + c] = h[c];
-    }
     const int64_t row0 = (q.b * p.T + q.t0 + warp * SPW) * p.D + q.c0 + cl;
-    T* y = static_cast<T*>(p.y);
+    T* y = static_cast<T*>(p.y) + row0;
+    auto store = [&](int s, float v0, float v1) {
+      const float v[2] = {v0, v1};
+      if (SSD_INDEX_OK(p.hdr, row0 + s * p.D + n - 1, p.batch * p.T * p.D, 61)) store_row<ALIGN>(y, v, n);
+      y += p.D;
+    };
+    const int live = p.y && n > 0 ? (int)min((int64_t)SPW, max((int64_t)0, steps)) : 0;   // steps to write
 #pragma unroll
-    for (int s = 0; s < SPW; ++s) {
-#pragma unroll
-      for (int c = 0; c < kCpl; ++c) h[c] = lookback::apply(w[s * kCpl + c], b[s * kCpl + c], h[c]);
-      if (y && nch > 0 && s < steps_left &&
-          SSD_INDEX_OK(p.hdr, row0 + s * p.D + nch - 1, p.batch * p.T * p.D, 61))
-        store_row<ALIGN>(y + row0 + s * p.D, h, nch);
+    for (int k = 0; k < kPairs; ++k) {
+      if constexpr (kCpl == 2) {
+        h = lookback::apply(w[k], b[k], h);
+        if (k < live) store(k, h.x, h.y);
+      } else {
+        h.y = lookback::apply(w[k].x, b[k].x, h.x);
+        if (2 * k < live) store(2 * k, h.y, 0.f);
+        h.x = lookback::apply(w[k].y, b[k].y, h.y);
+        if (2 * k + 1 < live) store(2 * k + 1, h.x, 0.f);
+      }
     }
-    if (p.final_state && q.ti == p.ntile - 1 && warp == kWarps - 1) {
-      const int64_t at = q.b * p.D + q.c0 + cl;
-#pragma unroll
-      for (int c = 0; c < kCpl; ++c)
-        if (c < nch && SSD_INDEX_OK(p.hdr, at + c, p.batch * p.D, 62)) p.final_state[at + c] = h[c];
-    }
-    cur = nxt;
-    nxt = later;
   }
   cp_async_wait_all();
 }
@@ -396,145 +427,156 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_forward_kernel(RecParams p
 constexpr int kSpwBwd = 8;
 static_assert(kWarps * kSpwBwd == kChunk, "a backward tile starts from one kept state");
 
-template <typename T, int ALIGN, int MINB, int STAGES>
+template <typename T, int ALIGN, int MINB>
 __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(RecParams p) {
   constexpr int SPW = kSpwBwd, kSteps = kWarps * SPW, kCh = Tile<T>::kCh, kCpl = Tile<T>::kCpl;
-  constexpr int kVals = SPW * kCpl, kWarpBytes = SPW * kRowBytes, kArray = kWarps * kWarpBytes;
+  constexpr int kPairs = Walk<T, SPW>::kPairs, kWarpBytes = SPW * kRowBytes, kArray = kWarps * kWarpBytes;
   constexpr int kStage = 4 * kArray;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ float2 maps[2][kWarps][kCh];   // forward (W, H) of every warp's steps
-  __shared__ float2 back[2][kWarps][kCh];   // reverse (W, Q)
-  __shared__ float after[2][kCh];           // C from the tile after
-  __shared__ float sums[2][kWarps][kCh];    // G kr over every warp's steps
-  __shared__ float rates[2][kCh], start[2][kCh];
-  __shared__ uint32_t s_ticket;
+  __shared__ float2 maps[kWarps][kCh];      // forward (W, H) of every warp's steps
+  __shared__ float2 back[kWarps][kCh];      // reverse (W, Q)
+  __shared__ float after[kWarps][kCh];      // C from the step after every warp's steps
+  __shared__ float sums[kWarps][kCh];       // G kr over every warp's steps
+  __shared__ float rates[2][kCh], start[2][kCh];   // -c softplus(decay), the kept state
+  __shared__ Place places[2];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int cl = lane * kCpl;
-  const T* src[4] = {static_cast<const T*>(p.x), static_cast<const T*>(p.ga), static_cast<const T*>(p.gx),
-                     static_cast<const T*>(p.dy)};
 
-  auto load = [&](uint32_t ticket, int stage) {
-    if (ticket < p.tiles) {
-      const Place q = place<T, kSteps, true>(p, ticket);
-      const int64_t bs[4] = {p.xs[0], p.as[0], p.gs[0], p.ds[0]}, ts[4] = {p.xs[1], p.as[1], p.gs[1], p.ds[1]};
-#pragma unroll
-      for (int a = 0; a < 4; ++a)
-        load_rows<T, SPW, ALIGN>(smem + stage * kStage + a * kArray + warp * kWarpBytes,
-                                 src[a] + q.b * bs[a] + q.c0, ts[a], q.t0 + warp * SPW, p.T, p.D - q.c0, lane);
+  auto load = [&](const Place& q, int stage) {
+    if (q.tile < p.tiles) {
+      const int64_t t = q.t0 + warp * SPW;
+      const int rows = (int)min((int64_t)SPW, max((int64_t)0, p.T - t)), bytes = q.left * (int)sizeof(T);
+      unsigned char* d = smem + stage * kStage + warp * kWarpBytes;
+      auto at = [&](const void* base, const int64_t (&s)[2]) {
+        return static_cast<const unsigned char*>(base) +
+               (rows > 0 ? (q.b * s[0] + t * s[1] + q.c0) * (int64_t)sizeof(T) : 0);
+      };
+      load_rows<SPW, ALIGN>(d, at(p.x, p.xs), p.xs[1] * sizeof(T), rows, bytes, lane);
+      load_rows<SPW, ALIGN>(d + kArray, at(p.ga, p.as), p.as[1] * sizeof(T), rows, bytes, lane);
+      load_rows<SPW, ALIGN>(d + 2 * kArray, at(p.gx, p.gs), p.gs[1] * sizeof(T), rows, bytes, lane);
+      load_rows<SPW, ALIGN>(d + 3 * kArray, at(p.dy, p.ds), p.ds[1] * sizeof(T), rows, bytes, lane);
     }
     cp_async_commit();
   };
-  auto take = [&]() { return atomicAdd(p.ticket, 1u); };
-  auto set_channels = [&](uint32_t ticket, int slot) {   // by one warp: rates and the kept state
-    if (ticket >= p.tiles) return;
-    const Place q = place<T, kSteps, true>(p, ticket);
+  auto fetch = [&](uint32_t last, int slot) {   // by one warp
+    uint32_t tile = last + gridDim.x;
+    if (p.ticket) {
+      if (lane == 0) tile = atomicAdd(p.ticket, 1u);
+      tile = __shfl_sync(0xffffffffu, tile, 0);
+    }
+    const Place q = place<T, kSteps, true>(p, tile);
+    if (lane == 0) places[slot] = q;
+    if (tile < p.tiles) {
+      const float* s = p.states_in + (q.b * p.nch + q.ti) * p.D + q.c0;
+#pragma unroll
+      for (int c = 0; c < kCpl; ++c) {
+        const bool in = cl + c < q.left;
+        rates[slot][cl + c] = in ? -p.c * softplus(p.decay[q.c0 + cl + c]) : 0.f;
+        start[slot][cl + c] = in ? s[cl + c] : 0.f;
+      }
+    }
+  };
+  // by one warp, once everyone's sums of the tile before are there: its row of ddecay partials
+  auto write_partial = [&](int64_t at, int left) {
 #pragma unroll
     for (int c = 0; c < kCpl; ++c) {
-      const int64_t d = q.c0 + cl + c;
-      rates[slot][cl + c] = d < p.D ? p.c * softplus(p.decay[d]) : 0.f;
-      start[slot][cl + c] = d < p.D ? p.states_in[(q.b * p.nch + q.ti) * p.D + d] : 0.f;
+      float v = 0.f;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) v += sums[k][cl + c];
+      if (cl + c < left && SSD_INDEX_OK(p.hdr, at + c, p.batch * p.nch * p.D, 65)) p.partial[at + c] = v;
     }
   };
 
-  uint32_t cur, nxt;
-  if (p.ticket) {
-    if (threadIdx.x == 0) s_ticket = take();
-    __syncthreads();
-    cur = s_ticket;
-    __syncthreads();
-    if (threadIdx.x == 0) s_ticket = take();
-    __syncthreads();
-    nxt = s_ticket;
-  } else {
-    cur = blockIdx.x;
-    nxt = cur + gridDim.x;
+  if (warp == 0) {
+    fetch(blockIdx.x - gridDim.x, 0);
+    __syncwarp();
+    fetch(blockIdx.x, 1);
   }
-  load(cur, 0);
-  if (warp == 2) set_channels(cur, 0);
   __syncthreads();
-  for (int it = 0; cur < p.tiles; ++it) {
+  load(places[0], 0);
+  int64_t partial_at = 0;
+  int partial_left = 0;
+  for (int it = 0;; ++it) {
     const int slot = it & 1;
-    load(nxt, (it + 1) % STAGES);
+    const Place q = places[slot];
+    if (q.tile >= p.tiles) break;
+    load(places[slot ^ 1], slot ^ 1);
     cp_async_wait<1>();
     __syncwarp();
-    const Place q = place<T, kSteps, true>(p, cur);
-    const int nch = (int)min((int64_t)kCpl, max((int64_t)0, p.D - q.c0 - cl));
-    const float2 rate2 = make_float2(rates[slot][cl], rates[slot][cl + kCpl - 1]);
-    const bool far = __any_sync(0xffffffffu, fmaxf(rate2.x, rate2.y) > kNear);
-    const int64_t steps_left = p.T - q.t0 - warp * SPW;
+    const float2 rate = make_float2(rates[slot][cl], rates[slot][cl + kCpl - 1]);
+    const bool far = __any_sync(0xffffffffu, fminf(rate.x, rate.y) < -kNear);
+    const float2 h0 = make_float2(start[slot][cl], start[slot][cl + kCpl - 1]);
+    const int64_t steps = p.T - q.t0 - warp * SPW;
 
-    const unsigned char* rows = smem + (it % STAGES) * kStage + warp * kWarpBytes;
-    float w[kVals], mi[kVals], xi[kVals], kr[kVals], r[kVals];   // value s * kCpl + c
-    float b[kVals];
+    const unsigned char* rows = smem + slot * kStage + warp * kWarpBytes;
+    // kr holds a i x / m (0 where m is), what h_{t-1} is compared with, until the state is known
+    float2 w[kPairs], mi[kPairs], xi[kPairs], kr[kPairs], r[kPairs];
+    auto coefficients = [&](auto far_c) {
 #pragma unroll
-    for (int k = 0; k < kVals / 2; ++k) {
-      const float2 x = pair_at(rows, k, lane, T());
-      const Gates2 g = gates2(pair_at(rows + kArray, k, lane, T()), pair_at(rows + 2 * kArray, k, lane, T()),
-                              rate2, far);
-      const float2 m = fp::mul2(g.m, g.i), bv = fp::mul2(m, x);
-      const float2 ic = fp::fma2(g.i, dup(-1.f), dup(1.f));
-      const float2 xv = fp::mul2(bv, ic);
-      // a i x / m (0 where m is): what kr subtracts from h_{t-1}
-      const float2 ix = fp::mul2(g.i, x);
-      const float2 over = make_float2(g.m.x > 0.f ? rcp_approx(g.m.x) : 0.f, g.m.y > 0.f ? rcp_approx(g.m.y) : 0.f);
-      const float2 a = fp::fma2(g.w, dup(1.f), dup(1.f));
-      const float2 sub = fp::mul2(fp::mul2(a, ix), over);
-      w[2 * k] = g.w.x, w[2 * k + 1] = g.w.y;
-      b[2 * k] = bv.x, b[2 * k + 1] = bv.y;
-      mi[2 * k] = m.x, mi[2 * k + 1] = m.y;
-      xi[2 * k] = xv.x, xi[2 * k + 1] = xv.y;
-      kr[2 * k] = sub.x, kr[2 * k + 1] = sub.y;
-      r[2 * k] = g.r.x, r[2 * k + 1] = g.r.y;
+      for (int k = 0; k < kPairs; ++k) {
+        r[k] = rcp2(one_plus_exp2(pair_at(rows + kArray, k, lane, T())));
+        w[k] = expm1_neg2<decltype(far_c)::value>(fp::mul2(rate, r[k]));
+        const float2 i = rcp2(one_plus_exp2(pair_at(rows + 2 * kArray, k, lane, T())));
+        const float2 u = one_minus_a2(w[k]);
+        // 1 / m; m below 2e-19 (its square no normal number) counts as closed
+        const float2 over = make_float2(u.x > kTiny ? rsqrt_approx(u.x) : 0.f, u.y > kTiny ? rsqrt_approx(u.y) : 0.f);
+        const float2 ix = fp::mul2(i, pair_at(rows, k, lane, T()));
+        const float2 m = fp::mul2(u, over);
+        mi[k] = fp::mul2(m, i);
+        xi[k] = fp::mul2(fp::mul2(m, ix), fp::fma2(i, dup(-1.f), dup(1.f)));
+        const float2 io = fp::mul2(ix, over);
+        kr[k] = fp::fma2(w[k], io, io);
+      }
+    };
+    if (far) coefficients(std::true_type());
+    else coefficients(std::false_type());
+    if (steps < SPW) {   // steps past the end change nothing (their x and dy are zeros)
+      Walk<T, SPW>::cut(w, steps);
+      Walk<T, SPW>::cut(mi, steps);
+      Walk<T, SPW>::cut(r, steps);
     }
-    if (steps_left < SPW) {   // steps past the end change nothing and hand nothing on
+    {
+      float2 W = make_float2(0.f, 0.f), H = W, Q = W;
 #pragma unroll
-      for (int s = 0; s < SPW; ++s)
-        if (s >= steps_left) {
-#pragma unroll
-          for (int c = 0; c < kCpl; ++c) {
-            const int k = s * kCpl + c;
-            w[k] = b[k] = mi[k] = xi[k] = kr[k] = 0.f;
-          }
+      for (int k = 0; k < kPairs; ++k) {
+        const float2 b = fp::mul2(mi[k], pair_at(rows, k, lane, T()));
+        if constexpr (kCpl == 2) {
+          H = lookback::apply(w[k], b, H);
+          W = lookback::apply(w[k], w[k], W);
+        } else {
+          H.x = lookback::apply(w[k].y, b.y, lookback::apply(w[k].x, b.x, H.x));
+          W.x = lookback::apply(w[k].y, w[k].y, lookback::apply(w[k].x, w[k].x, W.x));
         }
-    }
-#pragma unroll
-    for (int c = 0; c < kCpl; ++c) {
-      float W = 0.f, H = 0.f;
-#pragma unroll
-      for (int s = 0; s < SPW; ++s) {
-        H = lookback::apply(w[s * kCpl + c], b[s * kCpl + c], H);
-        W = lookback::apply(w[s * kCpl + c], w[s * kCpl + c], W);
       }
-      maps[slot][warp][cl + c] = make_float2(W, H);
-    }
-    // reverse map of the warp's steps: dy + C enters a step, a (dy + C) leaves it
-    float Wq[kCpl], Q[kCpl];
+      // the reverse map: dy + C enters a step, a (dy + C) leaves it
 #pragma unroll
-    for (int c = 0; c < kCpl; ++c) Q[c] = 0.f;
-#pragma unroll
-    for (int s = SPW - 1; s >= 0; --s) {
-#pragma unroll
-      for (int c = 0; c < kCpl; ++c) {
-        const float G = dy_at<T>(rows + 3 * kArray, s, lane, c) + Q[c];
-        Q[c] = lookback::apply(w[s * kCpl + c], 0.f, G);
+      for (int k = kPairs - 1; k >= 0; --k) {
+        const float2 dy = pair_at(rows + 3 * kArray, k, lane, T());
+        if constexpr (kCpl == 2) {
+          const float2 G = fp::add2(dy, Q);
+          Q = fp::fma2(w[k], G, G);
+        } else {
+          const float G1 = dy.y + Q.x, C1 = fmaf(w[k].y, G1, G1), G0 = dy.x + C1;
+          Q.x = fmaf(w[k].x, G0, G0);
+        }
+      }
+      maps[warp][cl] = make_float2(W.x, H.x);
+      back[warp][cl] = make_float2(W.x, Q.x);
+      if (kCpl == 2) {
+        maps[warp][cl + kCpl - 1] = make_float2(W.y, H.y);
+        back[warp][cl + kCpl - 1] = make_float2(W.y, Q.y);
       }
     }
-#pragma unroll
-    for (int c = 0; c < kCpl; ++c) {
-      Wq[c] = maps[slot][warp][cl + c].x;
-      back[slot][warp][cl + c] = make_float2(Wq[c], Q[c]);
-    }
-    __syncthreads();
-    uint32_t later = nxt + gridDim.x;
+    __syncthreads();   // A: the warps' maps are there, and the sums of the tile before
     if (warp == 0) {
-      float W[kCpl], H[kCpl], C[kCpl];
+      float W[kCpl], Q[kCpl], C[kCpl];
 #pragma unroll
       for (int c = 0; c < kCpl; ++c) {
-        W[c] = H[c] = 0.f;
+        W[c] = Q[c] = 0.f;
 #pragma unroll
         for (int k = kWarps - 1; k >= 0; --k) {
-          const float2 m = back[slot][k][cl + c];
-          H[c] = lookback::apply(m.x, m.y, H[c]);
+          const float2 m = back[k][cl + c];
+          Q[c] = lookback::apply(m.x, m.y, Q[c]);
           W[c] = lookback::apply(m.x, m.x, W[c]);
         }
       }
@@ -542,111 +584,107 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(RecParams 
       uint64_t v[kCpl];
       if (q.ti == p.ntile - 1) {
 #pragma unroll
-        for (int c = 0; c < kCpl; ++c) C[c] = p.dfinal && c < nch ? p.dfinal[q.b * p.D + q.c0 + cl + c] : 0.f;
+        for (int c = 0; c < kCpl; ++c)
+          C[c] = p.dfinal && cl + c < q.left ? p.dfinal[q.b * p.D + q.c0 + cl + c] : 0.f;
       } else {
         if (q.ti > 0) {
 #pragma unroll
-          for (int c = 0; c < kCpl; ++c) v[c] = lookback::word(W[c], H[c], lookback::kMap);
+          for (int c = 0; c < kCpl; ++c) v[c] = lookback::word(W[c], Q[c], lookback::kMap);
           lookback::publish(words, v);
         }
-        lookback::state_before<8>(words + kCh, kCh, p.ntile - 1 - q.ti, C, p.hdr, 401);
+        lookback::state_before<8 / kCpl>(words + kCh, kCh, p.ntile - 1 - q.ti, C, p.hdr, 401);
       }
       if (q.ti > 0) {
 #pragma unroll
         for (int c = 0; c < kCpl; ++c)
-          v[c] = lookback::word(0.f, lookback::apply(W[c], H[c], C[c]), lookback::kInclusive);
+          v[c] = lookback::word(0.f, lookback::apply(W[c], Q[c], C[c]), lookback::kInclusive);
         lookback::publish(words, v);
       }
 #pragma unroll
-      for (int c = 0; c < kCpl; ++c) after[slot][cl + c] = C[c];
+      for (int c = 0; c < kCpl; ++c) {
+#pragma unroll
+        for (int k = kWarps - 1; k >= 0; --k) {
+          after[k][cl + c] = C[c];
+          const float2 m = back[k][cl + c];
+          C[c] = lookback::apply(m.x, m.y, C[c]);
+        }
+        if (p.dinit && q.ti == 0 && cl + c < q.left) {
+          const int64_t at = q.b * p.D + q.c0 + cl + c;
+          if (SSD_INDEX_OK(p.hdr, at, p.batch * p.D, 64)) p.dinit[at] = C[c];
+        }
+      }
     } else if (warp == 1) {
-      if (p.ticket && lane == 0) s_ticket = take();
-    } else if (warp == 2) {
-      set_channels(nxt, slot ^ 1);
+      fetch(places[slot ^ 1].tile, slot);
+    } else if (warp == 2 && it > 0) {
+      write_partial(partial_at, partial_left);
     }
-    // the state before the warp's steps, and kr of every step (before C is needed)
-    {
-      float h[kCpl];
-#pragma unroll
-      for (int c = 0; c < kCpl; ++c) h[c] = start[slot][cl + c];
+    {   // the state before the warp's steps, and kr of every step
+      float2 h = h0;
       for (int k = 0; k < warp; ++k) {
+        const float2 m0 = maps[k][cl], m1 = maps[k][cl + kCpl - 1];
+        h = lookback::apply(make_float2(m0.x, m1.x), make_float2(m0.y, m1.y), h);
+      }
 #pragma unroll
-        for (int c = 0; c < kCpl; ++c) {
-          const float2 m = maps[slot][k][cl + c];
-          h[c] = lookback::apply(m.x, m.y, h[c]);
+      for (int k = 0; k < kPairs; ++k) {
+        const float2 b = fp::mul2(mi[k], pair_at(rows, k, lane, T()));
+        float2 prev = h;
+        if constexpr (kCpl == 2) {
+          h = lookback::apply(w[k], b, h);
+        } else {
+          prev.y = lookback::apply(w[k].x, b.x, prev.x);
+          h.x = lookback::apply(w[k].y, b.y, prev.y);
         }
-      }
-#pragma unroll
-      for (int s = 0; s < SPW; ++s) {
-#pragma unroll
-        for (int c = 0; c < kCpl; ++c) {
-          const int k = s * kCpl + c;
-          const float a = 1.f + w[k];
-          const float prev = h[c];
-          h[c] = lookback::apply(w[k], b[k], prev);
-          kr[k] = s < steps_left ? a * (prev - kr[k]) * r[k] : 0.f;
-        }
+        const float2 d = fp::mul2(fp::sub2(prev, kr[k]), r[k]);
+        kr[k] = fp::fma2(w[k], d, d);
       }
     }
-    __syncthreads();
-    if (p.ticket) later = s_ticket;
-    float C[kCpl], sum[kCpl];
-#pragma unroll
-    for (int c = 0; c < kCpl; ++c) {
-      C[c] = after[slot][cl + c];
-      sum[c] = 0.f;
-    }
-    for (int k = kWarps - 1; k > warp; --k) {
-#pragma unroll
-      for (int c = 0; c < kCpl; ++c) {
-        const float2 m = back[slot][k][cl + c];
-        C[c] = lookback::apply(m.x, m.y, C[c]);
-      }
-    }
+    __syncthreads();   // B: C from the step after every warp's steps
+    float2 C = make_float2(after[warp][cl], after[warp][cl + kCpl - 1]), sum = make_float2(0.f, 0.f);
+    const int n = min(kCpl, max(0, q.left - cl));
+    const int live = n > 0 ? (int)min((int64_t)SPW, max((int64_t)0, steps)) : 0;
     const int64_t row0 = (q.b * p.T + q.t0 + warp * SPW) * p.D + q.c0 + cl;
-#pragma unroll
-    for (int s = SPW - 1; s >= 0; --s) {
-      float vx[kCpl], va[kCpl], vg[kCpl];
-#pragma unroll
-      for (int c = 0; c < kCpl; ++c) {
-        const int k = s * kCpl + c;
-        const float G = dy_at<T>(rows + 3 * kArray, s, lane, c) + C[c];
-        const float e = G * kr[k];
-        vx[c] = G * mi[k];
-        vg[c] = G * xi[k];
-        va[c] = -(c ? rate2.y : rate2.x) * e * (1.f - r[k]);
-        sum[c] += e;
-        C[c] = lookback::apply(w[k], 0.f, G);
+    auto store = [&](int s, float2 vx, float2 va, float2 vg) {
+      const int64_t at = row0 + s * p.D;
+      if (SSD_INDEX_OK(p.hdr, at + n - 1, p.batch * p.T * p.D, 63)) {
+        const float x2[2] = {vx.x, vx.y}, a2[2] = {va.x, va.y}, g2[2] = {vg.x, vg.y};
+        store_row<ALIGN>(static_cast<T*>(p.dx) + at, x2, n);
+        store_row<ALIGN>(static_cast<T*>(p.dga) + at, a2, n);
+        store_row<ALIGN>(static_cast<T*>(p.dgx) + at, g2, n);
       }
-      if (nch > 0 && s < steps_left && SSD_INDEX_OK(p.hdr, row0 + s * p.D + nch - 1, p.batch * p.T * p.D, 63)) {
-        store_row<ALIGN>(static_cast<T*>(p.dx) + row0 + s * p.D, vx, nch);
-        store_row<ALIGN>(static_cast<T*>(p.dga) + row0 + s * p.D, va, nch);
-        store_row<ALIGN>(static_cast<T*>(p.dgx) + row0 + s * p.D, vg, nch);
+    };
+#pragma unroll
+    for (int k = kPairs - 1; k >= 0; --k) {
+      const float2 dy = pair_at(rows + 3 * kArray, k, lane, T());
+      float2 G;
+      if constexpr (kCpl == 2) {
+        G = fp::add2(dy, C);
+        C = fp::fma2(w[k], G, G);
+      } else {
+        G.y = dy.y + C.x;
+        G.x = dy.x + fmaf(w[k].y, G.y, G.y);
+        C.x = fmaf(w[k].x, G.x, G.x);
       }
-    }
-#pragma unroll
-    for (int c = 0; c < kCpl; ++c) sums[slot][warp][cl + c] = sum[c];
-    if (p.dinit && q.ti == 0 && warp == 0) {
-      const int64_t at = q.b * p.D + q.c0 + cl;
-#pragma unroll
-      for (int c = 0; c < kCpl; ++c)
-        if (c < nch && SSD_INDEX_OK(p.hdr, at + c, p.batch * p.D, 64)) p.dinit[at + c] = C[c];
-    }
-    __syncthreads();
-    if (warp == 3) {   // the tile's row of ddecay partials
-      const int64_t at = (q.b * p.nch + q.ti) * p.D + q.c0 + cl;
-#pragma unroll
-      for (int c = 0; c < kCpl; ++c) {
-        float v = 0.f;
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) v += sums[slot][k][cl + c];
-        if (c < nch && SSD_INDEX_OK(p.hdr, at + c, p.batch * p.nch * p.D, 65)) p.partial[at + c] = v;
+      const float2 e = fp::mul2(G, kr[k]);
+      sum = fp::add2(sum, e);
+      const float2 vx = fp::mul2(G, mi[k]), vg = fp::mul2(G, xi[k]);
+      const float2 va = fp::mul2(fp::mul2(rate, e), fp::fma2(r[k], dup(-1.f), dup(1.f)));
+      if constexpr (kCpl == 2) {
+        if (k < live) store(k, vx, va, vg);
+      } else {
+        if (2 * k + 1 < live)
+          store(2 * k + 1, make_float2(vx.y, 0.f), make_float2(va.y, 0.f), make_float2(vg.y, 0.f));
+        if (2 * k < live) store(2 * k, vx, va, vg);
       }
     }
-    cur = nxt;
-    nxt = later;
+    if constexpr (kCpl == 1) sum.x += sum.y;
+    sums[warp][cl] = sum.x;
+    if (kCpl == 2) sums[warp][cl + kCpl - 1] = sum.y;
+    partial_at = (q.b * p.nch + q.ti) * p.D + q.c0 + cl;
+    partial_left = q.left;
   }
   cp_async_wait_all();
+  __syncthreads();
+  if (warp == 2 && partial_left > 0) write_partial(partial_at, partial_left);
 }
 
 // ddecay[d] = -c sigmoid(decay) * sum of the partial rows: a block takes 32 channels, its warps every
@@ -699,7 +737,7 @@ ssd_status check_shape(const gated_recurrence_shape* s, bool backward) {
     if (s->x_stride[k] < 0 || s->gate_a_stride[k] < 0 || s->gate_x_stride[k] < 0 ||
         (backward && s->dy_stride[k] < 0))
       return SSD_ERR_INVALID_ARG;
-  if (s->d_model > kMaxElems || s->batch > kMaxElems / s->d_model ||
+  if (s->d_model > 0x7fffff00LL || s->batch > kMaxElems / s->d_model ||
       (s->batch > 0 && s->seqlen > kMaxElems / s->d_model / s->batch))
     return SSD_ERR_UNSUPPORTED;
   // blocks of the per-channel kernels, and tiles (tickets are 32 bits)
@@ -796,7 +834,7 @@ cudaError_t resident_blocks(K* kernel, int threads, int smem, int* out) {
 
 template <typename T, int ALIGN>
 cudaError_t launch_forward_as(RecParams p, cudaStream_t st) {
-  auto* kernel = rec_forward_kernel<T, kSpwFwd, ALIGN, 3>;
+  auto* kernel = rec_forward_kernel<T, kSpwFwd, ALIGN, 4>;
   constexpr int kSmem = 2 * 3 * kWarps * kSpwFwd * kRowBytes;
   int blocks = 0;
   cudaError_t e = resident_blocks(kernel, kThreads, kSmem, &blocks);
@@ -814,7 +852,8 @@ cudaError_t launch_forward_as(RecParams p, cudaStream_t st) {
 cudaError_t launch_forward(RecParams p, bool bf16, cudaStream_t st) {
   p.ntile = (p.T + kTileSteps - 1) / kTileSteps;
   const int64_t ch = bf16 ? Tile<__nv_bfloat16>::kCh : Tile<float>::kCh;
-  p.tiles = (uint32_t)(p.batch * ((p.D + ch - 1) / ch) * p.ntile);
+  p.cols = (uint32_t)((p.D + ch - 1) / ch);
+  p.tiles = (uint32_t)(p.batch * p.cols * p.ntile);
   const int align = row_align(bf16 ? 2 : 4, {{p.x, p.xs}, {p.ga, p.as}, {p.gx, p.gs}}, {p.y}, p.D);
   if (bf16)
     return align == 16 ? launch_forward_as<__nv_bfloat16, 16>(p, st)
@@ -825,7 +864,7 @@ cudaError_t launch_forward(RecParams p, bool bf16, cudaStream_t st) {
 
 template <typename T, int ALIGN>
 cudaError_t launch_backward_as(RecParams p, cudaStream_t st) {
-  auto* kernel = rec_backward_kernel<T, ALIGN, 2, 2>;
+  auto* kernel = rec_backward_kernel<T, ALIGN, 2>;
   constexpr int kSmem = 2 * 4 * kWarps * kSpwBwd * kRowBytes;
   int blocks = 0;
   cudaError_t e = resident_blocks(kernel, kThreads, kSmem, &blocks);
@@ -845,7 +884,8 @@ cudaError_t launch_backward_as(RecParams p, cudaStream_t st) {
 cudaError_t launch_backward(RecParams p, bool bf16, cudaStream_t st) {
   p.ntile = p.nch;
   const int64_t ch = bf16 ? Tile<__nv_bfloat16>::kCh : Tile<float>::kCh;
-  p.tiles = (uint32_t)(p.batch * ((p.D + ch - 1) / ch) * p.ntile);
+  p.cols = (uint32_t)((p.D + ch - 1) / ch);
+  p.tiles = (uint32_t)(p.batch * p.cols * p.ntile);
   const int align = row_align(bf16 ? 2 : 4, {{p.x, p.xs}, {p.ga, p.as}, {p.gx, p.gs}, {p.dy, p.ds}},
                               {p.dx, p.dga, p.dgx}, p.D);
   if (bf16)

@@ -10,6 +10,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "fp_helpers.cuh"
 
 namespace ssd {
 namespace lookback {
@@ -17,6 +18,8 @@ namespace lookback {
 constexpr uint32_t kMap = 1u, kInclusive = 2u;
 
 __device__ __forceinline__ float apply(float W, float H, float h) { return h + fmaf(W, h, H); }
+
+__device__ __forceinline__ float2 apply(float2 W, float2 H, float2 h) { return fp::add2(h, fp::fma2(W, h, H)); }
 
 __device__ __forceinline__ uint64_t word(float W, float H, uint32_t state) {
   if (W != W) H = W, W = 0.f;   // a NaN decay: the state after it is NaN whatever came before
