@@ -73,7 +73,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kRowBytes = 128;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kTiny = 4e-38f;   // above the smallest normal number (the approximations flush what is below)
+constexpr float kTiny = 1e-36f;   // well above the smallest normal number (the approximations flush what is below)
 
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
@@ -110,8 +110,10 @@ __device__ __forceinline__ float2 expm1_neg2(float2 l) {
   }
   return w;
 }
-// 1 - a^2 = -w (2 + w)
-__device__ __forceinline__ float2 one_minus_a2(float2 w) { return fp::mul2(w, fp::fma2(w, dup(-1.f), dup(-2.f))); }
+// 1 - a^2 = -w (2 + w), plus a number too small to matter that keeps it from being zero
+__device__ __forceinline__ float2 one_minus_a2(float2 w) {
+  return fp::fma2(w, fp::fma2(w, dup(-1.f), dup(-2.f)), dup(kTiny));
+}
 
 // Rows of one array for the calling warp: ROWS rows from `src` (the warp's first row, the tile's first
 // channel) on, kRowBytes each; `rows` and `bytes` are how many rows and bytes of a row lie inside the
@@ -238,14 +240,23 @@ struct Walk {
   }
 };
 
-template <typename T, int SPW, int ALIGN, int MINB>
-__global__ void __launch_bounds__(kThreads, MINB) rec_forward_kernel(RecParams p) {
-  constexpr int kSteps = kWarps * SPW, kCh = Tile<T>::kCh, kCpl = Tile<T>::kCpl;
-  constexpr int kPairs = Walk<T, SPW>::kPairs, kWarpBytes = SPW * kRowBytes, kArray = kWarps * kWarpBytes;
+// NW warps of 16 steps.  Half as many blocks of 8 warps wait for the look-back together, so bf16,
+// bound by issue slots, takes four blocks of 4 warps an SM (8 x 4096 x 2048: 111 us, 118 us with two
+// of 8); f32, whose rows are half as many channels, takes the longer tiles and with them half the
+// look-back's chain (1 x 131072 x 1024: 361 us, 380 us with 4 warps).
+template <typename T>
+struct Forward {
+  static constexpr int kNw = sizeof(T) == 2 ? 4 : 8, kSpw = 16, kSteps = kNw * kSpw, kBlocks = 16 / kNw;
+};
+
+template <typename T, int ALIGN>
+__global__ void __launch_bounds__(32 * Forward<T>::kNw, Forward<T>::kBlocks) rec_forward_kernel(RecParams p) {
+  constexpr int NW = Forward<T>::kNw, SPW = Forward<T>::kSpw, kSteps = Forward<T>::kSteps, kCh = Tile<T>::kCh, kCpl = Tile<T>::kCpl;
+  constexpr int kPairs = Walk<T, SPW>::kPairs, kWarpBytes = SPW * kRowBytes, kArray = NW * kWarpBytes;
   constexpr int kStage = 3 * kArray;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ float2 maps[kWarps][kCh];      // (W, H) of every warp's steps
-  __shared__ float before[kWarps][kCh];     // the state before every warp's steps
+  __shared__ float2 maps[NW][kCh];      // (W, H) of every warp's steps
+  __shared__ float before[NW][kCh];     // the state before every warp's steps
   __shared__ float rates[2][kCh];           // -c softplus(decay) of the tile's channels
   __shared__ Place places[2];               // of the tile in hand and the one being loaded
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -311,8 +322,8 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_forward_kernel(RecParams p
         // m i = sqrt(u) / d = u / sqrt(u d^2), u = 1 - a^2, d = 1 / i: one special function, not two.
         // Where d^2 overflows (i < 2^-64), m i is taken as 0.
         const float2 d = one_plus_exp2(pair_at(rows + 2 * kArray, k, lane, T()));
-        const float2 u = one_minus_a2(w[k]);
-        const float2 v = fp::mul2(fp::mul2(fp::add2(u, dup(kTiny)), d), d);   // never 0, nor 0 * inf
+        const float2 u = one_minus_a2(w[k]);                // at least kTiny:
+        const float2 v = fp::mul2(fp::mul2(u, d), d);       // never 0, nor 0 * inf
         const float2 mi = fp::mul2(u, make_float2(rsqrt_approx(v.x), rsqrt_approx(v.y)));
         b[k] = fp::mul2(mi, pair_at(rows, k, lane, T()));
       }
@@ -336,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_forward_kernel(RecParams p
       for (int c = 0; c < kCpl; ++c) {
         W[c] = H[c] = 0.f;
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
+        for (int k = 0; k < NW; ++k) {
           const float2 m = maps[k][cl + c];
           H[c] = lookback::apply(m.x, m.y, H[c]);
           W[c] = lookback::apply(m.x, m.x, W[c]);
@@ -354,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_forward_kernel(RecParams p
           for (int c = 0; c < kCpl; ++c) v[c] = lookback::word(W[c], H[c], lookback::kMap);
           lookback::publish(words, v);
         }
-        lookback::state_before<8 / kCpl>(words - kCh, -kCh, q.ti, h, p.hdr, 400);
+        lookback::state_before<8>(words - kCh, -kCh, q.ti, h, p.hdr, 400);
       }
       if (!last) {
 #pragma unroll
@@ -365,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_forward_kernel(RecParams p
 #pragma unroll
       for (int c = 0; c < kCpl; ++c) {
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
+        for (int k = 0; k < NW; ++k) {
           before[k][cl + c] = h[c];
           const float2 m = maps[k][cl + c];
           h[c] = lookback::apply(m.x, m.y, h[c]);
@@ -509,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(RecParams 
     const int64_t steps = p.T - q.t0 - warp * SPW;
 
     const unsigned char* rows = smem + slot * kStage + warp * kWarpBytes;
-    // kr holds a i x / m (0 where m is), what h_{t-1} is compared with, until the state is known
+    // kr holds a i x / m, what h_{t-1} is compared with, until the state is known; where r is 0, so is kr
     float2 w[kPairs], mi[kPairs], xi[kPairs], kr[kPairs], r[kPairs];
     auto coefficients = [&](auto far_c) {
 #pragma unroll
@@ -518,8 +529,7 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(RecParams 
         w[k] = expm1_neg2<decltype(far_c)::value>(fp::mul2(rate, r[k]));
         const float2 i = rcp2(one_plus_exp2(pair_at(rows + 2 * kArray, k, lane, T())));
         const float2 u = one_minus_a2(w[k]);
-        // 1 / m; m below 2e-19 (its square no normal number) counts as closed
-        const float2 over = make_float2(u.x > kTiny ? rsqrt_approx(u.x) : 0.f, u.y > kTiny ? rsqrt_approx(u.y) : 0.f);
+        const float2 over = make_float2(rsqrt_approx(u.x), rsqrt_approx(u.y));   // 1 / m, at most 1e18
         const float2 ix = fp::mul2(i, pair_at(rows, k, lane, T()));
         const float2 m = fp::mul2(u, over);
         mi[k] = fp::mul2(m, i);
@@ -792,9 +802,6 @@ cudaError_t set_rows(float* dst, const float* src, int64_t n, cudaStream_t st) {
              : cudaMemsetAsync(dst, 0, sizeof(float) * (size_t)n, st);
 }
 
-constexpr int kSpwFwd = 8;   // steps a warp takes of a forward tile
-constexpr int64_t kTileSteps = kWarps * kSpwFwd;
-
 // Alignment that every row of the arrays is known to have: 16, 4 or (bf16) 2 bytes.
 int row_align(size_t e, std::initializer_list<std::pair<const void*, const int64_t*>> in,
               std::initializer_list<const void*> out, int64_t D) {
@@ -834,10 +841,15 @@ cudaError_t resident_blocks(K* kernel, int threads, int smem, int* out) {
 
 template <typename T, int ALIGN>
 cudaError_t launch_forward_as(RecParams p, cudaStream_t st) {
-  auto* kernel = rec_forward_kernel<T, kSpwFwd, ALIGN, 4>;
-  constexpr int kSmem = 2 * 3 * kWarps * kSpwFwd * kRowBytes;
+  using F = Forward<T>;
+  auto* kernel = rec_forward_kernel<T, ALIGN>;
+  constexpr int kSmem = 2 * 3 * F::kSteps * kRowBytes;
+  static_assert(F::kSteps >= kMinTileSteps, "the workspace is sized for tiles of kMinTileSteps");
+  p.ntile = (p.T + F::kSteps - 1) / F::kSteps;
+  p.cols = (uint32_t)((p.D + Tile<T>::kCh - 1) / Tile<T>::kCh);
+  p.tiles = (uint32_t)(p.batch * p.cols * p.ntile);
   int blocks = 0;
-  cudaError_t e = resident_blocks(kernel, kThreads, kSmem, &blocks);
+  cudaError_t e = resident_blocks(kernel, 32 * F::kNw, kSmem, &blocks);
   if (e != cudaSuccess) return e;
   if (p.ntile > 1) {   // tickets and look-back words start at zero
     const size_t n = kWsAlign + sizeof(uint64_t) * (size_t)p.tiles * Tile<T>::kCh;
@@ -845,15 +857,11 @@ cudaError_t launch_forward_as(RecParams p, cudaStream_t st) {
   } else {
     p.ticket = nullptr;
   }
-  kernel<<<(unsigned)std::min<int64_t>(blocks, p.tiles), kThreads, kSmem, st>>>(p);
+  kernel<<<(unsigned)std::min<int64_t>(blocks, p.tiles), 32 * F::kNw, kSmem, st>>>(p);
   return cudaGetLastError();
 }
 
-cudaError_t launch_forward(RecParams p, bool bf16, cudaStream_t st) {
-  p.ntile = (p.T + kTileSteps - 1) / kTileSteps;
-  const int64_t ch = bf16 ? Tile<__nv_bfloat16>::kCh : Tile<float>::kCh;
-  p.cols = (uint32_t)((p.D + ch - 1) / ch);
-  p.tiles = (uint32_t)(p.batch * p.cols * p.ntile);
+cudaError_t launch_forward(const RecParams& p, bool bf16, cudaStream_t st) {
   const int align = row_align(bf16 ? 2 : 4, {{p.x, p.xs}, {p.ga, p.as}, {p.gx, p.gs}}, {p.y}, p.D);
   if (bf16)
     return align == 16 ? launch_forward_as<__nv_bfloat16, 16>(p, st)
