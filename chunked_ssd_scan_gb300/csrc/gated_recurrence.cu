@@ -9,13 +9,12 @@
 
 #include <algorithm>
 #include <initializer_list>
-#include <map>
-#include <mutex>
 #include <type_traits>
 #include <utility>
 
 #include "common.cuh"
 #include "fp_helpers.cuh"
+#include "launch.h"
 #include "lookback.cuh"
 
 namespace ssd {
@@ -813,30 +812,6 @@ int row_align(size_t e, std::initializer_list<std::pair<const void*, const int64
   for (const void* o : out) obits |= reinterpret_cast<uintptr_t>(o);
   if (obits % 4 != 0) return 2;
   return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
-}
-
-// Blocks of `kernel` that the device holds at once (looked up once per kernel and device).
-template <typename K>
-cudaError_t resident_blocks(K* kernel, int threads, int smem, int* out) {
-  static std::mutex mu;
-  static std::map<std::pair<const void*, int>, int> known;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> lock(mu);
-  const auto key = std::make_pair(reinterpret_cast<const void*>(kernel), dev);
-  const auto it = known.find(key);
-  if (it != known.end()) {
-    *out = it->second;
-    return cudaSuccess;
-  }
-  int sms = 0, per = 0;
-  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem);
-  if (e != cudaSuccess) return e;
-  *out = known[key] = sms * std::max(per, 1);
-  return cudaSuccess;
 }
 
 template <typename T, int ALIGN>

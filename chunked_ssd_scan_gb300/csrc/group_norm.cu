@@ -10,6 +10,7 @@
 
 #include "common.cuh"
 #include "fp_helpers.cuh"
+#include "launch.h"
 
 namespace ssd {
 namespace {
@@ -27,7 +28,8 @@ struct NormParams {
   int32_t tile_groups;  // map kernels: groups of a column tile
   int32_t chunks;       // map kernels: pieces that a sample's positions are cut into
   int64_t chunk_rows;
-  float *stats;         // map kernels: [N, chunks, G, 2], mean and M2 or the two gradient sums
+  float *stats;         // map kernels: [N, G, chunks, 2], mean and M2 or the two gradient sums
+  float *joined;        // [N, G, 2]
   float *part_w, *part_b;   // rows of parameter gradient partials [part_rows, C]
   int64_t part_rows;
   WsHeader* hdr;
@@ -37,42 +39,91 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// 1 / (1 + e^-z)
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + fp::ex2_approx(-z * kLog2e)); }
-template <bool kSilu>
-__device__ __forceinline__ float act_fwd(float z) {
-  return kSilu ? z * sigmoid(z) : z;
+__device__ __forceinline__ float2 dup(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
-// act'(z)
+// 1 / (1 + e^-z)
+__device__ __forceinline__ float2 sigmoid2(float2 z) {
+  const float2 t = fp::mul2(z, dup(-kLog2e));
+  const float2 d = fp::add2(make_float2(fp::ex2_approx(t.x), fp::ex2_approx(t.y)), dup(1.f));
+  return make_float2(rcp_approx(d.x), rcp_approx(d.y));
+}
 template <bool kSilu>
-__device__ __forceinline__ float act_grad(float z) {
-  if (!kSilu) return 1.f;
-  const float s = sigmoid(z);
-  return s * fmaf(z, 1.f - s, 1.f);
+__device__ __forceinline__ float2 act2(float2 z) {
+  return kSilu ? fp::mul2(z, sigmoid2(z)) : z;
+}
+// v act'(z); silu' = s + z (s - s^2)
+template <bool kSilu>
+__device__ __forceinline__ float2 times_act_grad2(float2 v, float2 z) {
+  if (!kSilu) return v;
+  const float2 s = sigmoid2(z);
+  const float2 ss = fp::fma2(fp::mul2(s, dup(-1.f)), s, s);
+  return fp::mul2(v, fp::fma2(z, ss, s));
 }
 
-// V neighbouring values as one load or store of up to 16 bytes.
+// V neighbouring values as one load or store of up to 16 bytes, in P pairs (V = 1: the second is 0).
 template <typename T, int V>
-struct alignas(sizeof(T) * V) Vec {
-  T v[V];
+struct Pack {
+  static constexpr int P = (V + 1) / 2;
+  static __device__ __forceinline__ void load(const T* p, float2 (&f)[P]) {
+    if constexpr (V == 1) {
+      f[0] = make_float2(ld_f32(p), 0.f);
+    } else if constexpr (sizeof(T) == 2) {
+      uint32_t u[P];
+      if constexpr (V == 8) *reinterpret_cast<uint4*>(u) = __ldg(reinterpret_cast<const uint4*>(p));
+      else if constexpr (V == 4) *reinterpret_cast<uint2*>(u) = __ldg(reinterpret_cast<const uint2*>(p));
+      else u[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+#pragma unroll
+      for (int k = 0; k < P; ++k) f[k] = make_float2(__uint_as_float(u[k] << 16), __uint_as_float(u[k] & 0xffff0000u));
+    } else {
+      if constexpr (V == 4) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(p));
+        f[0] = make_float2(v.x, v.y);
+        f[1] = make_float2(v.z, v.w);
+      } else {
+        f[0] = __ldg(reinterpret_cast<const float2*>(p));
+      }
+    }
+  }
+  static __device__ __forceinline__ void store(T* p, const float2 (&f)[P]) {
+    if constexpr (V == 1) {
+      st_from_f32(p, f[0].x);
+    } else if constexpr (sizeof(T) == 2) {
+      uint32_t u[P];
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f[k].x, f[k].y);
+        u[k] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      if constexpr (V == 8) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<uint4*>(u);
+      else if constexpr (V == 4) *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(u);
+      else *reinterpret_cast<uint32_t*>(p) = u[0];
+    } else {
+      if constexpr (V == 4) *reinterpret_cast<float4*>(p) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+      else *reinterpret_cast<float2*>(p) = f[0];
+    }
+  }
+  static __device__ __forceinline__ void param(const float* p, int64_t at, float none, float2 (&f)[P]) {
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      f[k].x = p ? __ldg(p + at + 2 * k) : none;
+      f[k].y = V == 1 ? 0.f : p ? __ldg(p + at + 2 * k + 1) : none;
+    }
+  }
+  static __device__ __forceinline__ void zero(float2 (&f)[P]) {
+#pragma unroll
+    for (int k = 0; k < P; ++k) f[k] = make_float2(0.f, 0.f);
+  }
 };
-template <typename T, int V>
-__device__ __forceinline__ void load_vec(const T* p, float (&f)[V]) {
-  const Vec<T, V> q = *reinterpret_cast<const Vec<T, V>*>(p);
-#pragma unroll
-  for (int k = 0; k < V; ++k) f[k] = (float)q.v[k];
-}
-template <typename T, int V>
-__device__ __forceinline__ void store_vec(T* p, const float (&f)[V]) {
-  Vec<T, V> q;
-#pragma unroll
-  for (int k = 0; k < V; ++k) st_from_f32(&q.v[k], f[k]);
-  *reinterpret_cast<Vec<T, V>*>(p) = q;
-}
+// a - b, and 0 in the second place of a single value
 template <int V>
-__device__ __forceinline__ void load_param(const float* p, int64_t at, float none, float (&f)[V]) {
-#pragma unroll
-  for (int k = 0; k < V; ++k) f[k] = p ? __ldg(p + at + k) : none;
+__device__ __forceinline__ float2 minus2(float2 a, float b) {
+  float2 d = fp::add2(a, dup(-b));
+  if (V == 1) d.y = 0.f;
+  return d;
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -83,18 +134,20 @@ __device__ __forceinline__ void load_param(const float* p, int64_t at, float non
 // Bound by memory: x and y once each.
 // ------------------------------------------------------------------------------------------------
 template <bool kBlock>
-__device__ __forceinline__ float group_sum(float v, int lanes, float (&part)[2][kWarps], int& phase) {
+__device__ __forceinline__ float2 group_sum(float2 v, int lanes, float2 (&part)[2][kWarps], int& phase) {
   if (!kBlock) {
-    for (int o = lanes / 2; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = lanes / 2; o > 0; o /= 2)
+      v = fp::add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
     return v;
   }
 #pragma unroll
-  for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 16; o > 0; o /= 2)
+    v = fp::add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
   if (threadIdx.x % 32 == 0) part[phase][threadIdx.x / 32] = v;
   __syncthreads();
-  float s = 0.f;
+  float2 s = part[phase][0];
 #pragma unroll
-  for (int k = 0; k < kWarps; ++k) s += part[phase][k];
+  for (int k = 1; k < kWarps; ++k) s = fp::add2(s, part[phase][k]);
   phase ^= 1;   // the next sum writes elsewhere, and its barrier ends the reads of this one
   return s;
 }
@@ -102,30 +155,25 @@ __device__ __forceinline__ float group_sum(float v, int lanes, float (&part)[2][
 // What a thread of a token kernel works on.
 template <int V, int K, bool kBlock>
 struct TokenSlot {
-  int64_t g, row, rows;   // its group, its first sample within a block's step, samples of a step
-  int64_t c;              // its first channel
+  int64_t g, c;           // its group and its first channel
+  int row, rows;          // its sample within a block's step, samples of a step
   bool in[K];             // which of its vectors lie inside the group
   int step;               // channels from one of its vectors to the next
   __device__ __forceinline__ TokenSlot(const NormParams& p) {
     int l;
+    row = 0;
+    rows = 1;
     if (kBlock) {
       g = blockIdx.y;
       l = threadIdx.x;
-      row = 0;
-      rows = 1;
       step = kThreads * V;
     } else {
       const int64_t slots = p.G * p.lanes;
-      int64_t s;
-      if (slots >= kThreads) {
-        s = (int64_t)blockIdx.y * kThreads + threadIdx.x;
-        row = 0;
-        rows = 1;
-      } else {
+      int64_t s = (int64_t)blockIdx.y * kThreads + threadIdx.x;
+      if (slots < kThreads) {
         rows = kThreads / (int)slots;
         row = threadIdx.x / (int)slots;
-        s = threadIdx.x % (int)slots;
-        if (row >= rows) s = slots;   // a thread too many
+        s = row < rows ? threadIdx.x % (int)slots : slots;   // slots: a thread too many
       }
       g = s / p.lanes;
       l = (int)(s % p.lanes);
@@ -139,64 +187,63 @@ struct TokenSlot {
 
 template <typename T, int V, int K, int U, bool kBlock, bool kSilu>
 __global__ void __launch_bounds__(kThreads) norm_token_forward_kernel(NormParams p) {
-  __shared__ float part[2][kWarps];
+  using Q = Pack<T, V>;
+  __shared__ float2 part[2][kWarps];
   int phase = 0;
   const TokenSlot<V, K, kBlock> t(p);
   const int lanes = p.lanes;
-  float w[K][V], bias[K][V];
+  float2 w[K][Q::P], bias[K][Q::P];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
+    Q::zero(w[k]);
+    Q::zero(bias[k]);
     if (t.in[k]) {
-      load_param<V>(p.w, t.c + k * t.step, 1.f, w[k]);
-      load_param<V>(p.bias, t.c + k * t.step, 0.f, bias[k]);
+      Q::param(p.w, t.c + k * t.step, 1.f, w[k]);
+      Q::param(p.bias, t.c + k * t.step, 0.f, bias[k]);
     }
   }
   const float inv = 1.f / (float)p.cg;
   const int64_t stride = (int64_t)gridDim.x * t.rows * U;
-  for (int64_t n0 = (int64_t)blockIdx.x * t.rows * U; n0 < p.N; n0 += stride) {
-    float x[U][K][V];
+  for (int64_t n0 = (int64_t)blockIdx.x * t.rows * U + t.row; n0 - t.row < p.N; n0 += stride) {
+    float2 x[U][K][Q::P];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t n = n0 + u * t.rows + t.row;
+      const int64_t n = n0 + u * t.rows;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (t.in[k] && n < p.N) {
-          load_vec<T, V>(static_cast<const T*>(p.x) + n * p.xs[0] + t.c + k * t.step, x[u][k]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < V; ++e) x[u][k][e] = 0.f;
-        }
+        if (t.in[k] && n < p.N) Q::load(static_cast<const T*>(p.x) + n * p.xs[0] + t.c + k * t.step, x[u][k]);
+        else Q::zero(x[u][k]);
       }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t n = n0 + u * t.rows + t.row;
-      float s = 0.f;
+      const int64_t n = n0 + u * t.rows;
+      float2 s = make_float2(0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int e = 0; e < V; ++e) s += x[u][k][e];
-      const float mean = group_sum<kBlock>(s, lanes, part, phase) * inv;
-      s = 0.f;
+        for (int e = 0; e < Q::P; ++e) s = fp::add2(s, x[u][k][e]);
+      s = group_sum<kBlock>(make_float2(s.x + s.y, 0.f), lanes, part, phase);
+      const float mean = s.x * inv;
+      s = make_float2(0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        if (t.in[k]) {
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            x[u][k][e] -= mean;
-            s = fmaf(x[u][k][e], x[u][k][e], s);
-          }
+        for (int e = 0; e < Q::P; ++e) {
+          x[u][k][e] = t.in[k] ? minus2<V>(x[u][k][e], mean) : make_float2(0.f, 0.f);
+          s = fp::fma2(x[u][k][e], x[u][k][e], s);
         }
-      const float rstd = 1.f / sqrtf(group_sum<kBlock>(s, lanes, part, phase) * inv + p.eps);
+      s = group_sum<kBlock>(make_float2(s.x + s.y, 0.f), lanes, part, phase);
+      const float rstd = 1.f / sqrtf(fmaf(s.x, inv, p.eps));
       if (n >= p.N) continue;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const int64_t at = n * p.C + t.c + k * t.step;
         if (!t.in[k] || !SSD_INDEX_OK(p.hdr, at + V - 1, p.N * p.C, 70)) continue;
 #pragma unroll
-        for (int e = 0; e < V; ++e)
-          x[u][k][e] = act_fwd<kSilu>(fmaf(x[u][k][e] * rstd, w[k][e], bias[k][e]));
-        store_vec<T, V>(static_cast<T*>(p.y) + at, x[u][k]);
+        for (int e = 0; e < Q::P; ++e)
+          x[u][k][e] = act2<kSilu>(fp::fma2(fp::mul2(x[u][k][e], dup(rstd)), w[k][e], bias[k][e]));
+        Q::store(static_cast<T*>(p.y) + at, x[u][k]);
       }
       if (p.mean && t.in[0] && t.c == t.g * p.cg && SSD_INDEX_OK(p.hdr, n * p.G + t.g, p.N * p.G, 71)) {
         p.mean[n * p.G + t.g] = mean;
@@ -208,90 +255,93 @@ __global__ void __launch_bounds__(kThreads) norm_token_forward_kernel(NormParams
 
 template <typename T, int V, int K, int U, bool kBlock, bool kSilu>
 __global__ void __launch_bounds__(kThreads) norm_token_backward_kernel(NormParams p) {
-  __shared__ float part[2][kWarps];
+  using Q = Pack<T, V>;
+  __shared__ float2 part[2][kWarps];
   int phase = 0;
   const TokenSlot<V, K, kBlock> t(p);
   const int lanes = p.lanes;
-  float w[K][V], bias[K][V], dw[K][V], db[K][V];
+  float2 w[K][Q::P], bias[K][Q::P], dw[K][Q::P], db[K][Q::P];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
+    Q::zero(w[k]);
+    Q::zero(bias[k]);
+    Q::zero(dw[k]);
+    Q::zero(db[k]);
     if (t.in[k]) {
-      load_param<V>(p.w, t.c + k * t.step, 1.f, w[k]);
-      load_param<V>(p.bias, t.c + k * t.step, 0.f, bias[k]);
+      Q::param(p.w, t.c + k * t.step, 1.f, w[k]);
+      Q::param(p.bias, t.c + k * t.step, 0.f, bias[k]);
     }
-#pragma unroll
-    for (int e = 0; e < V; ++e) dw[k][e] = db[k][e] = 0.f;
   }
   const float inv = 1.f / (float)p.cg;
   const int64_t stride = (int64_t)gridDim.x * t.rows * U;
-  for (int64_t n0 = (int64_t)blockIdx.x * t.rows * U; n0 < p.N; n0 += stride) {
-    float x[U][K][V], q[U][K][V], rstd[U], mean[U];
+  for (int64_t n0 = (int64_t)blockIdx.x * t.rows * U + t.row; n0 - t.row < p.N; n0 += stride) {
+    float2 x[U][K][Q::P], q[U][K][Q::P];
+    float rstd[U], mean[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t n = n0 + u * t.rows + t.row;
+      const int64_t n = n0 + u * t.rows;
       const bool live = t.g < p.G && n < p.N;
       mean[u] = live ? __ldg(p.mean_in + n * p.G + t.g) : 0.f;
       rstd[u] = live ? __ldg(p.rstd_in + n * p.G + t.g) : 0.f;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         if (t.in[k] && n < p.N) {
-          load_vec<T, V>(static_cast<const T*>(p.x) + n * p.xs[0] + t.c + k * t.step, x[u][k]);
-          load_vec<T, V>(static_cast<const T*>(p.dy) + n * p.ds[0] + t.c + k * t.step, q[u][k]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < V; ++e) x[u][k][e] = q[u][k][e] = 0.f;
+          Q::load(static_cast<const T*>(p.x) + n * p.xs[0] + t.c + k * t.step, x[u][k]);
+          Q::load(static_cast<const T*>(p.dy) + n * p.ds[0] + t.c + k * t.step, q[u][k]);
+        } else {   // dy = 0 adds nothing anywhere
+          Q::zero(x[u][k]);
+          Q::zero(q[u][k]);
         }
       }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t n = n0 + u * t.rows + t.row;
-      float s = 0.f, sx = 0.f;
+      const int64_t n = n0 + u * t.rows;
+      float2 s = make_float2(0.f, 0.f), sx = s;
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        if (t.in[k]) {
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const float xh = (x[u][k][e] - mean[u]) * rstd[u];
-            const float dz = q[u][k][e] * act_grad<kSilu>(fmaf(xh, w[k][e], bias[k][e]));
-            db[k][e] += dz;
-            dw[k][e] = fmaf(dz, xh, dw[k][e]);
-            x[u][k][e] = xh;
-            q[u][k][e] = dz * w[k][e];
-            s += q[u][k][e];
-            sx = fmaf(q[u][k][e], xh, sx);
-          }
+        for (int e = 0; e < Q::P; ++e) {
+          const float2 xh = fp::mul2(minus2<V>(x[u][k][e], mean[u]), dup(rstd[u]));
+          const float2 dz = times_act_grad2<kSilu>(q[u][k][e], fp::fma2(xh, w[k][e], bias[k][e]));
+          db[k][e] = fp::add2(db[k][e], dz);
+          dw[k][e] = fp::fma2(dz, xh, dw[k][e]);
+          x[u][k][e] = xh;
+          q[u][k][e] = fp::mul2(dz, w[k][e]);
+          s = fp::add2(s, q[u][k][e]);
+          sx = fp::fma2(q[u][k][e], xh, sx);
         }
-      s = group_sum<kBlock>(s, lanes, part, phase) * inv;
-      sx = group_sum<kBlock>(sx, lanes, part, phase) * inv;
+      s = group_sum<kBlock>(make_float2(s.x + s.y, sx.x + sx.y), lanes, part, phase);
       if (n >= p.N) continue;
+      const float2 ms = dup(-s.x * inv), mx = dup(-s.y * inv);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const int64_t at = n * p.C + t.c + k * t.step;
         if (!t.in[k] || !SSD_INDEX_OK(p.hdr, at + V - 1, p.N * p.C, 72)) continue;
 #pragma unroll
-        for (int e = 0; e < V; ++e) x[u][k][e] = rstd[u] * (q[u][k][e] - s - x[u][k][e] * sx);
-        store_vec<T, V>(static_cast<T*>(p.dx) + at, x[u][k]);
+        for (int e = 0; e < Q::P; ++e)
+          x[u][k][e] = fp::mul2(dup(rstd[u]), fp::fma2(x[u][k][e], mx, fp::add2(q[u][k][e], ms)));
+        Q::store(static_cast<T*>(p.dx) + at, x[u][k]);
       }
     }
   }
   if (p.part_rows == 0) return;
-  __shared__ float2 rows[kThreads][V];   // the block's rows of samples joined, one partial a block
-  const int slots = (int)min((int64_t)kThreads, p.G * p.lanes);   // threads of one row
+  __shared__ float4 rows[kThreads][Q::P];   // the block's rows of samples joined, one partial a block
+  const int slots = (int)min((int64_t)kThreads, p.G * lanes);   // threads of one row
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     if (!kBlock && t.rows > 1) {
       __syncthreads();
 #pragma unroll
-      for (int e = 0; e < V; ++e) rows[threadIdx.x][e] = make_float2(dw[k][e], db[k][e]);
+      for (int e = 0; e < Q::P; ++e) rows[threadIdx.x][e] = make_float4(dw[k][e].x, dw[k][e].y, db[k][e].x, db[k][e].y);
       __syncthreads();
       if (t.row > 0) continue;
       for (int r = 1; r < t.rows; ++r) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float2 v = rows[threadIdx.x + r * slots][e];
-          dw[k][e] += v.x;
-          db[k][e] += v.y;
+        for (int e = 0; e < Q::P; ++e) {
+          const float4 v = rows[threadIdx.x + r * slots][e];
+          dw[k][e] = fp::add2(dw[k][e], make_float2(v.x, v.y));
+          db[k][e] = fp::add2(db[k][e], make_float2(v.z, v.w));
         }
       }
     }
@@ -299,17 +349,17 @@ __global__ void __launch_bounds__(kThreads) norm_token_backward_kernel(NormParam
     if (!t.in[k] || !SSD_INDEX_OK(p.hdr, at + V - 1, p.part_rows * p.C, 73)) continue;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      p.part_w[at + e] = dw[k][e];
-      p.part_b[at + e] = db[k][e];
+      p.part_w[at + e] = e % 2 ? dw[k][e / 2].y : dw[k][e / 2].x;
+      p.part_b[at + e] = e % 2 ? db[k][e / 2].y : db[k][e / 2].x;
     }
   }
 }
 
 // ------------------------------------------------------------------------------------------------
 // Many positions a sample: a sample's positions are cut into chunks, a block takes one chunk of one
-// sample by one column tile of whole groups.  Two passes over x: the chunks' statistics, then
-// their join and the output; the second pass goes through the samples backwards, so that what the
-// first read last is still in L2.
+// sample by one column tile of whole groups.  Two passes over x: the chunks' statistics, a join of
+// them by one warp a group, and the output; the second pass goes through the samples backwards, so
+// that what the first read last is still in L2.
 // ------------------------------------------------------------------------------------------------
 // count, mean and sum of squares around the mean; joined pairwise (Chan, Golub and LeVeque), so no
 // difference of large squares is formed
@@ -317,10 +367,10 @@ struct Moments {
   float n, mean, m2;
 };
 __device__ __forceinline__ Moments join(const Moments& a, const Moments& b) {
-  const float n = a.n + b.n;
   if (b.n == 0.f) return a;
-  const float f = b.n / n, d = b.mean - a.mean;
-  return {n, fmaf(d, f, a.mean), a.m2 + b.m2 + d * d * a.n * f};
+  if (a.n == 0.f) return b;
+  const float n = a.n + b.n, f = __fdividef(b.n, n), d = b.mean - a.mean;
+  return {n, fmaf(d, f, a.mean), fmaf(d * d, a.n * f, a.m2 + b.m2)};
 }
 __device__ __forceinline__ Moments join_lanes(Moments m) {
 #pragma unroll
@@ -336,16 +386,18 @@ __device__ __forceinline__ Moments join_lanes(Moments m) {
 // wider than the block) of its tile, positions row, row + rows, ... of its chunk.
 template <int V>
 struct MapSlot {
-  int64_t n, chunk, g0, groups, s0, s1;   // sample, chunk, groups of the tile, positions [s0, s1)
-  int vecs, cols, rows, row, col;         // vectors of the tile, thread columns and rows
-  __device__ __forceinline__ MapSlot(const NormParams& p, int64_t block) {
-    const int64_t tiles = (p.G + p.tile_groups - 1) / p.tile_groups;
-    const int64_t tile = block % tiles;
-    chunk = block / tiles % p.chunks;
-    n = block / tiles / p.chunks;
-    g0 = tile * p.tile_groups;
-    groups = min((int64_t)p.tile_groups, p.G - g0);
-    vecs = (int)(groups * (p.cg / V));
+  int64_t n, s0, s1;                // sample, positions [s0, s1)
+  int chunk, g0, groups;            // chunk, groups of the tile
+  int gv, vecs, cols, rows, row, col;   // vectors of a group and of the tile, thread columns and rows
+  __device__ __forceinline__ MapSlot(const NormParams& p, uint32_t block) {
+    const uint32_t tiles = ((uint32_t)p.G + p.tile_groups - 1) / p.tile_groups;
+    const uint32_t tile = block % tiles, rest = block / tiles;
+    chunk = (int)(rest % (uint32_t)p.chunks);
+    n = rest / (uint32_t)p.chunks;
+    g0 = (int)tile * p.tile_groups;
+    groups = min(p.tile_groups, (int)p.G - g0);
+    gv = (int)p.cg / V;
+    vecs = groups * gv;
     cols = min(vecs, kThreads);
     rows = kThreads / cols;
     row = threadIdx.x / cols;
@@ -358,6 +410,7 @@ struct MapSlot {
 
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) norm_map_stats_kernel(NormParams p) {
+  using Q = Pack<T, V>;
   constexpr int U = 8;   // positions in flight: their moments are formed directly, around their mean
   __shared__ Moments all[kThreads];
   const MapSlot<V> t(p, blockIdx.x);
@@ -366,104 +419,43 @@ __global__ void __launch_bounds__(kThreads) norm_map_stats_kernel(NormParams p) 
     for (int v = t.col; v < t.vecs; v += kThreads) {
       const T* x = static_cast<const T*>(p.x) + t.n * p.xs[0] + t.channel(p, v);
       for (int64_t s = t.s0 + t.row; s < t.s1; s += U * t.rows) {
-        float f[U][V], sum = 0.f, sq = 0.f;
-        int have = 0;
+        const int have = (int)min((int64_t)U, (t.s1 - s + t.rows - 1) / t.rows);
+        const T* xs = x + s * p.xs[1];
+        const int64_t pitch = t.rows * p.xs[1];
+        float2 f[U][Q::P], sum = make_float2(0.f, 0.f), sq = sum;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const bool in = s + u * t.rows < t.s1;
-          if (in) load_vec<T, V>(x + (s + u * t.rows) * p.xs[1], f[u]);
-          have += in;
+          if (u < have) Q::load(xs + u * pitch, f[u]);
+          else Q::zero(f[u]);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (u < have) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) sum += f[u][e];
-          }
-        const float n = (float)(have * V), mean = sum / n;
+          for (int e = 0; e < Q::P; ++e) sum = fp::add2(sum, f[u][e]);
+        const float n = (float)(have * V), mean = __fdividef(sum.x + sum.y, n);
 #pragma unroll
         for (int u = 0; u < U; ++u)
           if (u < have) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-              const float d = f[u][e] - mean;
-              sq = fmaf(d, d, sq);
+            for (int e = 0; e < Q::P; ++e) {
+              const float2 d = minus2<V>(f[u][e], mean);
+              sq = fp::fma2(d, d, sq);
             }
           }
-        m = m.n == 0.f ? Moments{n, mean, sq} : join(m, {n, mean, sq});
+        m = join(m, {n, mean, sq.x + sq.y});
       }
     }
   all[threadIdx.x] = m;
   __syncthreads();
   // a warp a group: its threads are columns [k per, (k + 1) per) of every row
-  const int lane = threadIdx.x % 32, per = (int)(p.cg / V) < t.cols ? (int)(p.cg / V) : t.cols;
+  const int lane = threadIdx.x % 32, per = min(t.gv, t.cols);
   for (int k = threadIdx.x / 32; k < t.groups; k += kWarps) {
     Moments g = {0.f, 0.f, 0.f};
-    for (int j = lane; j < per * t.rows; j += 32) {
-      const Moments b = all[j / per * t.cols + k * per + j % per];
-      if (b.n > 0.f) g = g.n == 0.f ? b : join(g, b);
-    }
-    // lanes without values hand theirs over unchanged
+    for (int j = lane; j < per * t.rows; j += 32) g = join(g, all[j / per * t.cols + k * per + j % per]);
     g = join_lanes(g);
-    const int64_t at = ((t.n * p.chunks + t.chunk) * p.G + t.g0 + k) * 2;
-    if (lane == 0 && SSD_INDEX_OK(p.hdr, at + 1, p.N * p.chunks * p.G * 2, 74)) {
-      p.stats[at] = g.mean;
-      p.stats[at + 1] = g.m2;
-    }
-  }
-}
-
-template <typename T, int V, bool kSilu>
-__global__ void __launch_bounds__(kThreads) norm_map_apply_kernel(NormParams p) {
-  constexpr int U = 8;
-  __shared__ float2 fin[kThreads];   // mean and rstd of the tile's groups (at most kThreads of them)
-  const MapSlot<V> t(p, (int64_t)gridDim.x - 1 - blockIdx.x);
-  const int lane = threadIdx.x % 32;
-  for (int k = threadIdx.x / 32; k < t.groups; k += kWarps) {
-    Moments m = {0.f, 0.f, 0.f};
-    for (int c = lane; c < p.chunks; c += 32) {
-      const float* s = p.stats + ((t.n * p.chunks + c) * p.G + t.g0 + k) * 2;
-      const float n = (float)(min(p.S, (c + 1) * p.chunk_rows) - c * p.chunk_rows) * (float)p.cg;
-      const Moments b = {n, __ldcg(s), __ldcg(s + 1)};
-      m = m.n == 0.f ? b : join(m, b);
-    }
-    m = join_lanes(m);
-    if (lane == 0) {
-      const float rstd = 1.f / sqrtf(m.m2 / m.n + p.eps);
-      fin[k] = make_float2(m.mean, rstd);
-      const int64_t at = t.n * p.G + t.g0 + k;
-      if (p.mean && t.chunk == 0 && SSD_INDEX_OK(p.hdr, at, p.N * p.G, 75)) {
-        p.mean[at] = m.mean;
-        p.rstd[at] = rstd;
-      }
-    }
-  }
-  __syncthreads();
-  if (t.row >= t.rows) return;
-  for (int v = t.col; v < t.vecs; v += kThreads) {
-    const int64_t c = t.channel(p, v);
-    const float2 st = fin[v / (int)(p.cg / V)];
-    float a[V], b[V];   // z = x a + b would round around a large mean: (x - mean) a + bias instead
-    load_param<V>(p.w, c, 1.f, a);
-    load_param<V>(p.bias, c, 0.f, b);
-#pragma unroll
-    for (int e = 0; e < V; ++e) a[e] *= st.y;
-    const T* x = static_cast<const T*>(p.x) + t.n * p.xs[0] + c;
-    T* y = static_cast<T*>(p.y) + t.n * p.S * p.C + c;
-    for (int64_t s = t.s0 + t.row; s < t.s1; s += U * t.rows) {
-      float f[U][V];
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (s + u * t.rows < t.s1) load_vec<T, V>(x + (s + u * t.rows) * p.xs[1], f[u]);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t r = s + u * t.rows;
-        if (r >= t.s1 || !SSD_INDEX_OK(p.hdr, (t.n * p.S + r) * p.C + c + V - 1, p.N * p.S * p.C, 76)) continue;
-#pragma unroll
-        for (int e = 0; e < V; ++e) f[u][e] = act_fwd<kSilu>(fmaf(f[u][e] - st.x, a[e], b[e]));
-        store_vec<T, V>(y + r * p.C, f[u]);
-      }
-    }
+    const int64_t at = ((t.n * p.G + t.g0 + k) * p.chunks + t.chunk) * 2;
+    if (lane == 0 && SSD_INDEX_OK(p.hdr, at + 1, p.N * p.chunks * p.G * 2, 74))
+      *reinterpret_cast<float2*>(p.stats + at) = make_float2(g.mean, g.m2);
   }
 }
 
@@ -471,42 +463,51 @@ __global__ void __launch_bounds__(kThreads) norm_map_apply_kernel(NormParams p) 
 // group their sums times w, which the gradient of x needs.
 template <typename T, int V, bool kSilu>
 __global__ void __launch_bounds__(kThreads) norm_map_grad_sums_kernel(NormParams p) {
+  using Q = Pack<T, V>;
   constexpr int U = 4;
-  __shared__ float2 all[kThreads][V];
+  __shared__ float4 all[kThreads][Q::P];
+  __shared__ float2 wide[kThreads];
   const MapSlot<V> t(p, blockIdx.x);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int gv = (int)(p.cg / V);
-  float2 wide = make_float2(0.f, 0.f);   // a group wider than the block: this thread's share of its sums
+  float2 mine = make_float2(0.f, 0.f);   // of the first row's threads: their channels' sums times w
   for (int v0 = 0; v0 < t.vecs; v0 += kThreads) {
     const int v = v0 + t.col;
-    float dw[V], db[V], w[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) dw[e] = db[e] = w[e] = 0.f;
+    float2 dw[Q::P], db[Q::P], w[Q::P];
+    Q::zero(dw);
+    Q::zero(db);
+    Q::zero(w);
     if (t.row < t.rows && v < t.vecs) {
-      const int64_t c = t.channel(p, v), at = t.n * p.G + t.g0 + v / gv;
+      const int64_t c = t.channel(p, v), at = t.n * p.G + t.g0 + v / t.gv;
       const float mean = __ldg(p.mean_in + at), rstd = __ldg(p.rstd_in + at);
-      float bias[V];
-      load_param<V>(p.w, c, 1.f, w);
-      load_param<V>(p.bias, c, 0.f, bias);
+      float2 bias[Q::P];
+      Q::param(p.w, c, 1.f, w);
+      Q::param(p.bias, c, 0.f, bias);
       const T* x = static_cast<const T*>(p.x) + t.n * p.xs[0] + c;
       const T* dy = static_cast<const T*>(p.dy) + t.n * p.ds[0] + c;
       for (int64_t s = t.s0 + t.row; s < t.s1; s += U * t.rows) {
-        float f[U][V], d[U][V];
+        const int have = (int)min((int64_t)U, (t.s1 - s + t.rows - 1) / t.rows);
+        const T *xs = x + s * p.xs[1], *ys = dy + s * p.ds[1];
+        const int64_t px = t.rows * p.xs[1], py = t.rows * p.ds[1];
+        float2 f[U][Q::P], d[U][Q::P];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (s + u * t.rows < t.s1) {
-            load_vec<T, V>(x + (s + u * t.rows) * p.xs[1], f[u]);
-            load_vec<T, V>(dy + (s + u * t.rows) * p.ds[1], d[u]);
+        for (int u = 0; u < U; ++u) {
+          if (u < have) {
+            Q::load(xs + u * px, f[u]);
+            Q::load(ys + u * py, d[u]);
+          } else {
+            Q::zero(f[u]);
+            Q::zero(d[u]);
           }
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (s + u * t.rows < t.s1) {
+          if (u < have) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-              const float xh = (f[u][e] - mean) * rstd;
-              const float dz = d[u][e] * act_grad<kSilu>(fmaf(xh, w[e], bias[e]));
-              db[e] += dz;
-              dw[e] = fmaf(dz, xh, dw[e]);
+            for (int e = 0; e < Q::P; ++e) {
+              const float2 xh = fp::mul2(minus2<V>(f[u][e], mean), dup(rstd));
+              const float2 dz = times_act_grad2<kSilu>(d[u][e], fp::fma2(xh, w[e], bias[e]));
+              db[e] = fp::add2(db[e], dz);
+              dw[e] = fp::fma2(dz, xh, dw[e]);
             }
           }
       }
@@ -514,136 +515,198 @@ __global__ void __launch_bounds__(kThreads) norm_map_grad_sums_kernel(NormParams
     // over the block's rows, per channel
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < V; ++e) all[threadIdx.x][e] = make_float2(db[e], dw[e]);
+    for (int e = 0; e < Q::P; ++e) all[threadIdx.x][e] = make_float4(db[e].x, db[e].y, dw[e].x, dw[e].y);
     __syncthreads();
     if (t.row == 0 && v < t.vecs) {
-      float2 q = make_float2(0.f, 0.f);
       const int64_t at = (t.n * p.chunks + t.chunk) * p.C + t.channel(p, v);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        float2 s = all[t.col][e];
+      for (int e = 0; e < Q::P; ++e) {
         for (int r = 1; r < t.rows; ++r) {
-          s.x += all[r * t.cols + t.col][e].x;
-          s.y += all[r * t.cols + t.col][e].y;
+          const float4 a = all[r * t.cols + t.col][e];
+          db[e] = fp::add2(db[e], make_float2(a.x, a.y));
+          dw[e] = fp::add2(dw[e], make_float2(a.z, a.w));
         }
-        if (p.part_rows > 0 && SSD_INDEX_OK(p.hdr, at + e, p.part_rows * p.C, 77)) {
-          p.part_b[at + e] = s.x;
-          p.part_w[at + e] = s.y;
+        if (p.part_rows > 0 && SSD_INDEX_OK(p.hdr, at + min(2 * e + 1, V - 1), p.part_rows * p.C, 77)) {
+          p.part_b[at + 2 * e] = db[e].x;
+          p.part_w[at + 2 * e] = dw[e].x;
+          if (V > 1) {
+            p.part_b[at + 2 * e + 1] = db[e].y;
+            p.part_w[at + 2 * e + 1] = dw[e].y;
+          }
         }
-        q.x = fmaf(s.x, w[e], q.x);
-        q.y = fmaf(s.y, w[e], q.y);
+        mine.x += fmaf(db[e].x, w[e].x, db[e].y * w[e].y);
+        mine.y += fmaf(dw[e].x, w[e].x, dw[e].y * w[e].y);
       }
-      wide.x += q.x;
-      wide.y += q.y;
     }
   }
+  wide[threadIdx.x] = mine;
   __syncthreads();
-  all[threadIdx.x][0] = wide;   // (the threads of the first row hold the sums)
-  __syncthreads();
-  const int per = gv < t.cols ? gv : t.cols;
+  const int per = min(t.gv, t.cols);
   for (int k = warp; k < t.groups; k += kWarps) {
     float2 s = make_float2(0.f, 0.f);
-    for (int j = lane; j < per; j += 32) {
-      s.x += all[k * per + j][0].x;
-      s.y += all[k * per + j][0].y;
-    }
+    for (int j = lane; j < per; j += 32) s = fp::add2(s, wide[k * per + j]);
 #pragma unroll
-    for (int o = 16; o > 0; o /= 2) {
-      s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
-      s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
+    for (int o = 16; o > 0; o /= 2)
+      s = fp::add2(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, s.y, o)));
+    const int64_t at = ((t.n * p.G + t.g0 + k) * p.chunks + t.chunk) * 2;
+    if (lane == 0 && SSD_INDEX_OK(p.hdr, at + 1, p.N * p.chunks * p.G * 2, 78))
+      *reinterpret_cast<float2*>(p.stats + at) = s;
+  }
+}
+
+// dweight and dbias of 32 channels from share `part` of `parts` of the partial rows, by a block of 32
+// warps: a warp adds every 32nd row, eight loads of each array in flight, and the warps are joined in
+// their order into row `part`.
+__device__ __forceinline__ void param_grad(const NormParams& p, int64_t cols, int part, int parts) {
+  __shared__ float2 sums[32][33];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int64_t c = cols * 32 + lane;
+  const int64_t share = (p.part_rows + parts - 1) / parts, r0 = part * share, r1 = min(p.part_rows, r0 + share);
+  float2 s = make_float2(0.f, 0.f);
+  if (c < p.C) {
+    constexpr int U = 8;
+    for (int64_t r = r0 + warp; r < r1; r += 32 * U) {
+      const float *pw = p.part_w + r * p.C + c, *pb = p.part_b + r * p.C + c;
+      float2 v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        v[u] = r + 32 * u < r1 ? make_float2(__ldg(pw + u * 32 * p.C), __ldg(pb + u * 32 * p.C))
+                               : make_float2(0.f, 0.f);
+#pragma unroll
+      for (int u = 0; u < U; ++u) s = fp::add2(s, v[u]);
     }
-    const int64_t at = ((t.n * p.chunks + t.chunk) * p.G + t.g0 + k) * 2;
-    if (lane == 0 && SSD_INDEX_OK(p.hdr, at + 1, p.N * p.chunks * p.G * 2, 78)) {
-      p.stats[at] = s.x;
-      p.stats[at + 1] = s.y;
+  }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < p.C) {
+    float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v = fp::add2(v, sums[k][lane]);
+    if (p.dw) p.dw[part * p.C + c] = v.x;
+    if (p.db) p.db[part * p.C + c] = v.y;
+  }
+}
+__global__ void __launch_bounds__(1024) norm_param_grad_kernel(NormParams p) {
+  param_grad(p, blockIdx.x, blockIdx.y, gridDim.y);
+}
+
+// One warp a (sample, group): the chunks' statistics joined into `joined` [N, G, 2]: mean and rstd, or the
+// means of q and q xhat.  The blocks behind the groups' join the parameters' gradients instead (see
+// param_grad).
+template <bool kGrad>
+__global__ void __launch_bounds__(1024) norm_map_join_kernel(NormParams p, uint32_t group_blocks) {
+  if (blockIdx.x >= group_blocks) {
+    if (kGrad) param_grad(p, blockIdx.x - group_blocks, 0, 1);
+    return;
+  }
+  const int64_t at = (int64_t)blockIdx.x * 32 + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  if (at >= p.N * p.G) return;
+  const float2* st = reinterpret_cast<const float2*>(p.stats) + at * p.chunks;
+  float2 out;
+  if (kGrad) {
+    float2 m = make_float2(0.f, 0.f);
+    for (int c = lane; c < p.chunks; c += 32) m = fp::add2(m, __ldg(st + c));
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2)
+      m = fp::add2(m, make_float2(__shfl_xor_sync(0xffffffffu, m.x, o), __shfl_xor_sync(0xffffffffu, m.y, o)));
+    const float inv = 1.f / ((float)p.S * (float)p.cg);
+    out = make_float2(m.x * inv, m.y * inv);
+  } else {
+    Moments m = {0.f, 0.f, 0.f};
+    for (int c = lane; c < p.chunks; c += 32) {
+      const float n = (float)(min(p.S, (c + 1) * p.chunk_rows) - c * p.chunk_rows) * (float)p.cg;
+      const float2 s = __ldg(st + c);
+      m = join(m, {n, s.x, s.y});
+    }
+    m = join_lanes(m);
+    out = make_float2(m.mean, 1.f / sqrtf(m.m2 / m.n + p.eps));
+    if (lane == 0 && p.mean && SSD_INDEX_OK(p.hdr, at, p.N * p.G, 75)) {
+      p.mean[at] = out.x;
+      p.rstd[at] = out.y;
+    }
+  }
+  if (lane == 0) reinterpret_cast<float2*>(p.joined)[at] = out;
+}
+
+template <typename T, int V, bool kSilu>
+__global__ void __launch_bounds__(kThreads) norm_map_apply_kernel(NormParams p) {
+  using Q = Pack<T, V>;
+  constexpr int U = 8;
+  const MapSlot<V> t(p, gridDim.x - 1 - blockIdx.x);
+  if (t.row >= t.rows) return;
+  for (int v = t.col; v < t.vecs; v += kThreads) {
+    const int64_t c = t.channel(p, v);
+    const float2 st = __ldg(reinterpret_cast<const float2*>(p.joined) + t.n * p.G + t.g0 + v / t.gv);
+    float2 a[Q::P], b[Q::P];   // (x - mean) a + b: x a + b' would round around a large mean
+    Q::param(p.w, c, 1.f, a);
+    Q::param(p.bias, c, 0.f, b);
+#pragma unroll
+    for (int e = 0; e < Q::P; ++e) a[e] = fp::mul2(a[e], dup(st.y));
+    const T* x = static_cast<const T*>(p.x) + t.n * p.xs[0] + c;
+    T* y = static_cast<T*>(p.y) + t.n * p.S * p.C + c;
+    for (int64_t s = t.s0 + t.row; s < t.s1; s += U * t.rows) {
+      const int have = (int)min((int64_t)U, (t.s1 - s + t.rows - 1) / t.rows);
+      const T* xs = x + s * p.xs[1];
+      T* ys = y + s * p.C;
+      const int64_t px = t.rows * p.xs[1], py = t.rows * p.C;
+      float2 f[U][Q::P];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u < have) Q::load(xs + u * px, f[u]);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (u >= have || !SSD_INDEX_OK(p.hdr, (ys - static_cast<T*>(p.y)) + u * py + V - 1, p.N * p.S * p.C, 76))
+          continue;
+#pragma unroll
+        for (int e = 0; e < Q::P; ++e) f[u][e] = act2<kSilu>(fp::fma2(minus2<V>(f[u][e], st.x), a[e], b[e]));
+        Q::store(ys + u * py, f[u]);
+      }
     }
   }
 }
 
 template <typename T, int V, bool kSilu>
 __global__ void __launch_bounds__(kThreads) norm_map_grad_apply_kernel(NormParams p) {
+  using Q = Pack<T, V>;
   constexpr int U = 4;
-  __shared__ float2 fin[kThreads];   // mean q and mean q xhat of the tile's groups
-  const MapSlot<V> t(p, (int64_t)gridDim.x - 1 - blockIdx.x);
-  const int lane = threadIdx.x % 32, gv = (int)(p.cg / V);
-  const float inv = 1.f / ((float)p.S * (float)p.cg);
-  for (int k = threadIdx.x / 32; k < t.groups; k += kWarps) {
-    float2 m = make_float2(0.f, 0.f);
-    for (int c = lane; c < p.chunks; c += 32) {
-      const float* s = p.stats + ((t.n * p.chunks + c) * p.G + t.g0 + k) * 2;
-      m.x += __ldcg(s);
-      m.y += __ldcg(s + 1);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) {
-      m.x += __shfl_xor_sync(0xffffffffu, m.x, o);
-      m.y += __shfl_xor_sync(0xffffffffu, m.y, o);
-    }
-    if (lane == 0) fin[k] = make_float2(m.x * inv, m.y * inv);
-  }
-  __syncthreads();
+  const MapSlot<V> t(p, gridDim.x - 1 - blockIdx.x);
   if (t.row >= t.rows) return;
   for (int v = t.col; v < t.vecs; v += kThreads) {
-    const int64_t c = t.channel(p, v), at = t.n * p.G + t.g0 + v / gv;
+    const int64_t c = t.channel(p, v), at = t.n * p.G + t.g0 + v / t.gv;
     const float mean = __ldg(p.mean_in + at), rstd = __ldg(p.rstd_in + at);
-    const float2 m = fin[v / gv];
-    float w[V], bias[V];
-    load_param<V>(p.w, c, 1.f, w);
-    load_param<V>(p.bias, c, 0.f, bias);
+    const float2 m = __ldg(reinterpret_cast<const float2*>(p.joined) + at);
+    float2 w[Q::P], bias[Q::P];
+    Q::param(p.w, c, 1.f, w);
+    Q::param(p.bias, c, 0.f, bias);
     const T* x = static_cast<const T*>(p.x) + t.n * p.xs[0] + c;
     const T* dy = static_cast<const T*>(p.dy) + t.n * p.ds[0] + c;
     T* dx = static_cast<T*>(p.dx) + t.n * p.S * p.C + c;
     for (int64_t s = t.s0 + t.row; s < t.s1; s += U * t.rows) {
-      float f[U][V], d[U][V];
+      const int have = (int)min((int64_t)U, (t.s1 - s + t.rows - 1) / t.rows);
+      const T *xs = x + s * p.xs[1], *ys = dy + s * p.ds[1];
+      T* os = dx + s * p.C;
+      const int64_t px = t.rows * p.xs[1], py = t.rows * p.ds[1], po = t.rows * p.C;
+      float2 f[U][Q::P], d[U][Q::P];
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (s + u * t.rows < t.s1) {
-          load_vec<T, V>(x + (s + u * t.rows) * p.xs[1], f[u]);
-          load_vec<T, V>(dy + (s + u * t.rows) * p.ds[1], d[u]);
+        if (u < have) {
+          Q::load(xs + u * px, f[u]);
+          Q::load(ys + u * py, d[u]);
         }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t r = s + u * t.rows;
-        if (r >= t.s1 || !SSD_INDEX_OK(p.hdr, (t.n * p.S + r) * p.C + c + V - 1, p.N * p.S * p.C, 79)) continue;
+        if (u >= have || !SSD_INDEX_OK(p.hdr, (os - static_cast<T*>(p.dx)) + u * po + V - 1, p.N * p.S * p.C, 79))
+          continue;
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float xh = (f[u][e] - mean) * rstd;
-          const float q = d[u][e] * act_grad<kSilu>(fmaf(xh, w[e], bias[e])) * w[e];
-          f[u][e] = rstd * (q - m.x - xh * m.y);
+        for (int e = 0; e < Q::P; ++e) {
+          const float2 xh = fp::mul2(minus2<V>(f[u][e], mean), dup(rstd));
+          const float2 q = fp::mul2(times_act_grad2<kSilu>(d[u][e], fp::fma2(xh, w[e], bias[e])), w[e]);
+          f[u][e] = fp::mul2(dup(rstd), fp::fma2(xh, dup(-m.y), fp::add2(q, dup(-m.x))));
         }
-        store_vec<T, V>(dx + r * p.C, f[u]);
+        Q::store(os + u * po, f[u]);
       }
     }
-  }
-}
-
-// dweight and dbias: a block takes 32 channels and its share of the partial rows (blockIdx.y of
-// gridDim.y), its warps every 32nd row each, joined in warp order into row blockIdx.y.
-__global__ void __launch_bounds__(1024) norm_param_grad_kernel(NormParams p) {
-  __shared__ float2 part[32][33];
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
-  const int64_t share = (p.part_rows + gridDim.y - 1) / gridDim.y, r0 = blockIdx.y * share;
-  const int64_t r1 = min(p.part_rows, r0 + share);
-  float2 s = make_float2(0.f, 0.f);
-  if (c < p.C) {
-#pragma unroll 8
-    for (int64_t r = r0 + warp; r < r1; r += 32) {
-      s.x += p.part_w[r * p.C + c];
-      s.y += p.part_b[r * p.C + c];
-    }
-  }
-  part[warp][lane] = s;
-  __syncthreads();
-  if (warp == 0 && c < p.C) {
-    float2 v = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < 32; ++k) {
-      v.x += part[k][lane].x;
-      v.y += part[k][lane].y;
-    }
-    if (p.dw) p.dw[blockIdx.y * p.C + c] = v.x;
-    if (p.db) p.db[blockIdx.y * p.C + c] = v.y;
   }
 }
 
@@ -686,15 +749,16 @@ ssd_status done(cudaError_t e) { return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA
 
 // How a shape runs, and where its scratch lies.  Only the sizes decide (not the pointers or the
 // device), so the workspace's size is known beforehand.
-constexpr int kGridBlocks = 152 * 8;    // blocks that a map kernel is cut into, at least
-constexpr int kTokenBlocks = 152 * 4;   // blocks of the token backward, which writes a partial row each
-constexpr int kFoldRows = 64;           // partial rows are first joined to so many where there are many
+constexpr int kGridBlocks = 152 * 4;    // blocks that a map kernel is cut into, at least
+constexpr int kTokenBlocks = 152 * 3;   // blocks of the token backward, which writes a partial row each
+constexpr int kFewRows = 1024;          // up to so many partial rows are joined at once,
+constexpr int kFoldRows = 64;           // more through so many
 constexpr int kTokenWidth = 4 * kThreads;   // vectors of a group that a token kernel holds in registers
 struct NormPlan {
   int64_t part_rows = 0;
   int32_t chunks = 1;
   int64_t chunk_rows = 1;
-  size_t stats = 0, part_w = 0, part_b = 0, total = 0;
+  size_t stats = 0, joined = 0, part_w = 0, part_b = 0, total = 0;
 };
 
 // Largest vector (in values) that divides a group.
@@ -723,6 +787,8 @@ NormPlan norm_plan(const group_norm_shape* s, bool backward) {
   size_t off = sizeof(WsHeader);
   L.stats = off;
   off = align_up(off + sizeof(float) * 2 * (size_t)(N * L.chunks * s->groups), kWsAlign);
+  L.joined = off;
+  off = align_up(off + sizeof(float) * 2 * (size_t)(N * s->groups), kWsAlign);
   if (backward) {
     // a narrower vector (rows that are not aligned) may send a token's group to the map kernels
     L.part_rows = runs_as_tokens(S, s->groups, cg) ? kTokenBlocks
@@ -754,7 +820,7 @@ int call_vec(const group_norm_shape* s, std::initializer_list<const void*> array
 cudaError_t launch_param_grad(NormParams p, cudaStream_t st) {
   if (p.part_rows == 0) return cudaSuccess;
   const unsigned grid = (unsigned)((p.C + 31) / 32);
-  if (p.part_rows > 16 * kFoldRows) {
+  if (p.part_rows > kFewRows) {
     NormParams f = p;
     f.dw = p.part_w + p.part_rows * p.C;
     f.db = p.part_b + p.part_rows * p.C;
@@ -771,25 +837,29 @@ cudaError_t launch_param_grad(NormParams p, cudaStream_t st) {
 
 template <typename T, int V, int K, bool kBlock, bool kSilu>
 cudaError_t launch_tokens(NormParams p, bool backward, cudaStream_t st) {
-  constexpr int U = K == 1 ? 4 : K == 2 ? 2 : 1;
+  constexpr int UF = K == 1 ? 4 : K == 2 ? 2 : 1, UB = K == 1 ? 2 : 1;   // samples in flight
   const int64_t gv = p.cg / V;
   p.lanes = 1;
   while (!kBlock && p.lanes < 32 && p.lanes * K < gv) p.lanes *= 2;
   const int64_t slots = p.G * p.lanes;
   const int64_t rows = kBlock || slots >= kThreads ? 1 : kThreads / slots;
   const int64_t by = kBlock ? p.G : (slots + kThreads - 1) / kThreads;
-  const int64_t steps = (p.N + rows * U - 1) / (rows * U);
-  // forward: four blocks' worth of steps an SM at a time, each going on over the samples
-  int64_t bx = std::min<int64_t>(steps, std::max<int64_t>(1, 152 * 8 / by));
   if (backward) {
-    bx = std::min<int64_t>(steps, std::max<int64_t>(1, kTokenBlocks / by));
+    const int64_t steps = (p.N + rows * UB - 1) / (rows * UB);
+    const int64_t bx = std::min<int64_t>(steps, std::max<int64_t>(1, kTokenBlocks / by));
     p.part_rows = p.dw || p.db ? bx : 0;
-    norm_token_backward_kernel<T, V, K, U, kBlock, kSilu><<<dim3((unsigned)bx, (unsigned)by), kThreads, 0, st>>>(p);
-  } else {
-    norm_token_forward_kernel<T, V, K, U, kBlock, kSilu><<<dim3((unsigned)bx, (unsigned)by), kThreads, 0, st>>>(p);
+    norm_token_backward_kernel<T, V, K, UB, kBlock, kSilu><<<dim3((unsigned)bx, (unsigned)by), kThreads, 0, st>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? launch_param_grad(p, st) : e;
   }
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess && backward ? launch_param_grad(p, st) : e;
+  auto* kernel = norm_token_forward_kernel<T, V, K, UF, kBlock, kSilu>;
+  int blocks = 0;
+  const cudaError_t e = resident_blocks(kernel, kThreads, 0, &blocks);
+  if (e != cudaSuccess) return e;
+  const int64_t steps = (p.N + rows * UF - 1) / (rows * UF);
+  const int64_t bx = std::min<int64_t>(steps, std::max<int64_t>(1, blocks / by));
+  kernel<<<dim3((unsigned)bx, (unsigned)by), kThreads, 0, st>>>(p);
+  return cudaGetLastError();
 }
 
 template <typename T, int V, bool kSilu>
@@ -806,19 +876,26 @@ cudaError_t launch_as(NormParams p, bool backward, cudaStream_t st) {
   p.tile_groups = (int32_t)tile_groups(p.G, gv);
   p.part_rows = p.dw || p.db ? p.N * p.chunks : 0;
   const unsigned grid = (unsigned)(p.N * ((p.G + p.tile_groups - 1) / p.tile_groups) * p.chunks);
+  const unsigned group_blocks = (unsigned)((p.N * p.G + 31) / 32);
   if (!backward) {
     norm_map_stats_kernel<T, V><<<grid, kThreads, 0, st>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    norm_map_join_kernel<false><<<group_blocks, 1024, 0, st>>>(p, group_blocks);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     norm_map_apply_kernel<T, V, kSilu><<<grid, kThreads, 0, st>>>(p);
     return cudaGetLastError();
   }
   norm_map_grad_sums_kernel<T, V, kSilu><<<grid, kThreads, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  // few partial rows: the join's launch takes the parameters' gradients along
+  const bool along = p.part_rows > 0 && p.part_rows <= kFewRows;
+  norm_map_join_kernel<true><<<group_blocks + (along ? (unsigned)((p.C + 31) / 32) : 0u), 1024, 0, st>>>(p, group_blocks);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   norm_map_grad_apply_kernel<T, V, kSilu><<<grid, kThreads, 0, st>>>(p);
-  e = cudaGetLastError();
-  return e == cudaSuccess ? launch_param_grad(p, st) : e;
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return along ? cudaSuccess : launch_param_grad(p, st);
 }
 
 template <typename T, int V>
@@ -832,6 +909,7 @@ cudaError_t launch(NormParams p, const group_norm_shape* s, int vec, bool backwa
   p.chunks = L.chunks;
   p.chunk_rows = L.chunk_rows;
   p.stats = reinterpret_cast<float*>(ws + L.stats);
+  p.joined = reinterpret_cast<float*>(ws + L.joined);
   p.part_w = reinterpret_cast<float*>(ws + L.part_w);
   p.part_b = reinterpret_cast<float*>(ws + L.part_b);
   p.hdr = reinterpret_cast<WsHeader*>(ws);
