@@ -3,7 +3,11 @@
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
+#include <initializer_list>
+
 #include "common.cuh"
+#include "launch.h"
 
 namespace ssd {
 namespace {
@@ -12,60 +16,335 @@ constexpr int kThreads = 256;
 
 template <typename Id>
 __device__ __forceinline__ int64_t row_of(const Id* ids, int64_t i, int64_t V) {
-  const int64_t v = (int64_t)ids[i];
+  const int64_t v = (int64_t)__ldg(ids + i);
   return v >= 0 && v < V ? v : -1;
 }
 
-// One warp per token.
-template <typename T, typename Id>
-__global__ void __launch_bounds__(kThreads) embed_forward_kernel(const Id* ids, int64_t n, const T* table,
-                                                                 int64_t V, int64_t D, float scale, T* out) {
-  const int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
-  if (i >= n) return;
-  const int64_t v = row_of(ids, i, V);
-  for (int64_t d = threadIdx.x % 32; d < D; d += 32)
-    st_from_f32(out + i * D + d, v >= 0 ? scale * ld_f32(table + v * D + d) : 0.f);
+// V values as one load or store of up to 16 bytes.
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Vec {
+  T v[V];
+};
+
+// ------------------------------------------------------------------------------------------------
+// Forward: a thread takes one vector column of U tokens at a time, all their loads in flight.  Bound by
+// memory: the distinct rows once (repeated ones come from L2) and out once.
+// ------------------------------------------------------------------------------------------------
+template <typename T, typename Id, int V>
+__global__ void __launch_bounds__(kThreads) embed_forward_kernel(const Id* ids, int64_t n, const T* table, int64_t rows,
+                                                                 int64_t D, float scale, T* out, int cols,
+                                                                 int tokens) {
+  constexpr int U = 4;   // tokens in flight
+  const int col = threadIdx.x % cols, sub = threadIdx.x / cols;   // tokens: tokens a block takes at a time
+  const int64_t d = ((int64_t)blockIdx.y * cols + col) * V;
+  if (sub >= tokens || d >= D) return;
+  for (int64_t i0 = (int64_t)blockIdx.x * tokens * U + sub; i0 < n; i0 += (int64_t)gridDim.x * tokens * U) {
+    Vec<T, V> f[U];
+    int64_t row[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) row[u] = i0 + u * tokens < n ? row_of(ids, i0 + u * tokens, rows) : -1;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (row[u] >= 0) f[u] = *reinterpret_cast<const Vec<T, V>*>(table + row[u] * D + d);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u * tokens >= n) break;
+#pragma unroll
+      for (int e = 0; e < V; ++e) st_from_f32(&f[u].v[e], row[u] >= 0 ? scale * (float)f[u].v[e] : 0.f);
+      *reinterpret_cast<Vec<T, V>*>(out + (i0 + u * tokens) * D + d) = f[u];
+    }
+  }
 }
 
-// One block per row of the table: the block looks through all ids and adds its row's tokens in
-// their order.
-template <typename T, typename Id>
-__global__ void __launch_bounds__(kThreads) embed_backward_kernel(const Id* ids, int64_t n, const T* dout,
-                                                                  int64_t V, int64_t D, float scale,
-                                                                  float* dtable) {
-  __shared__ int64_t hits[kThreads];
-  __shared__ int warp_count[kThreads / 32];
-  const int64_t v = blockIdx.x;
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  for (int64_t d = threadIdx.x; d < D; d += kThreads) dtable[v * D + d] = 0.f;
-  for (int64_t i0 = 0; i0 < n; i0 += kThreads) {
-    const int64_t i = i0 + threadIdx.x;
-    const bool hit = i < n && row_of(ids, i, V) == v;
-    const unsigned ball = __ballot_sync(0xffffffffu, hit);
-    if (lane == 0) warp_count[warp] = __popc(ball);
-    if (__syncthreads_or(hit)) {
-      int at = __popc(ball & ((1u << lane) - 1)), total = 0;
-      for (int k = 0; k < kThreads / 32; ++k) {
-        if (k < warp) at += warp_count[k];
-        total += warp_count[k];
-      }
-      if (hit) hits[at] = i;
-      __syncthreads();
-      for (int64_t d = threadIdx.x; d < D; d += kThreads) {
-        float s = dtable[v * D + d];
-        for (int k = 0; k < total; ++k) s += scale * ld_f32(dout + hits[k] * D + d);
-        dtable[v * D + d] = s;
-      }
+// ------------------------------------------------------------------------------------------------
+// Backward.
+//
+// 1. The tokens are sorted by id, stably, so that a row's tokens stand together in their order: a radix
+//    sort of 8 bits a pass (count, scan, scatter), the padding's key behind all rows.  It is short
+//    of work, so its launches take along the writing of the rows that no token has.
+// 2. A subgroup of threads takes kPiece sorted tokens and adds their rows, writing each row's sum as its
+//    run ends; a run that goes on over the ends of a piece leaves partial sums instead,
+// 3. which the piece where the run starts joins, in order.
+// Bound by memory: dout once, every row of dtable once.
+// ------------------------------------------------------------------------------------------------
+constexpr int kBins = 256;
+constexpr int kKeys = 8;                        // keys of a thread
+constexpr int kSortTile = kThreads * kKeys;     // keys of a block
+
+struct EmbedParams {
+  const void* ids;
+  int64_t n, rows, D;
+  const void* dout;
+  float scale;
+  float* dtable;
+  uint8_t* used;                 // [rows] a token has this row
+  uint32_t *key[2], *pos[2];     // sorted ping-pong; a key is the row, or `rows` for padding
+  uint32_t* hist;                // [kBins, sort tiles]
+  float *head, *tail;            // [pieces, D] partial sums
+  int32_t sort_tiles, shift;
+  int32_t in;                    // which of key/pos is read
+  int32_t piece;                 // tokens of a piece
+  int64_t pieces;
+  int64_t fill0, fill1;          // rows that this launch clears where unused
+  int32_t work_blocks;           // blocks that sort; the rest clear
+  WsHeader* hdr;
+};
+
+// Rows [fill0, fill1) without tokens are zeros; the blocks behind the sorting ones, a row a block at a
+// time.
+__device__ __forceinline__ void clear_rows(const EmbedParams& p) {
+  const int64_t step = gridDim.x - p.work_blocks;
+  const bool wide = p.D % 4 == 0 && (reinterpret_cast<uintptr_t>(p.dtable) & 15) == 0;
+  for (int64_t r = p.fill0 + blockIdx.x - p.work_blocks; r < p.fill1; r += step) {
+    if (p.used[r]) continue;
+    float* row = p.dtable + r * p.D;
+    if (!SSD_INDEX_OK(p.hdr, (r + 1) * p.D - 1, p.rows * p.D, 80)) continue;
+    if (wide) {
+      for (int64_t d = threadIdx.x; d < p.D / 4; d += kThreads)
+        reinterpret_cast<float4*>(row)[d] = make_float4(0.f, 0.f, 0.f, 0.f);
+    } else {
+      for (int64_t d = threadIdx.x; d < p.D; d += kThreads) row[d] = 0.f;
     }
+  }
+}
+
+// The digits of a block's keys.
+__device__ __forceinline__ void count_digits(const EmbedParams& p, const uint32_t (&key)[kKeys], const bool (&in)[kKeys]) {
+  __shared__ uint32_t bins[kBins];
+  bins[threadIdx.x] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kKeys; ++k)
+    if (in[k]) atomicAdd(&bins[(key[k] >> p.shift) & (kBins - 1)], 1u);
+  __syncthreads();
+  p.hist[(int64_t)threadIdx.x * p.sort_tiles + blockIdx.x] = bins[threadIdx.x];
+}
+static_assert(kBins == kThreads, "a thread a bin");
+
+// First pass: keys from ids, the rows that occur, and the lowest digits.
+template <typename Id>
+__global__ void __launch_bounds__(kThreads) embed_keys_kernel(EmbedParams p) {
+  uint32_t key[kKeys];
+  bool in[kKeys];
+#pragma unroll
+  for (int k = 0; k < kKeys; ++k) {
+    const int64_t i = (int64_t)blockIdx.x * kSortTile + k * kThreads + threadIdx.x;
+    in[k] = i < p.n;
+    const int64_t r = in[k] ? row_of(static_cast<const Id*>(p.ids), i, p.rows) : -1;
+    key[k] = r < 0 ? (uint32_t)p.rows : (uint32_t)r;
+    if (r >= 0) p.used[r] = 1;
+    if (in[k]) p.key[p.in][i] = key[k];
+  }
+  count_digits(p, key, in);
+}
+
+__global__ void __launch_bounds__(kThreads) embed_count_kernel(EmbedParams p) {
+  if ((int)blockIdx.x >= p.work_blocks) return clear_rows(p);
+  uint32_t key[kKeys];
+  bool in[kKeys];
+#pragma unroll
+  for (int k = 0; k < kKeys; ++k) {
+    const int64_t i = (int64_t)blockIdx.x * kSortTile + k * kThreads + threadIdx.x;
+    in[k] = i < p.n;
+    key[k] = in[k] ? p.key[p.in][i] : 0u;
+  }
+  count_digits(p, key, in);
+}
+
+// hist becomes its exclusive prefix sum over digits, then tiles, by one block.
+__global__ void __launch_bounds__(kThreads) embed_scan_kernel(EmbedParams p) {
+  if (blockIdx.x > 0) return clear_rows(p);
+  __shared__ uint32_t warps[kThreads / 32];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int64_t n = (int64_t)kBins * p.sort_tiles;
+  uint32_t before = 0;
+  constexpr int kPer = 8;   // neighbouring entries of a thread at a time
+  for (int64_t at = 0; at < n; at += kThreads * kPer) {
+    uint32_t v[kPer], sum = 0;
+    const int64_t i0 = at + threadIdx.x * kPer;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) v[k] = i0 + k < n ? p.hist[i0 + k] : 0u;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const uint32_t x = v[k];
+      v[k] = sum;
+      sum += x;
+    }
+    uint32_t inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) warps[warp] = inc;
+    __syncthreads();
+    uint32_t base = before + inc - sum;
+#pragma unroll
+    for (int k = 0; k < kThreads / 32; ++k) {
+      if (k < warp) base += warps[k];
+      before += warps[k];
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      if (i0 + k < n) p.hist[i0 + k] = base + v[k];
     __syncthreads();
   }
+}
+
+// Keys and positions to their places by the pass's digit, equal digits in their order: a warp takes
+// neighbouring keys, 32 at a time.
+__global__ void __launch_bounds__(kThreads) embed_scatter_kernel(EmbedParams p) {
+  if ((int)blockIdx.x >= p.work_blocks) return clear_rows(p);
+  constexpr int kW = kThreads / 32;
+  __shared__ uint32_t seen[kW][kBins];   // keys of the warp with this digit
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  for (int k = threadIdx.x; k < kW * kBins; k += kThreads) (&seen[0][0])[k] = 0;
+  __syncthreads();
+  uint32_t key[kKeys], pos[kKeys], rank[kKeys];
+  const int64_t i0 = (int64_t)blockIdx.x * kSortTile + warp * 32 * kKeys + lane;
+#pragma unroll
+  for (int k = 0; k < kKeys; ++k) {
+    const int64_t i = i0 + k * 32;
+    const bool in = i < p.n;
+    key[k] = in ? p.key[p.in][i] : 0u;
+    pos[k] = in && p.shift > 0 ? p.pos[p.in][i] : (uint32_t)i;
+  }
+#pragma unroll
+  for (int k = 0; k < kKeys; ++k) {
+    const bool in = i0 + k * 32 < p.n;
+    const uint32_t digit = in ? (key[k] >> p.shift) & (kBins - 1) : kBins;
+    const uint32_t same = __match_any_sync(0xffffffffu, digit);
+    const uint32_t had = in ? seen[warp][digit] : 0u;
+    rank[k] = had + __popc(same & ((1u << lane) - 1));
+    __syncwarp();
+    if (in && lane == __ffs(same) - 1) seen[warp][digit] = had + __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+  {   // a thread a digit: where the warps' keys of it start
+    uint32_t base = p.hist[(int64_t)threadIdx.x * p.sort_tiles + blockIdx.x];
+#pragma unroll
+    for (int k = 0; k < kW; ++k) {
+      const uint32_t c = seen[k][threadIdx.x];
+      seen[k][threadIdx.x] = base;
+      base += c;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kKeys; ++k) {
+    if (i0 + k * 32 >= p.n) continue;
+    const int64_t at = seen[warp][(key[k] >> p.shift) & (kBins - 1)] + rank[k];
+    if (!SSD_INDEX_OK(p.hdr, at, p.n, 81)) continue;
+    p.key[p.in ^ 1][at] = key[k];
+    p.pos[p.in ^ 1][at] = pos[k];
+  }
+}
+
+// A vector of fp32 values to `p`, in the widest stores its alignment takes.
+template <int V>
+__device__ __forceinline__ void store_sum(float* p, const float (&v)[V], float scale) {
+  if (V % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+#pragma unroll
+    for (int k = 0; k + 3 < V; k += 4)
+      *reinterpret_cast<float4*>(p + k) = make_float4(scale * v[k], scale * v[k + 1], scale * v[k + 2], scale * v[k + 3]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k) p[k] = scale * v[k];
+  }
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads) embed_sum_kernel(EmbedParams p, int cols, int subs) {
+  constexpr int U = 8;   // rows in flight
+  const int col = threadIdx.x % cols, sub = threadIdx.x / cols;
+  const int64_t d = ((int64_t)blockIdx.y * cols + col) * V, piece = (int64_t)blockIdx.x * subs + sub;
+  if (sub >= subs || d >= p.D || piece >= p.pieces) return;
+  const uint32_t *key = p.key[p.in], *pos = p.pos[p.in], none = (uint32_t)p.rows;
+  const int64_t j0 = piece * p.piece, j1 = min(p.n, j0 + p.piece);
+  const T* dout = static_cast<const T*>(p.dout) + d;
+  uint32_t cur = __ldg(key + j0);
+  if (cur == none) return;
+  bool open = j0 > 0 && __ldg(key + j0 - 1) == cur;   // the run in hand started in an earlier piece
+  float acc[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) acc[e] = 0.f;
+  auto flush = [&](bool goes_on) {
+    if (open) {
+      if (SSD_INDEX_OK(p.hdr, piece * p.D + d + V - 1, p.pieces * p.D, 82)) store_sum<V>(p.head + piece * p.D + d, acc, 1.f);
+    } else if (goes_on) {
+      if (SSD_INDEX_OK(p.hdr, piece * p.D + d + V - 1, p.pieces * p.D, 83)) store_sum<V>(p.tail + piece * p.D + d, acc, 1.f);
+    } else if (SSD_INDEX_OK(p.hdr, cur * p.D + d + V - 1, p.rows * p.D, 84)) {
+      store_sum<V>(p.dtable + cur * p.D + d, acc, p.scale);
+    }
+  };
+  for (int64_t j = j0; j < j1; j += U) {
+    Vec<T, V> f[U];
+    uint32_t k[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      k[u] = j + u < j1 ? __ldg(key + j + u) : none;
+      if (k[u] != none) f[u] = *reinterpret_cast<const Vec<T, V>*>(dout + (int64_t)__ldg(pos + j + u) * p.D);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (k[u] == none) break;
+      if (k[u] != cur) {
+        flush(false);
+        open = false;
+        cur = k[u];
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] += (float)f[u].v[e];
+    }
+  }
+  flush(j1 < p.n && __ldg(key + j1) == cur);
+}
+
+// Runs over more than one piece: the piece where one starts adds the heads of those after it.
+template <int V>
+__global__ void __launch_bounds__(kThreads) embed_join_kernel(EmbedParams p, int cols, int subs) {
+  constexpr int U = 8;
+  const int col = threadIdx.x % cols, sub = threadIdx.x / cols;
+  const int64_t d = ((int64_t)blockIdx.y * cols + col) * V, piece = (int64_t)blockIdx.x * subs + sub;
+  if (sub >= subs || d >= p.D || piece >= p.pieces) return;
+  const uint32_t* key = p.key[p.in];
+  const int64_t j0 = piece * p.piece, j1 = j0 + p.piece;
+  if (j1 >= p.n) return;
+  const uint32_t run = __ldg(key + j1);   // the run that crosses the piece's end, if it is in this piece
+  if (run == (uint32_t)p.rows || __ldg(key + j1 - 1) != run) return;
+  if (j0 > 0 && __ldg(key + j0 - 1) == run) return;   // it started earlier
+  float acc[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) acc[e] = p.tail[piece * p.D + d + e];
+  for (int64_t q = piece + 1;; q += U) {
+    float h[U][V];
+    bool in[U];   // the run reaches piece q + u
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t start = (q + u) * p.piece;
+      in[u] = start < p.n && __ldg(key + start) == run;
+#pragma unroll
+      for (int e = 0; e < V; ++e) h[u][e] = in[u] ? p.head[(q + u) * p.D + d + e] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (in[u]) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] += h[u][e];
+      }
+    if (!in[U - 1]) break;
+  }
+  if (SSD_INDEX_OK(p.hdr, run * p.D + d + V - 1, p.rows * p.D, 85)) store_sum<V>(p.dtable + run * p.D + d, acc, p.scale);
 }
 
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
 
 ssd_status check_sizes(int64_t n, int64_t V, int64_t D) {
   if (n < 0 || V < 1 || D < 1) return SSD_ERR_INVALID_ARG;
-  if (n > 0x7fffffffLL || V > 0x7fffffffLL || D > kMaxElems / V || (n > 0 && D > kMaxElems / n))
+  if (n > 0x7fffffffLL || V >= 0x7fffffffLL || D > kMaxElems / V || (n > 0 && D > kMaxElems / n))
     return SSD_ERR_UNSUPPORTED;
   return SSD_OK;
 }
@@ -73,21 +352,134 @@ ssd_status check_sizes(int64_t n, int64_t V, int64_t D) {
 bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
 ssd_status done(cudaError_t e) { return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA; }
 
-template <typename T, typename Id>
-cudaError_t launch_forward(const void* ids, int64_t n, const void* table, int64_t V, int64_t D, float scale,
-                           void* out, cudaStream_t st) {
-  constexpr int kWarps = kThreads / 32;
-  embed_forward_kernel<T, Id><<<(unsigned)((n + kWarps - 1) / kWarps), kThreads, 0, st>>>(
-      static_cast<const Id*>(ids), n, static_cast<const T*>(table), V, D, scale, static_cast<T*>(out));
+// Vector width (values) that every row of the arrays is aligned to, 16 bytes at most.
+int row_vec(size_t e, int64_t D, std::initializer_list<const void*> arrays) {
+  uint64_t bits = (uint64_t)D * e;
+  for (const void* a : arrays) bits |= reinterpret_cast<uintptr_t>(a);
+  int v = (int)(16 / e);
+  while (v > 1 && bits % (v * e) != 0) v /= 2;
+  return v;
+}
+
+// Threads across a row of nv vectors, and how many rows a block takes side by side.
+struct Split {
+  int cols, subs;
+  unsigned slices;
+};
+Split split_row(int64_t nv) {
+  const int64_t slices = (nv + kThreads - 1) / kThreads;
+  const int cols = (int)((nv + slices - 1) / slices);
+  return {cols, kThreads / cols, (unsigned)slices};
+}
+
+template <typename T, typename Id, int V>
+cudaError_t launch_forward_as(const void* ids, int64_t n, const void* table, int64_t rows, int64_t D, float scale,
+                              void* out, cudaStream_t st) {
+  const Split s = split_row((D + V - 1) / V);
+  auto* kernel = embed_forward_kernel<T, Id, V>;
+  int blocks = 0;
+  const cudaError_t e = resident_blocks(kernel, kThreads, 0, &blocks);
+  if (e != cudaSuccess) return e;
+  const int64_t steps = (n + s.subs * 4 - 1) / (s.subs * 4);
+  const unsigned bx = (unsigned)std::min<int64_t>(steps, std::max<int64_t>(1, 4 * blocks / s.slices));
+  kernel<<<dim3(bx, s.slices), kThreads, 0, st>>>(static_cast<const Id*>(ids), n, static_cast<const T*>(table), rows, D,
+                                                  scale, static_cast<T*>(out), s.cols, s.subs);
   return cudaGetLastError();
 }
 
 template <typename T, typename Id>
-cudaError_t launch_backward(const void* ids, int64_t n, const void* dout, int64_t V, int64_t D, float scale,
-                            float* dtable, cudaStream_t st) {
-  embed_backward_kernel<T, Id><<<(unsigned)V, kThreads, 0, st>>>(
-      static_cast<const Id*>(ids), n, static_cast<const T*>(dout), V, D, scale, dtable);
+cudaError_t launch_forward(const void* ids, int64_t n, const void* table, int64_t rows, int64_t D, float scale,
+                           void* out, cudaStream_t st) {
+  switch (row_vec(sizeof(T), D, {table, out})) {
+    case 8:
+      if constexpr (sizeof(T) == 2) return launch_forward_as<T, Id, 8>(ids, n, table, rows, D, scale, out, st);
+    case 4: return launch_forward_as<T, Id, 4>(ids, n, table, rows, D, scale, out, st);
+    case 2: return launch_forward_as<T, Id, 2>(ids, n, table, rows, D, scale, out, st);
+    default: return launch_forward_as<T, Id, 1>(ids, n, table, rows, D, scale, out, st);
+  }
+}
+
+struct EmbedLayout {
+  size_t used = 0, key[2] = {0, 0}, pos[2] = {0, 0}, hist = 0, head = 0, tail = 0, total = 0;
+  int64_t sort_tiles = 0, pieces = 0;
+  int32_t piece = 0;
+};
+EmbedLayout embed_layout(int64_t n, int64_t rows, int64_t D) {
+  EmbedLayout L;
+  L.sort_tiles = (n + kSortTile - 1) / kSortTile;
+  // pieces of 32 tokens fill the machine from a few thousand tokens on; with many tokens longer ones keep
+  // a frequent row's partial sums few
+  L.piece = 32;
+  while (L.piece < 256 && n / L.piece > 4096) L.piece *= 2;
+  L.pieces = (n + L.piece - 1) / L.piece;
+  size_t off = sizeof(WsHeader);
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes, kWsAlign);
+    return at;
+  };
+  L.used = take((size_t)rows);
+  for (int k = 0; k < 2; ++k) L.key[k] = take(sizeof(uint32_t) * (size_t)n);
+  for (int k = 0; k < 2; ++k) L.pos[k] = take(sizeof(uint32_t) * (size_t)n);
+  L.hist = take(sizeof(uint32_t) * kBins * (size_t)L.sort_tiles);
+  L.head = take(sizeof(float) * (size_t)(L.pieces * D));
+  L.tail = take(sizeof(float) * (size_t)(L.pieces * D));
+  L.total = off;
+  return L;
+}
+
+template <typename T, int V>
+cudaError_t launch_sum(const EmbedParams& p, cudaStream_t st) {
+  const Split s = split_row((p.D + V - 1) / V);
+  const dim3 grid((unsigned)((p.pieces + s.subs - 1) / s.subs), s.slices);
+  embed_sum_kernel<T, V><<<grid, kThreads, 0, st>>>(p, s.cols, s.subs);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || p.pieces < 2) return e;
+  embed_join_kernel<V><<<grid, kThreads, 0, st>>>(p, s.cols, s.subs);
   return cudaGetLastError();
+}
+
+template <typename T, typename Id>
+cudaError_t launch_backward(EmbedParams p, cudaStream_t st) {
+  cudaError_t e = cudaMemsetAsync(p.used, 0, (size_t)p.rows, st);
+  if (e != cudaSuccess) return e;
+  int bits = 1;
+  while (bits < 32 && (p.rows >> bits) != 0) bits += 1;   // of the largest key, `rows`
+  const int passes = (bits + 7) / 8, launches = 3 * passes - 1;
+  // the rows are cleared in equal shares by the launches after the first
+  int done = 0;
+  auto share = [&](int work) {
+    p.work_blocks = work;
+    p.fill0 = p.rows * done / launches;
+    p.fill1 = p.rows * (done + 1) / launches;
+    done += 1;
+    return (unsigned)(work + std::max<int64_t>(1, std::min<int64_t>(152 * 8, p.fill1 - p.fill0)));
+  };
+  p.in = 0;
+  for (int pass = 0; pass < passes; ++pass) {
+    p.shift = 8 * pass;
+    if (pass == 0) {
+      embed_keys_kernel<Id><<<(unsigned)p.sort_tiles, kThreads, 0, st>>>(p);
+    } else {
+      const unsigned grid = share(p.sort_tiles);
+      embed_count_kernel<<<grid, kThreads, 0, st>>>(p);
+    }
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    unsigned grid = share(1);
+    embed_scan_kernel<<<grid, kThreads, 0, st>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    grid = share(p.sort_tiles);
+    embed_scatter_kernel<<<grid, kThreads, 0, st>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    p.in ^= 1;
+  }
+  switch (row_vec(sizeof(T), p.D, {p.dout})) {
+    case 8:
+      if constexpr (sizeof(T) == 2) return launch_sum<T, 8>(p, st);
+    case 4: return launch_sum<T, 4>(p, st);
+    case 2: return launch_sum<T, 2>(p, st);
+    default: return launch_sum<T, 1>(p, st);
+  }
 }
 
 }  // namespace
@@ -116,7 +508,7 @@ ssd_status embedding_forward(const void* ids, int32_t ids_bits, int64_t n, const
 }
 
 size_t embedding_backward_workspace_bytes(int64_t n, int64_t vocab, int64_t dim) {
-  return check_sizes(n, vocab, dim) == SSD_OK ? sizeof(WsHeader) : 0;
+  return check_sizes(n, vocab, dim) == SSD_OK ? embed_layout(n, vocab, dim).total : 0;
 }
 
 ssd_status embedding_backward(const void* ids, int32_t ids_bits, int64_t n, const void* dout,
@@ -137,9 +529,32 @@ ssd_status embedding_backward(const void* ids, int32_t ids_bits, int64_t n, cons
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (n == 0)
     return done(cudaMemsetAsync(dtable, 0, sizeof(float) * (size_t)(vocab * dim), st));
+  const EmbedLayout L = embed_layout(n, vocab, dim);
+  char* ws = static_cast<char*>(workspace);
+  EmbedParams p;
+  memset(&p, 0, sizeof(p));
+  p.ids = ids;
+  p.n = n;
+  p.rows = vocab;
+  p.D = dim;
+  p.dout = dout;
+  p.scale = scale;
+  p.dtable = dtable;
+  p.used = reinterpret_cast<uint8_t*>(ws + L.used);
+  for (int k = 0; k < 2; ++k) {
+    p.key[k] = reinterpret_cast<uint32_t*>(ws + L.key[k]);
+    p.pos[k] = reinterpret_cast<uint32_t*>(ws + L.pos[k]);
+  }
+  p.hist = reinterpret_cast<uint32_t*>(ws + L.hist);
+  p.head = reinterpret_cast<float*>(ws + L.head);
+  p.tail = reinterpret_cast<float*>(ws + L.tail);
+  p.sort_tiles = (int32_t)L.sort_tiles;
+  p.piece = L.piece;
+  p.pieces = L.pieces;
+  p.hdr = reinterpret_cast<WsHeader*>(ws);
   auto f = bf16 ? (ids_bits == 64 ? launch_backward<__nv_bfloat16, int64_t> : launch_backward<__nv_bfloat16, int32_t>)
                 : (ids_bits == 64 ? launch_backward<float, int64_t> : launch_backward<float, int32_t>);
-  return done(f(ids, n, dout, vocab, dim, scale, dtable, st));
+  return done(f(p, st));
 }
 
 }  // extern "C"
