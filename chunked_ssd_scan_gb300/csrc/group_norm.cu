@@ -64,28 +64,45 @@ __device__ __forceinline__ float2 times_act_grad2(float2 v, float2 z) {
   return fp::mul2(v, fp::fma2(z, ss, s));
 }
 
-// V neighbouring values as one load or store of up to 16 bytes, in P pairs (V = 1: the second is 0).
+template <int kBytes>
+struct RawOf;
+template <>
+struct RawOf<16> { using type = uint4; };
+template <>
+struct RawOf<8> { using type = uint2; };
+template <>
+struct RawOf<4> { using type = uint32_t; };
+template <>
+struct RawOf<2> { using type = uint16_t; };
+
+// V neighbouring values as one load or store of up to 16 bytes (Raw, as they wait for their turn), in P
+// pairs (V = 1: the second is 0).
 template <typename T, int V>
 struct Pack {
   static constexpr int P = (V + 1) / 2;
-  static __device__ __forceinline__ void load(const T* p, float2 (&f)[P]) {
-    if constexpr (V == 1) {
-      f[0] = make_float2(ld_f32(p), 0.f);
-    } else if constexpr (sizeof(T) == 2) {
-      uint32_t u[P];
-      if constexpr (V == 8) *reinterpret_cast<uint4*>(u) = __ldg(reinterpret_cast<const uint4*>(p));
-      else if constexpr (V == 4) *reinterpret_cast<uint2*>(u) = __ldg(reinterpret_cast<const uint2*>(p));
-      else u[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-#pragma unroll
-      for (int k = 0; k < P; ++k) f[k] = make_float2(__uint_as_float(u[k] << 16), __uint_as_float(u[k] & 0xffff0000u));
-    } else {
-      if constexpr (V == 4) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(p));
-        f[0] = make_float2(v.x, v.y);
-        f[1] = make_float2(v.z, v.w);
+  using Raw = typename RawOf<V * (int)sizeof(T)>::type;
+  static __device__ __forceinline__ Raw raw(const T* p) { return __ldg(reinterpret_cast<const Raw*>(p)); }
+  static __device__ __forceinline__ Raw none() {
+    Raw r;
+    memset(&r, 0, sizeof(r));
+    return r;
+  }
+  static __device__ __forceinline__ void unpack(const Raw& r, float2 (&f)[P]) {
+    if constexpr (sizeof(T) == 2) {
+      if constexpr (V == 1) {
+        f[0] = make_float2(__uint_as_float((uint32_t)r << 16), 0.f);
       } else {
-        f[0] = __ldg(reinterpret_cast<const float2*>(p));
+        uint32_t u[P];
+        memcpy(u, &r, sizeof(r));
+#pragma unroll
+        for (int k = 0; k < P; ++k)
+          f[k] = make_float2(__uint_as_float(u[k] << 16), __uint_as_float(u[k] & 0xffff0000u));
       }
+    } else {
+      float v[2 * P] = {};
+      memcpy(v, &r, sizeof(r));
+#pragma unroll
+      for (int k = 0; k < P; ++k) f[k] = make_float2(v[2 * k], v[2 * k + 1]);
     }
   }
   static __device__ __forceinline__ void store(T* p, const float2 (&f)[P]) {
@@ -204,17 +221,25 @@ __global__ void __launch_bounds__(kThreads) norm_token_forward_kernel(NormParams
   }
   const float inv = 1.f / (float)p.cg;
   const int64_t stride = (int64_t)gridDim.x * t.rows * U;
-  for (int64_t n0 = (int64_t)blockIdx.x * t.rows * U + t.row; n0 - t.row < p.N; n0 += stride) {
+  typename Q::Raw next[U][K];   // loads in flight while the samples before them are worked on
+  auto fetch = [&](int64_t n0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        next[u][k] = t.in[k] && n0 + u * t.rows < p.N
+                         ? Q::raw(static_cast<const T*>(p.x) + (n0 + u * t.rows) * p.xs[0] + t.c + k * t.step)
+                         : Q::none();
+  };
+  int64_t n0 = (int64_t)blockIdx.x * t.rows * U + t.row;
+  fetch(n0);
+  for (; n0 - t.row < p.N; n0 += stride) {
     float2 x[U][K][Q::P];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t n = n0 + u * t.rows;
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        if (t.in[k] && n < p.N) Q::load(static_cast<const T*>(p.x) + n * p.xs[0] + t.c + k * t.step, x[u][k]);
-        else Q::zero(x[u][k]);
-      }
-    }
+      for (int k = 0; k < K; ++k) Q::unpack(next[u][k], x[u][k]);
+    fetch(n0 + stride);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t n = n0 + u * t.rows;
@@ -274,26 +299,38 @@ __global__ void __launch_bounds__(kThreads) norm_token_backward_kernel(NormParam
   }
   const float inv = 1.f / (float)p.cg;
   const int64_t stride = (int64_t)gridDim.x * t.rows * U;
-  for (int64_t n0 = (int64_t)blockIdx.x * t.rows * U + t.row; n0 - t.row < p.N; n0 += stride) {
-    float2 x[U][K][Q::P], q[U][K][Q::P];
-    float rstd[U], mean[U];
+  typename Q::Raw nx[U][K], ny[U][K];   // loads in flight; dy = 0 where there is nothing adds nothing
+  float2 nst[U];
+  auto fetch = [&](int64_t n0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t n = n0 + u * t.rows;
       const bool live = t.g < p.G && n < p.N;
-      mean[u] = live ? __ldg(p.mean_in + n * p.G + t.g) : 0.f;
-      rstd[u] = live ? __ldg(p.rstd_in + n * p.G + t.g) : 0.f;
+      nst[u] = live ? make_float2(__ldg(p.mean_in + n * p.G + t.g), __ldg(p.rstd_in + n * p.G + t.g)) : dup(0.f);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (t.in[k] && n < p.N) {
-          Q::load(static_cast<const T*>(p.x) + n * p.xs[0] + t.c + k * t.step, x[u][k]);
-          Q::load(static_cast<const T*>(p.dy) + n * p.ds[0] + t.c + k * t.step, q[u][k]);
-        } else {   // dy = 0 adds nothing anywhere
-          Q::zero(x[u][k]);
-          Q::zero(q[u][k]);
-        }
+        const bool in = t.in[k] && n < p.N;
+        nx[u][k] = in ? Q::raw(static_cast<const T*>(p.x) + n * p.xs[0] + t.c + k * t.step) : Q::none();
+        ny[u][k] = in ? Q::raw(static_cast<const T*>(p.dy) + n * p.ds[0] + t.c + k * t.step) : Q::none();
       }
     }
+  };
+  int64_t n0 = (int64_t)blockIdx.x * t.rows * U + t.row;
+  fetch(n0);
+  for (; n0 - t.row < p.N; n0 += stride) {
+    float2 x[U][K][Q::P], q[U][K][Q::P];
+    float rstd[U], mean[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      mean[u] = nst[u].x;
+      rstd[u] = nst[u].y;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        Q::unpack(nx[u][k], x[u][k]);
+        Q::unpack(ny[u][k], q[u][k]);
+      }
+    }
+    fetch(n0 + stride);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t n = n0 + u * t.rows;
@@ -408,6 +445,44 @@ struct MapSlot {
   __device__ __forceinline__ int64_t channel(const NormParams& p, int v) const { return g0 * p.cg + (int64_t)v * V; }
 };
 
+// The positions of a thread in x and dy, U of them in flight ahead of those worked on.
+template <typename T, int V, int U>
+struct Pairs {
+  using Raw = typename Pack<T, V>::Raw;
+  const T *x, *dy;
+  int64_t px, py;
+  int left;   // positions still to load
+  Raw nx[U], ny[U];
+  __device__ __forceinline__ Pairs(const NormParams& p, const MapSlot<V>& t, int64_t c)
+      : x(static_cast<const T*>(p.x) + t.n * p.xs[0] + (t.s0 + t.row) * p.xs[1] + c),
+        dy(static_cast<const T*>(p.dy) + t.n * p.ds[0] + (t.s0 + t.row) * p.ds[1] + c),
+        px(t.rows * p.xs[1]),
+        py(t.rows * p.ds[1]),
+        left((int)((t.s1 - t.s0 - t.row + t.rows - 1) / t.rows)) {}
+  __device__ __forceinline__ void fetch() {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      nx[u] = u < left ? Pack<T, V>::raw(x + u * px) : Pack<T, V>::none();
+      ny[u] = u < left ? Pack<T, V>::raw(dy + u * py) : Pack<T, V>::none();
+    }
+    x += U * px;
+    dy += U * py;
+    left -= U;
+  }
+  __device__ __forceinline__ bool pending() const { return left + U > 0; }
+  // hands over what has been loaded, and loads on; how many of them there are
+  __device__ __forceinline__ int take(Raw (&rx)[U], Raw (&ry)[U]) {
+    const int have = min(U, left + U);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      rx[u] = nx[u];
+      ry[u] = ny[u];
+    }
+    fetch();
+    return have;
+  }
+};
+
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) norm_map_stats_kernel(NormParams p) {
   using Q = Pack<T, V>;
@@ -417,21 +492,27 @@ __global__ void __launch_bounds__(kThreads) norm_map_stats_kernel(NormParams p) 
   Moments m = {0.f, 0.f, 0.f};
   if (t.row < t.rows)
     for (int v = t.col; v < t.vecs; v += kThreads) {
-      const T* x = static_cast<const T*>(p.x) + t.n * p.xs[0] + t.channel(p, v);
-      for (int64_t s = t.s0 + t.row; s < t.s1; s += U * t.rows) {
-        const int have = (int)min((int64_t)U, (t.s1 - s + t.rows - 1) / t.rows);
-        const T* xs = x + s * p.xs[1];
-        const int64_t pitch = t.rows * p.xs[1];
+      const T* x = static_cast<const T*>(p.x) + t.n * p.xs[0] + (t.s0 + t.row) * p.xs[1] + t.channel(p, v);
+      const int64_t pitch = t.rows * p.xs[1];
+      int left = (int)((t.s1 - t.s0 - t.row + t.rows - 1) / t.rows);   // positions still to load
+      typename Q::Raw next[U];
+      auto fetch = [&]() {
+#pragma unroll
+        for (int u = 0; u < U; ++u) next[u] = u < left ? Q::raw(x + u * pitch) : Q::none();
+        x += U * pitch;
+        left -= U;
+      };
+      fetch();
+      while (left + U > 0) {
+        const int have = min(U, left + U);
         float2 f[U][Q::P], sum = make_float2(0.f, 0.f), sq = sum;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          if (u < have) Q::load(xs + u * pitch, f[u]);
-          else Q::zero(f[u]);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
+          Q::unpack(next[u], f[u]);
 #pragma unroll
           for (int e = 0; e < Q::P; ++e) sum = fp::add2(sum, f[u][e]);
+        }
+        fetch();
         const float n = (float)(have * V), mean = __fdividef(sum.x + sum.y, n);
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -482,30 +563,21 @@ __global__ void __launch_bounds__(kThreads) norm_map_grad_sums_kernel(NormParams
       float2 bias[Q::P];
       Q::param(p.w, c, 1.f, w);
       Q::param(p.bias, c, 0.f, bias);
-      const T* x = static_cast<const T*>(p.x) + t.n * p.xs[0] + c;
-      const T* dy = static_cast<const T*>(p.dy) + t.n * p.ds[0] + c;
-      for (int64_t s = t.s0 + t.row; s < t.s1; s += U * t.rows) {
-        const int have = (int)min((int64_t)U, (t.s1 - s + t.rows - 1) / t.rows);
-        const T *xs = x + s * p.xs[1], *ys = dy + s * p.ds[1];
-        const int64_t px = t.rows * p.xs[1], py = t.rows * p.ds[1];
-        float2 f[U][Q::P], d[U][Q::P];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (u < have) {
-            Q::load(xs + u * px, f[u]);
-            Q::load(ys + u * py, d[u]);
-          } else {
-            Q::zero(f[u]);
-            Q::zero(d[u]);
-          }
-        }
+      Pairs<T, V, U> in(p, t, c);
+      in.fetch();
+      while (in.pending()) {
+        typename Q::Raw rx[U], ry[U];
+        const int have = in.take(rx, ry);
 #pragma unroll
         for (int u = 0; u < U; ++u)
           if (u < have) {
+            float2 f[Q::P], d[Q::P];
+            Q::unpack(rx[u], f);
+            Q::unpack(ry[u], d);
 #pragma unroll
             for (int e = 0; e < Q::P; ++e) {
-              const float2 xh = fp::mul2(minus2<V>(f[u][e], mean), dup(rstd));
-              const float2 dz = times_act_grad2<kSilu>(d[u][e], fp::fma2(xh, w[e], bias[e]));
+              const float2 xh = fp::mul2(minus2<V>(f[e], mean), dup(rstd));
+              const float2 dz = times_act_grad2<kSilu>(d[e], fp::fma2(xh, w[e], bias[e]));
               db[e] = fp::add2(db[e], dz);
               dw[e] = fp::fma2(dz, xh, dw[e]);
             }
@@ -643,24 +715,33 @@ __global__ void __launch_bounds__(kThreads) norm_map_apply_kernel(NormParams p) 
     Q::param(p.bias, c, 0.f, b);
 #pragma unroll
     for (int e = 0; e < Q::P; ++e) a[e] = fp::mul2(a[e], dup(st.y));
-    const T* x = static_cast<const T*>(p.x) + t.n * p.xs[0] + c;
-    T* y = static_cast<T*>(p.y) + t.n * p.S * p.C + c;
-    for (int64_t s = t.s0 + t.row; s < t.s1; s += U * t.rows) {
-      const int have = (int)min((int64_t)U, (t.s1 - s + t.rows - 1) / t.rows);
-      const T* xs = x + s * p.xs[1];
-      T* ys = y + s * p.C;
-      const int64_t px = t.rows * p.xs[1], py = t.rows * p.C;
-      float2 f[U][Q::P];
+    const T* x = static_cast<const T*>(p.x) + t.n * p.xs[0] + (t.s0 + t.row) * p.xs[1] + c;
+    T* y = static_cast<T*>(p.y) + (t.n * p.S + t.s0 + t.row) * p.C + c;
+    const int64_t pitch = t.rows * p.xs[1], out = t.rows * p.C;
+    int left = (int)((t.s1 - t.s0 - t.row + t.rows - 1) / t.rows);
+    typename Q::Raw next[U];
+    auto fetch = [&]() {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (u < have) Q::load(xs + u * px, f[u]);
+      for (int u = 0; u < U; ++u) next[u] = u < left ? Q::raw(x + u * pitch) : Q::none();
+      x += U * pitch;
+      left -= U;
+    };
+    fetch();
+    while (left + U > 0) {
+      const int have = min(U, left + U);
+      typename Q::Raw now[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) now[u] = next[u];
+      fetch();
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (u >= have || !SSD_INDEX_OK(p.hdr, (ys - static_cast<T*>(p.y)) + u * py + V - 1, p.N * p.S * p.C, 76))
-          continue;
+        if (u >= have || !SSD_INDEX_OK(p.hdr, (y - static_cast<T*>(p.y)) + V - 1, p.N * p.S * p.C, 76)) continue;
+        float2 f[Q::P];
+        Q::unpack(now[u], f);
 #pragma unroll
-        for (int e = 0; e < Q::P; ++e) f[u][e] = act2<kSilu>(fp::fma2(minus2<V>(f[u][e], st.x), a[e], b[e]));
-        Q::store(ys + u * py, f[u]);
+        for (int e = 0; e < Q::P; ++e) f[e] = act2<kSilu>(fp::fma2(minus2<V>(f[e], st.x), a[e], b[e]));
+        Q::store(y, f);
+        y += out;
       }
     }
   }
@@ -679,32 +760,27 @@ __global__ void __launch_bounds__(kThreads) norm_map_grad_apply_kernel(NormParam
     float2 w[Q::P], bias[Q::P];
     Q::param(p.w, c, 1.f, w);
     Q::param(p.bias, c, 0.f, bias);
-    const T* x = static_cast<const T*>(p.x) + t.n * p.xs[0] + c;
-    const T* dy = static_cast<const T*>(p.dy) + t.n * p.ds[0] + c;
-    T* dx = static_cast<T*>(p.dx) + t.n * p.S * p.C + c;
-    for (int64_t s = t.s0 + t.row; s < t.s1; s += U * t.rows) {
-      const int have = (int)min((int64_t)U, (t.s1 - s + t.rows - 1) / t.rows);
-      const T *xs = x + s * p.xs[1], *ys = dy + s * p.ds[1];
-      T* os = dx + s * p.C;
-      const int64_t px = t.rows * p.xs[1], py = t.rows * p.ds[1], po = t.rows * p.C;
-      float2 f[U][Q::P], d[U][Q::P];
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (u < have) {
-          Q::load(xs + u * px, f[u]);
-          Q::load(ys + u * py, d[u]);
-        }
+    T* dx = static_cast<T*>(p.dx) + (t.n * p.S + t.s0 + t.row) * p.C + c;
+    const int64_t out = t.rows * p.C;
+    Pairs<T, V, U> in(p, t, c);
+    in.fetch();
+    while (in.pending()) {
+      typename Q::Raw rx[U], ry[U];
+      const int have = in.take(rx, ry);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (u >= have || !SSD_INDEX_OK(p.hdr, (os - static_cast<T*>(p.dx)) + u * po + V - 1, p.N * p.S * p.C, 79))
-          continue;
+        if (u >= have || !SSD_INDEX_OK(p.hdr, (dx - static_cast<T*>(p.dx)) + V - 1, p.N * p.S * p.C, 79)) continue;
+        float2 f[Q::P], d[Q::P];
+        Q::unpack(rx[u], f);
+        Q::unpack(ry[u], d);
 #pragma unroll
         for (int e = 0; e < Q::P; ++e) {
-          const float2 xh = fp::mul2(minus2<V>(f[u][e], mean), dup(rstd));
-          const float2 q = fp::mul2(times_act_grad2<kSilu>(d[u][e], fp::fma2(xh, w[e], bias[e])), w[e]);
-          f[u][e] = fp::mul2(dup(rstd), fp::fma2(xh, dup(-m.y), fp::add2(q, dup(-m.x))));
+          const float2 xh = fp::mul2(minus2<V>(f[e], mean), dup(rstd));
+          const float2 q = fp::mul2(times_act_grad2<kSilu>(d[e], fp::fma2(xh, w[e], bias[e])), w[e]);
+          f[e] = fp::mul2(dup(rstd), fp::fma2(xh, dup(-m.y), fp::add2(q, dup(-m.x))));
         }
-        Q::store(os + u * po, f[u]);
+        Q::store(dx, f);
+        dx += out;
       }
     }
   }
@@ -750,7 +826,7 @@ ssd_status done(cudaError_t e) { return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA
 // How a shape runs, and where its scratch lies.  Only the sizes decide (not the pointers or the
 // device), so the workspace's size is known beforehand.
 constexpr int kGridBlocks = 152 * 4;    // blocks that a map kernel is cut into, at least
-constexpr int kTokenBlocks = 152 * 3;   // blocks of the token backward, which writes a partial row each
+constexpr int kTokenBlocks = 152 * 4;   // most blocks of the token backward, which writes a partial row each
 constexpr int kFewRows = 1024;          // up to so many partial rows are joined at once,
 constexpr int kFoldRows = 64;           // more through so many
 constexpr int kTokenWidth = 4 * kThreads;   // vectors of a group that a token kernel holds in registers
@@ -846,10 +922,15 @@ cudaError_t launch_tokens(NormParams p, bool backward, cudaStream_t st) {
   const int64_t by = kBlock ? p.G : (slots + kThreads - 1) / kThreads;
   if (backward) {
     const int64_t steps = (p.N + rows * UB - 1) / (rows * UB);
-    const int64_t bx = std::min<int64_t>(steps, std::max<int64_t>(1, kTokenBlocks / by));
+    auto* kernel = norm_token_backward_kernel<T, V, K, UB, kBlock, kSilu>;
+    int blocks = 0;
+    cudaError_t e = resident_blocks(kernel, kThreads, 0, &blocks);
+    if (e != cudaSuccess) return e;
+    blocks = std::min(blocks, kTokenBlocks);
+    const int64_t bx = std::min<int64_t>(steps, std::max<int64_t>(1, blocks / by));
     p.part_rows = p.dw || p.db ? bx : 0;
-    norm_token_backward_kernel<T, V, K, UB, kBlock, kSilu><<<dim3((unsigned)bx, (unsigned)by), kThreads, 0, st>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    kernel<<<dim3((unsigned)bx, (unsigned)by), kThreads, 0, st>>>(p);
+    e = cudaGetLastError();
     return e == cudaSuccess ? launch_param_grad(p, st) : e;
   }
   auto* kernel = norm_token_forward_kernel<T, V, K, UF, kBlock, kSilu>;
