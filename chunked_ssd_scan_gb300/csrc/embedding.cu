@@ -38,20 +38,28 @@ __global__ void __launch_bounds__(kThreads) embed_forward_kernel(const Id* ids, 
   const int col = threadIdx.x % cols, sub = threadIdx.x / cols;   // tokens: tokens a block takes at a time
   const int64_t d = ((int64_t)blockIdx.y * cols + col) * V;
   if (sub >= tokens || d >= D) return;
-  for (int64_t i0 = (int64_t)blockIdx.x * tokens * U + sub; i0 < n; i0 += (int64_t)gridDim.x * tokens * U) {
+  const int64_t step = (int64_t)gridDim.x * tokens * U;
+  int64_t next[U];   // the rows of the tokens after these
+  auto fetch = [&](int64_t i0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) next[u] = i0 + u * tokens < n ? row_of(ids, i0 + u * tokens, rows) : -1;
+  };
+  int64_t i0 = (int64_t)blockIdx.x * tokens * U + sub;
+  fetch(i0);
+  for (; i0 < n; i0 += step) {
     Vec<T, V> f[U];
     int64_t row[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) row[u] = i0 + u * tokens < n ? row_of(ids, i0 + u * tokens, rows) : -1;
-#pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+      row[u] = next[u];
       if (row[u] >= 0) f[u] = *reinterpret_cast<const Vec<T, V>*>(table + row[u] * D + d);
+    }
+    fetch(i0 + step);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (i0 + u * tokens >= n) break;
 #pragma unroll
       for (int e = 0; e < V; ++e) st_from_f32(&f[u].v[e], row[u] >= 0 ? scale * (float)f[u].v[e] : 0.f);
-      *reinterpret_cast<Vec<T, V>*>(out + (i0 + u * tokens) * D + d) = f[u];
+      if (i0 + u * tokens < n) *reinterpret_cast<Vec<T, V>*>(out + (i0 + u * tokens) * D + d) = f[u];
     }
   }
 }
@@ -254,59 +262,73 @@ __device__ __forceinline__ void store_sum(float* p, const float (&v)[V], float s
   }
 }
 
+// A thread's vector of one row to its own place in shared memory, asynchronously where it has 4 bytes or
+// more (it alone reads it there).
+template <int kBytes>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  if constexpr (kBytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+  else if constexpr (kBytes == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(src) : "memory");
+  else if constexpr (kBytes == 4) asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(src) : "memory");
+  else *static_cast<uint16_t*>(dst) = *static_cast<const uint16_t*>(src);
+}
+
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) embed_sum_kernel(EmbedParams p, int cols, int subs) {
-  constexpr int U = 8;   // rows in flight
+  constexpr int kRing = 12;   // rows in flight: 48 KB a block, four blocks an SM
+  __shared__ Vec<T, V> ring[kRing][kThreads];
   const int col = threadIdx.x % cols, sub = threadIdx.x / cols;
   const int64_t d = ((int64_t)blockIdx.y * cols + col) * V, piece = (int64_t)blockIdx.x * subs + sub;
   if (sub >= subs || d >= p.D || piece >= p.pieces) return;
-  const uint32_t *key = p.key[p.in], *pos = p.pos[p.in], none = (uint32_t)p.rows;
-  const int64_t j0 = piece * p.piece, j1 = min(p.n, j0 + p.piece);
+  const uint32_t none = (uint32_t)p.rows;
+  const int64_t j0 = piece * p.piece;
+  const int n = (int)min((int64_t)p.piece, p.n - j0);
+  const uint32_t *key = p.key[p.in] + j0, *pos = p.pos[p.in] + j0;
   const T* dout = static_cast<const T*>(p.dout) + d;
-  uint32_t cur = __ldg(key + j0);
+  uint32_t cur = __ldg(key);
   if (cur == none) return;
-  bool open = j0 > 0 && __ldg(key + j0 - 1) == cur;   // the run in hand started in an earlier piece
+  bool open = j0 > 0 && __ldg(key - 1) == cur;   // the run in hand started in an earlier piece
   float acc[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) acc[e] = 0.f;
   auto flush = [&](bool goes_on) {
-    if (open) {
-      if (SSD_INDEX_OK(p.hdr, piece * p.D + d + V - 1, p.pieces * p.D, 82)) store_sum<V>(p.head + piece * p.D + d, acc, 1.f);
-    } else if (goes_on) {
-      if (SSD_INDEX_OK(p.hdr, piece * p.D + d + V - 1, p.pieces * p.D, 83)) store_sum<V>(p.tail + piece * p.D + d, acc, 1.f);
-    } else if (SSD_INDEX_OK(p.hdr, cur * p.D + d + V - 1, p.rows * p.D, 84)) {
-      store_sum<V>(p.dtable + cur * p.D + d, acc, p.scale);
-    }
+    float* to = open ? p.head + piece * p.D : goes_on ? p.tail + piece * p.D : p.dtable + cur * p.D;
+    const bool whole = !open && !goes_on;
+    if (SSD_INDEX_OK(p.hdr, (whole ? cur : piece) * p.D + d + V - 1, (whole ? p.rows : p.pieces) * p.D, 82))
+      store_sum<V>(to + d, acc, whole ? p.scale : 1.f);
   };
-  for (int64_t j = j0; j < j1; j += U) {
-    Vec<T, V> f[U];
-    uint32_t k[U];
+  auto request = [&](int j, int slot) {
+    if (j < n) copy_async<V * (int)sizeof(T)>(&ring[slot][threadIdx.x], dout + (int64_t)__ldg(pos + j) * p.D);
+    cp_async_commit();
+  };
+  for (int j = 0; j < kRing; ++j) request(j, j);
+  int slot = 0;
+  for (int j = 0; j < n; ++j) {
+    const uint32_t k = __ldg(key + j);
+    if (k == none) break;   // padding stands behind all rows
+    if (k != cur) {
+      flush(false);
+      open = false;
+      cur = k;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      k[u] = j + u < j1 ? __ldg(key + j + u) : none;
-      if (k[u] != none) f[u] = *reinterpret_cast<const Vec<T, V>*>(dout + (int64_t)__ldg(pos + j + u) * p.D);
+      for (int e = 0; e < V; ++e) acc[e] = 0.f;
     }
+    cp_async_wait<kRing - 1>();
+    const Vec<T, V> f = ring[slot][threadIdx.x];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (k[u] == none) break;
-      if (k[u] != cur) {
-        flush(false);
-        open = false;
-        cur = k[u];
-#pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = 0.f;
-      }
-#pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] += (float)f[u].v[e];
-    }
+    for (int e = 0; e < V; ++e) acc[e] += (float)f.v[e];
+    request(j + kRing, slot);
+    slot = slot + 1 == kRing ? 0 : slot + 1;
   }
-  flush(j1 < p.n && __ldg(key + j1) == cur);
+  cp_async_wait_all();
+  flush(j0 + n < p.n && __ldg(key + n) == cur);
 }
 
-// Runs over more than one piece: the piece where one starts adds the heads of those after it.
+// Runs over more than one piece: the piece where one starts adds the heads of those after it.  Keys and
+// heads are asked for together (a head that is not the run's is not used), sixteen pieces at a time.
 template <int V>
 __global__ void __launch_bounds__(kThreads) embed_join_kernel(EmbedParams p, int cols, int subs) {
-  constexpr int U = 8;
+  constexpr int U = 16;
   const int col = threadIdx.x % cols, sub = threadIdx.x / cols;
   const int64_t d = ((int64_t)blockIdx.y * cols + col) * V, piece = (int64_t)blockIdx.x * subs + sub;
   if (sub >= subs || d >= p.D || piece >= p.pieces) return;
@@ -314,30 +336,28 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(EmbedParams p, int
   const int64_t j0 = piece * p.piece, j1 = j0 + p.piece;
   if (j1 >= p.n) return;
   const uint32_t run = __ldg(key + j1);   // the run that crosses the piece's end, if it is in this piece
-  if (run == (uint32_t)p.rows || __ldg(key + j1 - 1) != run) return;
-  if (j0 > 0 && __ldg(key + j0 - 1) == run) return;   // it started earlier
-  float acc[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) acc[e] = p.tail[piece * p.D + d + e];
+  const uint32_t last = __ldg(key + j1 - 1), early = j0 > 0 ? __ldg(key + j0 - 1) : (uint32_t)p.rows;
+  if (run == (uint32_t)p.rows || last != run || early == run) return;   // or it started earlier
+  using F = Vec<float, V>;
+  F acc = *reinterpret_cast<const F*>(p.tail + piece * p.D + d);
   for (int64_t q = piece + 1;; q += U) {
-    float h[U][V];
+    F h[U];
     bool in[U];   // the run reaches piece q + u
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t start = (q + u) * p.piece;
-      in[u] = start < p.n && __ldg(key + start) == run;
-#pragma unroll
-      for (int e = 0; e < V; ++e) h[u][e] = in[u] ? p.head[(q + u) * p.D + d + e] : 0.f;
+      in[u] = q + u < p.pieces;
+      if (in[u]) {
+        h[u] = *reinterpret_cast<const F*>(p.head + (q + u) * p.D + d);
+        in[u] = __ldg(key + (q + u) * p.piece) == run;
+      }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (in[u]) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] += h[u][e];
-      }
+      for (int e = 0; e < V; ++e) acc.v[e] += in[u] ? h[u].v[e] : 0.f;
     if (!in[U - 1]) break;
   }
-  if (SSD_INDEX_OK(p.hdr, run * p.D + d + V - 1, p.rows * p.D, 85)) store_sum<V>(p.dtable + run * p.D + d, acc, p.scale);
+  if (SSD_INDEX_OK(p.hdr, run * p.D + d + V - 1, p.rows * p.D, 85)) store_sum<V>(p.dtable + run * p.D + d, acc.v, p.scale);
 }
 
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
@@ -381,7 +401,7 @@ cudaError_t launch_forward_as(const void* ids, int64_t n, const void* table, int
   const cudaError_t e = resident_blocks(kernel, kThreads, 0, &blocks);
   if (e != cudaSuccess) return e;
   const int64_t steps = (n + s.subs * 4 - 1) / (s.subs * 4);
-  const unsigned bx = (unsigned)std::min<int64_t>(steps, std::max<int64_t>(1, 4 * blocks / s.slices));
+  const unsigned bx = (unsigned)std::min<int64_t>(steps, std::max<int64_t>(1, blocks / s.slices));
   kernel<<<dim3(bx, s.slices), kThreads, 0, st>>>(static_cast<const Id*>(ids), n, static_cast<const T*>(table), rows, D,
                                                   scale, static_cast<T*>(out), s.cols, s.subs);
   return cudaGetLastError();
@@ -435,7 +455,12 @@ cudaError_t launch_sum(const EmbedParams& p, cudaStream_t st) {
   embed_sum_kernel<T, V><<<grid, kThreads, 0, st>>>(p, s.cols, s.subs);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.pieces < 2) return e;
-  embed_join_kernel<V><<<grid, kThreads, 0, st>>>(p, s.cols, s.subs);
+  // the partial rows are aligned as the width is
+  const int v = p.D % 4 == 0 ? 4 : p.D % 2 == 0 ? 2 : 1;
+  const Split js = split_row(p.D / v);
+  const dim3 jgrid((unsigned)((p.pieces + js.subs - 1) / js.subs), js.slices);
+  auto* join = v == 4 ? embed_join_kernel<4> : v == 2 ? embed_join_kernel<2> : embed_join_kernel<1>;
+  join<<<jgrid, kThreads, 0, st>>>(p, js.cols, js.subs);
   return cudaGetLastError();
 }
 

@@ -150,23 +150,32 @@ __device__ __forceinline__ float2 minus2(float2 a, float b) {
 // samples that its block takes, so weight and bias are read once, and has U samples in flight.
 // Bound by memory: x and y once each.
 // ------------------------------------------------------------------------------------------------
-template <bool kBlock>
-__device__ __forceinline__ float2 group_sum(float2 v, int lanes, float2 (&part)[2][kWarps], int& phase) {
+template <bool kBlock, int M>
+__device__ __forceinline__ void group_sum(float (&v)[M], int lanes, float (&part)[2][kWarps][M], int& phase) {
   if (!kBlock) {
-    for (int o = lanes / 2; o > 0; o /= 2)
-      v = fp::add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
-    return v;
+    for (int o = lanes / 2; o > 0; o /= 2) {
+#pragma unroll
+      for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(0xffffffffu, v[m], o);
+    }
+    return;
   }
 #pragma unroll
-  for (int o = 16; o > 0; o /= 2)
-    v = fp::add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
-  if (threadIdx.x % 32 == 0) part[phase][threadIdx.x / 32] = v;
-  __syncthreads();
-  float2 s = part[phase][0];
+  for (int o = 16; o > 0; o /= 2) {
 #pragma unroll
-  for (int k = 1; k < kWarps; ++k) s = fp::add2(s, part[phase][k]);
+    for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(0xffffffffu, v[m], o);
+  }
+  if (threadIdx.x % 32 == 0) {
+#pragma unroll
+    for (int m = 0; m < M; ++m) part[phase][threadIdx.x / 32][m] = v[m];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    v[m] = part[phase][0][m];
+#pragma unroll
+    for (int k = 1; k < kWarps; ++k) v[m] += part[phase][k][m];
+  }
   phase ^= 1;   // the next sum writes elsewhere, and its barrier ends the reads of this one
-  return s;
 }
 
 // What a thread of a token kernel works on.
@@ -205,7 +214,7 @@ struct TokenSlot {
 template <typename T, int V, int K, int U, bool kBlock, bool kSilu>
 __global__ void __launch_bounds__(kThreads) norm_token_forward_kernel(NormParams p) {
   using Q = Pack<T, V>;
-  __shared__ float2 part[2][kWarps];
+  __shared__ float part[2][kWarps][U];
   int phase = 0;
   const TokenSlot<V, K, kBlock> t(p);
   const int lanes = p.lanes;
@@ -233,8 +242,10 @@ __global__ void __launch_bounds__(kThreads) norm_token_forward_kernel(NormParams
   };
   int64_t n0 = (int64_t)blockIdx.x * t.rows * U + t.row;
   fetch(n0);
+  const bool first = p.mean && t.in[0] && t.c == t.g * p.cg;   // the lane that writes the statistics
   for (; n0 - t.row < p.N; n0 += stride) {
     float2 x[U][K][Q::P];
+    float mean[U], rstd[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -242,37 +253,49 @@ __global__ void __launch_bounds__(kThreads) norm_token_forward_kernel(NormParams
     fetch(n0 + stride);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t n = n0 + u * t.rows;
       float2 s = make_float2(0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int e = 0; e < Q::P; ++e) s = fp::add2(s, x[u][k][e]);
-      s = group_sum<kBlock>(make_float2(s.x + s.y, 0.f), lanes, part, phase);
-      const float mean = s.x * inv;
-      s = make_float2(0.f, 0.f);
+      mean[u] = s.x + s.y;
+    }
+    group_sum<kBlock>(mean, lanes, part, phase);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      mean[u] *= inv;
+      float2 s = make_float2(0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int e = 0; e < Q::P; ++e) {
-          x[u][k][e] = t.in[k] ? minus2<V>(x[u][k][e], mean) : make_float2(0.f, 0.f);
+          x[u][k][e] = t.in[k] ? minus2<V>(x[u][k][e], mean[u]) : make_float2(0.f, 0.f);
           s = fp::fma2(x[u][k][e], x[u][k][e], s);
         }
-      s = group_sum<kBlock>(make_float2(s.x + s.y, 0.f), lanes, part, phase);
-      const float rstd = 1.f / sqrtf(fmaf(s.x, inv, p.eps));
-      if (n >= p.N) continue;
+      rstd[u] = s.x + s.y;
+    }
+    group_sum<kBlock>(rstd, lanes, part, phase);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      rstd[u] = rsqrtf(fmaf(rstd[u], inv, p.eps));
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < Q::P; ++e)
+          x[u][k][e] = act2<kSilu>(fp::fma2(fp::mul2(x[u][k][e], dup(rstd[u])), w[k][e], bias[k][e]));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t n = n0 + u * t.rows;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const int64_t at = n * p.C + t.c + k * t.step;
-        if (!t.in[k] || !SSD_INDEX_OK(p.hdr, at + V - 1, p.N * p.C, 70)) continue;
-#pragma unroll
-        for (int e = 0; e < Q::P; ++e)
-          x[u][k][e] = act2<kSilu>(fp::fma2(fp::mul2(x[u][k][e], dup(rstd)), w[k][e], bias[k][e]));
-        Q::store(static_cast<T*>(p.y) + at, x[u][k]);
+        if (t.in[k] && n < p.N && SSD_INDEX_OK(p.hdr, at + V - 1, p.N * p.C, 70))
+          Q::store(static_cast<T*>(p.y) + at, x[u][k]);
       }
-      if (p.mean && t.in[0] && t.c == t.g * p.cg && SSD_INDEX_OK(p.hdr, n * p.G + t.g, p.N * p.G, 71)) {
-        p.mean[n * p.G + t.g] = mean;
-        p.rstd[n * p.G + t.g] = rstd;
+      if (first && n < p.N && SSD_INDEX_OK(p.hdr, n * p.G + t.g, p.N * p.G, 71)) {
+        p.mean[n * p.G + t.g] = mean[u];
+        p.rstd[n * p.G + t.g] = rstd[u];
       }
     }
   }
@@ -281,7 +304,7 @@ __global__ void __launch_bounds__(kThreads) norm_token_forward_kernel(NormParams
 template <typename T, int V, int K, int U, bool kBlock, bool kSilu>
 __global__ void __launch_bounds__(kThreads) norm_token_backward_kernel(NormParams p) {
   using Q = Pack<T, V>;
-  __shared__ float2 part[2][kWarps];
+  __shared__ float part[2][kWarps][2 * U];
   int phase = 0;
   const TokenSlot<V, K, kBlock> t(p);
   const int lanes = p.lanes;
@@ -319,7 +342,7 @@ __global__ void __launch_bounds__(kThreads) norm_token_backward_kernel(NormParam
   fetch(n0);
   for (; n0 - t.row < p.N; n0 += stride) {
     float2 x[U][K][Q::P], q[U][K][Q::P];
-    float rstd[U], mean[U];
+    float rstd[U], mean[U], sums[2 * U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       mean[u] = nst[u].x;
@@ -333,7 +356,6 @@ __global__ void __launch_bounds__(kThreads) norm_token_backward_kernel(NormParam
     fetch(n0 + stride);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t n = n0 + u * t.rows;
       float2 s = make_float2(0.f, 0.f), sx = s;
 #pragma unroll
       for (int k = 0; k < K; ++k)
@@ -348,17 +370,22 @@ __global__ void __launch_bounds__(kThreads) norm_token_backward_kernel(NormParam
           s = fp::add2(s, q[u][k][e]);
           sx = fp::fma2(q[u][k][e], xh, sx);
         }
-      s = group_sum<kBlock>(make_float2(s.x + s.y, sx.x + sx.y), lanes, part, phase);
-      if (n >= p.N) continue;
-      const float2 ms = dup(-s.x * inv), mx = dup(-s.y * inv);
+      sums[2 * u] = s.x + s.y;
+      sums[2 * u + 1] = sx.x + sx.y;
+    }
+    group_sum<kBlock>(sums, lanes, part, phase);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t n = n0 + u * t.rows;
+      const float2 ms = dup(-sums[2 * u] * inv), mx = dup(-sums[2 * u + 1] * inv);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const int64_t at = n * p.C + t.c + k * t.step;
-        if (!t.in[k] || !SSD_INDEX_OK(p.hdr, at + V - 1, p.N * p.C, 72)) continue;
 #pragma unroll
         for (int e = 0; e < Q::P; ++e)
           x[u][k][e] = fp::mul2(dup(rstd[u]), fp::fma2(x[u][k][e], mx, fp::add2(q[u][k][e], ms)));
-        Q::store(static_cast<T*>(p.dx) + at, x[u][k]);
+        if (t.in[k] && n < p.N && SSD_INDEX_OK(p.hdr, at + V - 1, p.N * p.C, 72))
+          Q::store(static_cast<T*>(p.dx) + at, x[u][k]);
       }
     }
   }
@@ -486,7 +513,7 @@ struct Pairs {
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) norm_map_stats_kernel(NormParams p) {
   using Q = Pack<T, V>;
-  constexpr int U = 8;   // positions in flight: their moments are formed directly, around their mean
+  constexpr int U = V * (int)sizeof(T) >= 16 ? 8 : 16;   // positions in flight: their moments are formed directly
   __shared__ Moments all[kThreads];
   const MapSlot<V> t(p, blockIdx.x);
   Moments m = {0.f, 0.f, 0.f};
@@ -516,12 +543,10 @@ __global__ void __launch_bounds__(kThreads) norm_map_stats_kernel(NormParams p) 
         const float n = (float)(have * V), mean = __fdividef(sum.x + sum.y, n);
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (u < have) {
 #pragma unroll
-            for (int e = 0; e < Q::P; ++e) {
-              const float2 d = minus2<V>(f[u][e], mean);
-              sq = fp::fma2(d, d, sq);
-            }
+          for (int e = 0; e < Q::P; ++e) {
+            const float2 d = u < have ? minus2<V>(f[u][e], mean) : make_float2(0.f, 0.f);
+            sq = fp::fma2(d, d, sq);
           }
         m = join(m, {n, mean, sq.x + sq.y});
       }
@@ -567,21 +592,20 @@ __global__ void __launch_bounds__(kThreads) norm_map_grad_sums_kernel(NormParams
       in.fetch();
       while (in.pending()) {
         typename Q::Raw rx[U], ry[U];
-        const int have = in.take(rx, ry);
+        in.take(rx, ry);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (u < have) {
-            float2 f[Q::P], d[Q::P];
-            Q::unpack(rx[u], f);
-            Q::unpack(ry[u], d);
+        for (int u = 0; u < U; ++u) {   // past the end dy = 0: nothing is added
+          float2 f[Q::P], d[Q::P];
+          Q::unpack(rx[u], f);
+          Q::unpack(ry[u], d);
 #pragma unroll
-            for (int e = 0; e < Q::P; ++e) {
-              const float2 xh = fp::mul2(minus2<V>(f[e], mean), dup(rstd));
-              const float2 dz = times_act_grad2<kSilu>(d[e], fp::fma2(xh, w[e], bias[e]));
-              db[e] = fp::add2(db[e], dz);
-              dw[e] = fp::fma2(dz, xh, dw[e]);
-            }
+          for (int e = 0; e < Q::P; ++e) {
+            const float2 xh = fp::mul2(minus2<V>(f[e], mean), dup(rstd));
+            const float2 dz = times_act_grad2<kSilu>(d[e], fp::fma2(xh, w[e], bias[e]));
+            db[e] = fp::add2(db[e], dz);
+            dw[e] = fp::fma2(dz, xh, dw[e]);
           }
+        }
       }
     }
     // over the block's rows, per channel
@@ -692,7 +716,7 @@ __global__ void __launch_bounds__(1024) norm_map_join_kernel(NormParams p, uint3
       m = join(m, {n, s.x, s.y});
     }
     m = join_lanes(m);
-    out = make_float2(m.mean, 1.f / sqrtf(m.m2 / m.n + p.eps));
+    out = make_float2(m.mean, rsqrtf(m.m2 / m.n + p.eps));
     if (lane == 0 && p.mean && SSD_INDEX_OK(p.hdr, at, p.N * p.G, 75)) {
       p.mean[at] = out.x;
       p.rstd[at] = out.y;
@@ -704,7 +728,7 @@ __global__ void __launch_bounds__(1024) norm_map_join_kernel(NormParams p, uint3
 template <typename T, int V, bool kSilu>
 __global__ void __launch_bounds__(kThreads) norm_map_apply_kernel(NormParams p) {
   using Q = Pack<T, V>;
-  constexpr int U = 8;
+  constexpr int U = V * (int)sizeof(T) >= 16 ? 4 : 8;
   const MapSlot<V> t(p, gridDim.x - 1 - blockIdx.x);
   if (t.row >= t.rows) return;
   for (int v = t.col; v < t.vecs; v += kThreads) {
@@ -879,11 +903,13 @@ NormPlan norm_plan(const group_norm_shape* s, bool backward) {
   return L;
 }
 
-// Vector width of a call: max_vec, or less where the arrays' rows are not aligned to it.
+// Vector width of a call: max_vec, or less where the arrays' rows are not aligned to it.  The gradient of
+// a map takes 8 bytes at most: with 16 its registers leave room for one block an SM less (8 x 4096 x 512
+// bf16: 49 us, 56 us with 16; tokens: 49 us with 16, 64 us with 8).
 int call_vec(const group_norm_shape* s, std::initializer_list<const void*> arrays,
-             std::initializer_list<const int64_t*> strides) {
+             std::initializer_list<const int64_t*> strides, bool backward) {
   const uint64_t e = s->io_dtype == SSD_BF16 ? 2 : 4;
-  uint64_t bits = 0;
+  uint64_t bits = backward && s->rows > 1 ? 8 : 0;
   for (const void* a : arrays) bits |= reinterpret_cast<uintptr_t>(a);
   for (const int64_t* st : strides) bits |= (uint64_t)(st[0] | st[1]) * e;
   int v = max_vec(s);
@@ -1040,7 +1066,7 @@ ssd_status group_norm_forward(const group_norm_shape* shape, const void* x, cons
   p.y = y;
   p.mean = mean;
   p.rstd = rstd;
-  const int vec = call_vec(shape, {x, y}, {p.xs});
+  const int vec = call_vec(shape, {x, y}, {p.xs}, false);
   return done(launch(p, shape, vec, false, static_cast<char*>(workspace), st));
 }
 
@@ -1078,7 +1104,7 @@ ssd_status group_norm_backward(const group_norm_shape* shape, const void* x, con
   p.dx = dx;
   p.dw = dweight;
   p.db = dbias;
-  const int vec = call_vec(shape, {x, dy, dx}, {p.xs, p.ds});
+  const int vec = call_vec(shape, {x, dy, dx}, {p.xs, p.ds}, true);
   return done(launch(p, shape, vec, true, static_cast<char*>(workspace), st));
 }
 
