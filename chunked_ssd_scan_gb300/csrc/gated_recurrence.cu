@@ -43,19 +43,6 @@ __device__ __forceinline__ float softplus(float d) { return fmaxf(d, 0.f) + log1
 // The decay is carried as w = a - 1 = expm1(l), and a step is h + (w h + b): near one, a itself has an
 // absolute rounding error of 2^-25 whose bias a channel with memory 1 / (1 - a) multiplies by
 // that memory, while w's error is relative to 1 - a.
-struct Gates {
-  float l, r, w, m, i;
-};
-__device__ __forceinline__ Gates gates(float ga, float gx, float rate) {
-  Gates g;
-  g.r = 1.f / (1.f + expf(-ga));
-  g.i = 1.f / (1.f + expf(-gx));
-  g.l = -rate * g.r;
-  g.w = expm1f(g.l);
-  g.m = sqrtf(-g.w * (2.f + g.w));   // 1 - a^2
-  return g;
-}
-__device__ __forceinline__ float decayed(const Gates& g, float h, float b) { return h + fmaf(g.w, h, b); }
 
 // ------------------------------------------------------------------------------------------------
 // Forward.
@@ -721,18 +708,61 @@ __global__ void __launch_bounds__(1024) rec_ddecay_kernel(RecParams p) {
   }
 }
 
-template <typename T>
-__global__ void rec_step_kernel(RecParams p) {
-  const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (id >= p.batch * p.D) return;
-  const int64_t b = id / p.D, d = id % p.D;
-  const Gates g = gates(ld_f32(static_cast<const T*>(p.ga) + b * p.as[0] + d),
-                        ld_f32(static_cast<const T*>(p.gx) + b * p.gs[0] + d),
-                        p.c * softplus(p.decay[d]));
-  const float h = decayed(g, p.init ? p.init[id] : 0.f,
-                          g.m * g.i * ld_f32(static_cast<const T*>(p.x) + b * p.xs[0] + d));
-  p.final_state[id] = h;
-  st_from_f32(static_cast<T*>(p.y) + id, h);
+// ------------------------------------------------------------------------------------------------
+// One step (serving): a thread takes V neighbouring channels of U sequences, so that the channels' rates
+// are formed once for them.  Bound by memory for many sequences, by the launch and one trip to
+// memory for few.
+// ------------------------------------------------------------------------------------------------
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Vals {
+  T v[V];
+};
+
+template <typename T, int V, int U>
+__global__ void __launch_bounds__(128) rec_step_kernel(RecParams p) {
+  constexpr int P = (V + 1) / 2;
+  const int64_t d = ((int64_t)blockIdx.x * 128 + threadIdx.x) * V;
+  if (d >= p.D) return;
+  Vals<T, V> x[U], ga[U], gx[U];
+  Vals<float, V> h[U];
+  const int64_t b0 = (int64_t)blockIdx.y * U;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t b = b0 + u < p.batch ? b0 + u : b0;
+    x[u] = *reinterpret_cast<const Vals<T, V>*>(static_cast<const T*>(p.x) + b * p.xs[0] + d);
+    ga[u] = *reinterpret_cast<const Vals<T, V>*>(static_cast<const T*>(p.ga) + b * p.as[0] + d);
+    gx[u] = *reinterpret_cast<const Vals<T, V>*>(static_cast<const T*>(p.gx) + b * p.gs[0] + d);
+    if (p.init) h[u] = *reinterpret_cast<const Vals<float, V>*>(p.init + b * p.D + d);
+  }
+  float2 rate[P];
+#pragma unroll
+  for (int k = 0; k < P; ++k)
+    rate[k] = make_float2(-p.c * softplus(p.decay[d + 2 * k]), V > 1 ? -p.c * softplus(p.decay[d + 2 * k + (V > 1)]) : 0.f);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    Vals<T, V> y;
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      auto pair = [&](const Vals<T, V>& v) { return make_float2((float)v.v[2 * k], V > 1 ? (float)v.v[2 * k + (V > 1)] : 0.f); };
+      const float2 w = expm1_neg2<true>(fp::mul2(rate[k], rcp2(one_plus_exp2(pair(ga[u])))));
+      const float2 q = one_minus_a2(w), i = rcp2(one_plus_exp2(pair(gx[u])));
+      const float2 m = fp::mul2(q, make_float2(rsqrt_approx(q.x), rsqrt_approx(q.y)));
+      float2 s = make_float2(0.f, 0.f);
+      if (p.init) s = make_float2(h[u].v[2 * k], V > 1 ? h[u].v[2 * k + (V > 1)] : 0.f);
+      s = lookback::apply(w, fp::mul2(fp::mul2(m, i), pair(x[u])), s);
+      h[u].v[2 * k] = s.x;
+      st_from_f32(&y.v[2 * k], s.x);
+      if (V > 1) {
+        h[u].v[2 * k + (V > 1)] = s.y;
+        st_from_f32(&y.v[2 * k + (V > 1)], s.y);
+      }
+    }
+    const int64_t at = (b0 + u) * p.D + d;
+    if (b0 + u < p.batch) {
+      *reinterpret_cast<Vals<float, V>*>(p.final_state + at) = h[u];
+      *reinterpret_cast<Vals<T, V>*>(static_cast<T*>(p.y) + at) = y;
+    }
+  }
 }
 
 constexpr int64_t kMinTileSteps = 64;   // no kernel's tile is shorter
@@ -878,6 +908,37 @@ cudaError_t launch_backward(RecParams p, bool bf16, cudaStream_t st) {
   return align == 16 ? launch_backward_as<float, 16>(p, st) : launch_backward_as<float, 4>(p, st);
 }
 
+template <typename T, int V, int U>
+cudaError_t launch_step_as(const RecParams& p, cudaStream_t st) {
+  const int64_t cols = (p.D + 128 * V - 1) / (128 * V), rows = (p.batch + U - 1) / U;
+  for (int64_t r0 = 0; r0 < rows; r0 += 65535) {   // gridDim.y
+    RecParams q = p;
+    const int64_t b0 = r0 * U;
+    q.batch = p.batch - b0;
+    q.x = static_cast<const T*>(p.x) + b0 * p.xs[0];
+    q.ga = static_cast<const T*>(p.ga) + b0 * p.as[0];
+    q.gx = static_cast<const T*>(p.gx) + b0 * p.gs[0];
+    q.init = p.init ? p.init + b0 * p.D : nullptr;
+    q.final_state = p.final_state + b0 * p.D;
+    q.y = static_cast<T*>(p.y) + b0 * p.D;
+    rec_step_kernel<T, V, U><<<dim3((unsigned)cols, (unsigned)std::min<int64_t>(65535, rows - r0)), 128, 0, st>>>(q);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+template <typename T>
+cudaError_t launch_step(const RecParams& p, cudaStream_t st) {
+  const uint64_t bits = (reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.ga) |
+                         reinterpret_cast<uintptr_t>(p.gx) | reinterpret_cast<uintptr_t>(p.y) |
+                         (uint64_t)(p.xs[0] | p.as[0] | p.gs[0] | p.D) * sizeof(T));
+  const uint64_t sbits = reinterpret_cast<uintptr_t>(p.init) | reinterpret_cast<uintptr_t>(p.final_state);
+  if (bits % (4 * sizeof(T)) != 0 || sbits % 16 != 0) return launch_step_as<T, 1, 1>(p, st);
+  // few sequences: every one to threads of its own, for the machine's sake
+  return p.batch * p.D < (int64_t)152 * 1024 * 4 ? launch_step_as<T, 4, 1>(p, st) : launch_step_as<T, 4, 2>(p, st);
+}
+
 ssd_status done(cudaError_t e) { return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA; }
 
 }  // namespace
@@ -1005,10 +1066,7 @@ ssd_status gated_recurrence_step(const gated_recurrence_shape* shape, const void
   p.y = y;
   p.final_state = state_out;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const unsigned grid = (unsigned)((p.batch * p.D + 127) / 128);
-  if (bf16) rec_step_kernel<__nv_bfloat16><<<grid, 128, 0, st>>>(p);
-  else rec_step_kernel<float><<<grid, 128, 0, st>>>(p);
-  return done(cudaGetLastError());
+  return done(bf16 ? launch_step<__nv_bfloat16>(p, st) : launch_step<float>(p, st));
 }
 
 }  // extern "C"
