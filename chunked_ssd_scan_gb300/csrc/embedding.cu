@@ -7,7 +7,9 @@
 #include <initializer_list>
 
 #include "common.cuh"
+#include "fp_helpers.cuh"
 #include "launch.h"
+#include "pack.cuh"
 
 namespace ssd {
 namespace {
@@ -34,6 +36,7 @@ template <typename T, typename Id, int V>
 __global__ void __launch_bounds__(kThreads) embed_forward_kernel(const Id* ids, int64_t n, const T* table, int64_t rows,
                                                                  int64_t D, float scale, T* out, int cols,
                                                                  int tokens) {
+  using Q = Pack<T, V>;
   constexpr int U = 4;   // tokens in flight
   const int col = threadIdx.x % cols, sub = threadIdx.x / cols;   // tokens: tokens a block takes at a time
   const int64_t d = ((int64_t)blockIdx.y * cols + col) * V;
@@ -45,22 +48,22 @@ __global__ void __launch_bounds__(kThreads) embed_forward_kernel(const Id* ids, 
     for (int u = 0; u < U; ++u) next[u] = i0 + u * tokens < n ? row_of(ids, i0 + u * tokens, rows) : -1;
   };
   int64_t i0 = (int64_t)blockIdx.x * tokens * U + sub;
+  T* o = out + i0 * D + d;
   fetch(i0);
   for (; i0 < n; i0 += step) {
-    Vec<T, V> f[U];
-    int64_t row[U];
+    typename Q::Raw f[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      row[u] = next[u];
-      if (row[u] >= 0) f[u] = *reinterpret_cast<const Vec<T, V>*>(table + row[u] * D + d);
-    }
+    for (int u = 0; u < U; ++u) f[u] = next[u] >= 0 ? Q::raw(table + next[u] * D + d) : Q::none();
     fetch(i0 + step);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < U; ++u, o += tokens * D) {
+      float2 v[Q::P];
+      Q::unpack(f[u], v);
 #pragma unroll
-      for (int e = 0; e < V; ++e) st_from_f32(&f[u].v[e], row[u] >= 0 ? scale * (float)f[u].v[e] : 0.f);
-      if (i0 + u * tokens < n) *reinterpret_cast<Vec<T, V>*>(out + (i0 + u * tokens) * D + d) = f[u];
+      for (int e = 0; e < Q::P; ++e) v[e] = fp::mul2(v[e], make_float2(scale, scale));
+      if (i0 + u * tokens < n) Q::store(o, v);
     }
+    o += (step - U * tokens) * D;
   }
 }
 
@@ -94,16 +97,17 @@ struct EmbedParams {
   int32_t piece;                 // tokens of a piece
   int64_t pieces;
   int64_t fill0, fill1;          // rows that this launch clears where unused
-  int32_t work_blocks;           // blocks that sort; the rest clear
+  int32_t work_blocks;           // blocks (in x) that sort or add; the rest clear
   WsHeader* hdr;
 };
 
-// Rows [fill0, fill1) without tokens are zeros; the blocks behind the sorting ones, a row a block at a
-// time.
+// Rows [fill0, fill1) without tokens are zeros, by the blocks behind the working ones, a row a block at
+// a time.
 __device__ __forceinline__ void clear_rows(const EmbedParams& p) {
-  const int64_t step = gridDim.x - p.work_blocks;
+  const int64_t step = (int64_t)(gridDim.x - p.work_blocks) * gridDim.y;
+  const int64_t first = (int64_t)(blockIdx.x - p.work_blocks) * gridDim.y + blockIdx.y;
   const bool wide = p.D % 4 == 0 && (reinterpret_cast<uintptr_t>(p.dtable) & 15) == 0;
-  for (int64_t r = p.fill0 + blockIdx.x - p.work_blocks; r < p.fill1; r += step) {
+  for (int64_t r = p.fill0 + first; r < p.fill1; r += step) {
     if (p.used[r]) continue;
     float* row = p.dtable + r * p.D;
     if (!SSD_INDEX_OK(p.hdr, (r + 1) * p.D - 1, p.rows * p.D, 80)) continue;
@@ -277,6 +281,7 @@ template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) embed_sum_kernel(EmbedParams p, int cols, int subs) {
   constexpr int kRing = 12;   // rows in flight: 48 KB a block, four blocks an SM
   __shared__ Vec<T, V> ring[kRing][kThreads];
+  if ((int)blockIdx.x >= p.work_blocks) return clear_rows(p);
   const int col = threadIdx.x % cols, sub = threadIdx.x / cols;
   const int64_t d = ((int64_t)blockIdx.y * cols + col) * V, piece = (int64_t)blockIdx.x * subs + sub;
   if (sub >= subs || d >= p.D || piece >= p.pieces) return;
@@ -329,6 +334,7 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(EmbedParams p, int 
 template <int V>
 __global__ void __launch_bounds__(kThreads) embed_join_kernel(EmbedParams p, int cols, int subs) {
   constexpr int U = 16;
+  if ((int)blockIdx.x >= p.work_blocks) return clear_rows(p);
   const int col = threadIdx.x % cols, sub = threadIdx.x / cols;
   const int64_t d = ((int64_t)blockIdx.y * cols + col) * V, piece = (int64_t)blockIdx.x * subs + sub;
   if (sub >= subs || d >= p.D || piece >= p.pieces) return;
@@ -448,19 +454,35 @@ EmbedLayout embed_layout(int64_t n, int64_t rows, int64_t D) {
   return L;
 }
 
+// The rows to clear, shared out to the launches after the first: a sorting step takes about 20 MB of
+// them (50000 x 2048) in the time that it needs by itself, the join of long runs three times that,
+// and the sums, bound by memory themselves, the rest.
+constexpr int kSortShare = 1, kSumShare = 8, kJoinShare = 3;
+struct Fill {
+  int64_t done = 0, all = 0;
+  unsigned take(EmbedParams& p, int share, int work) {
+    p.work_blocks = work;
+    p.fill0 = p.rows * done / all;
+    done += share;
+    p.fill1 = p.rows * done / all;
+    return (unsigned)(work + std::max<int64_t>(1, std::min<int64_t>(152 * 8, p.fill1 - p.fill0)));
+  }
+};
+
 template <typename T, int V>
-cudaError_t launch_sum(const EmbedParams& p, cudaStream_t st) {
+cudaError_t launch_sum(EmbedParams p, Fill& fill, cudaStream_t st) {
   const Split s = split_row((p.D + V - 1) / V);
-  const dim3 grid((unsigned)((p.pieces + s.subs - 1) / s.subs), s.slices);
-  embed_sum_kernel<T, V><<<grid, kThreads, 0, st>>>(p, s.cols, s.subs);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || p.pieces < 2) return e;
+  const int work = (int)((p.pieces + s.subs - 1) / s.subs);
+  const unsigned bx = fill.take(p, kSumShare, work);
+  embed_sum_kernel<T, V><<<dim3(bx, s.slices), kThreads, 0, st>>>(p, s.cols, s.subs);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   // the partial rows are aligned as the width is
   const int v = p.D % 4 == 0 ? 4 : p.D % 2 == 0 ? 2 : 1;
   const Split js = split_row(p.D / v);
-  const dim3 jgrid((unsigned)((p.pieces + js.subs - 1) / js.subs), js.slices);
+  const unsigned jx = fill.take(p, kJoinShare, (int)((p.pieces + js.subs - 1) / js.subs));
   auto* join = v == 4 ? embed_join_kernel<4> : v == 2 ? embed_join_kernel<2> : embed_join_kernel<1>;
-  join<<<jgrid, kThreads, 0, st>>>(p, js.cols, js.subs);
+  join<<<dim3(jx, js.slices), kThreads, 0, st>>>(p, js.cols, js.subs);
   return cudaGetLastError();
 }
 
@@ -470,40 +492,33 @@ cudaError_t launch_backward(EmbedParams p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   int bits = 1;
   while (bits < 32 && (p.rows >> bits) != 0) bits += 1;   // of the largest key, `rows`
-  const int passes = (bits + 7) / 8, launches = 3 * passes - 1;
-  // the rows are cleared in equal shares by the launches after the first
-  int done = 0;
-  auto share = [&](int work) {
-    p.work_blocks = work;
-    p.fill0 = p.rows * done / launches;
-    p.fill1 = p.rows * (done + 1) / launches;
-    done += 1;
-    return (unsigned)(work + std::max<int64_t>(1, std::min<int64_t>(152 * 8, p.fill1 - p.fill0)));
-  };
+  const int passes = (bits + 7) / 8;
+  Fill fill;
+  fill.all = (3 * passes - 1) * kSortShare + kSumShare + kJoinShare;
   p.in = 0;
   for (int pass = 0; pass < passes; ++pass) {
     p.shift = 8 * pass;
     if (pass == 0) {
       embed_keys_kernel<Id><<<(unsigned)p.sort_tiles, kThreads, 0, st>>>(p);
     } else {
-      const unsigned grid = share(p.sort_tiles);
+      const unsigned grid = fill.take(p, kSortShare, p.sort_tiles);
       embed_count_kernel<<<grid, kThreads, 0, st>>>(p);
     }
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    unsigned grid = share(1);
+    unsigned grid = fill.take(p, kSortShare, 1);
     embed_scan_kernel<<<grid, kThreads, 0, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    grid = share(p.sort_tiles);
+    grid = fill.take(p, kSortShare, p.sort_tiles);
     embed_scatter_kernel<<<grid, kThreads, 0, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     p.in ^= 1;
   }
   switch (row_vec(sizeof(T), p.D, {p.dout})) {
     case 8:
-      if constexpr (sizeof(T) == 2) return launch_sum<T, 8>(p, st);
-    case 4: return launch_sum<T, 4>(p, st);
-    case 2: return launch_sum<T, 2>(p, st);
-    default: return launch_sum<T, 1>(p, st);
+      if constexpr (sizeof(T) == 2) return launch_sum<T, 8>(p, fill, st);
+    case 4: return launch_sum<T, 4>(p, fill, st);
+    case 2: return launch_sum<T, 2>(p, fill, st);
+    default: return launch_sum<T, 1>(p, fill, st);
   }
 }
 

@@ -7,10 +7,12 @@
 
 #include <algorithm>
 #include <initializer_list>
+#include <type_traits>
 
 #include "common.cuh"
 #include "fp_helpers.cuh"
 #include "launch.h"
+#include "pack.cuh"
 
 namespace ssd {
 namespace {
@@ -64,77 +66,6 @@ __device__ __forceinline__ float2 times_act_grad2(float2 v, float2 z) {
   return fp::mul2(v, fp::fma2(z, ss, s));
 }
 
-template <int kBytes>
-struct RawOf;
-template <>
-struct RawOf<16> { using type = uint4; };
-template <>
-struct RawOf<8> { using type = uint2; };
-template <>
-struct RawOf<4> { using type = uint32_t; };
-template <>
-struct RawOf<2> { using type = uint16_t; };
-
-// V neighbouring values as one load or store of up to 16 bytes (Raw, as they wait for their turn), in P
-// pairs (V = 1: the second is 0).
-template <typename T, int V>
-struct Pack {
-  static constexpr int P = (V + 1) / 2;
-  using Raw = typename RawOf<V * (int)sizeof(T)>::type;
-  static __device__ __forceinline__ Raw raw(const T* p) { return __ldg(reinterpret_cast<const Raw*>(p)); }
-  static __device__ __forceinline__ Raw none() {
-    Raw r;
-    memset(&r, 0, sizeof(r));
-    return r;
-  }
-  static __device__ __forceinline__ void unpack(const Raw& r, float2 (&f)[P]) {
-    if constexpr (sizeof(T) == 2) {
-      if constexpr (V == 1) {
-        f[0] = make_float2(__uint_as_float((uint32_t)r << 16), 0.f);
-      } else {
-        uint32_t u[P];
-        memcpy(u, &r, sizeof(r));
-#pragma unroll
-        for (int k = 0; k < P; ++k)
-          f[k] = make_float2(__uint_as_float(u[k] << 16), __uint_as_float(u[k] & 0xffff0000u));
-      }
-    } else {
-      float v[2 * P] = {};
-      memcpy(v, &r, sizeof(r));
-#pragma unroll
-      for (int k = 0; k < P; ++k) f[k] = make_float2(v[2 * k], v[2 * k + 1]);
-    }
-  }
-  static __device__ __forceinline__ void store(T* p, const float2 (&f)[P]) {
-    if constexpr (V == 1) {
-      st_from_f32(p, f[0].x);
-    } else if constexpr (sizeof(T) == 2) {
-      uint32_t u[P];
-#pragma unroll
-      for (int k = 0; k < P; ++k) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(f[k].x, f[k].y);
-        u[k] = *reinterpret_cast<const uint32_t*>(&b);
-      }
-      if constexpr (V == 8) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<uint4*>(u);
-      else if constexpr (V == 4) *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(u);
-      else *reinterpret_cast<uint32_t*>(p) = u[0];
-    } else {
-      if constexpr (V == 4) *reinterpret_cast<float4*>(p) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-      else *reinterpret_cast<float2*>(p) = f[0];
-    }
-  }
-  static __device__ __forceinline__ void param(const float* p, int64_t at, float none, float2 (&f)[P]) {
-#pragma unroll
-    for (int k = 0; k < P; ++k) {
-      f[k].x = p ? __ldg(p + at + 2 * k) : none;
-      f[k].y = V == 1 ? 0.f : p ? __ldg(p + at + 2 * k + 1) : none;
-    }
-  }
-  static __device__ __forceinline__ void zero(float2 (&f)[P]) {
-#pragma unroll
-    for (int k = 0; k < P; ++k) f[k] = make_float2(0.f, 0.f);
-  }
-};
 // a - b, and 0 in the second place of a single value
 template <int V>
 __device__ __forceinline__ float2 minus2(float2 a, float b) {
@@ -487,13 +418,19 @@ struct Pairs {
         py(t.rows * p.ds[1]),
         left((int)((t.s1 - t.s0 - t.row + t.rows - 1) / t.rows)) {}
   __device__ __forceinline__ void fetch() {
+    if (left >= U) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      nx[u] = u < left ? Pack<T, V>::raw(x + u * px) : Pack<T, V>::none();
-      ny[u] = u < left ? Pack<T, V>::raw(dy + u * py) : Pack<T, V>::none();
+      for (int u = 0; u < U; ++u, x += px, dy += py) {
+        nx[u] = Pack<T, V>::raw(x);
+        ny[u] = Pack<T, V>::raw(dy);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        nx[u] = u < left ? Pack<T, V>::raw(x + u * px) : Pack<T, V>::none();
+        ny[u] = u < left ? Pack<T, V>::raw(dy + u * py) : Pack<T, V>::none();
+      }
     }
-    x += U * px;
-    dy += U * py;
     left -= U;
   }
   __device__ __forceinline__ bool pending() const { return left + U > 0; }
@@ -524,9 +461,13 @@ __global__ void __launch_bounds__(kThreads) norm_map_stats_kernel(NormParams p) 
       int left = (int)((t.s1 - t.s0 - t.row + t.rows - 1) / t.rows);   // positions still to load
       typename Q::Raw next[U];
       auto fetch = [&]() {
+        if (left >= U) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) next[u] = u < left ? Q::raw(x + u * pitch) : Q::none();
-        x += U * pitch;
+          for (int u = 0; u < U; ++u, x += pitch) next[u] = Q::raw(x);
+        } else {
+#pragma unroll
+          for (int u = 0; u < U; ++u) next[u] = u < left ? Q::raw(x + u * pitch) : Q::none();
+        }
         left -= U;
       };
       fetch();
@@ -541,13 +482,17 @@ __global__ void __launch_bounds__(kThreads) norm_map_stats_kernel(NormParams p) 
         }
         fetch();
         const float n = (float)(have * V), mean = __fdividef(sum.x + sum.y, n);
+        auto squares = [&](auto whole) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+          for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int e = 0; e < Q::P; ++e) {
-            const float2 d = u < have ? minus2<V>(f[u][e], mean) : make_float2(0.f, 0.f);
-            sq = fp::fma2(d, d, sq);
-          }
+            for (int e = 0; e < Q::P; ++e) {
+              const float2 d = decltype(whole)::value || u < have ? minus2<V>(f[u][e], mean) : make_float2(0.f, 0.f);
+              sq = fp::fma2(d, d, sq);
+            }
+        };
+        if (have == U) squares(std::true_type());
+        else squares(std::false_type());
         m = join(m, {n, mean, sq.x + sq.y});
       }
     }
@@ -745,9 +690,13 @@ __global__ void __launch_bounds__(kThreads) norm_map_apply_kernel(NormParams p) 
     int left = (int)((t.s1 - t.s0 - t.row + t.rows - 1) / t.rows);
     typename Q::Raw next[U];
     auto fetch = [&]() {
+      if (left >= U) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) next[u] = u < left ? Q::raw(x + u * pitch) : Q::none();
-      x += U * pitch;
+        for (int u = 0; u < U; ++u, x += pitch) next[u] = Q::raw(x);
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) next[u] = u < left ? Q::raw(x + u * pitch) : Q::none();
+      }
       left -= U;
     };
     fetch();
@@ -757,16 +706,20 @@ __global__ void __launch_bounds__(kThreads) norm_map_apply_kernel(NormParams p) 
 #pragma unroll
       for (int u = 0; u < U; ++u) now[u] = next[u];
       fetch();
+      auto write = [&](auto whole) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (u >= have || !SSD_INDEX_OK(p.hdr, (y - static_cast<T*>(p.y)) + V - 1, p.N * p.S * p.C, 76)) continue;
-        float2 f[Q::P];
-        Q::unpack(now[u], f);
+        for (int u = 0; u < U; ++u, y += out) {
+          float2 f[Q::P];
+          Q::unpack(now[u], f);
 #pragma unroll
-        for (int e = 0; e < Q::P; ++e) f[e] = act2<kSilu>(fp::fma2(minus2<V>(f[e], st.x), a[e], b[e]));
-        Q::store(y, f);
-        y += out;
-      }
+          for (int e = 0; e < Q::P; ++e) f[e] = act2<kSilu>(fp::fma2(minus2<V>(f[e], st.x), a[e], b[e]));
+          if ((decltype(whole)::value || u < have) &&
+              SSD_INDEX_OK(p.hdr, (y - static_cast<T*>(p.y)) + V - 1, p.N * p.S * p.C, 76))
+            Q::store(y, f);
+        }
+      };
+      if (have == U) write(std::true_type());
+      else write(std::false_type());
     }
   }
 }
@@ -791,21 +744,25 @@ __global__ void __launch_bounds__(kThreads) norm_map_grad_apply_kernel(NormParam
     while (in.pending()) {
       typename Q::Raw rx[U], ry[U];
       const int have = in.take(rx, ry);
+      auto write = [&](auto whole) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (u >= have || !SSD_INDEX_OK(p.hdr, (dx - static_cast<T*>(p.dx)) + V - 1, p.N * p.S * p.C, 79)) continue;
-        float2 f[Q::P], d[Q::P];
-        Q::unpack(rx[u], f);
-        Q::unpack(ry[u], d);
+        for (int u = 0; u < U; ++u, dx += out) {
+          float2 f[Q::P], d[Q::P];
+          Q::unpack(rx[u], f);
+          Q::unpack(ry[u], d);
 #pragma unroll
-        for (int e = 0; e < Q::P; ++e) {
-          const float2 xh = fp::mul2(minus2<V>(f[e], mean), dup(rstd));
-          const float2 q = fp::mul2(times_act_grad2<kSilu>(d[e], fp::fma2(xh, w[e], bias[e])), w[e]);
-          f[e] = fp::mul2(dup(rstd), fp::fma2(xh, dup(-m.y), fp::add2(q, dup(-m.x))));
+          for (int e = 0; e < Q::P; ++e) {
+            const float2 xh = fp::mul2(minus2<V>(f[e], mean), dup(rstd));
+            const float2 q = fp::mul2(times_act_grad2<kSilu>(d[e], fp::fma2(xh, w[e], bias[e])), w[e]);
+            f[e] = fp::mul2(dup(rstd), fp::fma2(xh, dup(-m.y), fp::add2(q, dup(-m.x))));
+          }
+          if ((decltype(whole)::value || u < have) &&
+              SSD_INDEX_OK(p.hdr, (dx - static_cast<T*>(p.dx)) + V - 1, p.N * p.S * p.C, 79))
+            Q::store(dx, f);
         }
-        Q::store(dx, f);
-        dx += out;
-      }
+      };
+      if (have == U) write(std::true_type());
+      else write(std::false_type());
     }
   }
 }
