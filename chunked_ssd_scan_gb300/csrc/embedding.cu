@@ -71,8 +71,8 @@ __global__ void __launch_bounds__(kThreads) embed_forward_kernel(const Id* ids, 
 // Backward.
 //
 // 1. The tokens are sorted by id, stably, so that a row's tokens stand together in their order: a radix
-//    sort of 8 bits a pass (count, scan, scatter), the padding's key behind all rows.  It is short
-//    of work, so its launches take along the writing of the rows that no token has.
+//    sort of 8 bits a pass, the padding's key behind all rows.  It is short of work, so its launches,
+//    like the others, take along the clearing of rows that no token has.
 // 2. A subgroup of threads takes kPiece sorted tokens and adds their rows, writing each row's sum as its
 //    run ends; a run that goes on over the ends of a piece leaves partial sums instead,
 // 3. which the piece where the run starts joins, in order.
@@ -90,7 +90,7 @@ struct EmbedParams {
   float* dtable;
   uint8_t* used;                 // [rows] a token has this row
   uint32_t *key[2], *pos[2];     // sorted ping-pong; a key is the row, or `rows` for padding
-  uint32_t* hist;                // [kBins, sort tiles]
+  uint32_t *hist, *next_hist;    // [kBins, sort tiles] of this pass and of the next (NULL: the last)
   float *head, *tail;            // [pieces, D] partial sums
   int32_t sort_tiles, shift;
   int32_t in;                    // which of key/pos is read
@@ -120,48 +120,31 @@ __device__ __forceinline__ void clear_rows(const EmbedParams& p) {
   }
 }
 
-// The digits of a block's keys.
-__device__ __forceinline__ void count_digits(const EmbedParams& p, const uint32_t (&key)[kKeys], const bool (&in)[kKeys]) {
+// Keys from ids, the rows that occur, and how many keys of a block have each lowest digit.
+template <typename Id>
+__global__ void __launch_bounds__(kThreads) embed_keys_kernel(EmbedParams p) {
   __shared__ uint32_t bins[kBins];
   bins[threadIdx.x] = 0;
   __syncthreads();
+  uint32_t key[kKeys];
 #pragma unroll
-  for (int k = 0; k < kKeys; ++k)
-    if (in[k]) atomicAdd(&bins[(key[k] >> p.shift) & (kBins - 1)], 1u);
+  for (int k = 0; k < kKeys; ++k) {
+    const int64_t i = (int64_t)blockIdx.x * kSortTile + k * kThreads + threadIdx.x;
+    const int64_t r = i < p.n ? row_of(static_cast<const Id*>(p.ids), i, p.rows) : -1;
+    key[k] = r < 0 ? (uint32_t)p.rows : (uint32_t)r;
+  }
+#pragma unroll
+  for (int k = 0; k < kKeys; ++k) {
+    const int64_t i = (int64_t)blockIdx.x * kSortTile + k * kThreads + threadIdx.x;
+    if (i >= p.n) continue;
+    if (key[k] != (uint32_t)p.rows) p.used[key[k]] = 1;
+    p.key[p.in][i] = key[k];
+    atomicAdd(&bins[key[k] & (kBins - 1)], 1u);
+  }
   __syncthreads();
   p.hist[(int64_t)threadIdx.x * p.sort_tiles + blockIdx.x] = bins[threadIdx.x];
 }
 static_assert(kBins == kThreads, "a thread a bin");
-
-// First pass: keys from ids, the rows that occur, and the lowest digits.
-template <typename Id>
-__global__ void __launch_bounds__(kThreads) embed_keys_kernel(EmbedParams p) {
-  uint32_t key[kKeys];
-  bool in[kKeys];
-#pragma unroll
-  for (int k = 0; k < kKeys; ++k) {
-    const int64_t i = (int64_t)blockIdx.x * kSortTile + k * kThreads + threadIdx.x;
-    in[k] = i < p.n;
-    const int64_t r = in[k] ? row_of(static_cast<const Id*>(p.ids), i, p.rows) : -1;
-    key[k] = r < 0 ? (uint32_t)p.rows : (uint32_t)r;
-    if (r >= 0) p.used[r] = 1;
-    if (in[k]) p.key[p.in][i] = key[k];
-  }
-  count_digits(p, key, in);
-}
-
-__global__ void __launch_bounds__(kThreads) embed_count_kernel(EmbedParams p) {
-  if ((int)blockIdx.x >= p.work_blocks) return clear_rows(p);
-  uint32_t key[kKeys];
-  bool in[kKeys];
-#pragma unroll
-  for (int k = 0; k < kKeys; ++k) {
-    const int64_t i = (int64_t)blockIdx.x * kSortTile + k * kThreads + threadIdx.x;
-    in[k] = i < p.n;
-    key[k] = in[k] ? p.key[p.in][i] : 0u;
-  }
-  count_digits(p, key, in);
-}
 
 // hist becomes its exclusive prefix sum over digits, then tiles, by one block.
 __global__ void __launch_bounds__(kThreads) embed_scan_kernel(EmbedParams p) {
@@ -204,7 +187,11 @@ __global__ void __launch_bounds__(kThreads) embed_scan_kernel(EmbedParams p) {
 }
 
 // Keys and positions to their places by the pass's digit, equal digits in their order: a warp takes
-// neighbouring keys, 32 at a time.
+// neighbouring keys, 32 at a time.  Counts the next pass's digits of the tiles that they go to (whole
+// numbers: the order of the additions does not matter).  Where the tiles are few every block forms the
+// prefix sums of the counts for itself, which spares the scan's launch.
+constexpr int kFewTiles = 64;
+template <bool kScanned>
 __global__ void __launch_bounds__(kThreads) embed_scatter_kernel(EmbedParams p) {
   if ((int)blockIdx.x >= p.work_blocks) return clear_rows(p);
   constexpr int kW = kThreads / 32;
@@ -234,7 +221,30 @@ __global__ void __launch_bounds__(kThreads) embed_scatter_kernel(EmbedParams p) 
   }
   __syncthreads();
   {   // a thread a digit: where the warps' keys of it start
-    uint32_t base = p.hist[(int64_t)threadIdx.x * p.sort_tiles + blockIdx.x];
+    const uint32_t* row = p.hist + (int64_t)threadIdx.x * p.sort_tiles;
+    uint32_t base;
+    if (kScanned) {
+      base = row[blockIdx.x];
+    } else {
+      __shared__ uint32_t warps[kW];
+      uint32_t all = 0, mine = 0;
+#pragma unroll 8
+      for (int k = 0; k < p.sort_tiles; ++k) {
+        const uint32_t c = row[k];
+        all += c;
+        mine += k < (int)blockIdx.x ? c : 0u;
+      }
+      uint32_t inc = all;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+      }
+      if (lane == 31) warps[warp] = inc;
+      __syncthreads();
+      base = inc - all + mine;
+      for (int k = 0; k < warp; ++k) base += warps[k];
+    }
 #pragma unroll
     for (int k = 0; k < kW; ++k) {
       const uint32_t c = seen[k][threadIdx.x];
@@ -250,6 +260,8 @@ __global__ void __launch_bounds__(kThreads) embed_scatter_kernel(EmbedParams p) 
     if (!SSD_INDEX_OK(p.hdr, at, p.n, 81)) continue;
     p.key[p.in ^ 1][at] = key[k];
     p.pos[p.in ^ 1][at] = pos[k];
+    if (p.next_hist)
+      atomicAdd(p.next_hist + (int64_t)((key[k] >> (p.shift + 8)) & (kBins - 1)) * p.sort_tiles + at / kSortTile, 1u);
   }
 }
 
@@ -330,10 +342,10 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(EmbedParams p, int 
 }
 
 // Runs over more than one piece: the piece where one starts adds the heads of those after it.  Keys and
-// heads are asked for together (a head that is not the run's is not used), sixteen pieces at a time.
+// heads are asked for together (a head that is not the run's is not used), eight pieces at a time.
 template <int V>
 __global__ void __launch_bounds__(kThreads) embed_join_kernel(EmbedParams p, int cols, int subs) {
-  constexpr int U = 16;
+  constexpr int U = 8;
   if ((int)blockIdx.x >= p.work_blocks) return clear_rows(p);
   const int col = threadIdx.x % cols, sub = threadIdx.x / cols;
   const int64_t d = ((int64_t)blockIdx.y * cols + col) * V, piece = (int64_t)blockIdx.x * subs + sub;
@@ -426,17 +438,23 @@ cudaError_t launch_forward(const void* ids, int64_t n, const void* table, int64_
 }
 
 struct EmbedLayout {
-  size_t used = 0, key[2] = {0, 0}, pos[2] = {0, 0}, hist = 0, head = 0, tail = 0, total = 0;
+  size_t used = 0, hist = 0, cleared = 0, key[2] = {0, 0}, pos[2] = {0, 0}, head = 0, tail = 0, total = 0;
   int64_t sort_tiles = 0, pieces = 0;
   int32_t piece = 0;
 };
+// Passes of 8 bits over keys up to `rows`.
+int embed_passes(int64_t rows) {
+  int passes = 1;
+  while (passes < 4 && (rows >> (8 * passes)) != 0) passes += 1;
+  return passes;
+}
 EmbedLayout embed_layout(int64_t n, int64_t rows, int64_t D) {
   EmbedLayout L;
   L.sort_tiles = (n + kSortTile - 1) / kSortTile;
-  // pieces of 32 tokens fill the machine from a few thousand tokens on; with many tokens longer ones keep
-  // a frequent row's partial sums few
+  // short pieces while they do not fill the machine (four blocks an SM), then longer ones: they keep the
+  // partial sums of frequent rows few
   L.piece = 32;
-  while (L.piece < 256 && n / L.piece > 4096) L.piece *= 2;
+  while (L.piece < 256 && n / L.piece > 4 * 152) L.piece *= 2;
   L.pieces = (n + L.piece - 1) / L.piece;
   size_t off = sizeof(WsHeader);
   auto take = [&](size_t bytes) {
@@ -444,20 +462,20 @@ EmbedLayout embed_layout(int64_t n, int64_t rows, int64_t D) {
     off = align_up(off + bytes, kWsAlign);
     return at;
   };
-  L.used = take((size_t)rows);
+  L.used = take((size_t)rows);   // cleared together with the counts behind it
+  L.hist = take(sizeof(uint32_t) * kBins * (size_t)L.sort_tiles * embed_passes(rows));
+  L.cleared = off - L.used;
   for (int k = 0; k < 2; ++k) L.key[k] = take(sizeof(uint32_t) * (size_t)n);
   for (int k = 0; k < 2; ++k) L.pos[k] = take(sizeof(uint32_t) * (size_t)n);
-  L.hist = take(sizeof(uint32_t) * kBins * (size_t)L.sort_tiles);
   L.head = take(sizeof(float) * (size_t)(L.pieces * D));
   L.tail = take(sizeof(float) * (size_t)(L.pieces * D));
   L.total = off;
   return L;
 }
 
-// The rows to clear, shared out to the launches after the first: a sorting step takes about 20 MB of
-// them (50000 x 2048) in the time that it needs by itself, the join of long runs three times that,
-// and the sums, bound by memory themselves, the rest.
-constexpr int kSortShare = 1, kSumShare = 8, kJoinShare = 3;
+// The rows to clear, shared out to the launches behind the first: a sorting step and the join of long
+// runs take a little of it in the time that they wait, the sums, bound by memory themselves, the rest.
+constexpr int kSortShare = 2, kSumShare = 8, kJoinShare = 2;
 struct Fill {
   int64_t done = 0, all = 0;
   unsigned take(EmbedParams& p, int share, int work) {
@@ -487,30 +505,29 @@ cudaError_t launch_sum(EmbedParams p, Fill& fill, cudaStream_t st) {
 }
 
 template <typename T, typename Id>
-cudaError_t launch_backward(EmbedParams p, cudaStream_t st) {
-  cudaError_t e = cudaMemsetAsync(p.used, 0, (size_t)p.rows, st);
+cudaError_t launch_backward(EmbedParams p, size_t cleared, cudaStream_t st) {
+  cudaError_t e = cudaMemsetAsync(p.used, 0, cleared, st);
   if (e != cudaSuccess) return e;
-  int bits = 1;
-  while (bits < 32 && (p.rows >> bits) != 0) bits += 1;   // of the largest key, `rows`
-  const int passes = (bits + 7) / 8;
+  const int passes = embed_passes(p.rows);
+  const bool scan = p.sort_tiles > kFewTiles;
   Fill fill;
-  fill.all = (3 * passes - 1) * kSortShare + kSumShare + kJoinShare;
+  fill.all = passes * (scan ? 2 : 1) * kSortShare + kSumShare + kJoinShare;
   p.in = 0;
+  embed_keys_kernel<Id><<<(unsigned)p.sort_tiles, kThreads, 0, st>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   for (int pass = 0; pass < passes; ++pass) {
     p.shift = 8 * pass;
-    if (pass == 0) {
-      embed_keys_kernel<Id><<<(unsigned)p.sort_tiles, kThreads, 0, st>>>(p);
-    } else {
-      const unsigned grid = fill.take(p, kSortShare, p.sort_tiles);
-      embed_count_kernel<<<grid, kThreads, 0, st>>>(p);
+    p.next_hist = pass + 1 < passes ? p.hist + (int64_t)kBins * p.sort_tiles : nullptr;
+    if (scan) {
+      const unsigned grid = fill.take(p, kSortShare, 1);
+      embed_scan_kernel<<<grid, kThreads, 0, st>>>(p);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
+    const unsigned grid = fill.take(p, kSortShare, p.sort_tiles);
+    if (scan) embed_scatter_kernel<true><<<grid, kThreads, 0, st>>>(p);
+    else embed_scatter_kernel<false><<<grid, kThreads, 0, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    unsigned grid = fill.take(p, kSortShare, 1);
-    embed_scan_kernel<<<grid, kThreads, 0, st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    grid = fill.take(p, kSortShare, p.sort_tiles);
-    embed_scatter_kernel<<<grid, kThreads, 0, st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    p.hist = p.next_hist;
     p.in ^= 1;
   }
   switch (row_vec(sizeof(T), p.D, {p.dout})) {
@@ -594,7 +611,7 @@ ssd_status embedding_backward(const void* ids, int32_t ids_bits, int64_t n, cons
   p.hdr = reinterpret_cast<WsHeader*>(ws);
   auto f = bf16 ? (ids_bits == 64 ? launch_backward<__nv_bfloat16, int64_t> : launch_backward<__nv_bfloat16, int32_t>)
                 : (ids_bits == 64 ? launch_backward<float, int64_t> : launch_backward<float, int32_t>);
-  return done(f(p, st));
+  return done(f(p, L.cleared, st));
 }
 
 }  // extern "C"

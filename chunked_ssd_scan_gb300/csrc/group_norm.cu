@@ -448,9 +448,9 @@ struct Pairs {
 };
 
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) norm_map_stats_kernel(NormParams p) {
+__global__ void __launch_bounds__(kThreads, 4) norm_map_stats_kernel(NormParams p) {
   using Q = Pack<T, V>;
-  constexpr int U = V * (int)sizeof(T) >= 16 ? 8 : 16;   // positions in flight: their moments are formed directly
+  constexpr int U = 8;   // positions in flight: their moments are formed directly
   __shared__ Moments all[kThreads];
   const MapSlot<V> t(p, blockIdx.x);
   Moments m = {0.f, 0.f, 0.f};
