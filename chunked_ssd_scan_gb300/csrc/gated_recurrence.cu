@@ -387,24 +387,30 @@ __global__ void __launch_bounds__(32 * Forward<T>::kNw, Forward<T>::kBlocks) rec
     }
     const int64_t row0 = (q.b * p.T + q.t0 + warp * SPW) * p.D + q.c0 + cl;
     T* y = static_cast<T*>(p.y) + row0;
-    auto store = [&](int s, float v0, float v1) {
-      const float v[2] = {v0, v1};
-      if (SSD_INDEX_OK(p.hdr, row0 + s * p.D + n - 1, p.batch * p.T * p.D, 61)) store_row<ALIGN>(y, v, n);
-      y += p.D;
-    };
     const int live = p.y && n > 0 ? (int)min((int64_t)SPW, max((int64_t)0, steps)) : 0;   // steps to write
+    auto walk = [&](auto whole) {
+      auto store = [&](int s, float v0, float v1) {
+        const float v[2] = {v0, v1};
+        if ((decltype(whole)::value || s < live) &&
+            SSD_INDEX_OK(p.hdr, row0 + s * p.D + n - 1, p.batch * p.T * p.D, 61))
+          store_row<ALIGN>(y, v, n);
+        y += p.D;
+      };
 #pragma unroll
-    for (int k = 0; k < kPairs; ++k) {
-      if constexpr (kCpl == 2) {
-        h = lookback::apply(w[k], b[k], h);
-        if (k < live) store(k, h.x, h.y);
-      } else {
-        h.y = lookback::apply(w[k].x, b[k].x, h.x);
-        if (2 * k < live) store(2 * k, h.y, 0.f);
-        h.x = lookback::apply(w[k].y, b[k].y, h.y);
-        if (2 * k + 1 < live) store(2 * k + 1, h.x, 0.f);
+      for (int k = 0; k < kPairs; ++k) {
+        if constexpr (kCpl == 2) {
+          h = lookback::apply(w[k], b[k], h);
+          store(k, h.x, h.y);
+        } else {
+          h.y = lookback::apply(w[k].x, b[k].x, h.x);
+          store(2 * k, h.y, 0.f);
+          h.x = lookback::apply(w[k].y, b[k].y, h.y);
+          store(2 * k + 1, h.x, 0.f);
+        }
       }
-    }
+    };
+    if (live == SPW) walk(std::true_type());
+    else if (live > 0) walk(std::false_type());
   }
   cp_async_wait_all();
 }
@@ -639,39 +645,45 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(RecParams 
     const int n = min(kCpl, max(0, q.left - cl));
     const int live = n > 0 ? (int)min((int64_t)SPW, max((int64_t)0, steps)) : 0;
     const int64_t row0 = (q.b * p.T + q.t0 + warp * SPW) * p.D + q.c0 + cl;
-    auto store = [&](int s, float2 vx, float2 va, float2 vg) {
-      const int64_t at = row0 + s * p.D;
-      if (SSD_INDEX_OK(p.hdr, at + n - 1, p.batch * p.T * p.D, 63)) {
-        const float x2[2] = {vx.x, vx.y}, a2[2] = {va.x, va.y}, g2[2] = {vg.x, vg.y};
-        store_row<ALIGN>(static_cast<T*>(p.dx) + at, x2, n);
-        store_row<ALIGN>(static_cast<T*>(p.dga) + at, a2, n);
-        store_row<ALIGN>(static_cast<T*>(p.dgx) + at, g2, n);
+    auto walk = [&](auto whole) {
+      const int64_t last = row0 + (SPW - 1) * p.D;
+      T *px = static_cast<T*>(p.dx) + last, *pa = static_cast<T*>(p.dga) + last, *pg = static_cast<T*>(p.dgx) + last;
+      auto store = [&](int s, float x0, float x1, float a0, float a1, float g0, float g1) {
+        if ((decltype(whole)::value || s < live) &&
+            SSD_INDEX_OK(p.hdr, row0 + s * p.D + n - 1, p.batch * p.T * p.D, 63)) {
+          const float x2[2] = {x0, x1}, a2[2] = {a0, a1}, g2[2] = {g0, g1};
+          store_row<ALIGN>(px, x2, n);
+          store_row<ALIGN>(pa, a2, n);
+          store_row<ALIGN>(pg, g2, n);
+        }
+        px -= p.D, pa -= p.D, pg -= p.D;
+      };
+#pragma unroll
+      for (int k = kPairs - 1; k >= 0; --k) {
+        const float2 dy = pair_at(rows + 3 * kArray, k, lane, T());
+        float2 G;
+        if constexpr (kCpl == 2) {
+          G = fp::add2(dy, C);
+          C = fp::fma2(w[k], G, G);
+        } else {
+          G.y = dy.y + C.x;
+          G.x = dy.x + fmaf(w[k].y, G.y, G.y);
+          C.x = fmaf(w[k].x, G.x, G.x);
+        }
+        const float2 e = fp::mul2(G, kr[k]);
+        sum = fp::add2(sum, e);
+        const float2 vx = fp::mul2(G, mi[k]), vg = fp::mul2(G, xi[k]);
+        const float2 va = fp::mul2(fp::mul2(rate, e), fp::fma2(r[k], dup(-1.f), dup(1.f)));
+        if constexpr (kCpl == 2) {
+          store(k, vx.x, vx.y, va.x, va.y, vg.x, vg.y);
+        } else {
+          store(2 * k + 1, vx.y, 0.f, va.y, 0.f, vg.y, 0.f);
+          store(2 * k, vx.x, 0.f, va.x, 0.f, vg.x, 0.f);
+        }
       }
     };
-#pragma unroll
-    for (int k = kPairs - 1; k >= 0; --k) {
-      const float2 dy = pair_at(rows + 3 * kArray, k, lane, T());
-      float2 G;
-      if constexpr (kCpl == 2) {
-        G = fp::add2(dy, C);
-        C = fp::fma2(w[k], G, G);
-      } else {
-        G.y = dy.y + C.x;
-        G.x = dy.x + fmaf(w[k].y, G.y, G.y);
-        C.x = fmaf(w[k].x, G.x, G.x);
-      }
-      const float2 e = fp::mul2(G, kr[k]);
-      sum = fp::add2(sum, e);
-      const float2 vx = fp::mul2(G, mi[k]), vg = fp::mul2(G, xi[k]);
-      const float2 va = fp::mul2(fp::mul2(rate, e), fp::fma2(r[k], dup(-1.f), dup(1.f)));
-      if constexpr (kCpl == 2) {
-        if (k < live) store(k, vx, va, vg);
-      } else {
-        if (2 * k + 1 < live)
-          store(2 * k + 1, make_float2(vx.y, 0.f), make_float2(va.y, 0.f), make_float2(vg.y, 0.f));
-        if (2 * k < live) store(2 * k, vx, va, vg);
-      }
-    }
+    if (live == SPW) walk(std::true_type());
+    else walk(std::false_type());
     if constexpr (kCpl == 1) sum.x += sum.y;
     sums[warp][cl] = sum.x;
     if (kCpl == 2) sums[warp][cl + kCpl - 1] = sum.y;
