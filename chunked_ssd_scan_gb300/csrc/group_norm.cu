@@ -39,6 +39,8 @@ struct NormParams {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kGridBlocks = 152;        // blocks that a map kernel is cut into: so many times what fits an SM
+constexpr int kMapForward = 4, kMapBackward = 3;   // blocks of a map kernel on an SM
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float2 dup(float v) { return make_float2(v, v); }
@@ -448,7 +450,7 @@ struct Pairs {
 };
 
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads, 4) norm_map_stats_kernel(NormParams p) {
+__global__ void __launch_bounds__(kThreads, kMapForward) norm_map_stats_kernel(NormParams p) {
   using Q = Pack<T, V>;
   constexpr int U = 8;   // positions in flight: their moments are formed directly
   __shared__ Moments all[kThreads];
@@ -498,14 +500,17 @@ __global__ void __launch_bounds__(kThreads, 4) norm_map_stats_kernel(NormParams 
     }
   all[threadIdx.x] = m;
   __syncthreads();
-  // a warp a group: its threads are columns [k per, (k + 1) per) of every row
-  const int lane = threadIdx.x % 32, per = min(t.gv, t.cols);
-  for (int k = threadIdx.x / 32; k < t.groups; k += kWarps) {
+  // a group's threads are columns [k per, (k + 1) per) of every row: a few of them are joined by one
+  // thread, more by a warp
+  const int lane = threadIdx.x % 32, per = min(t.gv, t.cols), members = per * t.rows;
+  const bool few = members <= 16;
+  for (int k = few ? threadIdx.x : threadIdx.x / 32; k < t.groups; k += few ? kThreads : kWarps) {
     Moments g = {0.f, 0.f, 0.f};
-    for (int j = lane; j < per * t.rows; j += 32) g = join(g, all[j / per * t.cols + k * per + j % per]);
-    g = join_lanes(g);
+    for (int j = few ? 0 : lane; j < members; j += few ? 1 : 32)
+      g = join(g, all[j / per * t.cols + k * per + j % per]);
+    if (!few) g = join_lanes(g);
     const int64_t at = ((t.n * p.G + t.g0 + k) * p.chunks + t.chunk) * 2;
-    if (lane == 0 && SSD_INDEX_OK(p.hdr, at + 1, p.N * p.chunks * p.G * 2, 74))
+    if ((few || lane == 0) && SSD_INDEX_OK(p.hdr, at + 1, p.N * p.chunks * p.G * 2, 74))
       *reinterpret_cast<float2*>(p.stats + at) = make_float2(g.mean, g.m2);
   }
 }
@@ -513,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 4) norm_map_stats_kernel(NormParams 
 // Per chunk and channel, sum dz and sum dz xhat (which are the parameters' gradients' partials), and per
 // group their sums times w, which the gradient of x needs.
 template <typename T, int V, bool kSilu>
-__global__ void __launch_bounds__(kThreads) norm_map_grad_sums_kernel(NormParams p) {
+__global__ void __launch_bounds__(kThreads, kMapBackward) norm_map_grad_sums_kernel(NormParams p) {
   using Q = Pack<T, V>;
   constexpr int U = 4;
   __shared__ float4 all[kThreads][Q::P];
@@ -671,7 +676,7 @@ __global__ void __launch_bounds__(1024) norm_map_join_kernel(NormParams p, uint3
 }
 
 template <typename T, int V, bool kSilu>
-__global__ void __launch_bounds__(kThreads) norm_map_apply_kernel(NormParams p) {
+__global__ void __launch_bounds__(kThreads, kMapForward) norm_map_apply_kernel(NormParams p) {
   using Q = Pack<T, V>;
   constexpr int U = V * (int)sizeof(T) >= 16 ? 4 : 8;
   const MapSlot<V> t(p, gridDim.x - 1 - blockIdx.x);
@@ -725,7 +730,7 @@ __global__ void __launch_bounds__(kThreads) norm_map_apply_kernel(NormParams p) 
 }
 
 template <typename T, int V, bool kSilu>
-__global__ void __launch_bounds__(kThreads) norm_map_grad_apply_kernel(NormParams p) {
+__global__ void __launch_bounds__(kThreads, kMapBackward) norm_map_grad_apply_kernel(NormParams p) {
   using Q = Pack<T, V>;
   constexpr int U = 4;
   const MapSlot<V> t(p, gridDim.x - 1 - blockIdx.x);
@@ -806,7 +811,6 @@ ssd_status done(cudaError_t e) { return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA
 
 // How a shape runs, and where its scratch lies.  Only the sizes decide (not the pointers or the
 // device), so the workspace's size is known beforehand.
-constexpr int kGridBlocks = 152 * 4;    // blocks that a map kernel is cut into, at least
 constexpr int kTokenBlocks = 152 * 4;   // most blocks of the token backward, which writes a partial row each
 constexpr int kFewRows = 1024;          // up to so many partial rows are joined at once,
 constexpr int kFoldRows = 64;           // more through so many
@@ -836,9 +840,9 @@ NormPlan norm_plan(const group_norm_shape* s, bool backward) {
   const int64_t cg = s->channels / s->groups, gv = cg / max_vec(s), N = s->batch, S = s->rows;
   const int64_t tg = tile_groups(s->groups, gv);
   const int64_t blocks = std::max<int64_t>(1, N * ((s->groups + tg - 1) / tg));
-  // enough chunks for the grid, none shorter than 16 positions, at most 1024 of them
-  L.chunks = (int32_t)std::max<int64_t>(
-      1, std::min<int64_t>({(kGridBlocks + blocks - 1) / blocks, (S + 15) / 16, 1024}));
+  // enough chunks for one round of blocks, none shorter than 16 positions, at most 1024 of them
+  const int64_t round = (int64_t)kGridBlocks * (backward ? kMapBackward : kMapForward);
+  L.chunks = (int32_t)std::max<int64_t>(1, std::min<int64_t>({round / blocks, (S + 15) / 16, 1024}));
   L.chunk_rows = std::max<int64_t>(1, (S + L.chunks - 1) / L.chunks);
   L.chunks = (int32_t)std::max<int64_t>(1, (S + L.chunk_rows - 1) / L.chunk_rows);
   size_t off = sizeof(WsHeader);

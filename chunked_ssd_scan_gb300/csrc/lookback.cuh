@@ -48,7 +48,8 @@ __device__ __forceinline__ uint64_t now_ns() {
 
 // State before a tile, for a warp whose lanes own N channels each: `words` is the lane's word of the
 // nearest tile before it, `step` the (signed) distance in words to the next older one and `have`
-// how many older tiles there are (at least one).  K words are looked at in each try; the wait is
+// how many older tiles there are (at least one).  A try reads the K nearest words at once; the nearest is
+// enough if it is inclusive, and the others are evaluated only once it holds anything.  The wait is
 // bounded (1 s, then SSD_ERR_TIMEOUT is latched and the call's results are void).
 template <int K, int N>
 __device__ __forceinline__ void state_before(const uint64_t* words, int64_t step, int64_t have, float (&h)[N],
@@ -65,24 +66,31 @@ __device__ __forceinline__ void state_before(const uint64_t* words, int64_t step
         for (int c = 0; c < N; ++c) v[j][c] = 0;
       }
     }
-    bool ok[N];
+    uint32_t least = kInclusive;   // the nearest words' least state
 #pragma unroll
     for (int c = 0; c < N; ++c) {
-      ok[c] = false;
-      h[c] = 0.f;
-#pragma unroll
-      for (int j = K - 1; j >= 0; --j) {
-        const uint32_t hi = (uint32_t)(v[j][c] >> 32), state = hi >> 30;
-        const float H = __uint_as_float((uint32_t)v[j][c]);
-        const float W = -__uint_as_float(hi & 0x3fffffffu);
-        h[c] = state == kInclusive ? H : apply(W, H, h[c]);
-        ok[c] = state == kInclusive || (ok[c] && state == kMap);
-      }
+      least = min(least, (uint32_t)(v[0][c] >> 62));
+      h[c] = __uint_as_float((uint32_t)v[0][c]);
     }
-    bool all = ok[0];
+    if (__all_sync(0xffffffffu, least == kInclusive)) return;
+    if (__all_sync(0xffffffffu, least != 0)) {
+      bool all = true;
 #pragma unroll
-    for (int c = 1; c < N; ++c) all = all && ok[c];
-    if (__all_sync(0xffffffffu, all)) return;
+      for (int c = 0; c < N; ++c) {
+        bool ok = false;
+        h[c] = 0.f;
+#pragma unroll
+        for (int j = K - 1; j >= 0; --j) {
+          const uint32_t hi = (uint32_t)(v[j][c] >> 32), state = hi >> 30;
+          const float H = __uint_as_float((uint32_t)v[j][c]);
+          const float W = -__uint_as_float(hi & 0x3fffffffu);
+          h[c] = state == kInclusive ? H : apply(W, H, h[c]);
+          ok = state == kInclusive || (ok && state == kMap);
+        }
+        all = all && ok;
+      }
+      if (__all_sync(0xffffffffu, all)) return;
+    }
     if ((tries & 255) == 255) {
       const uint64_t t = now_ns();
       if (t0 == 0) t0 = t;
