@@ -2,355 +2,11 @@
 //   xhat = (x - mean) rstd, z = xhat w + b, y = act(z), statistics over the S * C/G values of a
 //   sample's group; reverse mode, dz = dy act'(z), q = dz w:
 //   dx = rstd (q - mean(q) - xhat mean(q xhat)), dw = sum dz xhat, db = sum dz.
-#include <math.h>
-#include <string.h>
-
-#include <algorithm>
-#include <initializer_list>
-#include <type_traits>
-
-#include "common.cuh"
-#include "fp_helpers.cuh"
-#include "launch.h"
-#include "pack.cuh"
+#include "group_norm.cuh"
 
 namespace ssd {
+namespace norm {
 namespace {
-
-struct NormParams {
-  const void *x, *dy;
-  const float *w, *bias, *mean_in, *rstd_in;
-  void *y, *dx;
-  float *mean, *rstd, *dw, *db;
-  int64_t N, S, C, G, cg;
-  int64_t xs[2], ds[2];
-  float eps;
-  int32_t act;
-  int32_t lanes;        // token kernels: lanes of a group
-  int32_t tile_groups;  // map kernels: groups of a column tile
-  int32_t chunks;       // map kernels: pieces that a sample's positions are cut into
-  int64_t chunk_rows;
-  float *stats;         // map kernels: [N, G, chunks, 2], mean and M2 or the two gradient sums
-  float *joined;        // [N, G, 2]
-  float *part_w, *part_b;   // rows of parameter gradient partials [part_rows, C]
-  int64_t part_rows;
-  WsHeader* hdr;
-};
-
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kGridBlocks = 152;        // blocks that a map kernel is cut into: so many times what fits an SM
-constexpr int kMapForward = 4, kMapBackward = 3;   // blocks of a map kernel on an SM
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float2 dup(float v) { return make_float2(v, v); }
-__device__ __forceinline__ float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// 1 / (1 + e^-z)
-__device__ __forceinline__ float2 sigmoid2(float2 z) {
-  const float2 t = fp::mul2(z, dup(-kLog2e));
-  const float2 d = fp::add2(make_float2(fp::ex2_approx(t.x), fp::ex2_approx(t.y)), dup(1.f));
-  return make_float2(rcp_approx(d.x), rcp_approx(d.y));
-}
-template <bool kSilu>
-__device__ __forceinline__ float2 act2(float2 z) {
-  return kSilu ? fp::mul2(z, sigmoid2(z)) : z;
-}
-// v act'(z); silu' = s + z (s - s^2)
-template <bool kSilu>
-__device__ __forceinline__ float2 times_act_grad2(float2 v, float2 z) {
-  if (!kSilu) return v;
-  const float2 s = sigmoid2(z);
-  const float2 ss = fp::fma2(fp::mul2(s, dup(-1.f)), s, s);
-  return fp::mul2(v, fp::fma2(z, ss, s));
-}
-
-// a - b, and 0 in the second place of a single value
-template <int V>
-__device__ __forceinline__ float2 minus2(float2 a, float b) {
-  float2 d = fp::add2(a, dup(-b));
-  if (V == 1) d.y = 0.f;
-  return d;
-}
-
-// ------------------------------------------------------------------------------------------------
-// One position a sample (the norm of every token): a group's values stay in the registers of `lanes`
-// neighbouring lanes (or of a whole block), K vectors of V values each; the mean and then the
-// squares around it are summed over them by shuffles.  A thread keeps its channels for all the
-// samples that its block takes, so weight and bias are read once, and has U samples in flight.
-// Bound by memory: x and y once each.
-// ------------------------------------------------------------------------------------------------
-template <bool kBlock, int M>
-__device__ __forceinline__ void group_sum(float (&v)[M], int lanes, float (&part)[2][kWarps][M], int& phase) {
-  if (!kBlock) {
-    for (int o = lanes / 2; o > 0; o /= 2) {
-#pragma unroll
-      for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(0xffffffffu, v[m], o);
-    }
-    return;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o /= 2) {
-#pragma unroll
-    for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(0xffffffffu, v[m], o);
-  }
-  if (threadIdx.x % 32 == 0) {
-#pragma unroll
-    for (int m = 0; m < M; ++m) part[phase][threadIdx.x / 32][m] = v[m];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int m = 0; m < M; ++m) {
-    v[m] = part[phase][0][m];
-#pragma unroll
-    for (int k = 1; k < kWarps; ++k) v[m] += part[phase][k][m];
-  }
-  phase ^= 1;   // the next sum writes elsewhere, and its barrier ends the reads of this one
-}
-
-// What a thread of a token kernel works on.
-template <int V, int K, bool kBlock>
-struct TokenSlot {
-  int64_t g, c;           // its group and its first channel
-  int row, rows;          // its sample within a block's step, samples of a step
-  bool in[K];             // which of its vectors lie inside the group
-  int step;               // channels from one of its vectors to the next
-  __device__ __forceinline__ TokenSlot(const NormParams& p) {
-    int l;
-    row = 0;
-    rows = 1;
-    if (kBlock) {
-      g = blockIdx.y;
-      l = threadIdx.x;
-      step = kThreads * V;
-    } else {
-      const int64_t slots = p.G * p.lanes;
-      int64_t s = (int64_t)blockIdx.y * kThreads + threadIdx.x;
-      if (slots < kThreads) {
-        rows = kThreads / (int)slots;
-        row = threadIdx.x / (int)slots;
-        s = row < rows ? threadIdx.x % (int)slots : slots;   // slots: a thread too many
-      }
-      g = s / p.lanes;
-      l = (int)(s % p.lanes);
-      step = p.lanes * V;
-    }
-    c = g * p.cg + (int64_t)l * V;
-#pragma unroll
-    for (int k = 0; k < K; ++k) in[k] = g < p.G && (int64_t)l * V + (int64_t)k * step < p.cg;
-  }
-};
-
-template <typename T, int V, int K, int U, bool kBlock, bool kSilu>
-__global__ void __launch_bounds__(kThreads) norm_token_forward_kernel(NormParams p) {
-  using Q = Pack<T, V>;
-  __shared__ float part[2][kWarps][U];
-  int phase = 0;
-  const TokenSlot<V, K, kBlock> t(p);
-  const int lanes = p.lanes;
-  float2 w[K][Q::P], bias[K][Q::P];
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    Q::zero(w[k]);
-    Q::zero(bias[k]);
-    if (t.in[k]) {
-      Q::param(p.w, t.c + k * t.step, 1.f, w[k]);
-      Q::param(p.bias, t.c + k * t.step, 0.f, bias[k]);
-    }
-  }
-  const float inv = 1.f / (float)p.cg;
-  const int64_t stride = (int64_t)gridDim.x * t.rows * U;
-  typename Q::Raw next[U][K];   // loads in flight while the samples before them are worked on
-  auto fetch = [&](int64_t n0) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-        next[u][k] = t.in[k] && n0 + u * t.rows < p.N
-                         ? Q::raw(static_cast<const T*>(p.x) + (n0 + u * t.rows) * p.xs[0] + t.c + k * t.step)
-                         : Q::none();
-  };
-  int64_t n0 = (int64_t)blockIdx.x * t.rows * U + t.row;
-  fetch(n0);
-  const bool first = p.mean && t.in[0] && t.c == t.g * p.cg;   // the lane that writes the statistics
-  for (; n0 - t.row < p.N; n0 += stride) {
-    float2 x[U][K][Q::P];
-    float mean[U], rstd[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int k = 0; k < K; ++k) Q::unpack(next[u][k], x[u][k]);
-    fetch(n0 + stride);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int e = 0; e < Q::P; ++e) s = fp::add2(s, x[u][k][e]);
-      mean[u] = s.x + s.y;
-    }
-    group_sum<kBlock>(mean, lanes, part, phase);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      mean[u] *= inv;
-      float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int e = 0; e < Q::P; ++e) {
-          x[u][k][e] = t.in[k] ? minus2<V>(x[u][k][e], mean[u]) : make_float2(0.f, 0.f);
-          s = fp::fma2(x[u][k][e], x[u][k][e], s);
-        }
-      rstd[u] = s.x + s.y;
-    }
-    group_sum<kBlock>(rstd, lanes, part, phase);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      rstd[u] = rsqrtf(fmaf(rstd[u], inv, p.eps));
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int e = 0; e < Q::P; ++e)
-          x[u][k][e] = act2<kSilu>(fp::fma2(fp::mul2(x[u][k][e], dup(rstd[u])), w[k][e], bias[k][e]));
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t n = n0 + u * t.rows;
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int64_t at = n * p.C + t.c + k * t.step;
-        if (t.in[k] && n < p.N && SSD_INDEX_OK(p.hdr, at + V - 1, p.N * p.C, 70))
-          Q::store(static_cast<T*>(p.y) + at, x[u][k]);
-      }
-      if (first && n < p.N && SSD_INDEX_OK(p.hdr, n * p.G + t.g, p.N * p.G, 71)) {
-        p.mean[n * p.G + t.g] = mean[u];
-        p.rstd[n * p.G + t.g] = rstd[u];
-      }
-    }
-  }
-}
-
-template <typename T, int V, int K, int U, bool kBlock, bool kSilu>
-__global__ void __launch_bounds__(kThreads) norm_token_backward_kernel(NormParams p) {
-  using Q = Pack<T, V>;
-  __shared__ float part[2][kWarps][2 * U];
-  int phase = 0;
-  const TokenSlot<V, K, kBlock> t(p);
-  const int lanes = p.lanes;
-  float2 w[K][Q::P], bias[K][Q::P], dw[K][Q::P], db[K][Q::P];
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    Q::zero(w[k]);
-    Q::zero(bias[k]);
-    Q::zero(dw[k]);
-    Q::zero(db[k]);
-    if (t.in[k]) {
-      Q::param(p.w, t.c + k * t.step, 1.f, w[k]);
-      Q::param(p.bias, t.c + k * t.step, 0.f, bias[k]);
-    }
-  }
-  const float inv = 1.f / (float)p.cg;
-  const int64_t stride = (int64_t)gridDim.x * t.rows * U;
-  typename Q::Raw nx[U][K], ny[U][K];   // loads in flight; dy = 0 where there is nothing adds nothing
-  float2 nst[U];
-  auto fetch = [&](int64_t n0) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t n = n0 + u * t.rows;
-      const bool live = t.g < p.G && n < p.N;
-      nst[u] = live ? make_float2(__ldg(p.mean_in + n * p.G + t.g), __ldg(p.rstd_in + n * p.G + t.g)) : dup(0.f);
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const bool in = t.in[k] && n < p.N;
-        nx[u][k] = in ? Q::raw(static_cast<const T*>(p.x) + n * p.xs[0] + t.c + k * t.step) : Q::none();
-        ny[u][k] = in ? Q::raw(static_cast<const T*>(p.dy) + n * p.ds[0] + t.c + k * t.step) : Q::none();
-      }
-    }
-  };
-  int64_t n0 = (int64_t)blockIdx.x * t.rows * U + t.row;
-  fetch(n0);
-  for (; n0 - t.row < p.N; n0 += stride) {
-    float2 x[U][K][Q::P], q[U][K][Q::P];
-    float rstd[U], mean[U], sums[2 * U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      mean[u] = nst[u].x;
-      rstd[u] = nst[u].y;
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        Q::unpack(nx[u][k], x[u][k]);
-        Q::unpack(ny[u][k], q[u][k]);
-      }
-    }
-    fetch(n0 + stride);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float2 s = make_float2(0.f, 0.f), sx = s;
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int e = 0; e < Q::P; ++e) {
-          const float2 xh = fp::mul2(minus2<V>(x[u][k][e], mean[u]), dup(rstd[u]));
-          const float2 dz = times_act_grad2<kSilu>(q[u][k][e], fp::fma2(xh, w[k][e], bias[k][e]));
-          db[k][e] = fp::add2(db[k][e], dz);
-          dw[k][e] = fp::fma2(dz, xh, dw[k][e]);
-          x[u][k][e] = xh;
-          q[u][k][e] = fp::mul2(dz, w[k][e]);
-          s = fp::add2(s, q[u][k][e]);
-          sx = fp::fma2(q[u][k][e], xh, sx);
-        }
-      sums[2 * u] = s.x + s.y;
-      sums[2 * u + 1] = sx.x + sx.y;
-    }
-    group_sum<kBlock>(sums, lanes, part, phase);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t n = n0 + u * t.rows;
-      const float2 ms = dup(-sums[2 * u] * inv), mx = dup(-sums[2 * u + 1] * inv);
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int64_t at = n * p.C + t.c + k * t.step;
-#pragma unroll
-        for (int e = 0; e < Q::P; ++e)
-          x[u][k][e] = fp::mul2(dup(rstd[u]), fp::fma2(x[u][k][e], mx, fp::add2(q[u][k][e], ms)));
-        if (t.in[k] && n < p.N && SSD_INDEX_OK(p.hdr, at + V - 1, p.N * p.C, 72))
-          Q::store(static_cast<T*>(p.dx) + at, x[u][k]);
-      }
-    }
-  }
-  if (p.part_rows == 0) return;
-  __shared__ float4 rows[kThreads][Q::P];   // the block's rows of samples joined, one partial a block
-  const int slots = (int)min((int64_t)kThreads, p.G * lanes);   // threads of one row
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    if (!kBlock && t.rows > 1) {
-      __syncthreads();
-#pragma unroll
-      for (int e = 0; e < Q::P; ++e) rows[threadIdx.x][e] = make_float4(dw[k][e].x, dw[k][e].y, db[k][e].x, db[k][e].y);
-      __syncthreads();
-      if (t.row > 0) continue;
-      for (int r = 1; r < t.rows; ++r) {
-#pragma unroll
-        for (int e = 0; e < Q::P; ++e) {
-          const float4 v = rows[threadIdx.x + r * slots][e];
-          dw[k][e] = fp::add2(dw[k][e], make_float2(v.x, v.y));
-          db[k][e] = fp::add2(db[k][e], make_float2(v.z, v.w));
-        }
-      }
-    }
-    const int64_t at = (int64_t)blockIdx.x * p.C + t.c + k * t.step;
-    if (!t.in[k] || !SSD_INDEX_OK(p.hdr, at + V - 1, p.part_rows * p.C, 73)) continue;
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      p.part_w[at + e] = e % 2 ? dw[k][e / 2].y : dw[k][e / 2].x;
-      p.part_b[at + e] = e % 2 ? db[k][e / 2].y : db[k][e / 2].x;
-    }
-  }
-}
 
 // ------------------------------------------------------------------------------------------------
 // Many positions a sample: a sample's positions are cut into chunks, a block takes one chunk of one
@@ -600,42 +256,6 @@ __global__ void __launch_bounds__(kThreads, kMapBackward) norm_map_grad_sums_ker
   }
 }
 
-// dweight and dbias of 32 channels from share `part` of `parts` of the partial rows, by a block of 32
-// warps: a warp adds every 32nd row, eight loads of each array in flight, and the warps are joined in
-// their order into row `part`.
-__device__ __forceinline__ void param_grad(const NormParams& p, int64_t cols, int part, int parts) {
-  __shared__ float2 sums[32][33];
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int64_t c = cols * 32 + lane;
-  const int64_t share = (p.part_rows + parts - 1) / parts, r0 = part * share, r1 = min(p.part_rows, r0 + share);
-  float2 s = make_float2(0.f, 0.f);
-  if (c < p.C) {
-    constexpr int U = 8;
-    for (int64_t r = r0 + warp; r < r1; r += 32 * U) {
-      const float *pw = p.part_w + r * p.C + c, *pb = p.part_b + r * p.C + c;
-      float2 v[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        v[u] = r + 32 * u < r1 ? make_float2(__ldg(pw + u * 32 * p.C), __ldg(pb + u * 32 * p.C))
-                               : make_float2(0.f, 0.f);
-#pragma unroll
-      for (int u = 0; u < U; ++u) s = fp::add2(s, v[u]);
-    }
-  }
-  sums[warp][lane] = s;
-  __syncthreads();
-  if (warp == 0 && c < p.C) {
-    float2 v = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < 32; ++k) v = fp::add2(v, sums[k][lane]);
-    if (p.dw) p.dw[part * p.C + c] = v.x;
-    if (p.db) p.db[part * p.C + c] = v.y;
-  }
-}
-__global__ void __launch_bounds__(1024) norm_param_grad_kernel(NormParams p) {
-  param_grad(p, blockIdx.x, blockIdx.y, gridDim.y);
-}
-
 // One warp a (sample, group): the chunks' statistics joined into `joined` [N, G, 2]: mean and rstd, or the
 // means of q and q xhat.  The blocks behind the groups' join the parameters' gradients instead (see
 // param_grad).
@@ -649,10 +269,17 @@ __global__ void __launch_bounds__(1024) norm_map_join_kernel(NormParams p, uint3
   const int lane = threadIdx.x % 32;
   if (at >= p.N * p.G) return;
   const float2* st = reinterpret_cast<const float2*>(p.stats) + at * p.chunks;
+  constexpr int kAhead = 4;   // loads of a lane in flight
   float2 out;
   if (kGrad) {
     float2 m = make_float2(0.f, 0.f);
-    for (int c = lane; c < p.chunks; c += 32) m = fp::add2(m, __ldg(st + c));
+    for (int c0 = lane; c0 < p.chunks; c0 += 32 * kAhead) {
+      float2 s[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) s[k] = c0 + 32 * k < p.chunks ? __ldg(st + c0 + 32 * k) : make_float2(0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) m = fp::add2(m, s[k]);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o /= 2)
       m = fp::add2(m, make_float2(__shfl_xor_sync(0xffffffffu, m.x, o), __shfl_xor_sync(0xffffffffu, m.y, o)));
@@ -660,10 +287,16 @@ __global__ void __launch_bounds__(1024) norm_map_join_kernel(NormParams p, uint3
     out = make_float2(m.x * inv, m.y * inv);
   } else {
     Moments m = {0.f, 0.f, 0.f};
-    for (int c = lane; c < p.chunks; c += 32) {
-      const float n = (float)(min(p.S, (c + 1) * p.chunk_rows) - c * p.chunk_rows) * (float)p.cg;
-      const float2 s = __ldg(st + c);
-      m = join(m, {n, s.x, s.y});
+    for (int c0 = lane; c0 < p.chunks; c0 += 32 * kAhead) {
+      float2 s[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) s[k] = c0 + 32 * k < p.chunks ? __ldg(st + c0 + 32 * k) : make_float2(0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int c = c0 + 32 * k;
+        const float n = (float)(min(p.S, (c + 1) * p.chunk_rows) - c * p.chunk_rows) * (float)p.cg;
+        if (c < p.chunks) m = join(m, {n, s[k].x, s[k].y});
+      }
     }
     m = join_lanes(m);
     out = make_float2(m.mean, rsqrtf(m.m2 / m.n + p.eps));
@@ -811,10 +444,6 @@ ssd_status done(cudaError_t e) { return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA
 
 // How a shape runs, and where its scratch lies.  Only the sizes decide (not the pointers or the
 // device), so the workspace's size is known beforehand.
-constexpr int kTokenBlocks = 152 * 4;   // most blocks of the token backward, which writes a partial row each
-constexpr int kFewRows = 1024;          // up to so many partial rows are joined at once,
-constexpr int kFoldRows = 64;           // more through so many
-constexpr int kTokenWidth = 4 * kThreads;   // vectors of a group that a token kernel holds in registers
 struct NormPlan {
   int64_t part_rows = 0;
   int32_t chunks = 1;
@@ -878,69 +507,10 @@ int call_vec(const group_norm_shape* s, std::initializer_list<const void*> array
   return v;
 }
 
-// Joins the partial rows of the parameters' gradients: at once, or where there are many through
-// kFoldRows of them behind the others.
-cudaError_t launch_param_grad(NormParams p, cudaStream_t st) {
-  if (p.part_rows == 0) return cudaSuccess;
-  const unsigned grid = (unsigned)((p.C + 31) / 32);
-  if (p.part_rows > kFewRows) {
-    NormParams f = p;
-    f.dw = p.part_w + p.part_rows * p.C;
-    f.db = p.part_b + p.part_rows * p.C;
-    norm_param_grad_kernel<<<dim3(grid, kFoldRows), 1024, 0, st>>>(f);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    p.part_w = f.dw;
-    p.part_b = f.db;
-    p.part_rows = kFoldRows;
-  }
-  norm_param_grad_kernel<<<dim3(grid, 1), 1024, 0, st>>>(p);
-  return cudaGetLastError();
-}
-
-template <typename T, int V, int K, bool kBlock, bool kSilu>
-cudaError_t launch_tokens(NormParams p, bool backward, cudaStream_t st) {
-  constexpr int UF = K == 1 ? 4 : K == 2 ? 2 : 1, UB = K == 1 ? 2 : 1;   // samples in flight
-  const int64_t gv = p.cg / V;
-  p.lanes = 1;
-  while (!kBlock && p.lanes < 32 && p.lanes * K < gv) p.lanes *= 2;
-  const int64_t slots = p.G * p.lanes;
-  const int64_t rows = kBlock || slots >= kThreads ? 1 : kThreads / slots;
-  const int64_t by = kBlock ? p.G : (slots + kThreads - 1) / kThreads;
-  if (backward) {
-    const int64_t steps = (p.N + rows * UB - 1) / (rows * UB);
-    auto* kernel = norm_token_backward_kernel<T, V, K, UB, kBlock, kSilu>;
-    int blocks = 0;
-    cudaError_t e = resident_blocks(kernel, kThreads, 0, &blocks);
-    if (e != cudaSuccess) return e;
-    blocks = std::min(blocks, kTokenBlocks);
-    const int64_t bx = std::min<int64_t>(steps, std::max<int64_t>(1, blocks / by));
-    p.part_rows = p.dw || p.db ? bx : 0;
-    kernel<<<dim3((unsigned)bx, (unsigned)by), kThreads, 0, st>>>(p);
-    e = cudaGetLastError();
-    return e == cudaSuccess ? launch_param_grad(p, st) : e;
-  }
-  auto* kernel = norm_token_forward_kernel<T, V, K, UF, kBlock, kSilu>;
-  int blocks = 0;
-  const cudaError_t e = resident_blocks(kernel, kThreads, 0, &blocks);
-  if (e != cudaSuccess) return e;
-  const int64_t steps = (p.N + rows * UF - 1) / (rows * UF);
-  const int64_t bx = std::min<int64_t>(steps, std::max<int64_t>(1, blocks / by));
-  kernel<<<dim3((unsigned)bx, (unsigned)by), kThreads, 0, st>>>(p);
-  return cudaGetLastError();
-}
-
 template <typename T, int V, bool kSilu>
 cudaError_t launch_as(NormParams p, bool backward, cudaStream_t st) {
   const int64_t gv = p.cg / V;
-  if (runs_as_tokens(p.S, p.G, gv)) {
-    if (gv <= 32) return launch_tokens<T, V, 1, false, kSilu>(p, backward, st);
-    if (gv <= 64) return launch_tokens<T, V, 2, false, kSilu>(p, backward, st);
-    if (gv <= 128) return launch_tokens<T, V, 4, false, kSilu>(p, backward, st);
-    if (gv <= 256) return launch_tokens<T, V, 1, true, kSilu>(p, backward, st);
-    if (gv <= 512) return launch_tokens<T, V, 2, true, kSilu>(p, backward, st);
-    return launch_tokens<T, V, 4, true, kSilu>(p, backward, st);
-  }
+  if (runs_as_tokens(p.S, p.G, gv)) return run_tokens<T, V>(p, backward, st);
   p.tile_groups = (int32_t)tile_groups(p.G, gv);
   p.part_rows = p.dw || p.db ? p.N * p.chunks : 0;
   const unsigned grid = (unsigned)(p.N * ((p.G + p.tile_groups - 1) / p.tile_groups) * p.chunks);
@@ -992,9 +562,11 @@ cudaError_t launch(NormParams p, const group_norm_shape* s, int vec, bool backwa
 }
 
 }  // namespace
+}  // namespace norm
 }  // namespace ssd
 
 using namespace ssd;
+using namespace ssd::norm;
 
 extern "C" {
 
