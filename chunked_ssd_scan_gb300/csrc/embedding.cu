@@ -123,6 +123,7 @@ __device__ __forceinline__ void clear_rows(const EmbedParams& p) {
 // Keys from ids, the rows that occur, and how many keys of a block have each lowest digit.
 template <typename Id>
 __global__ void __launch_bounds__(kThreads) embed_keys_kernel(EmbedParams p) {
+  follow();
   __shared__ uint32_t bins[kBins];
   bins[threadIdx.x] = 0;
   __syncthreads();
@@ -146,8 +147,77 @@ __global__ void __launch_bounds__(kThreads) embed_keys_kernel(EmbedParams p) {
 }
 static_assert(kBins == kThreads, "a thread a bin");
 
+// Few tokens: one block sorts them in shared memory, all passes in one launch.
+template <typename Id>
+__global__ void __launch_bounds__(kThreads) embed_small_sort_kernel(EmbedParams p, int passes) {
+  constexpr int kW = kThreads / 32;
+  __shared__ uint32_t keys[2][kSortTile], places[2][kSortTile], seen[kW][kBins], warps[kW];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, n = (int)p.n;
+  follow();
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const int64_t r = row_of(static_cast<const Id*>(p.ids), i, p.rows);
+    keys[0][i] = r < 0 ? (uint32_t)p.rows : (uint32_t)r;
+    places[0][i] = (uint32_t)i;
+    if (r >= 0) p.used[r] = 1;
+  }
+  for (int pass = 0; pass < passes; ++pass) {
+    const uint32_t *key = keys[pass & 1], *pos = places[pass & 1];
+    const int shift = 8 * pass;
+    for (int k = threadIdx.x; k < kW * kBins; k += kThreads) (&seen[0][0])[k] = 0;
+    __syncthreads();
+    uint32_t rank[kKeys];
+    const int i0 = warp * 32 * kKeys + lane;   // a warp takes neighbouring keys, 32 at a time
+#pragma unroll
+    for (int k = 0; k < kKeys; ++k) {
+      const bool in = i0 + k * 32 < n;
+      const uint32_t digit = in ? (key[i0 + k * 32] >> shift) & (kBins - 1) : kBins;
+      const uint32_t same = __match_any_sync(0xffffffffu, digit);
+      const uint32_t had = in ? seen[warp][digit] : 0u;
+      rank[k] = had + __popc(same & ((1u << lane) - 1));
+      __syncwarp();
+      if (in && lane == __ffs(same) - 1) seen[warp][digit] = had + __popc(same);
+      __syncwarp();
+    }
+    __syncthreads();
+    uint32_t all = 0;   // a thread a digit
+#pragma unroll
+    for (int k = 0; k < kW; ++k) all += seen[k][threadIdx.x];
+    uint32_t inc = all;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) warps[warp] = inc;
+    __syncthreads();
+    uint32_t base = inc - all;
+    for (int k = 0; k < warp; ++k) base += warps[k];
+#pragma unroll
+    for (int k = 0; k < kW; ++k) {
+      const uint32_t c = seen[k][threadIdx.x];
+      seen[k][threadIdx.x] = base;
+      base += c;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kKeys; ++k) {
+      const int i = i0 + k * 32;
+      if (i >= n) continue;
+      const uint32_t at = seen[warp][(key[i] >> shift) & (kBins - 1)] + rank[k];
+      keys[(pass & 1) ^ 1][at] = key[i];
+      places[(pass & 1) ^ 1][at] = pos[i];
+    }
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    p.key[p.in][i] = keys[passes & 1][i];
+    p.pos[p.in][i] = places[passes & 1][i];
+  }
+}
+
 // hist becomes its exclusive prefix sum over digits, then tiles, by one block.
 __global__ void __launch_bounds__(kThreads) embed_scan_kernel(EmbedParams p) {
+  follow();
   if (blockIdx.x > 0) return clear_rows(p);
   __shared__ uint32_t warps[kThreads / 32];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -193,6 +263,7 @@ __global__ void __launch_bounds__(kThreads) embed_scan_kernel(EmbedParams p) {
 constexpr int kFewTiles = 64;
 template <bool kScanned>
 __global__ void __launch_bounds__(kThreads) embed_scatter_kernel(EmbedParams p) {
+  follow();
   if ((int)blockIdx.x >= p.work_blocks) return clear_rows(p);
   constexpr int kW = kThreads / 32;
   __shared__ uint32_t seen[kW][kBins];   // keys of the warp with this digit
@@ -291,6 +362,7 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src) {
 
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) embed_sum_kernel(EmbedParams p, int cols, int subs) {
+  follow();
   constexpr int kRing = 12;   // rows in flight: 48 KB a block, four blocks an SM
   __shared__ Vec<T, V> ring[kRing][kThreads];
   if ((int)blockIdx.x >= p.work_blocks) return clear_rows(p);
@@ -302,9 +374,9 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(EmbedParams p, int 
   const int n = (int)min((int64_t)p.piece, p.n - j0);
   const uint32_t *key = p.key[p.in] + j0, *pos = p.pos[p.in] + j0;
   const T* dout = static_cast<const T*>(p.dout) + d;
-  uint32_t cur = __ldg(key);
+  uint32_t cur = *key;
   if (cur == none) return;
-  bool open = j0 > 0 && __ldg(key - 1) == cur;   // the run in hand started in an earlier piece
+  bool open = j0 > 0 && key[-1] == cur;   // the run in hand started in an earlier piece
   float acc[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) acc[e] = 0.f;
@@ -315,13 +387,13 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(EmbedParams p, int 
       store_sum<V>(to + d, acc, whole ? p.scale : 1.f);
   };
   auto request = [&](int j, int slot) {
-    if (j < n) copy_async<V * (int)sizeof(T)>(&ring[slot][threadIdx.x], dout + (int64_t)__ldg(pos + j) * p.D);
+    if (j < n) copy_async<V * (int)sizeof(T)>(&ring[slot][threadIdx.x], dout + (int64_t)pos[j] * p.D);
     cp_async_commit();
   };
   for (int j = 0; j < kRing; ++j) request(j, j);
   int slot = 0;
   for (int j = 0; j < n; ++j) {
-    const uint32_t k = __ldg(key + j);
+    const uint32_t k = key[j];
     if (k == none) break;   // padding stands behind all rows
     if (k != cur) {
       flush(false);
@@ -338,13 +410,14 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(EmbedParams p, int 
     slot = slot + 1 == kRing ? 0 : slot + 1;
   }
   cp_async_wait_all();
-  flush(j0 + n < p.n && __ldg(key + n) == cur);
+  flush(j0 + n < p.n && key[n] == cur);
 }
 
 // Runs over more than one piece: the piece where one starts adds the heads of those after it.  Keys and
 // heads are asked for together (a head that is not the run's is not used), eight pieces at a time.
 template <int V>
 __global__ void __launch_bounds__(kThreads) embed_join_kernel(EmbedParams p, int cols, int subs) {
+  follow();
   constexpr int U = 8;
   if ((int)blockIdx.x >= p.work_blocks) return clear_rows(p);
   const int col = threadIdx.x % cols, sub = threadIdx.x / cols;
@@ -353,8 +426,8 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(EmbedParams p, int
   const uint32_t* key = p.key[p.in];
   const int64_t j0 = piece * p.piece, j1 = j0 + p.piece;
   if (j1 >= p.n) return;
-  const uint32_t run = __ldg(key + j1);   // the run that crosses the piece's end, if it is in this piece
-  const uint32_t last = __ldg(key + j1 - 1), early = j0 > 0 ? __ldg(key + j0 - 1) : (uint32_t)p.rows;
+  const uint32_t run = key[j1];   // the run that crosses the piece's end, if it is in this piece
+  const uint32_t last = key[j1 - 1], early = j0 > 0 ? key[j0 - 1] : (uint32_t)p.rows;
   if (run == (uint32_t)p.rows || last != run || early == run) return;   // or it started earlier
   using F = Vec<float, V>;
   F acc = *reinterpret_cast<const F*>(p.tail + piece * p.D + d);
@@ -366,7 +439,7 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(EmbedParams p, int
       in[u] = q + u < p.pieces;
       if (in[u]) {
         h[u] = *reinterpret_cast<const F*>(p.head + (q + u) * p.D + d);
-        in[u] = __ldg(key + (q + u) * p.piece) == run;
+        in[u] = key[(q + u) * p.piece] == run;
       }
     }
 #pragma unroll
@@ -492,16 +565,14 @@ cudaError_t launch_sum(EmbedParams p, Fill& fill, cudaStream_t st) {
   const Split s = split_row((p.D + V - 1) / V);
   const int work = (int)((p.pieces + s.subs - 1) / s.subs);
   const unsigned bx = fill.take(p, kSumShare, work);
-  embed_sum_kernel<T, V><<<dim3(bx, s.slices), kThreads, 0, st>>>(p, s.cols, s.subs);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  const cudaError_t e = launch_next(embed_sum_kernel<T, V>, dim3(bx, s.slices), kThreads, 0, st, p, s.cols, s.subs);
+  if (e != cudaSuccess || p.pieces < 2) return e;   // one piece: no run crosses its end
   // the partial rows are aligned as the width is
   const int v = p.D % 4 == 0 ? 4 : p.D % 2 == 0 ? 2 : 1;
   const Split js = split_row(p.D / v);
   const unsigned jx = fill.take(p, kJoinShare, (int)((p.pieces + js.subs - 1) / js.subs));
   auto* join = v == 4 ? embed_join_kernel<4> : v == 2 ? embed_join_kernel<2> : embed_join_kernel<1>;
-  join<<<dim3(jx, js.slices), kThreads, 0, st>>>(p, js.cols, js.subs);
-  return cudaGetLastError();
+  return launch_next(join, dim3(jx, js.slices), kThreads, 0, st, p, js.cols, js.subs);
 }
 
 template <typename T, typename Id>
@@ -509,24 +580,23 @@ cudaError_t launch_backward(EmbedParams p, size_t cleared, cudaStream_t st) {
   cudaError_t e = cudaMemsetAsync(p.used, 0, cleared, st);
   if (e != cudaSuccess) return e;
   const int passes = embed_passes(p.rows);
-  const bool scan = p.sort_tiles > kFewTiles;
+  const bool small = p.n <= kSortTile, scan = p.sort_tiles > kFewTiles;
   Fill fill;
-  fill.all = passes * (scan ? 2 : 1) * kSortShare + kSumShare + kJoinShare;
+  fill.all = (small ? 0 : passes * (scan ? 2 : 1) * kSortShare) + kSumShare + (p.pieces > 1 ? kJoinShare : 0);
   p.in = 0;
-  embed_keys_kernel<Id><<<(unsigned)p.sort_tiles, kThreads, 0, st>>>(p);
+  if (small) embed_small_sort_kernel<Id><<<1, kThreads, 0, st>>>(p, passes);
+  else embed_keys_kernel<Id><<<(unsigned)p.sort_tiles, kThreads, 0, st>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  for (int pass = 0; pass < passes; ++pass) {
+  for (int pass = 0; pass < passes && !small; ++pass) {
     p.shift = 8 * pass;
     p.next_hist = pass + 1 < passes ? p.hist + (int64_t)kBins * p.sort_tiles : nullptr;
     if (scan) {
       const unsigned grid = fill.take(p, kSortShare, 1);
-      embed_scan_kernel<<<grid, kThreads, 0, st>>>(p);
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      if ((e = launch_next(embed_scan_kernel, grid, kThreads, 0, st, p)) != cudaSuccess) return e;
     }
     const unsigned grid = fill.take(p, kSortShare, p.sort_tiles);
-    if (scan) embed_scatter_kernel<true><<<grid, kThreads, 0, st>>>(p);
-    else embed_scatter_kernel<false><<<grid, kThreads, 0, st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    auto* scatter = scan ? embed_scatter_kernel<true> : embed_scatter_kernel<false>;
+    if ((e = launch_next(scatter, grid, kThreads, 0, st, p)) != cudaSuccess) return e;
     p.hist = p.next_hist;
     p.in ^= 1;
   }

@@ -432,6 +432,7 @@ static_assert(kWarps * kSpwBwd == kChunk, "a backward tile starts from one kept 
 
 template <typename T, int ALIGN, int MINB>
 __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(RecParams p) {
+  follow();
   constexpr int SPW = kSpwBwd, kSteps = kWarps * SPW, kCh = Tile<T>::kCh, kCpl = Tile<T>::kCpl;
   constexpr int kPairs = Walk<T, SPW>::kPairs, kWarpBytes = SPW * kRowBytes, kArray = kWarps * kWarpBytes;
   constexpr int kStage = 4 * kArray;
@@ -699,6 +700,7 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(RecParams 
 // 32nd row each, joined in warp order.
 __global__ void __launch_bounds__(1024) rec_ddecay_kernel(RecParams p) {
   __shared__ float part[32][33];
+  follow();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int64_t d = (int64_t)blockIdx.x * 32 + lane, rows = p.batch * p.nch;
   float s[4] = {0.f, 0.f, 0.f, 0.f};
@@ -902,8 +904,7 @@ cudaError_t launch_backward_as(RecParams p, cudaStream_t st) {
   }
   kernel<<<(unsigned)std::min<int64_t>(blocks, p.tiles), kThreads, kSmem, st>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  rec_ddecay_kernel<<<(unsigned)((p.D + 31) / 32), 1024, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_next(rec_ddecay_kernel, (unsigned)((p.D + 31) / 32), 1024, 0, st, p);
 }
 
 cudaError_t launch_backward(RecParams p, bool bf16, cudaStream_t st) {

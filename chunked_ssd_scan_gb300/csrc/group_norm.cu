@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(kThreads, kMapForward) norm_map_stats_kernel(N
   using Q = Pack<T, V>;
   constexpr int U = 8;   // positions in flight: their moments are formed directly
   __shared__ Moments all[kThreads];
+  follow();
   const MapSlot<V> t(p, blockIdx.x);
   Moments m = {0.f, 0.f, 0.f};
   if (t.row < t.rows)
@@ -179,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, kMapBackward) norm_map_grad_sums_ker
   constexpr int U = 4;
   __shared__ float4 all[kThreads][Q::P];
   __shared__ float2 wide[kThreads];
+  follow();
   const MapSlot<V> t(p, blockIdx.x);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   float2 mine = make_float2(0.f, 0.f);   // of the first row's threads: their channels' sums times w
@@ -261,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, kMapBackward) norm_map_grad_sums_ker
 // param_grad).
 template <bool kGrad>
 __global__ void __launch_bounds__(1024) norm_map_join_kernel(NormParams p, uint32_t group_blocks) {
+  follow();
   if (blockIdx.x >= group_blocks) {
     if (kGrad) param_grad(p, blockIdx.x - group_blocks, 0, 1);
     return;
@@ -276,7 +279,7 @@ __global__ void __launch_bounds__(1024) norm_map_join_kernel(NormParams p, uint3
     for (int c0 = lane; c0 < p.chunks; c0 += 32 * kAhead) {
       float2 s[kAhead];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) s[k] = c0 + 32 * k < p.chunks ? __ldg(st + c0 + 32 * k) : make_float2(0.f, 0.f);
+      for (int k = 0; k < kAhead; ++k) s[k] = c0 + 32 * k < p.chunks ? __ldcg(st + c0 + 32 * k) : make_float2(0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) m = fp::add2(m, s[k]);
     }
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(1024) norm_map_join_kernel(NormParams p, uint3
     for (int c0 = lane; c0 < p.chunks; c0 += 32 * kAhead) {
       float2 s[kAhead];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) s[k] = c0 + 32 * k < p.chunks ? __ldg(st + c0 + 32 * k) : make_float2(0.f, 0.f);
+      for (int k = 0; k < kAhead; ++k) s[k] = c0 + 32 * k < p.chunks ? __ldcg(st + c0 + 32 * k) : make_float2(0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         const int c = c0 + 32 * k;
@@ -310,13 +313,14 @@ __global__ void __launch_bounds__(1024) norm_map_join_kernel(NormParams p, uint3
 
 template <typename T, int V, bool kSilu>
 __global__ void __launch_bounds__(kThreads, kMapForward) norm_map_apply_kernel(NormParams p) {
+  follow();
   using Q = Pack<T, V>;
   constexpr int U = V * (int)sizeof(T) >= 16 ? 4 : 8;
   const MapSlot<V> t(p, gridDim.x - 1 - blockIdx.x);
   if (t.row >= t.rows) return;
   for (int v = t.col; v < t.vecs; v += kThreads) {
     const int64_t c = t.channel(p, v);
-    const float2 st = __ldg(reinterpret_cast<const float2*>(p.joined) + t.n * p.G + t.g0 + v / t.gv);
+    const float2 st = __ldcg(reinterpret_cast<const float2*>(p.joined) + t.n * p.G + t.g0 + v / t.gv);
     float2 a[Q::P], b[Q::P];   // (x - mean) a + b: x a + b' would round around a large mean
     Q::param(p.w, c, 1.f, a);
     Q::param(p.bias, c, 0.f, b);
@@ -364,6 +368,7 @@ __global__ void __launch_bounds__(kThreads, kMapForward) norm_map_apply_kernel(N
 
 template <typename T, int V, bool kSilu>
 __global__ void __launch_bounds__(kThreads, kMapBackward) norm_map_grad_apply_kernel(NormParams p) {
+  follow();
   using Q = Pack<T, V>;
   constexpr int U = 4;
   const MapSlot<V> t(p, gridDim.x - 1 - blockIdx.x);
@@ -371,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, kMapBackward) norm_map_grad_apply_ke
   for (int v = t.col; v < t.vecs; v += kThreads) {
     const int64_t c = t.channel(p, v), at = t.n * p.G + t.g0 + v / t.gv;
     const float mean = __ldg(p.mean_in + at), rstd = __ldg(p.rstd_in + at);
-    const float2 m = __ldg(reinterpret_cast<const float2*>(p.joined) + at);
+    const float2 m = __ldcg(reinterpret_cast<const float2*>(p.joined) + at);
     float2 w[Q::P], bias[Q::P];
     Q::param(p.w, c, 1.f, w);
     Q::param(p.bias, c, 0.f, bias);
@@ -519,20 +524,19 @@ cudaError_t launch_as(NormParams p, bool backward, cudaStream_t st) {
     norm_map_stats_kernel<T, V><<<grid, kThreads, 0, st>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    norm_map_join_kernel<false><<<group_blocks, 1024, 0, st>>>(p, group_blocks);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    norm_map_apply_kernel<T, V, kSilu><<<grid, kThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    e = launch_next(norm_map_join_kernel<false>, group_blocks, 1024, 0, st, p, group_blocks);
+    if (e != cudaSuccess) return e;
+    return launch_next(norm_map_apply_kernel<T, V, kSilu>, grid, kThreads, 0, st, p);
   }
   norm_map_grad_sums_kernel<T, V, kSilu><<<grid, kThreads, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // few partial rows: the join's launch takes the parameters' gradients along
   const bool along = p.part_rows > 0 && p.part_rows <= kFewRows;
-  norm_map_join_kernel<true><<<group_blocks + (along ? (unsigned)((p.C + 31) / 32) : 0u), 1024, 0, st>>>(p, group_blocks);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  norm_map_grad_apply_kernel<T, V, kSilu><<<grid, kThreads, 0, st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const unsigned more = along ? (unsigned)((p.C + 31) / 32) : 0u;
+  e = launch_next(norm_map_join_kernel<true>, group_blocks + more, 1024, 0, st, p, group_blocks);
+  if (e != cudaSuccess) return e;
+  if ((e = launch_next(norm_map_grad_apply_kernel<T, V, kSilu>, grid, kThreads, 0, st, p)) != cudaSuccess) return e;
   return along ? cudaSuccess : launch_param_grad(p, st);
 }
 

@@ -96,7 +96,7 @@ static __device__ __forceinline__ void param_grad(const NormParams& p, int64_t c
       float2 v[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        v[u] = r + 32 * u < r1 ? make_float2(__ldg(pw + u * 32 * p.C), __ldg(pb + u * 32 * p.C))
+        v[u] = r + 32 * u < r1 ? make_float2(__ldcg(pw + u * 32 * p.C), __ldcg(pb + u * 32 * p.C))
                                : make_float2(0.f, 0.f);
 #pragma unroll
       for (int u = 0; u < U; ++u) s = fp::add2(s, v[u]);
@@ -113,6 +113,7 @@ static __device__ __forceinline__ void param_grad(const NormParams& p, int64_t c
   }
 }
 static __global__ void __launch_bounds__(1024) norm_param_grad_kernel(NormParams p) {
+  follow();
   param_grad(p, blockIdx.x, blockIdx.y, gridDim.y);
 }
 
@@ -125,15 +126,13 @@ inline cudaError_t launch_param_grad(NormParams p, cudaStream_t st) {
     NormParams f = p;
     f.dw = p.part_w + p.part_rows * p.C;
     f.db = p.part_b + p.part_rows * p.C;
-    norm_param_grad_kernel<<<dim3(grid, kFoldRows), 1024, 0, st>>>(f);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_next(norm_param_grad_kernel, dim3(grid, kFoldRows), 1024, 0, st, f);
     if (e != cudaSuccess) return e;
     p.part_w = f.dw;
     p.part_b = f.db;
     p.part_rows = kFoldRows;
   }
-  norm_param_grad_kernel<<<dim3(grid, 1), 1024, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_next(norm_param_grad_kernel, dim3(grid, 1), 1024, 0, st, p);
 }
 
 // Runs a call with one position a sample; a group is at most kTokenWidth vectors of V values.

@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(kThreads, kBlock || K > 1 ? 1 : 3) norm_token_
 
 template <typename T, int V, int K, int U, bool kBlock, bool kSilu, bool kFull>
 __global__ void __launch_bounds__(kThreads) norm_token_backward_kernel(NormParams p) {
+  follow();
   using Q = Pack<T, V>;
   __shared__ float part[2][kWarps][2 * U];
   int phase = 0;
