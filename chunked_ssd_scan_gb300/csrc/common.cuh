@@ -17,7 +17,8 @@ struct WsHeader {
   int32_t error;     // 0 = ok, otherwise an ssd_status value latched by a kernel
   int32_t pad0;
   int64_t detail;    // kernel-specific detail word of the first latched error
-  uint32_t reserved[60];
+  uint32_t counters[2];  // tickets taken and blocks done of a running kernel; zero between kernels
+  uint32_t reserved[58];
 };
 static_assert(sizeof(WsHeader) == 256, "workspace header must be 256 bytes");
 

@@ -33,7 +33,7 @@ struct RecParams {
   int64_t ntile;     // tiles in time
   uint32_t cols;     // tiles side by side in the channels of one sequence
   uint32_t tiles;    // tiles in all
-  uint32_t* ticket;  // NULL where the order of the tiles does not matter
+  uint32_t* ticket;  // tickets taken, blocks done; NULL where the order of the tiles does not matter
   uint64_t* words;
   WsHeader* hdr;
 };
@@ -192,6 +192,27 @@ __device__ __forceinline__ Place place(const RecParams& p, uint32_t tile) {
   return q;
 }
 
+// The look-back words are cleared by a kernel of their own, whose end only the first look-back of a block
+// waits for: the first tiles are loaded and worked on meanwhile.
+__global__ void __launch_bounds__(256) rec_clear_kernel(uint4* words, int64_t n) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < n; k += (int64_t)gridDim.x * 256)
+    words[k] = make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ void wait_for_words() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// At a kernel's end: the last block to get here leaves the tickets at zero for the next call.
+__device__ __forceinline__ void finish_tickets(const RecParams& p) {
+  __syncthreads();
+  if (p.ticket && threadIdx.x == 0) {
+    __threadfence();
+    if (atomicAdd(p.ticket + 1, 1u) == gridDim.x - 1) {
+      p.ticket[0] = 0;
+      p.ticket[1] = 0;
+    }
+  }
+}
+
 // A lane's values over its warp's SPW steps, in pairs: for bf16 the two channels of a step, for f32 two
 // steps of one channel.
 template <typename T, int SPW>
@@ -339,6 +360,7 @@ __global__ void __launch_bounds__(32 * Forward<T>::kNw, Forward<T>::kBlocks) rec
           W[c] = lookback::apply(m.x, m.x, W[c]);
         }
       }
+      if (it == 0) wait_for_words();
       uint64_t* words = p.words + q.word + cl;
       const bool last = q.ti == p.ntile - 1;
       uint64_t v[kCpl];
@@ -413,6 +435,7 @@ __global__ void __launch_bounds__(32 * Forward<T>::kNw, Forward<T>::kBlocks) rec
     else if (live > 0) walk(std::false_type());
   }
   cp_async_wait_all();
+  finish_tickets(p);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -432,7 +455,6 @@ static_assert(kWarps * kSpwBwd == kChunk, "a backward tile starts from one kept 
 
 template <typename T, int ALIGN, int MINB>
 __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(RecParams p) {
-  follow();
   constexpr int SPW = kSpwBwd, kSteps = kWarps * SPW, kCh = Tile<T>::kCh, kCpl = Tile<T>::kCpl;
   constexpr int kPairs = Walk<T, SPW>::kPairs, kWarpBytes = SPW * kRowBytes, kArray = kWarps * kWarpBytes;
   constexpr int kStage = 4 * kArray;
@@ -583,6 +605,7 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(RecParams 
           W[c] = lookback::apply(m.x, m.x, W[c]);
         }
       }
+      if (it == 0) wait_for_words();
       uint64_t* words = p.words + q.word + cl;
       uint64_t v[kCpl];
       if (q.ti == p.ntile - 1) {
@@ -694,6 +717,7 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(RecParams 
   cp_async_wait_all();
   __syncthreads();
   if (warp == 2 && partial_left > 0) write_partial(partial_at, partial_left);
+  finish_tickets(p);
 }
 
 // ddecay[d] = -c sigmoid(decay) * sum of the partial rows: a block takes 32 channels, its warps every
@@ -818,7 +842,7 @@ RecParams rec_params(const gated_recurrence_shape* s) {
 }
 
 struct RecLayout {
-  size_t scan = 0, states = 0, partial = 0, total = 0;   // scan: ticket, then look-back words
+  size_t scan = 0, states = 0, partial = 0, total = 0;   // scan: look-back words
 };
 RecLayout rec_layout(const gated_recurrence_shape* s, bool backward) {
   RecLayout L;
@@ -826,7 +850,7 @@ RecLayout rec_layout(const gated_recurrence_shape* s, bool backward) {
   L.scan = off;
   const int64_t ntile = (s->seqlen + kMinTileSteps - 1) / kMinTileSteps;
   if (ntile > 1)
-    off = align_up(off + kWsAlign + sizeof(uint64_t) * (size_t)(s->batch * ntile * align_up(s->d_model, 64)),
+    off = align_up(off + sizeof(uint64_t) * (size_t)(s->batch * ntile * align_up(s->d_model, 64)),
                    kWsAlign);
   if (backward) {
     L.states = off;
@@ -858,6 +882,23 @@ int row_align(size_t e, std::initializer_list<std::pair<const void*, const int64
   return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
 }
 
+// A tile kernel: behind the clearing of its look-back words, or by itself where it has one tile in time.
+template <typename T>
+cudaError_t launch_tiles(void (*kernel)(RecParams), RecParams p, int blocks, unsigned threads, size_t smem,
+                         cudaStream_t st) {
+  const unsigned grid = (unsigned)std::min<int64_t>(blocks, p.tiles);
+  if (p.ntile == 1) {
+    p.ticket = nullptr;
+    kernel<<<grid, threads, smem, st>>>(p);
+    return cudaGetLastError();
+  }
+  const int64_t n = (int64_t)p.tiles * Tile<T>::kCh * (int64_t)sizeof(uint64_t) / 16;
+  rec_clear_kernel<<<(unsigned)std::min<int64_t>((n + 255) / 256, 152 * 4), 256, 0, st>>>(
+      reinterpret_cast<uint4*>(p.words), n);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? launch_next(kernel, grid, threads, smem, st, p) : e;
+}
+
 template <typename T, int ALIGN>
 cudaError_t launch_forward_as(RecParams p, cudaStream_t st) {
   using F = Forward<T>;
@@ -870,14 +911,7 @@ cudaError_t launch_forward_as(RecParams p, cudaStream_t st) {
   int blocks = 0;
   cudaError_t e = resident_blocks(kernel, 32 * F::kNw, kSmem, &blocks);
   if (e != cudaSuccess) return e;
-  if (p.ntile > 1) {   // tickets and look-back words start at zero
-    const size_t n = kWsAlign + sizeof(uint64_t) * (size_t)p.tiles * Tile<T>::kCh;
-    if ((e = cudaMemsetAsync(p.ticket, 0, n, st)) != cudaSuccess) return e;
-  } else {
-    p.ticket = nullptr;
-  }
-  kernel<<<(unsigned)std::min<int64_t>(blocks, p.tiles), 32 * F::kNw, kSmem, st>>>(p);
-  return cudaGetLastError();
+  return launch_tiles<T>(kernel, p, blocks, 32 * F::kNw, kSmem, st);
 }
 
 cudaError_t launch_forward(const RecParams& p, bool bf16, cudaStream_t st) {
@@ -896,14 +930,7 @@ cudaError_t launch_backward_as(RecParams p, cudaStream_t st) {
   int blocks = 0;
   cudaError_t e = resident_blocks(kernel, kThreads, kSmem, &blocks);
   if (e != cudaSuccess) return e;
-  if (p.ntile > 1) {
-    const size_t n = kWsAlign + sizeof(uint64_t) * (size_t)p.tiles * Tile<T>::kCh;
-    if ((e = cudaMemsetAsync(p.ticket, 0, n, st)) != cudaSuccess) return e;
-  } else {
-    p.ticket = nullptr;
-  }
-  kernel<<<(unsigned)std::min<int64_t>(blocks, p.tiles), kThreads, kSmem, st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = launch_tiles<T>(kernel, p, blocks, kThreads, kSmem, st)) != cudaSuccess) return e;
   return launch_next(rec_ddecay_kernel, (unsigned)((p.D + 31) / 32), 1024, 0, st, p);
 }
 
@@ -996,8 +1023,8 @@ ssd_status gated_recurrence_forward(const gated_recurrence_shape* shape, const v
   p.states_out = states;
   char* ws = static_cast<char*>(workspace);
   p.hdr = reinterpret_cast<WsHeader*>(ws);
-  p.ticket = reinterpret_cast<uint32_t*>(ws + rec_layout(shape, false).scan);
-  p.words = reinterpret_cast<uint64_t*>(reinterpret_cast<char*>(p.ticket) + kWsAlign);
+  p.ticket = p.hdr->counters;
+  p.words = reinterpret_cast<uint64_t*>(ws + rec_layout(shape, false).scan);
   return done(launch_forward(p, shape->io_dtype == SSD_BF16, st));
 }
 
@@ -1037,8 +1064,8 @@ ssd_status gated_recurrence_backward(const gated_recurrence_shape* shape, const 
   p.decay = decay;
   p.init = init_state;
   p.hdr = reinterpret_cast<WsHeader*>(ws);
-  p.ticket = reinterpret_cast<uint32_t*>(ws + L.scan);
-  p.words = reinterpret_cast<uint64_t*>(ws + L.scan + kWsAlign);
+  p.ticket = p.hdr->counters;
+  p.words = reinterpret_cast<uint64_t*>(ws + L.scan);
   if (!states) {
     RecParams f = p;
     f.states_out = reinterpret_cast<float*>(ws + L.states);
