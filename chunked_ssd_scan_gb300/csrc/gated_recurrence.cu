@@ -16,6 +16,8 @@
 #include "fp_helpers.cuh"
 #include "launch.h"
 #include "lookback.cuh"
+#include "tc_ptx.cuh"
+#include "tensor_map.h"
 
 namespace ssd {
 namespace {
@@ -23,6 +25,7 @@ namespace {
 constexpr int kChunk = GATED_RECURRENCE_CHUNK;
 
 struct RecParams {
+  CUtensorMap map[4];   // x, gate_a, gate_x, dy in tiles (TMA kernels)
   const void *x, *ga, *gx, *dy;
   const float *decay, *init, *states_in, *dfinal;
   void *y, *dx, *dga, *dgx;
@@ -256,8 +259,35 @@ struct Forward {
   static constexpr int kNw = sizeof(T) == 2 ? 4 : 8, kSpw = 16, kSteps = kNw * kSpw, kBlocks = 16 / kNw;
 };
 
+// How a tile's rows get to shared memory: as one TMA box an array, or by every warp for its own rows in
+// copies of 16 bytes (arrays that TMA does not take: broadcast axes), 4 or 2.  A box costs its
+// block a few instructions, the copies a tenth of all (8 x 4096 x 2048 bf16: forward 98 us, 106 us by copies;
+// backward 226 and 238 us).
+constexpr int kTma = 32;
+
+__device__ __forceinline__ void tma_tile(void* dst, const CUtensorMap* map, uint64_t* bar, const Place& q) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+          tc::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(tc::smem_u32(bar)), "r"(q.c0), "r"((int32_t)q.t0), "r"((int32_t)q.b)
+      : "memory");
+}
+// By one thread: N arrays' boxes of `bytes` each into a stage.
+template <int N>
+__device__ __forceinline__ void tma_load(unsigned char* stage, const RecParams& p, uint64_t* bar, const Place& q,
+                                         int bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(tc::smem_u32(bar)), "r"(N * bytes)
+               : "memory");
+#pragma unroll
+  for (int a = 0; a < N; ++a) tma_tile(stage + a * bytes, p.map + a, bar, q);
+}
+// A stage's boxes are there (bounded: 1 s, then SSD_ERR_TIMEOUT is latched).
+__device__ __forceinline__ void tma_wait(uint64_t* bar, uint32_t phase, WsHeader* hdr) {
+  if (!tc::mbar_wait_bounded(bar, phase, 1000000000ull) && threadIdx.x == 0) latch_error(hdr, SSD_ERR_TIMEOUT, 402);
+}
+
 template <typename T, int ALIGN>
-__global__ void __launch_bounds__(32 * Forward<T>::kNw, Forward<T>::kBlocks) rec_forward_kernel(RecParams p) {
+__global__ void __launch_bounds__(32 * Forward<T>::kNw, Forward<T>::kBlocks) rec_forward_kernel(const __grid_constant__ RecParams p) {
   constexpr int NW = Forward<T>::kNw, SPW = Forward<T>::kSpw, kSteps = Forward<T>::kSteps, kCh = Tile<T>::kCh, kCpl = Tile<T>::kCpl;
   constexpr int kPairs = Walk<T, SPW>::kPairs, kWarpBytes = SPW * kRowBytes, kArray = NW * kWarpBytes;
   constexpr int kStage = 3 * kArray;
@@ -266,10 +296,15 @@ __global__ void __launch_bounds__(32 * Forward<T>::kNw, Forward<T>::kBlocks) rec
   __shared__ float before[NW][kCh];     // the state before every warp's steps
   __shared__ float rates[2][kCh];           // -c softplus(decay) of the tile's channels
   __shared__ Place places[2];               // of the tile in hand and the one being loaded
+  __shared__ uint64_t full[2];              // TMA: a stage's boxes have landed
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int cl = lane * kCpl;
 
   auto load = [&](const Place& q, int stage) {
+    if constexpr (ALIGN == kTma) {
+      if (threadIdx.x == 0 && q.tile < p.tiles) tma_load<3>(smem + stage * kStage, p, full + stage, q, kArray);
+      return;
+    }
     if (q.tile < p.tiles) {
       const int64_t t = q.t0 + warp * SPW;
       const int rows = (int)min((int64_t)SPW, max((int64_t)0, p.T - t)), bytes = q.left * (int)sizeof(T);
@@ -301,6 +336,11 @@ __global__ void __launch_bounds__(32 * Forward<T>::kNw, Forward<T>::kBlocks) rec
     }
   };
 
+  if (ALIGN == kTma && threadIdx.x == 0) {
+    tc::mbar_init(full, 1);
+    tc::mbar_init(full + 1, 1);
+    tc::fence_mbar_init();
+  }
   if (warp == 0) {
     fetch(blockIdx.x - gridDim.x, 0);
     __syncwarp();
@@ -313,8 +353,12 @@ __global__ void __launch_bounds__(32 * Forward<T>::kNw, Forward<T>::kBlocks) rec
     const Place q = places[slot];
     if (q.tile >= p.tiles) break;
     load(places[slot ^ 1], slot ^ 1);
-    cp_async_wait<1>();
-    __syncwarp();
+    if constexpr (ALIGN == kTma) {
+      tma_wait(full + slot, (it >> 1) & 1, p.hdr);
+    } else {
+      cp_async_wait<1>();
+      __syncwarp();
+    }
     const float2 rate = make_float2(rates[slot][cl], rates[slot][cl + kCpl - 1]);
     const bool far = __any_sync(0xffffffffu, fminf(rate.x, rate.y) < -kNear);
     const int64_t steps = p.T - q.t0 - warp * SPW;   // of this warp's that lie inside
@@ -454,7 +498,7 @@ constexpr int kSpwBwd = 8;
 static_assert(kWarps * kSpwBwd == kChunk, "a backward tile starts from one kept state");
 
 template <typename T, int ALIGN, int MINB>
-__global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(RecParams p) {
+__global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(const __grid_constant__ RecParams p) {
   constexpr int SPW = kSpwBwd, kSteps = kWarps * SPW, kCh = Tile<T>::kCh, kCpl = Tile<T>::kCpl;
   constexpr int kPairs = Walk<T, SPW>::kPairs, kWarpBytes = SPW * kRowBytes, kArray = kWarps * kWarpBytes;
   constexpr int kStage = 4 * kArray;
@@ -465,10 +509,15 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(RecParams 
   __shared__ float sums[kWarps][kCh];       // G kr over every warp's steps
   __shared__ float rates[2][kCh], start[2][kCh];   // -c softplus(decay), the kept state
   __shared__ Place places[2];
+  __shared__ uint64_t full[2];   // TMA: a stage's boxes have landed
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int cl = lane * kCpl;
 
   auto load = [&](const Place& q, int stage) {
+    if constexpr (ALIGN == kTma) {
+      if (threadIdx.x == 0 && q.tile < p.tiles) tma_load<4>(smem + stage * kStage, p, full + stage, q, kArray);
+      return;
+    }
     if (q.tile < p.tiles) {
       const int64_t t = q.t0 + warp * SPW;
       const int rows = (int)min((int64_t)SPW, max((int64_t)0, p.T - t)), bytes = q.left * (int)sizeof(T);
@@ -513,6 +562,11 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(RecParams 
     }
   };
 
+  if (ALIGN == kTma && threadIdx.x == 0) {
+    tc::mbar_init(full, 1);
+    tc::mbar_init(full + 1, 1);
+    tc::fence_mbar_init();
+  }
   if (warp == 0) {
     fetch(blockIdx.x - gridDim.x, 0);
     __syncwarp();
@@ -526,9 +580,13 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(RecParams 
     const int slot = it & 1;
     const Place q = places[slot];
     if (q.tile >= p.tiles) break;
-    load(places[slot ^ 1], slot ^ 1);
-    cp_async_wait<1>();
-    __syncwarp();
+    if constexpr (ALIGN != kTma) load(places[slot ^ 1], slot ^ 1);
+    if constexpr (ALIGN == kTma) {
+      tma_wait(full + slot, (it >> 1) & 1, p.hdr);
+    } else {
+      cp_async_wait<1>();
+      __syncwarp();
+    }
     const float2 rate = make_float2(rates[slot][cl], rates[slot][cl + kCpl - 1]);
     const bool far = __any_sync(0xffffffffu, fminf(rate.x, rate.y) < -kNear);
     const float2 h0 = make_float2(start[slot][cl], start[slot][cl + kCpl - 1]);
@@ -593,6 +651,9 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(RecParams 
       }
     }
     __syncthreads();   // A: the warps' maps are there, and the sums of the tile before
+    // A box replaces a tile that every warp has left only now (its rows are read to the tile's end; a third
+    // stage, asked for a tile earlier, took the L1 cache's room: 285 us instead of 226).
+    if constexpr (ALIGN == kTma) load(places[slot ^ 1], slot ^ 1);
     if (warp == 0) {
       float W[kCpl], Q[kCpl], C[kCpl];
 #pragma unroll
@@ -814,7 +875,7 @@ ssd_status check_shape(const gated_recurrence_shape* s, bool backward) {
     if (s->x_stride[k] < 0 || s->gate_a_stride[k] < 0 || s->gate_x_stride[k] < 0 ||
         (backward && s->dy_stride[k] < 0))
       return SSD_ERR_INVALID_ARG;
-  if (s->d_model > 0x7fffff00LL || s->batch > kMaxElems / s->d_model ||
+  if (s->d_model > 0x7fffff00LL || s->batch > 0x7fffffffLL || s->seqlen > 0x7fffffffLL || s->batch > kMaxElems / s->d_model ||
       (s->batch > 0 && s->seqlen > kMaxElems / s->d_model / s->batch))
     return SSD_ERR_UNSUPPORTED;
   // blocks of the per-channel kernels, and tiles (tickets are 32 bits)
@@ -914,8 +975,21 @@ cudaError_t launch_forward_as(RecParams p, cudaStream_t st) {
   return launch_tiles<T>(kernel, p, blocks, 32 * F::kNw, kSmem, st);
 }
 
-cudaError_t launch_forward(const RecParams& p, bool bf16, cudaStream_t st) {
+// Tensor maps of the first n of x, gate_a, gate_x and dy in tiles of `steps`.
+bool make_maps(RecParams& p, bool bf16, int steps, int n) {
+  const void* base[4] = {p.x, p.ga, p.gx, p.dy};
+  const int64_t* stride[4] = {p.xs, p.as, p.gs, p.ds};
+  const int ch = bf16 ? Tile<__nv_bfloat16>::kCh : Tile<float>::kCh;
+  for (int a = 0; a < n; ++a)
+    if (!make_tensor_map(&p.map[a], bf16, base[a], p.batch, p.T, p.D, stride[a][0], stride[a][1], steps, ch))
+      return false;
+  return true;
+}
+
+cudaError_t launch_forward(RecParams p, bool bf16, cudaStream_t st) {
   const int align = row_align(bf16 ? 2 : 4, {{p.x, p.xs}, {p.ga, p.as}, {p.gx, p.gs}}, {p.y}, p.D);
+  if (align == 16 && make_maps(p, bf16, bf16 ? Forward<__nv_bfloat16>::kSteps : Forward<float>::kSteps, 3))
+    return bf16 ? launch_forward_as<__nv_bfloat16, kTma>(p, st) : launch_forward_as<float, kTma>(p, st);
   if (bf16)
     return align == 16 ? launch_forward_as<__nv_bfloat16, 16>(p, st)
          : align == 4 ? launch_forward_as<__nv_bfloat16, 4>(p, st)
@@ -941,6 +1015,8 @@ cudaError_t launch_backward(RecParams p, bool bf16, cudaStream_t st) {
   p.tiles = (uint32_t)(p.batch * p.cols * p.ntile);
   const int align = row_align(bf16 ? 2 : 4, {{p.x, p.xs}, {p.ga, p.as}, {p.gx, p.gs}, {p.dy, p.ds}},
                               {p.dx, p.dga, p.dgx}, p.D);
+  if (align == 16 && make_maps(p, bf16, kChunk, 4))
+    return bf16 ? launch_backward_as<__nv_bfloat16, kTma>(p, st) : launch_backward_as<float, kTma>(p, st);
   if (bf16)
     return align == 16 ? launch_backward_as<__nv_bfloat16, 16>(p, st)
          : align == 4 ? launch_backward_as<__nv_bfloat16, 4>(p, st)
