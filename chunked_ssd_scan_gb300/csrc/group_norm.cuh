@@ -119,7 +119,7 @@ static __global__ void __launch_bounds__(1024) norm_param_grad_kernel(NormParams
 
 // Joins the partial rows of the parameters' gradients: at once, or where there are many through
 // kFoldRows of them behind the others.
-inline cudaError_t launch_param_grad(NormParams p, cudaStream_t st) {
+static cudaError_t launch_param_grad(NormParams p, cudaStream_t st) {
   if (p.part_rows == 0) return cudaSuccess;
   const unsigned grid = (unsigned)((p.C + 31) / 32);
   if (p.part_rows > kFewRows) {

@@ -10,6 +10,7 @@
 #include <utility>
 
 namespace ssd {
+namespace {   // of its own in every library: a process may hold the normal and the checked one
 
 // Blocks of `kernel` that the device holds at once (looked up once per kernel and device).
 template <typename K>
@@ -65,4 +66,5 @@ __device__ __forceinline__ void follow() {
 }
 #endif
 
+}  // namespace
 }  // namespace ssd

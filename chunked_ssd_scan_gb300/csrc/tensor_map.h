@@ -9,8 +9,9 @@
 #include <mutex>
 
 namespace ssd {
+namespace {
 
-inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -27,7 +28,7 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 // Map of base[batch][rows][cols] with the given strides (elements; the columns are contiguous) in boxes of
 // box_rows x box_cols, zeros outside.  The caller has checked that base and strides are multiples of 16
 // bytes.  False where the driver does not take it (an axis that is broadcast, for one).
-inline bool make_tensor_map(CUtensorMap* m, bool bf16, const void* base, int64_t batch, int64_t rows, int64_t cols,
+bool make_tensor_map(CUtensorMap* m, bool bf16, const void* base, int64_t batch, int64_t rows, int64_t cols,
                             int64_t batch_stride, int64_t row_stride, int box_rows, int box_cols) {
   const auto encode = tensor_map_encoder();
   const int64_t e = bf16 ? 2 : 4;
@@ -43,4 +44,5 @@ inline bool make_tensor_map(CUtensorMap* m, bool bf16, const void* base, int64_t
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+}  // namespace
 }  // namespace ssd
