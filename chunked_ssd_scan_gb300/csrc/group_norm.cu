@@ -13,6 +13,11 @@ namespace {
 // sample by one column tile of whole groups.  Two passes over x: the chunks' statistics, a join of
 // them by one warp a group, and the output; the second pass goes through the samples backwards, so
 // that what the first read last is still in L2.
+//
+// 6 x 3969 x 320 f32, 32 groups: 24 us for 61 MB (37 % of the measured copy rate: the statistics take 10 us,
+// their join 3, the output 12, of which 5 are writes); 8 x 4096 x 512 bf16 backward: 39 us for 101 MB
+// (38 %).  Vectors divide a group, so that a thread's values belong to one group each; a group of 10
+// f32 channels takes 8-byte loads.
 // ------------------------------------------------------------------------------------------------
 // count, mean and sum of squares around the mean; joined pairwise (Chan, Golub and LeVeque), so no
 // difference of large squares is formed

@@ -5,36 +5,47 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <map>
-#include <mutex>
-#include <utility>
+#include <atomic>
 
 namespace ssd {
 namespace {   // of its own in every library: a process may hold the normal and the checked one
 
-// Blocks of `kernel` that the device holds at once (looked up once per kernel and device).
-template <typename K>
-cudaError_t resident_blocks(K* kernel, int threads, int smem, int* out) {
-  static std::mutex mu;
-  static std::map<std::pair<const void*, int>, int> known;
+// Blocks of `kernel` that the device holds at once (looked up once per kernel and device; throws nothing).
+cudaError_t resident_blocks(const void* kernel, int threads, int smem, int* out) {
+  struct Known {
+    const void* kernel;
+    int dev, blocks;
+  };
+  constexpr int kMost = 256;   // more kernels than a translation unit has; beyond it, looked up every time
+  static Known known[kMost];
+  static int count = 0;
+  static std::atomic_flag busy = ATOMIC_FLAG_INIT;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> lock(mu);
-  const auto key = std::make_pair(reinterpret_cast<const void*>(kernel), dev);
-  const auto it = known.find(key);
-  if (it != known.end()) {
-    *out = it->second;
-    return cudaSuccess;
+  while (busy.test_and_set(std::memory_order_acquire)) {
   }
-  int sms = 0, per = 0;
-  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess && smem > 0)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem);
-  if (e != cudaSuccess) return e;
-  *out = known[key] = sms * std::max(per, 1);
-  return cudaSuccess;
+  int blocks = 0;
+  for (int k = 0; k < count; ++k)
+    if (known[k].kernel == kernel && known[k].dev == dev) blocks = known[k].blocks;
+  if (blocks == 0) {
+    int sms = 0, per = 0;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess && smem > 0)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem);
+    if (e == cudaSuccess) {
+      blocks = sms * std::max(per, 1);
+      if (count < kMost) known[count++] = {kernel, dev, blocks};
+    }
+  }
+  busy.clear(std::memory_order_release);
+  *out = blocks;
+  return e;
+}
+template <typename... P>
+cudaError_t resident_blocks(void (*kernel)(P...), int threads, int smem, int* out) {
+  return resident_blocks(reinterpret_cast<const void*>(kernel), threads, smem, out);
 }
 
 // Launch of a kernel that follows another one of the same call on the stream: its blocks may take their
