@@ -255,9 +255,9 @@ struct Walk {
 };
 
 // NW warps of 16 steps.  Half as many blocks of 8 warps wait for the look-back together, so bf16,
-// bound by issue slots, takes four blocks of 4 warps an SM (8 x 4096 x 2048: 111 us, 118 us with two
+// bound by issue slots, takes four blocks of 4 warps an SM (8 x 4096 x 2048: 98 us, 102 us with two
 // of 8); f32, whose rows are half as many channels, takes the longer tiles and with them half the
-// look-back's chain (1 x 131072 x 1024: 361 us, 380 us with 4 warps).
+// look-back's chain (1 x 131072 x 1024: 339 us, 364 us with 4 warps).
 template <typename T>
 struct Forward {
   static constexpr int kNw = sizeof(T) == 2 ? 4 : 8, kSpw = 16, kSteps = kNw * kSpw, kBlocks = 16 / kNw;
@@ -265,8 +265,8 @@ struct Forward {
 
 // How a tile's rows get to shared memory: as one TMA box an array, or by every warp for its own rows in
 // copies of 16 bytes (arrays that TMA does not take: broadcast axes), 4 or 2.  A box costs its
-// block a few instructions, the copies a tenth of all (8 x 4096 x 2048 bf16: forward 98 us, 106 us by copies;
-// backward 215 and 238 us).
+// block a few instructions, the copies a tenth of all (8 x 4096 x 2048 bf16: forward 98 us, 106 us by
+// copies; backward 215 and 245 us).
 constexpr int kTma = 32;
 
 __device__ __forceinline__ void tma_tile(void* dst, const CUtensorMap* map, uint64_t* bar, const Place& q) {

@@ -505,7 +505,7 @@ NormPlan norm_plan(const group_norm_shape* s, bool backward) {
 
 // Vector width of a call: max_vec, or less where the arrays' rows are not aligned to it.  The gradient of
 // a map takes 8 bytes at most: with 16 its registers leave room for one block an SM less (8 x 4096 x 512
-// bf16: 49 us, 56 us with 16; tokens: 49 us with 16, 64 us with 8).
+// bf16: 39 us, 63 us with 16; tokens: 47 us with 16, 67 us with 8, forward 29 and 42 us).
 int call_vec(const group_norm_shape* s, std::initializer_list<const void*> arrays,
              std::initializer_list<const int64_t*> strides, bool backward) {
   const uint64_t e = s->io_dtype == SSD_BF16 ? 2 : 4;

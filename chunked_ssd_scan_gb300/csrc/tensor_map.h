@@ -23,7 +23,7 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 
 // Map of base[batch][rows][cols] with the given strides (elements; the columns are contiguous) in boxes of
 // box_rows x box_cols, zeros outside.  The caller has checked that base and strides are multiples of 16
-// bytes.  False where the driver does not take it (an axis that is broadcast, for one).
+// bytes.  False where CUDA does not take it (an axis that is broadcast, for one).
 bool make_tensor_map(CUtensorMap* m, bool bf16, const void* base, int64_t batch, int64_t rows, int64_t cols,
                             int64_t batch_stride, int64_t row_stride, int box_rows, int box_cols) {
   const auto encode = tensor_map_encoder();
