@@ -77,9 +77,10 @@ __global__ void __launch_bounds__(kThreads) embed_forward_kernel(const Id* ids, 
 // 2. A subgroup of threads takes kPiece sorted tokens and adds their rows, writing each row's sum as its
 //    run ends; a run that goes on over the ends of a piece leaves partial sums instead,
 // 3. which the piece where the run starts joins, in order.
-// Bound by memory: dout once, every row of dtable once.  32768 tokens, 50000 x 2048 bf16: 117 us, 4.6 TB/s
-// of 544 MB (68 % of the measured copy rate): sorting takes 7 + 2 x 12 us beside 94 MB of clearing, the
-// sums 60 us for 401 MB, the join 19 us beside 47 MB.
+// Bound by memory: dout once, every row of dtable once.  32768 tokens, 50000 x 2048 bf16: 120 us, 4.5 TB/s
+// of 544 MB (67 % of the measured copy rate): sorting takes 7 + 2 x 12 us beside 94 MB of clearing, the
+// sums 60 us for 401 MB, the join 19 us beside 47 MB.  With few tokens and rows it is a chain of
+// five short launches: 14824 tokens, 10335 x 324 f32 take 40 us.
 // ------------------------------------------------------------------------------------------------
 constexpr int kBins = 256;
 constexpr int kKeys = 8;                        // keys of a thread
@@ -104,21 +105,30 @@ struct EmbedParams {
   WsHeader* hdr;
 };
 
-// Rows [fill0, fill1) without tokens are zeros, by the blocks behind the working ones, a row a block at
-// a time.
+// Rows [fill0, fill1) without tokens are zeros, by the warps of the blocks behind the working ones, four
+// neighbouring rows a warp at a time with the flags of the next four on their way.
 __device__ __forceinline__ void clear_rows(const EmbedParams& p) {
-  const int64_t step = (int64_t)(gridDim.x - p.work_blocks) * gridDim.y;
+  constexpr int kRows = 4;
+  const int lane = threadIdx.x % 32;
+  const int64_t blocks = (int64_t)(gridDim.x - p.work_blocks) * gridDim.y;
   const int64_t first = (int64_t)(blockIdx.x - p.work_blocks) * gridDim.y + blockIdx.y;
+  const int64_t step = blocks * (kThreads / 32) * kRows;
   const bool wide = p.D % 4 == 0 && (reinterpret_cast<uintptr_t>(p.dtable) & 15) == 0;
-  for (int64_t r = p.fill0 + first; r < p.fill1; r += step) {
-    if (p.used[r]) continue;
-    float* row = p.dtable + r * p.D;
-    if (!SSD_INDEX_OK(p.hdr, (r + 1) * p.D - 1, p.rows * p.D, 80)) continue;
-    if (wide) {
-      for (int64_t d = threadIdx.x; d < p.D / 4; d += kThreads)
-        reinterpret_cast<float4*>(row)[d] = make_float4(0.f, 0.f, 0.f, 0.f);
-    } else {
-      for (int64_t d = threadIdx.x; d < p.D; d += kThreads) row[d] = 0.f;
+  auto flag = [&](int64_t r) { return lane < kRows && r + lane < p.fill1 ? (int)p.used[r + lane] : 1; };
+  int64_t r = p.fill0 + (first * (kThreads / 32) + threadIdx.x / 32) * kRows;
+  int next = flag(r);
+  for (; r < p.fill1; r += step) {
+    unsigned empty = __ballot_sync(0xffffffffu, next == 0);
+    next = flag(r + step);
+    for (; empty != 0; empty &= empty - 1) {
+      const int64_t row = r + __ffs(empty) - 1;
+      if (!SSD_INDEX_OK(p.hdr, (row + 1) * p.D - 1, p.rows * p.D, 80)) continue;
+      float* to = p.dtable + row * p.D;
+      if (wide) {
+        for (int64_t d = lane; d < p.D / 4; d += 32) reinterpret_cast<float4*>(to)[d] = make_float4(0.f, 0.f, 0.f, 0.f);
+      } else {
+        for (int64_t d = lane; d < p.D; d += 32) to[d] = 0.f;
+      }
     }
   }
 }
@@ -527,10 +537,10 @@ int embed_passes(int64_t rows) {
 EmbedLayout embed_layout(int64_t n, int64_t rows, int64_t D) {
   EmbedLayout L;
   L.sort_tiles = (n + kSortTile - 1) / kSortTile;
-  // short pieces while they do not fill the machine (four blocks an SM), then longer ones: they keep the
-  // partial sums of frequent rows few
+  // short pieces while their threads (one a vector of 16 bytes of bf16) do not fill the machine, four
+  // blocks an SM, then longer ones: they keep the partial sums of frequent rows few
   L.piece = 32;
-  while (L.piece < 256 && n / L.piece > 4 * 152) L.piece *= 2;
+  while (L.piece < 256 && n / L.piece * ((D + 7) / 8) > 152 * 4 * kThreads) L.piece *= 2;
   L.pieces = (n + L.piece - 1) / L.piece;
   size_t off = sizeof(WsHeader);
   auto take = [&](size_t bytes) {
@@ -559,7 +569,8 @@ struct Fill {
     p.fill0 = p.rows * done / all;
     done += share;
     p.fill1 = p.rows * done / all;
-    return (unsigned)(work + std::max<int64_t>(1, std::min<int64_t>(152 * 8, p.fill1 - p.fill0)));
+    const int64_t blocks = (p.fill1 - p.fill0 + 31) / 32;   // 8 warps of 4 rows each
+    return (unsigned)(work + std::max<int64_t>(1, std::min<int64_t>(152 * 8, blocks)));
   }
 };
 

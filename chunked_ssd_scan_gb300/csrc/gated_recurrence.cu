@@ -108,15 +108,20 @@ __device__ __forceinline__ float2 one_minus_a2(float2 w) {
   return fp::fma2(w, fp::fma2(w, dup(-1.f), dup(-2.f)), dup(kTiny));
 }
 
+// Copy of 8 bytes, of which the first n are read and the others zeros.
+__device__ __forceinline__ void cp_async8(void* dst, const void* src, int n) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(n) : "memory");
+}
+
 // Rows of one array for the calling warp: ROWS rows from `src` (the warp's first row, the tile's first
 // channel) on, kRowBytes each; `rows` and `bytes` are how many rows and bytes of a row lie inside the
-// array, the rest becomes zeros.  ALIGN is what every row start is known to be aligned to: 16 (one
-// copy per 16 bytes), 4, or 2 (odd bf16 rows, through registers).
+// array, the rest becomes zeros.  ALIGN is what every row start is known to be aligned to: 16, 8 or
+// 4 (one copy per so many bytes), or 2 (odd bf16 rows, through registers).
 template <int ROWS, int ALIGN>
 __device__ __forceinline__ void load_rows(unsigned char* dst, const unsigned char* src, int64_t pitch, int rows,
                                           int bytes, int lane) {
   constexpr int kPer = ALIGN == 2 ? 4 : ALIGN;   // bytes a lane moves at a time
-  constexpr int kLanes = kRowBytes / kPer;       // lanes a row takes: 8 or 32
+  constexpr int kLanes = kRowBytes / kPer;       // lanes a row takes: 8, 16 or 32
   constexpr int kAtOnce = 32 / kLanes;
   static_assert(ROWS % kAtOnce == 0, "whole groups of rows");
   const int r = lane / kLanes, at = lane % kLanes * kPer;
@@ -134,6 +139,8 @@ __device__ __forceinline__ void load_rows(unsigned char* dst, const unsigned cha
     unsigned char* dk = d + k * kAtOnce * kRowBytes;
     if constexpr (ALIGN == 16) {
       cp_async16(dk, sk, n);
+    } else if constexpr (ALIGN == 8) {
+      cp_async8(dk, sk, n);
     } else if constexpr (ALIGN == 4) {
       if (n == 4) cp_async4(dk, sk);
       else *reinterpret_cast<uint32_t*>(dk) = 0u;   // the width is a multiple of 4 bytes
@@ -264,9 +271,10 @@ struct Forward {
 };
 
 // How a tile's rows get to shared memory: as one TMA box an array, or by every warp for its own rows in
-// copies of 16 bytes (arrays that TMA does not take: broadcast axes), 4 or 2.  A box costs its
+// copies of 16 bytes (arrays that TMA does not take: broadcast axes), 8, 4 or 2.  A box costs its
 // block a few instructions, the copies a tenth of all (8 x 4096 x 2048 bf16: forward 98 us, 106 us by
-// copies; backward 215 and 245 us).
+// copies of 16; backward 215 and 245 us); 29 x 12456 x 332 bf16, whose rows start on 8 bytes, takes
+// 360 us by copies of 8 and 410 by copies of 4.
 constexpr int kTma = 32;
 
 __device__ __forceinline__ void tma_tile(void* dst, const CUtensorMap* map, uint64_t* bar, const Place& q) {
@@ -938,7 +946,7 @@ cudaError_t set_rows(float* dst, const float* src, int64_t n, cudaStream_t st) {
              : cudaMemsetAsync(dst, 0, sizeof(float) * (size_t)n, st);
 }
 
-// Alignment that every row of the arrays is known to have: 16, 4 or (bf16) 2 bytes.
+// Alignment that every row of the arrays is known to have: 16, 8, 4 or (bf16) 2 bytes.
 int row_align(size_t e, std::initializer_list<std::pair<const void*, const int64_t*>> in,
               std::initializer_list<const void*> out, int64_t D) {
   uint64_t bits = 0;
@@ -948,7 +956,7 @@ int row_align(size_t e, std::initializer_list<std::pair<const void*, const int64
   uint64_t obits = (uint64_t)D * e;
   for (const void* o : out) obits |= reinterpret_cast<uintptr_t>(o);
   if (obits % 4 != 0) return 2;
-  return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
+  return bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : 2;
 }
 
 // A tile kernel: behind the clearing of its look-back words, or by itself where it has one tile in time.
@@ -1000,9 +1008,12 @@ cudaError_t launch_forward(RecParams p, bool bf16, cudaStream_t st) {
     return bf16 ? launch_forward_as<__nv_bfloat16, kTma>(p, st) : launch_forward_as<float, kTma>(p, st);
   if (bf16)
     return align == 16 ? launch_forward_as<__nv_bfloat16, 16>(p, st)
+         : align == 8 ? launch_forward_as<__nv_bfloat16, 8>(p, st)
          : align == 4 ? launch_forward_as<__nv_bfloat16, 4>(p, st)
                       : launch_forward_as<__nv_bfloat16, 2>(p, st);
-  return align == 16 ? launch_forward_as<float, 16>(p, st) : launch_forward_as<float, 4>(p, st);
+  return align == 16 ? launch_forward_as<float, 16>(p, st)
+       : align == 8 ? launch_forward_as<float, 8>(p, st)
+                    : launch_forward_as<float, 4>(p, st);
 }
 
 template <typename T, int ALIGN>
@@ -1027,9 +1038,12 @@ cudaError_t launch_backward(RecParams p, bool bf16, cudaStream_t st) {
     return bf16 ? launch_backward_as<__nv_bfloat16, kTma>(p, st) : launch_backward_as<float, kTma>(p, st);
   if (bf16)
     return align == 16 ? launch_backward_as<__nv_bfloat16, 16>(p, st)
+         : align == 8 ? launch_backward_as<__nv_bfloat16, 8>(p, st)
          : align == 4 ? launch_backward_as<__nv_bfloat16, 4>(p, st)
                       : launch_backward_as<__nv_bfloat16, 2>(p, st);
-  return align == 16 ? launch_backward_as<float, 16>(p, st) : launch_backward_as<float, 4>(p, st);
+  return align == 16 ? launch_backward_as<float, 16>(p, st)
+       : align == 8 ? launch_backward_as<float, 8>(p, st)
+                    : launch_backward_as<float, 4>(p, st);
 }
 
 template <typename T, int V, int U>
