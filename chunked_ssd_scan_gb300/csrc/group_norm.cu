@@ -507,11 +507,12 @@ NormPlan norm_plan(const group_norm_shape* s, bool backward) {
 // a map takes 8 bytes at most: with 16 its registers leave room for one block an SM less (8 x 4096 x 512
 // bf16: 39 us, 63 us with 16; tokens: 47 us with 16, 67 us with 8, forward 29 and 42 us).
 int call_vec(const group_norm_shape* s, std::initializer_list<const void*> arrays,
-             std::initializer_list<const int64_t*> strides, bool backward) {
+             std::initializer_list<const int64_t*> strides, bool backward, bool* aligned) {
   const uint64_t e = s->io_dtype == SSD_BF16 ? 2 : 4;
   uint64_t bits = backward && s->rows > 1 ? 8 : 0;
   for (const void* a : arrays) bits |= reinterpret_cast<uintptr_t>(a);
   for (const int64_t* st : strides) bits |= (uint64_t)(st[0] | st[1]) * e;
+  *aligned = ((bits & ~(uint64_t)(backward && s->rows > 1 ? 8 : 0)) | (uint64_t)s->channels * e) % 16 == 0;
   int v = max_vec(s);
   while (v > 1 && bits % (v * e) != 0) v /= 2;
   return v;
@@ -551,7 +552,18 @@ cudaError_t launch_act(const NormParams& p, bool backward, cudaStream_t st) {
                                : launch_as<T, V, false>(p, backward, st);
 }
 
-cudaError_t launch(NormParams p, const group_norm_shape* s, int vec, bool backward, char* ws, cudaStream_t st) {
+// Tokens whose groups only narrow vectors divide, but whose rows take wide ones.  Not for few of them: the
+// joins' barriers cost 64 x 520 bf16 2.4 us more (6.5 against 4.1), and save 23795 x 520 18 us (37
+// against 55).
+constexpr int64_t kStraddleValues = 1 << 17;
+bool straddles(const group_norm_shape* s, int vec, bool aligned) {
+  const int64_t cg = s->channels / s->groups, e = s->io_dtype == SSD_BF16 ? 2 : 4;
+  return s->rows == 1 && aligned && vec * e <= 4 && cg * e >= kStraddleLeast && cg <= kThreads &&
+         s->groups <= 65535 && s->batch * s->channels >= kStraddleValues;
+}
+
+cudaError_t launch(NormParams p, const group_norm_shape* s, int vec, bool aligned, bool backward, char* ws,
+                   cudaStream_t st) {
   const NormPlan L = norm_plan(s, backward);
   p.chunks = L.chunks;
   p.chunk_rows = L.chunk_rows;
@@ -560,6 +572,8 @@ cudaError_t launch(NormParams p, const group_norm_shape* s, int vec, bool backwa
   p.part_w = reinterpret_cast<float*>(ws + L.part_w);
   p.part_b = reinterpret_cast<float*>(ws + L.part_b);
   p.hdr = reinterpret_cast<WsHeader*>(ws);
+  if (straddles(s, vec, aligned))
+    return s->io_dtype == SSD_BF16 ? run_straddle<__nv_bfloat16>(p, backward, st) : run_straddle<float>(p, backward, st);
   if (s->io_dtype == SSD_BF16)
     return vec == 8 ? launch_act<__nv_bfloat16, 8>(p, backward, st)
          : vec == 4 ? launch_act<__nv_bfloat16, 4>(p, backward, st)
@@ -608,8 +622,9 @@ ssd_status group_norm_forward(const group_norm_shape* shape, const void* x, cons
   p.y = y;
   p.mean = mean;
   p.rstd = rstd;
-  const int vec = call_vec(shape, {x, y}, {p.xs}, false);
-  return done(launch(p, shape, vec, false, static_cast<char*>(workspace), st));
+  bool aligned = false;
+  const int vec = call_vec(shape, {x, y}, {p.xs}, false, &aligned);
+  return done(launch(p, shape, vec, aligned, false, static_cast<char*>(workspace), st));
 }
 
 ssd_status group_norm_backward(const group_norm_shape* shape, const void* x, const void* dy,
@@ -646,8 +661,9 @@ ssd_status group_norm_backward(const group_norm_shape* shape, const void* x, con
   p.dx = dx;
   p.dw = dweight;
   p.db = dbias;
-  const int vec = call_vec(shape, {x, dy, dx}, {p.xs, p.ds}, true);
-  return done(launch(p, shape, vec, true, static_cast<char*>(workspace), st));
+  bool aligned = false;
+  const int vec = call_vec(shape, {x, dy, dx}, {p.xs, p.ds}, true, &aligned);
+  return done(launch(p, shape, vec, aligned, true, static_cast<char*>(workspace), st));
 }
 
 }  // extern "C"

@@ -135,6 +135,12 @@ static cudaError_t launch_param_grad(NormParams p, cudaStream_t st) {
   return launch_next(norm_param_grad_kernel, dim3(grid, 1), 1024, 0, st, p);
 }
 
+// Runs a call with one position a sample whose rows start on 16 bytes, groups of kStraddleLeast bytes to
+// kThreads channels, none of the vectors that divide them wider than 4 bytes.
+constexpr int kStraddleLeast = 16;
+template <typename T>
+cudaError_t run_straddle(const NormParams& p, bool backward, cudaStream_t st);
+
 // Runs a call with one position a sample; a group is at most kTokenWidth vectors of V values.
 template <typename T, int V>
 cudaError_t run_tokens(const NormParams& p, bool backward, cudaStream_t st);

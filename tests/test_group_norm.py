@@ -267,6 +267,62 @@ def test_empty():
         assert torch.equal(g["dweight"], torch.zeros_like(w)) and torch.equal(g["dbias"], torch.zeros_like(w))
 
 
+# tokens in groups that no wide vector divides, rows that start on 16 bytes: one row and many, a tile that is
+# not full, several tiles, groups of a vector and of a block's width, two values past a vector
+ODD = [(300, 520, 40), (1, 24, 3), (7, 104, 8), (1300, 104, 8), (1000, 1000, 8), (5, 4040, 40), (60, 4040, 40),
+       (9, 2040, 8), (100, 2040, 8), (80, 2080, 32), (2000, 72, 4), (901, 160, 16), (4000, 1560, 40)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("act", ["silu", None])
+@pytest.mark.parametrize("shape", ODD, ids=str)
+def test_tokens_in_groups_of_odd_width(shape, act, dtype):
+    N, C, G = shape
+    d = inputs(N, 1, C, dtype, seed=15, layout="fused", dev="cuda")
+    out = {"y": Guarded(N * C * d["x"].element_size(), "cuda", GUARD_FILL),
+           "dx": Guarded(N * C * d["x"].element_size(), "cuda", GUARD_FILL)}
+    y, mean, rstd = pkg.group_norm_forward(d["x"], G, d["w"], d["bias"], activation=act,
+                                           y=out["y"].view(DT[dtype], (N, 1, C)))
+    plan = pkg.GroupNormBackwardPlan(d["x"], d["dy"], G, mean, rstd, d["w"], d["bias"], activation=act,
+                                     grads={"dx": out["dx"].view(DT[dtype], (N, 1, C))})
+    g = plan()
+    assert pkg.workspace_status(plan.workspace) == ("SSD_OK", 0)
+    for k, v in out.items():
+        v.check(k)
+    x, dy, w, b = (to_np(d[k]) for k in ("x", "dy", "w", "bias"))
+    ry, rm, rr = ref.group_norm(x, G, w, b, act=act)
+    ref.check(to_np(mean), rm, 0.0, "mean", scale=1.0)
+    ref.check(to_np(rstd), rr, 0.0, "rstd")
+    ref.check(to_np(y), ry, REL[dtype], "y")
+    r = ref.group_norm_grad(x, dy, G, w, b, act=act)
+    size = np.abs(to_np(rstd)).mean() * 1.5
+    ref.check(to_np(g["dx"]), r["dx"], REL[dtype], "dx", scale=np.maximum(np.abs(r["dx"]), size))
+    for k in ("dweight", "dbias"):
+        ref.check(to_np(g[k]), r[k], 0.0, k, scale=np.abs(r[k]) + np.sqrt(N))
+    again = pkg.group_norm_backward(d["x"], d["dy"], G, mean, rstd, d["w"], d["bias"], activation=act)
+    assert all(torch.equal(again[k], g[k]) for k in g)
+
+
+@pytest.mark.gpu
+def test_bad_values_stay_in_their_odd_group():
+    """Neighbouring groups share a thread's vector: a NaN of one must not reach the other."""
+    d = inputs(300, 1, 520, seed=16, dev="cuda")
+    x = d["x"].clone()
+    x[2, 0, 13] = float("nan")   # the first value of group 1, in a vector with the last of group 0
+    x[4, 0, 25] = float("inf")   # its last
+    y, mean, rstd = pkg.group_norm_forward(x, 40, d["w"], d["bias"])
+    g = pkg.group_norm_backward(x, d["dy"], 40, mean, rstd, d["w"], d["bias"])
+    clean = pkg.group_norm_forward(d["x"], 40, d["w"], d["bias"])
+    bad = torch.zeros(300, 1, 520, dtype=torch.bool, device="cuda")
+    bad[2, 0, 13:26] = bad[4, 0, 13:26] = True
+    assert torch.equal(y[~bad], clean[0][~bad]) and bool(torch.isnan(y[2, 0, 13:26]).all())
+    assert bool(torch.isfinite(g["dx"][~bad]).all())
+    ch = torch.zeros(520, dtype=torch.bool, device="cuda")
+    ch[13:26] = True
+    assert bool(torch.isfinite(g["dweight"][~ch]).all()) and bool(torch.isfinite(g["dbias"][~ch]).all())
+
+
 # ------------------------------------------------------------------------------------------------
 # refusals
 # ------------------------------------------------------------------------------------------------

@@ -48,7 +48,7 @@ def test_recurrence(checked, shape, layout, dtype):
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("layout", ["fused", "odd"])
 @pytest.mark.parametrize("shape", [(7, 1, 96, 12), (9, 1, 130, 13), (2, 1, 5000, 1), (2, 1000, 320, 32),
-                                   (3, 64, 66, 11), (2, 3, 20000, 1)], ids=str)
+                                   (3, 64, 66, 11), (2, 3, 20000, 1), (300, 1, 520, 40)], ids=str)
 def test_norm(checked, shape, layout, dtype):
     N, S, C, G = shape
     d = tn.inputs(N, S, C, dtype, seed=22, layout=layout, dev="cuda")
