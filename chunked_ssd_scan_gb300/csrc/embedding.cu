@@ -77,8 +77,8 @@ __global__ void __launch_bounds__(kThreads) embed_forward_kernel(const Id* ids, 
 // 2. A subgroup of threads takes kPiece sorted tokens and adds their rows, writing each row's sum as its
 //    run ends; a run that goes on over the ends of a piece leaves partial sums instead,
 // 3. which the piece where the run starts joins, in order.
-// Bound by memory: dout once, every row of dtable once.  32768 tokens, 50000 x 2048 bf16: 120 us, 4.5 TB/s
-// of 544 MB (67 % of the measured copy rate): sorting takes 7 + 2 x 12 us beside 94 MB of clearing, the
+// Bound by memory: dout once, every row of dtable once.  32768 tokens, 50000 x 2048 bf16: 117 us, 4.6 TB/s
+// of 544 MB (69 % of the measured copy rate): sorting takes 7 + 2 x 12 us beside 94 MB of clearing, the
 // sums 60 us for 401 MB, the join 19 us beside 47 MB.  With few tokens and rows it is a chain of
 // five short launches: 14824 tokens, 10335 x 324 f32 take 40 us.
 // ------------------------------------------------------------------------------------------------
@@ -339,13 +339,21 @@ __global__ void __launch_bounds__(kThreads) embed_scatter_kernel(EmbedParams p) 
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < kKeys; ++k) {
-    if (i0 + k * 32 >= p.n) continue;
-    const int64_t at = seen[warp][(key[k] >> p.shift) & (kBins - 1)] + rank[k];
-    if (!SSD_INDEX_OK(p.hdr, at, p.n, 81)) continue;
-    p.key[p.in ^ 1][at] = key[k];
-    p.pos[p.in ^ 1][at] = pos[k];
-    if (p.next_hist)
-      atomicAdd(p.next_hist + (int64_t)((key[k] >> (p.shift + 8)) & (kBins - 1)) * p.sort_tiles + at / kSortTile, 1u);
+    const bool in = i0 + k * 32 < p.n;
+    int64_t at = 0;
+    if (in) {
+      at = seen[warp][(key[k] >> p.shift) & (kBins - 1)] + rank[k];
+      if (SSD_INDEX_OK(p.hdr, at, p.n, 81)) {
+        p.key[p.in ^ 1][at] = key[k];
+        p.pos[p.in ^ 1][at] = pos[k];
+      }
+    }
+    if (p.next_hist) {   // lanes with the same count are added by one: the last pass may have two digits only
+      const uint32_t bin =
+          in ? ((key[k] >> (p.shift + 8)) & (kBins - 1)) * (uint32_t)p.sort_tiles + (uint32_t)(at / kSortTile) : ~0u;
+      const uint32_t same = __match_any_sync(0xffffffffu, bin);
+      if (in && lane == __ffs(same) - 1) atomicAdd(p.next_hist + bin, (uint32_t)__popc(same));
+    }
   }
 }
 
@@ -362,15 +370,13 @@ __device__ __forceinline__ void store_sum(float* p, const float (&v)[V], float s
   }
 }
 
-// A thread's vector of one row to its own place in shared memory, asynchronously where it has 4 bytes or
-// more (it alone reads it there).
+// A thread's vector of one row (4 bytes or more) to its own place in shared memory; it alone reads it there.
 template <int kBytes>
 __device__ __forceinline__ void copy_async(void* dst, const void* src) {
   const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
   if constexpr (kBytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
   else if constexpr (kBytes == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(src) : "memory");
   else if constexpr (kBytes == 4) asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(src) : "memory");
-  else *static_cast<uint16_t*>(dst) = *static_cast<const uint16_t*>(src);
 }
 
 template <typename T, int V>
@@ -403,6 +409,31 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(EmbedParams p, int 
     if (j < n) copy_async<V * (int)sizeof(T)>(&ring[slot][threadIdx.x], dout + (int64_t)pos[j] * p.D);
     cp_async_commit();
   };
+  if constexpr (V * (int)sizeof(T) < 4) {   // single bf16 values: no asynchronous copy takes them
+    constexpr int U = 16;
+    for (int j = 0; j < n; j += U) {
+      T f[U];
+      uint32_t k[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        k[u] = j + u < n ? key[j + u] : none;
+        if (k[u] != none) f[u] = dout[(int64_t)pos[j + u] * p.D];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (k[u] == none) continue;
+        if (k[u] != cur) {
+          flush(false);
+          open = false;
+          cur = k[u];
+          acc[0] = 0.f;
+        }
+        acc[0] += (float)f[u];
+      }
+    }
+    flush(j0 + n < p.n && key[n] == cur);
+    return;
+  }
   for (int j = 0; j < kRing; ++j) request(j, j);
   int slot = 0;
   for (int j = 0; j < n; ++j) {
@@ -427,11 +458,11 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(EmbedParams p, int 
 }
 
 // Runs over more than one piece: the piece where one starts adds the heads of those after it.  Keys and
-// heads are asked for together (a head that is not the run's is not used), eight pieces at a time.
+// heads are asked for together (a head that is not the run's is not used), 32 values a thread at a time.
 template <int V>
 __global__ void __launch_bounds__(kThreads) embed_join_kernel(EmbedParams p, int cols, int subs) {
   follow();
-  constexpr int U = 8;
+  constexpr int U = 32 / V;   // heads in flight
   if ((int)blockIdx.x >= p.work_blocks) return clear_rows(p);
   const int col = threadIdx.x % cols, sub = threadIdx.x / cols;
   const int64_t d = ((int64_t)blockIdx.y * cols + col) * V, piece = (int64_t)blockIdx.x * subs + sub;
@@ -537,10 +568,10 @@ int embed_passes(int64_t rows) {
 EmbedLayout embed_layout(int64_t n, int64_t rows, int64_t D) {
   EmbedLayout L;
   L.sort_tiles = (n + kSortTile - 1) / kSortTile;
-  // short pieces while their threads (one a vector of 16 bytes of bf16) do not fill the machine, four
-  // blocks an SM, then longer ones: they keep the partial sums of frequent rows few
+  // short pieces while they do not fill the machine (four blocks an SM), then longer ones: they keep the
+  // chain of partial sums that the join of a frequent row follows short
   L.piece = 32;
-  while (L.piece < 256 && n / L.piece * ((D + 7) / 8) > 152 * 4 * kThreads) L.piece *= 2;
+  while (L.piece < 256 && n / L.piece > 4 * 152) L.piece *= 2;
   L.pieces = (n + L.piece - 1) / L.piece;
   size_t off = sizeof(WsHeader);
   auto take = [&](size_t bytes) {
