@@ -596,10 +596,13 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(const __gr
     const int slot = it & 1;
     const Place q = places[slot];
     if (q.tile >= p.tiles) break;
-    if constexpr (ALIGN != kTma) load(places[slot ^ 1], slot ^ 1);
     if constexpr (ALIGN == kTma) {
       tma_wait(full + slot, (it >> 1) & 1, p.hdr);
     } else {
+      // The stage that is filled now held the tile before, whose dy the walk at its end read: a lane's
+      // copies cover rows that other lanes read, so every lane of the warp has to be through.
+      __syncwarp();
+      load(places[slot ^ 1], slot ^ 1);
       cp_async_wait<1>();
       __syncwarp();
     }

@@ -1,0 +1,64 @@
+"""Forms of the recurrence, the norm and the embedding that only some sizes, strides or alignments reach
+(GPU), each against the fp64 form."""
+import numpy as np
+import pytest
+import torch
+
+import chunked_ssd_scan_gb300 as pkg
+from tests import lm_reference as ref
+from tests import test_gated_recurrence as tr
+from tests.parity_util import to_np
+
+pytestmark = pytest.mark.gpu
+
+
+def moved(d, how, dtype):
+    """The inputs of test_gated_recurrence.inputs with other strides: what the axes of a model's tensors may be."""
+    d = dict(d)
+    b, T, D = d["x"].shape
+    if how == "dy_steps":        # the gradient of a mean over the steps
+        d["dy"] = d["dy"][:, :1].expand(b, T, D)
+    elif how == "dy_all":
+        d["dy"] = d["dy"][:1, :1].expand(b, T, D)
+    elif how == "x_batch":       # one sequence under several gates
+        d["x"] = d["x"][:1].expand(b, T, D)
+    elif how == "gates_steps":   # gates that do not change along time
+        for k in ("ga", "gx"):
+            d[k] = d[k][:, :1].expand(b, T, D)
+    elif how == "time_major":    # [T,b,D] in memory: the batch stride is the smaller one
+        for k in ("x", "ga", "gx", "dy"):
+            d[k] = d[k].transpose(0, 1).contiguous().transpose(0, 1)
+    elif how == "each_its_own":  # contiguous, time-major, a slice of wider rows, a slice that starts one element late
+        d["ga"] = d["ga"].transpose(0, 1).contiguous().transpose(0, 1)
+        d["gx"] = torch.cat((d["gx"], d["gx"]), 2)[..., D:]
+        d["dy"] = torch.cat((d["dy"][..., :1], d["dy"]), 2)[..., 1:]
+    return d
+
+
+# D: a multiple of 8 but not of a tile's width, and one that is odd (2-byte copies for bf16)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(3, 200, 72), (2, 129, 200), (2, 150, 31)], ids=str)
+@pytest.mark.parametrize("how", ["dy_steps", "dy_all", "x_batch", "gates_steps", "time_major", "each_its_own"])
+def test_recurrence_strides(how, shape, dtype):
+    d = moved(tr.inputs(*shape, dtype, seed=31, dev="cuda"), how, dtype)
+    args = (d["x"], d["ga"], d["gx"], d["decay"])
+    plan = pkg.GatedRecurrencePlan(*args, c=tr.C, init_state=d["init"], return_states=True)
+    y, fin, states = plan()
+    assert pkg.workspace_status(plan.workspace) == ("SSD_OK", 0)
+    ry, rf, rs = tr.reference(d)
+    ref.check(to_np(y), ry, tr.REL[dtype], "y")
+    ref.check(to_np(fin), rf, 0.0, "final_state", scale=ry[:, -1])
+    ref.check(to_np(states), rs, 0.0, "states")
+    back = pkg.GatedRecurrenceBackwardPlan(*args, d["dy"], c=tr.C, init_state=d["init"], states=states,
+                                           dfinal=d["dfinal"])
+    g = {k: to_np(v) for k, v in back().items()}
+    assert pkg.workspace_status(back.workspace) == ("SSD_OK", 0)
+    r = tr.reference_grad(d)
+    for k in ("dx", "dgate_x", "dgate_a"):
+        ref.check(g[k], r[k], tr.REL[dtype], k)
+    b, T, _ = shape
+    # the difference in dl is as in the contiguous form; G along broadcast steps grows to 1 / (1 - a) <= 1000
+    # times dy where dy does not change sign, so the sums' scale goes with the terms' own
+    size = np.abs(r["ddecay"]) + np.sqrt(b * T) * 4 * max(1.0, np.abs(r["dx"]).max())
+    ref.check(g["ddecay"], r["ddecay"], 0.0, "ddecay", scale=size)
+    ref.check(g["dinit"], r["dinit"], 0.0, "dinit")
