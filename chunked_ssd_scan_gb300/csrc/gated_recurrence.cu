@@ -43,9 +43,44 @@ struct RecParams {
 
 __device__ __forceinline__ float softplus(float d) { return fmaxf(d, 0.f) + log1pf(expf(-fabsf(d))); }
 
-// The decay is carried as w = a - 1 = expm1(l), and a step is h + (w h + b): near one, a itself has an
-// absolute rounding error of 2^-25 whose bias a channel with memory 1 / (1 - a) multiplies by
-// that memory, while w's error is relative to 1 - a.
+// A decay is kept as one number c (lookback.cuh): a - 1 = expm1(l) < 0 next to one, where a step is
+// h + (c h + b), and a itself below e^-1/4, where it is c h + b.  A warp whose channels cannot decay
+// faster than e^-1/4 a step does the first for all its values; others choose value by value (8 x 4096 x
+// 2048 bf16: 112 us forward, 250 us backward, where the first takes 102 and 227).  Both make NaN of an
+// infinite state next to one (inf - inf): an odd tile, one that meets values of kHuge or more, or NaN, is finished
+// by a function that goes through its steps once more, one by one, in a third form that does not (all tiles
+// odd: 207 us forward).  It is called, not part of the kernels: with its code inline they ran out of
+// registers (forward 145 us).
+constexpr float kInf = lookback::kInf;
+enum Form { kSlow, kMixed, kSafe };
+template <int F>
+__device__ __forceinline__ float step(float c, float b, float h) {   // a h + b
+  if (F == kSafe) return lookback::apply_safe(c, b, h);
+  if (F == kMixed) return lookback::apply(c, b, h);
+  return h + fmaf(c, h, b);
+}
+template <int F>
+__device__ __forceinline__ float2 step(float2 c, float2 b, float2 h) {
+  if (F == kSafe) return make_float2(lookback::apply_safe(c.x, b.x, h.x), lookback::apply_safe(c.y, b.y, h.y));
+  float2 t = fp::fma2(c, h, b);
+  if (F == kSlow) return fp::add2(h, t);
+  if (c.x < 0.f) t.x += h.x;
+  if (c.y < 0.f) t.y += h.y;
+  return t;
+}
+template <int F>
+__device__ __forceinline__ float decayed(float c, float v) {   // a v
+  if (F == kSafe && fabsf(v) == kInf) return v;
+  return fmaf(c, v, F == kSlow || c < 0.f ? v : 0.f);
+}
+template <int F>
+__device__ __forceinline__ float2 decayed(float2 c, float2 v) {
+  if (F == kSlow) return fp::fma2(c, v, v);
+  return make_float2(decayed<F>(c.x, v.x), decayed<F>(c.y, v.y));
+}
+constexpr float kHuge = 1e30f;   // what a tile makes of its maps stays finite below it
+__device__ __forceinline__ bool huge2(float2 v) { return !(fabsf(v.x) + fabsf(v.y) < kHuge); }   // or NaN
+__device__ __forceinline__ bool rarely(bool v) { return __builtin_expect(v, 0); }
 
 // ------------------------------------------------------------------------------------------------
 // Forward.
@@ -53,14 +88,14 @@ __device__ __forceinline__ float softplus(float d) { return fmaxf(d, 0.f) + log1
 // The work is cut into tiles of kSteps steps by one 128-byte row of channels.  A block takes tiles
 // by ticket, time-major, so a tile only ever waits for tiles with smaller tickets, which blocks
 // hold that are running: every wait ends.  The next tile's rows are in flight while this one is
-// computed.  A warp owns SPW consecutive steps of the tile, forms w and b = m i x once, in
-// registers, and composes its steps into one map; the maps of the block's warps and, by look-back, of
-// earlier tiles give the state before the warp's first step, and a second walk over the registers
-// writes y.  Every input byte is read once.
+// computed.  A warp owns SPW consecutive steps of the tile, forms c and b = m i x once, in
+// registers, and composes its steps into one map (its decay from the sum of the l); the maps of the
+// block's warps and, by look-back, of earlier tiles give the state before the warp's first step, and a
+// second walk over the registers writes y.  Every input byte is read once.
 //
-// 8 x 4096 x 2048 bf16 with states: 98 us, 5.5 TB/s of 541 MB (81 % of the measured copy rate), with the
-// special-function unit (4 a value) and the issue slots (30 instructions a value) each busy about
-// 60 % of the time; 1 x 131072 x 1024 f32: 339 us, 6.35 TB/s (94 %).
+// 8 x 4096 x 2048 bf16 with states: 102 us, 5.3 TB/s of 541 MB (78 % of the measured copy rate), with the
+// special-function unit (4 a value) and the issue slots (33 instructions a value) each busy more than half
+// of the time; 1 x 131072 x 1024 f32: 357 us, 6.0 TB/s (89 %).
 // ------------------------------------------------------------------------------------------------
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
@@ -68,6 +103,9 @@ constexpr int kRowBytes = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTiny = 1e-36f;   // well above the smallest normal number (the approximations flush what is below)
 
+// Special functions by approximation: 1/x is good to 2^-23, 2^x and 1/sqrt x to 2^-22, and v log2 e adds |v| 2^-23
+// to e^v, so a sigmoid s is good to about 2^-21 + (1 - s) |v| 2^-23.  The exact functions are several
+// instructions each, of which the kernels issue 33 and 63 a value in all.
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -84,28 +122,41 @@ __device__ __forceinline__ float2 one_plus_exp2(float2 v) {
   const float2 t = fp::mul2(v, dup(-kLog2e));
   return fp::add2(make_float2(fp::ex2_approx(t.x), fp::ex2_approx(t.y)), dup(1.f));
 }
+__device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
 __device__ __forceinline__ float2 rcp2(float2 d) { return make_float2(rcp_approx(d.x), rcp_approx(d.y)); }
-// expm1(l) for l <= 0.  Above -1/4 the Taylor polynomial of degree 6, whose remainder l^6 / 5040 is
-// 5e-8 of the value; below, 2^x - 1, whose error 2^-22 is at most 1e-6 of the value.  kFar = false
-// where no channel of the warp can leave the polynomial's range (l >= -rate).
+// l = rate r, and in the mixed form a little less: there c = 0 is a decay of zero, not of one.
+template <bool kFar>
+__device__ __forceinline__ float2 log_decay(float2 rate, float2 r) {
+  return kFar ? fp::fma2(rate, r, dup(-kTiny)) : fp::mul2(rate, r);
+}
+// c of a decay e^l.  Above -1/4 expm1 by the Taylor polynomial of degree 6, whose remainder l^6 / 5040 is 5e-8
+// of the value; below, 2^x, whose error is 2^-22 and the argument's |l| 2^-23.  kFar = false where no
+// channel of the warp can leave the polynomial's range (l >= -rate).
 constexpr float kNear = 0.25f;
 template <bool kFar>
-__device__ __forceinline__ float2 expm1_neg2(float2 l) {
+__device__ __forceinline__ float2 decay(float2 l) {
   float2 q = fp::fma2(l, dup(1.f / 720), dup(1.f / 120));
   q = fp::fma2(q, l, dup(1.f / 24));
   q = fp::fma2(q, l, dup(1.f / 6));
   q = fp::fma2(q, l, dup(0.5f));
-  float2 w = fp::fma2(fp::mul2(q, l), l, l);
+  float2 c = fp::fma2(fp::mul2(q, l), l, l);
   if (kFar) {
-    const float2 e = make_float2(fp::ex2_approx(l.x * kLog2e) - 1.f, fp::ex2_approx(l.y * kLog2e) - 1.f);
-    w.x = l.x < -kNear ? e.x : w.x;
-    w.y = l.y < -kNear ? e.y : w.y;
+    const float2 a = make_float2(fp::ex2_approx(l.x * kLog2e), fp::ex2_approx(l.y * kLog2e));
+    c.x = l.x < -kNear ? a.x : c.x;
+    c.y = l.y < -kNear ? a.y : c.y;
   }
-  return w;
+  return c;
 }
-// 1 - a^2 = -w (2 + w), plus a number too small to matter that keeps it from being zero
-__device__ __forceinline__ float2 one_minus_a2(float2 w) {
-  return fp::fma2(w, fp::fma2(w, dup(-1.f), dup(-2.f)), dup(kTiny));
+// 1 - a^2, without cancellation next to one: -c (2 + c), plus a number too small to matter that keeps it from
+// being zero.
+template <bool kFar>
+__device__ __forceinline__ float2 one_minus_a2(float2 c) {
+  float2 v = fp::fma2(c, fp::fma2(c, dup(-1.f), dup(-2.f)), dup(kTiny));
+  if (kFar) {
+    v.x = c.x < 0.f ? v.x : fmaf(-c.x, c.x, 1.f);
+    v.y = c.y < 0.f ? v.y : fmaf(-c.y, c.y, 1.f);
+  }
+  return v;
 }
 
 // Copy of 8 bytes, of which the first n are read and the others zeros.
@@ -232,39 +283,122 @@ __device__ __forceinline__ void finish_tickets(const RecParams& p) {
 template <typename T, int SPW>
 struct Walk {
   static constexpr int kCpl = Tile<T>::kCpl, kPairs = SPW * kCpl / 2;
-  // f(value index, pair) for every pair in step order
-  static __device__ __forceinline__ void compose(const float2 (&w)[kPairs], const float2 (&b)[kPairs], float2& W,
-                                                 float2& H) {
-    W = H = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < kPairs; ++k) {
-      if constexpr (kCpl == 2) {
-        H = lookback::apply(w[k], b[k], H);
-        W = lookback::apply(w[k], w[k], W);
-      } else {
-        H.x = lookback::apply(w[k].y, b[k].y, lookback::apply(w[k].x, b[k].x, H.x));
-        W.x = lookback::apply(w[k].y, w[k].y, lookback::apply(w[k].x, w[k].x, W.x));
-      }
-    }
+  // the state after pair k from the one before it (f32: in x; y is the state between its two steps)
+  template <int F>
+  static __device__ __forceinline__ float2 next(float2 c, float2 b, float2 h) {
+    if constexpr (kCpl == 2) return step<F>(c, b, h);
+    h.y = step<F>(c.x, b.x, h.x);
+    h.x = step<F>(c.y, b.y, h.y);
+    return h;
   }
-  // zeroes the pairs of steps from `steps` on
-  static __device__ __forceinline__ void cut(float2 (&v)[kPairs], int64_t steps) {
+  // the gradient that pair k hands to the step before it, from the one that is handed to it (f32: in x)
+  template <int F>
+  static __device__ __forceinline__ float2 before(float2 c, float2 dy, float2 Q) {
+    if constexpr (kCpl == 2) return decayed<F>(c, fp::add2(dy, Q));
+    Q.x = decayed<F>(c.x, dy.x + decayed<F>(c.y, dy.y + Q.x));
+    return Q;
+  }
+  // w of the steps so far and pair k's, in the slow form (f32: in x)
+  static __device__ __forceinline__ float2 together(float2 c, float2 w) {
+    if constexpr (kCpl == 2) return fp::add2(w, fp::fma2(c, w, c));
+    w.x += fmaf(c.x, w.x, c.x);
+    w.x += fmaf(c.y, w.x, c.y);
+    return w;
+  }
+  // sets the pairs of steps from `steps` on
+  static __device__ __forceinline__ void cut(float2 (&v)[kPairs], int steps, float to) {
 #pragma unroll
     for (int k = 0; k < kPairs; ++k) {
       if constexpr (kCpl == 2) {
-        if (k >= steps) v[k] = make_float2(0.f, 0.f);
+        if (k >= steps) v[k] = dup(to);
       } else {
-        if (2 * k >= steps) v[k].x = 0.f;
-        if (2 * k + 1 >= steps) v[k].y = 0.f;
+        if (2 * k >= steps) v[k].x = to;
+        if (2 * k + 1 >= steps) v[k].y = to;
       }
     }
   }
 };
 
+// By one warp: the maps of a block's warps as one (in time order, or backwards), and the states before each of
+// them from the one before the first, which becomes the one behind the last.
+template <int NW, int N, bool kBack, typename M, typename L>
+__device__ __forceinline__ void block_map(const M& maps, const L& logs, int cl, float (&A)[N], float (&H)[N]) {
+  float l[N];
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    H[c] = l[c] = 0.f;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) {
+      const float2 m = maps[kBack ? NW - 1 - k : k][cl + c];
+      H[c] = lookback::apply(m.x, m.y, H[c]);
+      l[c] += logs[k][cl + c];
+    }
+  }
+  const float2 a = decay<true>(make_float2(l[0], l[N - 1]));
+  A[0] = a.x;
+  A[N - 1] = N == 2 ? a.y : a.x;
+}
+template <int NW, int N, bool kBack, typename M, typename B>
+__device__ __forceinline__ void block_states(const M& maps, B& before, int cl, float (&h)[N]) {
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+#pragma unroll
+    for (int j = 0; j < NW; ++j) {
+      const int k = kBack ? NW - 1 - j : j;
+      before[k][cl + c] = h[c];
+      const float2 m = maps[k][cl + c];
+      h[c] = lookback::apply(m.x, m.y, h[c]);
+    }
+  }
+}
+
+// The same in the third form: the state before the `count`-th warp from the one before the first.
+template <int NW, int N, bool kBack, typename M>
+__device__ __forceinline__ float2 safe_state(const M& maps, int cl, int count, float2 h) {
+#pragma unroll 1
+  for (int j = 0; j < count; ++j) {
+    const int k = kBack ? NW - 1 - j : j;
+    const float2 m0 = maps[k][cl], m1 = maps[k][cl + N - 1];
+    h = step<kSafe>(make_float2(m0.x, m1.x), make_float2(m0.y, m1.y), h);
+  }
+  return h;
+}
+
+// A step formed from its row in shared memory (of x, gate_a, gate_x and, in the backward, dy), in the third form.
+struct Step {
+  float2 x, dy, c, mi, xi, io, r;
+};
+template <typename T, bool kBackward>
+__device__ __forceinline__ Step step_at(const unsigned char* row, int array, int lane, float2 rate) {
+  auto at = [&](int a) {
+    const unsigned char* v = row + a * array;
+    return Tile<T>::kCpl == 2 ? pair_at(v, 0, lane, __nv_bfloat16()) : dup(reinterpret_cast<const float*>(v)[lane]);
+  };
+  Step v;
+  v.x = at(0);
+  v.r = rcp2(one_plus_exp2(at(1)));
+  const float2 d = one_plus_exp2(at(2)), i = rcp2(d);
+  v.c = decay<true>(log_decay<true>(rate, v.r));
+  const float2 u = one_minus_a2<true>(v.c), over = make_float2(rsqrt_approx(u.x), rsqrt_approx(u.y));
+  const float2 m = fp::mul2(u, over);
+  v.mi = fp::mul2(m, i);
+  if (!kBackward) {   // as in the forward's other forms
+    const float2 d2 = fp::mul2(fp::mul2(u, d), d);
+    const float2 mi = fp::mul2(u, make_float2(rsqrt_approx(d2.x), rsqrt_approx(d2.y)));
+    v.mi = mi;
+  } else {
+    const float2 ix = fp::mul2(i, v.x);
+    v.dy = at(3);
+    v.xi = fp::mul2(fp::mul2(m, ix), fp::fma2(i, dup(-1.f), dup(1.f)));
+    v.io = decayed<kSafe>(v.c, fp::mul2(ix, fp::mul2(over, v.r)));
+  }
+  return v;
+}
+
 // NW warps of 16 steps.  Half as many blocks of 8 warps wait for the look-back together, so bf16,
-// bound by issue slots, takes four blocks of 4 warps an SM (8 x 4096 x 2048: 98 us, 102 us with two
-// of 8); f32, whose rows are half as many channels, takes the longer tiles and with them half the
-// look-back's chain (1 x 131072 x 1024: 339 us, 364 us with 4 warps).
+// bound by issue slots, takes four blocks of 4 warps an SM; f32, whose rows are half as many channels,
+// takes the longer tiles and with them half the look-back's chain (1 x 131072 x 1024: 357 us, 388 us with
+// 4 warps).
 template <typename T>
 struct Forward {
   static constexpr int kNw = sizeof(T) == 2 ? 4 : 8, kSpw = 16, kSteps = kNw * kSpw, kBlocks = 16 / kNw;
@@ -272,9 +406,9 @@ struct Forward {
 
 // How a tile's rows get to shared memory: as one TMA box an array, or by every warp for its own rows in
 // copies of 16 bytes (arrays that TMA does not take: broadcast axes), 8, 4 or 2.  A box costs its
-// block a few instructions, the copies a tenth of all (8 x 4096 x 2048 bf16: forward 98 us, 106 us by
-// copies of 16; backward 215 and 245 us); 29 x 12456 x 332 bf16, whose rows start on 8 bytes, takes
-// 360 us by copies of 8 and 410 by copies of 4.
+// block a few instructions, the copies a tenth of all (8 x 4096 x 2048 bf16: forward 102 us, 111 us by
+// copies of 16; backward 227 and 247 us); 29 x 12456 x 332 bf16, whose rows start on 8 bytes, takes
+// 357 us by copies of 8 and 395 by copies of 4.
 constexpr int kTma = 32;
 
 __device__ __forceinline__ void tma_tile(void* dst, const CUtensorMap* map, uint64_t* bar, const Place& q) {
@@ -298,23 +432,132 @@ __device__ __forceinline__ void tma_wait(uint64_t* bar, uint32_t phase, WsHeader
   if (!tc::mbar_wait_bounded(bar, phase, 1000000000ull) && threadIdx.x == 0) latch_error(hdr, SSD_ERR_TIMEOUT, 402);
 }
 
+template <typename T>
+struct ForwardShared {
+  static constexpr int NW = Forward<T>::kNw, kCh = Tile<T>::kCh;
+  float2 maps[NW][kCh];    // (c, H) of every warp's steps
+  float logs[NW][kCh];     // their log decays together
+  float before[NW][kCh];   // the state before every warp's steps
+  float rates[3][kCh];     // -c softplus(decay) of the tile's channels
+  Place places[3];         // of the tile in hand, the one being loaded and the one after it
+  int odd[2][2];           // the tile has huge values: in its maps, in the state before it
+  uint64_t full[2];        // TMA: a stage's boxes have landed
+};
+// By one warp: a tile's place and its channels' rates.
+template <typename T>
+__device__ __forceinline__ void fetch_forward(const RecParams& p, ForwardShared<T>& s, uint32_t last, int turn) {
+  constexpr int kCpl = Tile<T>::kCpl;
+  const int lane = threadIdx.x % 32, cl = lane * kCpl;
+  uint32_t tile = last + gridDim.x;
+  if (p.ticket) {
+    if (lane == 0) tile = atomicAdd(p.ticket, 1u);
+    tile = __shfl_sync(0xffffffffu, tile, 0);
+  }
+  const Place q = place<T, Forward<T>::kSteps, false>(p, tile);
+  if (lane == 0) s.places[turn] = q;
+  if (tile < p.tiles) {
+#pragma unroll
+    for (int c = 0; c < kCpl; ++c)
+      s.rates[turn][cl + c] = cl + c < q.left ? -p.c * softplus(p.decay[q.c0 + cl + c]) : 0.f;
+  }
+}
+
+// The rest of a tile with huge values: from its maps on (behind barrier A), or from the states before the warps'
+// steps (behind barrier B).  `stage`: the tile's rows; `slot`, `turn`: where it lies in `odd` and `places`.
+template <typename T, int ALIGN>
+__device__ __noinline__ void odd_forward(const RecParams& p, ForwardShared<T>& s, const unsigned char* stage, int slot,
+                                         int turn, bool maps, bool first) {
+  constexpr int NW = Forward<T>::kNw, SPW = Forward<T>::kSpw, kCh = Tile<T>::kCh, kCpl = Tile<T>::kCpl;
+  constexpr int kWarpBytes = SPW * kRowBytes, kArray = NW * kWarpBytes;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, cl = lane * kCpl;
+  const Place q = s.places[turn];
+  const float2 rate = make_float2(s.rates[turn][cl], s.rates[turn][cl + kCpl - 1]);
+  const int steps = (int)p.T - (int)q.t0 - warp * SPW, inside = min(SPW, max(0, steps));
+  const unsigned char* rows = stage + warp * kWarpBytes;
+  if (maps) {
+    float2 H = make_float2(0.f, 0.f);
+#pragma unroll 1
+    for (int k = 0; k < inside; ++k) {
+      const Step v = step_at<T, false>(rows + k * kRowBytes, kArray, lane, rate);
+      H = step<kSafe>(v.c, fp::mul2(v.mi, v.x), H);
+    }
+    s.maps[warp][cl].y = H.x;
+    if (kCpl == 2) s.maps[warp][cl + kCpl - 1].y = H.y;
+    __syncthreads();
+    if (warp == 0) {
+      float A[kCpl], H[kCpl], h[kCpl];
+      block_map<NW, kCpl, false>(s.maps, s.logs, cl, A, H);
+      const float2 all = safe_state<NW, kCpl, false>(s.maps, cl, NW, make_float2(0.f, 0.f));
+      H[0] = all.x;
+      H[kCpl - 1] = kCpl == 2 ? all.y : all.x;
+      if (first) wait_for_words();
+      uint64_t* words = p.words + q.word + cl;
+      const bool last = q.ti == p.ntile - 1;
+      uint64_t v[kCpl];
+      if (q.ti == 0) {
+#pragma unroll
+        for (int c = 0; c < kCpl; ++c) h[c] = p.init && cl + c < q.left ? p.init[q.b * p.D + q.c0 + cl + c] : 0.f;
+      } else {
+        if (!last) {
+#pragma unroll
+          for (int c = 0; c < kCpl; ++c) v[c] = lookback::map(A[c], H[c]);
+          lookback::publish(words, v);
+        }
+        lookback::state_before<1>(words - kCh, -kCh, q.ti, h, p.hdr, 400);
+      }
+      if (!last) {
+#pragma unroll
+        for (int c = 0; c < kCpl; ++c) v[c] = lookback::inclusive(lookback::apply_safe(A[c], H[c], h[c]));
+        lookback::publish(words, v);
+      }
+      s.before[0][cl] = h[0];
+      if (kCpl == 2) s.before[0][cl + kCpl - 1] = h[kCpl - 1];
+    } else if (warp == 1) {
+      const int next = turn == 2 ? 0 : turn + 1;
+      fetch_forward(p, s, s.places[next].tile, next == 2 ? 0 : next + 1);
+      if (lane < 2) s.odd[slot ^ 1][lane] = 0;
+    }
+    __syncthreads();
+  }
+  float2 h = safe_state<NW, kCpl, false>(s.maps, cl, warp, make_float2(s.before[0][cl], s.before[0][cl + kCpl - 1]));
+  const int n = min(kCpl, max(0, q.left - cl));
+  if (n > 0 && steps > 0) {
+    const int64_t states = (q.b * p.nch + (q.t0 + warp * SPW) / kChunk) * p.D + q.c0 + cl;
+    if (p.states_out && warp * SPW % kChunk == 0 && SSD_INDEX_OK(p.hdr, states + n - 1, p.batch * p.nch * p.D, 60)) {
+      p.states_out[states] = h.x;
+      if (n == 2) p.states_out[states + 1] = h.y;
+    }
+    const int64_t row0 = (q.b * p.T + q.t0 + warp * SPW) * p.D + q.c0 + cl;
+#pragma unroll 1
+    for (int k = 0; k < inside; ++k) {
+      const Step v = step_at<T, false>(rows + k * kRowBytes, kArray, lane, rate);
+      h = step<kSafe>(v.c, fp::mul2(v.mi, v.x), h);
+      const float o[2] = {h.x, h.y};
+      if (p.y && SSD_INDEX_OK(p.hdr, row0 + k * p.D + n - 1, p.batch * p.T * p.D, 61))
+        store_row<ALIGN>(static_cast<T*>(p.y) + row0 + k * p.D, o, n);
+    }
+    const int64_t at = q.b * p.D + q.c0 + cl;
+    if (p.final_state && steps <= SPW && SSD_INDEX_OK(p.hdr, at + n - 1, p.batch * p.D, 62)) {
+      p.final_state[at] = h.x;
+      if (n == 2) p.final_state[at + 1] = h.y;
+    }
+  }
+  __syncthreads();   // the rows and maps are read no more
+}
+
 template <typename T, int ALIGN>
 __global__ void __launch_bounds__(32 * Forward<T>::kNw, Forward<T>::kBlocks) rec_forward_kernel(const __grid_constant__ RecParams p) {
-  constexpr int NW = Forward<T>::kNw, SPW = Forward<T>::kSpw, kSteps = Forward<T>::kSteps, kCh = Tile<T>::kCh, kCpl = Tile<T>::kCpl;
+  constexpr int NW = Forward<T>::kNw, SPW = Forward<T>::kSpw, kCh = Tile<T>::kCh, kCpl = Tile<T>::kCpl;
   constexpr int kPairs = Walk<T, SPW>::kPairs, kWarpBytes = SPW * kRowBytes, kArray = NW * kWarpBytes;
   constexpr int kStage = 3 * kArray;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ float2 maps[NW][kCh];      // (W, H) of every warp's steps
-  __shared__ float before[NW][kCh];     // the state before every warp's steps
-  __shared__ float rates[2][kCh];           // -c softplus(decay) of the tile's channels
-  __shared__ Place places[2];               // of the tile in hand and the one being loaded
-  __shared__ uint64_t full[2];              // TMA: a stage's boxes have landed
+  __shared__ ForwardShared<T> s;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int cl = lane * kCpl;
 
   auto load = [&](const Place& q, int stage) {
     if constexpr (ALIGN == kTma) {
-      if (threadIdx.x == 0 && q.tile < p.tiles) tma_load<3>(smem + stage * kStage, p, full + stage, q, kArray);
+      if (threadIdx.x == 0 && q.tile < p.tiles) tma_load<3>(smem + stage * kStage, p, s.full + stage, q, kArray);
       return;
     }
     if (q.tile < p.tiles) {
@@ -322,9 +565,9 @@ __global__ void __launch_bounds__(32 * Forward<T>::kNw, Forward<T>::kBlocks) rec
       const int rows = (int)min((int64_t)SPW, max((int64_t)0, p.T - t)), bytes = q.left * (int)sizeof(T);
       unsigned char* d = smem + stage * kStage + warp * kWarpBytes;
       // a warp whose rows all lie past the end reads nothing: its pointers are the array's start
-      auto at = [&](const void* base, const int64_t (&s)[2]) {
+      auto at = [&](const void* base, const int64_t (&stride)[2]) {
         return static_cast<const unsigned char*>(base) +
-               (rows > 0 ? (q.b * s[0] + t * s[1] + q.c0) * (int64_t)sizeof(T) : 0);
+               (rows > 0 ? (q.b * stride[0] + t * stride[1] + q.c0) * (int64_t)sizeof(T) : 0);
       };
       load_rows<SPW, ALIGN>(d, at(p.x, p.xs), p.xs[1] * sizeof(T), rows, bytes, lane);
       load_rows<SPW, ALIGN>(d + kArray, at(p.ga, p.as), p.as[1] * sizeof(T), rows, bytes, lane);
@@ -332,90 +575,84 @@ __global__ void __launch_bounds__(32 * Forward<T>::kNw, Forward<T>::kBlocks) rec
     }
     cp_async_commit();
   };
-  // by one warp: the next tile's place and its channels' rates
-  auto fetch = [&](uint32_t last, int slot) {
-    uint32_t tile = last + gridDim.x;
-    if (p.ticket) {
-      if (lane == 0) tile = atomicAdd(p.ticket, 1u);
-      tile = __shfl_sync(0xffffffffu, tile, 0);
-    }
-    const Place q = place<T, kSteps, false>(p, tile);
-    if (lane == 0) places[slot] = q;
-    if (tile < p.tiles) {
-#pragma unroll
-      for (int c = 0; c < kCpl; ++c)
-        rates[slot][cl + c] = cl + c < q.left ? -p.c * softplus(p.decay[q.c0 + cl + c]) : 0.f;
-    }
-  };
-
   if (ALIGN == kTma && threadIdx.x == 0) {
-    tc::mbar_init(full, 1);
-    tc::mbar_init(full + 1, 1);
+    tc::mbar_init(s.full, 1);
+    tc::mbar_init(s.full + 1, 1);
     tc::fence_mbar_init();
   }
+  if (threadIdx.x < 4) s.odd[threadIdx.x / 2][threadIdx.x % 2] = 0;
   if (warp == 0) {
-    fetch(blockIdx.x - gridDim.x, 0);
+    fetch_forward(p, s, blockIdx.x - gridDim.x, 0);
     __syncwarp();
-    fetch(blockIdx.x, 1);
+    fetch_forward(p, s, blockIdx.x, 1);
   }
   __syncthreads();
-  load(places[0], 0);
-  for (int it = 0;; ++it) {
-    const int slot = it & 1;
-    const Place q = places[slot];
+  load(s.places[0], 0);
+  for (int it = 0, turn = 0;; ++it) {
+    const int slot = it & 1, here = turn, next = here == 2 ? 0 : here + 1;
+    turn = next;
+    const Place& q = s.places[here];
     if (q.tile >= p.tiles) break;
-    load(places[slot ^ 1], slot ^ 1);
+    load(s.places[next], slot ^ 1);
     if constexpr (ALIGN == kTma) {
-      tma_wait(full + slot, (it >> 1) & 1, p.hdr);
+      tma_wait(s.full + slot, (it >> 1) & 1, p.hdr);
     } else {
       cp_async_wait<1>();
       __syncwarp();
     }
-    const float2 rate = make_float2(rates[slot][cl], rates[slot][cl + kCpl - 1]);
+    const float2 rate = make_float2(s.rates[here][cl], s.rates[here][cl + kCpl - 1]);
+    // whether a channel of the tile can decay faster than e^-1/4 a step: the same for all warps
     const bool far = __any_sync(0xffffffffu, fminf(rate.x, rate.y) < -kNear);
-    const int64_t steps = p.T - q.t0 - warp * SPW;   // of this warp's that lie inside
+    const int steps = (int)p.T - (int)q.t0 - warp * SPW;   // of this warp's that lie inside; SPW or more: all
+    const int inside = min(SPW, max(0, steps));
 
     const unsigned char* rows = smem + slot * kStage + warp * kWarpBytes;
-    float2 w[kPairs], b[kPairs];
-    auto coefficients = [&](auto far_c) {
+    float2 dec[kPairs], b[kPairs];
+    auto first = [&](auto form) {   // the steps and their map
+      constexpr int F = decltype(form)::value;
+      constexpr bool kFar = F == kMixed;
+      float2 l = make_float2(0.f, 0.f);   // their log decays together
 #pragma unroll
       for (int k = 0; k < kPairs; ++k) {
-        const float2 r = rcp2(one_plus_exp2(pair_at(rows + kArray, k, lane, T())));
-        w[k] = expm1_neg2<decltype(far_c)::value>(fp::mul2(rate, r));
+        const float2 lk = log_decay<kFar>(rate, rcp2(one_plus_exp2(pair_at(rows + kArray, k, lane, T()))));
+        l = fp::add2(l, lk);
+        dec[k] = decay<kFar>(lk);
         // m i = sqrt(u) / d = u / sqrt(u d^2), u = 1 - a^2, d = 1 / i: one special function, not two.
         // Where d^2 overflows (i < 2^-64), m i is taken as 0.
         const float2 d = one_plus_exp2(pair_at(rows + 2 * kArray, k, lane, T()));
-        const float2 u = one_minus_a2(w[k]);                // at least kTiny:
+        const float2 u = one_minus_a2<kFar>(dec[k]);
         const float2 v = fp::mul2(fp::mul2(u, d), d);       // never 0, nor 0 * inf
         const float2 mi = fp::mul2(u, make_float2(rsqrt_approx(v.x), rsqrt_approx(v.y)));
         b[k] = fp::mul2(mi, pair_at(rows, k, lane, T()));
       }
-    };
-    if (far) coefficients(std::true_type());
-    else coefficients(std::false_type());
-    if (steps < SPW) {   // steps past the end change nothing
-      Walk<T, SPW>::cut(w, steps);
-      Walk<T, SPW>::cut(b, steps);
-    }
-    {
-      float2 W, H;
-      Walk<T, SPW>::compose(w, b, W, H);
-      maps[warp][cl] = make_float2(W.x, H.x);
-      if (kCpl == 2) maps[warp][cl + kCpl - 1] = make_float2(W.y, H.y);
-    }
-    __syncthreads();   // A: the warps' maps are there; everyone is done with this stage's rows
-    if (warp == 0) {
-      float W[kCpl], H[kCpl], h[kCpl];
-#pragma unroll
-      for (int c = 0; c < kCpl; ++c) {
-        W[c] = H[c] = 0.f;
-#pragma unroll
-        for (int k = 0; k < NW; ++k) {
-          const float2 m = maps[k][cl + c];
-          H[c] = lookback::apply(m.x, m.y, H[c]);
-          W[c] = lookback::apply(m.x, m.x, W[c]);
-        }
+      if (steps < SPW) {   // steps past the end change nothing; nobody needs the maps of such warps
+        Walk<T, SPW>::cut(dec, steps, -kTiny);
+        Walk<T, SPW>::cut(b, steps, 0.f);
       }
+      if constexpr (kCpl == 1) l = dup(l.x + l.y);
+      l = fp::add2(l, dup(-kTiny));   // maps are of the mixed form
+      const float2 all = decay<true>(l);
+      float2 H = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kPairs; ++k) H = Walk<T, SPW>::template next<F>(dec[k], b[k], H);
+      s.maps[warp][cl] = make_float2(all.x, H.x);
+      s.logs[warp][cl] = l.x;
+      if (kCpl == 2) {
+        s.maps[warp][cl + kCpl - 1] = make_float2(all.y, H.y);
+        s.logs[warp][cl + kCpl - 1] = l.y;
+      }
+      if (huge2(kCpl == 2 ? H : dup(H.x))) s.odd[slot][0] = 1;
+    };
+    if (far) first(std::integral_constant<int, kMixed>());
+    else first(std::integral_constant<int, kSlow>());
+    __syncthreads();   // A: the warps' maps are there; everyone is done with this stage's rows
+    if (rarely(s.odd[slot][0] != 0)) {
+      odd_forward<T, ALIGN>(p, s, smem + slot * kStage, slot, here, true, it == 0);
+      continue;
+    }
+    if (warp == 0) {
+      float A[kCpl], H[kCpl], h[kCpl];
+      block_map<NW, kCpl, false>(s.maps, s.logs, cl, A, H);
       if (it == 0) wait_for_words();
       uint64_t* words = p.words + q.word + cl;
       const bool last = q.ti == p.ntile - 1;
@@ -426,35 +663,28 @@ __global__ void __launch_bounds__(32 * Forward<T>::kNw, Forward<T>::kBlocks) rec
       } else {
         if (!last) {
 #pragma unroll
-          for (int c = 0; c < kCpl; ++c) v[c] = lookback::word(W[c], H[c], lookback::kMap);
+          for (int c = 0; c < kCpl; ++c) v[c] = lookback::map(A[c], H[c]);
           lookback::publish(words, v);
         }
         lookback::state_before<8>(words - kCh, -kCh, q.ti, h, p.hdr, 400);
       }
       if (!last) {
 #pragma unroll
-        for (int c = 0; c < kCpl; ++c)
-          v[c] = lookback::word(0.f, lookback::apply(W[c], H[c], h[c]), lookback::kInclusive);
+        for (int c = 0; c < kCpl; ++c) v[c] = lookback::inclusive(lookback::apply_safe(A[c], H[c], h[c]));
         lookback::publish(words, v);
       }
-#pragma unroll
-      for (int c = 0; c < kCpl; ++c) {
-#pragma unroll
-        for (int k = 0; k < NW; ++k) {
-          before[k][cl + c] = h[c];
-          const float2 m = maps[k][cl + c];
-          h[c] = lookback::apply(m.x, m.y, h[c]);
-        }
-        if (p.final_state && last && cl + c < q.left) {
-          const int64_t at = q.b * p.D + q.c0 + cl + c;
-          if (SSD_INDEX_OK(p.hdr, at, p.batch * p.D, 62)) p.final_state[at] = h[c];
-        }
-      }
+      if (huge2(make_float2(h[0], h[kCpl - 1]))) s.odd[slot][1] = 1;
+      block_states<NW, kCpl, false>(s.maps, s.before, cl, h);
     } else if (warp == 1) {
-      fetch(places[slot ^ 1].tile, slot);
+      fetch_forward(p, s, s.places[next].tile, next == 2 ? 0 : next + 1);
+      if (lane < 2) s.odd[slot ^ 1][lane] = 0;
     }
     __syncthreads();   // B: the states before the warps' steps are there, and the tile after the next
-    float2 h = make_float2(before[warp][cl], before[warp][cl + kCpl - 1]);
+    if (rarely(s.odd[slot][1] != 0)) {
+      odd_forward<T, ALIGN>(p, s, smem + slot * kStage, slot, here, false, false);
+      continue;
+    }
+    float2 h = make_float2(s.before[warp][cl], s.before[warp][cl + kCpl - 1]);
     const int n = min(kCpl, max(0, q.left - cl));   // this lane's channels that lie inside
     if (p.states_out && warp * SPW % kChunk == 0 && steps > 0) {
       const int64_t at = (q.b * p.nch + (q.t0 + warp * SPW) / kChunk) * p.D + q.c0 + cl;
@@ -464,31 +694,41 @@ __global__ void __launch_bounds__(32 * Forward<T>::kNw, Forward<T>::kBlocks) rec
       }
     }
     const int64_t row0 = (q.b * p.T + q.t0 + warp * SPW) * p.D + q.c0 + cl;
-    T* y = static_cast<T*>(p.y) + row0;
-    const int live = p.y && n > 0 ? (int)min((int64_t)SPW, max((int64_t)0, steps)) : 0;   // steps to write
-    auto walk = [&](auto whole) {
-      auto store = [&](int s, float v0, float v1) {
+    const int live = p.y && n > 0 ? inside : 0;   // steps to write
+    const bool ends = p.final_state && n > 0 && steps > 0 && steps <= SPW;   // the last step is this warp's
+    auto walk = [&](auto whole, auto form) {
+      T* y = static_cast<T*>(p.y) + row0;
+      auto store = [&](int t, float v0, float v1) {
         const float v[2] = {v0, v1};
-        if ((decltype(whole)::value || s < live) &&
-            SSD_INDEX_OK(p.hdr, row0 + s * p.D + n - 1, p.batch * p.T * p.D, 61))
+        if ((decltype(whole)::value || t < live) &&
+            SSD_INDEX_OK(p.hdr, row0 + t * p.D + n - 1, p.batch * p.T * p.D, 61))
           store_row<ALIGN>(y, v, n);
         y += p.D;
       };
 #pragma unroll
       for (int k = 0; k < kPairs; ++k) {
+        h = Walk<T, SPW>::template next<decltype(form)::value>(dec[k], b[k], h);
         if constexpr (kCpl == 2) {
-          h = lookback::apply(w[k], b[k], h);
           store(k, h.x, h.y);
         } else {
-          h.y = lookback::apply(w[k].x, b[k].x, h.x);
           store(2 * k, h.y, 0.f);
-          h.x = lookback::apply(w[k].y, b[k].y, h.y);
           store(2 * k + 1, h.x, 0.f);
         }
       }
     };
-    if (live == SPW) walk(std::true_type());
-    else if (live > 0) walk(std::false_type());
+    auto second = [&](auto form) {
+      if (live == SPW) walk(std::true_type(), form);
+      else if (live > 0 || ends) walk(std::false_type(), form);
+    };
+    if (far) second(std::integral_constant<int, kMixed>());
+    else second(std::integral_constant<int, kSlow>());
+    if (ends) {
+      const int64_t at = q.b * p.D + q.c0 + cl;
+      if (SSD_INDEX_OK(p.hdr, at + n - 1, p.batch * p.D, 62)) {
+        p.final_state[at] = h.x;
+        if (n == 2) p.final_state[at + 1] = h.y;
+      }
+    }
   }
   cp_async_wait_all();
   finish_tickets(p);
@@ -499,48 +739,203 @@ __global__ void __launch_bounds__(32 * Forward<T>::kNw, Forward<T>::kBlocks) rec
 //
 // The same tiles, from the last to the first; a tile's state comes from the states that the forward
 // kept (one a tile), so only dL/dh is carried by look-back: C = a G, the gradient that a tile hands
-// to the step before it, maps to C + W C + Q over a tile with the same W as the forward's.  A warp
+// to the step before it, maps to a C + Q over a tile with the same decay a as the forward's.  A warp
 // forms the forward maps of its steps, takes the state before them, walks them forward for
 //   mi = m i,  xi = mi x (1 - i),  kr = a (h_{t-1} - a i x / m) r,  r   (kept in registers)
 // and composes the reverse map; with C known a walk backwards gives G and writes
-//   dx = G mi, dgate_x = G xi, dgate_a = -rate G kr (1 - r)   and sums G kr for ddecay.
+//   dx = G mi, dgate_x = G xi, dgate_a = rate G kr (1 - r)   and sums G kr for ddecay.
 // ddecay: one partial row per tile, added in tile order by rec_ddecay_kernel.
 //
-// 8 x 4096 x 2048 bf16: 215 us, 4.4 TB/s of 944 MB (65 % of the measured copy rate): five values are kept
-// for every step and channel, so 128 registers a thread and two blocks an SM, which issue 62
+// 8 x 4096 x 2048 bf16: 227 us, 4.2 TB/s of 944 MB (61 % of the measured copy rate): five values are kept
+// for every step and channel, so 128 registers a thread (none spilled) and two blocks an SM, which issue 63
 // instructions a value half of the time and wait for their block's barriers and look-back otherwise.
 // ------------------------------------------------------------------------------------------------
 constexpr int kSpwBwd = 8;
 static_assert(kWarps * kSpwBwd == kChunk, "a backward tile starts from one kept state");
 
+template <typename T>
+struct BackwardShared {
+  static constexpr int kCh = Tile<T>::kCh;
+  float2 maps[kWarps][kCh];   // forward (c, H) of every warp's steps
+  float2 back[kWarps][kCh];   // reverse (c, Q)
+  float logs[kWarps][kCh];    // their log decays together
+  float after[kWarps][kCh];   // C from the step after every warp's steps
+  float sums[kWarps][kCh];    // G kr over every warp's steps
+  float rates[3][kCh];        // -c softplus(decay)
+  float start[3][kCh];        // the kept state
+  int64_t partial_at;         // where the tile before has its row of ddecay partials,
+  int partial_left;           // and how many of its channels lie inside (warp 2's)
+  Place places[3];            // of the tile in hand, the one being loaded and the one after it
+  int odd[2][2];              // the tile has huge values: in its maps, in what its warps start from
+  uint64_t full[2];           // TMA: a stage's boxes have landed
+};
+// By one warp: a tile's place, its channels' rates and the state before it.
+template <typename T>
+__device__ __forceinline__ void fetch_backward(const RecParams& p, BackwardShared<T>& s, uint32_t last, int turn) {
+  constexpr int kCpl = Tile<T>::kCpl;
+  const int lane = threadIdx.x % 32, cl = lane * kCpl;
+  uint32_t tile = last + gridDim.x;
+  if (p.ticket) {
+    if (lane == 0) tile = atomicAdd(p.ticket, 1u);
+    tile = __shfl_sync(0xffffffffu, tile, 0);
+  }
+  const Place q = place<T, kChunk, true>(p, tile);
+  if (lane == 0) s.places[turn] = q;
+  if (tile < p.tiles) {
+    const float* kept = p.states_in + (q.b * p.nch + q.ti) * p.D + q.c0;
+#pragma unroll
+    for (int c = 0; c < kCpl; ++c) {
+      const bool in = cl + c < q.left;
+      s.rates[turn][cl + c] = in ? -p.c * softplus(p.decay[q.c0 + cl + c]) : 0.f;
+      s.start[turn][cl + c] = in ? kept[cl + c] : 0.f;
+    }
+  }
+}
+// By warp 2, once everyone's sums of a tile are there: its row of ddecay partials.
+template <typename T>
+__device__ __forceinline__ void write_partial(const RecParams& p, const BackwardShared<T>& s) {
+  constexpr int kCpl = Tile<T>::kCpl;
+  const int cl = threadIdx.x % 32 * kCpl;
+  const int64_t at = s.partial_at + cl;
+#pragma unroll
+  for (int c = 0; c < kCpl; ++c) {
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) v += s.sums[k][cl + c];
+    if (cl + c < s.partial_left && SSD_INDEX_OK(p.hdr, at + c, p.batch * p.nch * p.D, 65)) p.partial[at + c] = v;
+  }
+}
+
+// The rest of a tile with huge values, as odd_forward.  Returns the warp's sum of G kr.
+template <typename T, int ALIGN>
+__device__ __noinline__ float2 odd_backward(const RecParams& p, BackwardShared<T>& s, const unsigned char* stage,
+                                            int slot, int turn, bool maps, bool first) {
+  constexpr int SPW = kSpwBwd, kCh = Tile<T>::kCh, kCpl = Tile<T>::kCpl;
+  constexpr int kWarpBytes = SPW * kRowBytes, kArray = kWarps * kWarpBytes;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, cl = lane * kCpl;
+  const Place q = s.places[turn];
+  const float2 rate = make_float2(s.rates[turn][cl], s.rates[turn][cl + kCpl - 1]);
+  const int steps = (int)p.T - (int)q.t0 - warp * SPW, inside = min(SPW, max(0, steps));
+  const unsigned char* rows = stage + warp * kWarpBytes;
+  if (maps) {
+    float2 H = make_float2(0.f, 0.f), Q = H;
+#pragma unroll 1
+    for (int k = 0; k < inside; ++k) {
+      const Step v = step_at<T, true>(rows + k * kRowBytes, kArray, lane, rate);
+      H = step<kSafe>(v.c, fp::mul2(v.mi, v.x), H);
+    }
+#pragma unroll 1
+    for (int k = inside - 1; k >= 0; --k) {
+      const Step v = step_at<T, true>(rows + k * kRowBytes, kArray, lane, rate);
+      Q = decayed<kSafe>(v.c, fp::add2(v.dy, Q));
+    }
+    s.maps[warp][cl].y = H.x;
+    s.back[warp][cl].y = Q.x;
+    if (kCpl == 2) {
+      s.maps[warp][cl + kCpl - 1].y = H.y;
+      s.back[warp][cl + kCpl - 1].y = Q.y;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      float A[kCpl], R[kCpl], C[kCpl];
+      block_map<kWarps, kCpl, true>(s.back, s.logs, cl, A, R);
+      const float2 all = safe_state<kWarps, kCpl, true>(s.back, cl, kWarps, make_float2(0.f, 0.f));
+      R[0] = all.x;
+      R[kCpl - 1] = kCpl == 2 ? all.y : all.x;
+      if (first) wait_for_words();
+      uint64_t* words = p.words + q.word + cl;
+      uint64_t v[kCpl];
+      if (q.ti == p.ntile - 1) {
+#pragma unroll
+        for (int c = 0; c < kCpl; ++c)
+          C[c] = p.dfinal && cl + c < q.left ? p.dfinal[q.b * p.D + q.c0 + cl + c] : 0.f;
+      } else {
+        if (q.ti > 0) {
+#pragma unroll
+          for (int c = 0; c < kCpl; ++c) v[c] = lookback::map(A[c], R[c]);
+          lookback::publish(words, v);
+        }
+        lookback::state_before<1>(words + kCh, kCh, p.ntile - 1 - q.ti, C, p.hdr, 401);
+      }
+      if (q.ti > 0) {
+#pragma unroll
+        for (int c = 0; c < kCpl; ++c) v[c] = lookback::inclusive(lookback::apply_safe(A[c], R[c], C[c]));
+        lookback::publish(words, v);
+      }
+      s.after[kWarps - 1][cl] = C[0];
+      if (kCpl == 2) s.after[kWarps - 1][cl + kCpl - 1] = C[kCpl - 1];
+    } else if (warp == 1) {
+      const int next = turn == 2 ? 0 : turn + 1;
+      fetch_backward(p, s, s.places[next].tile, next == 2 ? 0 : next + 1);
+      if (lane < 2) s.odd[slot ^ 1][lane] = 0;
+    } else if (warp == 2 && !first) {
+      write_partial(p, s);
+    }
+    __syncthreads();
+  }
+  float2 prev[SPW], sum = make_float2(0.f, 0.f);
+  float2 h = safe_state<kWarps, kCpl, false>(s.maps, cl, warp, make_float2(s.start[turn][cl], s.start[turn][cl + kCpl - 1]));
+  float2 C = safe_state<kWarps, kCpl, true>(s.back, cl, kWarps - 1 - warp,
+                                            make_float2(s.after[kWarps - 1][cl], s.after[kWarps - 1][cl + kCpl - 1]));
+  const int n = min(kCpl, max(0, q.left - cl)), live = n > 0 ? inside : 0;
+  const int64_t row0 = (q.b * p.T + q.t0 + warp * SPW) * p.D + q.c0 + cl;
+#pragma unroll 1
+  for (int k = 0; k < live; ++k) {
+    const Step v = step_at<T, true>(rows + k * kRowBytes, kArray, lane, rate);
+    prev[k] = h;
+    h = step<kSafe>(v.c, fp::mul2(v.mi, v.x), h);
+  }
+#pragma unroll 1
+  for (int k = live - 1; k >= 0; --k) {
+    const Step v = step_at<T, true>(rows + k * kRowBytes, kArray, lane, rate);
+    const float2 G = fp::add2(v.dy, C);
+    C = decayed<kSafe>(v.c, G);
+    const float2 kr = decayed<kSafe>(v.c, fp::fma2(prev[k], v.r, neg2(v.io)));
+    const float2 vx = fp::mul2(G, v.mi), vg = fp::mul2(G, v.xi);
+    const float2 va = fp::mul2(G, fp::mul2(fp::mul2(rate, kr), fp::fma2(v.r, dup(-1.f), dup(1.f))));
+    if (kCpl == 2 || k % 2 == 0) sum.x = fmaf(G.x, kr.x, sum.x);   // in the order of the other forms
+    if (kCpl == 2 || k % 2 == 1) sum.y = fmaf(G.y, kr.y, sum.y);
+    const int64_t at = row0 + k * p.D;
+    if (SSD_INDEX_OK(p.hdr, at + n - 1, p.batch * p.T * p.D, 63)) {
+      const float x2[2] = {vx.x, vx.y}, a2[2] = {va.x, va.y}, g2[2] = {vg.x, vg.y};
+      store_row<ALIGN>(static_cast<T*>(p.dx) + at, x2, n);
+      store_row<ALIGN>(static_cast<T*>(p.dga) + at, a2, n);
+      store_row<ALIGN>(static_cast<T*>(p.dgx) + at, g2, n);
+    }
+  }
+  if (warp == 0 && p.dinit && q.ti == 0 && n > 0) {
+    const int64_t at = q.b * p.D + q.c0 + cl;
+    if (SSD_INDEX_OK(p.hdr, at + n - 1, p.batch * p.D, 64)) {
+      p.dinit[at] = C.x;
+      if (n == 2) p.dinit[at + 1] = C.y;
+    }
+  }
+  __syncthreads();   // the rows and maps are read no more
+  return sum;
+}
+
 template <typename T, int ALIGN, int MINB>
 __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(const __grid_constant__ RecParams p) {
-  constexpr int SPW = kSpwBwd, kSteps = kWarps * SPW, kCh = Tile<T>::kCh, kCpl = Tile<T>::kCpl;
+  constexpr int SPW = kSpwBwd, kCh = Tile<T>::kCh, kCpl = Tile<T>::kCpl;
   constexpr int kPairs = Walk<T, SPW>::kPairs, kWarpBytes = SPW * kRowBytes, kArray = kWarps * kWarpBytes;
   constexpr int kStage = 4 * kArray;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ float2 maps[kWarps][kCh];      // forward (W, H) of every warp's steps
-  __shared__ float2 back[kWarps][kCh];      // reverse (W, Q)
-  __shared__ float after[kWarps][kCh];      // C from the step after every warp's steps
-  __shared__ float sums[kWarps][kCh];       // G kr over every warp's steps
-  __shared__ float rates[2][kCh], start[2][kCh];   // -c softplus(decay), the kept state
-  __shared__ Place places[2];
-  __shared__ uint64_t full[2];   // TMA: a stage's boxes have landed
+  __shared__ BackwardShared<T> s;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int cl = lane * kCpl;
 
   auto load = [&](const Place& q, int stage) {
     if constexpr (ALIGN == kTma) {
-      if (threadIdx.x == 0 && q.tile < p.tiles) tma_load<4>(smem + stage * kStage, p, full + stage, q, kArray);
+      if (threadIdx.x == 0 && q.tile < p.tiles) tma_load<4>(smem + stage * kStage, p, s.full + stage, q, kArray);
       return;
     }
     if (q.tile < p.tiles) {
       const int64_t t = q.t0 + warp * SPW;
       const int rows = (int)min((int64_t)SPW, max((int64_t)0, p.T - t)), bytes = q.left * (int)sizeof(T);
       unsigned char* d = smem + stage * kStage + warp * kWarpBytes;
-      auto at = [&](const void* base, const int64_t (&s)[2]) {
+      auto at = [&](const void* base, const int64_t (&stride)[2]) {
         return static_cast<const unsigned char*>(base) +
-               (rows > 0 ? (q.b * s[0] + t * s[1] + q.c0) * (int64_t)sizeof(T) : 0);
+               (rows > 0 ? (q.b * stride[0] + t * stride[1] + q.c0) * (int64_t)sizeof(T) : 0);
       };
       load_rows<SPW, ALIGN>(d, at(p.x, p.xs), p.xs[1] * sizeof(T), rows, bytes, lane);
       load_rows<SPW, ALIGN>(d + kArray, at(p.ga, p.as), p.as[1] * sizeof(T), rows, bytes, lane);
@@ -549,142 +944,117 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(const __gr
     }
     cp_async_commit();
   };
-  auto fetch = [&](uint32_t last, int slot) {   // by one warp
-    uint32_t tile = last + gridDim.x;
-    if (p.ticket) {
-      if (lane == 0) tile = atomicAdd(p.ticket, 1u);
-      tile = __shfl_sync(0xffffffffu, tile, 0);
-    }
-    const Place q = place<T, kSteps, true>(p, tile);
-    if (lane == 0) places[slot] = q;
-    if (tile < p.tiles) {
-      const float* s = p.states_in + (q.b * p.nch + q.ti) * p.D + q.c0;
-#pragma unroll
-      for (int c = 0; c < kCpl; ++c) {
-        const bool in = cl + c < q.left;
-        rates[slot][cl + c] = in ? -p.c * softplus(p.decay[q.c0 + cl + c]) : 0.f;
-        start[slot][cl + c] = in ? s[cl + c] : 0.f;
-      }
-    }
-  };
-  // by one warp, once everyone's sums of the tile before are there: its row of ddecay partials
-  auto write_partial = [&](int64_t at, int left) {
-#pragma unroll
-    for (int c = 0; c < kCpl; ++c) {
-      float v = 0.f;
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k) v += sums[k][cl + c];
-      if (cl + c < left && SSD_INDEX_OK(p.hdr, at + c, p.batch * p.nch * p.D, 65)) p.partial[at + c] = v;
-    }
-  };
-
   if (ALIGN == kTma && threadIdx.x == 0) {
-    tc::mbar_init(full, 1);
-    tc::mbar_init(full + 1, 1);
+    tc::mbar_init(s.full, 1);
+    tc::mbar_init(s.full + 1, 1);
     tc::fence_mbar_init();
   }
+  if (threadIdx.x < 4) s.odd[threadIdx.x / 2][threadIdx.x % 2] = 0;
   if (warp == 0) {
-    fetch(blockIdx.x - gridDim.x, 0);
+    fetch_backward(p, s, blockIdx.x - gridDim.x, 0);
     __syncwarp();
-    fetch(blockIdx.x, 1);
+    fetch_backward(p, s, blockIdx.x, 1);
   }
   __syncthreads();
-  load(places[0], 0);
-  int64_t partial_at = 0;
-  int partial_left = 0;
-  for (int it = 0;; ++it) {
-    const int slot = it & 1;
-    const Place q = places[slot];
+  load(s.places[0], 0);
+  if (threadIdx.x == 64) s.partial_left = 0;
+  for (int it = 0, turn = 0;; ++it) {
+    const int slot = it & 1, here = turn, next = here == 2 ? 0 : here + 1;
+    turn = next;
+    const Place& q = s.places[here];
     if (q.tile >= p.tiles) break;
     if constexpr (ALIGN == kTma) {
-      tma_wait(full + slot, (it >> 1) & 1, p.hdr);
+      tma_wait(s.full + slot, (it >> 1) & 1, p.hdr);
     } else {
       // The stage that is filled now held the tile before, whose dy the walk at its end read: a lane's
       // copies cover rows that other lanes read, so every lane of the warp has to be through.
       __syncwarp();
-      load(places[slot ^ 1], slot ^ 1);
+      load(s.places[next], slot ^ 1);
       cp_async_wait<1>();
       __syncwarp();
     }
-    const float2 rate = make_float2(rates[slot][cl], rates[slot][cl + kCpl - 1]);
-    const bool far = __any_sync(0xffffffffu, fminf(rate.x, rate.y) < -kNear);
-    const float2 h0 = make_float2(start[slot][cl], start[slot][cl + kCpl - 1]);
-    const int64_t steps = p.T - q.t0 - warp * SPW;
+    const float2 rate = make_float2(s.rates[here][cl], s.rates[here][cl + kCpl - 1]);
+    const bool far = __any_sync(0xffffffffu, fminf(rate.x, rate.y) < -kNear);   // as in the forward
+    const float2 h0 = make_float2(s.start[here][cl], s.start[here][cl + kCpl - 1]);
+    const int steps = (int)p.T - (int)q.t0 - warp * SPW, inside = min(SPW, max(0, steps));
 
     const unsigned char* rows = smem + slot * kStage + warp * kWarpBytes;
-    // kr holds a i x / m, what h_{t-1} is compared with, until the state is known; where r is 0, so is kr
-    float2 w[kPairs], mi[kPairs], xi[kPairs], kr[kPairs], r[kPairs];
-    auto coefficients = [&](auto far_c) {
+    // kr holds a i x r / m, what h_{t-1} r is compared with, until the state is known (r / m does not overflow)
+    float2 dec[kPairs], mi[kPairs], xi[kPairs], kr[kPairs], r[kPairs];
+    auto first = [&](auto form) {   // the steps and their maps
+      constexpr int F = decltype(form)::value;
+      constexpr bool kFar = F == kMixed;
+      float2 l = make_float2(0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < kPairs; ++k) {
         r[k] = rcp2(one_plus_exp2(pair_at(rows + kArray, k, lane, T())));
-        w[k] = expm1_neg2<decltype(far_c)::value>(fp::mul2(rate, r[k]));
+        const float2 lk = log_decay<kFar>(rate, r[k]);
+        l = fp::add2(l, lk);
+        dec[k] = decay<kFar>(lk);
         const float2 i = rcp2(one_plus_exp2(pair_at(rows + 2 * kArray, k, lane, T())));
-        const float2 u = one_minus_a2(w[k]);
+        const float2 u = one_minus_a2<kFar>(dec[k]);
         const float2 over = make_float2(rsqrt_approx(u.x), rsqrt_approx(u.y));   // 1 / m, at most 1e18
         const float2 ix = fp::mul2(i, pair_at(rows, k, lane, T()));
         const float2 m = fp::mul2(u, over);
         mi[k] = fp::mul2(m, i);
         xi[k] = fp::mul2(fp::mul2(m, ix), fp::fma2(i, dup(-1.f), dup(1.f)));
-        const float2 io = fp::mul2(ix, over);
-        kr[k] = fp::fma2(w[k], io, io);
+        kr[k] = decayed<F>(dec[k], fp::mul2(ix, fp::mul2(over, r[k])));
       }
-    };
-    if (far) coefficients(std::true_type());
-    else coefficients(std::false_type());
-    if (steps < SPW) {   // steps past the end change nothing (their x and dy are zeros)
-      Walk<T, SPW>::cut(w, steps);
-      Walk<T, SPW>::cut(mi, steps);
-      Walk<T, SPW>::cut(r, steps);
-    }
-    {
-      float2 W = make_float2(0.f, 0.f), H = W, Q = W;
+      if (steps < SPW) {   // steps past the end change nothing (their x and dy are zeros)
+        Walk<T, SPW>::cut(dec, steps, -kTiny);
+        Walk<T, SPW>::cut(mi, steps, 0.f);
+        Walk<T, SPW>::cut(r, steps, 0.f);
+        l = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k) l = fp::add2(l, fp::mul2(rate, r[k]));
+      }
+      if constexpr (kCpl == 1) l = dup(l.x + l.y);
+      l = fp::add2(l, dup(-kTiny));   // maps are of the mixed form
+      float2 H = make_float2(0.f, 0.f), Q = H, all = dup(-kTiny);
 #pragma unroll
       for (int k = 0; k < kPairs; ++k) {
-        const float2 b = fp::mul2(mi[k], pair_at(rows, k, lane, T()));
-        if constexpr (kCpl == 2) {
-          H = lookback::apply(w[k], b, H);
-          W = lookback::apply(w[k], w[k], W);
-        } else {
-          H.x = lookback::apply(w[k].y, b.y, lookback::apply(w[k].x, b.x, H.x));
-          W.x = lookback::apply(w[k].y, w[k].y, lookback::apply(w[k].x, w[k].x, W.x));
-        }
+        H = Walk<T, SPW>::template next<F>(dec[k], fp::mul2(mi[k], pair_at(rows, k, lane, T())), H);
+        if (!kFar) all = Walk<T, SPW>::together(dec[k], all);
       }
+      // eight steps of e^-1/4 are 0.135: the w of all of them still holds their decay to a few units
+      if (kFar) all = decay<true>(l);
+      else all = make_float2(all.x < -kNear ? 1.f + all.x : all.x, all.y < -kNear ? 1.f + all.y : all.y);
       // the reverse map: dy + C enters a step, a (dy + C) leaves it
 #pragma unroll
-      for (int k = kPairs - 1; k >= 0; --k) {
-        const float2 dy = pair_at(rows + 3 * kArray, k, lane, T());
-        if constexpr (kCpl == 2) {
-          const float2 G = fp::add2(dy, Q);
-          Q = fp::fma2(w[k], G, G);
-        } else {
-          const float G1 = dy.y + Q.x, C1 = fmaf(w[k].y, G1, G1), G0 = dy.x + C1;
-          Q.x = fmaf(w[k].x, G0, G0);
-        }
-      }
-      maps[warp][cl] = make_float2(W.x, H.x);
-      back[warp][cl] = make_float2(W.x, Q.x);
+      for (int k = kPairs - 1; k >= 0; --k)
+        Q = Walk<T, SPW>::template before<F>(dec[k], pair_at(rows + 3 * kArray, k, lane, T()), Q);
+      s.maps[warp][cl] = make_float2(all.x, H.x);
+      s.back[warp][cl] = make_float2(all.x, Q.x);
+      s.logs[warp][cl] = l.x;
       if (kCpl == 2) {
-        maps[warp][cl + kCpl - 1] = make_float2(W.y, H.y);
-        back[warp][cl + kCpl - 1] = make_float2(W.y, Q.y);
+        s.maps[warp][cl + kCpl - 1] = make_float2(all.y, H.y);
+        s.back[warp][cl + kCpl - 1] = make_float2(all.y, Q.y);
+        s.logs[warp][cl + kCpl - 1] = l.y;
       }
-    }
+      if (huge2(kCpl == 2 ? H : dup(H.x)) || huge2(kCpl == 2 ? Q : dup(Q.x))) s.odd[slot][0] = 1;
+    };
+    if (far) first(std::integral_constant<int, kMixed>());
+    else first(std::integral_constant<int, kSlow>());
     __syncthreads();   // A: the warps' maps are there, and the sums of the tile before
     // A box replaces a tile that every warp has left only now (its rows are read to the tile's end; a third
     // stage, asked for a tile earlier, took the L1 cache's room: 285 us instead of 215).
-    if constexpr (ALIGN == kTma) load(places[slot ^ 1], slot ^ 1);
-    if (warp == 0) {
-      float W[kCpl], Q[kCpl], C[kCpl];
-#pragma unroll
-      for (int c = 0; c < kCpl; ++c) {
-        W[c] = Q[c] = 0.f;
-#pragma unroll
-        for (int k = kWarps - 1; k >= 0; --k) {
-          const float2 m = back[k][cl + c];
-          Q[c] = lookback::apply(m.x, m.y, Q[c]);
-          W[c] = lookback::apply(m.x, m.x, W[c]);
-        }
+    if constexpr (ALIGN == kTma) load(s.places[next], slot ^ 1);
+    auto put_sum = [&](float2 sum) {
+      s.sums[warp][cl] = sum.x;
+      if (kCpl == 2) s.sums[warp][cl + kCpl - 1] = sum.y;
+      else s.sums[warp][cl] += sum.y;
+      if (threadIdx.x == 64) {
+        s.partial_at = (q.b * p.nch + q.ti) * p.D + q.c0;
+        s.partial_left = q.left;
       }
+    };
+    if (rarely(s.odd[slot][0] != 0)) {
+      put_sum(odd_backward<T, ALIGN>(p, s, smem + slot * kStage, slot, here, true, it == 0));
+      continue;
+    }
+    if (warp == 0) {
+      float A[kCpl], Q[kCpl], C[kCpl];
+      block_map<kWarps, kCpl, true>(s.back, s.logs, cl, A, Q);
       if (it == 0) wait_for_words();
       uint64_t* words = p.words + q.word + cl;
       uint64_t v[kCpl];
@@ -695,66 +1065,73 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(const __gr
       } else {
         if (q.ti > 0) {
 #pragma unroll
-          for (int c = 0; c < kCpl; ++c) v[c] = lookback::word(W[c], Q[c], lookback::kMap);
+          for (int c = 0; c < kCpl; ++c) v[c] = lookback::map(A[c], Q[c]);
           lookback::publish(words, v);
         }
         lookback::state_before<8 / kCpl>(words + kCh, kCh, p.ntile - 1 - q.ti, C, p.hdr, 401);
       }
       if (q.ti > 0) {
 #pragma unroll
-        for (int c = 0; c < kCpl; ++c)
-          v[c] = lookback::word(0.f, lookback::apply(W[c], Q[c], C[c]), lookback::kInclusive);
+        for (int c = 0; c < kCpl; ++c) v[c] = lookback::inclusive(lookback::apply_safe(A[c], Q[c], C[c]));
         lookback::publish(words, v);
       }
+      if (huge2(make_float2(C[0], C[kCpl - 1]))) s.odd[slot][1] = 1;
+      block_states<kWarps, kCpl, true>(s.back, s.after, cl, C);
 #pragma unroll
       for (int c = 0; c < kCpl; ++c) {
-#pragma unroll
-        for (int k = kWarps - 1; k >= 0; --k) {
-          after[k][cl + c] = C[c];
-          const float2 m = back[k][cl + c];
-          C[c] = lookback::apply(m.x, m.y, C[c]);
-        }
         if (p.dinit && q.ti == 0 && cl + c < q.left) {
           const int64_t at = q.b * p.D + q.c0 + cl + c;
           if (SSD_INDEX_OK(p.hdr, at, p.batch * p.D, 64)) p.dinit[at] = C[c];
         }
       }
     } else if (warp == 1) {
-      fetch(places[slot ^ 1].tile, slot);
+      fetch_backward(p, s, s.places[next].tile, next == 2 ? 0 : next + 1);
+      if (lane < 2) s.odd[slot ^ 1][lane] = 0;
     } else if (warp == 2 && it > 0) {
-      write_partial(partial_at, partial_left);
+      write_partial(p, s);
     }
     {   // the state before the warp's steps, and kr of every step
       float2 h = h0;
       for (int k = 0; k < warp; ++k) {
-        const float2 m0 = maps[k][cl], m1 = maps[k][cl + kCpl - 1];
-        h = lookback::apply(make_float2(m0.x, m1.x), make_float2(m0.y, m1.y), h);
+        const float2 m0 = s.maps[k][cl], m1 = s.maps[k][cl + kCpl - 1];
+        h = step<kMixed>(make_float2(m0.x, m1.x), make_float2(m0.y, m1.y), h);
       }
+      if (huge2(h)) s.odd[slot][1] = 1;
+      auto states = [&](auto form) {
+        constexpr int F = decltype(form)::value;
 #pragma unroll
-      for (int k = 0; k < kPairs; ++k) {
-        const float2 b = fp::mul2(mi[k], pair_at(rows, k, lane, T()));
-        float2 prev = h;
-        if constexpr (kCpl == 2) {
-          h = lookback::apply(w[k], b, h);
-        } else {
-          prev.y = lookback::apply(w[k].x, b.x, prev.x);
-          h.x = lookback::apply(w[k].y, b.y, prev.y);
+        for (int k = 0; k < kPairs; ++k) {
+          const float2 b = fp::mul2(mi[k], pair_at(rows, k, lane, T()));
+          float2 prev = h;
+          if constexpr (kCpl == 2) {
+            h = step<F>(dec[k], b, h);
+          } else {
+            prev.y = step<F>(dec[k].x, b.x, prev.x);
+            h.x = step<F>(dec[k].y, b.y, prev.y);
+          }
+          kr[k] = decayed<F>(dec[k], fp::fma2(prev, r[k], neg2(kr[k])));
+          r[k] = fp::mul2(fp::mul2(rate, kr[k]), fp::fma2(r[k], dup(-1.f), dup(1.f)));   // of dgate_a
         }
-        const float2 d = fp::mul2(fp::sub2(prev, kr[k]), r[k]);
-        kr[k] = fp::fma2(w[k], d, d);
-      }
+      };
+      if (far) states(std::integral_constant<int, kMixed>());
+      else states(std::integral_constant<int, kSlow>());
     }
     __syncthreads();   // B: C from the step after every warp's steps
-    float2 C = make_float2(after[warp][cl], after[warp][cl + kCpl - 1]), sum = make_float2(0.f, 0.f);
+    if (rarely(s.odd[slot][1] != 0)) {
+      put_sum(odd_backward<T, ALIGN>(p, s, smem + slot * kStage, slot, here, false, false));
+      continue;
+    }
+    float2 C = make_float2(s.after[warp][cl], s.after[warp][cl + kCpl - 1]), sum = make_float2(0.f, 0.f);
     const int n = min(kCpl, max(0, q.left - cl));
-    const int live = n > 0 ? (int)min((int64_t)SPW, max((int64_t)0, steps)) : 0;
+    const int live = n > 0 ? inside : 0;
     const int64_t row0 = (q.b * p.T + q.t0 + warp * SPW) * p.D + q.c0 + cl;
-    auto walk = [&](auto whole) {
+    auto walk = [&](auto whole, auto form) {
+      constexpr int F = decltype(form)::value;
       const int64_t last = row0 + (SPW - 1) * p.D;
       T *px = static_cast<T*>(p.dx) + last, *pa = static_cast<T*>(p.dga) + last, *pg = static_cast<T*>(p.dgx) + last;
-      auto store = [&](int s, float x0, float x1, float a0, float a1, float g0, float g1) {
-        if ((decltype(whole)::value || s < live) &&
-            SSD_INDEX_OK(p.hdr, row0 + s * p.D + n - 1, p.batch * p.T * p.D, 63)) {
+      auto store = [&](int t, float x0, float x1, float a0, float a1, float g0, float g1) {
+        if ((decltype(whole)::value || t < live) &&
+            SSD_INDEX_OK(p.hdr, row0 + t * p.D + n - 1, p.batch * p.T * p.D, 63)) {
           const float x2[2] = {x0, x1}, a2[2] = {a0, a1}, g2[2] = {g0, g1};
           store_row<ALIGN>(px, x2, n);
           store_row<ALIGN>(pa, a2, n);
@@ -768,16 +1145,14 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(const __gr
         float2 G;
         if constexpr (kCpl == 2) {
           G = fp::add2(dy, C);
-          C = fp::fma2(w[k], G, G);
+          C = decayed<F>(dec[k], G);
         } else {
           G.y = dy.y + C.x;
-          G.x = dy.x + fmaf(w[k].y, G.y, G.y);
-          C.x = fmaf(w[k].x, G.x, G.x);
+          G.x = dy.x + decayed<F>(dec[k].y, G.y);
+          C.x = decayed<F>(dec[k].x, G.x);
         }
-        const float2 e = fp::mul2(G, kr[k]);
-        sum = fp::add2(sum, e);
-        const float2 vx = fp::mul2(G, mi[k]), vg = fp::mul2(G, xi[k]);
-        const float2 va = fp::mul2(fp::mul2(rate, e), fp::fma2(r[k], dup(-1.f), dup(1.f)));
+        sum = fp::fma2(G, kr[k], sum);
+        const float2 vx = fp::mul2(G, mi[k]), vg = fp::mul2(G, xi[k]), va = fp::mul2(G, r[k]);
         if constexpr (kCpl == 2) {
           store(k, vx.x, vx.y, va.x, va.y, vg.x, vg.y);
         } else {
@@ -786,17 +1161,17 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(const __gr
         }
       }
     };
-    if (live == SPW) walk(std::true_type());
-    else walk(std::false_type());
-    if constexpr (kCpl == 1) sum.x += sum.y;
-    sums[warp][cl] = sum.x;
-    if (kCpl == 2) sums[warp][cl + kCpl - 1] = sum.y;
-    partial_at = (q.b * p.nch + q.ti) * p.D + q.c0 + cl;
-    partial_left = q.left;
+    auto second = [&](auto form) {
+      if (live == SPW) walk(std::true_type(), form);
+      else walk(std::false_type(), form);
+    };
+    if (far) second(std::integral_constant<int, kMixed>());
+    else second(std::integral_constant<int, kSlow>());
+    put_sum(sum);
   }
   cp_async_wait_all();
   __syncthreads();
-  if (warp == 2 && partial_left > 0) write_partial(partial_at, partial_left);
+  if (warp == 2 && s.partial_left > 0) write_partial(p, s);
   finish_tickets(p);
 }
 
@@ -862,12 +1237,12 @@ __global__ void __launch_bounds__(128) rec_step_kernel(RecParams p) {
 #pragma unroll
     for (int k = 0; k < P; ++k) {
       auto pair = [&](const Vals<T, V>& v) { return make_float2((float)v.v[2 * k], V > 1 ? (float)v.v[2 * k + (V > 1)] : 0.f); };
-      const float2 w = expm1_neg2<true>(fp::mul2(rate[k], rcp2(one_plus_exp2(pair(ga[u])))));
-      const float2 q = one_minus_a2(w), i = rcp2(one_plus_exp2(pair(gx[u])));
+      const float2 c = decay<true>(log_decay<true>(rate[k], rcp2(one_plus_exp2(pair(ga[u])))));
+      const float2 q = one_minus_a2<true>(c), i = rcp2(one_plus_exp2(pair(gx[u])));
       const float2 m = fp::mul2(q, make_float2(rsqrt_approx(q.x), rsqrt_approx(q.y)));
       float2 s = make_float2(0.f, 0.f);
       if (p.init) s = make_float2(h[u].v[2 * k], V > 1 ? h[u].v[2 * k + (V > 1)] : 0.f);
-      s = lookback::apply(w, fp::mul2(fp::mul2(m, i), pair(x[u])), s);
+      s = step<kSafe>(c, fp::mul2(fp::mul2(m, i), pair(x[u])), s);
       h[u].v[2 * k] = s.x;
       st_from_f32(&y.v[2 * k], s.x);
       if (V > 1) {

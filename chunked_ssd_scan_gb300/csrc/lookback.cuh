@@ -1,12 +1,18 @@
 // Carry of an elementwise linear recurrence along tiles that run on different blocks: a decoupled
-// look-back whose words hold a value and its state together, so that no fence is needed.
+// look-back (Merrill and Garland, Single-pass Parallel Prefix Scan with Decoupled Look-back, 2016) whose
+// words hold a value and its state together, so that no fence is needed.
 //
-// A tile of steps maps the state before it, h, to h + W h + H (W + 1 the product of its decays, kept
-// minus one: W lies in [-1, 0]).  Its word is 64 bits: H in the low half, |W| in the high half,
-// whose two top bits are free (|W| <= 1) and hold the word's state: 0 nothing (the words are
-// cleared before the launch), 1 the tile's own map, 2 inclusive (H is the state after the tile).
-// A reader evaluates the maps from the nearest inclusive word on, oldest first, with the very
-// operations that made the inclusive words: the result has the same bits wherever it starts.
+// A step, or a span of steps, maps the state before it, h, to a h + H.  Its decay a in [0, 1] is kept as one
+// number c: near one as c = a - 1 < 0 (a itself has an absolute rounding error of 2^-25 that a channel with
+// memory 1 / (1 - a) multiplies by that memory), and where a is small as c = a >= 0 (h + ((a - 1) h + H)
+// would leave the rounding of a large h behind, 2^-24 |h|, where a h is long gone).  No decay is exactly
+// one: c <= -kTiny.
+//
+// A tile's word is 64 bits: H in the low half, c, with |c| <= 1, in the high half, whose bit 30 (the top bit of
+// the exponent) is free and set.  Without it the high half is 0 for nothing (the words are cleared before
+// the launch) or 1 for an inclusive word (H is the state after the tile).  A reader evaluates the maps
+// from the nearest inclusive word on, oldest first, with the very operations that made the inclusive
+// words: the result has the same bits wherever it starts.
 #pragma once
 
 #include "common.cuh"
@@ -15,16 +21,21 @@
 namespace ssd {
 namespace lookback {
 
-constexpr uint32_t kMap = 1u, kInclusive = 2u;
+constexpr uint32_t kMap = 1u << 30, kInclusive = 1u;
+constexpr float kInf = __builtin_huge_valf();
 
-__device__ __forceinline__ float apply(float W, float H, float h) { return h + fmaf(W, h, H); }
+// a h + H.  NaN for an infinite h next to one (inf - inf) and where a is 0.
+__device__ __forceinline__ float apply(float c, float H, float h) {
+  return fmaf(c, h, H) + (c < 0.f ? h : 0.f);
+}
+// The same, but an infinite h stays what it is (no decay is zero, if fp32 makes it so).  Where the results of
+// a chain of apply are not NaN, this chain's are the same.
+__device__ __forceinline__ float apply_safe(float c, float H, float h) { return fabsf(h) == kInf ? h + H : apply(c, H, h); }
 
-__device__ __forceinline__ float2 apply(float2 W, float2 H, float2 h) { return fp::add2(h, fp::fma2(W, h, H)); }
-
-__device__ __forceinline__ uint64_t word(float W, float H, uint32_t state) {
-  if (W != W) H = W, W = 0.f;   // a NaN decay: the state after it is NaN whatever came before
-  const uint32_t hi = (__float_as_uint(W) & 0x3fffffffu) | (state << 30);
-  return ((uint64_t)hi << 32) | __float_as_uint(H);
+__device__ __forceinline__ uint64_t inclusive(float h) { return ((uint64_t)kInclusive << 32) | __float_as_uint(h); }
+__device__ __forceinline__ uint64_t map(float c, float H) {
+  if (c != c) H = c, c = 0.f;   // a NaN decay: the state after it is NaN whatever came before
+  return ((uint64_t)(__float_as_uint(c) | kMap) << 32) | __float_as_uint(H);
 }
 
 __device__ __forceinline__ void publish(uint64_t* p, const uint64_t (&v)[1]) {
@@ -50,7 +61,9 @@ __device__ __forceinline__ uint64_t now_ns() {
 // nearest tile before it, `step` the (signed) distance in words to the next older one and `have`
 // how many older tiles there are (at least one).  A try reads the K nearest words at once; the nearest is
 // enough if it is inclusive, and the others are evaluated only once it holds anything.  The wait is
-// bounded (1 s, then SSD_ERR_TIMEOUT is latched and the call's results are void).
+// bounded (1 s, then SSD_ERR_TIMEOUT is latched and the call's results are void).  Maps evaluated behind an
+// infinite state may give a NaN that is none: with a NaN the try is not over before the nearest is
+// inclusive.
 template <int K, int N>
 __device__ __forceinline__ void state_before(const uint64_t* words, int64_t step, int64_t have, float (&h)[N],
                                              WsHeader* hdr, int64_t site) {
@@ -66,14 +79,16 @@ __device__ __forceinline__ void state_before(const uint64_t* words, int64_t step
         for (int c = 0; c < N; ++c) v[j][c] = 0;
       }
     }
-    uint32_t least = kInclusive;   // the nearest words' least state
+    bool known = true, some = true;   // the nearest words are inclusive, hold anything
 #pragma unroll
     for (int c = 0; c < N; ++c) {
-      least = min(least, (uint32_t)(v[0][c] >> 62));
+      const uint32_t hi = (uint32_t)(v[0][c] >> 32);
+      known = known && hi == kInclusive;
+      some = some && hi != 0;
       h[c] = __uint_as_float((uint32_t)v[0][c]);
     }
-    if (__all_sync(0xffffffffu, least == kInclusive)) return;
-    if (__all_sync(0xffffffffu, least != 0)) {
+    if (__all_sync(0xffffffffu, known)) return;
+    if (__all_sync(0xffffffffu, some)) {
       bool all = true;
 #pragma unroll
       for (int c = 0; c < N; ++c) {
@@ -81,13 +96,12 @@ __device__ __forceinline__ void state_before(const uint64_t* words, int64_t step
         h[c] = 0.f;
 #pragma unroll
         for (int j = K - 1; j >= 0; --j) {
-          const uint32_t hi = (uint32_t)(v[j][c] >> 32), state = hi >> 30;
-          const float H = __uint_as_float((uint32_t)v[j][c]);
-          const float W = -__uint_as_float(hi & 0x3fffffffu);
-          h[c] = state == kInclusive ? H : apply(W, H, h[c]);
-          ok = state == kInclusive || (ok && state == kMap);
+          const uint32_t hi = (uint32_t)(v[j][c] >> 32);
+          const float H = __uint_as_float((uint32_t)v[j][c]), a = __uint_as_float(hi & ~kMap);
+          h[c] = hi == kInclusive ? H : apply(a, H, h[c]);
+          ok = hi == kInclusive || (ok && hi != 0);
         }
-        all = all && ok;
+        all = all && ok && h[c] == h[c];
       }
       if (__all_sync(0xffffffffu, all)) return;
     }

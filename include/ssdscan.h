@@ -416,7 +416,12 @@ size_t gated_recurrence_workspace_bytes(const gated_recurrence_shape* shape, int
  * init_state (NULL = zeros), final_state (NULL = not written) [batch, d_model] f32.
  * states: NULL, or f32 [batch, ceil(seqlen / GATED_RECURRENCE_CHUNK), d_model] that receives the
  * state before steps 0, 64, 128, ... for gated_recurrence_backward.  y may be NULL.
- * 1 - a^2 is formed without cancellation, so channels that hardly decay keep their precision.
+ * 1 - a^2 is formed without cancellation, so channels that hardly decay keep their precision; where
+ * a is small the state is multiplied by a itself, so nothing of a large state outlives its decay.
+ * Errors relative to a value are those of fp32 special functions, 2^-22 to 2^-20 each.
+ * Infinities: no decay of finite inputs is zero, so an infinite x or init_state leaves its channel's
+ * state infinite from there on, however small a is; infinities of both signs, and NaN, give NaN from
+ * there on, in their channel only.  (Tiles with NaN or states of 1e30 or more take longer.)
  * Asynchronous on `stream`; INVALID_ARG / UNSUPPORTED / WORKSPACE leave every output untouched.
  */
 ssd_status gated_recurrence_forward(const gated_recurrence_shape* shape, const void* x,
@@ -433,7 +438,7 @@ ssd_status gated_recurrence_forward(const gated_recurrence_shape* shape, const v
  * dy strided io_dtype, dfinal [batch, d_model] f32 (NULL = zero).  states: what the forward kept,
  * or NULL (the call then recomputes them in its workspace, one more pass over x and the gates).
  * Where a gate is so closed that 1 - a^2 is zero in fp32, the gradients through it are zero (their
- * limit).
+ * limit).  An infinite dy or dfinal leaves dL/dh infinite for all steps before it, as above.
  */
 ssd_status gated_recurrence_backward(const gated_recurrence_shape* shape, const void* x,
                                      const void* gate_a, const void* gate_x, const float* decay,
