@@ -46,10 +46,10 @@ __device__ __forceinline__ float softplus(float d) { return fmaxf(d, 0.f) + log1
 // A decay is kept as one number c (lookback.cuh): a - 1 = expm1(l) < 0 next to one, where a step is
 // h + (c h + b), and a itself below e^-1/4, where it is c h + b.  A warp whose channels cannot decay
 // faster than e^-1/4 a step does the first for all its values; others choose value by value (8 x 4096 x
-// 2048 bf16: 112 us forward, 250 us backward, where the first takes 102 and 227).  Both make NaN of an
+// 2048 bf16: 113 us forward, 250 us backward, where the first takes 104 and 227).  Both make NaN of an
 // infinite state next to one (inf - inf): an odd tile, one that meets values of kHuge or more, or NaN, is finished
 // by a function that goes through its steps once more, one by one, in a third form that does not (all tiles
-// odd: 207 us forward).  It is called, not part of the kernels: with its code inline they ran out of
+// odd: 218 us forward).  It is called, not part of the kernels: with its code inline they ran out of
 // registers (forward 145 us).
 constexpr float kInf = lookback::kInf;
 enum Form { kSlow, kMixed, kSafe };
@@ -93,9 +93,9 @@ __device__ __forceinline__ bool rarely(bool v) { return __builtin_expect(v, 0); 
 // block's warps and, by look-back, of earlier tiles give the state before the warp's first step, and a
 // second walk over the registers writes y.  Every input byte is read once.
 //
-// 8 x 4096 x 2048 bf16 with states: 102 us, 5.3 TB/s of 541 MB (78 % of the measured copy rate), with the
+// 8 x 4096 x 2048 bf16 with states: 104 us, 5.2 TB/s of 541 MB (77 % of the measured copy rate), with the
 // special-function unit (4 a value) and the issue slots (33 instructions a value) each busy more than half
-// of the time; 1 x 131072 x 1024 f32: 357 us, 6.0 TB/s (89 %).
+// of the time; 1 x 131072 x 1024 f32: 359 us, 6.0 TB/s (89 %).
 // ------------------------------------------------------------------------------------------------
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
@@ -364,6 +364,19 @@ __device__ __forceinline__ float2 safe_state(const M& maps, int cl, int count, f
   return h;
 }
 
+// Whether a lane's rows hold an input gate so closed that its 1 / i overflows when squared, but not so that i is 0.
+template <typename T, int ROWS>
+__device__ __forceinline__ bool hardly_open(const unsigned char* rows, int lane) {
+  bool any = false;
+#pragma unroll 1
+  for (int k = 0; k < ROWS; ++k) {
+    const unsigned char* row = rows + k * kRowBytes;
+    const float2 g = Tile<T>::kCpl == 2 ? pair_at(row, 0, lane, __nv_bfloat16()) : dup(reinterpret_cast<const float*>(row)[lane]);
+    any = any || (g.x < -44.f && g.x > -89.f) || (g.y < -44.f && g.y > -89.f);   // 2^64 = e^44.4, 2^128 = e^88.7
+  }
+  return any;
+}
+
 // A step formed from its row in shared memory (of x, gate_a, gate_x and, in the backward, dy), in the third form.
 struct Step {
   float2 x, dy, c, mi, xi, io, r;
@@ -382,10 +395,10 @@ __device__ __forceinline__ Step step_at(const unsigned char* row, int array, int
   const float2 u = one_minus_a2<true>(v.c), over = make_float2(rsqrt_approx(u.x), rsqrt_approx(u.y));
   const float2 m = fp::mul2(u, over);
   v.mi = fp::mul2(m, i);
-  if (!kBackward) {   // as in the forward's other forms
+  if (!kBackward) {   // as in the forward's other forms, while that is good
     const float2 d2 = fp::mul2(fp::mul2(u, d), d);
     const float2 mi = fp::mul2(u, make_float2(rsqrt_approx(d2.x), rsqrt_approx(d2.y)));
-    v.mi = mi;
+    v.mi = make_float2(d2.x < kInf ? mi.x : v.mi.x, d2.y < kInf ? mi.y : v.mi.y);
   } else {
     const float2 ix = fp::mul2(i, v.x);
     v.dy = at(3);
@@ -397,7 +410,7 @@ __device__ __forceinline__ Step step_at(const unsigned char* row, int array, int
 
 // NW warps of 16 steps.  Half as many blocks of 8 warps wait for the look-back together, so bf16,
 // bound by issue slots, takes four blocks of 4 warps an SM; f32, whose rows are half as many channels,
-// takes the longer tiles and with them half the look-back's chain (1 x 131072 x 1024: 357 us, 388 us with
+// takes the longer tiles and with them half the look-back's chain (1 x 131072 x 1024: 359 us, 388 us with
 // 4 warps).
 template <typename T>
 struct Forward {
@@ -406,7 +419,7 @@ struct Forward {
 
 // How a tile's rows get to shared memory: as one TMA box an array, or by every warp for its own rows in
 // copies of 16 bytes (arrays that TMA does not take: broadcast axes), 8, 4 or 2.  A box costs its
-// block a few instructions, the copies a tenth of all (8 x 4096 x 2048 bf16: forward 102 us, 111 us by
+// block a few instructions, the copies a tenth of all (8 x 4096 x 2048 bf16: forward 104 us, 111 us by
 // copies of 16; backward 227 and 247 us); 29 x 12456 x 332 bf16, whose rows start on 8 bytes, takes
 // 357 us by copies of 8 and 395 by copies of 4.
 constexpr int kTma = 32;
@@ -611,17 +624,18 @@ __global__ void __launch_bounds__(32 * Forward<T>::kNw, Forward<T>::kBlocks) rec
     auto first = [&](auto form) {   // the steps and their map
       constexpr int F = decltype(form)::value;
       constexpr bool kFar = F == kMixed;
-      float2 l = make_float2(0.f, 0.f);   // their log decays together
+      float2 l = make_float2(0.f, 0.f), most = l;   // their log decays together; infinite where a d^2 is
 #pragma unroll
       for (int k = 0; k < kPairs; ++k) {
         const float2 lk = log_decay<kFar>(rate, rcp2(one_plus_exp2(pair_at(rows + kArray, k, lane, T()))));
         l = fp::add2(l, lk);
         dec[k] = decay<kFar>(lk);
-        // m i = sqrt(u) / d = u / sqrt(u d^2), u = 1 - a^2, d = 1 / i: one special function, not two.
-        // Where d^2 overflows (i < 2^-64), m i is taken as 0.
+        // m i = sqrt(u) / d = u / sqrt(u d^2), u = 1 - a^2, d = 1 / i: one special function, not two.  Where d^2
+        // overflows, i < 2^-64, that is 0: such tiles are odd too.
         const float2 d = one_plus_exp2(pair_at(rows + 2 * kArray, k, lane, T()));
         const float2 u = one_minus_a2<kFar>(dec[k]);
         const float2 v = fp::mul2(fp::mul2(u, d), d);       // never 0, nor 0 * inf
+        most = fp::add2(most, v);
         const float2 mi = fp::mul2(u, make_float2(rsqrt_approx(v.x), rsqrt_approx(v.y)));
         b[k] = fp::mul2(mi, pair_at(rows, k, lane, T()));
       }
@@ -641,7 +655,9 @@ __global__ void __launch_bounds__(32 * Forward<T>::kNw, Forward<T>::kBlocks) rec
         s.maps[warp][cl + kCpl - 1] = make_float2(all.y, H.y);
         s.logs[warp][cl + kCpl - 1] = l.y;
       }
-      if (huge2(kCpl == 2 ? H : dup(H.x))) s.odd[slot][0] = 1;
+      const bool large = huge2(kCpl == 2 ? H : dup(H.x));
+      if (rarely(large || !(most.x + most.y < kInf)))
+        if (large || hardly_open<T, SPW>(rows + 2 * kArray, lane)) s.odd[slot][0] = 1;
     };
     if (far) first(std::integral_constant<int, kMixed>());
     else first(std::integral_constant<int, kSlow>());

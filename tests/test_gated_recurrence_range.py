@@ -151,6 +151,27 @@ def test_large_states_closed_by_one_step(bD, dtype):
     within(to_np(state), e.h[:, 0], e.eh[:, 0], "f32", "state")
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_closed_input_gate_on_large_values(dtype):
+    """i far below 2^-64, but not too small for fp32, times an x that makes up for it."""
+    d = mixed(2, 150, 72, dtype, seed=43)
+    g = torch.Generator().manual_seed(44)
+    at = torch.randint(0, 5, (2, 150, 72), generator=g).cuda()
+    gx, x = (d[k].float() for k in ("gx", "x"))
+    for k, (gate, size) in enumerate(((-43.0, 1e15), (-46.0, 1e20), (-60.0, 1e25), (-80.0, 1e33))):
+        gx = torch.where(at == k, gate, gx)
+        x = torch.where(at == k, torch.randn(x.shape, generator=g).cuda() * size, x)
+    d["gx"], d["x"] = gx.to(DT[dtype]), x.to(DT[dtype])
+    n = {k: to_np(v) for k, v in d.items()}
+    e = Errors(n["x"], n["ga"], n["gx"], n["decay"], n["init"])
+    y, fin, _ = forward(d)
+    within(to_np(y), e.h, e.eh, dtype, "y")
+    within(to_np(fin), e.h[:, -1], e.eh[:, -1], "f32", "final_state")
+    y, _ = pkg.gated_recurrence_step(*(d[k][:, 0] for k in ("x", "ga", "gx")), d["decay"], d["init"].clone(), c=C)
+    within(to_np(y), e.h[:, 0], e.eh[:, 0], dtype, "y of one step")
+
+
 def ordinary(b, T, D, dtype, seed, strong):
     """Decays of 0.9 to 0.999 at an open gate, or of e^-0.1 to e^-12."""
     g = torch.Generator().manual_seed(seed)
