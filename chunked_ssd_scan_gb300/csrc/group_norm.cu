@@ -614,7 +614,12 @@ ssd_status group_norm_forward(const group_norm_shape* shape, const void* x, cons
       workspace_bytes < group_norm_workspace_bytes(shape, 0))
     return SSD_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (empty) return SSD_OK;
+  if (empty) {   // samples without positions: the mean of nothing is NaN, all its bits set
+    const size_t bytes = sizeof(float) * (size_t)(shape->batch * shape->groups);
+    for (float* d : {mean, rstd})
+      if (d && bytes > 0 && cudaMemsetAsync(d, 0xff, bytes, st) != cudaSuccess) return SSD_ERR_CUDA;
+    return SSD_OK;
+  }
   NormParams p = norm_params(shape);
   p.x = x;
   p.w = weight;

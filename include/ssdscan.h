@@ -480,7 +480,8 @@ size_t group_norm_workspace_bytes(const group_norm_shape* shape, int32_t backwar
  *   y[n,s,c] = act((x[n,s,c] - mean) rstd weight[c] + bias[c])
  * x [batch, rows, channels] strided, y contiguous, io_dtype; weight (NULL = ones), bias (NULL =
  * zeros) [channels] f32; mean, rstd [batch, groups] f32 (both or neither NULL).  The variance is
- * summed around the mean, not as a difference of squares.
+ * summed around the mean, not as a difference of squares.  Samples without positions (rows = 0)
+ * have NaN for mean and rstd.
  */
 ssd_status group_norm_forward(const group_norm_shape* shape, const void* x, const float* weight,
                               const float* bias, void* y, float* mean, float* rstd,
