@@ -44,7 +44,7 @@ __device__ __forceinline__ Moments join_lanes(Moments m) {
 // wider than the block) of its tile, positions row, row + rows, ... of its chunk.
 template <int V>
 struct MapSlot {
-  int64_t n, s0, s1;                // sample, positions [s0, s1)
+  int64_t n, s0, s1;                // sample (or the first of them), positions [s0, s1)
   int chunk, g0, groups;            // chunk, groups of the tile
   int gv, vecs, cols, rows, row, col;   // vectors of a group and of the tile, thread columns and rows
   __device__ __forceinline__ MapSlot(const NormParams& p, uint32_t block) {
@@ -177,8 +177,16 @@ __global__ void __launch_bounds__(kThreads, kMapForward) norm_map_stats_kernel(N
   }
 }
 
+// Writes a partial sum, or adds to it; one thread alone does so, in its order (the addition is an atomic one
+// because it does not wait for the value that it adds to).
+__device__ __forceinline__ void put(float* p, float v, bool more) {
+  if (more) atomicAdd(p, v);
+  else *p = v;
+}
+
 // Per chunk and channel, sum dz and sum dz xhat (which are the parameters' gradients' partials), and per
-// group their sums times w, which the gradient of x needs.
+// group their sums times w, which the gradient of x needs.  Where there are more samples than slots, a
+// block takes every slots-th sample and adds to the partial row that it wrote for the first.
 template <typename T, int V, bool kSilu>
 __global__ void __launch_bounds__(kThreads, kMapBackward) norm_map_grad_sums_kernel(NormParams p) {
   using Q = Pack<T, V>;
@@ -186,80 +194,84 @@ __global__ void __launch_bounds__(kThreads, kMapBackward) norm_map_grad_sums_ker
   __shared__ float4 all[kThreads][Q::P];
   __shared__ float2 wide[kThreads];
   follow();
-  const MapSlot<V> t(p, blockIdx.x);
+  MapSlot<V> t(p, blockIdx.x);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  float2 mine = make_float2(0.f, 0.f);   // of the first row's threads: their channels' sums times w
-  for (int v0 = 0; v0 < t.vecs; v0 += kThreads) {
-    const int v = v0 + t.col;
-    float2 dw[Q::P], db[Q::P], w[Q::P];
-    Q::zero(dw);
-    Q::zero(db);
-    Q::zero(w);
-    if (t.row < t.rows && v < t.vecs) {
-      const int64_t c = t.channel(p, v), at = t.n * p.G + t.g0 + v / t.gv;
-      const float mean = __ldg(p.mean_in + at), rstd = __ldg(p.rstd_in + at);
-      float2 bias[Q::P];
-      Q::param(p.w, c, 1.f, w);
-      Q::param(p.bias, c, 0.f, bias);
-      Pairs<T, V, U> in(p, t, c);
-      in.fetch();
-      while (in.pending()) {
-        typename Q::Raw rx[U], ry[U];
-        in.take(rx, ry);
+  for (; t.n < p.N; t.n += p.slots) {
+    float2 mine = make_float2(0.f, 0.f);   // of the first row's threads: their channels' sums times w
+    for (int v0 = 0; v0 < t.vecs; v0 += kThreads) {
+      const int v = v0 + t.col;
+      float2 dw[Q::P], db[Q::P], w[Q::P];
+      Q::zero(dw);
+      Q::zero(db);
+      Q::zero(w);
+      if (t.row < t.rows && v < t.vecs) {
+        const int64_t c = t.channel(p, v), at = t.n * p.G + t.g0 + v / t.gv;
+        const float mean = __ldg(p.mean_in + at), rstd = __ldg(p.rstd_in + at);
+        float2 bias[Q::P];
+        Q::param(p.w, c, 1.f, w);
+        Q::param(p.bias, c, 0.f, bias);
+        Pairs<T, V, U> in(p, t, c);
+        in.fetch();
+        while (in.pending()) {
+          typename Q::Raw rx[U], ry[U];
+          in.take(rx, ry);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {   // past the end dy = 0: nothing is added
-          float2 f[Q::P], d[Q::P];
-          Q::unpack(rx[u], f);
-          Q::unpack(ry[u], d);
+          for (int u = 0; u < U; ++u) {   // past the end dy = 0: nothing is added
+            float2 f[Q::P], d[Q::P];
+            Q::unpack(rx[u], f);
+            Q::unpack(ry[u], d);
 #pragma unroll
-          for (int e = 0; e < Q::P; ++e) {
-            const float2 xh = fp::mul2(minus2<V>(f[e], mean), dup(rstd));
-            const float2 dz = times_act_grad2<kSilu>(d[e], fp::fma2(xh, w[e], bias[e]));
-            db[e] = fp::add2(db[e], dz);
-            dw[e] = fp::fma2(dz, xh, dw[e]);
+            for (int e = 0; e < Q::P; ++e) {
+              const float2 xh = fp::mul2(minus2<V>(f[e], mean), dup(rstd));
+              const float2 dz = times_act_grad2<kSilu>(d[e], fp::fma2(xh, w[e], bias[e]));
+              db[e] = fp::add2(db[e], dz);
+              dw[e] = fp::fma2(dz, xh, dw[e]);
+            }
           }
         }
       }
-    }
-    // over the block's rows, per channel
-    __syncthreads();
+      // over the block's rows, per channel
+      __syncthreads();
 #pragma unroll
-    for (int e = 0; e < Q::P; ++e) all[threadIdx.x][e] = make_float4(db[e].x, db[e].y, dw[e].x, dw[e].y);
-    __syncthreads();
-    if (t.row == 0 && v < t.vecs) {
-      const int64_t at = (t.n * p.chunks + t.chunk) * p.C + t.channel(p, v);
+      for (int e = 0; e < Q::P; ++e) all[threadIdx.x][e] = make_float4(db[e].x, db[e].y, dw[e].x, dw[e].y);
+      __syncthreads();
+      if (t.row == 0 && v < t.vecs) {
+        const bool more = t.n >= p.slots;   // not the block's first sample
+        const uint32_t slot = (uint32_t)t.n % (uint32_t)p.slots;   // fewer than 2^31 samples
+        const int64_t at = ((int64_t)slot * p.chunks + t.chunk) * p.C + t.channel(p, v);
 #pragma unroll
-      for (int e = 0; e < Q::P; ++e) {
-        for (int r = 1; r < t.rows; ++r) {
-          const float4 a = all[r * t.cols + t.col][e];
-          db[e] = fp::add2(db[e], make_float2(a.x, a.y));
-          dw[e] = fp::add2(dw[e], make_float2(a.z, a.w));
-        }
-        if (p.part_rows > 0 && SSD_INDEX_OK(p.hdr, at + min(2 * e + 1, V - 1), p.part_rows * p.C, 77)) {
-          p.part_b[at + 2 * e] = db[e].x;
-          p.part_w[at + 2 * e] = dw[e].x;
-          if (V > 1) {
-            p.part_b[at + 2 * e + 1] = db[e].y;
-            p.part_w[at + 2 * e + 1] = dw[e].y;
+        for (int e = 0; e < Q::P; ++e) {
+          for (int r = 1; r < t.rows; ++r) {
+            const float4 a = all[r * t.cols + t.col][e];
+            db[e] = fp::add2(db[e], make_float2(a.x, a.y));
+            dw[e] = fp::add2(dw[e], make_float2(a.z, a.w));
           }
+          if (p.part_rows > 0 && SSD_INDEX_OK(p.hdr, at + min(2 * e + 1, V - 1), p.part_rows * p.C, 77)) {
+            put(p.part_b + at + 2 * e, db[e].x, more);
+            put(p.part_w + at + 2 * e, dw[e].x, more);
+            if (V > 1) {
+              put(p.part_b + at + 2 * e + 1, db[e].y, more);
+              put(p.part_w + at + 2 * e + 1, dw[e].y, more);
+            }
+          }
+          mine.x += fmaf(db[e].x, w[e].x, db[e].y * w[e].y);
+          mine.y += fmaf(dw[e].x, w[e].x, dw[e].y * w[e].y);
         }
-        mine.x += fmaf(db[e].x, w[e].x, db[e].y * w[e].y);
-        mine.y += fmaf(dw[e].x, w[e].x, dw[e].y * w[e].y);
       }
     }
-  }
-  wide[threadIdx.x] = mine;
-  __syncthreads();
-  const int per = min(t.gv, t.cols);
-  for (int k = warp; k < t.groups; k += kWarps) {
-    float2 s = make_float2(0.f, 0.f);
-    for (int j = lane; j < per; j += 32) s = fp::add2(s, wide[k * per + j]);
+    wide[threadIdx.x] = mine;
+    __syncthreads();
+    const int per = min(t.gv, t.cols);
+    for (int k = warp; k < t.groups; k += kWarps) {
+      float2 s = make_float2(0.f, 0.f);
+      for (int j = lane; j < per; j += 32) s = fp::add2(s, wide[k * per + j]);
 #pragma unroll
-    for (int o = 16; o > 0; o /= 2)
-      s = fp::add2(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, s.y, o)));
-    const int64_t at = ((t.n * p.G + t.g0 + k) * p.chunks + t.chunk) * 2;
-    if (lane == 0 && SSD_INDEX_OK(p.hdr, at + 1, p.N * p.chunks * p.G * 2, 78))
-      *reinterpret_cast<float2*>(p.stats + at) = s;
+      for (int o = 16; o > 0; o /= 2)
+        s = fp::add2(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, s.y, o)));
+      const int64_t at = ((t.n * p.G + t.g0 + k) * p.chunks + t.chunk) * 2;
+      if (lane == 0 && SSD_INDEX_OK(p.hdr, at + 1, p.N * p.chunks * p.G * 2, 78))
+        *reinterpret_cast<float2*>(p.stats + at) = s;
+    }
   }
 }
 
@@ -270,7 +282,7 @@ template <bool kGrad>
 __global__ void __launch_bounds__(1024) norm_map_join_kernel(NormParams p, uint32_t group_blocks) {
   follow();
   if (blockIdx.x >= group_blocks) {
-    if (kGrad) param_grad(p, blockIdx.x - group_blocks, 0, 1);
+    if (kGrad) param_grad(p, blockIdx.x - group_blocks);
     return;
   }
   const int64_t at = (int64_t)blockIdx.x * 32 + threadIdx.x / 32;
@@ -474,6 +486,9 @@ int64_t tile_groups(int64_t G, int64_t gv) { return std::max<int64_t>(1, std::mi
 
 bool runs_as_tokens(int64_t S, int64_t G, int64_t gv) { return S == 1 && G <= 65535 && gv <= kTokenWidth; }
 
+// Samples side by side in the gradient sums; samples in chunks are few.
+int64_t map_slots(int64_t N, int64_t chunks) { return chunks > 1 ? N : std::min<int64_t>(N, kMapRows); }
+
 NormPlan norm_plan(const group_norm_shape* s, bool backward) {
   NormPlan L;
   const int64_t cg = s->channels / s->groups, gv = cg / max_vec(s), N = s->batch, S = s->rows;
@@ -491,13 +506,14 @@ NormPlan norm_plan(const group_norm_shape* s, bool backward) {
   off = align_up(off + sizeof(float) * 2 * (size_t)(N * s->groups), kWsAlign);
   if (backward) {
     // a narrower vector (rows that are not aligned) may send a token's group to the map kernels
+    const int64_t maps = map_slots(N, L.chunks) * L.chunks;
     L.part_rows = runs_as_tokens(S, s->groups, cg) ? kTokenBlocks
-                : runs_as_tokens(S, s->groups, gv) ? std::max<int64_t>(kTokenBlocks, N)
-                                                   : N * L.chunks;
+                : runs_as_tokens(S, s->groups, gv) ? std::max<int64_t>(kTokenBlocks, maps)
+                                                   : maps;
     L.part_w = off;
-    off = align_up(off + sizeof(float) * (size_t)((L.part_rows + kFoldRows) * s->channels), kWsAlign);
+    off = align_up(off + sizeof(float) * (size_t)(L.part_rows * s->channels), kWsAlign);
     L.part_b = off;
-    off = align_up(off + sizeof(float) * (size_t)((L.part_rows + kFoldRows) * s->channels), kWsAlign);
+    off = align_up(off + sizeof(float) * (size_t)(L.part_rows * s->channels), kWsAlign);
   }
   L.total = off;
   return L;
@@ -523,8 +539,10 @@ cudaError_t launch_as(NormParams p, bool backward, cudaStream_t st) {
   const int64_t gv = p.cg / V;
   if (runs_as_tokens(p.S, p.G, gv)) return run_tokens<T, V>(p, backward, st);
   p.tile_groups = (int32_t)tile_groups(p.G, gv);
-  p.part_rows = p.dw || p.db ? p.N * p.chunks : 0;
-  const unsigned grid = (unsigned)(p.N * ((p.G + p.tile_groups - 1) / p.tile_groups) * p.chunks);
+  p.slots = map_slots(p.N, p.chunks);
+  p.part_rows = p.dw || p.db ? p.slots * p.chunks : 0;
+  const int64_t tiles = (p.G + p.tile_groups - 1) / p.tile_groups;
+  const unsigned grid = (unsigned)(p.N * tiles * p.chunks), sums = (unsigned)(p.slots * tiles * p.chunks);
   const unsigned group_blocks = (unsigned)((p.N * p.G + 31) / 32);
   if (!backward) {
     norm_map_stats_kernel<T, V><<<grid, kThreads, 0, st>>>(p);
@@ -534,16 +552,14 @@ cudaError_t launch_as(NormParams p, bool backward, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     return launch_next(norm_map_apply_kernel<T, V, kSilu>, grid, kThreads, 0, st, p);
   }
-  norm_map_grad_sums_kernel<T, V, kSilu><<<grid, kThreads, 0, st>>>(p);
+  norm_map_grad_sums_kernel<T, V, kSilu><<<sums, kThreads, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // few partial rows: the join's launch takes the parameters' gradients along
-  const bool along = p.part_rows > 0 && p.part_rows <= kFewRows;
-  const unsigned more = along ? (unsigned)((p.C + 31) / 32) : 0u;
+  // the join's launch takes the parameters' gradients along
+  const unsigned more = p.part_rows > 0 ? (unsigned)((p.C + 31) / 32) : 0u;
   e = launch_next(norm_map_join_kernel<true>, group_blocks + more, 1024, 0, st, p, group_blocks);
   if (e != cudaSuccess) return e;
-  if ((e = launch_next(norm_map_grad_apply_kernel<T, V, kSilu>, grid, kThreads, 0, st, p)) != cudaSuccess) return e;
-  return along ? cudaSuccess : launch_param_grad(p, st);
+  return launch_next(norm_map_grad_apply_kernel<T, V, kSilu>, grid, kThreads, 0, st, p);
 }
 
 template <typename T, int V>

@@ -29,6 +29,7 @@ struct NormParams {
   int32_t tile_groups;  // map kernels: groups of a column tile
   int32_t chunks;       // map kernels: pieces that a sample's positions are cut into
   int64_t chunk_rows;
+  int64_t slots;        // map gradient sums: samples that are worked on side by side
   float *stats;         // map kernels: [N, G, chunks, 2], mean and M2 or the two gradient sums
   float *joined;        // [N, G, 2]
   float *part_w, *part_b;   // rows of parameter gradient partials [part_rows, C]
@@ -77,27 +78,27 @@ __device__ __forceinline__ float2 minus2(float2 a, float b) {
 
 constexpr int kTokenBlocks = 152 * 4;   // most blocks of the token backward, which writes a partial row each
 constexpr int kTokenWidth = 4 * kThreads;   // vectors of a group that a token kernel holds in registers
-constexpr int kFewRows = 1024;   // up to so many partial rows are joined at once,
-constexpr int kFoldRows = 64;    // more through so many
+// Most samples that a map kernel's gradient sums take side by side, each with a partial row: twice what the
+// machine holds of its blocks.  Beyond it a block goes on to further samples and adds to its row (a row for
+// every sample took 461 MB, now 55 MB, for 100000 x 2 x 512 bf16, and 2610 us, now 2455).
+constexpr int kMapRows = 2 * kGridBlocks * kMapBackward;
 
-// dweight and dbias of 32 channels from share `part` of `parts` of the partial rows, by a block of 32
-// warps: a warp adds every 32nd row, eight loads of each array in flight, and the warps are joined in
-// their order into row `part`.
-static __device__ __forceinline__ void param_grad(const NormParams& p, int64_t cols, int part, int parts) {
+// dweight and dbias of 32 channels from the partial rows, by a block of 32 warps: a warp adds every 32nd
+// row, eight loads of each array in flight, and the warps are joined in their order.
+static __device__ __forceinline__ void param_grad(const NormParams& p, int64_t cols) {
   __shared__ float2 sums[32][33];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int64_t c = cols * 32 + lane;
-  const int64_t share = (p.part_rows + parts - 1) / parts, r0 = part * share, r1 = min(p.part_rows, r0 + share);
   float2 s = make_float2(0.f, 0.f);
   if (c < p.C) {
     constexpr int U = 8;
-    for (int64_t r = r0 + warp; r < r1; r += 32 * U) {
+    for (int64_t r = warp; r < p.part_rows; r += 32 * U) {
       const float *pw = p.part_w + r * p.C + c, *pb = p.part_b + r * p.C + c;
       float2 v[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        v[u] = r + 32 * u < r1 ? make_float2(__ldcg(pw + u * 32 * p.C), __ldcg(pb + u * 32 * p.C))
-                               : make_float2(0.f, 0.f);
+        v[u] = r + 32 * u < p.part_rows ? make_float2(__ldcg(pw + u * 32 * p.C), __ldcg(pb + u * 32 * p.C))
+                                        : make_float2(0.f, 0.f);
 #pragma unroll
       for (int u = 0; u < U; ++u) s = fp::add2(s, v[u]);
     }
@@ -108,31 +109,19 @@ static __device__ __forceinline__ void param_grad(const NormParams& p, int64_t c
     float2 v = make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < 32; ++k) v = fp::add2(v, sums[k][lane]);
-    if (p.dw) p.dw[part * p.C + c] = v.x;
-    if (p.db) p.db[part * p.C + c] = v.y;
+    if (p.dw) p.dw[c] = v.x;
+    if (p.db) p.db[c] = v.y;
   }
 }
 static __global__ void __launch_bounds__(1024) norm_param_grad_kernel(NormParams p) {
   follow();
-  param_grad(p, blockIdx.x, blockIdx.y, gridDim.y);
+  param_grad(p, blockIdx.x);
 }
 
-// Joins the partial rows of the parameters' gradients: at once, or where there are many through
-// kFoldRows of them behind the others.
-static cudaError_t launch_param_grad(NormParams p, cudaStream_t st) {
+// Joins the partial rows of the parameters' gradients.
+static cudaError_t launch_param_grad(const NormParams& p, cudaStream_t st) {
   if (p.part_rows == 0) return cudaSuccess;
-  const unsigned grid = (unsigned)((p.C + 31) / 32);
-  if (p.part_rows > kFewRows) {
-    NormParams f = p;
-    f.dw = p.part_w + p.part_rows * p.C;
-    f.db = p.part_b + p.part_rows * p.C;
-    const cudaError_t e = launch_next(norm_param_grad_kernel, dim3(grid, kFoldRows), 1024, 0, st, f);
-    if (e != cudaSuccess) return e;
-    p.part_w = f.dw;
-    p.part_b = f.db;
-    p.part_rows = kFoldRows;
-  }
-  return launch_next(norm_param_grad_kernel, dim3(grid, 1), 1024, 0, st, p);
+  return launch_next(norm_param_grad_kernel, dim3((unsigned)((p.C + 31) / 32)), 1024, 0, st, p);
 }
 
 // Runs a call with one position a sample whose rows start on 16 bytes, groups of kStraddleLeast bytes to

@@ -22,6 +22,9 @@ from . import (_I64, _VP, SSD_BF16, SSD_F32, SSDError, _check_cuda, _ptr, _strea
 #: Steps between the states that the recurrence keeps for its backward pass.
 GATED_RECURRENCE_CHUNK = 64
 
+#: Bytes at the start of a workspace that are zero before its first call.
+HEADER_BYTES = 256
+
 ACTIVATIONS = {None: 0, "none": 0, "silu": 1}
 _IO = {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16}
 
@@ -107,7 +110,9 @@ class _Plan:
         if need == 0:
             raise SSDError(2, f"{what} (sizes not supported)")
         if given is None:
-            return torch.zeros(need, dtype=torch.uint8, device=self._device)   # zero header
+            given = torch.empty(need, dtype=torch.uint8, device=self._device)
+            given[:HEADER_BYTES].zero_()
+            return given
         _check_cuda("workspace", given, torch.uint8)
         return given
 

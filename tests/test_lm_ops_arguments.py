@@ -17,3 +17,55 @@ def test_statistics_of_no_positions(shape, dtype):
     y, m, r = pkg.group_norm_forward(x, 4, mean=mean, rstd=rstd)
     assert y.shape == x.shape and m.data_ptr() == mean.data_ptr()
     assert bool(torch.isnan(m).all()) and bool(torch.isnan(r).all()) and m.shape == r.shape == (shape[0], 4)
+
+
+def _norm_shape(N, S, C, G, io):
+    st = (ctypes.c_int64 * 2)(S * C, C)
+    return pkg.lm_ops.group_norm_shape(N, S, C, G, st, st, 1e-5, 1, io)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from chunked_ssd_scan_gb300 import _build
+    _build.build()
+    return pkg.load_library()
+
+
+# tokens in wide groups that some vectors take into registers, and some that none does; maps of few positions
+@pytest.mark.parametrize("io", [0, 1], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(131072, 1, 4096, 1), (131072, 1, 8192, 1), (100000, 1, 4999, 1), (70000, 1, 2048, 2),
+                                   (40000, 16, 64, 8), (20000, 2, 20000, 1)], ids=str)
+def test_norm_backward_workspace_does_not_grow_with_the_activation(lib, shape, io):
+    """Two floats a sample's group and chunk and two for the join, and partial rows of parameter gradients whose
+    number is bounded whatever N is: at most 912, twice C floats each."""
+    N, S, C, G = shape
+    need = lambda n: lib.group_norm_workspace_bytes(ctypes.byref(_norm_shape(n, S, C, G, io)), 1)   # noqa: E731
+    assert 0 < need(N) <= 16 * N * G + 2 * 912 * 4 * C + 5 * 256
+    assert need(2 * N) - need(N) <= 16 * N * G + 5 * 256
+
+
+@pytest.mark.gpu
+def test_a_workspace_made_here_is_zero_in_its_header_only():
+    """The header alone has to be: nothing else of a workspace is read before it is written.  What is handed out is
+    filled with 0xff before, and the results stay."""
+    g = torch.Generator().manual_seed(51)
+    x, dy = (torch.randn(3000, 96, generator=g).cuda() for _ in range(2))
+    _, mean, rstd = pkg.group_norm_forward(x, 6)
+    want = pkg.group_norm_backward(x, dy, 6, mean, rstd)
+    ids = torch.randint(0, 500, (3000,), generator=g).cuda()
+    wemb = pkg.embedding_backward(ids, dy, 500)
+    r = [torch.randn(2, 300, 96, generator=g).cuda() for _ in range(4)]
+    decay = torch.randn(96, generator=g).cuda() - 4
+    wrec = pkg.gated_recurrence_backward(*r[:3], decay, r[3])
+    torch.cuda.synchronize()
+    junk = torch.full((64 << 20,), 0xff, dtype=torch.uint8, device="cuda")
+    del junk   # the allocator gives it out again
+    plan = pkg.GroupNormBackwardPlan(x, dy, 6, mean, rstd)
+    assert not bool(plan.workspace[:256].any())
+    assert all(torch.equal(v, want[k]) for k, v in plan().items())
+    plan = pkg.EmbeddingBackwardPlan(ids, dy, 500)
+    assert not bool(plan.workspace[:256].any())
+    assert torch.equal(plan(), wemb)
+    plan = pkg.GatedRecurrenceBackwardPlan(*r[:3], decay, r[3])
+    assert not bool(plan.workspace[:256].any())
+    assert all(torch.equal(v, wrec[k]) for k, v in plan().items())

@@ -7,6 +7,7 @@ import torch
 import chunked_ssd_scan_gb300 as pkg
 from tests import lm_reference as ref
 from tests import test_gated_recurrence as tr
+from tests import test_group_norm as tn
 from tests.parity_util import to_np
 
 pytestmark = pytest.mark.gpu
@@ -62,3 +63,29 @@ def test_recurrence_strides(how, shape, dtype):
     size = np.abs(r["ddecay"]) + np.sqrt(b * T) * 4 * max(1.0, np.abs(r["dx"]).max())
     ref.check(g["ddecay"], r["ddecay"], 0.0, "ddecay", scale=size)
     ref.check(g["dinit"], r["dinit"], 0.0, "dinit")
+
+
+# more samples than the gradient sums take side by side, in maps and in tokens whose groups no token kernel holds
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("act", ["silu", None])
+@pytest.mark.parametrize("layout", ["plain", "odd"])
+@pytest.mark.parametrize("shape", [(1500, 4, 24, 3), (1500, 1, 1031, 1), (913, 2, 40, 5), (3000, 17, 16, 1),
+                                   (2100, 3, 600, 2)], ids=str)
+def test_norm_backward_of_many_samples(shape, layout, act, dtype):
+    N, S, C, G = shape
+    d = tn.inputs(N, S, C, dtype, seed=32, layout=layout, dev="cuda")
+    y, mean, rstd = pkg.group_norm_forward(d["x"], G, d["w"], d["bias"], activation=act)
+    x, dy, w, b = (to_np(d[k]) for k in ("x", "dy", "w", "bias"))
+    ref.check(to_np(y), ref.group_norm(x, G, w, b, act=act)[0], tn.REL[dtype], "y")
+    plan = pkg.GroupNormBackwardPlan(d["x"], d["dy"], G, mean, rstd, d["w"], d["bias"], activation=act)
+    g = plan()
+    assert pkg.workspace_status(plan.workspace) == ("SSD_OK", 0)
+    r = ref.group_norm_grad(x, dy, G, w, b, act=act)
+    size = np.abs(to_np(rstd)).mean() * 1.5
+    ref.check(to_np(g["dx"]), r["dx"], tn.REL[dtype], "dx", scale=np.maximum(np.abs(r["dx"]), size))
+    for k in ("dweight", "dbias"):
+        ref.check(to_np(g[k]), r[k], 0.0, k, scale=np.abs(r[k]) + np.sqrt(N * S))
+    again = pkg.group_norm_backward(d["x"], d["dy"], G, mean, rstd, d["w"], d["bias"], activation=act)
+    assert all(torch.equal(again[k], g[k]) for k in g)
+    only = pkg.group_norm_backward(d["x"], d["dy"], G, mean, rstd, d["w"], d["bias"], activation=act, param_grads=False)
+    assert torch.equal(only["dx"], g["dx"])
