@@ -538,6 +538,10 @@ template <typename T, int V, bool kSilu>
 cudaError_t launch_as(NormParams p, bool backward, cudaStream_t st) {
   const int64_t gv = p.cg / V;
   if (runs_as_tokens(p.S, p.G, gv)) return run_tokens<T, V>(p, backward, st);
+  // gradients take 8 bytes at most, as of maps (call_vec): 16384 x 16384 bf16 in one group 5.0 ms with 16, whose
+  // registers spilled, and 2.8 with 8
+  if constexpr (V * sizeof(T) > 8)
+    if (backward) return launch_as<T, V / 2, kSilu>(p, backward, st);
   p.tile_groups = (int32_t)tile_groups(p.G, gv);
   p.slots = map_slots(p.N, p.chunks);
   p.part_rows = p.dw || p.db ? p.slots * p.chunks : 0;
@@ -552,14 +556,16 @@ cudaError_t launch_as(NormParams p, bool backward, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     return launch_next(norm_map_apply_kernel<T, V, kSilu>, grid, kThreads, 0, st, p);
   }
-  norm_map_grad_sums_kernel<T, V, kSilu><<<sums, kThreads, 0, st>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  // the join's launch takes the parameters' gradients along
-  const unsigned more = p.part_rows > 0 ? (unsigned)((p.C + 31) / 32) : 0u;
-  e = launch_next(norm_map_join_kernel<true>, group_blocks + more, 1024, 0, st, p, group_blocks);
-  if (e != cudaSuccess) return e;
-  return launch_next(norm_map_grad_apply_kernel<T, V, kSilu>, grid, kThreads, 0, st, p);
+  if constexpr (V * sizeof(T) <= 8) {
+    norm_map_grad_sums_kernel<T, V, kSilu><<<sums, kThreads, 0, st>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // the join's launch takes the parameters' gradients along
+    const unsigned more = p.part_rows > 0 ? (unsigned)((p.C + 31) / 32) : 0u;
+    e = launch_next(norm_map_join_kernel<true>, group_blocks + more, 1024, 0, st, p, group_blocks);
+    if (e != cudaSuccess) return e;
+    return launch_next(norm_map_grad_apply_kernel<T, V, kSilu>, grid, kThreads, 0, st, p);
+  }
 }
 
 template <typename T, int V>

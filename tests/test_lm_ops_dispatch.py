@@ -89,3 +89,20 @@ def test_norm_backward_of_many_samples(shape, layout, act, dtype):
     assert all(torch.equal(again[k], g[k]) for k in g)
     only = pkg.group_norm_backward(d["x"], d["dy"], G, mean, rstd, d["w"], d["bias"], activation=act, param_grads=False)
     assert torch.equal(only["dx"], g["dx"])
+
+
+# tokens in one group that is too wide for a token kernel, with rows that the widest vectors divide
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [3, 950])
+def test_norm_of_very_wide_tokens(N, dtype):
+    C = 16384
+    d = tn.inputs(N, 1, C, dtype, seed=33, dev="cuda")
+    y, mean, rstd = pkg.group_norm_forward(d["x"], 1, d["w"], d["bias"])
+    x, dy, w, b = (to_np(d[k]) for k in ("x", "dy", "w", "bias"))
+    ref.check(to_np(y), ref.group_norm(x, 1, w, b)[0], tn.REL[dtype], "y")
+    g = pkg.group_norm_backward(d["x"], d["dy"], 1, mean, rstd, d["w"], d["bias"])
+    r = ref.group_norm_grad(x, dy, 1, w, b)
+    size = np.abs(to_np(rstd)).mean() * 1.5
+    ref.check(to_np(g["dx"]), r["dx"], tn.REL[dtype], "dx", scale=np.maximum(np.abs(r["dx"]), size))
+    for k in ("dweight", "dbias"):
+        ref.check(to_np(g[k]), r[k], 0.0, k, scale=np.abs(r[k]) + np.sqrt(N))
