@@ -534,38 +534,46 @@ int call_vec(const group_norm_shape* s, std::initializer_list<const void*> array
   return v;
 }
 
+// The map kernels' tiles for vectors of V values; blocks of one sample.
+int64_t map_tiles(NormParams& p, int V) {
+  p.tile_groups = (int32_t)tile_groups(p.G, p.cg / V);
+  return (p.G + p.tile_groups - 1) / p.tile_groups * p.chunks;
+}
+
 template <typename T, int V, bool kSilu>
-cudaError_t launch_as(NormParams p, bool backward, cudaStream_t st) {
-  const int64_t gv = p.cg / V;
-  if (runs_as_tokens(p.S, p.G, gv)) return run_tokens<T, V>(p, backward, st);
-  // gradients take 8 bytes at most, as of maps (call_vec): 16384 x 16384 bf16 in one group 5.0 ms with 16, whose
-  // registers spilled, and 2.8 with 8
-  if constexpr (V * sizeof(T) > 8)
-    if (backward) return launch_as<T, V / 2, kSilu>(p, backward, st);
-  p.tile_groups = (int32_t)tile_groups(p.G, gv);
+cudaError_t launch_map_forward(NormParams p, cudaStream_t st) {
+  const unsigned grid = (unsigned)(p.N * map_tiles(p, V)), group_blocks = (unsigned)((p.N * p.G + 31) / 32);
+  norm_map_stats_kernel<T, V><<<grid, kThreads, 0, st>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  e = launch_next(norm_map_join_kernel<false>, group_blocks, 1024, 0, st, p, group_blocks);
+  if (e != cudaSuccess) return e;
+  return launch_next(norm_map_apply_kernel<T, V, kSilu>, grid, kThreads, 0, st, p);
+}
+
+template <typename T, int V, bool kSilu>
+cudaError_t launch_map_backward(NormParams p, cudaStream_t st) {
+  const int64_t blocks = map_tiles(p, V);
+  const unsigned group_blocks = (unsigned)((p.N * p.G + 31) / 32);
   p.slots = map_slots(p.N, p.chunks);
   p.part_rows = p.dw || p.db ? p.slots * p.chunks : 0;
-  const int64_t tiles = (p.G + p.tile_groups - 1) / p.tile_groups;
-  const unsigned grid = (unsigned)(p.N * tiles * p.chunks), sums = (unsigned)(p.slots * tiles * p.chunks);
-  const unsigned group_blocks = (unsigned)((p.N * p.G + 31) / 32);
-  if (!backward) {
-    norm_map_stats_kernel<T, V><<<grid, kThreads, 0, st>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    e = launch_next(norm_map_join_kernel<false>, group_blocks, 1024, 0, st, p, group_blocks);
-    if (e != cudaSuccess) return e;
-    return launch_next(norm_map_apply_kernel<T, V, kSilu>, grid, kThreads, 0, st, p);
-  }
-  if constexpr (V * sizeof(T) <= 8) {
-    norm_map_grad_sums_kernel<T, V, kSilu><<<sums, kThreads, 0, st>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    // the join's launch takes the parameters' gradients along
-    const unsigned more = p.part_rows > 0 ? (unsigned)((p.C + 31) / 32) : 0u;
-    e = launch_next(norm_map_join_kernel<true>, group_blocks + more, 1024, 0, st, p, group_blocks);
-    if (e != cudaSuccess) return e;
-    return launch_next(norm_map_grad_apply_kernel<T, V, kSilu>, grid, kThreads, 0, st, p);
-  }
+  norm_map_grad_sums_kernel<T, V, kSilu><<<(unsigned)(p.slots * blocks), kThreads, 0, st>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // the join's launch takes the parameters' gradients along
+  const unsigned more = p.part_rows > 0 ? (unsigned)((p.C + 31) / 32) : 0u;
+  e = launch_next(norm_map_join_kernel<true>, group_blocks + more, 1024, 0, st, p, group_blocks);
+  if (e != cudaSuccess) return e;
+  return launch_next(norm_map_grad_apply_kernel<T, V, kSilu>, (unsigned)(p.N * blocks), kThreads, 0, st, p);
+}
+
+template <typename T, int V, bool kSilu>
+cudaError_t launch_as(const NormParams& p, bool backward, cudaStream_t st) {
+  if (runs_as_tokens(p.S, p.G, p.cg / V)) return run_tokens<T, V>(p, backward, st);
+  if (!backward) return launch_map_forward<T, V, kSilu>(p, st);
+  // gradients take 8 bytes at most, as of maps (call_vec): 16384 x 16384 bf16 in one group 5.0 ms with 16, whose
+  // registers spilled, and 2.8 with 8
+  return launch_map_backward<T, (V * (int)sizeof(T) > 8 ? V / 2 : V), kSilu>(p, st);
 }
 
 template <typename T, int V>
