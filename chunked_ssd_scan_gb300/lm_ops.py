@@ -4,8 +4,14 @@ in include/ssdscan.h).
 
 Every operator is a function and a plan.  A plan checks its arguments, allocates outputs and
 workspace once and makes only the C call when it is called; the function makes a plan and calls it.
-With ``stream`` given, what is allocated here belongs to that stream, and the inputs' memory is
-kept from reuse until the work on that stream is done.
+With ``stream`` given, what is allocated here belongs to that stream, and the memory of the inputs,
+and of outputs and a workspace that the caller passes, is kept from reuse until the work on that
+stream is done.
+
+A ``workspace`` of the caller's is a uint8 tensor of at least as many bytes as the operator's
+``..._workspace_bytes`` function in the C library says, on the inputs' device.  Its first
+``HEADER_BYTES`` are zero before its first call (the recurrence counts its tiles there and leaves
+zeros behind), and one call at a time uses it.
 """
 from __future__ import annotations
 
@@ -95,16 +101,21 @@ class _Plan:
         if device.index != torch.cuda.current_device():
             raise ValueError(f"tensors are on {device}, not on the current CUDA device")
         self._lib = load_library()
-        self._device, self._stream = device, stream
+        self._device, self._stream, self._given = device, stream, []
         return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
     def _out(self, name, given, dtype, shape):
         if given is None:
             return torch.empty(shape, dtype=dtype, device=self._device)
         _check_cuda(name, given, dtype, shape)
+        self._passed(name, given)
+        return given
+
+    def _passed(self, name, given):
+        """A buffer of the caller's that the call writes."""
         if given.device != self._device:
             raise ValueError(f"{name} must be on {self._device}, got {given.device}")
-        return given
+        self._given.append(given)
 
     def _workspace(self, given, need, what):
         if need == 0:
@@ -114,6 +125,7 @@ class _Plan:
             given[:HEADER_BYTES].zero_()
             return given
         _check_cuda("workspace", given, torch.uint8)
+        self._passed("workspace", given)
         return given
 
     def _finish(self, inputs, args):
@@ -122,7 +134,8 @@ class _Plan:
         for t in self.inputs:
             if t.device != self._device:
                 raise ValueError(f"all tensors must be on {self._device}, one is on {t.device}")
-            if self._stream is not None:
+        if self._stream is not None:
+            for t in (*self.inputs, *self._given):
                 t.record_stream(self._stream)
         self._args = (*args, _stream_handle(self._stream))
         self._fn = getattr(self._lib, self._name)

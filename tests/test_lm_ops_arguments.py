@@ -69,3 +69,50 @@ def test_a_workspace_made_here_is_zero_in_its_header_only():
     plan = pkg.GatedRecurrenceBackwardPlan(*r[:3], decay, r[3])
     assert not bool(plan.workspace[:256].any())
     assert all(torch.equal(v, wrec[k]) for k, v in plan().items())
+
+
+@pytest.mark.gpu
+def test_what_the_caller_passes_is_kept_for_the_stream(monkeypatch):
+    """Inputs, outputs and a workspace that the caller passes are recorded on the plan's stream, so that their memory
+    is not given out again while the work on it goes on."""
+    seen = set()
+    real = torch.Tensor.record_stream
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: (seen.add((t.data_ptr(), s.cuda_stream)), real(t, s))[1])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    new = lambda *s: torch.zeros(*s, device="cuda")   # noqa: E731
+    ws = lambda: torch.zeros(1 << 22, dtype=torch.uint8, device="cuda")   # noqa: E731
+    x, ga, gx, dy = (new(2, 70, 8) for _ in range(4))
+    decay, init = new(8), new(2, 8)
+    ids, table = torch.zeros(5, dtype=torch.int64, device="cuda"), new(6, 8)
+    calls = [
+        (pkg.GatedRecurrencePlan, (x, ga, gx, decay), dict(init_state=init, y=new(2, 70, 8), final_state=new(2, 8),
+                                                           states=new(2, 2, 8), workspace=ws())),
+        (pkg.GatedRecurrenceBackwardPlan, (x, ga, gx, decay, dy), dict(
+            states=new(2, 2, 8), dfinal=new(2, 8), workspace=ws(),
+            grads={"dx": new(2, 70, 8), "dgate_a": new(2, 70, 8), "dgate_x": new(2, 70, 8), "ddecay": new(8),
+                   "dinit": new(2, 8)})),
+        (pkg.GatedRecurrenceStepPlan, (x[:, 0], ga[:, 0], gx[:, 0], decay, init), dict(y=new(2, 8), state_out=new(2, 8))),
+        (pkg.GroupNormPlan, (x, 2, decay), dict(bias=new(8), y=new(2, 70, 8), mean=new(2, 2), rstd=new(2, 2),
+                                                workspace=ws())),
+        (pkg.GroupNormBackwardPlan, (x, dy, 2, new(2, 2), new(2, 2)), dict(
+            workspace=ws(), grads={"dx": new(2, 70, 8), "dweight": new(8), "dbias": new(8)})),
+        (pkg.EmbeddingPlan, (ids, table), dict(out=new(5, 8))),
+        (pkg.EmbeddingBackwardPlan, (ids, new(5, 8), 6), dict(dtable=new(6, 8), workspace=ws()))]
+    for plan, args, kw in calls:
+        seen.clear()
+        plan(*args, stream=side, **kw)()
+        grads = kw.pop("grads", {})
+        for t in (*args, *kw.values(), *grads.values()):
+            if isinstance(t, torch.Tensor):
+                assert (t.data_ptr(), side.cuda_stream) in seen, (plan.__name__, tuple(t.shape))
+    side.synchronize()
+
+
+@pytest.mark.gpu
+def test_a_workspace_elsewhere_is_refused():
+    x = torch.zeros(2, 5, 8, device="cuda")
+    for bad in (torch.zeros(1 << 20, dtype=torch.uint8), torch.zeros(1 << 20, device="cuda"),
+                torch.zeros(1 << 21, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            pkg.group_norm_forward(x, 2, workspace=bad)
