@@ -53,15 +53,19 @@ __global__ void __launch_bounds__(kThreads) embed_forward_kernel(const Id* ids, 
   fetch(i0);
   for (; i0 < n; i0 += step) {
     typename Q::Raw f[U];
+    float times[U];   // padding is zeros whatever the scale
 #pragma unroll
-    for (int u = 0; u < U; ++u) f[u] = next[u] >= 0 ? Q::raw(table + next[u] * D + d) : Q::none();
+    for (int u = 0; u < U; ++u) {
+      f[u] = next[u] >= 0 ? Q::raw(table + next[u] * D + d) : Q::none();
+      times[u] = next[u] >= 0 ? scale : 0.f;
+    }
     fetch(i0 + step);
 #pragma unroll
     for (int u = 0; u < U; ++u, o += tokens * D) {
       float2 v[Q::P];
       Q::unpack(f[u], v);
 #pragma unroll
-      for (int e = 0; e < Q::P; ++e) v[e] = fp::mul2(v[e], make_float2(scale, scale));
+      for (int e = 0; e < Q::P; ++e) v[e] = fp::mul2(v[e], make_float2(times[u], times[u]));
       if (i0 + u * tokens < n) Q::store(o, v);
     }
     o += (step - U * tokens) * D;

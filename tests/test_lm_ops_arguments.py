@@ -116,3 +116,18 @@ def test_a_workspace_elsewhere_is_refused():
                 torch.zeros(1 << 21, dtype=torch.uint8, device="cuda")[::2]):
         with pytest.raises(ValueError):
             pkg.group_norm_forward(x, 2, workspace=bad)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("D", [40, 41])
+@pytest.mark.parametrize("scale", [float("inf"), float("nan"), 0.0, -2.0])
+def test_padding_is_zeros_whatever_the_scale(scale, D, dtype):
+    ids = torch.tensor([1, -1, 2, 99, 0, -7, 1], device="cuda")
+    table = torch.ones(3, D, dtype=dtype, device="cuda")
+    out = pkg.embedding_forward(ids, table, scale=scale).float()
+    pad = torch.tensor([False, True, False, True, False, True, False], device="cuda")
+    assert torch.equal(out[pad], torch.zeros(3, D, device="cuda"))
+    assert torch.equal(out[~pad].nan_to_num(7.0, 8.0), torch.full((4, D), scale, device="cuda").nan_to_num(7.0, 8.0))
+    g = pkg.embedding_backward(ids, torch.ones(7, D, dtype=dtype, device="cuda"), 5, scale=scale)
+    assert torch.equal(g[3:], torch.zeros(2, D, device="cuda"))   # rows without tokens
