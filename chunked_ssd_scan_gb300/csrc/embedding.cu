@@ -531,6 +531,9 @@ Split split_row(int64_t nv) {
   return {cols, kThreads / cols, (unsigned)slices};
 }
 
+// Rows are cut into slices of a block's vectors each, at most 65535 of them (a grid's second axis).
+bool too_wide(int64_t D, int vec) { return (D + vec - 1) / vec > (int64_t)kThreads * 65535; }
+
 template <typename T, typename Id, int V>
 cudaError_t launch_forward_as(const void* ids, int64_t n, const void* table, int64_t rows, int64_t D, float scale,
                               void* out, cudaStream_t st) {
@@ -678,6 +681,7 @@ ssd_status embedding_forward(const void* ids, int32_t ids_bits, int64_t n, const
   if (misaligned(ids, ids_bits / 8) || misaligned(table, e) || misaligned(out, e))
     return SSD_ERR_INVALID_ARG;
   if (n == 0) return SSD_OK;
+  if (too_wide(dim, row_vec(e, dim, {table, out}))) return SSD_ERR_UNSUPPORTED;
   auto f = bf16 ? (ids_bits == 64 ? launch_forward<__nv_bfloat16, int64_t> : launch_forward<__nv_bfloat16, int32_t>)
                 : (ids_bits == 64 ? launch_forward<float, int64_t> : launch_forward<float, int32_t>);
   return done(f(ids, n, table, vocab, dim, scale, out, static_cast<cudaStream_t>(stream)));
@@ -699,6 +703,10 @@ ssd_status embedding_backward(const void* ids, int32_t ids_bits, int64_t n, cons
   if (!dtable || (n > 0 && (!ids || !dout))) return SSD_ERR_INVALID_ARG;
   if (misaligned(ids, ids_bits / 8) || misaligned(dout, bf16 ? 2 : 4) || misaligned(dtable, 4))
     return SSD_ERR_INVALID_ARG;
+  // the join of partial f32 rows, of more than one piece, may have narrower vectors than the sums
+  if (n > 0 && (too_wide(dim, row_vec(bf16 ? 2 : 4, dim, {dout})) ||
+                (embed_layout(n, vocab, dim).pieces > 1 && too_wide(dim, row_vec(4, dim, {})))))
+    return SSD_ERR_UNSUPPORTED;
   if (!workspace || misaligned(workspace, kWsAlign) ||
       workspace_bytes < embedding_backward_workspace_bytes(n, vocab, dim))
     return SSD_ERR_WORKSPACE;

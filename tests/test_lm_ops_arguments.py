@@ -131,3 +131,34 @@ def test_padding_is_zeros_whatever_the_scale(scale, D, dtype):
     assert torch.equal(out[~pad].nan_to_num(7.0, 8.0), torch.full((4, D), scale, device="cuda").nan_to_num(7.0, 8.0))
     g = pkg.embedding_backward(ids, torch.ones(7, D, dtype=dtype, device="cuda"), 5, scale=scale)
     assert torch.equal(g[3:], torch.zeros(2, D, device="cuda"))   # rows without tokens
+
+
+def test_rows_too_wide_are_refused_as_unsupported(lib):
+    """Rows of more vectors than a grid has blocks for: refused on the host, none of these pointers is read."""
+    A = 0x100000
+    vp = ctypes.c_void_p
+
+    def fwd(D, io, table=A):
+        return lib.embedding_forward(vp(A), 64, 1, vp(table), 1, D, io, 1.0, vp(A), None)
+
+    def bwd(D, io, dout=A):
+        return lib.embedding_backward(vp(A), 64, 1, vp(dout), 1, D, io, 1.0, vp(A), vp(A), ctypes.c_size_t(1 << 45), None)
+
+    most = 65535 * 256
+    assert fwd(most + 1, 0) == 2 and fwd(most + 1, 1) == 2            # an odd width: one value a vector
+    assert fwd(8 * most + 8, 1) == 2 and fwd(4 * most + 4, 0) == 2    # the widest vectors
+    assert fwd(2 * most, 1, table=A + 2) == 2                         # rows that start on 2 bytes
+    assert bwd(most + 1, 0) == 2 and bwd(4 * most + 4, 0) == 2 and bwd(2 * most, 1, dout=A + 2) == 2
+
+
+@pytest.mark.gpu
+def test_wide_rows():
+    """34 million values a row, in vectors of four: within the limit."""
+    D = 1 << 25
+    table = torch.arange(D, dtype=torch.float32, device="cuda").repeat(2, 1)
+    table[1].neg_()
+    ids = torch.tensor([1, 5, 0], device="cuda")
+    out = pkg.embedding_forward(ids, table)
+    assert torch.equal(out[0], table[1]) and torch.equal(out[2], table[0]) and not bool(out[1].any())
+    g = pkg.embedding_backward(ids, out, 2)
+    assert torch.equal(g, table)
