@@ -1579,7 +1579,10 @@ ssd_status gated_recurrence_backward(const gated_recurrence_shape* shape, const 
 ssd_status gated_recurrence_step(const gated_recurrence_shape* shape, const void* x,
                                  const void* gate_a, const void* gate_x, const float* decay,
                                  const float* state, void* y, float* state_out, void* stream) {
-  const ssd_status bad = check_shape(shape, false);
+  if (!shape) return SSD_ERR_INVALID_ARG;
+  gated_recurrence_shape one = *shape;   // the step strides are ignored
+  one.x_stride[1] = one.gate_a_stride[1] = one.gate_x_stride[1] = 0;
+  const ssd_status bad = check_shape(&one, false);
   if (bad != SSD_OK) return bad;
   if (shape->seqlen != 1) return SSD_ERR_INVALID_ARG;
   const bool bf16 = shape->io_dtype == SSD_BF16;

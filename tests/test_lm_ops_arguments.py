@@ -162,3 +162,13 @@ def test_wide_rows():
     assert torch.equal(out[0], table[1]) and torch.equal(out[2], table[0]) and not bool(out[1].any())
     g = pkg.embedding_backward(ids, out, 2)
     assert torch.equal(g, table)
+
+
+def test_step_strides_are_ignored_by_the_single_step(lib):
+    """A shape without sequences launches nothing and reads none of these pointers."""
+    two = lambda *v: (ctypes.c_int64 * 2)(*v)   # noqa: E731
+    vp = ctypes.c_void_p
+    s = pkg.lm_ops.gated_recurrence_shape(0, 1, 8, two(8, -3), two(8, -3), two(8, -3), two(0, 0), 8.0, 0)
+    assert lib.gated_recurrence_step(ctypes.byref(s), *[vp(0x100000)] * 7, None) == 0
+    s.x_stride[0] = -8
+    assert lib.gated_recurrence_step(ctypes.byref(s), *[vp(0x100000)] * 7, None) == 1
