@@ -6,6 +6,7 @@ import torch
 
 import chunked_ssd_scan_gb300 as pkg
 from tests import lm_reference as ref
+from tests import test_embedding as te
 from tests import test_gated_recurrence as tr
 from tests import test_group_norm as tn
 from tests.parity_util import to_np
@@ -106,3 +107,39 @@ def test_norm_of_very_wide_tokens(N, dtype):
     ref.check(to_np(g["dx"]), r["dx"], tn.REL[dtype], "dx", scale=np.maximum(np.abs(r["dx"]), size))
     for k in ("dweight", "dbias"):
         ref.check(to_np(g[k]), r[k], 0.0, k, scale=np.abs(r[k]) + np.sqrt(N))
+
+
+# sequences enough for two a thread, an odd number of them, and one row that is not aligned for it
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("layout", ["plain", "fused", "odd"])
+@pytest.mark.parametrize("bD", [(257, 2560), (512, 1216), (2049, 305)], ids=str)
+def test_step_of_many_sequences(bD, layout, dtype):
+    b, D = bD
+    d = tr.inputs(b, 1, D, dtype, seed=34, layout=layout, dev="cuda")
+    ry, rf, _ = tr.reference(d)
+    y, state = pkg.gated_recurrence_step(d["x"][:, 0], d["ga"][:, 0], d["gx"][:, 0], d["decay"], d["init"], c=tr.C)
+    ref.check(to_np(y), ry[:, 0], tr.REL[dtype], "y")
+    ref.check(to_np(state), rf, 0.0, "state")
+
+
+# more tokens than 64 tiles of 2048 sorted keys, keys of one, two and three digits
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("idt", [torch.int32, torch.int64], ids=["i32", "i64"])
+@pytest.mark.parametrize("case", [("zipf", 131073, 70000, 24), ("zipf", 300001, 90001, 12), ("uniform", 140001, 200, 40),
+                                  ("one", 200000, 70000, 8), ("ends", 131072 + 7, 500, 33),
+                                  ("uniform", 131072, 300, 20)], ids=str)
+def test_embedding_gradient_of_many_tokens(case, idt, dtype):
+    kind, n, V, D = case
+    ids = te.make_ids(kind, n, V, seed=35).to(idt).cuda()
+    dout = torch.randn(n, D, generator=torch.Generator().manual_seed(36)).to(te.DT[dtype]).cuda()
+    plan = pkg.EmbeddingBackwardPlan(ids, dout, V, scale=0.3)
+    g = plan()
+    assert pkg.workspace_status(plan.workspace) == ("SSD_OK", 0)
+    npids = ids.cpu().numpy().astype(np.int64)
+    r = ref.embedding_grad(npids, to_np(dout), V, np.float64(np.float32(0.3)))
+    # as in test_embedding: a row is a sum of `count` terms of size 0.3
+    count = np.bincount(npids[(npids >= 0) & (npids < V)], minlength=V)[:, None]
+    got = to_np(g)
+    assert np.all(np.abs(got - r) <= 2e-5 * 0.3 * np.sqrt(count) * (1 + np.abs(r)))
+    assert np.all(got[count[:, 0] == 0] == 0)
+    assert torch.equal(pkg.embedding_backward(ids, dout, V, scale=0.3), g)
