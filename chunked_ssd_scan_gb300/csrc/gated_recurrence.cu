@@ -46,10 +46,10 @@ __device__ __forceinline__ float softplus(float d) { return fmaxf(d, 0.f) + log1
 // A decay is kept as one number c (lookback.cuh): a - 1 = expm1(l) < 0 next to one, where a step is
 // h + (c h + b), and a itself below e^-1/4, where it is c h + b.  A warp whose channels cannot decay
 // faster than e^-1/4 a step does the first for all its values; others choose value by value (8 x 4096 x
-// 2048 bf16: 113 us forward, 250 us backward, where the first takes 104 and 227).  Both make NaN of an
+// 2048 bf16: 111 us forward, 234 us backward, where the first takes 103 and 215).  Both make NaN of an
 // infinite state next to one (inf - inf): an odd tile, one that meets values of kHuge or more, or NaN, is finished
 // by a function that goes through its steps once more, one by one, in a third form that does not (all tiles
-// odd: 218 us forward).  It is called, not part of the kernels: with its code inline they ran out of
+// odd: 217 us forward).  It is called, not part of the kernels: with its code inline they ran out of
 // registers (forward 145 us).
 constexpr float kInf = lookback::kInf;
 enum Form { kSlow, kMixed, kSafe };
@@ -93,9 +93,9 @@ __device__ __forceinline__ bool rarely(bool v) { return __builtin_expect(v, 0); 
 // block's warps and, by look-back, of earlier tiles give the state before the warp's first step, and a
 // second walk over the registers writes y.  Every input byte is read once.
 //
-// 8 x 4096 x 2048 bf16 with states: 104 us, 5.2 TB/s of 541 MB (77 % of the measured copy rate), with the
+// 8 x 4096 x 2048 bf16 with states: 103 us, 5.3 TB/s of 541 MB (78 % of the measured copy rate), with the
 // special-function unit (4 a value) and the issue slots (33 instructions a value) each busy more than half
-// of the time; 1 x 131072 x 1024 f32: 359 us, 6.0 TB/s (89 %).
+// of the time; 1 x 131072 x 1024 f32: 355 us, 6.1 TB/s (89 %).
 // ------------------------------------------------------------------------------------------------
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
@@ -105,7 +105,7 @@ constexpr float kTiny = 1e-36f;   // well above the smallest normal number (the 
 
 // Special functions by approximation: 1/x is good to 2^-23, 2^x and 1/sqrt x to 2^-22, and v log2 e adds |v| 2^-23
 // to e^v, so a sigmoid s is good to about 2^-21 + (1 - s) |v| 2^-23.  The exact functions are several
-// instructions each, of which the kernels issue 33 and 63 a value in all.
+// instructions each, of which the kernels issue 33 and 62 a value in all.
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -298,13 +298,6 @@ struct Walk {
     Q.x = decayed<F>(c.x, dy.x + decayed<F>(c.y, dy.y + Q.x));
     return Q;
   }
-  // w of the steps so far and pair k's, in the slow form (f32: in x)
-  static __device__ __forceinline__ float2 together(float2 c, float2 w) {
-    if constexpr (kCpl == 2) return fp::add2(w, fp::fma2(c, w, c));
-    w.x += fmaf(c.x, w.x, c.x);
-    w.x += fmaf(c.y, w.x, c.y);
-    return w;
-  }
   // sets the pairs of steps from `steps` on
   static __device__ __forceinline__ void cut(float2 (&v)[kPairs], int steps, float to) {
 #pragma unroll
@@ -364,7 +357,8 @@ __device__ __forceinline__ float2 safe_state(const M& maps, int cl, int count, f
   return h;
 }
 
-// Whether a lane's rows hold an input gate so closed that its 1 / i overflows when squared, but not so that i is 0.
+// Whether a lane's rows hold an input gate so closed that its 1 / i overflows when squared, but not so that i is 0
+// (-inf in every 16th step, as a mask, takes 8 x 4096 x 2048 bf16 from 103 to 119 us).
 template <typename T, int ROWS>
 __device__ __forceinline__ bool hardly_open(const unsigned char* rows, int lane) {
   bool any = false;
@@ -409,9 +403,9 @@ __device__ __forceinline__ Step step_at(const unsigned char* row, int array, int
 }
 
 // NW warps of 16 steps.  Half as many blocks of 8 warps wait for the look-back together, so bf16,
-// bound by issue slots, takes four blocks of 4 warps an SM; f32, whose rows are half as many channels,
-// takes the longer tiles and with them half the look-back's chain (1 x 131072 x 1024: 359 us, 388 us with
-// 4 warps).
+// bound by issue slots, takes four blocks of 4 warps an SM (8 x 4096 x 2048: 103 us, 107 us with two of
+// 8); f32, whose rows are half as many channels, takes the longer tiles and with them half the look-back's
+// chain (1 x 131072 x 1024: 355 us, 381 us with 4 warps).
 template <typename T>
 struct Forward {
   static constexpr int kNw = sizeof(T) == 2 ? 4 : 8, kSpw = 16, kSteps = kNw * kSpw, kBlocks = 16 / kNw;
@@ -419,9 +413,9 @@ struct Forward {
 
 // How a tile's rows get to shared memory: as one TMA box an array, or by every warp for its own rows in
 // copies of 16 bytes (arrays that TMA does not take: broadcast axes), 8, 4 or 2.  A box costs its
-// block a few instructions, the copies a tenth of all (8 x 4096 x 2048 bf16: forward 104 us, 111 us by
-// copies of 16; backward 227 and 247 us); 29 x 12456 x 332 bf16, whose rows start on 8 bytes, takes
-// 357 us by copies of 8 and 395 by copies of 4.
+// block a few instructions, the copies a tenth of all (8 x 4096 x 2048 bf16: forward 103 us, 111 us by
+// copies of 16; backward 215 and 253 us); 29 x 12456 x 332 bf16, whose rows start on 8 bytes, takes
+// 355 us by copies of 8 and 392 by copies of 4.
 constexpr int kTma = 32;
 
 __device__ __forceinline__ void tma_tile(void* dst, const CUtensorMap* map, uint64_t* bar, const Place& q) {
@@ -453,7 +447,6 @@ struct ForwardShared {
   float before[NW][kCh];   // the state before every warp's steps
   float rates[3][kCh];     // -c softplus(decay) of the tile's channels
   Place places[3];         // of the tile in hand, the one being loaded and the one after it
-  int odd[2][2];           // the tile has huge values: in its maps, in the state before it
   uint64_t full[2];        // TMA: a stage's boxes have landed
 };
 // By one warp: a tile's place and its channels' rates.
@@ -476,10 +469,10 @@ __device__ __forceinline__ void fetch_forward(const RecParams& p, ForwardShared<
 }
 
 // The rest of a tile with huge values: from its maps on (behind barrier A), or from the states before the warps'
-// steps (behind barrier B).  `stage`: the tile's rows; `slot`, `turn`: where it lies in `odd` and `places`.
+// steps (behind barrier B).  `stage`: the tile's rows; `turn`: where it lies in `places`.
 template <typename T, int ALIGN>
-__device__ __noinline__ void odd_forward(const RecParams& p, ForwardShared<T>& s, const unsigned char* stage, int slot,
-                                         int turn, bool maps, bool first) {
+__device__ __noinline__ void odd_forward(const RecParams& p, ForwardShared<T>& s, const unsigned char* stage, int turn,
+                                         bool maps, bool first) {
   constexpr int NW = Forward<T>::kNw, SPW = Forward<T>::kSpw, kCh = Tile<T>::kCh, kCpl = Tile<T>::kCpl;
   constexpr int kWarpBytes = SPW * kRowBytes, kArray = NW * kWarpBytes;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, cl = lane * kCpl;
@@ -528,7 +521,6 @@ __device__ __noinline__ void odd_forward(const RecParams& p, ForwardShared<T>& s
     } else if (warp == 1) {
       const int next = turn == 2 ? 0 : turn + 1;
       fetch_forward(p, s, s.places[next].tile, next == 2 ? 0 : next + 1);
-      if (lane < 2) s.odd[slot ^ 1][lane] = 0;
     }
     __syncthreads();
   }
@@ -593,7 +585,6 @@ __global__ void __launch_bounds__(32 * Forward<T>::kNw, Forward<T>::kBlocks) rec
     tc::mbar_init(s.full + 1, 1);
     tc::fence_mbar_init();
   }
-  if (threadIdx.x < 4) s.odd[threadIdx.x / 2][threadIdx.x % 2] = 0;
   if (warp == 0) {
     fetch_forward(p, s, blockIdx.x - gridDim.x, 0);
     __syncwarp();
@@ -621,6 +612,7 @@ __global__ void __launch_bounds__(32 * Forward<T>::kNw, Forward<T>::kBlocks) rec
 
     const unsigned char* rows = smem + slot * kStage + warp * kWarpBytes;
     float2 dec[kPairs], b[kPairs];
+    bool large = false;   // a huge value, or NaN
     auto first = [&](auto form) {   // the steps and their map
       constexpr int F = decltype(form)::value;
       constexpr bool kFar = F == kMixed;
@@ -655,15 +647,14 @@ __global__ void __launch_bounds__(32 * Forward<T>::kNw, Forward<T>::kBlocks) rec
         s.maps[warp][cl + kCpl - 1] = make_float2(all.y, H.y);
         s.logs[warp][cl + kCpl - 1] = l.y;
       }
-      const bool large = huge2(kCpl == 2 ? H : dup(H.x));
-      if (rarely(large || !(most.x + most.y < kInf)))
-        if (large || hardly_open<T, SPW>(rows + 2 * kArray, lane)) s.odd[slot][0] = 1;
+      large = huge2(kCpl == 2 ? H : dup(H.x));
+      if (rarely(!(most.x + most.y < kInf))) large = large || hardly_open<T, SPW>(rows + 2 * kArray, lane);
     };
     if (far) first(std::integral_constant<int, kMixed>());
     else first(std::integral_constant<int, kSlow>());
-    __syncthreads();   // A: the warps' maps are there; everyone is done with this stage's rows
-    if (rarely(s.odd[slot][0] != 0)) {
-      odd_forward<T, ALIGN>(p, s, smem + slot * kStage, slot, here, true, it == 0);
+    // A: the warps' maps are there; everyone is done with this stage's rows
+    if (rarely(__syncthreads_or(large))) {
+      odd_forward<T, ALIGN>(p, s, smem + slot * kStage, here, true, it == 0);
       continue;
     }
     if (warp == 0) {
@@ -682,22 +673,23 @@ __global__ void __launch_bounds__(32 * Forward<T>::kNw, Forward<T>::kBlocks) rec
           for (int c = 0; c < kCpl; ++c) v[c] = lookback::map(A[c], H[c]);
           lookback::publish(words, v);
         }
-        lookback::state_before<8>(words - kCh, -kCh, q.ti, h, p.hdr, 400);
+        // 8 words at a time save 4 % of a lone long sequence's chain (1 x 109272 x 576 bf16: 201 us, 210 with 7, 240
+        // with 5) and cost the registers 2 % of the others' (8 x 4096 x 2048: 104.4, 102.7 and 102.7)
+        lookback::state_before<7>(words - kCh, -kCh, q.ti, h, p.hdr, 400);
       }
       if (!last) {
 #pragma unroll
         for (int c = 0; c < kCpl; ++c) v[c] = lookback::inclusive(lookback::apply_safe(A[c], H[c], h[c]));
         lookback::publish(words, v);
       }
-      if (huge2(make_float2(h[0], h[kCpl - 1]))) s.odd[slot][1] = 1;
+      large = huge2(make_float2(h[0], h[kCpl - 1]));
       block_states<NW, kCpl, false>(s.maps, s.before, cl, h);
     } else if (warp == 1) {
       fetch_forward(p, s, s.places[next].tile, next == 2 ? 0 : next + 1);
-      if (lane < 2) s.odd[slot ^ 1][lane] = 0;
     }
-    __syncthreads();   // B: the states before the warps' steps are there, and the tile after the next
-    if (rarely(s.odd[slot][1] != 0)) {
-      odd_forward<T, ALIGN>(p, s, smem + slot * kStage, slot, here, false, false);
+    // B: the states before the warps' steps are there, and the tile after the next
+    if (rarely(__syncthreads_or(large))) {
+      odd_forward<T, ALIGN>(p, s, smem + slot * kStage, here, false, false);
       continue;
     }
     float2 h = make_float2(s.before[warp][cl], s.before[warp][cl + kCpl - 1]);
@@ -762,13 +754,22 @@ __global__ void __launch_bounds__(32 * Forward<T>::kNw, Forward<T>::kBlocks) rec
 //   dx = G mi, dgate_x = G xi, dgate_a = rate G kr (1 - r)   and sums G kr for ddecay.
 // ddecay: one partial row per tile, added in tile order by rec_ddecay_kernel.
 //
-// 8 x 4096 x 2048 bf16: 227 us, 4.2 TB/s of 944 MB (61 % of the measured copy rate): five values are kept
-// for every step and channel, so 128 registers a thread (none spilled) and two blocks an SM, which issue 63
+// 8 x 4096 x 2048 bf16: 215 us, 4.4 TB/s of 944 MB (65 % of the measured copy rate): five values are kept
+// for every step and channel, so 128 registers a thread (none spilled) and two blocks an SM, which issue 62
 // instructions a value half of the time and wait for their block's barriers and look-back otherwise.
 // ------------------------------------------------------------------------------------------------
 constexpr int kSpwBwd = 8;
 static_assert(kWarps * kSpwBwd == kChunk, "a backward tile starts from one kept state");
 
+// The tile after `last`, for one warp.
+__device__ __forceinline__ uint32_t take_ticket(const RecParams& p, uint32_t last) {
+  uint32_t tile = last + gridDim.x;
+  if (p.ticket) {
+    if (threadIdx.x % 32 == 0) tile = atomicAdd(p.ticket, 1u);
+    tile = __shfl_sync(0xffffffffu, tile, 0);
+  }
+  return tile;
+}
 template <typename T>
 struct BackwardShared {
   static constexpr int kCh = Tile<T>::kCh;
@@ -782,19 +783,13 @@ struct BackwardShared {
   int64_t partial_at;         // where the tile before has its row of ddecay partials,
   int partial_left;           // and how many of its channels lie inside (warp 2's)
   Place places[3];            // of the tile in hand, the one being loaded and the one after it
-  int odd[2][2];              // the tile has huge values: in its maps, in what its warps start from
   uint64_t full[2];           // TMA: a stage's boxes have landed
 };
 // By one warp: a tile's place, its channels' rates and the state before it.
 template <typename T>
-__device__ __forceinline__ void fetch_backward(const RecParams& p, BackwardShared<T>& s, uint32_t last, int turn) {
+__device__ __forceinline__ void fetch_backward(const RecParams& p, BackwardShared<T>& s, uint32_t tile, int turn) {
   constexpr int kCpl = Tile<T>::kCpl;
   const int lane = threadIdx.x % 32, cl = lane * kCpl;
-  uint32_t tile = last + gridDim.x;
-  if (p.ticket) {
-    if (lane == 0) tile = atomicAdd(p.ticket, 1u);
-    tile = __shfl_sync(0xffffffffu, tile, 0);
-  }
   const Place q = place<T, kChunk, true>(p, tile);
   if (lane == 0) s.places[turn] = q;
   if (tile < p.tiles) {
@@ -825,7 +820,7 @@ __device__ __forceinline__ void write_partial(const RecParams& p, const Backward
 // The rest of a tile with huge values, as odd_forward.  Returns the warp's sum of G kr.
 template <typename T, int ALIGN>
 __device__ __noinline__ float2 odd_backward(const RecParams& p, BackwardShared<T>& s, const unsigned char* stage,
-                                            int slot, int turn, bool maps, bool first) {
+                                            int turn, uint32_t after, bool maps, bool first) {
   constexpr int SPW = kSpwBwd, kCh = Tile<T>::kCh, kCpl = Tile<T>::kCpl;
   constexpr int kWarpBytes = SPW * kRowBytes, kArray = kWarps * kWarpBytes;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, cl = lane * kCpl;
@@ -882,8 +877,7 @@ __device__ __noinline__ float2 odd_backward(const RecParams& p, BackwardShared<T
       if (kCpl == 2) s.after[kWarps - 1][cl + kCpl - 1] = C[kCpl - 1];
     } else if (warp == 1) {
       const int next = turn == 2 ? 0 : turn + 1;
-      fetch_backward(p, s, s.places[next].tile, next == 2 ? 0 : next + 1);
-      if (lane < 2) s.odd[slot ^ 1][lane] = 0;
+      fetch_backward(p, s, __shfl_sync(0xffffffffu, after, 0), next == 2 ? 0 : next + 1);
     } else if (warp == 2 && !first) {
       write_partial(p, s);
     }
@@ -965,11 +959,10 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(const __gr
     tc::mbar_init(s.full + 1, 1);
     tc::fence_mbar_init();
   }
-  if (threadIdx.x < 4) s.odd[threadIdx.x / 2][threadIdx.x % 2] = 0;
   if (warp == 0) {
-    fetch_backward(p, s, blockIdx.x - gridDim.x, 0);
-    __syncwarp();
-    fetch_backward(p, s, blockIdx.x, 1);
+    const uint32_t one = take_ticket(p, blockIdx.x - gridDim.x), two = take_ticket(p, blockIdx.x);
+    fetch_backward(p, s, one, 0);
+    fetch_backward(p, s, two, 1);
   }
   __syncthreads();
   load(s.places[0], 0);
@@ -990,6 +983,8 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(const __gr
       __syncwarp();
     }
     const float2 rate = make_float2(s.rates[here][cl], s.rates[here][cl + kCpl - 1]);
+    uint32_t after = s.places[next].tile + gridDim.x;   // of warp 1's lane 0: the tile after the next, asked for early
+    if (warp == 1 && lane == 0 && p.ticket) after = atomicAdd(p.ticket, 1u);
     const bool far = __any_sync(0xffffffffu, fminf(rate.x, rate.y) < -kNear);   // as in the forward
     const float2 h0 = make_float2(s.start[here][cl], s.start[here][cl + kCpl - 1]);
     const int steps = (int)p.T - (int)q.t0 - warp * SPW, inside = min(SPW, max(0, steps));
@@ -997,6 +992,7 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(const __gr
     const unsigned char* rows = smem + slot * kStage + warp * kWarpBytes;
     // kr holds a i x r / m, what h_{t-1} r is compared with, until the state is known (r / m does not overflow)
     float2 dec[kPairs], mi[kPairs], xi[kPairs], kr[kPairs], r[kPairs];
+    bool large = false;   // a huge value, or NaN
     auto first = [&](auto form) {   // the steps and their maps
       constexpr int F = decltype(form)::value;
       constexpr bool kFar = F == kMixed;
@@ -1026,15 +1022,11 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(const __gr
       }
       if constexpr (kCpl == 1) l = dup(l.x + l.y);
       l = fp::add2(l, dup(-kTiny));   // maps are of the mixed form
-      float2 H = make_float2(0.f, 0.f), Q = H, all = dup(-kTiny);
+      const float2 all = decay<true>(l);
+      float2 H = make_float2(0.f, 0.f), Q = H;
 #pragma unroll
-      for (int k = 0; k < kPairs; ++k) {
+      for (int k = 0; k < kPairs; ++k)
         H = Walk<T, SPW>::template next<F>(dec[k], fp::mul2(mi[k], pair_at(rows, k, lane, T())), H);
-        if (!kFar) all = Walk<T, SPW>::together(dec[k], all);
-      }
-      // eight steps of e^-1/4 are 0.135: the w of all of them still holds their decay to a few units
-      if (kFar) all = decay<true>(l);
-      else all = make_float2(all.x < -kNear ? 1.f + all.x : all.x, all.y < -kNear ? 1.f + all.y : all.y);
       // the reverse map: dy + C enters a step, a (dy + C) leaves it
 #pragma unroll
       for (int k = kPairs - 1; k >= 0; --k)
@@ -1047,11 +1039,12 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(const __gr
         s.back[warp][cl + kCpl - 1] = make_float2(all.y, Q.y);
         s.logs[warp][cl + kCpl - 1] = l.y;
       }
-      if (huge2(kCpl == 2 ? H : dup(H.x)) || huge2(kCpl == 2 ? Q : dup(Q.x))) s.odd[slot][0] = 1;
+      large = huge2(kCpl == 2 ? H : dup(H.x)) || huge2(kCpl == 2 ? Q : dup(Q.x));
     };
     if (far) first(std::integral_constant<int, kMixed>());
     else first(std::integral_constant<int, kSlow>());
-    __syncthreads();   // A: the warps' maps are there, and the sums of the tile before
+    // A: the warps' maps are there, and the sums of the tile before
+    const bool odd_maps = __syncthreads_or(large);
     // A box replaces a tile that every warp has left only now (its rows are read to the tile's end; a third
     // stage, asked for a tile earlier, took the L1 cache's room: 285 us instead of 215).
     if constexpr (ALIGN == kTma) load(s.places[next], slot ^ 1);
@@ -1064,8 +1057,8 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(const __gr
         s.partial_left = q.left;
       }
     };
-    if (rarely(s.odd[slot][0] != 0)) {
-      put_sum(odd_backward<T, ALIGN>(p, s, smem + slot * kStage, slot, here, true, it == 0));
+    if (rarely(odd_maps)) {
+      put_sum(odd_backward<T, ALIGN>(p, s, smem + slot * kStage, here, after, true, it == 0));
       continue;
     }
     if (warp == 0) {
@@ -1091,7 +1084,7 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(const __gr
         for (int c = 0; c < kCpl; ++c) v[c] = lookback::inclusive(lookback::apply_safe(A[c], Q[c], C[c]));
         lookback::publish(words, v);
       }
-      if (huge2(make_float2(C[0], C[kCpl - 1]))) s.odd[slot][1] = 1;
+      large = huge2(make_float2(C[0], C[kCpl - 1]));
       block_states<kWarps, kCpl, true>(s.back, s.after, cl, C);
 #pragma unroll
       for (int c = 0; c < kCpl; ++c) {
@@ -1101,8 +1094,7 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(const __gr
         }
       }
     } else if (warp == 1) {
-      fetch_backward(p, s, s.places[next].tile, next == 2 ? 0 : next + 1);
-      if (lane < 2) s.odd[slot ^ 1][lane] = 0;
+      fetch_backward(p, s, __shfl_sync(0xffffffffu, after, 0), next == 2 ? 0 : next + 1);
     } else if (warp == 2 && it > 0) {
       write_partial(p, s);
     }
@@ -1112,7 +1104,7 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(const __gr
         const float2 m0 = s.maps[k][cl], m1 = s.maps[k][cl + kCpl - 1];
         h = step<kMixed>(make_float2(m0.x, m1.x), make_float2(m0.y, m1.y), h);
       }
-      if (huge2(h)) s.odd[slot][1] = 1;
+      large = large || huge2(h);
       auto states = [&](auto form) {
         constexpr int F = decltype(form)::value;
 #pragma unroll
@@ -1132,9 +1124,9 @@ __global__ void __launch_bounds__(kThreads, MINB) rec_backward_kernel(const __gr
       if (far) states(std::integral_constant<int, kMixed>());
       else states(std::integral_constant<int, kSlow>());
     }
-    __syncthreads();   // B: C from the step after every warp's steps
-    if (rarely(s.odd[slot][1] != 0)) {
-      put_sum(odd_backward<T, ALIGN>(p, s, smem + slot * kStage, slot, here, false, false));
+    // B: C from the step after every warp's steps
+    if (rarely(__syncthreads_or(large))) {
+      put_sum(odd_backward<T, ALIGN>(p, s, smem + slot * kStage, here, after, false, false));
       continue;
     }
     float2 C = make_float2(s.after[warp][cl], s.after[warp][cl + kCpl - 1]), sum = make_float2(0.f, 0.f);

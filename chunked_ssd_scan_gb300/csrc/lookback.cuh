@@ -9,10 +9,11 @@
 // one: c <= -kTiny.
 //
 // A tile's word is 64 bits: H in the low half, c, with |c| <= 1, in the high half, whose bit 30 (the top bit of
-// the exponent) is free and set.  Without it the high half is 0 for nothing (the words are cleared before
-// the launch) or 1 for an inclusive word (H is the state after the tile).  A reader evaluates the maps
-// from the nearest inclusive word on, oldest first, with the very operations that made the inclusive
-// words: the result has the same bits wherever it starts.
+// the exponent) is free and set in every word that holds anything (the words are cleared before the
+// launch).  An inclusive word, whose H is the state after the tile, has c = -0, which no map has: as a map
+// it gives H whatever came before.  A reader evaluates the maps from the nearest inclusive word on,
+// oldest first, with the very operations that made the inclusive words: the result has the same bits
+// wherever it starts.
 #pragma once
 
 #include "common.cuh"
@@ -21,12 +22,12 @@
 namespace ssd {
 namespace lookback {
 
-constexpr uint32_t kMap = 1u << 30, kInclusive = 1u;
+constexpr uint32_t kMap = 1u << 30, kInclusive = 3u << 30;
 constexpr float kInf = __builtin_huge_valf();
 
-// a h + H.  NaN for an infinite h next to one (inf - inf) and where a is 0.
+// a h + H.  NaN for an infinite h: inf - inf next to one, 0 inf where a is small.
 __device__ __forceinline__ float apply(float c, float H, float h) {
-  return fmaf(c, h, H) + (c < 0.f ? h : 0.f);
+  return fmaf(c < 0.f ? 1.f : 0.f, h, fmaf(c, h, H));
 }
 // The same, but an infinite h stays what it is (no decay is zero, if fp32 makes it so).  Where the results of
 // a chain of apply are not NaN, this chain's are the same.
@@ -62,8 +63,8 @@ __device__ __forceinline__ uint64_t now_ns() {
 // how many older tiles there are (at least one).  A try reads the K nearest words at once; the nearest is
 // enough if it is inclusive, and the others are evaluated only once it holds anything.  The wait is
 // bounded (1 s, then SSD_ERR_TIMEOUT is latched and the call's results are void).  Maps evaluated behind an
-// infinite state may give a NaN that is none: with a NaN the try is not over before the nearest is
-// inclusive.
+// infinite state, inclusive ones among them, may give a NaN that is none: with a NaN the try is not over
+// before the nearest is inclusive.
 template <int K, int N>
 __device__ __forceinline__ void state_before(const uint64_t* words, int64_t step, int64_t have, float (&h)[N],
                                              WsHeader* hdr, int64_t site) {
@@ -98,7 +99,7 @@ __device__ __forceinline__ void state_before(const uint64_t* words, int64_t step
         for (int j = K - 1; j >= 0; --j) {
           const uint32_t hi = (uint32_t)(v[j][c] >> 32);
           const float H = __uint_as_float((uint32_t)v[j][c]), a = __uint_as_float(hi & ~kMap);
-          h[c] = hi == kInclusive ? H : apply(a, H, h[c]);
+          h[c] = apply(a, H, h[c]);
           ok = hi == kInclusive || (ok && hi != 0);
         }
         all = all && ok && h[c] == h[c];
