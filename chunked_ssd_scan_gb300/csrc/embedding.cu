@@ -76,7 +76,8 @@ __global__ void __launch_bounds__(kThreads) embed_forward_kernel(const Id* ids, 
 // Backward.
 //
 // 1. The tokens are sorted by id, stably, so that a row's tokens stand together in their order: a radix
-//    sort of 8 bits a pass, the padding's key behind all rows.  It is short of work, so its launches,
+//    sort of 8 bits a pass, least significant digit first (Knuth, The Art of Computer Programming 3, 5.2.5),
+//    the padding's key behind all rows.  It is short of work, so its launches,
 //    like the others, take along the clearing of rows that no token has.
 // 2. A subgroup of threads takes kPiece sorted tokens and adds their rows, writing each row's sum as its
 //    run ends; a run that goes on over the ends of a piece leaves partial sums instead,

@@ -94,7 +94,7 @@ __device__ __forceinline__ bool rarely(bool v) { return __builtin_expect(v, 0); 
 // second walk over the registers writes y.  Every input byte is read once.
 //
 // 8 x 4096 x 2048 bf16 with states: 103 us, 5.3 TB/s of 541 MB (78 % of the measured copy rate), with the
-// special-function unit (4 a value) and the issue slots (33 instructions a value) each busy more than half
+// special-function unit (4 a value) and the issue slots (31 instructions a value) each busy more than half
 // of the time; 1 x 131072 x 1024 f32: 355 us, 6.1 TB/s (89 %).
 // ------------------------------------------------------------------------------------------------
 constexpr int kWarps = 8;
@@ -105,7 +105,7 @@ constexpr float kTiny = 1e-36f;   // well above the smallest normal number (the 
 
 // Special functions by approximation: 1/x is good to 2^-23, 2^x and 1/sqrt x to 2^-22, and v log2 e adds |v| 2^-23
 // to e^v, so a sigmoid s is good to about 2^-21 + (1 - s) |v| 2^-23.  The exact functions are several
-// instructions each, of which the kernels issue 33 and 62 a value in all.
+// instructions each, of which the kernels issue 31 and 62 a value in all.
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
