@@ -28,7 +28,10 @@ __all__ = [
     "GatedRecurrencePlan", "GatedRecurrenceBackwardPlan", "GatedRecurrenceStepPlan",
     "GATED_RECURRENCE_CHUNK", "group_norm_forward", "group_norm_backward", "GroupNormPlan",
     "GroupNormBackwardPlan", "embedding_forward", "embedding_backward", "EmbeddingPlan",
-    "EmbeddingBackwardPlan",
+    "EmbeddingBackwardPlan", "gated_delta_rule_forward", "gated_delta_rule_backward",
+    "gated_delta_rule_step", "GatedDeltaRulePlan", "GatedDeltaRuleBackwardPlan",
+    "GatedDeltaRuleStepPlan", "GATED_DELTA_RULE_CHUNK", "rms_norm_forward", "rms_norm_backward",
+    "RMSNormPlan", "RMSNormBackwardPlan", "RMS_NORM_BLOCK", "token_sample", "TokenSamplePlan",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -634,7 +637,11 @@ def workspace_status(workspace: torch.Tensor, stream=None):
 
 from . import lm_ops  # noqa: E402  (uses the helpers above)
 from .lm_ops import (  # noqa: E402,F401
-    GATED_RECURRENCE_CHUNK, EmbeddingBackwardPlan, EmbeddingPlan, GatedRecurrenceBackwardPlan,
-    GatedRecurrencePlan, GatedRecurrenceStepPlan, GroupNormBackwardPlan, GroupNormPlan,
-    embedding_backward, embedding_forward, gated_recurrence_backward, gated_recurrence_forward,
-    gated_recurrence_step, group_norm_backward, group_norm_forward)
+    GATED_DELTA_RULE_CHUNK, GATED_RECURRENCE_CHUNK, RMS_NORM_BLOCK, EmbeddingBackwardPlan,
+    EmbeddingPlan, GatedDeltaRuleBackwardPlan, GatedDeltaRulePlan, GatedDeltaRuleStepPlan,
+    GatedRecurrenceBackwardPlan, GatedRecurrencePlan, GatedRecurrenceStepPlan,
+    GroupNormBackwardPlan, GroupNormPlan, RMSNormBackwardPlan, RMSNormPlan, TokenSamplePlan,
+    embedding_backward, embedding_forward, gated_delta_rule_backward, gated_delta_rule_forward,
+    gated_delta_rule_step, gated_recurrence_backward, gated_recurrence_forward,
+    gated_recurrence_step, group_norm_backward, group_norm_forward, rms_norm_backward,
+    rms_norm_forward, token_sample)

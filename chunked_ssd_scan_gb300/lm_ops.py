@@ -1,6 +1,7 @@
 """Operators around a scan in a recurrent language model: the gated linear recurrence, the
-channels-last group norm with an activation and the token embedding (declarations and contracts
-in include/ssdscan.h).
+channels-last group norm with an activation, the token embedding, the gated delta rule, the
+root-mean-square norm with the residual's addition and an 8-bit output, and the drawing of tokens
+(declarations and contracts in include/ssdscan.h).
 
 Every operator is a function and a plan.  A plan checks its arguments, allocates outputs and
 workspace once and makes only the C call when it is called; the function makes a plan and calls it.
@@ -31,7 +32,14 @@ GATED_RECURRENCE_CHUNK = 64
 #: Bytes at the start of a workspace that are zero before its first call.
 HEADER_BYTES = 256
 
+#: Steps between the states that the delta rule keeps for its backward pass.
+GATED_DELTA_RULE_CHUNK = 64
+
+#: Channels that share a scale where the norm's 8-bit output has scales for blocks.
+RMS_NORM_BLOCK = 128
+
 ACTIVATIONS = {None: 0, "none": 0, "silu": 1}
+QUANTIZE = {None: 0, "none": 0, "token": 1, "block": 2}
 _IO = {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16}
 
 
@@ -47,11 +55,42 @@ class group_norm_shape(ctypes.Structure):
                 ("activation", ctypes.c_int32), ("io_dtype", ctypes.c_int32)]
 
 
+class gated_delta_rule_shape(ctypes.Structure):
+    _fields_ = [("batch", _I64), ("seqlen", _I64), ("key_heads", _I64), ("heads", _I64),
+                ("key_dim", _I64), ("value_dim", _I64), ("q_stride", _I64 * 3),
+                ("k_stride", _I64 * 3), ("v_stride", _I64 * 3), ("dy_stride", _I64 * 3),
+                ("g_stride", _I64 * 2), ("beta_stride", _I64 * 2), ("scale", ctypes.c_float),
+                ("io_dtype", ctypes.c_int32)]
+
+
+class rms_norm_shape(ctypes.Structure):
+    _fields_ = [("rows", _I64), ("channels", _I64), ("x_stride", _I64), ("res_stride", _I64),
+                ("dy_stride", _I64), ("eps", ctypes.c_float), ("quantize", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32)]
+
+
+class token_sample_shape(ctypes.Structure):
+    _fields_ = [("rows", _I64), ("vocab", _I64), ("logits_stride", _I64),
+                ("temperature", ctypes.c_float), ("top_p", ctypes.c_float),
+                ("min_p", ctypes.c_float), ("top_k", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32)]
+
+
 def _declare(lib) -> None:
     """Result and argument types of this module's C functions."""
     size, i32, f32 = ctypes.c_size_t, ctypes.c_int32, ctypes.c_float
     R, G = ctypes.POINTER(gated_recurrence_shape), ctypes.POINTER(group_norm_shape)
+    D, N = ctypes.POINTER(gated_delta_rule_shape), ctypes.POINTER(rms_norm_shape)
+    S = ctypes.POINTER(token_sample_shape)
     for name, res, args in (
+            ("gated_delta_rule_workspace_bytes", size, [D, i32]),
+            ("gated_delta_rule_forward", ctypes.c_int, [D] + [_VP] * 10 + [size, _VP]),
+            ("gated_delta_rule_backward", ctypes.c_int, [D] + [_VP] * 16 + [size, _VP]),
+            ("gated_delta_rule_step", ctypes.c_int, [D] + [_VP] * 9),
+            ("rms_norm_workspace_bytes", size, [N]),
+            ("rms_norm_forward", ctypes.c_int, [N] + [_VP] * 8),
+            ("rms_norm_backward", ctypes.c_int, [N] + [_VP] * 8 + [size, _VP]),
+            ("token_sample", ctypes.c_int, [S] + [_VP] * 9),
             ("gated_recurrence_workspace_bytes", size, [R, i32]),
             ("gated_recurrence_forward", ctypes.c_int, [R] + [_VP] * 9 + [size, _VP]),
             ("gated_recurrence_backward", ctypes.c_int, [R] + [_VP] * 14 + [size, _VP]),
@@ -497,3 +536,376 @@ def embedding_backward(ids, dout, num_rows: int, *, scale: float = 1.0, dtable=N
     the ids (the same bits every run)."""
     return EmbeddingBackwardPlan(ids, dout, num_rows, scale=scale, dtable=dtable,
                                  workspace=workspace, stream=stream)()
+
+
+def _strides3(t, axes):
+    """Strides of three axes; an axis of one element (or none) has stride 0."""
+    return (_I64 * 3)(*(0 if a is None or t.shape[a] <= 1 else t.stride(a) for a in axes))
+
+
+def _check_delta(q, k, v, g, beta, init_state, scale, step=False):
+    lead = "[b" if step else "[b,T"
+    if not isinstance(q, torch.Tensor) or q.dim() != (3 if step else 4):
+        raise ValueError(f"q must be {lead},Hk,K]")
+    if not isinstance(v, torch.Tensor) or v.dim() != q.dim():
+        raise ValueError(f"v must be {lead},H,V]")
+    _io_dtype("q", q)
+    Hk, K, H, V = *q.shape[-2:], *v.shape[-2:]
+    if min(Hk, K, H, V) < 1 or H % Hk:
+        raise ValueError(f"the {Hk} key heads must divide the {H} heads, and no head be empty")
+    if K > 256:
+        raise ValueError(f"a key head has at most 256 channels, got {K}")
+    _check_rows("q", q, None, q.shape)
+    _check_rows("k", k, q.dtype, q.shape)
+    _check_rows("v", v, q.dtype, (*q.shape[:-2], H, V))
+    for name, t in (("g", g), ("beta", beta)):
+        if t is not None or name == "beta":
+            _check_rows(name, t, torch.float32, (*q.shape[:-2], H))
+    if init_state is not None:
+        _check_cuda("init_state", init_state, torch.float32, (q.shape[0], H, V, K))
+    scale = K ** -0.5 if scale is None else float(scale)
+    if not math.isfinite(scale):
+        raise ValueError(f"scale must be finite, got {scale}")
+    return scale
+
+
+def _delta_shape(q, k, v, g, beta, dy, scale, step=False) -> gated_delta_rule_shape:
+    axes = (0, None, 1) if step else (0, 1, 2)
+    three = lambda t: _strides3(t, axes)   # noqa: E731
+    two = lambda t: (_I64 * 2)(*_strides3(t, (*axes[:2], None))[:2])   # noqa: E731
+    return gated_delta_rule_shape(
+        q.shape[0], 1 if step else q.shape[1], q.shape[-2], v.shape[-2], q.shape[-1], v.shape[-1],
+        three(q), three(k), three(v), (_I64 * 3)() if dy is None else three(dy),
+        (_I64 * 2)() if g is None else two(g), two(beta), scale, _IO[q.dtype])
+
+
+class GatedDeltaRulePlan(_Plan):
+    """Arguments of ``gated_delta_rule_forward`` checked once, for repeated calls on the same
+    buffers; calling the plan returns (y, final_state, states)."""
+
+    _name = "gated_delta_rule_forward"
+
+    def __init__(self, q, k, v, g, beta, *, scale: Optional[float] = None, init_state=None, y=None,
+                 final_state=None, return_final_state: bool = True, states=None,
+                 return_states: bool = False, workspace=None, stream=None):
+        scale = _check_delta(q, k, v, g, beta, init_state, scale)
+        b, T, H, V = v.shape
+        K = q.shape[-1]
+        self.shape = _delta_shape(q, k, v, g, beta, None, scale)
+        with self._begin(q.device, stream):
+            self.y = self._out("y", y, q.dtype, (b, T, H, V))
+            if return_final_state or final_state is not None:
+                final_state = self._out("final_state", final_state, torch.float32, (b, H, V, K))
+            if return_states or states is not None:
+                states = self._out("states", states, torch.float32,
+                                   (b, -(-T // GATED_DELTA_RULE_CHUNK), H, V, K))
+            need = int(self._lib.gated_delta_rule_workspace_bytes(ctypes.byref(self.shape), 0))
+            self.workspace = self._workspace(workspace, need, "gated_delta_rule_workspace_bytes")
+        self.final_state, self.states = final_state, states
+        self._finish((q, k, v, g, beta, init_state),
+                     (ctypes.byref(self.shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+                      _ptr(init_state), _ptr(self.y), _ptr(final_state), _ptr(states),
+                      _ptr(self.workspace), ctypes.c_size_t(self.workspace.numel())))
+
+    def __call__(self):
+        self._call()
+        return self.y, self.final_state, self.states
+
+
+def gated_delta_rule_forward(q, k, v, g, beta, *, scale: Optional[float] = None, init_state=None,
+                             y=None, final_state=None, return_final_state: bool = True,
+                             states=None, return_states: bool = False, workspace=None,
+                             stream=None):
+    """Gated delta rule through ``gated_delta_rule_forward``, for every sequence and head a state
+    S [V,K]:
+
+        S = exp(g_t) S;  S = S + beta_t (v_t - S k_t) k_t^T;  y_t = scale S q_t
+
+    q, k [b,T,Hk,K] and v [b,T,H,V] (all f32 or all bf16; any strides with a contiguous last axis;
+    head h reads q and k of h // (H / Hk)), g (None: zeros) and beta [b,T,H] f32, init_state
+    [b,H,V,K] f32; scale is K^-1/2 unless given.  Returns (y, final_state, states): y [b,T,H,V] in
+    q's dtype, final_state f32 and, with ``return_states``, the states [b, ceil(T/64), H, V, K] f32
+    that ``gated_delta_rule_backward`` takes (None where not requested)."""
+    return GatedDeltaRulePlan(q, k, v, g, beta, scale=scale, init_state=init_state, y=y,
+                              final_state=final_state, return_final_state=return_final_state,
+                              states=states, return_states=return_states, workspace=workspace,
+                              stream=stream)()
+
+
+class GatedDeltaRuleBackwardPlan(_Plan):
+    """Arguments of ``gated_delta_rule_backward`` checked once; calling the plan returns the dict
+    dq, dk, dv (q's dtype), dg (None where g is), dbeta and dinit (f32; None unless
+    return_dinit)."""
+
+    _name = "gated_delta_rule_backward"
+
+    def __init__(self, q, k, v, g, beta, dy, *, scale: Optional[float] = None, init_state=None,
+                 states=None, dfinal=None, return_dinit: bool = True,
+                 grads: Optional[dict] = None, workspace=None, stream=None):
+        scale = _check_delta(q, k, v, g, beta, init_state, scale)
+        b, T, H, V = v.shape
+        K = q.shape[-1]
+        _check_rows("dy", dy, q.dtype, v.shape)
+        if states is not None:
+            _check_cuda("states", states, torch.float32,
+                        (b, -(-T // GATED_DELTA_RULE_CHUNK), H, V, K))
+        if dfinal is not None:
+            _check_cuda("dfinal", dfinal, torch.float32, (b, H, V, K))
+        self.shape = _delta_shape(q, k, v, g, beta, dy, scale)
+        out = dict(grads or {})
+        with self._begin(q.device, stream):
+            for name, like in (("dq", q), ("dk", q), ("dv", v)):
+                out[name] = self._out(name, out.get(name), q.dtype, tuple(like.shape))
+            out["dg"] = (None if g is None else
+                         self._out("dg", out.get("dg"), torch.float32, (b, T, H)))
+            out["dbeta"] = self._out("dbeta", out.get("dbeta"), torch.float32, (b, T, H))
+            out["dinit"] = (self._out("dinit", out.get("dinit"), torch.float32, (b, H, V, K))
+                            if return_dinit else None)
+            need = int(self._lib.gated_delta_rule_workspace_bytes(ctypes.byref(self.shape), 1))
+            self.workspace = self._workspace(workspace, need, "gated_delta_rule_workspace_bytes")
+        self.grads = out
+        self._finish((q, k, v, g, beta, dy, init_state, states, dfinal),
+                     (ctypes.byref(self.shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+                      _ptr(init_state), _ptr(states), _ptr(dy), _ptr(dfinal), _ptr(out["dq"]),
+                      _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["dbeta"]),
+                      _ptr(out["dinit"]), _ptr(self.workspace),
+                      ctypes.c_size_t(self.workspace.numel())))
+
+    def __call__(self):
+        self._call()
+        return self.grads
+
+
+def gated_delta_rule_backward(q, k, v, g, beta, dy, *, scale: Optional[float] = None,
+                              init_state=None, states=None, dfinal=None,
+                              return_dinit: bool = True, grads=None, workspace=None, stream=None):
+    """Gradients of <dy, y> + <dfinal, final_state> for ``gated_delta_rule_forward`` on the same
+    inputs.  ``states`` is what the forward kept (``return_states``); without it the call recomputes
+    it.  Returns a dict dq, dk (summed over the heads that share them), dv, dg, dbeta, dinit."""
+    return GatedDeltaRuleBackwardPlan(q, k, v, g, beta, dy, scale=scale, init_state=init_state,
+                                      states=states, dfinal=dfinal, return_dinit=return_dinit,
+                                      grads=grads, workspace=workspace, stream=stream)()
+
+
+class GatedDeltaRuleStepPlan(_Plan):
+    """Arguments of ``gated_delta_rule_step`` checked once; calling the plan returns (y, state_out).
+    Without ``state_out`` the state is updated in place."""
+
+    _name = "gated_delta_rule_step"
+
+    def __init__(self, q, k, v, g, beta, state, *, scale: Optional[float] = None, y=None,
+                 state_out=None, stream=None):
+        if state is None:
+            raise ValueError("state must be a [b,H,V,K] float32 tensor")
+        scale = _check_delta(q, k, v, g, beta, state, scale, step=True)
+        self.shape = _delta_shape(q, k, v, g, beta, None, scale, step=True)
+        with self._begin(q.device, stream):
+            self.y = self._out("y", y, q.dtype, tuple(v.shape))
+            self.state_out = self._out("state_out", state if state_out is None else state_out,
+                                       torch.float32, tuple(state.shape))
+        self._finish((q, k, v, g, beta, state),
+                     (ctypes.byref(self.shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+                      _ptr(state), _ptr(self.y), _ptr(self.state_out)))
+
+    def __call__(self):
+        self._call()
+        return self.y, self.state_out
+
+
+def gated_delta_rule_step(q, k, v, g, beta, state, *, scale: Optional[float] = None, y=None,
+                          state_out=None, stream=None):
+    """One step of the rule for every sequence of a batch (serving): q, k [b,Hk,K], v [b,H,V], g
+    (None: zeros), beta [b,H], state [b,H,V,K] f32, updated in place unless ``state_out`` is given.
+    Returns (y, state)."""
+    return GatedDeltaRuleStepPlan(q, k, v, g, beta, state, scale=scale, y=y, state_out=state_out,
+                                  stream=stream)()
+
+
+def _row_view(name, t, like=None):
+    """t as [N,C] without a copy: [N,C] with any row stride, or contiguous [...,C]."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if like is not None and tuple(t.shape) != tuple(like.shape):
+        raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
+    if t.dim() < 1 or t.shape[-1] < 1:
+        raise ValueError(f"{name} must be [...,C] with at least one channel")
+    if t.dim() == 2:
+        return t
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous (or [N,C] with a contiguous last axis)")
+    return t.view(math.prod(t.shape[:-1]), t.shape[-1])
+
+
+def _rms_shape(x, res, dy, eps, quantize) -> rms_norm_shape:
+    stride = lambda t: 0 if t is None or t.shape[0] <= 1 else t.stride(0)   # noqa: E731
+    return rms_norm_shape(*x.shape, stride(x), stride(res), stride(dy), float(eps),
+                          QUANTIZE[quantize], _IO[x.dtype])
+
+
+class RMSNormPlan(_Plan):
+    """Arguments of ``rms_norm_forward`` checked once; calling the plan returns (y, h, rstd,
+    scale)."""
+
+    _name = "rms_norm_forward"
+
+    def __init__(self, x, weight=None, *, residual=None, eps: float = 1e-6,
+                 quantize: Optional[str] = None, y=None, h=None, rstd=None, scale=None,
+                 stream=None):
+        v = _row_view("x", x)
+        _io_dtype("x", x)
+        _check_rows("x", v, None, v.shape)
+        r = None
+        if residual is not None:
+            r = _row_view("residual", residual, x)
+            _check_rows("residual", r, x.dtype, v.shape)
+        if quantize not in QUANTIZE:
+            raise ValueError(f"quantize must be one of {sorted(map(str, QUANTIZE))}")
+        if not (eps >= 0 and math.isfinite(eps)):
+            raise ValueError(f"eps must be finite and not negative, got {eps}")
+        N, C = v.shape
+        if weight is not None:
+            _check_cuda("weight", weight, torch.float32, (C,))
+        kind = QUANTIZE[quantize]
+        if scale is not None and not kind:
+            raise ValueError("scale is an output of an 8-bit y only")
+        self.shape = _rms_shape(v, r, None, eps, quantize)
+        with self._begin(x.device, stream):
+            self.y = self._out("y", y, torch.float8_e4m3fn if kind else x.dtype, tuple(x.shape))
+            if residual is not None or h is not None:
+                h = self._out("h", h, x.dtype, tuple(x.shape))
+            self.rstd = self._out("rstd", rstd, torch.float32, tuple(x.shape[:-1]))
+            if kind:
+                scale = self._out("scale", scale, torch.float32,
+                                  (*x.shape[:-1], 1 if kind == 1 else -(-C // RMS_NORM_BLOCK)))
+        self.h, self.scale = h, scale
+        self._finish((x, residual, weight),
+                     (ctypes.byref(self.shape), _ptr(x), _ptr(residual), _ptr(weight),
+                      _ptr(self.y), _ptr(h), _ptr(self.rstd), _ptr(scale)))
+
+    def __call__(self):
+        self._call()
+        return self.y, self.h, self.rstd, self.scale
+
+
+def rms_norm_forward(x, weight=None, *, residual=None, eps: float = 1e-6,
+                     quantize: Optional[str] = None, y=None, h=None, rstd=None, scale=None,
+                     stream=None):
+    """Root-mean-square norm of every row, after the residual's addition, through
+    ``rms_norm_forward``:
+
+        h = x + residual;  y = h / sqrt(mean(h^2) + eps) * weight
+
+    x and residual [N,C] (any row stride) or contiguous [...,C], f32 or bf16; weight [C] f32 (None:
+    ones).  Returns (y, h, rstd, scale): h (None without a residual) is the sum in x's dtype, the
+    residual of the next layer; rstd [...] f32 is for ``rms_norm_backward``.  With ``quantize``
+    "token" or "block" y is float8_e4m3fn and stands for y * scale, with a scale f32 [...,1] for
+    every row or [..., ceil(C/128)] for every 128 channels (None otherwise)."""
+    return RMSNormPlan(x, weight, residual=residual, eps=eps, quantize=quantize, y=y, h=h,
+                       rstd=rstd, scale=scale, stream=stream)()
+
+
+class RMSNormBackwardPlan(_Plan):
+    """Arguments of ``rms_norm_backward`` checked once; calling the plan returns the dict dx (h's
+    dtype) and dweight (f32; None without ``param_grads``)."""
+
+    _name = "rms_norm_backward"
+
+    def __init__(self, h, dy, rstd, weight=None, *, dresidual=None, param_grads: bool = True,
+                 grads: Optional[dict] = None, workspace=None, stream=None):
+        v = _row_view("h", h)
+        _io_dtype("h", h)
+        _check_rows("h", v, None, v.shape)
+        d = _row_view("dy", dy, h)
+        _check_rows("dy", d, h.dtype, v.shape)
+        r = None
+        if dresidual is not None:
+            r = _row_view("dresidual", dresidual, h)
+            _check_rows("dresidual", r, h.dtype, v.shape)
+        N, C = v.shape
+        _check_cuda("rstd", rstd, torch.float32, tuple(h.shape[:-1]))
+        if weight is not None:
+            _check_cuda("weight", weight, torch.float32, (C,))
+        self.shape = _rms_shape(v, r, d, 0.0, None)
+        g = dict(grads or {})
+        with self._begin(h.device, stream):
+            g["dx"] = self._out("dx", g.get("dx"), h.dtype, tuple(h.shape))
+            g["dweight"] = (self._out("dweight", g.get("dweight"), torch.float32, (C,))
+                            if param_grads else None)
+            need = int(self._lib.rms_norm_workspace_bytes(ctypes.byref(self.shape)))
+            self.workspace = self._workspace(workspace, need, "rms_norm_workspace_bytes")
+        self.grads = g
+        self._finish((h, dy, rstd, weight, dresidual),
+                     (ctypes.byref(self.shape), _ptr(h), _ptr(dy), _ptr(rstd), _ptr(weight),
+                      _ptr(dresidual), _ptr(g["dx"]), _ptr(g["dweight"]), _ptr(self.workspace),
+                      ctypes.c_size_t(self.workspace.numel())))
+
+    def __call__(self):
+        self._call()
+        return self.grads
+
+
+def rms_norm_backward(h, dy, rstd, weight=None, *, dresidual=None, param_grads: bool = True,
+                      grads=None, workspace=None, stream=None):
+    """Gradients of <dy, y> + <dresidual, h> for ``rms_norm_forward``; h and rstd are what it
+    returned (h is x where there was no residual).  Returns a dict dx, the gradient of x and of the
+    residual alike, and dweight."""
+    return RMSNormBackwardPlan(h, dy, rstd, weight, dresidual=dresidual, param_grads=param_grads,
+                               grads=grads, workspace=workspace, stream=stream)()
+
+
+class TokenSamplePlan(_Plan):
+    """Arguments of ``token_sample`` checked once; calling the plan returns (ids, logprob)."""
+
+    _name = "token_sample"
+
+    def __init__(self, logits, u, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, ids=None,
+                 logprob=None, stream=None):
+        if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+            raise ValueError("logits must be [n,V]")
+        _io_dtype("logits", logits)
+        _check_rows("logits", logits, None, logits.shape)
+        n, V = logits.shape
+        if not 1 <= V <= 1 << 20:
+            raise ValueError(f"logits must have 1 to {1 << 20} columns, got {V}")
+        _check_cuda("u", u, torch.float32, (n,))
+        given, plain = {}, {}
+        for name, t, none, dtype in (("temperature", temperature, 1.0, torch.float32),
+                                     ("top_k", top_k, 0, torch.int32),
+                                     ("top_p", top_p, 1.0, torch.float32),
+                                     ("min_p", min_p, 0.0, torch.float32)):
+            given[name] = t if isinstance(t, torch.Tensor) else None
+            plain[name] = none if t is None or given[name] is not None else t
+            if given[name] is not None:
+                _check_cuda(name, t, dtype, (n,))
+        if not plain["temperature"] >= 0:
+            raise ValueError(f"temperature must not be negative, got {temperature}")
+        if plain["top_p"] != plain["top_p"] or plain["min_p"] != plain["min_p"]:
+            raise ValueError("top_p and min_p must be numbers")
+        self.shape = token_sample_shape(
+            n, V, logits.stride(0) if n > 1 else 0, float(plain["temperature"]),
+            float(plain["top_p"]), float(plain["min_p"]), min(max(int(plain["top_k"]), 0), V),
+            _IO[logits.dtype])
+        with self._begin(logits.device, stream):
+            self.ids = self._out("ids", ids, torch.int64, (n,))
+            self.logprob = self._out("logprob", logprob, torch.float32, (n,))
+        self._finish((logits, u, *given.values()),
+                     (ctypes.byref(self.shape), _ptr(logits), _ptr(u),
+                      *(_ptr(given[k]) for k in ("temperature", "top_k", "top_p", "min_p")),
+                      _ptr(self.ids), _ptr(self.logprob)))
+
+    def __call__(self):
+        self._call()
+        return self.ids, self.logprob
+
+
+def token_sample(logits, u, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, ids=None,
+                 logprob=None, stream=None):
+    """Draws one token for every row of logits [n,V] (f32 or bf16) from random numbers u [n] f32 in
+    [0,1) through ``token_sample``.  Of the tokens by falling logit (equal ones by rising index) a
+    row keeps the first ``top_k`` (<= 0: all), of these those of at least ``min_p`` times the
+    largest probability, of these the fewest that hold ``top_p`` of their sum; the token drawn is
+    the first by index at which the running sum of the kept weights exp(logit / temperature)
+    exceeds u times their sum.  Temperature 0 takes the largest logit.  Each setting is a number or
+    a tensor [n] (top_k int32, the others f32).  Returns (ids [n] int64, logprob [n] f32)."""
+    return TokenSamplePlan(logits, u, temperature=temperature, top_k=top_k, top_p=top_p,
+                           min_p=min_p, ids=ids, logprob=logprob, stream=stream)()

@@ -519,6 +519,158 @@ ssd_status embedding_backward(const void* ids, int32_t ids_bits, int64_t n, cons
                               float* dtable, void* workspace, size_t workspace_bytes,
                               void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Gated delta rule, root-mean-square norm and token sampling, under the rules of the operators
+ * above.
+ * ------------------------------------------------------------------------------------------ */
+
+/* Steps between the states that gated_delta_rule_forward keeps for the backward pass. */
+#define GATED_DELTA_RULE_CHUNK 64
+
+typedef struct gated_delta_rule_shape {
+  int64_t batch;         /* b >= 0 */
+  int64_t seqlen;        /* T >= 0 */
+  int64_t key_heads;     /* Hk >= 1, divides heads: head h reads q and k of h / (H / Hk) */
+  int64_t heads;         /* H >= 1 */
+  int64_t key_dim;       /* K, 1 .. 256 */
+  int64_t value_dim;     /* V >= 1 */
+  int64_t q_stride[3];   /* of the batch axis, the step axis and the head axis, >= 0 */
+  int64_t k_stride[3];
+  int64_t v_stride[3];
+  int64_t dy_stride[3];  /* gated_delta_rule_backward only */
+  int64_t g_stride[2];   /* of the batch axis and the step axis */
+  int64_t beta_stride[2];
+  float scale;           /* of the output, finite */
+  int32_t io_dtype;      /* ssd_dtype of q, k, v, y, dy, dq, dk and dv */
+} gated_delta_rule_shape;
+
+/*
+ * Bytes of device workspace (256-byte aligned, the first 256 bytes zero before the first call) that
+ * gated_delta_rule_forward (backward = 0) or gated_delta_rule_backward (backward = 1) needs; 0 if
+ * the shape is invalid or not supported.
+ */
+size_t gated_delta_rule_workspace_bytes(const gated_delta_rule_shape* shape, int32_t backward);
+
+/*
+ * Gated delta rule, for every sequence b and head h with a state S [V, K]:
+ *   S  = exp(g[b,t,h]) S;   u = beta[b,t,h] (v[b,t,h] - S k[b,t,h']);   S = S + u k[b,t,h']^T
+ *   y[b,t,h] = scale S q[b,t,h'],   h' = h / (H / Hk)
+ * q, k [b,T,Hk,K], v [b,T,H,V] strided, y [b,T,H,V] contiguous, all io_dtype; g (NULL = zeros) and
+ * beta [b,T,H] f32 strided; init_state (NULL = zeros) and final_state (NULL = not written)
+ * [b,H,V,K] f32.  states: NULL, or f32 [b, ceil(T / GATED_DELTA_RULE_CHUNK), H, V, K] that receives
+ * the state before steps 0, 64, 128, ... for gated_delta_rule_backward.  y may be NULL.
+ * g below -200 is a decay of zero, as in fp32.  States and sums are fp32.  With bf16 inputs whose K
+ * and V are multiples of 8 and whose rows start on 16-byte boundaries, sequences longer than a few
+ * steps run on the tensor cores, where what is computed on the way (the state, the writes, the inverse
+ * of a chunk's triangular system) enters a product as two bf16 terms, 16 bits of mantissa.
+ * Asynchronous on `stream`; INVALID_ARG / UNSUPPORTED / WORKSPACE leave every output untouched.
+ */
+ssd_status gated_delta_rule_forward(const gated_delta_rule_shape* shape, const void* q,
+                                    const void* k, const void* v, const float* g,
+                                    const float* beta, const float* init_state, void* y,
+                                    float* final_state, float* states, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/*
+ * Reverse mode of gated_delta_rule_forward for the loss <dy, y> + <dfinal, final_state>:
+ *   dq, dk [b,T,Hk,K] (summed over the heads that share them), dv [b,T,H,V] io_dtype contiguous;
+ *   dg (may be NULL), dbeta [b,T,H] f32 contiguous; dinit [b,H,V,K] f32 (may be NULL).
+ * dy strided io_dtype, dfinal [b,H,V,K] f32 (NULL = zeros).  states: what the forward kept, or NULL
+ * (the call then recomputes them in its workspace).  Sums run in a fixed order: the same bits every
+ * run.
+ */
+ssd_status gated_delta_rule_backward(const gated_delta_rule_shape* shape, const void* q,
+                                     const void* k, const void* v, const float* g,
+                                     const float* beta, const float* init_state,
+                                     const float* states, const void* dy, const float* dfinal,
+                                     void* dq, void* dk, void* dv, float* dg, float* dbeta,
+                                     float* dinit, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
+/*
+ * One step of the rule for every sequence of a batch (serving): shape->seqlen must be 1 and the step
+ * strides are ignored.  state [b,H,V,K] f32 is read (NULL = zeros), state_out receives the new state
+ * and may be the same buffer as state.  y [b,H,V] io_dtype.
+ */
+ssd_status gated_delta_rule_step(const gated_delta_rule_shape* shape, const void* q, const void* k,
+                                 const void* v, const float* g, const float* beta,
+                                 const float* state, void* y, float* state_out, void* stream);
+
+/* What rms_norm_forward writes as y: io_dtype, or 8 bits (1 sign, 4 exponent, 3 mantissa bits, largest
+ * value 448) with an f32 scale for every row or for every 128 channels of a row. */
+typedef enum ssd_quantize { SSD_QUANT_NONE = 0, SSD_QUANT_TOKEN = 1, SSD_QUANT_BLOCK = 2 } ssd_quantize;
+#define RMS_NORM_BLOCK 128
+
+typedef struct rms_norm_shape {
+  int64_t rows;         /* N >= 0 */
+  int64_t channels;     /* C >= 1 */
+  int64_t x_stride;     /* of the row axis, >= 0 (backward: of h) */
+  int64_t res_stride;   /* of residual (backward: of dresidual) */
+  int64_t dy_stride;    /* rms_norm_backward only */
+  float eps;            /* >= 0 and finite */
+  int32_t quantize;     /* ssd_quantize; rms_norm_forward only */
+  int32_t io_dtype;     /* ssd_dtype of x, residual, h, y (unless quantized), dy, dresidual, dx */
+} rms_norm_shape;
+
+/* Bytes of device workspace of rms_norm_backward, under the rules of
+ * gated_delta_rule_workspace_bytes (the forward needs none). */
+size_t rms_norm_workspace_bytes(const rms_norm_shape* shape);
+
+/*
+ * Root-mean-square norm of every row, after the residual's addition:
+ *   h = x + residual;  rstd = 1 / sqrt(mean(h^2) + eps);  y = h rstd weight
+ * x, residual (NULL = none) [N,C] strided rows; h [N,C] io_dtype contiguous (the sum, rounded once;
+ * NULL = not written; may be the buffer of x or of residual if that is contiguous); weight [C] f32
+ * (NULL = ones); rstd [N] f32 (may be NULL).  y [N,C] contiguous: io_dtype, or with quantize 8-bit
+ * values q and scale f32 [N, 1] or [N, ceil(C / RMS_NORM_BLOCK)]: scale is the largest |y| it covers
+ * over 448 (1 where all are zero), q = y / scale rounded to nearest, ties to even.  The norm is taken
+ * of the unrounded sum; all arithmetic is fp32.
+ */
+ssd_status rms_norm_forward(const rms_norm_shape* shape, const void* x, const void* residual,
+                            const float* weight, void* y, void* h, float* rstd, float* scale,
+                            void* stream);
+
+/*
+ * Reverse mode of rms_norm_forward for <dy, y> + <dresidual, h>, from the h and rstd that the forward
+ * wrote (h is x where there was no residual):
+ *   dx = rstd (weight dy - xh mean(weight dy xh)) + dresidual,  xh = h rstd;  dweight = sum dy xh
+ * dx [N,C] io_dtype contiguous (the gradient of x and of residual alike), dresidual (NULL = none)
+ * strided, dweight [C] f32 (may be NULL; summed in a fixed order).
+ */
+ssd_status rms_norm_backward(const rms_norm_shape* shape, const void* h, const void* dy,
+                             const float* rstd, const float* weight, const void* dresidual,
+                             void* dx, float* dweight, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+typedef struct token_sample_shape {
+  int64_t rows;           /* n >= 0 */
+  int64_t vocab;          /* V, 1 .. 2^20 */
+  int64_t logits_stride;  /* of the row axis, >= 0 */
+  float temperature;      /* used where the array of the same name is NULL, likewise below */
+  float top_p;
+  float min_p;
+  int32_t top_k;
+  int32_t io_dtype;       /* ssd_dtype of logits */
+} token_sample_shape;
+
+/*
+ * Draws one token for every row of logits [n,V] (strided rows) from the random numbers u [n] f32 in
+ * [0,1).  In the order of falling logits, equal ones by rising index, with weights
+ * w = exp((logit - largest logit) / temperature), a row keeps its first top_k tokens (<= 0: all), of
+ * these those with w >= min_p (<= 0: all), of these the fewest whose sum is at least top_p of their
+ * sum (>= 1: all; the first token is always kept).  The token drawn is the first, by rising index, at
+ * which the running sum of the kept weights exceeds u times their sum.  temperature 0 takes the largest
+ * logit (the lowest index of equal ones).  ids [n] int64; logprob [n] f32 (may be NULL): the logarithm
+ * of the drawn token's share.  NaN counts as -inf; +inf weighs 1 and all else nothing; a row of only
+ * -inf draws -1, with logprob NaN.  Weights are fixed-point numbers whose sums do not depend on an
+ * order: 2^-31 of a weight, 2^-42 of the largest.
+ * temperature, top_p, min_p [n] f32 and top_k [n] int32, each NULL or contiguous; values outside their
+ * range (a negative or NaN temperature, a NaN) act as 1, 1, 0 and 0.
+ */
+ssd_status token_sample(const token_sample_shape* shape, const void* logits, const float* u,
+                        const float* temperature, const int32_t* top_k, const float* top_p,
+                        const float* min_p, int64_t* ids, float* logprob, void* stream);
+
 /*
  * Reads (and clears) the device-side error word of a workspace after synchronising `stream`.
  * Returns SSD_OK, or SSD_ERR_TIMEOUT if a device wait of an earlier call on this workspace gave
