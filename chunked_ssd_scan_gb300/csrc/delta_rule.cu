@@ -16,7 +16,7 @@
 #include <algorithm>
 #include <initializer_list>
 
-#include "delta_rule.cuh"
+#include "delta_tc.cuh"
 #include "launch.h"
 
 namespace ssd {
@@ -554,14 +554,20 @@ ssd_status check_shape(const gated_delta_rule_shape* s, bool back) {
 }
 
 struct Layout {
-  size_t err, du, states, dstates, partial, total;
+  size_t err, du, states, dstates, partial, chunks, total;
 };
+// Whether strides and pointers may let the tensor-core kernels take a call of this shape.
+bool tc_shape(const gated_delta_rule_shape* s) {
+  return s->io_dtype == SSD_BF16 && s->key_dim % 8 == 0 && s->key_dim <= 128 && s->value_dim % 8 == 0 && s->seqlen >= kChunk / 2;
+}
 int key_blocks(int64_t K) { return (int)((K + 63) / 64); }
 Layout layout(const gated_delta_rule_shape* s, bool back) {
   Layout L = {};
   size_t at = sizeof(WsHeader);
+  const size_t nch = (size_t)((s->seqlen + kChunk - 1) / kChunk);
+  L.chunks = at;
+  if (!back && tc_shape(s)) at = align_up(at + tc_forward_bytes(s->batch, (int64_t)nch, s->heads), kWsAlign);
   if (back) {
-    const size_t nch = (size_t)((s->seqlen + kChunk - 1) / kChunk);
     const size_t steps = (size_t)(s->batch * s->seqlen * s->heads * s->value_dim) * 4;
     const size_t states = (size_t)s->batch * nch * (size_t)(s->heads * s->value_dim * s->key_dim) * 4;
     auto take = [&](size_t bytes) {
@@ -694,6 +700,7 @@ ssd_status gated_delta_rule_forward(const gated_delta_rule_shape* shape, const v
   p.final_state = final_state;
   p.states_out = states;
   p.hdr = static_cast<WsHeader*>(workspace);
+  if (tc_shape(shape) && tc_takes(p, false)) return done(tc_forward(p, static_cast<char*>(workspace) + L.chunks, st));
   return done(bf16 ? launch_walk<__nv_bfloat16>(p, false, st) : launch_walk<float>(p, false, st));
 }
 

@@ -1,0 +1,603 @@
+// Gated delta rule on the tensor cores, bf16 inputs, chunk by chunk of 64 steps (declarations in include/ssdscan.h).
+// With D_i the decay from the chunk's start to step i, E_i that behind it, M_ij between, S the state before the chunk:
+//   A_ij = beta_i M_ij (k_i . k_j), j < i;   T = (I + A)^-1 diag(beta)
+//   U = T (V - diag(D) K S^T)                          the writes of all steps: the triangular system solved
+//   y = scale (diag(D) Q S^T + (M o Q K^T) U);   S' = D_last S + (diag(E) U)^T K
+// Two kernels.  T and P = scale M o Q K^T do not depend on the state: delta_chunk_kernel makes them for all chunks in
+// parallel.  delta_chain_kernel walks a sequence's chunks with its state on chip, one block a head and 128 values, in
+// transposed form: values are the 128 lanes of TMEM, so that what one product leaves in an accumulator is, after
+// scaling, the next product's A operand in TMEM, without a trip through shared memory.
+// Operands that are computed (S, U, T, P and what lies between) enter a product as two bf16 terms, hi and lo: products
+// with an input take two passes, between two computed ones three (lo lo is left out, 2^-18).  One term would leave
+// states and outputs off by 3e-3.  States are kept in fp32 registers and products added to them there: the tensor
+// core's own accumulation truncates, which over a long memory would show.
+#include <cudaTypedefs.h>
+#include <string.h>
+
+#include <algorithm>
+
+#include "delta_tc.cuh"
+#include "launch.h"
+#include "tensor_map.h"
+
+namespace ssd {
+namespace {
+
+using namespace delta;
+
+constexpr uint32_t kDHi = sdesc_sw128_hi(1024);
+
+// ---------------------------------------------------------------------------------------------------------------------
+// T and P of every chunk and head.  One product stacks K on Q (128 rows) against K: rows 0..63 are K K^T, the others
+// Q K^T; both are of the key head, the heads that share it take turns with their own decays and betas.
+// ---------------------------------------------------------------------------------------------------------------------
+constexpr int kPrepThreads = 128;
+constexpr int kPitch = 68;
+
+template <int KB>
+struct PrepSmem {
+  uint8_t kq[KB * 2 * kTileBytes];   // blocks of 64 keys: 64 rows of K, 64 of Q
+  float a[kChunk][kPitch], x[kChunk][kPitch];
+  ChunkDecay c;
+  uint64_t loaded, done;
+  uint32_t tmem;
+  int abort, keep;
+};
+
+// Column `j` of (I + A)^-1 by forward substitution, rows from kFrom on (those before are zero: j >= kFrom).
+template <int kFrom, int KB>
+__device__ __forceinline__ void solve_column(PrepSmem<KB>& sm, int j) {
+  float x[kChunk - kFrom];
+#pragma unroll
+  for (int i = kFrom; i < kChunk; ++i) {
+    float s0 = i == j ? 1.f : 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+    for (int m = kFrom; m < i; m += 4) {
+      const float4 a = *reinterpret_cast<const float4*>(&sm.a[i][m]);   // zero from the diagonal on
+      s0 = fmaf(-a.x, x[m - kFrom], s0);
+      if (m + 1 < i) s1 = fmaf(-a.y, x[m + 1 - kFrom], s1);
+      if (m + 2 < i) s2 = fmaf(-a.z, x[m + 2 - kFrom], s2);
+      if (m + 3 < i) s3 = fmaf(-a.w, x[m + 3 - kFrom], s3);
+    }
+    x[i - kFrom] = (s0 + s1) + (s2 + s3);
+    sm.x[i][j] = x[i - kFrom];
+  }
+}
+
+__device__ __forceinline__ void store_split_row(uint8_t* hi, uint8_t* lo, int row, const float (&v)[8], int col) {
+  uint4 h, l;
+  split2(v[0], v[1], h.x, l.x);
+  split2(v[2], v[3], h.y, l.y);
+  split2(v[4], v[5], h.z, l.z);
+  split2(v[6], v[7], h.w, l.w);
+  *reinterpret_cast<uint4*>(hi + sw128_off16(row, col)) = h;
+  *reinterpret_cast<uint4*>(lo + sw128_off16(row, col)) = l;
+}
+
+template <int KB>
+__global__ void __launch_bounds__(kPrepThreads) delta_chunk_kernel(const __grid_constant__ Params p,
+                                                                   const __grid_constant__ TcMaps m, TcBuffers buf) {
+  extern __shared__ __align__(1024) uint8_t raw[];
+  PrepSmem<KB>& sm = *reinterpret_cast<PrepSmem<KB>*>(raw);
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x / 32), 0), lane = threadIdx.x % 32;
+  int64_t id = blockIdx.x;
+  const int64_t hk = id % p.Hk;
+  id /= p.Hk;
+  const int64_t chunk = id % p.nch, b = id / p.nch, t0 = chunk * kChunk, group = p.H / p.Hk;
+  const int n = (int)min((int64_t)kChunk, p.T - t0);
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.loaded, 1);
+    mbar_init(&sm.done, 1);
+    sm.abort = sm.keep = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&sm.tmem, 64);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  bool ok = true;
+  if (warp == 0) {
+    mbar_arrive_expect_tx_elect(&sm.loaded, KB * 2 * kTileBytes);
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      tma_load_4d_elect(sm.kq + kb * 2 * kTileBytes, &m.k, &sm.loaded, kb * 64, (int)t0, (int)hk, (int)b);
+      tma_load_4d_elect(sm.kq + (kb * 2 + 1) * kTileBytes, &m.q, &sm.loaded, kb * 64, (int)t0, (int)hk, (int)b);
+    }
+    ok = wait_bar(&sm.loaded, 0, &sm.abort, p.hdr, 1);
+    if (ok) {
+      const uint32_t lo = sdesc_sw128_lo(smem_u32(sm.kq), 0);
+#pragma unroll
+      for (int ks = 0; ks < KB * 4; ++ks) {
+        const uint32_t at = lo + (((ks >> 2) * 2 * kTileBytes + (ks & 3) * 32) >> 4);
+        mma_ss_we(tmem, at, kDHi, at, kDHi, idesc_bf16(128, 64, 0, 0), ks > 0);
+      }
+    }
+    if (ok) mma_commit_elect(&sm.done);   // else every wait for it ends by the abort flag
+  }
+  const bool done = wait_bar(&sm.done, 0, &sm.abort, p.hdr, 2);
+  if (!done && ok) sm.keep = 1;   // a product may still write TMEM: it stays allocated
+  tc_fence_after();
+  const int row = (warp & 1) * 32 + lane;
+  const uint32_t mine = tmem + ((uint32_t)(warp * 32) << 16);
+  for (int64_t h = hk * group; done && h < (hk + 1) * group; ++h) {
+    const int64_t cell = (b * p.nch + chunk) * p.H + h;
+    uint8_t* out = buf.squares + cell * kSquareBytes;
+    __syncthreads();
+    if (warp == 0) chunk_decay_warp(p, sm.c, b, t0, n, h, lane);
+    __syncthreads();
+    if (threadIdx.x < kChunk) buf.decays[cell * 2 * kChunk + threadIdx.x] = sm.c.from[threadIdx.x];
+    else buf.decays[cell * 2 * kChunk + threadIdx.x] = sm.c.to[threadIdx.x - kChunk];
+    const float hi = sm.c.hi[row], lo = sm.c.lo[row];
+    const float by = warp < 2 ? sm.c.beta[row] : p.scale;
+    const int last = warp < 2 ? row - 1 : row;   // the strict part of A, P with its diagonal
+#pragma unroll 1
+    for (int c0 = 0; c0 < kChunk; c0 += 16) {
+      float v[16];
+      tmem_ld16(mine + c0, v);
+      tmem_ld_wait();
+      reg_tie(v);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int c = c0 + j;
+        v[j] = c <= last ? v[j] * by * __expf((hi - sm.c.hi[c]) + (lo - sm.c.lo[c])) : 0.f;
+      }
+      if (warp < 2) {
+#pragma unroll
+        for (int j = 0; j < 16; j += 4)
+          *reinterpret_cast<float4*>(&sm.a[row][c0 + j]) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+      } else {
+        float w[8];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) w[j] = v[half * 8 + j];
+          store_split_row(out + 2 * kTileBytes, out + 3 * kTileBytes, row, w, c0 + half * 8);
+        }
+      }
+    }
+    __syncthreads();
+    if (warp == 0) {
+      solve_column<0, KB>(sm, lane);
+    } else if (warp == 1) {
+      solve_column<32, KB>(sm, 32 + lane);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) sm.x[i][32 + lane] = 0.f;
+    }
+    __syncthreads();
+    // rows of T by two threads each
+    const int r = threadIdx.x >> 1, first = (threadIdx.x & 1) * 32;
+#pragma unroll
+    for (int c = first; c < first + 32; c += 8) {
+      float w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = sm.x[r][c + j] * sm.c.beta[c + j];
+      store_split_row(out, out + kTileBytes, r, w, c);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0 && !sm.keep) tmem_dealloc(tmem, 64);
+}
+
+// ---------------------------------------------------------------------------------------------------------------------
+// The walk.  TMEM columns: the state's two terms, X = S K^T and after it -D X's two terms, U's accumulator and after it
+// U's two terms, E U's two terms, (E U)^T K, y.  Halves of 32 columns keep hi then lo of themselves, so that a warp that
+// has read a half may write its terms over it.
+// ---------------------------------------------------------------------------------------------------------------------
+constexpr int kChainThreads = 14 * 32;
+constexpr uint32_t kColS = 0, kColX = 128, kColU = 192, kColW = 256, kColD = 320, kColO = 448;
+
+template <int KB>
+struct Stage {
+  uint8_t k[KB * kTileBytes], q[KB * kTileBytes], v[2 * kTileBytes], t[2 * kTileBytes], p[2 * kTileBytes];
+  float from[kChunk], to[kChunk];
+  uint8_t pad[512];
+};
+struct ChainBars {
+  uint64_t full[2], empty[2], s_ready[2], x_full, r_ready, u_full, w_ready, u_ready, d_full, o1_full, o_scaled, o2_full,
+      o_free, drain;
+};
+template <int KB>
+struct ChainSmem {
+  Stage<KB> st[2];
+  uint8_t y[2 * kTileBytes];
+  ChainBars bar;
+  uint32_t tmem;
+  int abort, keep;
+};
+
+// Column of the k-step `ks` (16 steps of the chunk) of an operand kept in halves; lo is 16 further.
+__device__ __forceinline__ uint32_t half_col(int ks) { return (uint32_t)((ks >> 1) * 32 + (ks & 1) * 8); }
+
+// Two terms of 32 columns, written over the 32 columns' place: hi in the first 16, lo in the others.
+__device__ __forceinline__ void store_half(uint32_t at, const float (&v)[32]) {
+  uint32_t hi[16], lo[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) split2(v[2 * j], v[2 * j + 1], hi[j], lo[j]);
+  tmem_st16u(at, hi);
+  tmem_st16u(at + 16, lo);
+}
+
+template <int KB>
+__global__ void __launch_bounds__(kChainThreads, 1)
+    delta_chain_kernel(const __grid_constant__ Params p, const __grid_constant__ TcMaps m, TcBuffers buf, int vtiles) {
+  extern __shared__ __align__(1024) uint8_t raw[];
+  ChainSmem<KB>& sm = *reinterpret_cast<ChainSmem<KB>*>(raw);
+  ChainBars& bar = sm.bar;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x / 32), 0), lane = threadIdx.x % 32;
+  const int vtile = blockIdx.x % vtiles, h = (blockIdx.x / vtiles) % (int)p.H, b = blockIdx.x / vtiles / (int)p.H;
+  const int hk = h / (int)(p.H / p.Hk), v0 = vtile * 128, nch = (int)p.nch;
+  constexpr int Kp = KB * 64;
+  volatile int* abort = &sm.abort;
+  if (threadIdx.x == 0) {
+    sm.abort = sm.keep = 0;
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar.full[s], 1);
+      mbar_init(&bar.empty[s], 1);
+      mbar_init(&bar.s_ready[s], 4);
+    }
+    for (uint64_t* one : {&bar.x_full, &bar.u_full, &bar.d_full, &bar.o1_full, &bar.o2_full, &bar.drain}) mbar_init(one, 1);
+    for (uint64_t* eight : {&bar.r_ready, &bar.w_ready, &bar.u_ready}) mbar_init(eight, 8);
+    mbar_init(&bar.o_scaled, 4);
+    mbar_init(&bar.o_free, 4);
+    fence_mbar_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(&sm.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+
+  if (warp == 13) {   // loads
+    int issued = 0;
+    for (int c = 0; c < nch; ++c) {
+      const int s = c & 1;
+      if (c >= 2 && !wait_bar(&bar.empty[s], ((c >> 1) - 1) & 1, abort, p.hdr, 10)) break;
+      Stage<KB>& st = sm.st[s];
+      const int64_t cell = ((int64_t)b * nch + c) * p.H + h;
+      mbar_arrive_expect_tx_elect(&bar.full[s], (2 * KB + 6) * kTileBytes + kDecayBytes);
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        tma_load_4d_elect(st.k + kb * kTileBytes, &m.k, &bar.full[s], kb * 64, c * kChunk, hk, b);
+        tma_load_4d_elect(st.q + kb * kTileBytes, &m.q, &bar.full[s], kb * 64, c * kChunk, hk, b);
+      }
+      tma_load_4d_elect(st.v, &m.v, &bar.full[s], v0, c * kChunk, h, b);
+      tma_load_4d_elect(st.v + kTileBytes, &m.v, &bar.full[s], v0 + 64, c * kChunk, h, b);
+      bulk_load_elect(st.t, buf.squares + cell * kSquareBytes, 4 * kTileBytes, &bar.full[s]);
+      bulk_load_elect(st.from, buf.decays + cell * 2 * kChunk, kDecayBytes, &bar.full[s]);
+      issued = c + 1;
+    }
+    bool drained = true;   // nothing may still be written to this block's shared memory when it ends
+    for (int s = 0; s < 2; ++s) {
+      const int loads = issued > s ? (issued - 1 - s) / 2 + 1 : 0;
+      if (loads > 0) drained &= mbar_wait_bounded(&bar.full[s], (loads - 1) & 1, 2000000000ull);
+    }
+    if (!drained && lane == 0) latch_error(p.hdr, SSD_ERR_TIMEOUT, 11);
+  } else if (warp == 12) {   // products
+    constexpr uint32_t id_k = idesc_bf16(128, 64, 0, 0), id_v = idesc_bf16(128, 64, 1, 0), id_d = idesc_bf16(128, Kp, 0, 1);
+    for (int c = 0; c < nch; ++c) {
+      const int s = c & 1;
+      const uint32_t par = c & 1;
+      Stage<KB>& st = sm.st[s];
+      const uint32_t k_lo = sdesc_sw128_lo(smem_u32(st.k), 0), q_lo = sdesc_sw128_lo(smem_u32(st.q), 0);
+      const uint32_t km_lo = sdesc_sw128_lo(smem_u32(st.k), kTileBytes), v_lo = sdesc_sw128_lo(smem_u32(st.v), kTileBytes);
+      const uint32_t t_lo = sdesc_sw128_lo(smem_u32(st.t), 0), p_lo = sdesc_sw128_lo(smem_u32(st.p), 0);
+      constexpr uint32_t kLo = kTileBytes >> 4;   // from a square's hi to its lo
+      if (!wait_bar(&bar.full[s], (c >> 1) & 1, abort, p.hdr, 12)) break;
+      // X = S K^T, the first half of the keys as soon as its terms are there
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (!wait_bar(&bar.s_ready[half], par, abort, p.hdr, 13)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = half * KB * 2; ks < (half + 1) * KB * 2; ++ks) {
+          const uint32_t at = k_lo + (((ks >> 2) * kTileBytes + (ks & 3) * 32) >> 4);
+          mma_ts_we(tmem + kColX, tmem + kColS + ks * 8, at, kDHi, id_k, ks > 0);
+          mma_ts_we(tmem + kColX, tmem + kColS + Kp / 2 + ks * 8, at, kDHi, id_k, 1);
+        }
+      }
+      if (*abort) break;
+      mma_commit_elect(&bar.x_full);
+      // U = V T^T - (D X) T^T
+      if (c > 0 && !wait_bar(&bar.o2_full, (c - 1) & 1, abort, p.hdr, 14)) break;   // U's terms have been read
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        mma_ss_we(tmem + kColU, v_lo + ks * (2048 >> 4), kDHi, t_lo + ks * 2, kDHi, id_v, ks > 0);
+        mma_ss_we(tmem + kColU, v_lo + ks * (2048 >> 4), kDHi, t_lo + kLo + ks * 2, kDHi, id_v, 1);
+      }
+      if (!wait_bar(&bar.r_ready, par, abort, p.hdr, 15)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        const uint32_t a = tmem + kColX + half_col(ks);
+        mma_ts_we(tmem + kColU, a, t_lo + ks * 2, kDHi, id_k, 1);
+        mma_ts_we(tmem + kColU, a, t_lo + kLo + ks * 2, kDHi, id_k, 1);
+        mma_ts_we(tmem + kColU, a + 16, t_lo + ks * 2, kDHi, id_k, 1);
+      }
+      mma_commit_elect(&bar.u_full);
+      // S Q^T, while U is turned into operands
+      if (c > 0 && !wait_bar(&bar.o_free, (c - 1) & 1, abort, p.hdr, 16)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int ks = 0; ks < KB * 4; ++ks) {
+        const uint32_t at = q_lo + (((ks >> 2) * kTileBytes + (ks & 3) * 32) >> 4);
+        mma_ts_we(tmem + kColO, tmem + kColS + ks * 8, at, kDHi, id_k, ks > 0);
+        mma_ts_we(tmem + kColO, tmem + kColS + Kp / 2 + ks * 8, at, kDHi, id_k, 1);
+      }
+      mma_commit_elect(&bar.o1_full);
+      // (E U)^T K
+      if (!wait_bar(&bar.w_ready, par, abort, p.hdr, 17)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        const uint32_t a = tmem + kColW + half_col(ks);
+        mma_ts_we(tmem + kColD, a, km_lo + ks * (2048 >> 4), kDHi, id_d, ks > 0);
+        mma_ts_we(tmem + kColD, a + 16, km_lo + ks * (2048 >> 4), kDHi, id_d, 1);
+      }
+      mma_commit_elect(&bar.d_full);
+      // y = scale D S Q^T + U P^T
+      if (!wait_bar(&bar.u_ready, par, abort, p.hdr, 18)) break;
+      if (!wait_bar(&bar.o_scaled, par, abort, p.hdr, 19)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        const uint32_t a = tmem + kColU + half_col(ks);
+        mma_ts_we(tmem + kColO, a, p_lo + ks * 2, kDHi, id_k, 1);
+        mma_ts_we(tmem + kColO, a, p_lo + kLo + ks * 2, kDHi, id_k, 1);
+        mma_ts_we(tmem + kColO, a + 16, p_lo + ks * 2, kDHi, id_k, 1);
+      }
+      mma_commit_elect(&bar.o2_full);
+      mma_commit_elect(&bar.empty[s]);
+    }
+    mma_commit_elect(&bar.drain);
+    if (!mbar_wait_bounded(&bar.drain, 0, 2000000000ull) && lane == 0) {
+      sm.keep = 1;   // products may still write TMEM: it stays allocated
+      latch_error(p.hdr, SSD_ERR_TIMEOUT, 20);
+    }
+  } else if (warp < 8) {   // the state, and the operands on the way to the next one; a thread has a value and half the keys
+    constexpr int KH = Kp / 2;
+    const int half = warp >> 2, row = v0 + (warp & 3) * 32 + lane, k0 = half * KH;
+    const bool live = row < p.V;
+    const int64_t at = (((int64_t)b * p.H + h) * p.V + row) * p.K + k0;
+    float S[KH];
+#pragma unroll
+    for (int k = 0; k < KH; ++k) S[k] = p.init && live && k0 + k < p.K ? p.init[at + k] : 0.f;
+    const bool wide_s = (reinterpret_cast<uintptr_t>(p.states_out) & 31) == 0;
+    const bool wide_f = (reinterpret_cast<uintptr_t>(p.final_state) & 31) == 0;
+    for (int c = 0; c < nch; ++c) {
+      const int s = c & 1;
+      const uint32_t par = c & 1;
+      const Stage<KB>& st = sm.st[s];
+      // the state's terms
+#pragma unroll
+      for (int k = 0; k < KH; k += 32) {
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) split2(S[k + 2 * j], S[k + 2 * j + 1], hi[j], lo[j]);
+        tmem_st16u(tmem + lanes + kColS + (k0 + k) / 2, hi);
+        tmem_st16u(tmem + lanes + kColS + Kp / 2 + (k0 + k) / 2, lo);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.s_ready[half]);
+      if (p.states_out && live) {
+        float* to = p.states_out + (((int64_t)b * nch + c) * p.H + h) * p.V * p.K + (int64_t)row * p.K + k0;
+#pragma unroll
+        for (int k = 0; k < KH; k += 8)
+          if (k0 + k < p.K) store8(to + k, S + k, wide_s);
+      }
+      if (!wait_bar(&bar.full[s], (c >> 1) & 1, abort, p.hdr, 21)) break;   // the decays
+      const float all = st.from[kChunk - 1];
+      if (!wait_bar(&bar.x_full, par, abort, p.hdr, 22)) break;
+      tc_fence_after();
+      float x[32];
+      tmem_ld32(tmem + lanes + kColX + half * 32, x);
+      tmem_ld_wait();
+      reg_tie(x);
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(&st.from[half * 32 + j]);
+        x[j] *= -f.x;
+        x[j + 1] *= -f.y;
+        x[j + 2] *= -f.z;
+        x[j + 3] *= -f.w;
+      }
+      store_half(tmem + lanes + kColX + half * 32, x);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.r_ready);
+      if (!wait_bar(&bar.u_full, par, abort, p.hdr, 23)) break;
+      tc_fence_after();
+      tmem_ld32(tmem + lanes + kColU + half * 32, x);
+      tmem_ld_wait();
+      reg_tie(x);
+      float w[32];
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(&st.to[half * 32 + j]);
+        w[j] = x[j] * f.x;
+        w[j + 1] = x[j + 1] * f.y;
+        w[j + 2] = x[j + 2] * f.z;
+        w[j + 3] = x[j + 3] * f.w;
+      }
+      store_half(tmem + lanes + kColW + half * 32, w);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.w_ready);
+      store_half(tmem + lanes + kColU + half * 32, x);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.u_ready);
+      if (!wait_bar(&bar.d_full, par, abort, p.hdr, 24)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < KH; k += 32) {
+        tmem_ld32(tmem + lanes + kColD + k0 + k, x);
+        tmem_ld_wait();
+        reg_tie(x);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) S[k + j] = fmaf(all, S[k + j], x[j]);
+      }
+    }
+    if (p.final_state && live && !*abort) {
+#pragma unroll
+      for (int k = 0; k < KH; k += 8)
+        if (k0 + k < p.K) store8(p.final_state + at + k, S + k, wide_f);
+    }
+  } else {   // y: a thread has a value
+    const int v = (warp & 3) * 32 + lane;
+    uint8_t* column = sm.y + (v >> 6) * kTileBytes;
+    for (int c = 0; c < nch; ++c) {
+      const int s = c & 1;
+      const uint32_t par = c & 1;
+      const Stage<KB>& st = sm.st[s];
+      if (!wait_bar(&bar.full[s], (c >> 1) & 1, abort, p.hdr, 25)) break;
+      if (!wait_bar(&bar.o1_full, par, abort, p.hdr, 26)) break;
+      tc_fence_after();
+      float o[32];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        tmem_ld32(tmem + lanes + kColO + half * 32, o);
+        tmem_ld_wait();
+        reg_tie(o);
+        uint32_t u[32];
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&st.from[half * 32 + j]);
+          u[j] = __float_as_uint(o[j] * (f.x * p.scale));
+          u[j + 1] = __float_as_uint(o[j + 1] * (f.y * p.scale));
+          u[j + 2] = __float_as_uint(o[j + 2] * (f.z * p.scale));
+          u[j + 3] = __float_as_uint(o[j + 3] * (f.w * p.scale));
+        }
+        tmem_st32u(tmem + lanes + kColO + half * 32, u);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.o_scaled);
+      if (!wait_bar(&bar.o2_full, par, abort, p.hdr, 27)) break;
+      tc_fence_after();
+      float o2[32];
+      tmem_ld32(tmem + lanes + kColO, o);
+      tmem_ld32(tmem + lanes + kColO + 32, o2);
+      tmem_ld_wait();
+      reg_tie(o);
+      reg_tie(o2);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.o_free);
+      if (p.y) {
+        if (warp == 8 && lane == 0) bulk_wait_group_read<0>();   // the last chunk's rows have left
+        named_barrier(1, 128);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          *reinterpret_cast<__nv_bfloat16*>(column + sw128_off16(j, v & 63)) = __float2bfloat16_rn(o[j]);
+          *reinterpret_cast<__nv_bfloat16*>(column + sw128_off16(j + 32, v & 63)) = __float2bfloat16_rn(o2[j]);
+        }
+        fence_proxy_async_smem();
+        named_barrier(1, 128);
+        if (warp == 8 && lane == 0) {
+          tma_store_4d(&m.y, sm.y, v0, c * kChunk, h, b);
+          if (v0 + 64 < p.V) tma_store_4d(&m.y, sm.y + kTileBytes, v0 + 64, c * kChunk, h, b);
+          bulk_commit_group();
+        }
+      }
+    }
+    if (warp == 8 && lane == 0) bulk_wait_group<0>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12 && !sm.keep) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------------------------------------ host
+// Map of [batch, steps, heads, cols] in boxes of 64 steps and 64 columns of one head.
+bool head_map(CUtensorMap* m, const void* base, int64_t batch, int64_t T, int64_t heads, int64_t cols, const int64_t* stride) {
+  const auto encode = tensor_map_encoder();
+  if (!encode || !base) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)cols, (cuuint64_t)T, (cuuint64_t)heads, (cuuint64_t)batch};
+  const int64_t of[3] = {T > 1 ? stride[1] : 8, heads > 1 ? stride[2] : 8, batch > 1 ? stride[0] : 8};
+  cuuint64_t strides[3];
+  for (int a = 0; a < 3; ++a) {
+    if (of[a] <= 0 || of[a] % 8 != 0) return false;
+    strides[a] = (cuuint64_t)of[a] * 2;
+  }
+  const cuuint32_t box[4] = {64, 64, 1, 1}, one[4] = {1, 1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, one,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool rows_fit(const void* base, const int64_t* stride, int64_t batch, int64_t T, int64_t heads) {
+  if (reinterpret_cast<uintptr_t>(base) % 16 != 0) return false;
+  const int64_t n[3] = {batch, T, heads};
+  for (int a = 0; a < 3; ++a)
+    if (n[a] > 1 && (stride[a] <= 0 || stride[a] % 8 != 0 || stride[a] >= (int64_t)1 << 38)) return false;
+  return true;
+}
+
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <int KB>
+cudaError_t forward_as(const Params& p, const TcMaps& m, const TcBuffers& buf, cudaStream_t st) {
+  constexpr int prep = sizeof(PrepSmem<KB>), chain = sizeof(ChainSmem<KB>);
+  static_assert(chain <= 232448, "shared memory of a block");
+  cudaError_t e = allow_smem(delta_chunk_kernel<KB>, prep);
+  if (e == cudaSuccess) e = allow_smem(delta_chain_kernel<KB>, chain);
+  if (e != cudaSuccess) return e;
+  delta_chunk_kernel<KB><<<(unsigned)(p.batch * p.nch * p.Hk), kPrepThreads, prep, st>>>(p, m, buf);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int vtiles = (int)((p.V + 127) / 128);
+  delta_chain_kernel<KB><<<(unsigned)(p.batch * p.H * vtiles), kChainThreads, chain, st>>>(p, m, buf, vtiles);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+namespace delta {
+
+size_t tc_forward_bytes(int64_t batch, int64_t nch, int64_t H) {
+  return (size_t)(batch * nch * H) * (kSquareBytes + kDecayBytes);
+}
+
+bool tc_takes(const Params& p, bool backward) {
+  const int64_t most = INT32_MAX / 2;
+  if (p.K % 8 != 0 || p.K > 128 || p.V % 8 != 0 || p.T > most || p.batch > most || p.T < kChunk / 2) return false;
+  return rows_fit(p.q, p.qs, p.batch, p.T, p.Hk) && rows_fit(p.k, p.ks, p.batch, p.T, p.Hk) &&
+         rows_fit(p.v, p.vs, p.batch, p.T, p.H) && reinterpret_cast<uintptr_t>(p.y) % 16 == 0;
+}
+
+cudaError_t tc_forward(const Params& p, void* buffers, cudaStream_t st) {
+  TcMaps m;
+  memset(&m, 0, sizeof(m));
+  const int64_t ys[3] = {p.T * p.H * p.V, p.H * p.V, p.V};
+  if (!head_map(&m.q, p.q, p.batch, p.T, p.Hk, p.K, p.qs) || !head_map(&m.k, p.k, p.batch, p.T, p.Hk, p.K, p.ks) ||
+      !head_map(&m.v, p.v, p.batch, p.T, p.H, p.V, p.vs) || (p.y && !head_map(&m.y, p.y, p.batch, p.T, p.H, p.V, ys)))
+    return cudaErrorInvalidValue;
+  TcBuffers buf;
+  buf.squares = static_cast<uint8_t*>(buffers);
+  buf.decays = reinterpret_cast<float*>(buf.squares + (size_t)(p.batch * p.nch * p.H) * kSquareBytes);
+  return p.K <= 64 ? forward_as<1>(p, m, buf, st) : forward_as<2>(p, m, buf, st);
+}
+
+}  // namespace delta
+}  // namespace ssd
