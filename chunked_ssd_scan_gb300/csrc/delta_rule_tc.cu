@@ -36,32 +36,102 @@ constexpr int kPitch = 68;
 
 template <int KB>
 struct PrepSmem {
-  uint8_t kq[KB * 2 * kTileBytes];   // blocks of 64 keys: 64 rows of K, 64 of Q
-  float a[kChunk][kPitch], x[kChunk][kPitch];
+  union {
+    uint8_t kq[KB * 2 * kTileBytes];   // blocks of 64 keys: 64 rows of K, 64 of Q; done with once the product is
+    struct {
+      float a[kChunk][kPitch], x[kChunk][kPitch];
+    };
+  };
   ChunkDecay c;
   uint64_t loaded, done;
   uint32_t tmem;
   int abort, keep;
 };
 
-// Column `j` of (I + A)^-1 by forward substitution, rows from kFrom on (those before are zero: j >= kFrom).
-template <int kFrom, int KB>
-__device__ __forceinline__ void solve_column(PrepSmem<KB>& sm, int j) {
-  float x[kChunk - kFrom];
+// (I + A)^-1 below and on the diagonal of `x`, for A strictly below the diagonal of `a`: the 16 x 16 blocks on the
+// diagonal by forward substitution, a column a lane, then pairs of them by X21 = -X22 (A21 X11), whose inner product
+// waits above the diagonal of `a`.  All threads; fp32 throughout.  (Every column by forward substitution, 64 rows one
+// after the other in 43 KB of straight code: 298 us instead of PREPUS for 8 x 4096 x 16 heads.)
+__device__ __forceinline__ void invert(float (&a)[kChunk][kPitch], float (&x)[kChunk][kPitch]) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int d0 = (tid >> 5) * 16;
+  if (lane < 16) {
+    float v[16];
 #pragma unroll
-  for (int i = kFrom; i < kChunk; ++i) {
-    float s0 = i == j ? 1.f : 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+    for (int i = 0; i < 16; ++i) {
+      float s0 = i == lane ? 1.f : 0.f, s1 = 0.f;
 #pragma unroll
-    for (int m = kFrom; m < i; m += 4) {
-      const float4 a = *reinterpret_cast<const float4*>(&sm.a[i][m]);   // zero from the diagonal on
-      s0 = fmaf(-a.x, x[m - kFrom], s0);
-      if (m + 1 < i) s1 = fmaf(-a.y, x[m + 1 - kFrom], s1);
-      if (m + 2 < i) s2 = fmaf(-a.z, x[m + 2 - kFrom], s2);
-      if (m + 3 < i) s3 = fmaf(-a.w, x[m + 3 - kFrom], s3);
+      for (int m = 0; m < i; m += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(&a[d0 + i][d0 + m]);
+        s0 = fmaf(-f.x, v[m], s0);
+        if (m + 1 < i) s1 = fmaf(-f.y, v[m + 1], s1);
+        if (m + 2 < i) s0 = fmaf(-f.z, v[m + 2], s0);
+        if (m + 3 < i) s1 = fmaf(-f.w, v[m + 3], s1);
+      }
+      v[i] = s0 + s1;
+      x[d0 + i][d0 + lane] = v[i];
     }
-    x[i - kFrom] = (s0 + s1) + (s2 + s3);
-    sm.x[i][j] = x[i - kFrom];
   }
+  __syncthreads();
+  {   // two pairs of blocks of 16, four neighbours a thread
+    const int r0 = (tid >> 6) * 32, i = (tid & 63) >> 2, j = (tid & 3) * 4;
+    float y[4] = {};
+    for (int m = j; m < 16; ++m) {
+      const float f = a[r0 + 16 + i][r0 + m];
+      const float4 g = *reinterpret_cast<const float4*>(&x[r0 + m][r0 + j]);
+      y[0] = fmaf(f, g.x, y[0]);
+      y[1] = fmaf(f, g.y, y[1]);
+      y[2] = fmaf(f, g.z, y[2]);
+      y[3] = fmaf(f, g.w, y[3]);
+    }
+    *reinterpret_cast<float4*>(&a[r0 + i][r0 + 16 + j]) = make_float4(y[0], y[1], y[2], y[3]);
+    __syncthreads();
+    float z[4] = {};
+    for (int m = 0; m <= i; ++m) {
+      const float f = x[r0 + 16 + i][r0 + 16 + m];
+      const float4 g = *reinterpret_cast<const float4*>(&a[r0 + m][r0 + 16 + j]);
+      z[0] = fmaf(-f, g.x, z[0]);
+      z[1] = fmaf(-f, g.y, z[1]);
+      z[2] = fmaf(-f, g.z, z[2]);
+      z[3] = fmaf(-f, g.w, z[3]);
+    }
+    *reinterpret_cast<float4*>(&x[r0 + 16 + i][r0 + j]) = make_float4(z[0], z[1], z[2], z[3]);
+  }
+  __syncthreads();
+  {   // one pair of blocks of 32, two rows of four neighbours a thread; rows i and 31 - i, so that threads have as much to do
+    const int i0 = tid >> 3, i1 = 31 - i0, j = (tid & 7) * 4;
+    float y[2][4] = {};
+    for (int m = j; m < 32; ++m) {
+      const float f = a[32 + i0][m], e = a[32 + i1][m];
+      const float4 g = *reinterpret_cast<const float4*>(&x[m][j]);
+      y[0][0] = fmaf(f, g.x, y[0][0]);
+      y[0][1] = fmaf(f, g.y, y[0][1]);
+      y[0][2] = fmaf(f, g.z, y[0][2]);
+      y[0][3] = fmaf(f, g.w, y[0][3]);
+      y[1][0] = fmaf(e, g.x, y[1][0]);
+      y[1][1] = fmaf(e, g.y, y[1][1]);
+      y[1][2] = fmaf(e, g.z, y[1][2]);
+      y[1][3] = fmaf(e, g.w, y[1][3]);
+    }
+    *reinterpret_cast<float4*>(&a[i0][32 + j]) = make_float4(y[0][0], y[0][1], y[0][2], y[0][3]);
+    *reinterpret_cast<float4*>(&a[i1][32 + j]) = make_float4(y[1][0], y[1][1], y[1][2], y[1][3]);
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int i = r ? i1 : i0;
+      float z[4] = {};
+      for (int m = 0; m <= i; ++m) {
+        const float f = x[32 + i][32 + m];
+        const float4 g = *reinterpret_cast<const float4*>(&a[m][32 + j]);
+        z[0] = fmaf(-f, g.x, z[0]);
+        z[1] = fmaf(-f, g.y, z[1]);
+        z[2] = fmaf(-f, g.z, z[2]);
+        z[3] = fmaf(-f, g.w, z[3]);
+      }
+      *reinterpret_cast<float4*>(&x[32 + i][j]) = make_float4(z[0], z[1], z[2], z[3]);
+    }
+  }
+  __syncthreads();
 }
 
 __device__ __forceinline__ void store_split_row(uint8_t* hi, uint8_t* lo, int row, const float (&v)[8], int col) {
@@ -75,7 +145,7 @@ __device__ __forceinline__ void store_split_row(uint8_t* hi, uint8_t* lo, int ro
 }
 
 template <int KB>
-__global__ void __launch_bounds__(kPrepThreads) delta_chunk_kernel(const __grid_constant__ Params p,
+__global__ void __launch_bounds__(kPrepThreads, 6) delta_chunk_kernel(const __grid_constant__ Params p,
                                                                    const __grid_constant__ TcMaps m, TcBuffers buf) {
   extern __shared__ __align__(1024) uint8_t raw[];
   PrepSmem<KB>& sm = *reinterpret_cast<PrepSmem<KB>*>(raw);
@@ -141,9 +211,12 @@ __global__ void __launch_bounds__(kPrepThreads) delta_chunk_kernel(const __grid_
       tmem_ld_wait();
       reg_tie(v);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const int c = c0 + j;
-        v[j] = c <= last ? v[j] * by * __expf((hi - sm.c.hi[c]) + (lo - sm.c.lo[c])) : 0.f;
+      for (int j = 0; j < 16; j += 4) {
+        const float4 ch = *reinterpret_cast<const float4*>(&sm.c.hi[c0 + j]), cl = *reinterpret_cast<const float4*>(&sm.c.lo[c0 + j]);
+        v[j] = c0 + j <= last ? v[j] * by * __expf((hi - ch.x) + (lo - cl.x)) : 0.f;
+        v[j + 1] = c0 + j + 1 <= last ? v[j + 1] * by * __expf((hi - ch.y) + (lo - cl.y)) : 0.f;
+        v[j + 2] = c0 + j + 2 <= last ? v[j + 2] * by * __expf((hi - ch.z) + (lo - cl.z)) : 0.f;
+        v[j + 3] = c0 + j + 3 <= last ? v[j + 3] * by * __expf((hi - ch.w) + (lo - cl.w)) : 0.f;
       }
       if (warp < 2) {
 #pragma unroll
@@ -160,21 +233,14 @@ __global__ void __launch_bounds__(kPrepThreads) delta_chunk_kernel(const __grid_
       }
     }
     __syncthreads();
-    if (warp == 0) {
-      solve_column<0, KB>(sm, lane);
-    } else if (warp == 1) {
-      solve_column<32, KB>(sm, 32 + lane);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) sm.x[i][32 + lane] = 0.f;
-    }
-    __syncthreads();
+    invert(sm.a, sm.x);
     // rows of T by two threads each
     const int r = threadIdx.x >> 1, first = (threadIdx.x & 1) * 32;
 #pragma unroll
     for (int c = first; c < first + 32; c += 8) {
       float w[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = sm.x[r][c + j] * sm.c.beta[c + j];
+      for (int j = 0; j < 8; ++j) w[j] = c + j <= r ? sm.x[r][c + j] * sm.c.beta[c + j] : 0.f;
       store_split_row(out, out + kTileBytes, r, w, c);
     }
   }
@@ -205,6 +271,7 @@ template <int KB>
 struct ChainSmem {
   Stage<KB> st[2];
   uint8_t y[2 * kTileBytes];
+  uint8_t s[2][128 * 128];   // 128 rows of 32 values of the state on their way out, for each half of the keys
   ChainBars bar;
   uint32_t tmem;
   int abort, keep;
@@ -220,6 +287,27 @@ __device__ __forceinline__ void store_half(uint32_t at, const float (&v)[32]) {
   for (int j = 0; j < 16; ++j) split2(v[2 * j], v[2 * j + 1], hi[j], lo[j]);
   tmem_st16u(at, hi);
   tmem_st16u(at + 16, lo);
+}
+
+// 32 of a thread's keys (from `first` of its half) of the state before a chunk, through shared memory: rows of 128 bytes,
+// swizzled, leave as one tile.  By the four warps of a half.  (Straight from the registers, 32 bytes of 32 rows an
+// instruction, the walk took 4.7 us a chunk instead of CHAINUS.)
+template <int KB>
+__device__ __forceinline__ void send_state(ChainSmem<KB>& sm, const TcMaps& m, const float (&S)[KB * 32], int half, int first,
+                                           int v0, int cell, int64_t K) {
+  const int t = threadIdx.x & 127;
+  if (t == 0) bulk_wait_group_read<0>();   // the tile before has left
+  named_barrier(2 + half, 128);
+  uint8_t* to = sm.s[half];
+#pragma unroll
+  for (int k = 0; k < 32; k += 4)
+    *reinterpret_cast<float4*>(to + sw128_off32(t, k)) = make_float4(S[first + k], S[first + k + 1], S[first + k + 2], S[first + k + 3]);
+  fence_proxy_async_smem();
+  named_barrier(2 + half, 128);
+  if (t == 0 && half * KB * 32 + first < K) {
+    tma_store_4d(&m.states, to, half * KB * 32 + first, v0, cell, 0);
+    bulk_commit_group();
+  }
 }
 
 template <int KB>
@@ -370,7 +458,6 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     float S[KH];
 #pragma unroll
     for (int k = 0; k < KH; ++k) S[k] = p.init && live && k0 + k < p.K ? p.init[at + k] : 0.f;
-    const bool wide_s = (reinterpret_cast<uintptr_t>(p.states_out) & 31) == 0;
     const bool wide_f = (reinterpret_cast<uintptr_t>(p.final_state) & 31) == 0;
     for (int c = 0; c < nch; ++c) {
       const int s = c & 1;
@@ -389,12 +476,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.s_ready[half]);
-      if (p.states_out && live) {
-        float* to = p.states_out + (((int64_t)b * nch + c) * p.H + h) * p.V * p.K + (int64_t)row * p.K + k0;
-#pragma unroll
-        for (int k = 0; k < KH; k += 8)
-          if (k0 + k < p.K) store8(to + k, S + k, wide_s);
-      }
+      const int cell = (b * nch + c) * (int)p.H + h;
+      if (p.states_out) send_state<KB>(sm, m, S, half, 0, v0, cell, p.K);
       if (!wait_bar(&bar.full[s], (c >> 1) & 1, abort, p.hdr, 21)) break;   // the decays
       const float all = st.from[kChunk - 1];
       if (!wait_bar(&bar.x_full, par, abort, p.hdr, 22)) break;
@@ -416,6 +499,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.r_ready);
+      if (KB == 2 && p.states_out) send_state<KB>(sm, m, S, half, KH / 2, v0, cell, p.K);
       if (!wait_bar(&bar.u_full, par, abort, p.hdr, 23)) break;
       tc_fence_after();
       tmem_ld32(tmem + lanes + kColU + half * 32, x);
@@ -451,6 +535,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         for (int j = 0; j < 32; ++j) S[k + j] = fmaf(all, S[k + j], x[j]);
       }
     }
+    if ((threadIdx.x & 127) == 0) bulk_wait_group<0>();
     if (p.final_state && live && !*abort) {
 #pragma unroll
       for (int k = 0; k < KH; k += 8)
@@ -551,6 +636,18 @@ bool rows_fit(const void* base, const int64_t* stride, int64_t batch, int64_t T,
   return true;
 }
 
+// Map of [cells, V, K] f32 states in boxes of 128 values and 32 keys.
+bool state_map(CUtensorMap* m, const void* base, int64_t cells, int64_t V, int64_t K) {
+  const auto encode = tensor_map_encoder();
+  if (!encode) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)K, (cuuint64_t)V, (cuuint64_t)cells, 1};
+  const cuuint64_t strides[3] = {(cuuint64_t)K * 4, (cuuint64_t)(K * V * 4), (cuuint64_t)(K * V * 4)};
+  const cuuint32_t box[4] = {32, 128, 1, 1}, one[4] = {1, 1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, const_cast<void*>(base), dims, strides, box, one,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename K>
 cudaError_t allow_smem(K kernel, int bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -583,7 +680,8 @@ bool tc_takes(const Params& p, bool backward) {
   const int64_t most = INT32_MAX / 2;
   if (p.K % 8 != 0 || p.K > 128 || p.V % 8 != 0 || p.T > most || p.batch > most || p.T < kChunk / 2) return false;
   return rows_fit(p.q, p.qs, p.batch, p.T, p.Hk) && rows_fit(p.k, p.ks, p.batch, p.T, p.Hk) &&
-         rows_fit(p.v, p.vs, p.batch, p.T, p.H) && reinterpret_cast<uintptr_t>(p.y) % 16 == 0;
+         rows_fit(p.v, p.vs, p.batch, p.T, p.H) && reinterpret_cast<uintptr_t>(p.y) % 16 == 0 &&
+         reinterpret_cast<uintptr_t>(p.states_out) % 16 == 0 && p.batch * p.nch * p.H < most;
 }
 
 cudaError_t tc_forward(const Params& p, void* buffers, cudaStream_t st) {
@@ -591,7 +689,8 @@ cudaError_t tc_forward(const Params& p, void* buffers, cudaStream_t st) {
   memset(&m, 0, sizeof(m));
   const int64_t ys[3] = {p.T * p.H * p.V, p.H * p.V, p.V};
   if (!head_map(&m.q, p.q, p.batch, p.T, p.Hk, p.K, p.qs) || !head_map(&m.k, p.k, p.batch, p.T, p.Hk, p.K, p.ks) ||
-      !head_map(&m.v, p.v, p.batch, p.T, p.H, p.V, p.vs) || (p.y && !head_map(&m.y, p.y, p.batch, p.T, p.H, p.V, ys)))
+      !head_map(&m.v, p.v, p.batch, p.T, p.H, p.V, p.vs) || (p.y && !head_map(&m.y, p.y, p.batch, p.T, p.H, p.V, ys)) ||
+      (p.states_out && !state_map(&m.states, p.states_out, p.batch * p.nch * p.H, p.V, p.K)))
     return cudaErrorInvalidValue;
   TcBuffers buf;
   buf.squares = static_cast<uint8_t*>(buffers);

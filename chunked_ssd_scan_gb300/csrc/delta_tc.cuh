@@ -20,7 +20,7 @@ constexpr uint32_t kTileBytes = kChunk * kChunk * 2;
 constexpr uint32_t kSquareBytes = 4 * kTileBytes, kDecayBytes = 2 * kChunk * 4;
 
 struct TcMaps {
-  CUtensorMap q, k, v, y, dy, dv, dq, dk;
+  CUtensorMap q, k, v, y, dy, dv, dq, dk, states;
 };
 
 struct TcBuffers {
