@@ -566,7 +566,7 @@ Layout layout(const gated_delta_rule_shape* s, bool back) {
   size_t at = sizeof(WsHeader);
   const size_t nch = (size_t)((s->seqlen + kChunk - 1) / kChunk);
   L.chunks = at;
-  if (!back && tc_shape(s)) at = align_up(at + tc_forward_bytes(s->batch, (int64_t)nch, s->heads), kWsAlign);
+  if (tc_shape(s)) at = align_up(at + tc_bytes(s->batch, (int64_t)nch, s->heads, back), kWsAlign);
   if (back) {
     const size_t steps = (size_t)(s->batch * s->seqlen * s->heads * s->value_dim) * 4;
     const size_t states = (size_t)s->batch * nch * (size_t)(s->heads * s->value_dim * s->key_dim) * 4;
@@ -731,15 +731,7 @@ ssd_status gated_delta_rule_backward(const gated_delta_rule_shape* shape, const 
   p.beta = beta;
   p.hdr = reinterpret_cast<WsHeader*>(ws);
   p.err = reinterpret_cast<float*>(ws + L.err);
-  Params f = p;   // v - S k of every step, from the states before the chunks
-  f.states_in = states;
-  if (!states) {
-    f.init = init_state;
-    f.states_out = reinterpret_cast<float*>(ws + L.states);
-  }
-  cudaError_t ce = bf16 ? launch_walk<__nv_bfloat16>(f, states != nullptr, st) : launch_walk<float>(f, states != nullptr, st);
-  if (ce != cudaSuccess) return SSD_ERR_CUDA;
-  p.states_in = states ? states : f.states_out;
+  p.states_in = states ? states : reinterpret_cast<float*>(ws + L.states);
   p.dy = dy;
   p.dfinal = dfinal;
   p.dq = dq;
@@ -751,6 +743,13 @@ ssd_status gated_delta_rule_backward(const gated_delta_rule_shape* shape, const 
   p.du = reinterpret_cast<float*>(ws + L.du);
   p.dstates = reinterpret_cast<float*>(ws + L.dstates);
   p.partial = reinterpret_cast<float*>(ws + L.partial);
+  if (!states) p.init = init_state;
+  if (tc_shape(shape) && tc_takes(p, true)) return done(tc_backward(p, states != nullptr, ws + L.chunks, st));
+  Params f = p;   // v - S k of every step, from the states before the chunks
+  f.y = nullptr;
+  f.states_out = states ? nullptr : const_cast<float*>(p.states_in);
+  const cudaError_t ce = bf16 ? launch_walk<__nv_bfloat16>(f, states != nullptr, st) : launch_walk<float>(f, states != nullptr, st);
+  if (ce != cudaSuccess) return SSD_ERR_CUDA;
   return done(bf16 ? launch_backward<__nv_bfloat16>(p, st) : launch_backward<float>(p, st));
 }
 

@@ -25,8 +25,6 @@ namespace {
 
 using namespace delta;
 
-constexpr uint32_t kDHi = sdesc_sw128_hi(1024);
-
 // ---------------------------------------------------------------------------------------------------------------------
 // T and P of every chunk and head.  One product stacks K on Q (128 rows) against K: rows 0..63 are K K^T, the others
 // Q K^T; both are of the key head, the heads that share it take turns with their own decays and betas.
@@ -195,12 +193,17 @@ __global__ void __launch_bounds__(kPrepThreads, 6) delta_chunk_kernel(const __gr
   const uint32_t mine = tmem + ((uint32_t)(warp * 32) << 16);
   for (int64_t h = hk * group; done && h < (hk + 1) * group; ++h) {
     const int64_t cell = (b * p.nch + chunk) * p.H + h;
-    uint8_t* out = buf.squares + cell * kSquareBytes;
+    uint8_t* out = buf.squares + cell * buf.square;
     __syncthreads();
     if (warp == 0) chunk_decay_warp(p, sm.c, b, t0, n, h, lane);
     __syncthreads();
-    if (threadIdx.x < kChunk) buf.decays[cell * 2 * kChunk + threadIdx.x] = sm.c.from[threadIdx.x];
-    else buf.decays[cell * 2 * kChunk + threadIdx.x] = sm.c.to[threadIdx.x - kChunk];
+    float* decays = buf.decays + cell * 3 * kChunk;
+    if (threadIdx.x < kChunk) {
+      decays[threadIdx.x] = sm.c.from[threadIdx.x];
+      decays[2 * kChunk + threadIdx.x] = sm.c.beta[threadIdx.x];
+    } else {
+      decays[threadIdx.x] = sm.c.to[threadIdx.x - kChunk];
+    }
     const float hi = sm.c.hi[row], lo = sm.c.lo[row];
     const float by = warp < 2 ? sm.c.beta[row] : p.scale;
     const int last = warp < 2 ? row - 1 : row;   // the strict part of A, P with its diagonal
@@ -242,6 +245,11 @@ __global__ void __launch_bounds__(kPrepThreads, 6) delta_chunk_kernel(const __gr
 #pragma unroll
       for (int j = 0; j < 8; ++j) w[j] = c + j <= r ? sm.x[r][c + j] * sm.c.beta[c + j] : 0.f;
       store_split_row(out, out + kTileBytes, r, w, c);
+      if (buf.square > square_bytes(false)) {   // without beta, for the backward walk
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = c + j <= r ? sm.x[r][c + j] : 0.f;
+        store_split_row(out + 4 * kTileBytes, out + 5 * kTileBytes, r, w, c);
+      }
     }
   }
   tc_fence_before();
@@ -260,8 +268,8 @@ constexpr uint32_t kColS = 0, kColX = 128, kColU = 192, kColW = 256, kColD = 320
 template <int KB>
 struct Stage {
   uint8_t k[KB * kTileBytes], q[KB * kTileBytes], v[2 * kTileBytes], t[2 * kTileBytes], p[2 * kTileBytes];
-  float from[kChunk], to[kChunk];
-  uint8_t pad[512];
+  float from[kChunk], to[kChunk], beta[kChunk];
+  uint8_t pad[256];
 };
 struct ChainBars {
   uint64_t full[2], empty[2], s_ready[2], x_full, r_ready, u_full, w_ready, u_ready, d_full, o1_full, o_scaled, o2_full,
@@ -276,39 +284,6 @@ struct ChainSmem {
   uint32_t tmem;
   int abort, keep;
 };
-
-// Column of the k-step `ks` (16 steps of the chunk) of an operand kept in halves; lo is 16 further.
-__device__ __forceinline__ uint32_t half_col(int ks) { return (uint32_t)((ks >> 1) * 32 + (ks & 1) * 8); }
-
-// Two terms of 32 columns, written over the 32 columns' place: hi in the first 16, lo in the others.
-__device__ __forceinline__ void store_half(uint32_t at, const float (&v)[32]) {
-  uint32_t hi[16], lo[16];
-#pragma unroll
-  for (int j = 0; j < 16; ++j) split2(v[2 * j], v[2 * j + 1], hi[j], lo[j]);
-  tmem_st16u(at, hi);
-  tmem_st16u(at + 16, lo);
-}
-
-// 32 of a thread's keys (from `first` of its half) of the state before a chunk, through shared memory: rows of 128 bytes,
-// swizzled, leave as one tile.  By the four warps of a half.  (Straight from the registers, 32 bytes of 32 rows an
-// instruction, the walk took 4.7 us a chunk instead of CHAINUS.)
-template <int KB>
-__device__ __forceinline__ void send_state(ChainSmem<KB>& sm, const TcMaps& m, const float (&S)[KB * 32], int half, int first,
-                                           int v0, int cell, int64_t K) {
-  const int t = threadIdx.x & 127;
-  if (t == 0) bulk_wait_group_read<0>();   // the tile before has left
-  named_barrier(2 + half, 128);
-  uint8_t* to = sm.s[half];
-#pragma unroll
-  for (int k = 0; k < 32; k += 4)
-    *reinterpret_cast<float4*>(to + sw128_off32(t, k)) = make_float4(S[first + k], S[first + k + 1], S[first + k + 2], S[first + k + 3]);
-  fence_proxy_async_smem();
-  named_barrier(2 + half, 128);
-  if (t == 0 && half * KB * 32 + first < K) {
-    tma_store_4d(&m.states, to, half * KB * 32 + first, v0, cell, 0);
-    bulk_commit_group();
-  }
-}
 
 template <int KB>
 __global__ void __launch_bounds__(kChainThreads, 1)
@@ -359,8 +334,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       }
       tma_load_4d_elect(st.v, &m.v, &bar.full[s], v0, c * kChunk, h, b);
       tma_load_4d_elect(st.v + kTileBytes, &m.v, &bar.full[s], v0 + 64, c * kChunk, h, b);
-      bulk_load_elect(st.t, buf.squares + cell * kSquareBytes, 4 * kTileBytes, &bar.full[s]);
-      bulk_load_elect(st.from, buf.decays + cell * 2 * kChunk, kDecayBytes, &bar.full[s]);
+      bulk_load_elect(st.t, buf.squares + cell * buf.square, 4 * kTileBytes, &bar.full[s]);
+      bulk_load_elect(st.from, buf.decays + cell * 3 * kChunk, kDecayBytes, &bar.full[s]);
       issued = c + 1;
     }
     bool drained = true;   // nothing may still be written to this block's shared memory when it ends
@@ -378,7 +353,6 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       const uint32_t k_lo = sdesc_sw128_lo(smem_u32(st.k), 0), q_lo = sdesc_sw128_lo(smem_u32(st.q), 0);
       const uint32_t km_lo = sdesc_sw128_lo(smem_u32(st.k), kTileBytes), v_lo = sdesc_sw128_lo(smem_u32(st.v), kTileBytes);
       const uint32_t t_lo = sdesc_sw128_lo(smem_u32(st.t), 0), p_lo = sdesc_sw128_lo(smem_u32(st.p), 0);
-      constexpr uint32_t kLo = kTileBytes >> 4;   // from a square's hi to its lo
       if (!wait_bar(&bar.full[s], (c >> 1) & 1, abort, p.hdr, 12)) break;
       // X = S K^T, the first half of the keys as soon as its terms are there
 #pragma unroll
@@ -464,20 +438,13 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       const uint32_t par = c & 1;
       const Stage<KB>& st = sm.st[s];
       // the state's terms
-#pragma unroll
-      for (int k = 0; k < KH; k += 32) {
-        uint32_t hi[16], lo[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) split2(S[k + 2 * j], S[k + 2 * j + 1], hi[j], lo[j]);
-        tmem_st16u(tmem + lanes + kColS + (k0 + k) / 2, hi);
-        tmem_st16u(tmem + lanes + kColS + Kp / 2 + (k0 + k) / 2, lo);
-      }
+      store_state_terms(tmem + lanes + kColS + k0 / 2, Kp / 2, S);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.s_ready[half]);
       const int cell = (b * nch + c) * (int)p.H + h;
-      if (p.states_out) send_state<KB>(sm, m, S, half, 0, v0, cell, p.K);
+      if (p.states_out) send_state(sm.s[half], &m.states, S, half, 0, v0, cell, p.K);
       if (!wait_bar(&bar.full[s], (c >> 1) & 1, abort, p.hdr, 21)) break;   // the decays
       const float all = st.from[kChunk - 1];
       if (!wait_bar(&bar.x_full, par, abort, p.hdr, 22)) break;
@@ -499,7 +466,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.r_ready);
-      if (KB == 2 && p.states_out) send_state<KB>(sm, m, S, half, KH / 2, v0, cell, p.K);
+      if constexpr (KB == 2)
+        if (p.states_out) send_state(sm.s[half], &m.states, S, half, KH / 2, v0, cell, p.K);
       if (!wait_bar(&bar.u_full, par, abort, p.hdr, 23)) break;
       tc_fence_after();
       tmem_ld32(tmem + lanes + kColU + half * 32, x);
@@ -611,6 +579,48 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 }
 
 // ------------------------------------------------------------------------------------------------ host
+bool rows_fit(const void* base, const int64_t* stride, int64_t batch, int64_t T, int64_t heads) {
+  if (reinterpret_cast<uintptr_t>(base) % 16 != 0) return false;
+  const int64_t n[3] = {batch, T, heads};
+  for (int a = 0; a < 3; ++a)
+    if (n[a] > 1 && (stride[a] <= 0 || stride[a] % 8 != 0 || stride[a] >= (int64_t)1 << 38)) return false;
+  return true;
+}
+
+template <int KB>
+cudaError_t chunks_as(const Params& p, const TcMaps& m, const TcBuffers& buf, cudaStream_t st) {
+  constexpr int smem = sizeof(PrepSmem<KB>);
+  const cudaError_t e = cudaFuncSetAttribute(delta_chunk_kernel<KB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  delta_chunk_kernel<KB><<<(unsigned)(p.batch * p.nch * p.Hk), kPrepThreads, smem, st>>>(p, m, buf);
+  return cudaGetLastError();
+}
+
+template <int KB>
+cudaError_t chain_as(const Params& p, const TcMaps& m, const TcBuffers& buf, cudaStream_t st) {
+  constexpr int smem = sizeof(ChainSmem<KB>);
+  static_assert(smem <= 232448, "shared memory of a block");
+  const cudaError_t e = cudaFuncSetAttribute(delta_chain_kernel<KB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int vtiles = (int)((p.V + 127) / 128);
+  delta_chain_kernel<KB><<<(unsigned)(p.batch * p.H * vtiles), kChainThreads, smem, st>>>(p, m, buf, vtiles);
+  return cudaGetLastError();
+}
+
+TcBuffers buffers_in(void* at, const Params& p, bool backward) {
+  const size_t cells = (size_t)(p.batch * p.nch * p.H);
+  TcBuffers buf;
+  buf.square = square_bytes(backward);
+  buf.squares = static_cast<uint8_t*>(at);
+  buf.decays = reinterpret_cast<float*>(buf.squares + cells * buf.square);
+  buf.writes = reinterpret_cast<uint8_t*>(buf.decays) + align_up(cells * kDecayBytes, kWsAlign);
+  return buf;
+}
+
+}  // namespace
+
+namespace delta {
+
 // Map of [batch, steps, heads, cols] in boxes of 64 steps and 64 columns of one head.
 bool head_map(CUtensorMap* m, const void* base, int64_t batch, int64_t T, int64_t heads, int64_t cols, const int64_t* stride) {
   const auto encode = tensor_map_encoder();
@@ -628,14 +638,6 @@ bool head_map(CUtensorMap* m, const void* base, int64_t batch, int64_t T, int64_
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool rows_fit(const void* base, const int64_t* stride, int64_t batch, int64_t T, int64_t heads) {
-  if (reinterpret_cast<uintptr_t>(base) % 16 != 0) return false;
-  const int64_t n[3] = {batch, T, heads};
-  for (int a = 0; a < 3; ++a)
-    if (n[a] > 1 && (stride[a] <= 0 || stride[a] % 8 != 0 || stride[a] >= (int64_t)1 << 38)) return false;
-  return true;
-}
-
 // Map of [cells, V, K] f32 states in boxes of 128 values and 32 keys.
 bool state_map(CUtensorMap* m, const void* base, int64_t cells, int64_t V, int64_t K) {
   const auto encode = tensor_map_encoder();
@@ -648,40 +650,22 @@ bool state_map(CUtensorMap* m, const void* base, int64_t cells, int64_t V, int64
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename K>
-cudaError_t allow_smem(K kernel, int bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
-template <int KB>
-cudaError_t forward_as(const Params& p, const TcMaps& m, const TcBuffers& buf, cudaStream_t st) {
-  constexpr int prep = sizeof(PrepSmem<KB>), chain = sizeof(ChainSmem<KB>);
-  static_assert(chain <= 232448, "shared memory of a block");
-  cudaError_t e = allow_smem(delta_chunk_kernel<KB>, prep);
-  if (e == cudaSuccess) e = allow_smem(delta_chain_kernel<KB>, chain);
-  if (e != cudaSuccess) return e;
-  delta_chunk_kernel<KB><<<(unsigned)(p.batch * p.nch * p.Hk), kPrepThreads, prep, st>>>(p, m, buf);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const int vtiles = (int)((p.V + 127) / 128);
-  delta_chain_kernel<KB><<<(unsigned)(p.batch * p.H * vtiles), kChainThreads, chain, st>>>(p, m, buf, vtiles);
-  return cudaGetLastError();
-}
-
-}  // namespace
-
-namespace delta {
-
-size_t tc_forward_bytes(int64_t batch, int64_t nch, int64_t H) {
-  return (size_t)(batch * nch * H) * (kSquareBytes + kDecayBytes);
+size_t tc_bytes(int64_t batch, int64_t nch, int64_t H, bool backward) {
+  const size_t cells = (size_t)(batch * nch * H);
+  return cells * square_bytes(backward) + align_up(cells * kDecayBytes, kWsAlign) + (backward ? cells * 4 * kTileBytes : 0);
 }
 
 bool tc_takes(const Params& p, bool backward) {
   const int64_t most = INT32_MAX / 2;
   if (p.K % 8 != 0 || p.K > 128 || p.V % 8 != 0 || p.T > most || p.batch > most || p.T < kChunk / 2) return false;
-  return rows_fit(p.q, p.qs, p.batch, p.T, p.Hk) && rows_fit(p.k, p.ks, p.batch, p.T, p.Hk) &&
-         rows_fit(p.v, p.vs, p.batch, p.T, p.H) && reinterpret_cast<uintptr_t>(p.y) % 16 == 0 &&
-         reinterpret_cast<uintptr_t>(p.states_out) % 16 == 0 && p.batch * p.nch * p.H < most;
+  if (p.batch * p.nch * p.H >= most) return false;
+  if (!rows_fit(p.q, p.qs, p.batch, p.T, p.Hk) || !rows_fit(p.k, p.ks, p.batch, p.T, p.Hk) ||
+      !rows_fit(p.v, p.vs, p.batch, p.T, p.H))
+    return false;
+  auto on16 = [](const void* a) { return reinterpret_cast<uintptr_t>(a) % 16 == 0; };
+  if (!backward) return on16(p.y) && on16(p.states_out);
+  return p.V <= 128 && rows_fit(p.dy, p.ds, p.batch, p.T, p.H) && on16(p.dq) && on16(p.dk) && on16(p.dv) &&
+         on16(p.states_in) && on16(p.dfinal);
 }
 
 cudaError_t tc_forward(const Params& p, void* buffers, cudaStream_t st) {
@@ -692,10 +676,34 @@ cudaError_t tc_forward(const Params& p, void* buffers, cudaStream_t st) {
       !head_map(&m.v, p.v, p.batch, p.T, p.H, p.V, p.vs) || (p.y && !head_map(&m.y, p.y, p.batch, p.T, p.H, p.V, ys)) ||
       (p.states_out && !state_map(&m.states, p.states_out, p.batch * p.nch * p.H, p.V, p.K)))
     return cudaErrorInvalidValue;
-  TcBuffers buf;
-  buf.squares = static_cast<uint8_t*>(buffers);
-  buf.decays = reinterpret_cast<float*>(buf.squares + (size_t)(p.batch * p.nch * p.H) * kSquareBytes);
-  return p.K <= 64 ? forward_as<1>(p, m, buf, st) : forward_as<2>(p, m, buf, st);
+  const TcBuffers buf = buffers_in(buffers, p, false);
+  const cudaError_t e = p.K <= 64 ? chunks_as<1>(p, m, buf, st) : chunks_as<2>(p, m, buf, st);
+  if (e != cudaSuccess) return e;
+  return p.K <= 64 ? chain_as<1>(p, m, buf, st) : chain_as<2>(p, m, buf, st);
+}
+
+cudaError_t tc_backward(const Params& p, bool states_known, void* buffers, cudaStream_t st) {
+  TcMaps m;
+  memset(&m, 0, sizeof(m));
+  const int64_t ks[3] = {p.T * p.Hk * p.K, p.Hk * p.K, p.K};
+  const int64_t cells = p.batch * p.nch * p.H;
+  if (!head_map(&m.q, p.q, p.batch, p.T, p.Hk, p.K, p.qs) || !head_map(&m.k, p.k, p.batch, p.T, p.Hk, p.K, p.ks) ||
+      !head_map(&m.v, p.v, p.batch, p.T, p.H, p.V, p.vs) || !head_map(&m.dy, p.dy, p.batch, p.T, p.H, p.V, p.ds) ||
+      !head_map(&m.dq, p.dq, p.batch, p.T, p.Hk, p.K, ks) || !head_map(&m.dk, p.dk, p.batch, p.T, p.Hk, p.K, ks))
+    return cudaErrorInvalidValue;
+  const TcBuffers buf = buffers_in(buffers, p, true);
+  cudaError_t e = p.K <= 64 ? chunks_as<1>(p, m, buf, st) : chunks_as<2>(p, m, buf, st);
+  if (e == cudaSuccess && !states_known) {
+    Params f = p;
+    f.y = nullptr;
+    f.final_state = nullptr;
+    f.states_out = const_cast<float*>(p.states_in);
+    if (!state_map(&m.states, f.states_out, cells, p.V, p.K)) return cudaErrorInvalidValue;
+    e = p.K <= 64 ? chain_as<1>(f, m, buf, st) : chain_as<2>(f, m, buf, st);
+  }
+  if (e != cudaSuccess) return e;
+  if (!state_map(&m.states, p.dstates, cells, p.V, p.K)) return cudaErrorInvalidValue;
+  return tc_backward_kernels(p, m, buf, st);
 }
 
 }  // namespace delta

@@ -1,0 +1,799 @@
+// Gated delta rule on the tensor cores, backward (the forms and the notation are those of delta_rule_tc.cu).  With G the
+// gradient of the state behind a chunk and I_ = (I + A)^-1:
+//   dU = P^T dY + diag(E) K G^T;   dR = I_^T dU, the gradient of v - S k;   dV = beta dR
+//   gradient of the state before the chunk = D_last G + scale (diag(D) dY)^T Q - (diag(D beta) dR)^T K
+// is a walk from the last chunk to the first, of the forward walk's form (delta_chain_back_kernel); it leaves dR and G
+// of every chunk.  From these, the states that the forward kept and U, formed anew, all else follows chunk by chunk in
+// parallel (delta_grad_kernel), keys in the 128 lanes of TMEM:
+//   dQ^T = scale S^T dY^T diag(D) + K^T Bm^T,               Bm = scale M o (dY U^T)
+//   dK^T = G^T U^T diag(E) - S^T dR^T diag(D beta) + Q^T Bm + (K^T N'^T) diag(beta) + K^T diag(beta) N',
+//                                                           N' = -M o (dR U^T) below the diagonal
+//   dbeta_i = dR_i . v_i - k_i . (D_i S^T dR_i - (K^T N'^T)_i)
+//   dg_i = sum_{j >= i} (q_j . dq_j - beta_j dR_j . v_j) + D_last <G, S> + sum_j E_j k_j . G^T u_j
+// (dq_j of one head; the sum over a chunk's steps, not over the sequence, whose terms would cancel).
+#include <string.h>
+
+#include <algorithm>
+
+#include "delta_tc.cuh"
+#include "launch.h"
+
+namespace ssd {
+namespace {
+
+using namespace delta;
+
+// ---------------------------------------------------------------------------------------------------------------------
+// The walk.  TMEM columns: G's two terms, P^T dY, K G^T and after it dU's two terms, dR, what of it enters G, the sum
+// that G takes.  K and dY have two buffers, the others one: what is used early in a chunk is loaded again while the
+// rest of it runs.
+// ---------------------------------------------------------------------------------------------------------------------
+constexpr int kChainThreads = 14 * 32;
+constexpr uint32_t kColG = 0, kColY = 128, kColU = 192, kColR = 256, kColW = 320, kColD = 384;
+
+template <int KB>
+struct BackSmem {
+  uint8_t k[2][KB * kTileBytes], dy[2][2 * kTileBytes];
+  uint8_t q[KB * kTileBytes], t[2 * kTileBytes], p[2 * kTileBytes];
+  uint8_t dys[2][2 * kTileBytes];   // scale D dY, hi and lo
+  uint8_t r[4 * kTileBytes];        // dR on its way out: by 64 values, hi then lo
+  uint8_t s[2][128 * 128];          // G on its way out
+  float decays[2][3 * kChunk];
+  uint64_t kdy_full[2], kdy_empty[2], q_full, q_empty, t_full, t_empty, p_full, p_empty;
+  uint64_t g_ready[2], y_full, u_ready, r_full, w_ready, r_free, dys_ready, d_full, drain;
+  uint32_t tmem;
+  int abort, keep;
+};
+
+template <int KB>
+__global__ void __launch_bounds__(kChainThreads, 1)
+    delta_chain_back_kernel(const __grid_constant__ Params p, const __grid_constant__ TcMaps m, TcBuffers buf) {
+  extern __shared__ __align__(1024) uint8_t raw[];
+  BackSmem<KB>& sm = *reinterpret_cast<BackSmem<KB>*>(raw);
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x / 32), 0), lane = threadIdx.x % 32;
+  const int h = blockIdx.x % (int)p.H, b = blockIdx.x / (int)p.H, hk = h / (int)(p.H / p.Hk), nch = (int)p.nch;
+  constexpr int Kp = KB * 64;
+  volatile int* abort = &sm.abort;
+  if (threadIdx.x == 0) {
+    sm.abort = sm.keep = 0;
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sm.kdy_full[s], 1);
+      mbar_init(&sm.kdy_empty[s], 1);
+      mbar_init(&sm.g_ready[s], 4);
+    }
+    for (uint64_t* one : {&sm.q_full, &sm.q_empty, &sm.t_full, &sm.t_empty, &sm.p_full, &sm.p_empty, &sm.y_full, &sm.r_full,
+                          &sm.d_full, &sm.drain})
+      mbar_init(one, 1);
+    mbar_init(&sm.u_ready, 8);
+    mbar_init(&sm.w_ready, 8);
+    mbar_init(&sm.r_free, 4);
+    mbar_init(&sm.dys_ready, 4);
+    fence_mbar_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(&sm.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+  // n counts chunks done, c is the chunk: nch - 1 - n
+  if (warp == 13) {   // loads
+    int pairs = 0, ps = 0, ts = 0, qs = 0;   // loads issued
+    for (int n = 0; n < nch; ++n) {
+      const int s = n & 1, c = nch - 1 - n;
+      const uint32_t par = (n - 1) & 1;
+      const int64_t cell = ((int64_t)b * nch + c) * p.H + h;
+      const uint8_t* sq = buf.squares + cell * buf.square;
+      if (n >= 2 && !wait_bar(&sm.kdy_empty[s], ((n >> 1) - 1) & 1, abort, p.hdr, 40)) break;
+      mbar_arrive_expect_tx_elect(&sm.kdy_full[s], (KB + 2) * kTileBytes + kDecayBytes);
+      bulk_load_elect(sm.decays[s], buf.decays + cell * 3 * kChunk, kDecayBytes, &sm.kdy_full[s]);
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+        tma_load_4d_elect(sm.k[s] + kb * kTileBytes, &m.k, &sm.kdy_full[s], kb * 64, c * kChunk, hk, b);
+      tma_load_4d_elect(sm.dy[s], &m.dy, &sm.kdy_full[s], 0, c * kChunk, h, b);
+      tma_load_4d_elect(sm.dy[s] + kTileBytes, &m.dy, &sm.kdy_full[s], 64, c * kChunk, h, b);
+      pairs = n + 1;
+      if (n >= 1 && !wait_bar(&sm.p_empty, par, abort, p.hdr, 41)) break;
+      mbar_arrive_expect_tx_elect(&sm.p_full, 2 * kTileBytes);
+      bulk_load_elect(sm.p, sq + 2 * kTileBytes, 2 * kTileBytes, &sm.p_full);
+      ps = n + 1;
+      if (n >= 1 && !wait_bar(&sm.t_empty, par, abort, p.hdr, 42)) break;
+      mbar_arrive_expect_tx_elect(&sm.t_full, 2 * kTileBytes);
+      bulk_load_elect(sm.t, sq + 4 * kTileBytes, 2 * kTileBytes, &sm.t_full);
+      ts = n + 1;
+      if (n >= 1 && !wait_bar(&sm.q_empty, par, abort, p.hdr, 43)) break;
+      mbar_arrive_expect_tx_elect(&sm.q_full, KB * kTileBytes);
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+        tma_load_4d_elect(sm.q + kb * kTileBytes, &m.q, &sm.q_full, kb * 64, c * kChunk, hk, b);
+      qs = n + 1;
+    }
+    bool drained = true;
+    for (int s = 0; s < 2; ++s) {
+      const int loads = pairs > s ? (pairs - 1 - s) / 2 + 1 : 0;
+      if (loads > 0) drained &= mbar_wait_bounded(&sm.kdy_full[s], (loads - 1) & 1, 2000000000ull);
+    }
+    if (ps > 0) drained &= mbar_wait_bounded(&sm.p_full, (ps - 1) & 1, 2000000000ull);
+    if (ts > 0) drained &= mbar_wait_bounded(&sm.t_full, (ts - 1) & 1, 2000000000ull);
+    if (qs > 0) drained &= mbar_wait_bounded(&sm.q_full, (qs - 1) & 1, 2000000000ull);
+    if (!drained && lane == 0) latch_error(p.hdr, SSD_ERR_TIMEOUT, 44);
+  } else if (warp == 12) {   // products
+    constexpr uint32_t id_k = idesc_bf16(128, 64, 0, 0), id_p = idesc_bf16(128, 64, 1, 1), id_t = idesc_bf16(128, 64, 0, 1);
+    constexpr uint32_t id_q = idesc_bf16(128, Kp, 1, 1), id_d = idesc_bf16(128, Kp, 0, 1);
+    const uint32_t p_lo = sdesc_sw128_lo(smem_u32(sm.p), 0), t_lo = sdesc_sw128_lo(smem_u32(sm.t), 0);
+    const uint32_t q_lo = sdesc_sw128_lo(smem_u32(sm.q), kTileBytes);
+    const uint32_t s_hi = sdesc_sw128_lo(smem_u32(sm.dys[0]), kTileBytes), s_lo = sdesc_sw128_lo(smem_u32(sm.dys[1]), kTileBytes);
+    for (int n = 0; n < nch; ++n) {
+      const int s = n & 1;
+      const uint32_t par = n & 1;
+      const uint32_t k_lo = sdesc_sw128_lo(smem_u32(sm.k[s]), 0), km_lo = sdesc_sw128_lo(smem_u32(sm.k[s]), kTileBytes);
+      const uint32_t dy_lo = sdesc_sw128_lo(smem_u32(sm.dy[s]), kTileBytes);
+      if (!wait_bar(&sm.kdy_full[s], (n >> 1) & 1, abort, p.hdr, 45)) break;
+      if (!wait_bar(&sm.p_full, par, abort, p.hdr, 46)) break;
+      // P^T dY (its accumulator was read before the chunk before this one was through)
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        mma_ss_we(tmem + kColY, dy_lo + ks * (2048 >> 4), kDHi, p_lo + ks * (2048 >> 4), kDHi, id_p, ks > 0);
+        mma_ss_we(tmem + kColY, dy_lo + ks * (2048 >> 4), kDHi, p_lo + kLo + ks * (2048 >> 4), kDHi, id_p, 1);
+      }
+      mma_commit_elect(&sm.p_empty);
+      // K G^T
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (!wait_bar(&sm.g_ready[half], par, abort, p.hdr, 47)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = half * KB * 2; ks < (half + 1) * KB * 2; ++ks) {
+          const uint32_t at = k_lo + (((ks >> 2) * kTileBytes + (ks & 3) * 32) >> 4);
+          mma_ts_we(tmem + kColU, tmem + kColG + ks * 8, at, kDHi, id_k, ks > 0);
+          mma_ts_we(tmem + kColU, tmem + kColG + Kp / 2 + ks * 8, at, kDHi, id_k, 1);
+        }
+      }
+      if (*abort) break;
+      mma_commit_elect(&sm.y_full);
+      // scale (D dY)^T Q, while dU is made
+      if (!wait_bar(&sm.q_full, par, abort, p.hdr, 48)) break;
+      if (!wait_bar(&sm.dys_ready, par, abort, p.hdr, 49)) break;
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        mma_ss_we(tmem + kColD, s_hi + ks * (2048 >> 4), kDHi, q_lo + ks * (2048 >> 4), kDHi, id_q, ks > 0);
+        mma_ss_we(tmem + kColD, s_lo + ks * (2048 >> 4), kDHi, q_lo + ks * (2048 >> 4), kDHi, id_q, 1);
+      }
+      mma_commit_elect(&sm.q_empty);
+      // dR^T = dU^T I_
+      if (!wait_bar(&sm.t_full, par, abort, p.hdr, 50)) break;
+      if (n > 0 && !wait_bar(&sm.r_free, (n - 1) & 1, abort, p.hdr, 51)) break;
+      if (!wait_bar(&sm.u_ready, par, abort, p.hdr, 52)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        const uint32_t a = tmem + kColU + half_col(ks);
+        mma_ts_we(tmem + kColR, a, t_lo + ks * (2048 >> 4), kDHi, id_t, ks > 0);
+        mma_ts_we(tmem + kColR, a, t_lo + kLo + ks * (2048 >> 4), kDHi, id_t, 1);
+        mma_ts_we(tmem + kColR, a + 16, t_lo + ks * (2048 >> 4), kDHi, id_t, 1);
+      }
+      mma_commit_elect(&sm.r_full);
+      mma_commit_elect(&sm.t_empty);
+      // - (D beta dR)^T K
+      if (!wait_bar(&sm.w_ready, par, abort, p.hdr, 53)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        const uint32_t a = tmem + kColW + half_col(ks);
+        mma_ts_we(tmem + kColD, a, km_lo + ks * (2048 >> 4), kDHi, id_d, 1);
+        mma_ts_we(tmem + kColD, a + 16, km_lo + ks * (2048 >> 4), kDHi, id_d, 1);
+      }
+      mma_commit_elect(&sm.d_full);
+      mma_commit_elect(&sm.kdy_empty[s]);
+    }
+    mma_commit_elect(&sm.drain);
+    if (!mbar_wait_bounded(&sm.drain, 0, 2000000000ull) && lane == 0) {
+      sm.keep = 1;
+      latch_error(p.hdr, SSD_ERR_TIMEOUT, 54);
+    }
+  } else if (warp < 8) {   // G; a thread has a value and half the keys
+    constexpr int KH = Kp / 2;
+    const int half = warp >> 2, row = (warp & 3) * 32 + lane, k0 = half * KH;
+    const bool live = row < p.V;
+    const int64_t at = (((int64_t)b * p.H + h) * p.V + row) * p.K + k0;
+    float G[KH];
+#pragma unroll
+    for (int k = 0; k < KH; ++k) G[k] = p.dfinal && live && k0 + k < p.K ? p.dfinal[at + k] : 0.f;
+    for (int n = 0; n < nch; ++n) {
+      const int s = n & 1, c = nch - 1 - n;
+      const uint32_t par = n & 1;
+      const float* from = sm.decays[s];
+      const float *to = from + kChunk, *beta = from + 2 * kChunk;
+      store_state_terms(tmem + lanes + kColG + k0 / 2, Kp / 2, G);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.g_ready[half]);
+      const int cell = (b * nch + c) * (int)p.H + h;
+      send_state(sm.s[half], &m.states, G, half, 0, 0, cell, p.K);
+      if (!wait_bar(&sm.kdy_full[s], (n >> 1) & 1, abort, p.hdr, 55)) break;   // the decays
+      const float all = from[kChunk - 1];
+      if (!wait_bar(&sm.y_full, par, abort, p.hdr, 56)) break;
+      tc_fence_after();
+      float x[32], y[32];
+      tmem_ld32(tmem + lanes + kColY + half * 32, y);
+      tmem_ld32(tmem + lanes + kColU + half * 32, x);
+      tmem_ld_wait();
+      reg_tie(x);
+      reg_tie(y);
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(&to[half * 32 + j]);
+        x[j] = fmaf(x[j], f.x, y[j]);
+        x[j + 1] = fmaf(x[j + 1], f.y, y[j + 1]);
+        x[j + 2] = fmaf(x[j + 2], f.z, y[j + 2]);
+        x[j + 3] = fmaf(x[j + 3], f.w, y[j + 3]);
+      }
+      store_half(tmem + lanes + kColU + half * 32, x);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.u_ready);
+      if constexpr (KB == 2) send_state(sm.s[half], &m.states, G, half, KH / 2, 0, cell, p.K);
+      if (!wait_bar(&sm.r_full, par, abort, p.hdr, 57)) break;
+      tc_fence_after();
+      tmem_ld32(tmem + lanes + kColR + half * 32, x);
+      tmem_ld_wait();
+      reg_tie(x);
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(&from[half * 32 + j]);
+        const float4 g = *reinterpret_cast<const float4*>(&beta[half * 32 + j]);
+        x[j] *= -f.x * g.x;
+        x[j + 1] *= -f.y * g.y;
+        x[j + 2] *= -f.z * g.z;
+        x[j + 3] *= -f.w * g.w;
+      }
+      store_half(tmem + lanes + kColW + half * 32, x);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.w_ready);
+      if (!wait_bar(&sm.d_full, par, abort, p.hdr, 58)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < KH; k += 32) {
+        tmem_ld32(tmem + lanes + kColD + k0 + k, x);
+        tmem_ld_wait();
+        reg_tie(x);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) G[k + j] = fmaf(all, G[k + j], x[j]);
+      }
+    }
+    if ((threadIdx.x & 127) == 0) bulk_wait_group<0>();
+    if (p.dinit && live && !*abort) {
+      const bool wide = (reinterpret_cast<uintptr_t>(p.dinit) & 31) == 0;
+#pragma unroll
+      for (int k = 0; k < KH; k += 8)
+        if (k0 + k < p.K) store8(p.dinit + at + k, G + k, wide);
+    }
+  } else {   // scale D dY in two terms, and dR on its way out
+    const int t = threadIdx.x - 256, v = (warp & 3) * 32 + lane;
+    for (int n = 0; n < nch; ++n) {
+      const int s = n & 1, c = nch - 1 - n;
+      const uint32_t par = n & 1;
+      if (!wait_bar(&sm.kdy_full[s], (n >> 1) & 1, abort, p.hdr, 59)) break;
+      if (n > 0 && !wait_bar(&sm.d_full, (n - 1) & 1, abort, p.hdr, 60)) break;   // the last terms have been read
+#pragma unroll
+      for (int m8 = 0; m8 < 8; ++m8) {   // 16 bytes of a row
+        const int at = m8 * 128 + t, blk = at >> 9, i = (at >> 3) & 63, col = (at & 7) * 8;
+        const uint32_t off = blk * kTileBytes + sw128_off16(i, col);
+        const uint4 d = *reinterpret_cast<const uint4*>(sm.dy[s] + off);
+        const float f = sm.decays[s][i] * p.scale;
+        uint4 hi, lo;
+        split2(__uint_as_float(d.x << 16) * f, __uint_as_float(d.x & 0xffff0000u) * f, hi.x, lo.x);
+        split2(__uint_as_float(d.y << 16) * f, __uint_as_float(d.y & 0xffff0000u) * f, hi.y, lo.y);
+        split2(__uint_as_float(d.z << 16) * f, __uint_as_float(d.z & 0xffff0000u) * f, hi.z, lo.z);
+        split2(__uint_as_float(d.w << 16) * f, __uint_as_float(d.w & 0xffff0000u) * f, hi.w, lo.w);
+        *reinterpret_cast<uint4*>(sm.dys[0] + off) = hi;
+        *reinterpret_cast<uint4*>(sm.dys[1] + off) = lo;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.dys_ready);
+      if (!wait_bar(&sm.r_full, par, abort, p.hdr, 61)) break;
+      tc_fence_after();
+      float r0[32], r1[32];
+      tmem_ld32(tmem + lanes + kColR, r0);
+      tmem_ld32(tmem + lanes + kColR + 32, r1);
+      tmem_ld_wait();
+      reg_tie(r0);
+      reg_tie(r1);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.r_free);
+      if (warp == 8 && lane == 0) bulk_wait_group_read<0>();
+      named_barrier(1, 128);
+      uint8_t* out = sm.r + (v >> 6) * 2 * kTileBytes;
+#pragma unroll
+      for (int j = 0; j < 64; ++j) {
+        const float x = j < 32 ? r0[j & 31] : r1[j & 31];
+        const __nv_bfloat16 hi = __float2bfloat16_rn(x);
+        const uint32_t off = sw128_off16(j, v & 63);
+        *reinterpret_cast<__nv_bfloat16*>(out + off) = hi;
+        *reinterpret_cast<__nv_bfloat16*>(out + kTileBytes + off) = __float2bfloat16_rn(x - __bfloat162float(hi));
+      }
+      fence_proxy_async_smem();
+      named_barrier(1, 128);
+      if (warp == 8 && lane == 0) {
+        const int64_t cell = ((int64_t)b * nch + c) * p.H + h;
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(buf.writes + cell * 4 * kTileBytes),
+                     "r"(smem_u32(sm.r)), "r"(4 * kTileBytes)
+                     : "memory");
+        bulk_commit_group();
+      }
+    }
+    if (warp == 8 && lane == 0) bulk_wait_group<0>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12 && !sm.keep) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------------------------------
+// One chunk and key head a block; the heads that share the keys one after the other.
+// ---------------------------------------------------------------------------------------------------------------------
+constexpr int kGradThreads = 256;
+// TMEM: X and -D X, then dY U^T over dR U^T; U, then the products with dR's second term; S^T dY^T; S^T dR^T; G^T U^T;
+// K^T Bm^T; Q^T Bm + K^T diag(beta) N'; K^T N'^T.
+enum : uint32_t { kX = 0, kU = 64, kSY = 128, kSR = 192, kGU = 256, kKB = 320, kQB = 384, kKN = 448 };
+
+struct GradSmem {
+  uint8_t k[2 * kTileBytes], q[2 * kTileBytes];
+  uint8_t dyr[2][3 * kTileBytes];     // by 64 values: dY, dR hi, dR lo
+  uint8_t u[4 * kTileBytes];          // hi by 64 values, lo
+  uint8_t s[4][2 * kTileBytes];       // S, then G: hi by 64 keys, lo; 128 rows of values
+  uint8_t v[2 * kTileBytes], t[2 * kTileBytes];   // then Bm hi, lo; N' hi, lo
+  uint8_t n2[2 * kTileBytes];         // diag(beta) N'
+  ChunkDecay c;
+  float dot[kChunk];                  // dR . v
+  uint64_t loaded, done, shadow;
+  uint32_t tmem;
+  int abort, keep;
+};
+static_assert(sizeof(GradSmem) <= 232448, "shared memory of a block");
+
+// The rows of a state [V, K] f32 as two terms in shared memory, zeros around it; with kInner the sum of the products with
+// what stood there.
+template <bool kInner>
+__device__ __forceinline__ float stage_state(GradSmem& sm, const float* S, int64_t V, int64_t K) {
+  float inner = 0.f;
+#pragma unroll 2
+  for (int it = 0; it < 8; ++it) {
+    const int at = it * kGradThreads + threadIdx.x, row = at >> 4, col = (at & 15) * 8;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    if (S && row < V && col < K) {
+      a = *reinterpret_cast<const float4*>(S + row * K + col);
+      b = *reinterpret_cast<const float4*>(S + row * K + col + 4);
+    }
+    uint8_t* hi_at = sm.s[col >> 6] + sw128_off16(row, col & 63);
+    uint8_t* lo_at = hi_at + 4 * kTileBytes;
+    if constexpr (kInner) {
+      const uint4 h = *reinterpret_cast<const uint4*>(hi_at), l = *reinterpret_cast<const uint4*>(lo_at);
+      auto pair = [&](uint32_t hh, uint32_t ll, float x, float y) {
+        inner = fmaf(x, __uint_as_float(hh << 16) + __uint_as_float(ll << 16), inner);
+        inner = fmaf(y, __uint_as_float(hh & 0xffff0000u) + __uint_as_float(ll & 0xffff0000u), inner);
+      };
+      pair(h.x, l.x, a.x, a.y);
+      pair(h.y, l.y, a.z, a.w);
+      pair(h.z, l.z, b.x, b.y);
+      pair(h.w, l.w, b.z, b.w);
+    }
+    uint4 hi, lo;
+    split2(a.x, a.y, hi.x, lo.x);
+    split2(a.z, a.w, hi.y, lo.y);
+    split2(b.x, b.y, hi.z, lo.z);
+    split2(b.z, b.w, hi.w, lo.w);
+    *reinterpret_cast<uint4*>(hi_at) = hi;
+    *reinterpret_cast<uint4*>(lo_at) = lo;
+  }
+  return inner;
+}
+
+__global__ void __launch_bounds__(kGradThreads, 1)
+    delta_grad_kernel(const __grid_constant__ Params p, const __grid_constant__ TcMaps m, TcBuffers buf) {
+  extern __shared__ __align__(1024) uint8_t raw[];
+  GradSmem& sm = *reinterpret_cast<GradSmem*>(raw);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid / 32, 0), lane = tid % 32;
+  const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
+  int64_t id = blockIdx.x;
+  const int64_t hk = id % p.Hk;
+  id /= p.Hk;
+  const int64_t chunk = id % p.nch, b = id / p.nch, t0 = chunk * kChunk, group = p.H / p.Hk, KV = p.K * p.V;
+  const int n = (int)min((int64_t)kChunk, p.T - t0);
+  if (tid == 0) {
+    mbar_init(&sm.loaded, 1);
+    mbar_init(&sm.done, 1);
+    mbar_init(&sm.shadow, 1);
+    sm.abort = sm.keep = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&sm.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem, mine = tmem + ((uint32_t)(quarter * 32) << 16);
+  volatile int* abort = &sm.abort;
+  constexpr uint32_t kk = idesc_bf16(128, 64, 0, 0), mk = idesc_bf16(128, 64, 1, 0), mm = idesc_bf16(128, 64, 1, 1);
+  constexpr uint32_t kStep = 2048 >> 4, kStateLo = (4 * kTileBytes) >> 4;
+  const uint32_t k_lo = sdesc_sw128_lo(smem_u32(sm.k), 0), km_lo = sdesc_sw128_lo(smem_u32(sm.k), kTileBytes);
+  const uint32_t qm_lo = sdesc_sw128_lo(smem_u32(sm.q), kTileBytes);
+  const uint32_t s_lo = sdesc_sw128_lo(smem_u32(sm.s[0]), 0), sm_lo = sdesc_sw128_lo(smem_u32(sm.s[0]), 2 * kTileBytes);
+  const uint32_t dyr_lo = sdesc_sw128_lo(smem_u32(sm.dyr[0]), 0), u_lo = sdesc_sw128_lo(smem_u32(sm.u), 0);
+  const uint32_t v_lo = sdesc_sw128_lo(smem_u32(sm.v), kTileBytes), t_lo = sdesc_sw128_lo(smem_u32(sm.t), 0);
+  const uint32_t bm_lo = sdesc_sw128_lo(smem_u32(sm.v), 0), n1_lo = t_lo, n2_lo = sdesc_sw128_lo(smem_u32(sm.n2), 0);
+  // of 128 values in blocks of 64: step ks of 16
+  auto by64 = [](int ks, uint32_t block) { return (ks >> 2) * (block >> 4) + (ks & 3) * 2; };
+  uint32_t phase = 0, shadows = 0;
+  float dq[32] = {}, dk[32] = {};
+  bool ok = true;
+  for (int64_t h = hk * group; ok && h < (hk + 1) * group; ++h) {
+    const int64_t cell = (b * p.nch + chunk) * p.H + h;
+    const uint32_t turn = (uint32_t)(h - hk * group) & 1;
+    __syncthreads();   // what the head before has left in shared memory and TMEM has been read
+    if (warp == 0) {
+      const bool first = h == hk * group;
+      mbar_arrive_expect_tx_elect(&sm.loaded, (first ? 14 : 10) * kTileBytes);
+      if (first) {
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {   // keys past K are zeros
+          tma_load_4d_elect(sm.k + kb * kTileBytes, &m.k, &sm.loaded, kb * 64, (int)t0, (int)hk, (int)b);
+          tma_load_4d_elect(sm.q + kb * kTileBytes, &m.q, &sm.loaded, kb * 64, (int)t0, (int)hk, (int)b);
+        }
+      }
+#pragma unroll
+      for (int vb = 0; vb < 2; ++vb) {
+        tma_load_4d_elect(sm.dyr[vb], &m.dy, &sm.loaded, vb * 64, (int)t0, (int)h, (int)b);
+        tma_load_4d_elect(sm.v + vb * kTileBytes, &m.v, &sm.loaded, vb * 64, (int)t0, (int)h, (int)b);
+        bulk_load_elect(sm.dyr[vb] + kTileBytes, buf.writes + (cell * 4 + vb * 2) * kTileBytes, 2 * kTileBytes, &sm.loaded);
+      }
+      bulk_load_elect(sm.t, buf.squares + cell * buf.square, 2 * kTileBytes, &sm.loaded);
+    } else if (warp == 1) {
+      chunk_decay_warp(p, sm.c, b, t0, n, h, lane);
+    }
+    stage_state<false>(sm, p.states_in + cell * KV, p.V, p.K);
+    fence_proxy_async_smem();
+    const bool here = wait_bar(&sm.loaded, turn, abort, p.hdr, 70);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (!here || *abort) break;   // (the same for all: the flag is set before the barrier)
+    if (warp == 0) {
+      // X = S K^T and V T^T
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        mma_ss_we(tmem + kX, s_lo + by64(ks, 2 * kTileBytes), kDHi, k_lo + by64(ks, kTileBytes), kDHi, kk, ks > 0);
+        mma_ss_we(tmem + kX, s_lo + kStateLo + by64(ks, 2 * kTileBytes), kDHi, k_lo + by64(ks, kTileBytes), kDHi, kk, 1);
+      }
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        mma_ss_we(tmem + kU, v_lo + ks * kStep, kDHi, t_lo + ks * 2, kDHi, mk, ks > 0);
+        mma_ss_we(tmem + kU, v_lo + ks * kStep, kDHi, t_lo + kLo + ks * 2, kDHi, mk, 1);
+      }
+      mma_commit_elect(&sm.done);
+      // S^T dY^T and S^T dR^T
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        const uint32_t a = sm_lo + ks * kStep, at = dyr_lo + by64(ks, 3 * kTileBytes);
+        mma_ss_we(tmem + kSY, a, kDHi, at, kDHi, mk, ks > 0);
+        mma_ss_we(tmem + kSY, a + kStateLo, kDHi, at, kDHi, mk, 1);
+        mma_ss_we(tmem + kSR, a, kDHi, at + kLo, kDHi, mk, ks > 0);
+        mma_ss_we(tmem + kSR, a, kDHi, at + 2 * kLo, kDHi, mk, 1);
+        mma_ss_we(tmem + kSR, a + kStateLo, kDHi, at + kLo, kDHi, mk, 1);
+      }
+      mma_commit_elect(&sm.shadow);
+    }
+    // dv = beta dR, and dR . v: four threads a step, 16 bytes at a time
+    {
+      const int i = tid >> 2, part = tid & 3;
+      const float beta = sm.c.beta[i];
+      float dot = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int col = (e * 4 + part) * 8, vb = col >> 6;
+        const uint32_t off = sw128_off16(i, col & 63);
+        const uint4 hi = *reinterpret_cast<const uint4*>(sm.dyr[vb] + kTileBytes + off);
+        const uint4 lo = *reinterpret_cast<const uint4*>(sm.dyr[vb] + 2 * kTileBytes + off);
+        const uint4 v = *reinterpret_cast<const uint4*>(sm.v + vb * kTileBytes + off);
+        uint32_t out[4];
+        auto pair = [&](uint32_t a, uint32_t l, uint32_t w, uint32_t& o) {
+          const float x = __uint_as_float(a << 16) + __uint_as_float(l << 16);
+          const float y = __uint_as_float(a & 0xffff0000u) + __uint_as_float(l & 0xffff0000u);
+          dot = fmaf(x, __uint_as_float(w << 16), dot);
+          dot = fmaf(y, __uint_as_float(w & 0xffff0000u), dot);
+          const __nv_bfloat162 r = __floats2bfloat162_rn(beta * x, beta * y);
+          o = *reinterpret_cast<const uint32_t*>(&r);
+        };
+        pair(hi.x, lo.x, v.x, out[0]);
+        pair(hi.y, lo.y, v.y, out[1]);
+        pair(hi.z, lo.z, v.z, out[2]);
+        pair(hi.w, lo.w, v.w, out[3]);
+        if (i < n && col < p.V)
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dv) + ((b * p.T + t0 + i) * p.H + h) * p.V + col) =
+              make_uint4(out[0], out[1], out[2], out[3]);
+      }
+      dot += __shfl_xor_sync(0xffffffffu, dot, 1);
+      dot += __shfl_xor_sync(0xffffffffu, dot, 2);
+      if (part == 0) sm.dot[i] = dot;
+    }
+    ok = wait_bar(&sm.done, phase++ & 1, abort, p.hdr, 71);
+    tc_fence_after();
+    float x[32];
+    if (ok) {   // -D X
+      tmem_ld32(mine + kX + half * 32, x);
+      tmem_ld_wait();
+      reg_tie(x);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) x[j] *= -sm.c.from[half * 32 + j];
+      store_half(mine + kX + half * 32, x);
+      tmem_st_wait();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (*abort) break;
+    if (warp == 0) {
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        const uint32_t a = tmem + kX + half_col(ks);
+        mma_ts_we(tmem + kU, a, t_lo + ks * 2, kDHi, kk, 1);
+        mma_ts_we(tmem + kU, a, t_lo + kLo + ks * 2, kDHi, kk, 1);
+        mma_ts_we(tmem + kU, a + 16, t_lo + ks * 2, kDHi, kk, 1);
+      }
+      mma_commit_elect(&sm.done);
+    }
+    ok = wait_bar(&sm.done, phase++ & 1, abort, p.hdr, 72);
+    tc_fence_after();
+    if (ok) {   // U's rows, by steps
+      tmem_ld32(mine + kU + half * 32, x);
+      tmem_ld_wait();
+      reg_tie(x);
+      uint8_t* at = sm.u + (row >> 6) * kTileBytes;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const __nv_bfloat16 hi = __float2bfloat16_rn(x[j]);
+        const uint32_t off = sw128_off16(half * 32 + j, row & 63);
+        *reinterpret_cast<__nv_bfloat16*>(at + off) = hi;
+        *reinterpret_cast<__nv_bfloat16*>(at + 2 * kTileBytes + off) = __float2bfloat16_rn(x[j] - __bfloat162float(hi));
+      }
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (*abort) break;
+    if (warp == 0) {
+      // [dY; dR hi] U^T, and (rows 64..127) dR lo U^T
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        const uint32_t a = dyr_lo + by64(ks, 3 * kTileBytes), at = u_lo + by64(ks, kTileBytes);
+        mma_ss_we(tmem + kX, a, kDHi, at, kDHi, kk, ks > 0);
+        mma_ss_we(tmem + kX, a, kDHi, at + 2 * kLo, kDHi, kk, 1);
+        mma_ss_we(tmem + kU, a + kLo, kDHi, at, kDHi, kk, ks > 0);
+      }
+      mma_commit_elect(&sm.done);
+    }
+    // G takes the state's place
+    ok = wait_bar(&sm.shadow, shadows++ & 1, abort, p.hdr, 73);
+    float inner = 0.f;
+    if (ok) inner = stage_state<true>(sm, p.dstates + cell * KV, p.V, p.K) * sm.c.from[kChunk - 1];
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (*abort) break;
+    if (warp == 0) {
+      // G^T U^T
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        const uint32_t a = sm_lo + ks * kStep, at = u_lo + by64(ks, kTileBytes);
+        mma_ss_we(tmem + kGU, a, kDHi, at, kDHi, mk, ks > 0);
+        mma_ss_we(tmem + kGU, a, kDHi, at + 2 * kLo, kDHi, mk, 1);
+        mma_ss_we(tmem + kGU, a + kStateLo, kDHi, at, kDHi, mk, 1);
+      }
+    }
+    ok = wait_bar(&sm.done, phase++ & 1, abort, p.hdr, 74);
+    tc_fence_after();
+    if (ok) {
+      // lanes 0..63: Bm's rows; 64..127: N's
+      const int i = row & 63;
+      const bool lower = quarter >= 2;
+      float y[32];
+      tmem_ld32(mine + kX + half * 32, x);
+      tmem_ld32(mine + kU + half * 32, y);
+      tmem_ld_wait();
+      reg_tie(x);
+      reg_tie(y);
+      const float ch = sm.c.hi[i], cl = sm.c.lo[i], beta = sm.c.beta[i], by = lower ? -1.f : p.scale;
+      const int last = lower ? i - 1 : i;
+      uint8_t* to = lower ? sm.t : sm.v;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const int c = half * 32 + j;
+        const float f = lower ? x[j] + y[j] : x[j];
+        x[j] = c <= last ? f * by * __expf((ch - sm.c.hi[c]) + (cl - sm.c.lo[c])) : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 32; j += 8) {
+        const uint32_t off = sw128_off16(i, half * 32 + j);
+        uint4 hi, lo;
+        split2(x[j], x[j + 1], hi.x, lo.x);
+        split2(x[j + 2], x[j + 3], hi.y, lo.y);
+        split2(x[j + 4], x[j + 5], hi.z, lo.z);
+        split2(x[j + 6], x[j + 7], hi.w, lo.w);
+        *reinterpret_cast<uint4*>(to + off) = hi;
+        *reinterpret_cast<uint4*>(to + kTileBytes + off) = lo;
+        if (lower) {
+          split2(beta * x[j], beta * x[j + 1], hi.x, lo.x);
+          split2(beta * x[j + 2], beta * x[j + 3], hi.y, lo.y);
+          split2(beta * x[j + 4], beta * x[j + 5], hi.z, lo.z);
+          split2(beta * x[j + 6], beta * x[j + 7], hi.w, lo.w);
+          *reinterpret_cast<uint4*>(sm.n2 + off) = hi;
+          *reinterpret_cast<uint4*>(sm.n2 + kTileBytes + off) = lo;
+        }
+      }
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (*abort) break;
+    if (warp == 0) {
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        const uint32_t k = km_lo + ks * kStep, q = qm_lo + ks * kStep;
+        mma_ss_we(tmem + kKB, k, kDHi, bm_lo + ks * 2, kDHi, mk, ks > 0);
+        mma_ss_we(tmem + kKB, k, kDHi, bm_lo + kLo + ks * 2, kDHi, mk, 1);
+        mma_ss_we(tmem + kQB, q, kDHi, bm_lo + ks * kStep, kDHi, mm, ks > 0);
+        mma_ss_we(tmem + kQB, q, kDHi, bm_lo + kLo + ks * kStep, kDHi, mm, 1);
+        mma_ss_we(tmem + kQB, k, kDHi, n2_lo + ks * kStep, kDHi, mm, 1);
+        mma_ss_we(tmem + kQB, k, kDHi, n2_lo + kLo + ks * kStep, kDHi, mm, 1);
+        mma_ss_we(tmem + kKN, k, kDHi, n1_lo + ks * 2, kDHi, mk, ks > 0);
+        mma_ss_we(tmem + kKN, k, kDHi, n1_lo + kLo + ks * 2, kDHi, mk, 1);
+      }
+      mma_commit_elect(&sm.done);
+    }
+    ok = wait_bar(&sm.done, phase++ & 1, abort, p.hdr, 75);
+    tc_fence_after();
+    // this thread's key, 32 steps: dq, dk, and over the keys q . dq, k . (D S^T dR - K^T N'^T), and E k . G^T u
+    float* sums = reinterpret_cast<float*>(sm.u);   // [4 quarters][2][64]; U has been read
+    if (ok) {
+      const uint8_t* kt = sm.k + (row >> 6) * kTileBytes;
+      const uint8_t* qt = sm.q + (row >> 6) * kTileBytes;
+#pragma unroll
+      for (int j0 = 0; j0 < 32; j0 += 16) {
+        const uint32_t c0 = half * 32 + j0;
+        float sy[16], sr[16], gu[16], kb[16], qb[16], kn[16];
+        tmem_ld16(mine + kSY + c0, sy);
+        tmem_ld16(mine + kSR + c0, sr);
+        tmem_ld16(mine + kGU + c0, gu);
+        tmem_ld16(mine + kKB + c0, kb);
+        tmem_ld16(mine + kQB + c0, qb);
+        tmem_ld16(mine + kKN + c0, kn);
+        tmem_ld_wait();
+        reg_tie(sy);
+        reg_tie(sr);
+        reg_tie(gu);
+        reg_tie(kb);
+        reg_tie(qb);
+        reg_tie(kn);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int i = c0 + j;
+          const float from = sm.c.from[i], to = sm.c.to[i], beta = sm.c.beta[i];
+          const float kv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(kt + sw128_off16(i, row & 63)));
+          const float qv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(qt + sw128_off16(i, row & 63)));
+          const float q1 = fmaf(p.scale * from, sy[j], kb[j]);
+          const float read = fmaf(from, sr[j], -kn[j]), wrote = to * gu[j];
+          dq[j0 + j] += q1;
+          dk[j0 + j] += wrote - beta * read + qb[j];
+          inner = fmaf(kv, wrote, inner);
+          float a = qv * q1, z = kv * read;
+#pragma unroll
+          for (int o = 16; o; o >>= 1) {
+            a += __shfl_xor_sync(0xffffffffu, a, o);
+            z += __shfl_xor_sync(0xffffffffu, z, o);
+          }
+          if (lane == (i & 31)) {
+            sums[(quarter * 2) * kChunk + i] = a;
+            sums[(quarter * 2 + 1) * kChunk + i] = z;
+          }
+        }
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, o);
+      if (lane == 0) sums[8 * kChunk + warp] = inner;
+    }
+    __syncthreads();
+    if (*abort) break;
+    if (tid < kChunk) {
+      float a = 0.f, z = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        a += sums[w * 2 * kChunk + tid];
+        z += sums[(w * 2 + 1) * kChunk + tid];
+      }
+      const int64_t at = (b * p.T + t0 + tid) * p.H + h;
+      if (tid < n) p.dbeta[at] = sm.dot[tid] - z;
+      sums[9 * kChunk + tid] = a - sm.c.beta[tid] * sm.dot[tid];
+    }
+    __syncthreads();
+    if (tid < n && p.dg) {
+      float s = 0.f;
+      for (int w = 0; w < 8; ++w) s += sums[8 * kChunk + w];
+      for (int j = n - 1; j >= tid; --j) s += sums[9 * kChunk + j];
+      p.dg[(b * p.T + t0 + tid) * p.H + h] = s;
+    }
+  }
+  if (ok && !*abort) {   // dq, dk by steps: through S's place
+    __syncthreads();
+    uint8_t* to = sm.s[0] + (row >> 6) * kTileBytes;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const uint32_t off = sw128_off16(half * 32 + j, row & 63);
+      *reinterpret_cast<__nv_bfloat16*>(to + off) = __float2bfloat16_rn(dq[j]);
+      *reinterpret_cast<__nv_bfloat16*>(to + 2 * kTileBytes + off) = __float2bfloat16_rn(dk[j]);
+    }
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (tid == 0) {
+      for (int kb = 0; kb < (p.K > 64 ? 2 : 1); ++kb) {
+        tma_store_4d(&m.dq, sm.s[0] + kb * kTileBytes, kb * 64, (int)t0, (int)hk, (int)b);
+        tma_store_4d(&m.dk, sm.s[0] + (2 + kb) * kTileBytes, kb * 64, (int)t0, (int)hk, (int)b);
+      }
+      bulk_commit_group();
+      bulk_wait_group<0>();
+    }
+  }
+  if (*abort) {   // a load or a product may be on its way: wait for it, as long as for any other
+    if (warp == 0) {
+      mma_commit_elect(&sm.shadow);
+      const uint32_t turn = (uint32_t)shadows & 1;
+      if (!mbar_wait_bounded(&sm.shadow, turn, 2000000000ull)) sm.keep = 1;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0 && !sm.keep) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int KB>
+cudaError_t walk_as(const Params& p, const TcMaps& m, const TcBuffers& buf, cudaStream_t st) {
+  constexpr int smem = sizeof(BackSmem<KB>);
+  static_assert(smem <= 232448, "shared memory of a block");
+  const cudaError_t e = cudaFuncSetAttribute(delta_chain_back_kernel<KB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  delta_chain_back_kernel<KB><<<(unsigned)(p.batch * p.H), kChainThreads, smem, st>>>(p, m, buf);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+namespace delta {
+
+cudaError_t tc_backward_kernels(const Params& p, const TcMaps& m, const TcBuffers& buf, cudaStream_t st) {
+  cudaError_t e = p.K <= 64 ? walk_as<1>(p, m, buf, st) : walk_as<2>(p, m, buf, st);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(delta_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(GradSmem));
+  if (e != cudaSuccess) return e;
+  delta_grad_kernel<<<(unsigned)(p.batch * p.nch * p.Hk), kGradThreads, sizeof(GradSmem), st>>>(p, m, buf);
+  return cudaGetLastError();
+}
+
+}  // namespace delta
+}  // namespace ssd

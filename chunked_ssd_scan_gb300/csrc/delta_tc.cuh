@@ -15,17 +15,20 @@ using namespace tc;
 
 // A square of chunk steps as the tensor core reads it: 64 rows of 64 bf16, 128-byte swizzled, hi term then lo.
 constexpr uint32_t kTileBytes = kChunk * kChunk * 2;
-// Of every chunk and head in the workspace: T = (I + A)^-1 diag(beta) hi and lo, P hi and lo, then e^(sum of g up to a
-// step) and e^(sum behind it).
-constexpr uint32_t kSquareBytes = 4 * kTileBytes, kDecayBytes = 2 * kChunk * 4;
+// Of every chunk and head in the workspace: T = (I + A)^-1 diag(beta) hi and lo, P hi and lo, for the backward pass
+// (I + A)^-1 hi and lo; and e^(sum of g up to a step), e^(sum behind it), beta.
+constexpr uint32_t kDecayBytes = 3 * kChunk * 4;
+constexpr uint32_t square_bytes(bool backward) { return (backward ? 6 : 4) * kTileBytes; }
 
 struct TcMaps {
-  CUtensorMap q, k, v, y, dy, dv, dq, dk, states;
+  CUtensorMap q, k, v, y, dy, dq, dk, states;   // states: kept by the forward walk, or the backward's gradients
 };
 
 struct TcBuffers {
-  uint8_t* squares;   // [b*nch*H][kSquareBytes]
-  float* decays;      // [b*nch*H][2][kChunk]
+  uint8_t* squares;    // [b*nch*H][square]
+  float* decays;       // [b*nch*H][3][kChunk]
+  uint8_t* writes;     // backward: gradients of v - S k, [b*nch*H][2 blocks of 64 values][hi, lo][kTileBytes]
+  uint32_t square;
 };
 
 constexpr long long kWaitCycles = 4000000000ll;   // a wait gives up after about 2 s
@@ -79,10 +82,63 @@ __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+constexpr uint32_t kDHi = sdesc_sw128_hi(1024);
+constexpr uint32_t kLo = kTileBytes >> 4;   // from a square's hi to its lo, in a descriptor's units
+
+// Column of the k-step `ks` (16 steps of the chunk) of an operand kept in halves of 32 columns; lo is 16 further.
+__device__ __forceinline__ uint32_t half_col(int ks) { return (uint32_t)((ks >> 1) * 32 + (ks & 1) * 8); }
+
+// Two terms of 32 columns, written over the 32 columns' place: hi in the first 16, lo in the others.
+__device__ __forceinline__ void store_half(uint32_t at, const float (&v)[32]) {
+  uint32_t hi[16], lo[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) split2(v[2 * j], v[2 * j + 1], hi[j], lo[j]);
+  tmem_st16u(at, hi);
+  tmem_st16u(at + 16, lo);
+}
+
+// The terms of 32 NK keys of a state's row (a thread's), hi at `at` and lo `lo` columns further.
+template <int N>
+__device__ __forceinline__ void store_state_terms(uint32_t at, uint32_t lo_at, const float (&S)[N]) {
+#pragma unroll
+  for (int k = 0; k < N; k += 32) {
+    uint32_t hi[16], lo[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) split2(S[k + 2 * j], S[k + 2 * j + 1], hi[j], lo[j]);
+    tmem_st16u(at + k / 2, hi);
+    tmem_st16u(at + lo_at + k / 2, lo);
+  }
+}
+
+// 32 of a thread's keys (from `first` of its half) of the state before a chunk, through shared memory: rows of 128 bytes,
+// swizzled, leave as one tile of `map`.  By the four warps of a half.  (Straight from the registers, 32 bytes of 32
+// rows an instruction, the forward walk took 4.7 us a chunk instead of 3.6.)
+template <int KH>
+__device__ __forceinline__ void send_state(uint8_t* to, const CUtensorMap* map, const float (&S)[KH], int half, int first,
+                                           int v0, int cell, int64_t K) {
+  const int t = threadIdx.x & 127;
+  if (t == 0) bulk_wait_group_read<0>();   // the tile before has left
+  named_barrier(2 + half, 128);
+#pragma unroll
+  for (int k = 0; k < 32; k += 4)
+    *reinterpret_cast<float4*>(to + sw128_off32(t, k)) = make_float4(S[first + k], S[first + k + 1], S[first + k + 2], S[first + k + 3]);
+  fence_proxy_async_smem();
+  named_barrier(2 + half, 128);
+  if (t == 0 && half * KH + first < K) {
+    tma_store_4d(map, to, half * KH + first, v0, cell, 0);
+    bulk_commit_group();
+  }
+}
+
 // Whether the tensor-core kernels take a call, its workspace, and the call itself (delta_rule_tc.cu).
 bool tc_takes(const Params& p, bool backward);
-size_t tc_forward_bytes(int64_t batch, int64_t nch, int64_t H);
+size_t tc_bytes(int64_t batch, int64_t nch, int64_t H, bool backward);
 cudaError_t tc_forward(const Params& p, void* buffers, cudaStream_t st);
+cudaError_t tc_backward(const Params& p, bool states_known, void* buffers, cudaStream_t st);   // fills states_in where not
+// The backward walk and the chunks' gradients (delta_rule_tc_back.cu).
+cudaError_t tc_backward_kernels(const Params& p, const TcMaps& m, const TcBuffers& buf, cudaStream_t st);
+bool head_map(CUtensorMap* m, const void* base, int64_t batch, int64_t T, int64_t heads, int64_t cols, const int64_t* stride);
+bool state_map(CUtensorMap* m, const void* base, int64_t cells, int64_t V, int64_t K);
 
 }  // namespace delta
 }  // namespace ssd
