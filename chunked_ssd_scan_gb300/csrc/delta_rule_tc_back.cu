@@ -9,8 +9,10 @@
 //   dK^T = G^T U^T diag(E) - S^T dR^T diag(D beta) + Q^T Bm + (K^T N'^T) diag(beta) + K^T diag(beta) N',
 //                                                           N' = -M o (dR U^T) below the diagonal
 //   dbeta_i = dR_i . v_i - k_i . (D_i S^T dR_i - (K^T N'^T)_i)
-//   dg_i = sum_{j >= i} (q_j . dq_j - beta_j dR_j . v_j) + D_last <G, S> + sum_j E_j k_j . G^T u_j
-// (dq_j of one head; the sum over a chunk's steps, not over the sequence, whose terms would cancel).
+//   dg_i = D_last <G, S> + sum_{a >= i} (scale D_a q_a . S^T dy_a - beta_a D_a k_a . S^T dR_a) + sum_{b < i} E_b k_b . G^T u_b
+//          + sum_{a >= i > b} (Bm_ab q_a . k_b + beta_a N'_ab k_a . k_b)
+// that is, every product that the decay of step i is a factor of.  (The shorter sum of q . dq - dv . v over the steps
+// behind i has the same value, but its terms cancel: with operands in two terms dg was off by 1e-5 to 3e-5.)
 #include <string.h>
 
 #include <algorithm>
@@ -350,7 +352,7 @@ constexpr int kGradThreads = 256;
 enum : uint32_t { kX = 0, kU = 64, kSY = 128, kSR = 192, kGU = 256, kKB = 320, kQB = 384, kKN = 448 };
 
 struct GradSmem {
-  uint8_t k[2 * kTileBytes], q[2 * kTileBytes];
+  uint8_t qk[2][2 * kTileBytes];      // by 64 keys: Q, K
   uint8_t dyr[2][3 * kTileBytes];     // by 64 values: dY, dR hi, dR lo
   uint8_t u[4 * kTileBytes];          // hi by 64 values, lo
   uint8_t s[4][2 * kTileBytes];       // S, then G: hi by 64 keys, lo; 128 rows of values
@@ -430,8 +432,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   volatile int* abort = &sm.abort;
   constexpr uint32_t kk = idesc_bf16(128, 64, 0, 0), mk = idesc_bf16(128, 64, 1, 0), mm = idesc_bf16(128, 64, 1, 1);
   constexpr uint32_t kStep = 2048 >> 4, kStateLo = (4 * kTileBytes) >> 4;
-  const uint32_t k_lo = sdesc_sw128_lo(smem_u32(sm.k), 0), km_lo = sdesc_sw128_lo(smem_u32(sm.k), kTileBytes);
-  const uint32_t qm_lo = sdesc_sw128_lo(smem_u32(sm.q), kTileBytes);
+  const uint32_t qk_lo = sdesc_sw128_lo(smem_u32(sm.qk[0]), 0), k_lo = qk_lo + kLo;
+  const uint32_t qm_lo = sdesc_sw128_lo(smem_u32(sm.qk[0]), 2 * kTileBytes), km_lo = qm_lo + kLo;
   const uint32_t s_lo = sdesc_sw128_lo(smem_u32(sm.s[0]), 0), sm_lo = sdesc_sw128_lo(smem_u32(sm.s[0]), 2 * kTileBytes);
   const uint32_t dyr_lo = sdesc_sw128_lo(smem_u32(sm.dyr[0]), 0), u_lo = sdesc_sw128_lo(smem_u32(sm.u), 0);
   const uint32_t v_lo = sdesc_sw128_lo(smem_u32(sm.v), kTileBytes), t_lo = sdesc_sw128_lo(smem_u32(sm.t), 0);
@@ -451,8 +453,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       if (first) {
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {   // keys past K are zeros
-          tma_load_4d_elect(sm.k + kb * kTileBytes, &m.k, &sm.loaded, kb * 64, (int)t0, (int)hk, (int)b);
-          tma_load_4d_elect(sm.q + kb * kTileBytes, &m.q, &sm.loaded, kb * 64, (int)t0, (int)hk, (int)b);
+          tma_load_4d_elect(sm.qk[kb], &m.q, &sm.loaded, kb * 64, (int)t0, (int)hk, (int)b);
+          tma_load_4d_elect(sm.qk[kb] + kTileBytes, &m.k, &sm.loaded, kb * 64, (int)t0, (int)hk, (int)b);
         }
       }
 #pragma unroll
@@ -476,8 +478,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       // X = S K^T and V T^T
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {
-        mma_ss_we(tmem + kX, s_lo + by64(ks, 2 * kTileBytes), kDHi, k_lo + by64(ks, kTileBytes), kDHi, kk, ks > 0);
-        mma_ss_we(tmem + kX, s_lo + kStateLo + by64(ks, 2 * kTileBytes), kDHi, k_lo + by64(ks, kTileBytes), kDHi, kk, 1);
+        mma_ss_we(tmem + kX, s_lo + by64(ks, 2 * kTileBytes), kDHi, k_lo + by64(ks, 2 * kTileBytes), kDHi, kk, ks > 0);
+        mma_ss_we(tmem + kX, s_lo + kStateLo + by64(ks, 2 * kTileBytes), kDHi, k_lo + by64(ks, 2 * kTileBytes), kDHi, kk, 1);
       }
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
@@ -495,6 +497,10 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         mma_ss_we(tmem + kSR, a, kDHi, at + 2 * kLo, kDHi, mk, 1);
         mma_ss_we(tmem + kSR, a + kStateLo, kDHi, at + kLo, kDHi, mk, 1);
       }
+      // [Q; K] K^T, where K^T N'^T will be
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks)
+        mma_ss_we(tmem + kKN, qk_lo + by64(ks, 2 * kTileBytes), kDHi, k_lo + by64(ks, 2 * kTileBytes), kDHi, kk, ks > 0);
       mma_commit_elect(&sm.shadow);
     }
     // dv = beta dR, and dR . v: four threads a step, 16 bytes at a time
@@ -606,6 +612,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
     ok = wait_bar(&sm.done, phase++ & 1, abort, p.hdr, 74);
     tc_fence_after();
+    float across = 0.f, row_sum = 0.f;   // sum over the pairs of steps around the lane's; of this row
     if (ok) {
       // lanes 0..63: Bm's rows; 64..127: N's
       const int i = row & 63;
@@ -644,6 +651,18 @@ __global__ void __launch_bounds__(kGradThreads, 1)
           *reinterpret_cast<uint4*>(sm.n2 + kTileBytes + off) = lo;
         }
       }
+      // products of pairs a > b, summed along this row (a) over the columns before each, then over the rows from it on
+      tmem_ld32(mine + kKN + half * 32, y);
+      tmem_ld_wait();
+      reg_tie(y);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        float s = i >= half * 32 + j ? row_sum : 0.f;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == j) across = s;
+        row_sum = fmaf(x[j], lower ? beta * y[j] : y[j], row_sum);
+      }
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -667,11 +686,10 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
     ok = wait_bar(&sm.done, phase++ & 1, abort, p.hdr, 75);
     tc_fence_after();
-    // this thread's key, 32 steps: dq, dk, and over the keys q . dq, k . (D S^T dR - K^T N'^T), and E k . G^T u
-    float* sums = reinterpret_cast<float*>(sm.u);   // [4 quarters][2][64]; U has been read
+    // this thread's key, 32 steps: dq, dk, and three sums over the keys, by quarters of the lanes
+    float* sums = reinterpret_cast<float*>(sm.u);   // [3][4][64], then by warps across and inner, by rows row_sum
     if (ok) {
-      const uint8_t* kt = sm.k + (row >> 6) * kTileBytes;
-      const uint8_t* qt = sm.q + (row >> 6) * kTileBytes;
+      const uint8_t *qt = sm.qk[row >> 6], *kt = qt + kTileBytes;
 #pragma unroll
       for (int j0 = 0; j0 < 32; j0 += 16) {
         const uint32_t c0 = half * 32 + j0;
@@ -695,46 +713,50 @@ __global__ void __launch_bounds__(kGradThreads, 1)
           const float from = sm.c.from[i], to = sm.c.to[i], beta = sm.c.beta[i];
           const float kv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(kt + sw128_off16(i, row & 63)));
           const float qv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(qt + sw128_off16(i, row & 63)));
-          const float q1 = fmaf(p.scale * from, sy[j], kb[j]);
-          const float read = fmaf(from, sr[j], -kn[j]), wrote = to * gu[j];
-          dq[j0 + j] += q1;
-          dk[j0 + j] += wrote - beta * read + qb[j];
-          inner = fmaf(kv, wrote, inner);
-          float a = qv * q1, z = kv * read;
+          const float q1 = p.scale * from * sy[j], r1 = from * sr[j], wrote = to * gu[j];
+          dq[j0 + j] += q1 + kb[j];
+          dk[j0 + j] += wrote - beta * (r1 - kn[j]) + qb[j];
+          float s0 = kv * (r1 - kn[j]), s1 = fmaf(qv, q1, -beta * kv * r1), s2 = kv * wrote;
 #pragma unroll
           for (int o = 16; o; o >>= 1) {
-            a += __shfl_xor_sync(0xffffffffu, a, o);
-            z += __shfl_xor_sync(0xffffffffu, z, o);
+            s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+            s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+            s2 += __shfl_xor_sync(0xffffffffu, s2, o);
           }
           if (lane == (i & 31)) {
-            sums[(quarter * 2) * kChunk + i] = a;
-            sums[(quarter * 2 + 1) * kChunk + i] = z;
+            sums[quarter * kChunk + i] = s0;
+            sums[(4 + quarter) * kChunk + i] = s1;
+            sums[(8 + quarter) * kChunk + i] = s2;
           }
         }
       }
+      sums[12 * kChunk + quarter * kChunk + half * 32 + lane] = across;
+      if (half == 0) sums[16 * kChunk + row] = row_sum;
 #pragma unroll
       for (int o = 16; o; o >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, o);
-      if (lane == 0) sums[8 * kChunk + warp] = inner;
+      if (lane == 0) sums[18 * kChunk + warp] = inner;
     }
     __syncthreads();
     if (*abort) break;
-    if (tid < kChunk) {
-      float a = 0.f, z = 0.f;
+    if (tid < n) {
+      float z = 0.f, g = 0.f;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        a += sums[w * 2 * kChunk + tid];
-        z += sums[(w * 2 + 1) * kChunk + tid];
+        z += sums[w * kChunk + tid];
+        g += sums[(12 + w) * kChunk + tid];
       }
       const int64_t at = (b * p.T + t0 + tid) * p.H + h;
-      if (tid < n) p.dbeta[at] = sm.dot[tid] - z;
-      sums[9 * kChunk + tid] = a - sm.c.beta[tid] * sm.dot[tid];
-    }
-    __syncthreads();
-    if (tid < n && p.dg) {
-      float s = 0.f;
-      for (int w = 0; w < 8; ++w) s += sums[8 * kChunk + w];
-      for (int j = n - 1; j >= tid; --j) s += sums[9 * kChunk + j];
-      p.dg[(b * p.T + t0 + tid) * p.H + h] = s;
+      p.dbeta[at] = sm.dot[tid] - z;
+      if (p.dg) {
+        for (int w = 0; w < 8; ++w) g += sums[18 * kChunk + w];
+        for (int a = tid; a < n; ++a) {
+          for (int w = 4; w < 8; ++w) g += sums[w * kChunk + a];
+          if (tid >= 32) g += sums[16 * kChunk + a] + sums[17 * kChunk + a];   // pairs whose earlier step is among the first 32
+        }
+        for (int a = 0; a < tid; ++a)
+          for (int w = 8; w < 12; ++w) g += sums[w * kChunk + a];
+        p.dg[at] = g;
+      }
     }
   }
   if (ok && !*abort) {   // dq, dk by steps: through S's place

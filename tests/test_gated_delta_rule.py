@@ -216,7 +216,11 @@ def test_keys_all_alike(dtype):
     want = ref.delta(h["q"], h["k"], h["v"], h["g"], h["beta"], h["init"])
     for got, w, what in zip(r, want, ("y", "final_state", "states")):
         ref.check(to_np(got), w, dtype, what, rounded=what == "y", scale=size * np.maximum(1.0, np.abs(w)))
-    check_backward(run_backward(d, dtype, None), d, dtype)
+    # the walk backwards is of the same form, with dR for the writes
+    got = run_backward(d, dtype, None)
+    want = ref.delta_grad(h["q"], h["k"], h["v"], h["g"], h["beta"], h["dy"], h["init"], None, h["dfinal"])
+    for k, w in want.items():
+        ref.check(to_np(got[k]), w, dtype, k, rounded=k in ("dq", "dk", "dv"), scale=size * np.maximum(1.0, np.abs(w)))
 
 
 @pytest.mark.gpu
