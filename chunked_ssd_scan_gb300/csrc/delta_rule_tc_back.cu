@@ -371,14 +371,20 @@ static_assert(sizeof(GradSmem) <= 232448, "shared memory of a block");
 template <bool kInner>
 __device__ __forceinline__ float stage_state(GradSmem& sm, const float* S, int64_t V, int64_t K) {
   float inner = 0.f;
-#pragma unroll 2
+  float4 f[16];   // all loads at once: in eight rounds of two this took a third of the kernel's time
+#pragma unroll
   for (int it = 0; it < 8; ++it) {
     const int at = it * kGradThreads + threadIdx.x, row = at >> 4, col = (at & 15) * 8;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    f[2 * it] = f[2 * it + 1] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (S && row < V && col < K) {
-      a = *reinterpret_cast<const float4*>(S + row * K + col);
-      b = *reinterpret_cast<const float4*>(S + row * K + col + 4);
+      f[2 * it] = __ldcs(reinterpret_cast<const float4*>(S + row * K + col));
+      f[2 * it + 1] = __ldcs(reinterpret_cast<const float4*>(S + row * K + col + 4));
     }
+  }
+#pragma unroll
+  for (int it = 0; it < 8; ++it) {
+    const int at = it * kGradThreads + threadIdx.x, row = at >> 4, col = (at & 15) * 8;
+    const float4 a = f[2 * it], b = f[2 * it + 1];
     uint8_t* hi_at = sm.s[col >> 6] + sw128_off16(row, col & 63);
     uint8_t* lo_at = hi_at + 4 * kTileBytes;
     if constexpr (kInner) {
@@ -401,6 +407,34 @@ __device__ __forceinline__ float stage_state(GradSmem& sm, const float* S, int64
     *reinterpret_cast<uint4*>(lo_at) = lo;
   }
   return inner;
+}
+
+// Sums of N columns over a warp's lanes: lane l has that of column l % N.  Halving: N - 1 exchanges where sums column by
+// column take 5 N.
+template <int N>
+__device__ __forceinline__ float sum_columns(float (&v)[N]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = N / 2; o; o >>= 1) {
+    const bool upper = lane & o;
+#pragma unroll
+    for (int j = 0; j < o; ++j) {
+      const float keep = upper ? v[j + o] : v[j], give = upper ? v[j] : v[j + o];
+      v[j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
+#pragma unroll
+  for (int o = N; o < 32; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  return v[0];
+}
+
+__device__ __forceinline__ float scan_up(float v, int lane) {   // sum over the lanes up to this one
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
 }
 
 __global__ void __launch_bounds__(kGradThreads, 1)
@@ -657,12 +691,11 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       reg_tie(y);
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
-        float s = i >= half * 32 + j ? row_sum : 0.f;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == j) across = s;
-        row_sum = fmaf(x[j], lower ? beta * y[j] : y[j], row_sum);
+        const float w = lower ? beta * y[j] : y[j];
+        y[j] = i >= half * 32 + j ? row_sum : 0.f;
+        row_sum = fmaf(x[j], w, row_sum);
       }
+      across = sum_columns(y);
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -716,18 +749,15 @@ __global__ void __launch_bounds__(kGradThreads, 1)
           const float q1 = p.scale * from * sy[j], r1 = from * sr[j], wrote = to * gu[j];
           dq[j0 + j] += q1 + kb[j];
           dk[j0 + j] += wrote - beta * (r1 - kn[j]) + qb[j];
-          float s0 = kv * (r1 - kn[j]), s1 = fmaf(qv, q1, -beta * kv * r1), s2 = kv * wrote;
-#pragma unroll
-          for (int o = 16; o; o >>= 1) {
-            s0 += __shfl_xor_sync(0xffffffffu, s0, o);
-            s1 += __shfl_xor_sync(0xffffffffu, s1, o);
-            s2 += __shfl_xor_sync(0xffffffffu, s2, o);
-          }
-          if (lane == (i & 31)) {
-            sums[quarter * kChunk + i] = s0;
-            sums[(4 + quarter) * kChunk + i] = s1;
-            sums[(8 + quarter) * kChunk + i] = s2;
-          }
+          sy[j] = kv * (r1 - kn[j]);
+          sr[j] = fmaf(qv, q1, -beta * kv * r1);
+          gu[j] = kv * wrote;
+        }
+        const float s0 = sum_columns(sy), s1 = sum_columns(sr), s2 = sum_columns(gu);
+        if (lane < 16) {
+          sums[quarter * kChunk + c0 + lane] = s0;
+          sums[(4 + quarter) * kChunk + c0 + lane] = s1;
+          sums[(8 + quarter) * kChunk + c0 + lane] = s2;
         }
       }
       sums[12 * kChunk + quarter * kChunk + half * 32 + lane] = across;
@@ -738,24 +768,38 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
     __syncthreads();
     if (*abort) break;
-    if (tid < n) {
-      float z = 0.f, g = 0.f;
+    if (warp == 0) {   // a lane has steps 2 l and 2 l + 1
+      float z[2], rho[2], sigma[2], pairs[2], g[2];
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        z += sums[w * kChunk + tid];
-        g += sums[(12 + w) * kChunk + tid];
-      }
-      const int64_t at = (b * p.T + t0 + tid) * p.H + h;
-      p.dbeta[at] = sm.dot[tid] - z;
-      if (p.dg) {
-        for (int w = 0; w < 8; ++w) g += sums[18 * kChunk + w];
-        for (int a = tid; a < n; ++a) {
-          for (int w = 4; w < 8; ++w) g += sums[w * kChunk + a];
-          if (tid >= 32) g += sums[16 * kChunk + a] + sums[17 * kChunk + a];   // pairs whose earlier step is among the first 32
+      for (int e = 0; e < 2; ++e) {
+        const int i = 2 * lane + e;
+        z[e] = rho[e] = sigma[e] = g[e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          z[e] += sums[w * kChunk + i];
+          rho[e] += sums[(4 + w) * kChunk + i];
+          sigma[e] += sums[(8 + w) * kChunk + i];
+          g[e] += sums[(12 + w) * kChunk + i];
         }
-        for (int a = 0; a < tid; ++a)
-          for (int w = 8; w < 12; ++w) g += sums[w * kChunk + a];
-        p.dg[at] = g;
+        pairs[e] = sums[16 * kChunk + i] + sums[17 * kChunk + i];   // of row i, with the first 32 steps
+      }
+      float all = lane < 8 ? sums[18 * kChunk + lane] : 0.f;
+      all = __shfl_sync(0xffffffffu, scan_up(all, lane), 31);
+      // from a step to the chunk's end; the sums before it
+      const float r1 = scan_up(rho[0] + rho[1], lane), rt = __shfl_sync(0xffffffffu, r1, 31);
+      const float p1 = scan_up(pairs[0] + pairs[1], lane), pt = __shfl_sync(0xffffffffu, p1, 31);
+      const float s1 = scan_up(sigma[0] + sigma[1], lane);
+      const float after = rt - r1, p_after = pt - p1, before = s1 - sigma[0] - sigma[1];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int i = 2 * lane + e;
+        g[e] += all + after + rho[1] + (e ? 0.f : rho[0]) + before + (e ? sigma[0] : 0.f);
+        if (i >= 32) g[e] += p_after + pairs[1] + (e ? 0.f : pairs[0]);
+        if (i < n) {
+          const int64_t at = (b * p.T + t0 + i) * p.H + h;
+          p.dbeta[at] = sm.dot[i] - z[e];
+          if (p.dg) p.dg[at] = g[e];
+        }
       }
     }
   }
