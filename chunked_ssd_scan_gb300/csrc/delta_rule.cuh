@@ -32,8 +32,7 @@ __device__ __forceinline__ float decay_log(const Params& p, int64_t b, int64_t t
   return g < kNoDecay ? kNoDecay : g;
 }
 
-// Sums of g within a chunk as pairs of floats (double in parts), and what they make of it: thread i < 64 of
-// the first two warps holds step i's g.  `last` is the chunk's last step.
+// Sums of g within a chunk as pairs of floats, and what they make of it.
 struct ChunkDecay {
   float hi[kChunk], lo[kChunk];   // sum of g over the chunk's steps up to i
   float beta[kChunk];
@@ -44,28 +43,37 @@ __device__ __forceinline__ float decay_between(const ChunkDecay& c, int i, int j
   return expf((c.hi[i] - c.hi[j]) + (c.lo[i] - c.lo[j]));
 }
 
+// (hi, lo) += (h, l): the exact sum of the first parts, and what its rounding left with the second ones.
+__device__ __forceinline__ void add_pair(float& hi, float& lo, float h, float l) {
+  const float s = hi + h, back = s - hi, rest = (hi - (s - back)) + (h - back) + (lo + l);
+  hi = s + rest;
+  lo = rest - (hi - s);
+}
+
 // By one whole warp; lane l holds the steps 2l and 2l + 1.
 __device__ __forceinline__ void chunk_decay_warp(const Params& p, ChunkDecay& c, int64_t b, int64_t t0, int n,
                                                  int64_t h, int lane) {
   const int i0 = 2 * lane, i1 = i0 + 1;
-  const double g0 = i0 < n ? (double)decay_log(p, b, t0 + i0, h) : 0.0;
-  const double g1 = i1 < n ? (double)decay_log(p, b, t0 + i1, h) : 0.0;
-  double sum = g0 + g1;
+  const float g0 = i0 < n ? decay_log(p, b, t0 + i0, h) : 0.f, g1 = i1 < n ? decay_log(p, b, t0 + i1, h) : 0.f;
+  // sums as pairs of floats (in fp64 this scan alone took 5000 cycles)
+  float hi = g0, lo = 0.f;
+  add_pair(hi, lo, g1, 0.f);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const double up = __shfl_up_sync(0xffffffffu, sum, o);
-    if (lane >= o) sum += up;
+    const float uh = __shfl_up_sync(0xffffffffu, hi, o), ul = __shfl_up_sync(0xffffffffu, lo, o);
+    if (lane >= o) add_pair(hi, lo, uh, ul);
   }
-  const double total = __shfl_sync(0xffffffffu, sum, 31);
-  const double c0 = sum - g1, c1 = sum;
-  c.hi[i0] = (float)c0;
-  c.lo[i0] = (float)(c0 - (double)(float)c0);
-  c.hi[i1] = (float)c1;
-  c.lo[i1] = (float)(c1 - (double)(float)c1);
-  c.from[i0] = expf((float)c0);
-  c.from[i1] = expf((float)c1);
-  c.to[i0] = expf((float)(total - c0));
-  c.to[i1] = expf((float)(total - c1));
+  const float th = __shfl_sync(0xffffffffu, hi, 31), tl = __shfl_sync(0xffffffffu, lo, 31);
+  float h0 = hi, l0 = lo;
+  add_pair(h0, l0, -g1, 0.f);
+  c.hi[i0] = h0;
+  c.lo[i0] = l0;
+  c.hi[i1] = hi;
+  c.lo[i1] = lo;
+  c.from[i0] = expf(h0);
+  c.from[i1] = expf(hi);
+  c.to[i0] = expf((th - h0) + (tl - l0));
+  c.to[i1] = expf((th - hi) + (tl - lo));
   const float* bp = p.beta + b * p.bs[0] + h;
   c.beta[i0] = i0 < n ? __ldg(bp + (t0 + i0) * p.bs[1]) : 0.f;
   c.beta[i1] = i1 < n ? __ldg(bp + (t0 + i1) * p.bs[1]) : 0.f;

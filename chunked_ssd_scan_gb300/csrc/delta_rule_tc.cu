@@ -30,7 +30,7 @@ using namespace delta;
 // Q K^T; both are of the key head, the heads that share it take turns with their own decays and betas.
 // ---------------------------------------------------------------------------------------------------------------------
 constexpr int kPrepThreads = 128;
-constexpr int kPitch = 68;
+constexpr int kPitch = 72;   // rows of 16-by-8 fragments on different banks
 
 template <int KB>
 struct PrepSmem {
@@ -46,13 +46,44 @@ struct PrepSmem {
   int abort, keep;
 };
 
-// (I + A)^-1 below and on the diagonal of `x`, for A strictly below the diagonal of `a`: the 16 x 16 blocks on the
-// diagonal by forward substitution, a column a lane, then pairs of them by X21 = -X22 (A21 X11), whose inner product
-// waits above the diagonal of `a`.  All threads; fp32 throughout.  (Every column by forward substitution, 64 rows one
-// after the other in 43 KB of straight code: 298 us instead of PREPUS for 8 x 4096 x 16 heads.)
-__device__ __forceinline__ void invert(float (&a)[kChunk][kPitch], float (&x)[kChunk][kPitch]) {
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int d0 = (tid >> 5) * 16;
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+using Square = float[kChunk][kPitch];
+
+// 16 x 8 of the product of a's rows from r, columns from k, with b's rows from m, columns from n, over 16 of them; a warp,
+// in two bf16 terms.  These blocks are too small for a tcgen05 tile of 128 rows.
+__device__ __forceinline__ void block_product(float (&acc)[4], const Square& a, int r, int k, const Square& b, int m, int n) {
+  const int g = (threadIdx.x & 31) >> 2, t = (threadIdx.x & 3) * 2;
+  uint32_t ah[4], al[4], bh[2], bl[2];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 v = *reinterpret_cast<const float2*>(&a[r + g + (e & 1) * 8][k + t + (e >> 1) * 8]);
+    split2(v.x, v.y, ah[e], al[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < 2; ++e) split2(b[m + t + e * 8][n + g], b[m + t + 1 + e * 8][n + g], bh[e], bl[e]);
+  mma16(acc, ah, bh);
+  mma16(acc, ah, bl);
+  mma16(acc, al, bh);
+}
+__device__ __forceinline__ void store_block(Square& to, int r, int n, const float (&v)[4], float sign) {
+  const int g = (threadIdx.x & 31) >> 2, t = (threadIdx.x & 3) * 2;
+  *reinterpret_cast<float2*>(&to[r + g][n + t]) = make_float2(sign * v[0], sign * v[1]);
+  *reinterpret_cast<float2*>(&to[r + g + 8][n + t]) = make_float2(sign * v[2], sign * v[3]);
+}
+
+// (I + A)^-1 on and below the diagonal of `x`, for A strictly below the diagonal of `a`: the 16 x 16 blocks on the
+// diagonal by forward substitution in fp32, a column a lane, then pairs of blocks by X21 = -X22 (A21 X11), whose inner
+// product waits above the diagonal of `a`.  All four warps.  (Every column by forward substitution, 64 rows one after
+// the other: the whole kernel took 298 us for 8 x 4096 x 16 heads; the pairs by fp32 loops 164 us.)
+__device__ __forceinline__ void invert(Square& a, Square& x) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int d0 = warp * 16;
   if (lane < 16) {
     float v[16];
 #pragma unroll
@@ -69,64 +100,37 @@ __device__ __forceinline__ void invert(float (&a)[kChunk][kPitch], float (&x)[kC
       v[i] = s0 + s1;
       x[d0 + i][d0 + lane] = v[i];
     }
-  }
-  __syncthreads();
-  {   // two pairs of blocks of 16, four neighbours a thread
-    const int r0 = (tid >> 6) * 32, i = (tid & 63) >> 2, j = (tid & 3) * 4;
-    float y[4] = {};
-    for (int m = j; m < 16; ++m) {
-      const float f = a[r0 + 16 + i][r0 + m];
-      const float4 g = *reinterpret_cast<const float4*>(&x[r0 + m][r0 + j]);
-      y[0] = fmaf(f, g.x, y[0]);
-      y[1] = fmaf(f, g.y, y[1]);
-      y[2] = fmaf(f, g.z, y[2]);
-      y[3] = fmaf(f, g.w, y[3]);
-    }
-    *reinterpret_cast<float4*>(&a[r0 + i][r0 + 16 + j]) = make_float4(y[0], y[1], y[2], y[3]);
-    __syncthreads();
-    float z[4] = {};
-    for (int m = 0; m <= i; ++m) {
-      const float f = x[r0 + 16 + i][r0 + 16 + m];
-      const float4 g = *reinterpret_cast<const float4*>(&a[r0 + m][r0 + 16 + j]);
-      z[0] = fmaf(-f, g.x, z[0]);
-      z[1] = fmaf(-f, g.y, z[1]);
-      z[2] = fmaf(-f, g.z, z[2]);
-      z[3] = fmaf(-f, g.w, z[3]);
-    }
-    *reinterpret_cast<float4*>(&x[r0 + 16 + i][r0 + j]) = make_float4(z[0], z[1], z[2], z[3]);
-  }
-  __syncthreads();
-  {   // one pair of blocks of 32, two rows of four neighbours a thread; rows i and 31 - i, so that threads have as much to do
-    const int i0 = tid >> 3, i1 = 31 - i0, j = (tid & 7) * 4;
-    float y[2][4] = {};
-    for (int m = j; m < 32; ++m) {
-      const float f = a[32 + i0][m], e = a[32 + i1][m];
-      const float4 g = *reinterpret_cast<const float4*>(&x[m][j]);
-      y[0][0] = fmaf(f, g.x, y[0][0]);
-      y[0][1] = fmaf(f, g.y, y[0][1]);
-      y[0][2] = fmaf(f, g.z, y[0][2]);
-      y[0][3] = fmaf(f, g.w, y[0][3]);
-      y[1][0] = fmaf(e, g.x, y[1][0]);
-      y[1][1] = fmaf(e, g.y, y[1][1]);
-      y[1][2] = fmaf(e, g.z, y[1][2]);
-      y[1][3] = fmaf(e, g.w, y[1][3]);
-    }
-    *reinterpret_cast<float4*>(&a[i0][32 + j]) = make_float4(y[0][0], y[0][1], y[0][2], y[0][3]);
-    *reinterpret_cast<float4*>(&a[i1][32 + j]) = make_float4(y[1][0], y[1][1], y[1][2], y[1][3]);
-    __syncthreads();
+  } else if ((warp & 1) == 0) {   // above the diagonal, for the products to come
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int i = r ? i1 : i0;
+    for (int i = 0; i < 16; ++i) x[d0 + i][d0 + lane] = 0.f;
+  }
+  __syncthreads();
+  {   // two pairs of blocks of 16, eight columns a warp
+    const int r = (warp >> 1) * 32, n = (warp & 1) * 8;
+    float y[4] = {}, z[4] = {};
+    block_product(y, a, r + 16, r, x, r, r + n);
+    store_block(a, r, r + 16 + n, y, 1.f);
+    __syncwarp();   // a warp's product needs its own columns alone
+    block_product(z, x, r + 16, r + 16, a, r, r + 16 + n);
+    store_block(x, r + 16, r + n, z, -1.f);
+  }
+  __syncthreads();
+  {   // one pair of blocks of 32, eight columns a warp; blocks that are zero above a diagonal are left out
+    const int n = warp * 8;
+#pragma unroll
+    for (int r = 0; r < 32; r += 16) {
+      float y[4] = {};
+      if (n < 16) block_product(y, a, 32 + r, 0, x, 0, n);
+      block_product(y, a, 32 + r, 16, x, 16, n);
+      store_block(a, r, 32 + n, y, 1.f);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < 32; r += 16) {
       float z[4] = {};
-      for (int m = 0; m <= i; ++m) {
-        const float f = x[32 + i][32 + m];
-        const float4 g = *reinterpret_cast<const float4*>(&a[m][32 + j]);
-        z[0] = fmaf(-f, g.x, z[0]);
-        z[1] = fmaf(-f, g.y, z[1]);
-        z[2] = fmaf(-f, g.z, z[2]);
-        z[3] = fmaf(-f, g.w, z[3]);
-      }
-      *reinterpret_cast<float4*>(&x[32 + i][j]) = make_float4(z[0], z[1], z[2], z[3]);
+      block_product(z, x, 32 + r, 32, a, 0, 32 + n);
+      if (r > 0) block_product(z, x, 32 + r, 48, a, 16, 32 + n);
+      store_block(x, 32 + r, n, z, -1.f);
     }
   }
   __syncthreads();
@@ -213,6 +217,10 @@ __global__ void __launch_bounds__(kPrepThreads, 6) delta_chunk_kernel(const __gr
       tmem_ld16(mine + c0, v);
       tmem_ld_wait();
       reg_tie(v);
+      if ((warp & 1) * 32 + 31 < c0) {   // above the diagonal
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = 0.f;
+      } else
 #pragma unroll
       for (int j = 0; j < 16; j += 4) {
         const float4 ch = *reinterpret_cast<const float4*>(&sm.c.hi[c0 + j]), cl = *reinterpret_cast<const float4*>(&sm.c.lo[c0 + j]);

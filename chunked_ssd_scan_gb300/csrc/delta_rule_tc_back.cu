@@ -346,17 +346,18 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 // ---------------------------------------------------------------------------------------------------------------------
 // One chunk and key head a block; the heads that share the keys one after the other.
 // ---------------------------------------------------------------------------------------------------------------------
-constexpr int kGradThreads = 256;
-// TMEM: X and -D X, then dY U^T over dR U^T; U, then the products with dR's second term; S^T dY^T; S^T dR^T; G^T U^T;
-// K^T Bm^T; Q^T Bm + K^T diag(beta) N'; K^T N'^T.
-enum : uint32_t { kX = 0, kU = 64, kSY = 128, kSR = 192, kGU = 256, kKB = 320, kQB = 384, kKN = 448 };
+constexpr int kGradThreads = 512;   // 16 columns of TMEM a warp (32 and 256 threads: 473 us instead of GRADUS, latency)
+// TMEM: X and -D X, then [dY; dR hi] with U's first term; U, then with its second; S^T dY^T; S^T dR^T; G^T U^T; K^T Bm^T;
+// [Q; K] K^T, then K^T N'^T; dR lo U^T, then Q^T Bm + K^T diag(beta) N'.  Operands that follow each other in shared
+// memory enter one product of 128 columns: with 64 the reading of the operands (6 KB for 32 cycles' work) bounds it.
+enum : uint32_t { kX = 0, kU = 64, kSY = 128, kSR = 192, kGU = 256, kKB = 320, kKN = 384, kQB = 448 };
 
 struct GradSmem {
   uint8_t qk[2][2 * kTileBytes];      // by 64 keys: Q, K
   uint8_t dyr[2][3 * kTileBytes];     // by 64 values: dY, dR hi, dR lo
-  uint8_t u[4 * kTileBytes];          // hi by 64 values, lo
+  uint8_t u[2][2 * kTileBytes];       // by 64 values: hi, lo
   uint8_t s[4][2 * kTileBytes];       // S, then G: hi by 64 keys, lo; 128 rows of values
-  uint8_t v[2 * kTileBytes], t[2 * kTileBytes];   // then Bm hi, lo; N' hi, lo
+  uint8_t v[2 * kTileBytes], t[2 * kTileBytes];   // then Bm hi, N' hi; Bm lo, N' lo
   uint8_t n2[2 * kTileBytes];         // diag(beta) N'
   ChunkDecay c;
   float dot[kChunk];                  // dR . v
@@ -371,9 +372,9 @@ static_assert(sizeof(GradSmem) <= 232448, "shared memory of a block");
 template <bool kInner>
 __device__ __forceinline__ float stage_state(GradSmem& sm, const float* S, int64_t V, int64_t K) {
   float inner = 0.f;
-  float4 f[16];   // all loads at once: in eight rounds of two this took a third of the kernel's time
+  float4 f[8];   // all loads at once
 #pragma unroll
-  for (int it = 0; it < 8; ++it) {
+  for (int it = 0; it < 4; ++it) {
     const int at = it * kGradThreads + threadIdx.x, row = at >> 4, col = (at & 15) * 8;
     f[2 * it] = f[2 * it + 1] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (S && row < V && col < K) {
@@ -382,7 +383,7 @@ __device__ __forceinline__ float stage_state(GradSmem& sm, const float* S, int64
     }
   }
 #pragma unroll
-  for (int it = 0; it < 8; ++it) {
+  for (int it = 0; it < 4; ++it) {
     const int at = it * kGradThreads + threadIdx.x, row = at >> 4, col = (at & 15) * 8;
     const float4 a = f[2 * it], b = f[2 * it + 1];
     uint8_t* hi_at = sm.s[col >> 6] + sw128_off16(row, col & 63);
@@ -407,6 +408,16 @@ __device__ __forceinline__ float stage_state(GradSmem& sm, const float* S, int64
     *reinterpret_cast<uint4*>(lo_at) = lo;
   }
   return inner;
+}
+
+// 8 consecutive columns of TMEM.
+__device__ __forceinline__ void tmem_ld8(uint32_t at, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(at));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // Sums of N columns over a warp's lanes: lane l has that of column l % N.  Halving: N - 1 exchanges where sums column by
@@ -442,7 +453,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   extern __shared__ __align__(1024) uint8_t raw[];
   GradSmem& sm = *reinterpret_cast<GradSmem*>(raw);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid / 32, 0), lane = tid % 32;
-  const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
+  const int quarter = warp & 3, c0 = (warp >> 2) * 16, row = quarter * 32 + lane;   // lanes and columns of TMEM
   int64_t id = blockIdx.x;
   const int64_t hk = id % p.Hk;
   id /= p.Hk;
@@ -465,17 +476,18 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   const uint32_t tmem = sm.tmem, mine = tmem + ((uint32_t)(quarter * 32) << 16);
   volatile int* abort = &sm.abort;
   constexpr uint32_t kk = idesc_bf16(128, 64, 0, 0), mk = idesc_bf16(128, 64, 1, 0), mm = idesc_bf16(128, 64, 1, 1);
+  constexpr uint32_t kk2 = idesc_bf16(128, 128, 0, 0), mk2 = idesc_bf16(128, 128, 1, 0);
   constexpr uint32_t kStep = 2048 >> 4, kStateLo = (4 * kTileBytes) >> 4;
   const uint32_t qk_lo = sdesc_sw128_lo(smem_u32(sm.qk[0]), 0), k_lo = qk_lo + kLo;
   const uint32_t qm_lo = sdesc_sw128_lo(smem_u32(sm.qk[0]), 2 * kTileBytes), km_lo = qm_lo + kLo;
   const uint32_t s_lo = sdesc_sw128_lo(smem_u32(sm.s[0]), 0), sm_lo = sdesc_sw128_lo(smem_u32(sm.s[0]), 2 * kTileBytes);
   const uint32_t dyr_lo = sdesc_sw128_lo(smem_u32(sm.dyr[0]), 0), u_lo = sdesc_sw128_lo(smem_u32(sm.u), 0);
   const uint32_t v_lo = sdesc_sw128_lo(smem_u32(sm.v), kTileBytes), t_lo = sdesc_sw128_lo(smem_u32(sm.t), 0);
-  const uint32_t bm_lo = sdesc_sw128_lo(smem_u32(sm.v), 0), n1_lo = t_lo, n2_lo = sdesc_sw128_lo(smem_u32(sm.n2), 0);
+  const uint32_t bm_lo = sdesc_sw128_lo(smem_u32(sm.v), 0), n2_lo = sdesc_sw128_lo(smem_u32(sm.n2), 0);
   // of 128 values in blocks of 64: step ks of 16
   auto by64 = [](int ks, uint32_t block) { return (ks >> 2) * (block >> 4) + (ks & 3) * 2; };
   uint32_t phase = 0, shadows = 0;
-  float dq[32] = {}, dk[32] = {};
+  float dq[16] = {}, dk[16] = {};
   bool ok = true;
   for (int64_t h = hk * group; ok && h < (hk + 1) * group; ++h) {
     const int64_t cell = (b * p.nch + chunk) * p.H + h;
@@ -521,30 +533,15 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         mma_ss_we(tmem + kU, v_lo + ks * kStep, kDHi, t_lo + kLo + ks * 2, kDHi, mk, 1);
       }
       mma_commit_elect(&sm.done);
-      // S^T dY^T and S^T dR^T
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks) {
-        const uint32_t a = sm_lo + ks * kStep, at = dyr_lo + by64(ks, 3 * kTileBytes);
-        mma_ss_we(tmem + kSY, a, kDHi, at, kDHi, mk, ks > 0);
-        mma_ss_we(tmem + kSY, a + kStateLo, kDHi, at, kDHi, mk, 1);
-        mma_ss_we(tmem + kSR, a, kDHi, at + kLo, kDHi, mk, ks > 0);
-        mma_ss_we(tmem + kSR, a, kDHi, at + 2 * kLo, kDHi, mk, 1);
-        mma_ss_we(tmem + kSR, a + kStateLo, kDHi, at + kLo, kDHi, mk, 1);
-      }
-      // [Q; K] K^T, where K^T N'^T will be
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks)
-        mma_ss_we(tmem + kKN, qk_lo + by64(ks, 2 * kTileBytes), kDHi, k_lo + by64(ks, 2 * kTileBytes), kDHi, kk, ks > 0);
-      mma_commit_elect(&sm.shadow);
     }
-    // dv = beta dR, and dR . v: four threads a step, 16 bytes at a time
+    // dv = beta dR, and dR . v: eight threads a step, 16 bytes at a time
     {
-      const int i = tid >> 2, part = tid & 3;
+      const int i = tid >> 3, part = tid & 7;
       const float beta = sm.c.beta[i];
       float dot = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int col = (e * 4 + part) * 8, vb = col >> 6;
+      for (int e = 0; e < 2; ++e) {
+        const int col = (e * 8 + part) * 8, vb = col >> 6;
         const uint32_t off = sw128_off16(i, col & 63);
         const uint4 hi = *reinterpret_cast<const uint4*>(sm.dyr[vb] + kTileBytes + off);
         const uint4 lo = *reinterpret_cast<const uint4*>(sm.dyr[vb] + 2 * kTileBytes + off);
@@ -568,18 +565,22 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       }
       dot += __shfl_xor_sync(0xffffffffu, dot, 1);
       dot += __shfl_xor_sync(0xffffffffu, dot, 2);
+      dot += __shfl_xor_sync(0xffffffffu, dot, 4);
       if (part == 0) sm.dot[i] = dot;
     }
     ok = wait_bar(&sm.done, phase++ & 1, abort, p.hdr, 71);
     tc_fence_after();
-    float x[32];
-    if (ok) {   // -D X
-      tmem_ld32(mine + kX + half * 32, x);
+    float x[16];
+    if (ok) {   // -D X: hi over its first 8 columns, lo over the others
+      tmem_ld16(mine + kX + c0, x);
       tmem_ld_wait();
       reg_tie(x);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) x[j] *= -sm.c.from[half * 32 + j];
-      store_half(mine + kX + half * 32, x);
+      for (int j = 0; j < 16; ++j) x[j] *= -sm.c.from[c0 + j];
+      uint32_t terms[16];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) split2(x[2 * j], x[2 * j + 1], terms[j], terms[8 + j]);
+      tmem_st16u(mine + kX + c0, terms);
       tmem_st_wait();
     }
     tc_fence_before();
@@ -589,26 +590,39 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     if (warp == 0) {
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
-        const uint32_t a = tmem + kX + half_col(ks);
+        const uint32_t a = tmem + kX + ks * 16;
         mma_ts_we(tmem + kU, a, t_lo + ks * 2, kDHi, kk, 1);
         mma_ts_we(tmem + kU, a, t_lo + kLo + ks * 2, kDHi, kk, 1);
-        mma_ts_we(tmem + kU, a + 16, t_lo + ks * 2, kDHi, kk, 1);
+        mma_ts_we(tmem + kU, a + 8, t_lo + ks * 2, kDHi, kk, 1);
       }
       mma_commit_elect(&sm.done);
+      // S^T [dY; dR]^T
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        const uint32_t a = sm_lo + ks * kStep, at = dyr_lo + by64(ks, 3 * kTileBytes);
+        mma_ss_we(tmem + kSY, a, kDHi, at, kDHi, mk2, ks > 0);
+        mma_ss_we(tmem + kSY, a + kStateLo, kDHi, at, kDHi, mk2, 1);
+        mma_ss_we(tmem + kSR, a, kDHi, at + 2 * kLo, kDHi, mk, 1);
+      }
+      // [Q; K] K^T, where K^T N'^T will be
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks)
+        mma_ss_we(tmem + kKN, qk_lo + by64(ks, 2 * kTileBytes), kDHi, k_lo + by64(ks, 2 * kTileBytes), kDHi, kk, ks > 0);
+      mma_commit_elect(&sm.shadow);
     }
     ok = wait_bar(&sm.done, phase++ & 1, abort, p.hdr, 72);
     tc_fence_after();
     if (ok) {   // U's rows, by steps
-      tmem_ld32(mine + kU + half * 32, x);
+      tmem_ld16(mine + kU + c0, x);
       tmem_ld_wait();
       reg_tie(x);
-      uint8_t* at = sm.u + (row >> 6) * kTileBytes;
+      uint8_t* at = sm.u[row >> 6];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
+      for (int j = 0; j < 16; ++j) {
         const __nv_bfloat16 hi = __float2bfloat16_rn(x[j]);
-        const uint32_t off = sw128_off16(half * 32 + j, row & 63);
+        const uint32_t off = sw128_off16(c0 + j, row & 63);
         *reinterpret_cast<__nv_bfloat16*>(at + off) = hi;
-        *reinterpret_cast<__nv_bfloat16*>(at + 2 * kTileBytes + off) = __float2bfloat16_rn(x[j] - __bfloat162float(hi));
+        *reinterpret_cast<__nv_bfloat16*>(at + kTileBytes + off) = __float2bfloat16_rn(x[j] - __bfloat162float(hi));
       }
     }
     fence_proxy_async_smem();
@@ -620,10 +634,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       // [dY; dR hi] U^T, and (rows 64..127) dR lo U^T
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {
-        const uint32_t a = dyr_lo + by64(ks, 3 * kTileBytes), at = u_lo + by64(ks, kTileBytes);
-        mma_ss_we(tmem + kX, a, kDHi, at, kDHi, kk, ks > 0);
-        mma_ss_we(tmem + kX, a, kDHi, at + 2 * kLo, kDHi, kk, 1);
-        mma_ss_we(tmem + kU, a + kLo, kDHi, at, kDHi, kk, ks > 0);
+        const uint32_t a = dyr_lo + by64(ks, 3 * kTileBytes), at = u_lo + by64(ks, 2 * kTileBytes);
+        mma_ss_we(tmem + kX, a, kDHi, at, kDHi, kk2, ks > 0);
+        mma_ss_we(tmem + kQB, a + kLo, kDHi, at, kDHi, kk, ks > 0);
       }
       mma_commit_elect(&sm.done);
     }
@@ -638,9 +651,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       // G^T U^T
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {
-        const uint32_t a = sm_lo + ks * kStep, at = u_lo + by64(ks, kTileBytes);
+        const uint32_t a = sm_lo + ks * kStep, at = u_lo + by64(ks, 2 * kTileBytes);
         mma_ss_we(tmem + kGU, a, kDHi, at, kDHi, mk, ks > 0);
-        mma_ss_we(tmem + kGU, a, kDHi, at + 2 * kLo, kDHi, mk, 1);
+        mma_ss_we(tmem + kGU, a, kDHi, at + kLo, kDHi, mk, 1);
         mma_ss_we(tmem + kGU, a + kStateLo, kDHi, at, kDHi, mk, 1);
       }
     }
@@ -651,31 +664,33 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       // lanes 0..63: Bm's rows; 64..127: N's
       const int i = row & 63;
       const bool lower = quarter >= 2;
-      float y[32];
-      tmem_ld32(mine + kX + half * 32, x);
-      tmem_ld32(mine + kU + half * 32, y);
+      float y[16], z[16];
+      tmem_ld16(mine + kX + c0, x);
+      tmem_ld16(mine + kU + c0, y);
+      tmem_ld16(mine + kQB + c0, z);
       tmem_ld_wait();
       reg_tie(x);
       reg_tie(y);
+      reg_tie(z);
       const float ch = sm.c.hi[i], cl = sm.c.lo[i], beta = sm.c.beta[i], by = lower ? -1.f : p.scale;
       const int last = lower ? i - 1 : i;
-      uint8_t* to = lower ? sm.t : sm.v;
+      uint8_t* to = lower ? sm.v + kTileBytes : sm.v;   // lo: in t, at the same place
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const int c = half * 32 + j;
-        const float f = lower ? x[j] + y[j] : x[j];
+      for (int j = 0; j < 16; ++j) {
+        const int c = c0 + j;
+        const float f = lower ? (x[j] + y[j]) + z[j] : x[j] + y[j];
         x[j] = c <= last ? f * by * __expf((ch - sm.c.hi[c]) + (cl - sm.c.lo[c])) : 0.f;
       }
 #pragma unroll
-      for (int j = 0; j < 32; j += 8) {
-        const uint32_t off = sw128_off16(i, half * 32 + j);
+      for (int j = 0; j < 16; j += 8) {
+        const uint32_t off = sw128_off16(i, c0 + j);
         uint4 hi, lo;
         split2(x[j], x[j + 1], hi.x, lo.x);
         split2(x[j + 2], x[j + 3], hi.y, lo.y);
         split2(x[j + 4], x[j + 5], hi.z, lo.z);
         split2(x[j + 6], x[j + 7], hi.w, lo.w);
         *reinterpret_cast<uint4*>(to + off) = hi;
-        *reinterpret_cast<uint4*>(to + kTileBytes + off) = lo;
+        *reinterpret_cast<uint4*>(to + 2 * kTileBytes + off) = lo;
         if (lower) {
           split2(beta * x[j], beta * x[j + 1], hi.x, lo.x);
           split2(beta * x[j + 2], beta * x[j + 3], hi.y, lo.y);
@@ -685,14 +700,15 @@ __global__ void __launch_bounds__(kGradThreads, 1)
           *reinterpret_cast<uint4*>(sm.n2 + kTileBytes + off) = lo;
         }
       }
-      // products of pairs a > b, summed along this row (a) over the columns before each, then over the rows from it on
-      tmem_ld32(mine + kKN + half * 32, y);
+      // products of pairs a > b, summed along this row (a) over this warp's columns before each, then over the rows from
+      // it on
+      tmem_ld16(mine + kKN + c0, y);
       tmem_ld_wait();
       reg_tie(y);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
+      for (int j = 0; j < 16; ++j) {
         const float w = lower ? beta * y[j] : y[j];
-        y[j] = i >= half * 32 + j ? row_sum : 0.f;
+        y[j] = i >= c0 + j ? row_sum : 0.f;
         row_sum = fmaf(x[j], w, row_sum);
       }
       across = sum_columns(y);
@@ -706,33 +722,30 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
         const uint32_t k = km_lo + ks * kStep, q = qm_lo + ks * kStep;
-        mma_ss_we(tmem + kKB, k, kDHi, bm_lo + ks * 2, kDHi, mk, ks > 0);
-        mma_ss_we(tmem + kKB, k, kDHi, bm_lo + kLo + ks * 2, kDHi, mk, 1);
+        mma_ss_we(tmem + kKB, k, kDHi, bm_lo + ks * 2, kDHi, mk2, ks > 0);   // with N' beside Bm
+        mma_ss_we(tmem + kKB, k, kDHi, bm_lo + 2 * kLo + ks * 2, kDHi, mk2, 1);
         mma_ss_we(tmem + kQB, q, kDHi, bm_lo + ks * kStep, kDHi, mm, ks > 0);
-        mma_ss_we(tmem + kQB, q, kDHi, bm_lo + kLo + ks * kStep, kDHi, mm, 1);
+        mma_ss_we(tmem + kQB, q, kDHi, bm_lo + 2 * kLo + ks * kStep, kDHi, mm, 1);
         mma_ss_we(tmem + kQB, k, kDHi, n2_lo + ks * kStep, kDHi, mm, 1);
         mma_ss_we(tmem + kQB, k, kDHi, n2_lo + kLo + ks * kStep, kDHi, mm, 1);
-        mma_ss_we(tmem + kKN, k, kDHi, n1_lo + ks * 2, kDHi, mk, ks > 0);
-        mma_ss_we(tmem + kKN, k, kDHi, n1_lo + kLo + ks * 2, kDHi, mk, 1);
       }
       mma_commit_elect(&sm.done);
     }
     ok = wait_bar(&sm.done, phase++ & 1, abort, p.hdr, 75);
     tc_fence_after();
-    // this thread's key, 32 steps: dq, dk, and three sums over the keys, by quarters of the lanes
-    float* sums = reinterpret_cast<float*>(sm.u);   // [3][4][64], then by warps across and inner, by rows row_sum
+    // this thread's key, 16 steps: dq, dk, and three sums over the keys, by quarters of the lanes
+    float* sums = reinterpret_cast<float*>(sm.u[0]);   // [3][4][64]; across [4][64], row_sum [4][128], inner [16]
     if (ok) {
       const uint8_t *qt = sm.qk[row >> 6], *kt = qt + kTileBytes;
 #pragma unroll
-      for (int j0 = 0; j0 < 32; j0 += 16) {
-        const uint32_t c0 = half * 32 + j0;
-        float sy[16], sr[16], gu[16], kb[16], qb[16], kn[16];
-        tmem_ld16(mine + kSY + c0, sy);
-        tmem_ld16(mine + kSR + c0, sr);
-        tmem_ld16(mine + kGU + c0, gu);
-        tmem_ld16(mine + kKB + c0, kb);
-        tmem_ld16(mine + kQB + c0, qb);
-        tmem_ld16(mine + kKN + c0, kn);
+      for (int j0 = 0; j0 < 16; j0 += 8) {
+        float sy[8], sr[8], gu[8], kb[8], qb[8], kn[8];
+        tmem_ld8(mine + kSY + c0 + j0, sy);
+        tmem_ld8(mine + kSR + c0 + j0, sr);
+        tmem_ld8(mine + kGU + c0 + j0, gu);
+        tmem_ld8(mine + kKB + c0 + j0, kb);
+        tmem_ld8(mine + kQB + c0 + j0, qb);
+        tmem_ld8(mine + kKN + c0 + j0, kn);
         tmem_ld_wait();
         reg_tie(sy);
         reg_tie(sr);
@@ -741,8 +754,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         reg_tie(qb);
         reg_tie(kn);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int i = c0 + j;
+        for (int j = 0; j < 8; ++j) {
+          const int i = c0 + j0 + j;
           const float from = sm.c.from[i], to = sm.c.to[i], beta = sm.c.beta[i];
           const float kv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(kt + sw128_off16(i, row & 63)));
           const float qv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(qt + sw128_off16(i, row & 63)));
@@ -754,22 +767,22 @@ __global__ void __launch_bounds__(kGradThreads, 1)
           gu[j] = kv * wrote;
         }
         const float s0 = sum_columns(sy), s1 = sum_columns(sr), s2 = sum_columns(gu);
-        if (lane < 16) {
-          sums[quarter * kChunk + c0 + lane] = s0;
-          sums[(4 + quarter) * kChunk + c0 + lane] = s1;
-          sums[(8 + quarter) * kChunk + c0 + lane] = s2;
+        if (lane < 8) {
+          sums[quarter * kChunk + c0 + j0 + lane] = s0;
+          sums[(4 + quarter) * kChunk + c0 + j0 + lane] = s1;
+          sums[(8 + quarter) * kChunk + c0 + j0 + lane] = s2;
         }
       }
-      sums[12 * kChunk + quarter * kChunk + half * 32 + lane] = across;
-      if (half == 0) sums[16 * kChunk + row] = row_sum;
+      if (lane < 16) sums[(12 + quarter) * kChunk + c0 + lane] = across;
+      sums[16 * kChunk + (c0 >> 4) * 128 + row] = row_sum;
 #pragma unroll
       for (int o = 16; o; o >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, o);
-      if (lane == 0) sums[18 * kChunk + warp] = inner;
+      if (lane == 0) sums[24 * kChunk + warp] = inner;
     }
     __syncthreads();
     if (*abort) break;
     if (warp == 0) {   // a lane has steps 2 l and 2 l + 1
-      float z[2], rho[2], sigma[2], pairs[2], g[2];
+      float z[2], rho[2], sigma[2], g[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int i = 2 * lane + e;
@@ -781,20 +794,27 @@ __global__ void __launch_bounds__(kGradThreads, 1)
           sigma[e] += sums[(8 + w) * kChunk + i];
           g[e] += sums[(12 + w) * kChunk + i];
         }
-        pairs[e] = sums[16 * kChunk + i] + sums[17 * kChunk + i];   // of row i, with the first 32 steps
       }
-      float all = lane < 8 ? sums[18 * kChunk + lane] : 0.f;
+      // pairs whose earlier step is in an earlier warp's columns: rows from a step on
+#pragma unroll
+      for (int c = 0; c < 3; ++c) {
+        const float* of = sums + 16 * kChunk + c * 128;
+        const float p0 = of[2 * lane] + of[64 + 2 * lane], p1 = of[2 * lane + 1] + of[65 + 2 * lane];
+        const float upto = scan_up(p0 + p1, lane), rest = __shfl_sync(0xffffffffu, upto, 31) - upto + p1;
+        if (2 * lane >= 16 * (c + 1)) {
+          g[0] += rest + p0;
+          g[1] += rest;
+        }
+      }
+      float all = lane < 16 ? sums[24 * kChunk + lane] : 0.f;
       all = __shfl_sync(0xffffffffu, scan_up(all, lane), 31);
       // from a step to the chunk's end; the sums before it
-      const float r1 = scan_up(rho[0] + rho[1], lane), rt = __shfl_sync(0xffffffffu, r1, 31);
-      const float p1 = scan_up(pairs[0] + pairs[1], lane), pt = __shfl_sync(0xffffffffu, p1, 31);
-      const float s1 = scan_up(sigma[0] + sigma[1], lane);
-      const float after = rt - r1, p_after = pt - p1, before = s1 - sigma[0] - sigma[1];
+      const float r1 = scan_up(rho[0] + rho[1], lane), after = __shfl_sync(0xffffffffu, r1, 31) - r1;
+      const float before = scan_up(sigma[0] + sigma[1], lane) - sigma[0] - sigma[1];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int i = 2 * lane + e;
         g[e] += all + after + rho[1] + (e ? 0.f : rho[0]) + before + (e ? sigma[0] : 0.f);
-        if (i >= 32) g[e] += p_after + pairs[1] + (e ? 0.f : pairs[0]);
         if (i < n) {
           const int64_t at = (b * p.T + t0 + i) * p.H + h;
           p.dbeta[at] = sm.dot[i] - z[e];
@@ -807,8 +827,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     __syncthreads();
     uint8_t* to = sm.s[0] + (row >> 6) * kTileBytes;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const uint32_t off = sw128_off16(half * 32 + j, row & 63);
+    for (int j = 0; j < 16; ++j) {
+      const uint32_t off = sw128_off16(c0 + j, row & 63);
       *reinterpret_cast<__nv_bfloat16*>(to + off) = __float2bfloat16_rn(dq[j]);
       *reinterpret_cast<__nv_bfloat16*>(to + 2 * kTileBytes + off) = __float2bfloat16_rn(dk[j]);
     }
