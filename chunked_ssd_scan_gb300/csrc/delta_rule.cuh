@@ -37,6 +37,8 @@ struct ChunkDecay {
   float hi[kChunk], lo[kChunk];   // sum of g over the chunk's steps up to i
   float beta[kChunk];
   float from[kChunk], to[kChunk]; // e^(sum up to i), e^(sum behind i)
+  float back[kChunk];             // e^-(sum up to i)
+  int plain;                      // whether no sum of the chunk is beyond e^+-80: from[i] back[j] is the decay between
 };
 
 __device__ __forceinline__ float decay_between(const ChunkDecay& c, int i, int j) {   // j <= i
@@ -72,6 +74,10 @@ __device__ __forceinline__ void chunk_decay_warp(const Params& p, ChunkDecay& c,
   c.lo[i1] = lo;
   c.from[i0] = expf(h0);
   c.from[i1] = expf(hi);
+  c.back[i0] = expf(-h0);
+  c.back[i1] = expf(-hi);
+  const bool plain = __all_sync(0xffffffffu, fabsf(h0) <= 80.f && fabsf(hi) <= 80.f);
+  if (lane == 0) c.plain = plain;
   c.to[i0] = expf((th - h0) + (tl - l0));
   c.to[i1] = expf((th - hi) + (tl - lo));
   const float* bp = p.beta + b * p.bs[0] + h;

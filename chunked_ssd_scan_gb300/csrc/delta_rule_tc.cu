@@ -172,6 +172,7 @@ __global__ void __launch_bounds__(kPrepThreads, 6) delta_chunk_kernel(const __gr
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
   bool ok = true;
+  if (warp == 1) chunk_decay_warp(p, sm.c, b, t0, n, hk * group, lane);
   if (warp == 0) {
     mbar_arrive_expect_tx_elect(&sm.loaded, KB * 2 * kTileBytes);
 #pragma unroll
@@ -199,8 +200,10 @@ __global__ void __launch_bounds__(kPrepThreads, 6) delta_chunk_kernel(const __gr
     const int64_t cell = (b * p.nch + chunk) * p.H + h;
     uint8_t* out = buf.squares + cell * buf.square;
     __syncthreads();
-    if (warp == 0) chunk_decay_warp(p, sm.c, b, t0, n, h, lane);
-    __syncthreads();
+    if (h > hk * group) {
+      if (warp == 1) chunk_decay_warp(p, sm.c, b, t0, n, h, lane);
+      __syncthreads();
+    }
     float* decays = buf.decays + cell * 3 * kChunk;
     if (threadIdx.x < kChunk) {
       decays[threadIdx.x] = sm.c.from[threadIdx.x];
@@ -209,25 +212,33 @@ __global__ void __launch_bounds__(kPrepThreads, 6) delta_chunk_kernel(const __gr
       decays[threadIdx.x] = sm.c.to[threadIdx.x - kChunk];
     }
     const float hi = sm.c.hi[row], lo = sm.c.lo[row];
-    const float by = warp < 2 ? sm.c.beta[row] : p.scale;
+    const float by = warp < 2 ? sm.c.beta[row] : p.scale, by_from = by * sm.c.from[row];
     const int last = warp < 2 ? row - 1 : row;   // the strict part of A, P with its diagonal
+    const bool plain = sm.c.plain;
 #pragma unroll 1
     for (int c0 = 0; c0 < kChunk; c0 += 16) {
       float v[16];
-      tmem_ld16(mine + c0, v);
-      tmem_ld_wait();
-      reg_tie(v);
       if ((warp & 1) * 32 + 31 < c0) {   // above the diagonal
 #pragma unroll
         for (int j = 0; j < 16; ++j) v[j] = 0.f;
-      } else
+      } else {
+        tmem_ld16(mine + c0, v);
+        tmem_ld_wait();
+        reg_tie(v);
+        if (plain) {
 #pragma unroll
-      for (int j = 0; j < 16; j += 4) {
-        const float4 ch = *reinterpret_cast<const float4*>(&sm.c.hi[c0 + j]), cl = *reinterpret_cast<const float4*>(&sm.c.lo[c0 + j]);
-        v[j] = c0 + j <= last ? v[j] * by * __expf((hi - ch.x) + (lo - cl.x)) : 0.f;
-        v[j + 1] = c0 + j + 1 <= last ? v[j + 1] * by * __expf((hi - ch.y) + (lo - cl.y)) : 0.f;
-        v[j + 2] = c0 + j + 2 <= last ? v[j + 2] * by * __expf((hi - ch.z) + (lo - cl.z)) : 0.f;
-        v[j + 3] = c0 + j + 3 <= last ? v[j + 3] * by * __expf((hi - ch.w) + (lo - cl.w)) : 0.f;
+          for (int j = 0; j < 16; j += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(&sm.c.back[c0 + j]);
+            v[j] = c0 + j <= last ? v[j] * (by_from * f.x) : 0.f;
+            v[j + 1] = c0 + j + 1 <= last ? v[j + 1] * (by_from * f.y) : 0.f;
+            v[j + 2] = c0 + j + 2 <= last ? v[j + 2] * (by_from * f.z) : 0.f;
+            v[j + 3] = c0 + j + 3 <= last ? v[j + 3] * (by_from * f.w) : 0.f;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            v[j] = c0 + j <= last ? v[j] * by * __expf((hi - sm.c.hi[c0 + j]) + (lo - sm.c.lo[c0 + j])) : 0.f;
+        }
       }
       if (warp < 2) {
 #pragma unroll
@@ -267,10 +278,9 @@ __global__ void __launch_bounds__(kPrepThreads, 6) delta_chunk_kernel(const __gr
 
 // ---------------------------------------------------------------------------------------------------------------------
 // The walk.  TMEM columns: the state's two terms, X = S K^T and after it -D X's two terms, U's accumulator and after it
-// U's two terms, E U's two terms, (E U)^T K, y.  Halves of 32 columns keep hi then lo of themselves, so that a warp that
-// has read a half may write its terms over it.
+// U's two terms, E U's two terms, (E U)^T K, y.  Every 16 columns keep hi then lo of themselves, so that a warp that
+// has read them may write its terms over them.
 // ---------------------------------------------------------------------------------------------------------------------
-constexpr int kChainThreads = 14 * 32;
 constexpr uint32_t kColS = 0, kColX = 128, kColU = 192, kColW = 256, kColD = 320, kColO = 448;
 
 template <int KB>
@@ -280,21 +290,21 @@ struct Stage {
   uint8_t pad[256];
 };
 struct ChainBars {
-  uint64_t full[2], empty[2], s_ready[2], x_full, r_ready, u_full, w_ready, u_ready, d_full, o1_full, o_scaled, o2_full,
+  uint64_t full[2], empty[2], s_ready[4], x_full, r_ready, u_full, w_ready, u_ready, d_full, o1_full, o_scaled, o2_full,
       o_free, drain;
 };
 template <int KB>
 struct ChainSmem {
   Stage<KB> st[2];
   uint8_t y[2 * kTileBytes];
-  uint8_t s[2][128 * 128];   // 128 rows of 32 values of the state on their way out, for each half of the keys
+  uint8_t s[4][128 * 64];   // 128 rows of 16 keys of the state on their way out, for each quarter of the keys
   ChainBars bar;
   uint32_t tmem;
   int abort, keep;
 };
 
 template <int KB>
-__global__ void __launch_bounds__(kChainThreads, 1)
+__global__ void __launch_bounds__(kWalkThreads, 1)
     delta_chain_kernel(const __grid_constant__ Params p, const __grid_constant__ TcMaps m, TcBuffers buf, int vtiles) {
   extern __shared__ __align__(1024) uint8_t raw[];
   ChainSmem<KB>& sm = *reinterpret_cast<ChainSmem<KB>*>(raw);
@@ -309,15 +319,14 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar.full[s], 1);
       mbar_init(&bar.empty[s], 1);
-      mbar_init(&bar.s_ready[s], 4);
     }
+    for (uint64_t* four : {&bar.s_ready[0], &bar.s_ready[1], &bar.s_ready[2], &bar.s_ready[3], &bar.o_scaled, &bar.o_free})
+      mbar_init(four, 4);
     for (uint64_t* one : {&bar.x_full, &bar.u_full, &bar.d_full, &bar.o1_full, &bar.o2_full, &bar.drain}) mbar_init(one, 1);
-    for (uint64_t* eight : {&bar.r_ready, &bar.w_ready, &bar.u_ready}) mbar_init(eight, 8);
-    mbar_init(&bar.o_scaled, 4);
-    mbar_init(&bar.o_free, 4);
+    for (uint64_t* all : {&bar.r_ready, &bar.w_ready, &bar.u_ready}) mbar_init(all, kStateWarps);
     fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == 20) {
     tmem_alloc(&sm.tmem, 512);
     tmem_relinquish();
   }
@@ -327,7 +336,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   const uint32_t tmem = sm.tmem;
   const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
 
-  if (warp == 13) {   // loads
+  if (warp == 21) {   // loads
     int issued = 0;
     for (int c = 0; c < nch; ++c) {
       const int s = c & 1;
@@ -352,7 +361,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       if (loads > 0) drained &= mbar_wait_bounded(&bar.full[s], (loads - 1) & 1, 2000000000ull);
     }
     if (!drained && lane == 0) latch_error(p.hdr, SSD_ERR_TIMEOUT, 11);
-  } else if (warp == 12) {   // products
+  } else if (warp == 20) {   // products
     constexpr uint32_t id_k = idesc_bf16(128, 64, 0, 0), id_v = idesc_bf16(128, 64, 1, 0), id_d = idesc_bf16(128, Kp, 0, 1);
     for (int c = 0; c < nch; ++c) {
       const int s = c & 1;
@@ -362,13 +371,13 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       const uint32_t km_lo = sdesc_sw128_lo(smem_u32(st.k), kTileBytes), v_lo = sdesc_sw128_lo(smem_u32(st.v), kTileBytes);
       const uint32_t t_lo = sdesc_sw128_lo(smem_u32(st.t), 0), p_lo = sdesc_sw128_lo(smem_u32(st.p), 0);
       if (!wait_bar(&bar.full[s], (c >> 1) & 1, abort, p.hdr, 12)) break;
-      // X = S K^T, the first half of the keys as soon as its terms are there
+      // X = S K^T, a quarter of the keys as soon as its terms are there
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (!wait_bar(&bar.s_ready[half], par, abort, p.hdr, 13)) break;
+      for (int part = 0; part < 4; ++part) {
+        if (!wait_bar(&bar.s_ready[part], par, abort, p.hdr, 13)) break;
         tc_fence_after();
 #pragma unroll
-        for (int ks = half * KB * 2; ks < (half + 1) * KB * 2; ++ks) {
+        for (int ks = part * KB; ks < (part + 1) * KB; ++ks) {
           const uint32_t at = k_lo + (((ks >> 2) * kTileBytes + (ks & 3) * 32) >> 4);
           mma_ts_we(tmem + kColX, tmem + kColS + ks * 8, at, kDHi, id_k, ks > 0);
           mma_ts_we(tmem + kColX, tmem + kColS + Kp / 2 + ks * 8, at, kDHi, id_k, 1);
@@ -387,10 +396,10 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       tc_fence_after();
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
-        const uint32_t a = tmem + kColX + half_col(ks);
+        const uint32_t a = tmem + kColX + ks * 16;
         mma_ts_we(tmem + kColU, a, t_lo + ks * 2, kDHi, id_k, 1);
         mma_ts_we(tmem + kColU, a, t_lo + kLo + ks * 2, kDHi, id_k, 1);
-        mma_ts_we(tmem + kColU, a + 16, t_lo + ks * 2, kDHi, id_k, 1);
+        mma_ts_we(tmem + kColU, a + 8, t_lo + ks * 2, kDHi, id_k, 1);
       }
       mma_commit_elect(&bar.u_full);
       // S Q^T, while U is turned into operands
@@ -408,9 +417,9 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       tc_fence_after();
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
-        const uint32_t a = tmem + kColW + half_col(ks);
+        const uint32_t a = tmem + kColW + ks * 16;
         mma_ts_we(tmem + kColD, a, km_lo + ks * (2048 >> 4), kDHi, id_d, ks > 0);
-        mma_ts_we(tmem + kColD, a + 16, km_lo + ks * (2048 >> 4), kDHi, id_d, 1);
+        mma_ts_we(tmem + kColD, a + 8, km_lo + ks * (2048 >> 4), kDHi, id_d, 1);
       }
       mma_commit_elect(&bar.d_full);
       // y = scale D S Q^T + U P^T
@@ -419,10 +428,10 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       tc_fence_after();
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
-        const uint32_t a = tmem + kColU + half_col(ks);
+        const uint32_t a = tmem + kColU + ks * 16;
         mma_ts_we(tmem + kColO, a, p_lo + ks * 2, kDHi, id_k, 1);
         mma_ts_we(tmem + kColO, a, p_lo + kLo + ks * 2, kDHi, id_k, 1);
-        mma_ts_we(tmem + kColO, a + 16, p_lo + ks * 2, kDHi, id_k, 1);
+        mma_ts_we(tmem + kColO, a + 8, p_lo + ks * 2, kDHi, id_k, 1);
       }
       mma_commit_elect(&bar.o2_full);
       mma_commit_elect(&bar.empty[s]);
@@ -432,70 +441,68 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       sm.keep = 1;   // products may still write TMEM: it stays allocated
       latch_error(p.hdr, SSD_ERR_TIMEOUT, 20);
     }
-  } else if (warp < 8) {   // the state, and the operands on the way to the next one; a thread has a value and half the keys
-    constexpr int KH = Kp / 2;
-    const int half = warp >> 2, row = v0 + (warp & 3) * 32 + lane, k0 = half * KH;
+  } else if (warp < kStateWarps) {   // the state, and the operands on the way to the next one
+    constexpr int KQ = Kp / 4;
+    const int part = warp >> 2, row = v0 + (warp & 3) * 32 + lane, k0 = part * KQ, j0 = part * 16;
     const bool live = row < p.V;
     const int64_t at = (((int64_t)b * p.H + h) * p.V + row) * p.K + k0;
-    float S[KH];
+    float S[KQ];
 #pragma unroll
-    for (int k = 0; k < KH; ++k) S[k] = p.init && live && k0 + k < p.K ? p.init[at + k] : 0.f;
-    const bool wide_f = (reinterpret_cast<uintptr_t>(p.final_state) & 31) == 0;
+    for (int k = 0; k < KQ; ++k) S[k] = p.init && live && k0 + k < p.K ? p.init[at + k] : 0.f;
     for (int c = 0; c < nch; ++c) {
       const int s = c & 1;
       const uint32_t par = c & 1;
       const Stage<KB>& st = sm.st[s];
-      // the state's terms
       store_state_terms(tmem + lanes + kColS + k0 / 2, Kp / 2, S);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.s_ready[half]);
+      if (lane == 0) mbar_arrive(&bar.s_ready[part]);
       const int cell = (b * nch + c) * (int)p.H + h;
-      if (p.states_out) send_state(sm.s[half], &m.states, S, half, 0, v0, cell, p.K);
+      if (p.states_out) send_state(sm.s[part], &m.states, S, part, 0, v0, cell, p.K);
       if (!wait_bar(&bar.full[s], (c >> 1) & 1, abort, p.hdr, 21)) break;   // the decays
       const float all = st.from[kChunk - 1];
       if (!wait_bar(&bar.x_full, par, abort, p.hdr, 22)) break;
       tc_fence_after();
-      float x[32];
-      tmem_ld32(tmem + lanes + kColX + half * 32, x);
+      float x[16];
+      tmem_ld16(tmem + lanes + kColX + j0, x);
       tmem_ld_wait();
       reg_tie(x);
 #pragma unroll
-      for (int j = 0; j < 32; j += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(&st.from[half * 32 + j]);
+      for (int j = 0; j < 16; j += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(&st.from[j0 + j]);
         x[j] *= -f.x;
         x[j + 1] *= -f.y;
         x[j + 2] *= -f.z;
         x[j + 3] *= -f.w;
       }
-      store_half(tmem + lanes + kColX + half * 32, x);
+      store_terms(tmem + lanes + kColX + j0, x);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.r_ready);
       if constexpr (KB == 2)
-        if (p.states_out) send_state(sm.s[half], &m.states, S, half, KH / 2, v0, cell, p.K);
+        if (p.states_out) send_state(sm.s[part], &m.states, S, part, KQ / 2, v0, cell, p.K);
       if (!wait_bar(&bar.u_full, par, abort, p.hdr, 23)) break;
       tc_fence_after();
-      tmem_ld32(tmem + lanes + kColU + half * 32, x);
+      tmem_ld16(tmem + lanes + kColU + j0, x);
       tmem_ld_wait();
       reg_tie(x);
-      float w[32];
+      float w[16];
 #pragma unroll
-      for (int j = 0; j < 32; j += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(&st.to[half * 32 + j]);
+      for (int j = 0; j < 16; j += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(&st.to[j0 + j]);
         w[j] = x[j] * f.x;
         w[j + 1] = x[j + 1] * f.y;
         w[j + 2] = x[j + 2] * f.z;
         w[j + 3] = x[j + 3] * f.w;
       }
-      store_half(tmem + lanes + kColW + half * 32, w);
+      store_terms(tmem + lanes + kColW + j0, w);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.w_ready);
-      store_half(tmem + lanes + kColU + half * 32, x);
+      store_terms(tmem + lanes + kColU + j0, x);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -503,19 +510,20 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       if (!wait_bar(&bar.d_full, par, abort, p.hdr, 24)) break;
       tc_fence_after();
 #pragma unroll
-      for (int k = 0; k < KH; k += 32) {
-        tmem_ld32(tmem + lanes + kColD + k0 + k, x);
+      for (int k = 0; k < KQ; k += 16) {
+        tmem_ld16(tmem + lanes + kColD + k0 + k, x);
         tmem_ld_wait();
         reg_tie(x);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) S[k + j] = fmaf(all, S[k + j], x[j]);
+        for (int j = 0; j < 16; ++j) S[k + j] = fmaf(all, S[k + j], x[j]);
       }
     }
     if ((threadIdx.x & 127) == 0) bulk_wait_group<0>();
     if (p.final_state && live && !*abort) {
+      const bool wide = (reinterpret_cast<uintptr_t>(p.final_state) & 31) == 0;
 #pragma unroll
-      for (int k = 0; k < KH; k += 8)
-        if (k0 + k < p.K) store8(p.final_state + at + k, S + k, wide_f);
+      for (int k = 0; k < KQ; k += 8)
+        if (k0 + k < p.K) store8(p.final_state + at + k, S + k, wide);
     }
   } else {   // y: a thread has a value
     const int v = (warp & 3) * 32 + lane;
@@ -560,7 +568,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.o_free);
       if (p.y) {
-        if (warp == 8 && lane == 0) bulk_wait_group_read<0>();   // the last chunk's rows have left
+        if (warp == kStateWarps && lane == 0) bulk_wait_group_read<0>();   // the last chunk's rows have left
         named_barrier(1, 128);
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
@@ -569,18 +577,18 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         }
         fence_proxy_async_smem();
         named_barrier(1, 128);
-        if (warp == 8 && lane == 0) {
+        if (warp == kStateWarps && lane == 0) {
           tma_store_4d(&m.y, sm.y, v0, c * kChunk, h, b);
           if (v0 + 64 < p.V) tma_store_4d(&m.y, sm.y + kTileBytes, v0 + 64, c * kChunk, h, b);
           bulk_commit_group();
         }
       }
     }
-    if (warp == 8 && lane == 0) bulk_wait_group<0>();
+    if (warp == kStateWarps && lane == 0) bulk_wait_group<0>();
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12 && !sm.keep) {
+  if (warp == 20 && !sm.keep) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -611,7 +619,7 @@ cudaError_t chain_as(const Params& p, const TcMaps& m, const TcBuffers& buf, cud
   const cudaError_t e = cudaFuncSetAttribute(delta_chain_kernel<KB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int vtiles = (int)((p.V + 127) / 128);
-  delta_chain_kernel<KB><<<(unsigned)(p.batch * p.H * vtiles), kChainThreads, smem, st>>>(p, m, buf, vtiles);
+  delta_chain_kernel<KB><<<(unsigned)(p.batch * p.H * vtiles), kWalkThreads, smem, st>>>(p, m, buf, vtiles);
   return cudaGetLastError();
 }
 
@@ -646,15 +654,15 @@ bool head_map(CUtensorMap* m, const void* base, int64_t batch, int64_t T, int64_
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Map of [cells, V, K] f32 states in boxes of 128 values and 32 keys.
+// Map of [cells, V, K] f32 states in boxes of 128 values and 16 keys.
 bool state_map(CUtensorMap* m, const void* base, int64_t cells, int64_t V, int64_t K) {
   const auto encode = tensor_map_encoder();
   if (!encode) return false;
   const cuuint64_t dims[4] = {(cuuint64_t)K, (cuuint64_t)V, (cuuint64_t)cells, 1};
   const cuuint64_t strides[3] = {(cuuint64_t)K * 4, (cuuint64_t)(K * V * 4), (cuuint64_t)(K * V * 4)};
-  const cuuint32_t box[4] = {32, 128, 1, 1}, one[4] = {1, 1, 1, 1};
+  const cuuint32_t box[4] = {16, 128, 1, 1}, one[4] = {1, 1, 1, 1};
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, const_cast<void*>(base), dims, strides, box, one,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -30,7 +30,6 @@ using namespace delta;
 // that G takes.  K and dY have two buffers, the others one: what is used early in a chunk is loaded again while the
 // rest of it runs.
 // ---------------------------------------------------------------------------------------------------------------------
-constexpr int kChainThreads = 14 * 32;
 constexpr uint32_t kColG = 0, kColY = 128, kColU = 192, kColR = 256, kColW = 320, kColD = 384;
 
 template <int KB>
@@ -39,16 +38,16 @@ struct BackSmem {
   uint8_t q[KB * kTileBytes], t[2 * kTileBytes], p[2 * kTileBytes];
   uint8_t dys[2][2 * kTileBytes];   // scale D dY, hi and lo
   uint8_t r[4 * kTileBytes];        // dR on its way out: by 64 values, hi then lo
-  uint8_t s[2][128 * 128];          // G on its way out
+  uint8_t s[4][128 * 64];           // G on its way out
   float decays[2][3 * kChunk];
   uint64_t kdy_full[2], kdy_empty[2], q_full, q_empty, t_full, t_empty, p_full, p_empty;
-  uint64_t g_ready[2], y_full, u_ready, r_full, w_ready, r_free, dys_ready, d_full, drain;
+  uint64_t g_ready[4], y_full, u_ready, r_full, w_ready, r_free, dys_ready, d_full, drain;
   uint32_t tmem;
   int abort, keep;
 };
 
 template <int KB>
-__global__ void __launch_bounds__(kChainThreads, 1)
+__global__ void __launch_bounds__(kWalkThreads, 1)
     delta_chain_back_kernel(const __grid_constant__ Params p, const __grid_constant__ TcMaps m, TcBuffers buf) {
   extern __shared__ __align__(1024) uint8_t raw[];
   BackSmem<KB>& sm = *reinterpret_cast<BackSmem<KB>*>(raw);
@@ -61,18 +60,17 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.kdy_full[s], 1);
       mbar_init(&sm.kdy_empty[s], 1);
-      mbar_init(&sm.g_ready[s], 4);
     }
+    for (uint64_t* four : {&sm.g_ready[0], &sm.g_ready[1], &sm.g_ready[2], &sm.g_ready[3], &sm.r_free, &sm.dys_ready})
+      mbar_init(four, 4);
     for (uint64_t* one : {&sm.q_full, &sm.q_empty, &sm.t_full, &sm.t_empty, &sm.p_full, &sm.p_empty, &sm.y_full, &sm.r_full,
                           &sm.d_full, &sm.drain})
       mbar_init(one, 1);
-    mbar_init(&sm.u_ready, 8);
-    mbar_init(&sm.w_ready, 8);
-    mbar_init(&sm.r_free, 4);
-    mbar_init(&sm.dys_ready, 4);
+    mbar_init(&sm.u_ready, kStateWarps);
+    mbar_init(&sm.w_ready, kStateWarps);
     fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == 20) {
     tmem_alloc(&sm.tmem, 512);
     tmem_relinquish();
   }
@@ -82,7 +80,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   const uint32_t tmem = sm.tmem;
   const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
   // n counts chunks done, c is the chunk: nch - 1 - n
-  if (warp == 13) {   // loads
+  if (warp == 21) {   // loads
     int pairs = 0, ps = 0, ts = 0, qs = 0;   // loads issued
     for (int n = 0; n < nch; ++n) {
       const int s = n & 1, c = nch - 1 - n;
@@ -122,7 +120,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     if (ts > 0) drained &= mbar_wait_bounded(&sm.t_full, (ts - 1) & 1, 2000000000ull);
     if (qs > 0) drained &= mbar_wait_bounded(&sm.q_full, (qs - 1) & 1, 2000000000ull);
     if (!drained && lane == 0) latch_error(p.hdr, SSD_ERR_TIMEOUT, 44);
-  } else if (warp == 12) {   // products
+  } else if (warp == 20) {   // products
     constexpr uint32_t id_k = idesc_bf16(128, 64, 0, 0), id_p = idesc_bf16(128, 64, 1, 1), id_t = idesc_bf16(128, 64, 0, 1);
     constexpr uint32_t id_q = idesc_bf16(128, Kp, 1, 1), id_d = idesc_bf16(128, Kp, 0, 1);
     const uint32_t p_lo = sdesc_sw128_lo(smem_u32(sm.p), 0), t_lo = sdesc_sw128_lo(smem_u32(sm.t), 0);
@@ -144,11 +142,11 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       mma_commit_elect(&sm.p_empty);
       // K G^T
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (!wait_bar(&sm.g_ready[half], par, abort, p.hdr, 47)) break;
+      for (int part = 0; part < 4; ++part) {
+        if (!wait_bar(&sm.g_ready[part], par, abort, p.hdr, 47)) break;
         tc_fence_after();
 #pragma unroll
-        for (int ks = half * KB * 2; ks < (half + 1) * KB * 2; ++ks) {
+        for (int ks = part * KB; ks < (part + 1) * KB; ++ks) {
           const uint32_t at = k_lo + (((ks >> 2) * kTileBytes + (ks & 3) * 32) >> 4);
           mma_ts_we(tmem + kColU, tmem + kColG + ks * 8, at, kDHi, id_k, ks > 0);
           mma_ts_we(tmem + kColU, tmem + kColG + Kp / 2 + ks * 8, at, kDHi, id_k, 1);
@@ -172,10 +170,10 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       tc_fence_after();
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
-        const uint32_t a = tmem + kColU + half_col(ks);
+        const uint32_t a = tmem + kColU + ks * 16;
         mma_ts_we(tmem + kColR, a, t_lo + ks * (2048 >> 4), kDHi, id_t, ks > 0);
         mma_ts_we(tmem + kColR, a, t_lo + kLo + ks * (2048 >> 4), kDHi, id_t, 1);
-        mma_ts_we(tmem + kColR, a + 16, t_lo + ks * (2048 >> 4), kDHi, id_t, 1);
+        mma_ts_we(tmem + kColR, a + 8, t_lo + ks * (2048 >> 4), kDHi, id_t, 1);
       }
       mma_commit_elect(&sm.r_full);
       mma_commit_elect(&sm.t_empty);
@@ -184,9 +182,9 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       tc_fence_after();
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
-        const uint32_t a = tmem + kColW + half_col(ks);
+        const uint32_t a = tmem + kColW + ks * 16;
         mma_ts_we(tmem + kColD, a, km_lo + ks * (2048 >> 4), kDHi, id_d, 1);
-        mma_ts_we(tmem + kColD, a + 16, km_lo + ks * (2048 >> 4), kDHi, id_d, 1);
+        mma_ts_we(tmem + kColD, a + 8, km_lo + ks * (2048 >> 4), kDHi, id_d, 1);
       }
       mma_commit_elect(&sm.d_full);
       mma_commit_elect(&sm.kdy_empty[s]);
@@ -196,14 +194,14 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       sm.keep = 1;
       latch_error(p.hdr, SSD_ERR_TIMEOUT, 54);
     }
-  } else if (warp < 8) {   // G; a thread has a value and half the keys
-    constexpr int KH = Kp / 2;
-    const int half = warp >> 2, row = (warp & 3) * 32 + lane, k0 = half * KH;
+  } else if (warp < kStateWarps) {   // G
+    constexpr int KQ = Kp / 4;
+    const int part = warp >> 2, row = (warp & 3) * 32 + lane, k0 = part * KQ, j0 = part * 16;
     const bool live = row < p.V;
     const int64_t at = (((int64_t)b * p.H + h) * p.V + row) * p.K + k0;
-    float G[KH];
+    float G[KQ];
 #pragma unroll
-    for (int k = 0; k < KH; ++k) G[k] = p.dfinal && live && k0 + k < p.K ? p.dfinal[at + k] : 0.f;
+    for (int k = 0; k < KQ; ++k) G[k] = p.dfinal && live && k0 + k < p.K ? p.dfinal[at + k] : 0.f;
     for (int n = 0; n < nch; ++n) {
       const int s = n & 1, c = nch - 1 - n;
       const uint32_t par = n & 1;
@@ -213,48 +211,48 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.g_ready[half]);
+      if (lane == 0) mbar_arrive(&sm.g_ready[part]);
       const int cell = (b * nch + c) * (int)p.H + h;
-      send_state(sm.s[half], &m.states, G, half, 0, 0, cell, p.K);
+      send_state(sm.s[part], &m.states, G, part, 0, 0, cell, p.K);
       if (!wait_bar(&sm.kdy_full[s], (n >> 1) & 1, abort, p.hdr, 55)) break;   // the decays
       const float all = from[kChunk - 1];
       if (!wait_bar(&sm.y_full, par, abort, p.hdr, 56)) break;
       tc_fence_after();
-      float x[32], y[32];
-      tmem_ld32(tmem + lanes + kColY + half * 32, y);
-      tmem_ld32(tmem + lanes + kColU + half * 32, x);
+      float x[16], y[16];
+      tmem_ld16(tmem + lanes + kColY + j0, y);
+      tmem_ld16(tmem + lanes + kColU + j0, x);
       tmem_ld_wait();
       reg_tie(x);
       reg_tie(y);
 #pragma unroll
-      for (int j = 0; j < 32; j += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(&to[half * 32 + j]);
+      for (int j = 0; j < 16; j += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(&to[j0 + j]);
         x[j] = fmaf(x[j], f.x, y[j]);
         x[j + 1] = fmaf(x[j + 1], f.y, y[j + 1]);
         x[j + 2] = fmaf(x[j + 2], f.z, y[j + 2]);
         x[j + 3] = fmaf(x[j + 3], f.w, y[j + 3]);
       }
-      store_half(tmem + lanes + kColU + half * 32, x);
+      store_terms(tmem + lanes + kColU + j0, x);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.u_ready);
-      if constexpr (KB == 2) send_state(sm.s[half], &m.states, G, half, KH / 2, 0, cell, p.K);
+      if constexpr (KB == 2) send_state(sm.s[part], &m.states, G, part, KQ / 2, 0, cell, p.K);
       if (!wait_bar(&sm.r_full, par, abort, p.hdr, 57)) break;
       tc_fence_after();
-      tmem_ld32(tmem + lanes + kColR + half * 32, x);
+      tmem_ld16(tmem + lanes + kColR + j0, x);
       tmem_ld_wait();
       reg_tie(x);
 #pragma unroll
-      for (int j = 0; j < 32; j += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(&from[half * 32 + j]);
-        const float4 g = *reinterpret_cast<const float4*>(&beta[half * 32 + j]);
+      for (int j = 0; j < 16; j += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(&from[j0 + j]);
+        const float4 g = *reinterpret_cast<const float4*>(&beta[j0 + j]);
         x[j] *= -f.x * g.x;
         x[j + 1] *= -f.y * g.y;
         x[j + 2] *= -f.z * g.z;
         x[j + 3] *= -f.w * g.w;
       }
-      store_half(tmem + lanes + kColW + half * 32, x);
+      store_terms(tmem + lanes + kColW + j0, x);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -262,23 +260,23 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       if (!wait_bar(&sm.d_full, par, abort, p.hdr, 58)) break;
       tc_fence_after();
 #pragma unroll
-      for (int k = 0; k < KH; k += 32) {
-        tmem_ld32(tmem + lanes + kColD + k0 + k, x);
+      for (int k = 0; k < KQ; k += 16) {
+        tmem_ld16(tmem + lanes + kColD + k0 + k, x);
         tmem_ld_wait();
         reg_tie(x);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) G[k + j] = fmaf(all, G[k + j], x[j]);
+        for (int j = 0; j < 16; ++j) G[k + j] = fmaf(all, G[k + j], x[j]);
       }
     }
     if ((threadIdx.x & 127) == 0) bulk_wait_group<0>();
     if (p.dinit && live && !*abort) {
       const bool wide = (reinterpret_cast<uintptr_t>(p.dinit) & 31) == 0;
 #pragma unroll
-      for (int k = 0; k < KH; k += 8)
+      for (int k = 0; k < KQ; k += 8)
         if (k0 + k < p.K) store8(p.dinit + at + k, G + k, wide);
     }
   } else {   // scale D dY in two terms, and dR on its way out
-    const int t = threadIdx.x - 256, v = (warp & 3) * 32 + lane;
+    const int t = threadIdx.x - kStateWarps * 32, v = (warp & 3) * 32 + lane;
     for (int n = 0; n < nch; ++n) {
       const int s = n & 1, c = nch - 1 - n;
       const uint32_t par = n & 1;
@@ -312,7 +310,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.r_free);
-      if (warp == 8 && lane == 0) bulk_wait_group_read<0>();
+      if (warp == kStateWarps && lane == 0) bulk_wait_group_read<0>();
       named_barrier(1, 128);
       uint8_t* out = sm.r + (v >> 6) * 2 * kTileBytes;
 #pragma unroll
@@ -325,7 +323,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       }
       fence_proxy_async_smem();
       named_barrier(1, 128);
-      if (warp == 8 && lane == 0) {
+      if (warp == kStateWarps && lane == 0) {
         const int64_t cell = ((int64_t)b * nch + c) * p.H + h;
         asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(buf.writes + cell * 4 * kTileBytes),
                      "r"(smem_u32(sm.r)), "r"(4 * kTileBytes)
@@ -333,11 +331,11 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         bulk_commit_group();
       }
     }
-    if (warp == 8 && lane == 0) bulk_wait_group<0>();
+    if (warp == kStateWarps && lane == 0) bulk_wait_group<0>();
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12 && !sm.keep) {
+  if (warp == 20 && !sm.keep) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -864,7 +862,7 @@ cudaError_t walk_as(const Params& p, const TcMaps& m, const TcBuffers& buf, cuda
   static_assert(smem <= 232448, "shared memory of a block");
   const cudaError_t e = cudaFuncSetAttribute(delta_chain_back_kernel<KB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  delta_chain_back_kernel<KB><<<(unsigned)(p.batch * p.H), kChainThreads, smem, st>>>(p, m, buf);
+  delta_chain_back_kernel<KB><<<(unsigned)(p.batch * p.H), kWalkThreads, smem, st>>>(p, m, buf);
   return cudaGetLastError();
 }
 

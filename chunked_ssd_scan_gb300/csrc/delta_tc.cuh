@@ -82,50 +82,60 @@ __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// 8 consecutive columns of TMEM.
+__device__ __forceinline__ void tmem_st8u(uint32_t at, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 constexpr uint32_t kDHi = sdesc_sw128_hi(1024);
 constexpr uint32_t kLo = kTileBytes >> 4;   // from a square's hi to its lo, in a descriptor's units
 
-// Column of the k-step `ks` (16 steps of the chunk) of an operand kept in halves of 32 columns; lo is 16 further.
-__device__ __forceinline__ uint32_t half_col(int ks) { return (uint32_t)((ks >> 1) * 32 + (ks & 1) * 8); }
-
-// Two terms of 32 columns, written over the 32 columns' place: hi in the first 16, lo in the others.
-__device__ __forceinline__ void store_half(uint32_t at, const float (&v)[32]) {
-  uint32_t hi[16], lo[16];
+// Two terms of 16 columns, written over the 16 columns' place: hi in the first 8, lo in the others; as an operand this is
+// one k-step of hi and one of lo.
+__device__ __forceinline__ void store_terms(uint32_t at, const float (&v)[16]) {
+  uint32_t u[16];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) split2(v[2 * j], v[2 * j + 1], hi[j], lo[j]);
-  tmem_st16u(at, hi);
-  tmem_st16u(at + 16, lo);
+  for (int j = 0; j < 8; ++j) split2(v[2 * j], v[2 * j + 1], u[j], u[8 + j]);
+  tmem_st16u(at, u);
 }
 
-// The terms of 32 NK keys of a state's row (a thread's), hi at `at` and lo `lo` columns further.
+// The walks' 16 state warps, four to each quarter of the lanes: a thread has a value's quarter of the keys, and 16 steps
+// of a chunk.  (Eight warps with halves: 2.44 us a chunk instead of CHUNKUS; what they do between two products is a
+// chain of latencies.)
+constexpr int kStateWarps = 16, kWalkThreads = 22 * 32;   // and four at the output, one for products, one for loads
+
+// The two terms of a thread's keys: hi at `at`, lo `lo` columns further.
 template <int N>
 __device__ __forceinline__ void store_state_terms(uint32_t at, uint32_t lo_at, const float (&S)[N]) {
 #pragma unroll
-  for (int k = 0; k < N; k += 32) {
-    uint32_t hi[16], lo[16];
+  for (int k = 0; k < N; k += 16) {
+    uint32_t hi[8], lo[8];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) split2(S[k + 2 * j], S[k + 2 * j + 1], hi[j], lo[j]);
-    tmem_st16u(at + k / 2, hi);
-    tmem_st16u(at + lo_at + k / 2, lo);
+    for (int j = 0; j < 8; ++j) split2(S[k + 2 * j], S[k + 2 * j + 1], hi[j], lo[j]);
+    tmem_st8u(at + k / 2, hi);
+    tmem_st8u(at + lo_at + k / 2, lo);
   }
 }
 
-// 32 of a thread's keys (from `first` of its half) of the state before a chunk, through shared memory: rows of 128 bytes,
-// swizzled, leave as one tile of `map`.  By the four warps of a half.  (Straight from the registers, 32 bytes of 32
-// rows an instruction, the forward walk took 4.7 us a chunk instead of 3.6.)
-template <int KH>
-__device__ __forceinline__ void send_state(uint8_t* to, const CUtensorMap* map, const float (&S)[KH], int half, int first,
+// 16 of a thread's keys (from `first` of its quarter) of the state at a chunk's border, through shared memory: rows of 64
+// bytes, swizzled, leave as one tile of `map`.  By the four warps of a quarter of the keys.  (Straight from the
+// registers, 32 bytes of 32 rows an instruction, the forward walk took a third longer.)
+template <int KQ>
+__device__ __forceinline__ void send_state(uint8_t* to, const CUtensorMap* map, const float (&S)[KQ], int quarter, int first,
                                            int v0, int cell, int64_t K) {
   const int t = threadIdx.x & 127;
   if (t == 0) bulk_wait_group_read<0>();   // the tile before has left
-  named_barrier(2 + half, 128);
+  named_barrier(2 + quarter, 128);
 #pragma unroll
-  for (int k = 0; k < 32; k += 4)
-    *reinterpret_cast<float4*>(to + sw128_off32(t, k)) = make_float4(S[first + k], S[first + k + 1], S[first + k + 2], S[first + k + 3]);
+  for (int k = 0; k < 16; k += 4)
+    *reinterpret_cast<float4*>(to + t * 64 + (((k >> 2) ^ ((t >> 1) & 3)) << 4)) =
+        make_float4(S[first + k], S[first + k + 1], S[first + k + 2], S[first + k + 3]);
   fence_proxy_async_smem();
-  named_barrier(2 + half, 128);
-  if (t == 0 && half * KH + first < K) {
-    tma_store_4d(map, to, half * KH + first, v0, cell, 0);
+  named_barrier(2 + quarter, 128);
+  if (t == 0 && quarter * KQ + first < K) {
+    tma_store_4d(map, to, quarter * KQ + first, v0, cell, 0);
     bulk_commit_group();
   }
 }
