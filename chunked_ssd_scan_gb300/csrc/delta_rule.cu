@@ -566,7 +566,7 @@ Layout layout(const gated_delta_rule_shape* s, bool back) {
   size_t at = sizeof(WsHeader);
   const size_t nch = (size_t)((s->seqlen + kChunk - 1) / kChunk);
   L.chunks = at;
-  if (tc_shape(s)) at = align_up(at + tc_bytes(s->batch, (int64_t)nch, s->heads, back), kWsAlign);
+  if (tc_shape(s)) at = align_up(at + tc_bytes(s->batch, (int64_t)nch, s->heads, s->value_dim, s->key_dim, back), kWsAlign);
   if (back) {
     const size_t steps = (size_t)(s->batch * s->seqlen * s->heads * s->value_dim) * 4;
     const size_t states = (size_t)s->batch * nch * (size_t)(s->heads * s->value_dim * s->key_dim) * 4;

@@ -303,15 +303,22 @@ struct ChainSmem {
   int abort, keep;
 };
 
-template <int KB>
+// kY: with the outputs; without them Q, P and the products with them are left out.
+template <int KB, bool kY>
 __global__ void __launch_bounds__(kWalkThreads, 1)
-    delta_chain_kernel(const __grid_constant__ Params p, const __grid_constant__ TcMaps m, TcBuffers buf, int vtiles) {
+    delta_chain_kernel(const __grid_constant__ Params p, const __grid_constant__ TcMaps m, TcBuffers buf, int vtiles,
+                       Segments seg) {
   extern __shared__ __align__(1024) uint8_t raw[];
   ChainSmem<KB>& sm = *reinterpret_cast<ChainSmem<KB>*>(raw);
   ChainBars& bar = sm.bar;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x / 32), 0), lane = threadIdx.x % 32;
-  const int vtile = blockIdx.x % vtiles, h = (blockIdx.x / vtiles) % (int)p.H, b = blockIdx.x / vtiles / (int)p.H;
-  const int hk = h / (int)(p.H / p.Hk), v0 = vtile * 128, nch = (int)p.nch;
+  const int real = seg.pre ? seg.n - 1 : seg.n;   // segments with values of a sequence
+  const int per = real * vtiles + (seg.pre ? seg.n - 2 : 0), seq = blockIdx.x / per, job = blockIdx.x % per;
+  const bool identity = job >= real * vtiles;
+  const int part_of = identity ? 1 + job - real * vtiles : job / vtiles, v0 = identity ? 0 : job % vtiles * 128;
+  const int h = seq % (int)p.H, b = seq / (int)p.H, hk = h / (int)(p.H / p.Hk);
+  const int first = part_of * seg.chunks, all_chunks = (int)p.nch, nch = min(seg.chunks, all_chunks - first);
+  const int64_t seg_at = (int64_t)seq * seg.n + part_of;
   constexpr int Kp = KB * 64;
   volatile int* abort = &sm.abort;
   if (threadIdx.x == 0) {
@@ -342,16 +349,19 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       const int s = c & 1;
       if (c >= 2 && !wait_bar(&bar.empty[s], ((c >> 1) - 1) & 1, abort, p.hdr, 10)) break;
       Stage<KB>& st = sm.st[s];
-      const int64_t cell = ((int64_t)b * nch + c) * p.H + h;
-      mbar_arrive_expect_tx_elect(&bar.full[s], (2 * KB + 6) * kTileBytes + kDecayBytes);
+      const int64_t cell = ((int64_t)b * all_chunks + first + c) * p.H + h;
+      const int t0 = (first + c) * kChunk;
+      mbar_arrive_expect_tx_elect(&bar.full[s], ((kY ? 2 * KB + 4 : KB + 2) + (identity ? 0 : 2)) * kTileBytes + kDecayBytes);
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
-        tma_load_4d_elect(st.k + kb * kTileBytes, &m.k, &bar.full[s], kb * 64, c * kChunk, hk, b);
-        tma_load_4d_elect(st.q + kb * kTileBytes, &m.q, &bar.full[s], kb * 64, c * kChunk, hk, b);
+        tma_load_4d_elect(st.k + kb * kTileBytes, &m.k, &bar.full[s], kb * 64, t0, hk, b);
+        if (kY) tma_load_4d_elect(st.q + kb * kTileBytes, &m.q, &bar.full[s], kb * 64, t0, hk, b);
       }
-      tma_load_4d_elect(st.v, &m.v, &bar.full[s], v0, c * kChunk, h, b);
-      tma_load_4d_elect(st.v + kTileBytes, &m.v, &bar.full[s], v0 + 64, c * kChunk, h, b);
-      bulk_load_elect(st.t, buf.squares + cell * buf.square, 4 * kTileBytes, &bar.full[s]);
+      if (!identity) {
+        tma_load_4d_elect(st.v, &m.v, &bar.full[s], v0, t0, h, b);
+        tma_load_4d_elect(st.v + kTileBytes, &m.v, &bar.full[s], v0 + 64, t0, h, b);
+      }
+      bulk_load_elect(st.t, buf.squares + cell * buf.square, (kY ? 4 : 2) * kTileBytes, &bar.full[s]);
       bulk_load_elect(st.from, buf.decays + cell * 3 * kChunk, kDecayBytes, &bar.full[s]);
       issued = c + 1;
     }
@@ -386,23 +396,25 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       if (*abort) break;
       mma_commit_elect(&bar.x_full);
       // U = V T^T - (D X) T^T
-      if (c > 0 && !wait_bar(&bar.o2_full, (c - 1) & 1, abort, p.hdr, 14)) break;   // U's terms have been read
+      if (kY && c > 0 && !wait_bar(&bar.o2_full, (c - 1) & 1, abort, p.hdr, 14)) break;   // U's terms have been read
+      if (!identity) {
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        mma_ss_we(tmem + kColU, v_lo + ks * (2048 >> 4), kDHi, t_lo + ks * 2, kDHi, id_v, ks > 0);
-        mma_ss_we(tmem + kColU, v_lo + ks * (2048 >> 4), kDHi, t_lo + kLo + ks * 2, kDHi, id_v, 1);
+        for (int ks = 0; ks < 4; ++ks) {
+          mma_ss_we(tmem + kColU, v_lo + ks * (2048 >> 4), kDHi, t_lo + ks * 2, kDHi, id_v, ks > 0);
+          mma_ss_we(tmem + kColU, v_lo + ks * (2048 >> 4), kDHi, t_lo + kLo + ks * 2, kDHi, id_v, 1);
+        }
       }
       if (!wait_bar(&bar.r_ready, par, abort, p.hdr, 15)) break;
       tc_fence_after();
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
         const uint32_t a = tmem + kColX + ks * 16;
-        mma_ts_we(tmem + kColU, a, t_lo + ks * 2, kDHi, id_k, 1);
+        mma_ts_we(tmem + kColU, a, t_lo + ks * 2, kDHi, id_k, ks > 0 || !identity);
         mma_ts_we(tmem + kColU, a, t_lo + kLo + ks * 2, kDHi, id_k, 1);
         mma_ts_we(tmem + kColU, a + 8, t_lo + ks * 2, kDHi, id_k, 1);
       }
       mma_commit_elect(&bar.u_full);
-      // S Q^T, while U is turned into operands
+      if constexpr (kY) {   // S Q^T, while U is turned into operands
       if (c > 0 && !wait_bar(&bar.o_free, (c - 1) & 1, abort, p.hdr, 16)) break;
       tc_fence_after();
 #pragma unroll
@@ -412,6 +424,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         mma_ts_we(tmem + kColO, tmem + kColS + Kp / 2 + ks * 8, at, kDHi, id_k, 1);
       }
       mma_commit_elect(&bar.o1_full);
+      }
       // (E U)^T K
       if (!wait_bar(&bar.w_ready, par, abort, p.hdr, 17)) break;
       tc_fence_after();
@@ -422,7 +435,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         mma_ts_we(tmem + kColD, a + 8, km_lo + ks * (2048 >> 4), kDHi, id_d, 1);
       }
       mma_commit_elect(&bar.d_full);
-      // y = scale D S Q^T + U P^T
+      if constexpr (kY) {   // y = scale D S Q^T + U P^T
       if (!wait_bar(&bar.u_ready, par, abort, p.hdr, 18)) break;
       if (!wait_bar(&bar.o_scaled, par, abort, p.hdr, 19)) break;
       tc_fence_after();
@@ -434,6 +447,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         mma_ts_we(tmem + kColO, a + 8, p_lo + ks * 2, kDHi, id_k, 1);
       }
       mma_commit_elect(&bar.o2_full);
+      }
       mma_commit_elect(&bar.empty[s]);
     }
     mma_commit_elect(&bar.drain);
@@ -444,11 +458,13 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
   } else if (warp < kStateWarps) {   // the state, and the operands on the way to the next one
     constexpr int KQ = Kp / 4;
     const int part = warp >> 2, row = v0 + (warp & 3) * 32 + lane, k0 = part * KQ, j0 = part * 16;
-    const bool live = row < p.V;
-    const int64_t at = (((int64_t)b * p.H + h) * p.V + row) * p.K + k0;
+    const bool live = row < (identity ? p.K : p.V);
+    const int64_t at = (int64_t)row * p.K + k0, KV = p.K * p.V;
+    const float* init = identity ? nullptr : part_of == 0 ? (p.init ? p.init + seq * KV : nullptr)
+                        : seg.pre ? nullptr : seg.start + seg_at * KV;
     float S[KQ];
 #pragma unroll
-    for (int k = 0; k < KQ; ++k) S[k] = p.init && live && k0 + k < p.K ? p.init[at + k] : 0.f;
+    for (int k = 0; k < KQ; ++k) S[k] = init && live && k0 + k < p.K ? init[at + k] : identity && row == k0 + k ? 1.f : 0.f;
     for (int c = 0; c < nch; ++c) {
       const int s = c & 1;
       const uint32_t par = c & 1;
@@ -458,8 +474,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.s_ready[part]);
-      const int cell = (b * nch + c) * (int)p.H + h;
-      if (p.states_out) send_state(sm.s[part], &m.states, S, part, 0, v0, cell, p.K);
+      const int cell = (b * all_chunks + first + c) * (int)p.H + h;
+      const bool keep = p.states_out && !seg.pre;
+      if (keep) send_state(sm.s[part], &m.states, S, part, 0, v0, cell, p.K);
       if (!wait_bar(&bar.full[s], (c >> 1) & 1, abort, p.hdr, 21)) break;   // the decays
       const float all = st.from[kChunk - 1];
       if (!wait_bar(&bar.x_full, par, abort, p.hdr, 22)) break;
@@ -482,7 +499,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.r_ready);
       if constexpr (KB == 2)
-        if (p.states_out) send_state(sm.s[part], &m.states, S, part, KQ / 2, v0, cell, p.K);
+        if (keep) send_state(sm.s[part], &m.states, S, part, KQ / 2, v0, cell, p.K);
       if (!wait_bar(&bar.u_full, par, abort, p.hdr, 23)) break;
       tc_fence_after();
       tmem_ld16(tmem + lanes + kColU + j0, x);
@@ -502,11 +519,13 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.w_ready);
-      store_terms(tmem + lanes + kColU + j0, x);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.u_ready);
+      if constexpr (kY) {
+        store_terms(tmem + lanes + kColU + j0, x);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.u_ready);
+      }
       if (!wait_bar(&bar.d_full, par, abort, p.hdr, 24)) break;
       tc_fence_after();
 #pragma unroll
@@ -519,13 +538,15 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       }
     }
     if ((threadIdx.x & 127) == 0) bulk_wait_group<0>();
-    if (p.final_state && live && !*abort) {
-      const bool wide = (reinterpret_cast<uintptr_t>(p.final_state) & 31) == 0;
+    float* end = seg.pre ? (identity ? seg.map + seg_at * p.K * p.K : seg.end + seg_at * KV)
+                 : part_of == seg.n - 1 && p.final_state ? p.final_state + seq * KV : nullptr;
+    if (end && live && !*abort) {
+      const bool wide = (reinterpret_cast<uintptr_t>(end) & 31) == 0;
 #pragma unroll
       for (int k = 0; k < KQ; k += 8)
-        if (k0 + k < p.K) store8(p.final_state + at + k, S + k, wide);
+        if (k0 + k < p.K) store8(end + at + k, S + k, wide);
     }
-  } else {   // y: a thread has a value
+  } else if constexpr (kY) {   // y: a thread has a value
     const int v = (warp & 3) * 32 + lane;
     uint8_t* column = sm.y + (v >> 6) * kTileBytes;
     for (int c = 0; c < nch; ++c) {
@@ -578,8 +599,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         fence_proxy_async_smem();
         named_barrier(1, 128);
         if (warp == kStateWarps && lane == 0) {
-          tma_store_4d(&m.y, sm.y, v0, c * kChunk, h, b);
-          if (v0 + 64 < p.V) tma_store_4d(&m.y, sm.y + kTileBytes, v0 + 64, c * kChunk, h, b);
+          tma_store_4d(&m.y, sm.y, v0, (first + c) * kChunk, h, b);
+          if (v0 + 64 < p.V) tma_store_4d(&m.y, sm.y + kTileBytes, v0 + 64, (first + c) * kChunk, h, b);
           bulk_commit_group();
         }
       }
@@ -594,7 +615,65 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
   }
 }
 
+// The state before every segment: 16 rows of a sequence a block, a thread a key.
+__global__ void __launch_bounds__(128) delta_carry_kernel(const __grid_constant__ Params p, Segments seg, int tiles) {
+  __shared__ float row[2][16][128];
+  const int seq = blockIdx.x / tiles, v0 = blockIdx.x % tiles * 16, k = threadIdx.x;
+  const int64_t KV = p.K * p.V, at = (int64_t)seq * seg.n;
+  const bool in = k < p.K;
+  float s[16];
+#pragma unroll
+  for (int r = 0; r < 16; ++r) s[r] = in && v0 + r < p.V ? seg.end[at * KV + (v0 + r) * p.K + k] : 0.f;
+  for (int i = 1; i < seg.n; ++i) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      row[i & 1][r][k] = s[r];
+      if (in && v0 + r < p.V) seg.start[(at + i) * KV + (v0 + r) * p.K + k] = s[r];
+    }
+    if (i + 1 == seg.n) break;
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[r] = in && v0 + r < p.V ? seg.end[(at + i) * KV + (v0 + r) * p.K + k] : 0.f;
+    const float* map = seg.map + (at + i) * p.K * p.K;
+    for (int j = 0; in && j < p.K; j += 8) {   // K is a multiple of 8
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = map[(j + e) * p.K + k];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[r] = fmaf(row[i & 1][r][j + e], f[e], s[r]);
+    }
+  }
+}
+
 // ------------------------------------------------------------------------------------------------ host
+constexpr int kSms = 152, kMostSegments = 16;
+
+// Segments of a sequence, by what the passes take: a chunk 2.25 us with outputs, 1.9 us without, blocks in rounds of one
+// an SM, a segment's carry 4 us.  (1 x 32768 x 16 heads: LONG1 us in one segment, LONGN us in SEGN.)
+int segments_for(int64_t batch, int64_t nch, int64_t H, int64_t V) {
+  const int64_t vtiles = (V + 127) / 128, seqs = batch * H;
+  int best = 1;
+  double least = 0;
+  for (int n = 1; n <= kMostSegments && (n == 1 || seqs * vtiles * n <= 2 * kSms); ++n) {
+    const int64_t len = (nch + n - 1) / n;
+    if ((n - 1) * len >= nch) continue;   // the last one would be empty
+    auto rounds = [](int64_t blocks) { return (double)((blocks + kSms - 1) / kSms); };
+    double us = rounds(seqs * vtiles * n) * len * 2.25;
+    if (n > 1) us += rounds(seqs * ((n - 1) * vtiles + n - 2)) * len * 1.9 + 4.0 * n + 10;
+    if (n == 1 || us < 0.9 * least) {
+      best = n;
+      least = us;
+    }
+  }
+  return best;
+}
+size_t segment_bytes(int64_t batch, int64_t nch, int64_t H, int64_t V, int64_t K) {
+  const int n = segments_for(batch, nch, H, V);
+  return n == 1 ? 0 : (size_t)(batch * H * n) * (size_t)(2 * V * K + K * K) * 4;
+}
+
 bool rows_fit(const void* base, const int64_t* stride, int64_t batch, int64_t T, int64_t heads) {
   if (reinterpret_cast<uintptr_t>(base) % 16 != 0) return false;
   const int64_t n[3] = {batch, T, heads};
@@ -612,15 +691,39 @@ cudaError_t chunks_as(const Params& p, const TcMaps& m, const TcBuffers& buf, cu
   return cudaGetLastError();
 }
 
-template <int KB>
-cudaError_t chain_as(const Params& p, const TcMaps& m, const TcBuffers& buf, cudaStream_t st) {
+template <int KB, bool kY>
+cudaError_t walk_as(const Params& p, const TcMaps& m, const TcBuffers& buf, const Segments& seg, cudaStream_t st) {
   constexpr int smem = sizeof(ChainSmem<KB>);
   static_assert(smem <= 232448, "shared memory of a block");
-  const cudaError_t e = cudaFuncSetAttribute(delta_chain_kernel<KB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const auto kernel = delta_chain_kernel<KB, kY>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int vtiles = (int)((p.V + 127) / 128);
-  delta_chain_kernel<KB><<<(unsigned)(p.batch * p.H * vtiles), kWalkThreads, smem, st>>>(p, m, buf, vtiles);
+  const int vtiles = (int)((p.V + 127) / 128), per = seg.pre ? (seg.n - 1) * vtiles + seg.n - 2 : seg.n * vtiles;
+  kernel<<<(unsigned)(p.batch * p.H * per), kWalkThreads, smem, st>>>(p, m, buf, vtiles, seg);
   return cudaGetLastError();
+}
+
+template <int KB>
+cudaError_t chain_as(const Params& p, const TcMaps& m, const TcBuffers& buf, float* segments, cudaStream_t st) {
+  Segments seg;
+  memset(&seg, 0, sizeof(seg));
+  seg.n = segments_for(p.batch, p.nch, p.H, p.V);
+  seg.chunks = (int)((p.nch + seg.n - 1) / seg.n);
+  if (seg.n > 1) {
+    const int64_t states = p.batch * p.H * seg.n * p.V * p.K;
+    seg.start = segments;
+    seg.end = segments + states;
+    seg.map = segments + 2 * states;
+    seg.pre = 1;
+    cudaError_t e = walk_as<KB, false>(p, m, buf, seg, st);
+    if (e != cudaSuccess) return e;
+    seg.pre = 0;
+    const int tiles = (int)((p.V + 15) / 16);
+    delta_carry_kernel<<<(unsigned)(p.batch * p.H * tiles), 128, 0, st>>>(p, seg, tiles);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return p.y ? walk_as<KB, true>(p, m, buf, seg, st) : walk_as<KB, false>(p, m, buf, seg, st);
 }
 
 TcBuffers buffers_in(void* at, const Params& p, bool backward) {
@@ -631,6 +734,9 @@ TcBuffers buffers_in(void* at, const Params& p, bool backward) {
   buf.decays = reinterpret_cast<float*>(buf.squares + cells * buf.square);
   buf.writes = reinterpret_cast<uint8_t*>(buf.decays) + align_up(cells * kDecayBytes, kWsAlign);
   return buf;
+}
+float* segments_in(const TcBuffers& buf, const Params& p, bool backward) {
+  return reinterpret_cast<float*>(buf.writes + (backward ? (size_t)(p.batch * p.nch * p.H) * 4 * kTileBytes : 0));
 }
 
 }  // namespace
@@ -666,9 +772,10 @@ bool state_map(CUtensorMap* m, const void* base, int64_t cells, int64_t V, int64
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-size_t tc_bytes(int64_t batch, int64_t nch, int64_t H, bool backward) {
+size_t tc_bytes(int64_t batch, int64_t nch, int64_t H, int64_t V, int64_t K, bool backward) {
   const size_t cells = (size_t)(batch * nch * H);
-  return cells * square_bytes(backward) + align_up(cells * kDecayBytes, kWsAlign) + (backward ? cells * 4 * kTileBytes : 0);
+  return cells * square_bytes(backward) + align_up(cells * kDecayBytes, kWsAlign) + (backward ? cells * 4 * kTileBytes : 0) +
+         segment_bytes(batch, nch, H, V, K);
 }
 
 bool tc_takes(const Params& p, bool backward) {
@@ -695,7 +802,8 @@ cudaError_t tc_forward(const Params& p, void* buffers, cudaStream_t st) {
   const TcBuffers buf = buffers_in(buffers, p, false);
   const cudaError_t e = p.K <= 64 ? chunks_as<1>(p, m, buf, st) : chunks_as<2>(p, m, buf, st);
   if (e != cudaSuccess) return e;
-  return p.K <= 64 ? chain_as<1>(p, m, buf, st) : chain_as<2>(p, m, buf, st);
+  float* segments = segments_in(buf, p, false);
+  return p.K <= 64 ? chain_as<1>(p, m, buf, segments, st) : chain_as<2>(p, m, buf, segments, st);
 }
 
 cudaError_t tc_backward(const Params& p, bool states_known, void* buffers, cudaStream_t st) {
@@ -715,7 +823,8 @@ cudaError_t tc_backward(const Params& p, bool states_known, void* buffers, cudaS
     f.final_state = nullptr;
     f.states_out = const_cast<float*>(p.states_in);
     if (!state_map(&m.states, f.states_out, cells, p.V, p.K)) return cudaErrorInvalidValue;
-    e = p.K <= 64 ? chain_as<1>(f, m, buf, st) : chain_as<2>(f, m, buf, st);
+    float* segments = segments_in(buf, p, true);
+    e = p.K <= 64 ? chain_as<1>(f, m, buf, segments, st) : chain_as<2>(f, m, buf, segments, st);
   }
   if (e != cudaSuccess) return e;
   if (!state_map(&m.states, p.dstates, cells, p.V, p.K)) return cudaErrorInvalidValue;

@@ -31,6 +31,15 @@ struct TcBuffers {
   uint32_t square;
 };
 
+// A sequence cut into segments that are walked at once, where there are fewer sequences than SMs.  A row s of the state
+// becomes s M + n over a segment: a first pass (pre) walks every segment but the last from zero (the first from the
+// initial state) for its n, and every one but the first and last from the rows of the identity, without values, for its M;
+// a carry makes of them the state before every segment, and the full pass starts there.
+struct Segments {
+  int n, chunks, pre;   // segments of a sequence, chunks of a segment (the last may have fewer)
+  float *start, *end, *map;   // [b*H*n][V][K]: states before and behind segments; [b*H*n][K][K]: M
+};
+
 constexpr long long kWaitCycles = 4000000000ll;   // a wait gives up after about 2 s
 
 static __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, WsHeader* hdr, int site) {
@@ -142,7 +151,7 @@ __device__ __forceinline__ void send_state(uint8_t* to, const CUtensorMap* map, 
 
 // Whether the tensor-core kernels take a call, its workspace, and the call itself (delta_rule_tc.cu).
 bool tc_takes(const Params& p, bool backward);
-size_t tc_bytes(int64_t batch, int64_t nch, int64_t H, bool backward);
+size_t tc_bytes(int64_t batch, int64_t nch, int64_t H, int64_t V, int64_t K, bool backward);
 cudaError_t tc_forward(const Params& p, void* buffers, cudaStream_t st);
 cudaError_t tc_backward(const Params& p, bool states_known, void* buffers, cudaStream_t st);   // fills states_in where not
 // The backward walk and the chunks' gradients (delta_rule_tc_back.cu).
