@@ -204,10 +204,11 @@ __global__ void __launch_bounds__(kPrepThreads, 6) delta_chunk_kernel(const __gr
       if (warp == 1) chunk_decay_warp(p, sm.c, b, t0, n, h, lane);
       __syncthreads();
     }
-    float* decays = buf.decays + cell * 3 * kChunk;
+    float* decays = buf.decays + cell * kDecays;
     if (threadIdx.x < kChunk) {
       decays[threadIdx.x] = sm.c.from[threadIdx.x];
       decays[2 * kChunk + threadIdx.x] = sm.c.beta[threadIdx.x];
+      decays[3 * kChunk + threadIdx.x] = sm.c.from[threadIdx.x] * p.scale;
     } else {
       decays[threadIdx.x] = sm.c.to[threadIdx.x - kChunk];
     }
@@ -286,8 +287,7 @@ constexpr uint32_t kColS = 0, kColX = 128, kColU = 192, kColW = 256, kColD = 320
 template <int KB>
 struct Stage {
   uint8_t k[KB * kTileBytes], q[KB * kTileBytes], v[2 * kTileBytes], t[2 * kTileBytes], p[2 * kTileBytes];
-  float from[kChunk], to[kChunk], beta[kChunk];
-  uint8_t pad[256];
+  float from[kChunk], to[kChunk], beta[kChunk], scaled[kChunk];
 };
 struct ChainBars {
   uint64_t full[2], empty[2], s_ready[4], x_full, r_ready, u_full, w_ready, u_ready, d_full, o1_full, o_scaled, o2_full,
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         tma_load_4d_elect(st.v + kTileBytes, &m.v, &bar.full[s], v0 + 64, t0, h, b);
       }
       bulk_load_elect(st.t, buf.squares + cell * buf.square, (kY ? 4 : 2) * kTileBytes, &bar.full[s]);
-      bulk_load_elect(st.from, buf.decays + cell * 3 * kChunk, kDecayBytes, &bar.full[s]);
+      bulk_load_elect(st.from, buf.decays + cell * kDecays, kDecayBytes, &bar.full[s]);
       issued = c + 1;
     }
     bool drained = true;   // nothing may still be written to this block's shared memory when it ends
@@ -465,7 +465,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     float S[KQ];
 #pragma unroll
     for (int k = 0; k < KQ; ++k) S[k] = init && live && k0 + k < p.K ? init[at + k] : identity && row == k0 + k ? 1.f : 0.f;
-    for (int c = 0; c < nch; ++c) {
+    const bool keep = p.states_out && !seg.pre;
+    int cell = (b * all_chunks + first) * (int)p.H + h;
+    for (int c = 0; c < nch; ++c, cell += (int)p.H) {
       const int s = c & 1;
       const uint32_t par = c & 1;
       const Stage<KB>& st = sm.st[s];
@@ -474,8 +476,6 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.s_ready[part]);
-      const int cell = (b * all_chunks + first + c) * (int)p.H + h;
-      const bool keep = p.states_out && !seg.pre;
       if (keep) send_state(sm.s[part], &m.states, S, part, 0, v0, cell, p.K);
       if (!wait_bar(&bar.full[s], (c >> 1) & 1, abort, p.hdr, 21)) break;   // the decays
       const float all = st.from[kChunk - 1];
@@ -505,16 +505,16 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       tmem_ld16(tmem + lanes + kColU + j0, x);
       tmem_ld_wait();
       reg_tie(x);
-      float w[16];
+      {
+        uint32_t u[16];
 #pragma unroll
-      for (int j = 0; j < 16; j += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(&st.to[j0 + j]);
-        w[j] = x[j] * f.x;
-        w[j + 1] = x[j + 1] * f.y;
-        w[j + 2] = x[j + 2] * f.z;
-        w[j + 3] = x[j + 3] * f.w;
+        for (int j = 0; j < 16; j += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&st.to[j0 + j]);
+          split2(x[j] * f.x, x[j + 1] * f.y, u[j / 2], u[8 + j / 2]);
+          split2(x[j + 2] * f.z, x[j + 3] * f.w, u[j / 2 + 1], u[8 + j / 2 + 1]);
+        }
+        tmem_st16u(tmem + lanes + kColW + j0, u);
       }
-      store_terms(tmem + lanes + kColW + j0, w);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -556,46 +556,46 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       if (!wait_bar(&bar.full[s], (c >> 1) & 1, abort, p.hdr, 25)) break;
       if (!wait_bar(&bar.o1_full, par, abort, p.hdr, 26)) break;
       tc_fence_after();
-      float o[32];
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        tmem_ld32(tmem + lanes + kColO + half * 32, o);
+      // 16 columns at a time: with more the kernel's 80 registers spill, and a reload from beyond the L1 stalls the walk
+#pragma unroll 1
+      for (int j0 = 0; j0 < kChunk; j0 += 16) {
+        float o[16];
+        tmem_ld16(tmem + lanes + kColO + j0, o);
         tmem_ld_wait();
         reg_tie(o);
-        uint32_t u[32];
+        uint32_t u[16];
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(&st.from[half * 32 + j]);
-          u[j] = __float_as_uint(o[j] * (f.x * p.scale));
-          u[j + 1] = __float_as_uint(o[j + 1] * (f.y * p.scale));
-          u[j + 2] = __float_as_uint(o[j + 2] * (f.z * p.scale));
-          u[j + 3] = __float_as_uint(o[j + 3] * (f.w * p.scale));
+        for (int j = 0; j < 16; j += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&st.scaled[j0 + j]);
+          u[j] = __float_as_uint(o[j] * f.x);
+          u[j + 1] = __float_as_uint(o[j + 1] * f.y);
+          u[j + 2] = __float_as_uint(o[j + 2] * f.z);
+          u[j + 3] = __float_as_uint(o[j + 3] * f.w);
         }
-        tmem_st32u(tmem + lanes + kColO + half * 32, u);
+        tmem_st16u(tmem + lanes + kColO + j0, u);
       }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.o_scaled);
+      if (warp == kStateWarps && lane == 0) bulk_wait_group_read<0>();   // the last chunk's rows have left
+      named_barrier(1, 128);
       if (!wait_bar(&bar.o2_full, par, abort, p.hdr, 27)) break;
       tc_fence_after();
-      float o2[32];
-      tmem_ld32(tmem + lanes + kColO, o);
-      tmem_ld32(tmem + lanes + kColO + 32, o2);
-      tmem_ld_wait();
-      reg_tie(o);
-      reg_tie(o2);
+#pragma unroll 1
+      for (int j0 = 0; j0 < kChunk; j0 += 16) {
+        float o[16];
+        tmem_ld16(tmem + lanes + kColO + j0, o);
+        tmem_ld_wait();
+        reg_tie(o);
+#pragma unroll
+        for (int j = 0; j < 16; j += 2)
+          store_pair(column + sw128_off16(j0 + j, v & 63), column + sw128_off16(j0 + j + 1, v & 63), o[j], o[j + 1]);
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.o_free);
-      if (p.y) {
-        if (warp == kStateWarps && lane == 0) bulk_wait_group_read<0>();   // the last chunk's rows have left
-        named_barrier(1, 128);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          *reinterpret_cast<__nv_bfloat16*>(column + sw128_off16(j, v & 63)) = __float2bfloat16_rn(o[j]);
-          *reinterpret_cast<__nv_bfloat16*>(column + sw128_off16(j + 32, v & 63)) = __float2bfloat16_rn(o2[j]);
-        }
+      {
         fence_proxy_async_smem();
         named_barrier(1, 128);
         if (warp == kStateWarps && lane == 0) {
@@ -635,14 +635,14 @@ __global__ void __launch_bounds__(128) delta_carry_kernel(const __grid_constant_
 #pragma unroll
     for (int r = 0; r < 16; ++r) s[r] = in && v0 + r < p.V ? seg.end[(at + i) * KV + (v0 + r) * p.K + k] : 0.f;
     const float* map = seg.map + (at + i) * p.K * p.K;
-    for (int j = 0; in && j < p.K; j += 8) {   // K is a multiple of 8
-      float f[8];
+    for (int j = 0; in && j < p.K; j += 32) {
+      float f[32];   // on their way at once
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = map[(j + e) * p.K + k];
+      for (int e = 0; e < 32; ++e) f[e] = j + e < p.K ? map[(j + e) * p.K + k] : 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
+      for (int e = 0; e < 32; ++e)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[r] = fmaf(row[i & 1][r][j + e], f[e], s[r]);
+        for (int r = 0; r < 16; ++r) s[r] = fmaf(row[i & 1][r][(j + e) & 127], f[e], s[r]);
     }
   }
 }

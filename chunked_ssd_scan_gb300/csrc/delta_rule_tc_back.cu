@@ -39,7 +39,7 @@ struct BackSmem {
   uint8_t dys[2][2 * kTileBytes];   // scale D dY, hi and lo
   uint8_t r[4 * kTileBytes];        // dR on its way out: by 64 values, hi then lo
   uint8_t s[4][128 * 64];           // G on its way out
-  float decays[2][3 * kChunk];
+  float decays[2][kDecays];
   uint64_t kdy_full[2], kdy_empty[2], q_full, q_empty, t_full, t_empty, p_full, p_empty;
   uint64_t g_ready[4], y_full, u_ready, r_full, w_ready, r_free, dys_ready, d_full, drain;
   uint32_t tmem;
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       const uint8_t* sq = buf.squares + cell * buf.square;
       if (n >= 2 && !wait_bar(&sm.kdy_empty[s], ((n >> 1) - 1) & 1, abort, p.hdr, 40)) break;
       mbar_arrive_expect_tx_elect(&sm.kdy_full[s], (KB + 2) * kTileBytes + kDecayBytes);
-      bulk_load_elect(sm.decays[s], buf.decays + cell * 3 * kChunk, kDecayBytes, &sm.kdy_full[s]);
+      bulk_load_elect(sm.decays[s], buf.decays + cell * kDecays, kDecayBytes, &sm.kdy_full[s]);
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb)
         tma_load_4d_elect(sm.k[s] + kb * kTileBytes, &m.k, &sm.kdy_full[s], kb * 64, c * kChunk, hk, b);
@@ -202,20 +202,18 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     float G[KQ];
 #pragma unroll
     for (int k = 0; k < KQ; ++k) G[k] = p.dfinal && live && k0 + k < p.K ? p.dfinal[at + k] : 0.f;
-    for (int n = 0; n < nch; ++n) {
-      const int s = n & 1, c = nch - 1 - n;
+    int cell = (b * nch + nch - 1) * (int)p.H + h;
+    for (int n = 0; n < nch; ++n, cell -= (int)p.H) {
+      const int s = n & 1;
       const uint32_t par = n & 1;
-      const float* from = sm.decays[s];
-      const float *to = from + kChunk, *beta = from + 2 * kChunk;
       store_state_terms(tmem + lanes + kColG + k0 / 2, Kp / 2, G);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.g_ready[part]);
-      const int cell = (b * nch + c) * (int)p.H + h;
       send_state(sm.s[part], &m.states, G, part, 0, 0, cell, p.K);
       if (!wait_bar(&sm.kdy_full[s], (n >> 1) & 1, abort, p.hdr, 55)) break;   // the decays
-      const float all = from[kChunk - 1];
+      const float all = sm.decays[s][kChunk - 1];
       if (!wait_bar(&sm.y_full, par, abort, p.hdr, 56)) break;
       tc_fence_after();
       float x[16], y[16];
@@ -226,7 +224,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       reg_tie(y);
 #pragma unroll
       for (int j = 0; j < 16; j += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(&to[j0 + j]);
+        const float4 f = *reinterpret_cast<const float4*>(&sm.decays[s][kChunk + j0 + j]);
         x[j] = fmaf(x[j], f.x, y[j]);
         x[j + 1] = fmaf(x[j + 1], f.y, y[j + 1]);
         x[j + 2] = fmaf(x[j + 2], f.z, y[j + 2]);
@@ -245,12 +243,19 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       reg_tie(x);
 #pragma unroll
       for (int j = 0; j < 16; j += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(&from[j0 + j]);
-        const float4 g = *reinterpret_cast<const float4*>(&beta[j0 + j]);
-        x[j] *= -f.x * g.x;
-        x[j + 1] *= -f.y * g.y;
-        x[j + 2] *= -f.z * g.z;
-        x[j + 3] *= -f.w * g.w;
+        const float4 f = *reinterpret_cast<const float4*>(&sm.decays[s][j0 + j]);
+        x[j] *= -f.x;
+        x[j + 1] *= -f.y;
+        x[j + 2] *= -f.z;
+        x[j + 3] *= -f.w;
+      }
+#pragma unroll
+      for (int j = 0; j < 16; j += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(&sm.decays[s][2 * kChunk + j0 + j]);
+        x[j] *= f.x;
+        x[j + 1] *= f.y;
+        x[j + 2] *= f.z;
+        x[j + 3] *= f.w;
       }
       store_terms(tmem + lanes + kColW + j0, x);
       tmem_st_wait();
@@ -282,12 +287,12 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       const uint32_t par = n & 1;
       if (!wait_bar(&sm.kdy_full[s], (n >> 1) & 1, abort, p.hdr, 59)) break;
       if (n > 0 && !wait_bar(&sm.d_full, (n - 1) & 1, abort, p.hdr, 60)) break;   // the last terms have been read
-#pragma unroll
+#pragma unroll 2
       for (int m8 = 0; m8 < 8; ++m8) {   // 16 bytes of a row
         const int at = m8 * 128 + t, blk = at >> 9, i = (at >> 3) & 63, col = (at & 7) * 8;
         const uint32_t off = blk * kTileBytes + sw128_off16(i, col);
         const uint4 d = *reinterpret_cast<const uint4*>(sm.dy[s] + off);
-        const float f = sm.decays[s][i] * p.scale;
+        const float f = sm.decays[s][3 * kChunk + i];
         uint4 hi, lo;
         split2(__uint_as_float(d.x << 16) * f, __uint_as_float(d.x & 0xffff0000u) * f, hi.x, lo.x);
         split2(__uint_as_float(d.y << 16) * f, __uint_as_float(d.y & 0xffff0000u) * f, hi.y, lo.y);
@@ -301,26 +306,22 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       if (lane == 0) mbar_arrive(&sm.dys_ready);
       if (!wait_bar(&sm.r_full, par, abort, p.hdr, 61)) break;
       tc_fence_after();
-      float r0[32], r1[32];
-      tmem_ld32(tmem + lanes + kColR, r0);
-      tmem_ld32(tmem + lanes + kColR + 32, r1);
-      tmem_ld_wait();
-      reg_tie(r0);
-      reg_tie(r1);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.r_free);
       if (warp == kStateWarps && lane == 0) bulk_wait_group_read<0>();
       named_barrier(1, 128);
       uint8_t* out = sm.r + (v >> 6) * 2 * kTileBytes;
+#pragma unroll 1
+      for (int j0 = 0; j0 < kChunk; j0 += 16) {
+        float r[16];
+        tmem_ld16(tmem + lanes + kColR + j0, r);
+        tmem_ld_wait();
+        reg_tie(r);
 #pragma unroll
-      for (int j = 0; j < 64; ++j) {
-        const float x = j < 32 ? r0[j & 31] : r1[j & 31];
-        const __nv_bfloat16 hi = __float2bfloat16_rn(x);
-        const uint32_t off = sw128_off16(j, v & 63);
-        *reinterpret_cast<__nv_bfloat16*>(out + off) = hi;
-        *reinterpret_cast<__nv_bfloat16*>(out + kTileBytes + off) = __float2bfloat16_rn(x - __bfloat162float(hi));
+        for (int j = 0; j < 16; j += 2)
+          store_pair_terms(out + sw128_off16(j0 + j, v & 63), out + sw128_off16(j0 + j + 1, v & 63), kTileBytes, r[j], r[j + 1]);
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.r_free);
       fence_proxy_async_smem();
       named_barrier(1, 128);
       if (warp == kStateWarps && lane == 0) {
@@ -616,12 +617,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       reg_tie(x);
       uint8_t* at = sm.u[row >> 6];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const __nv_bfloat16 hi = __float2bfloat16_rn(x[j]);
-        const uint32_t off = sw128_off16(c0 + j, row & 63);
-        *reinterpret_cast<__nv_bfloat16*>(at + off) = hi;
-        *reinterpret_cast<__nv_bfloat16*>(at + kTileBytes + off) = __float2bfloat16_rn(x[j] - __bfloat162float(hi));
-      }
+      for (int j = 0; j < 16; j += 2)
+        store_pair_terms(at + sw128_off16(c0 + j, row & 63), at + sw128_off16(c0 + j + 1, row & 63), kTileBytes, x[j], x[j + 1]);
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -672,12 +669,15 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       reg_tie(z);
       const float ch = sm.c.hi[i], cl = sm.c.lo[i], beta = sm.c.beta[i], by = lower ? -1.f : p.scale;
       const int last = lower ? i - 1 : i;
+      const bool plain = sm.c.plain;
+      const float mine_from = sm.c.from[i];
       uint8_t* to = lower ? sm.v + kTileBytes : sm.v;   // lo: in t, at the same place
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const int c = c0 + j;
         const float f = lower ? (x[j] + y[j]) + z[j] : x[j] + y[j];
-        x[j] = c <= last ? f * by * __expf((ch - sm.c.hi[c]) + (cl - sm.c.lo[c])) : 0.f;
+        const float decay = plain ? mine_from * sm.c.back[c] : __expf((ch - sm.c.hi[c]) + (cl - sm.c.lo[c]));
+        x[j] = c <= last ? f * by * decay : 0.f;
       }
 #pragma unroll
       for (int j = 0; j < 16; j += 8) {
@@ -825,10 +825,10 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     __syncthreads();
     uint8_t* to = sm.s[0] + (row >> 6) * kTileBytes;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const uint32_t off = sw128_off16(c0 + j, row & 63);
-      *reinterpret_cast<__nv_bfloat16*>(to + off) = __float2bfloat16_rn(dq[j]);
-      *reinterpret_cast<__nv_bfloat16*>(to + 2 * kTileBytes + off) = __float2bfloat16_rn(dk[j]);
+    for (int j = 0; j < 16; j += 2) {
+      uint8_t *first = to + sw128_off16(c0 + j, row & 63), *second = to + sw128_off16(c0 + j + 1, row & 63);
+      store_pair(first, second, dq[j], dq[j + 1]);
+      store_pair(first + 2 * kTileBytes, second + 2 * kTileBytes, dk[j], dk[j + 1]);
     }
     fence_proxy_async_smem();
     __syncthreads();

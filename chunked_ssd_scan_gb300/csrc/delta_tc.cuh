@@ -16,8 +16,9 @@ using namespace tc;
 // A square of chunk steps as the tensor core reads it: 64 rows of 64 bf16, 128-byte swizzled, hi term then lo.
 constexpr uint32_t kTileBytes = kChunk * kChunk * 2;
 // Of every chunk and head in the workspace: T = (I + A)^-1 diag(beta) hi and lo, P hi and lo, for the backward pass
-// (I + A)^-1 hi and lo; and e^(sum of g up to a step), e^(sum behind it), beta.
-constexpr uint32_t kDecayBytes = 3 * kChunk * 4;
+// (I + A)^-1 hi and lo; and e^(sum of g up to a step), e^(sum behind it), beta, the first times the output's scale.
+constexpr int kDecays = 4 * kChunk;
+constexpr uint32_t kDecayBytes = kDecays * 4;
 constexpr uint32_t square_bytes(bool backward) { return (backward ? 6 : 4) * kTileBytes; }
 
 struct TcMaps {
@@ -26,7 +27,7 @@ struct TcMaps {
 
 struct TcBuffers {
   uint8_t* squares;    // [b*nch*H][square]
-  float* decays;       // [b*nch*H][3][kChunk]
+  float* decays;       // [b*nch*H][4][kChunk]
   uint8_t* writes;     // backward: gradients of v - S k, [b*nch*H][2 blocks of 64 values][hi, lo][kTileBytes]
   uint32_t square;
 };
@@ -64,6 +65,23 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   hi = *reinterpret_cast<const uint32_t*>(&h);
   const __nv_bfloat162 l = __floats2bfloat162_rn(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
   lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
+// A pair of values as bf16 to two rows of a tile, two bytes each.  (Converted together: a single conversion takes four
+// times a pair's.)
+__device__ __forceinline__ void store_pair(uint8_t* first, uint8_t* second, float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  *reinterpret_cast<__nv_bfloat16*>(first) = __low2bfloat16(h);
+  *reinterpret_cast<__nv_bfloat16*>(second) = __high2bfloat16(h);
+}
+// Both terms: hi there, lo `lo` bytes further.
+__device__ __forceinline__ void store_pair_terms(uint8_t* first, uint8_t* second, uint32_t lo, float a, float b) {
+  uint32_t h, l;
+  split2(a, b, h, l);
+  *reinterpret_cast<uint16_t*>(first) = (uint16_t)h;
+  *reinterpret_cast<uint16_t*>(second) = (uint16_t)(h >> 16);
+  *reinterpret_cast<uint16_t*>(first + lo) = (uint16_t)l;
+  *reinterpret_cast<uint16_t*>(second + lo) = (uint16_t)(l >> 16);
 }
 
 // 1-D copy global -> shared by one elected lane; addresses and size are multiples of 16 bytes.
@@ -137,10 +155,12 @@ __device__ __forceinline__ void send_state(uint8_t* to, const CUtensorMap* map, 
   const int t = threadIdx.x & 127;
   if (t == 0) bulk_wait_group_read<0>();   // the tile before has left
   named_barrier(2 + quarter, 128);
+  const uint32_t at = smem_u32(to) + t * 64 + (((t >> 1) & 3) << 4);
 #pragma unroll
   for (int k = 0; k < 16; k += 4)
-    *reinterpret_cast<float4*>(to + t * 64 + (((k >> 2) ^ ((t >> 1) & 3)) << 4)) =
-        make_float4(S[first + k], S[first + k + 1], S[first + k + 2], S[first + k + 3]);
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ (k << 2)), "f"(S[first + k]), "f"(S[first + k + 1]),
+                 "f"(S[first + k + 2]), "f"(S[first + k + 3])
+                 : "memory");
   fence_proxy_async_smem();
   named_barrier(2 + quarter, 128);
   if (t == 0 && quarter * KQ + first < K) {
