@@ -149,34 +149,59 @@ __global__ void __launch_bounds__(kThreads) delta_walk_kernel(const __grid_const
     if (p.states_out && t % kChunk == 0)
       w.store(p.states_out + ((b * p.nch + t / kChunk) * p.H + h) * KV, v0, p.V, p.K);
     const int n = (int)min((int64_t)kTile, end - t);
-    for (int i = 0; i < n; ++i) {
-      float kk[KE], qq[KE];
-      row_of(kk, sm.k[i], w.l);
-      row_of(qq, sm.q[i], w.l);
-      const float a = sm.gate[i], beta = sm.gate[kTile + i];
+    // Steps past the end have k = 0 and a gate of zero; they would clear the state, so the last tile stops before them.
+    // The outputs' sums over a row's lanes wait until all steps of the tile are through: on the way from one step to the
+    // next lies only the product with k.  (With them in between a step took 660 cycles.)
+    float part[2][kTile];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float d0 = 0.f, d1 = 0.f;
+    for (int i = 0; i < kTile; ++i) {
+      part[0][i] = part[1][i] = 0.f;
+      if (i < n) {
+        float kk[KE];
+        row_of(kk, sm.k[i], w.l);
+        const float a = sm.gate[i], beta = sm.gate[kTile + i];
+        float u[2];
 #pragma unroll
-        for (int e = 0; e < KE; e += 2) {
-          d0 = fmaf(w.s[r][e], kk[e], d0);
-          d1 = fmaf(w.s[r][e + 1], kk[e + 1], d1);
+        for (int r = 0; r < 2; ++r) {
+          float d0 = 0.f, d1 = 0.f, d2 = 0.f, d3 = 0.f;
+#pragma unroll
+          for (int e = 0; e < KE; e += 4) {
+            d0 = fmaf(w.s[r][e], kk[e], d0);
+            d1 = fmaf(w.s[r][e + 1], kk[e + 1], d1);
+            d2 = fmaf(w.s[r][e + 2], kk[e + 2], d2);
+            d3 = fmaf(w.s[r][e + 3], kk[e + 3], d3);
+          }
+          const float err = fmaf(-a, sum8((d0 + d1) + (d2 + d3)), sm.v[i][w.row[r]]);
+          u[r] = beta * err;
+          if (w.l == 0 && p.err) sm.err[i][w.row[r]] = err;
         }
-        const float err = fmaf(-a, sum8(d0 + d1), sm.v[i][w.row[r]]), u = beta * err;
-        float o0 = 0.f, o1 = 0.f;
+        float qq[KE];
+        row_of(qq, sm.q[i], w.l);
 #pragma unroll
-        for (int e = 0; e < KE; e += 2) {
-          w.s[r][e] = fmaf(a, w.s[r][e], u * kk[e]);
-          w.s[r][e + 1] = fmaf(a, w.s[r][e + 1], u * kk[e + 1]);
-          o0 = fmaf(w.s[r][e], qq[e], o0);
-          o1 = fmaf(w.s[r][e + 1], qq[e + 1], o1);
-        }
-        const float o = sum8(o0 + o1);
-        if (w.l == 0) {
-          sm.out[i][w.row[r]] = o * p.scale;
-          sm.err[i][w.row[r]] = err;
+        for (int r = 0; r < 2; ++r) {
+          float o0 = 0.f, o1 = 0.f;
+#pragma unroll
+          for (int e = 0; e < KE; e += 2) {
+            w.s[r][e] = fmaf(a, w.s[r][e], u[r] * kk[e]);
+            w.s[r][e + 1] = fmaf(a, w.s[r][e + 1], u[r] * kk[e + 1]);
+            o0 = fmaf(w.s[r][e], qq[e], o0);
+            o1 = fmaf(w.s[r][e + 1], qq[e + 1], o1);
+          }
+          part[r][i] = o0 + o1;
         }
       }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {   // lane l of a row's eight gets the sum of step l
+#pragma unroll
+      for (int o = 4; o; o >>= 1)
+#pragma unroll
+        for (int j = 0; j < o; ++j) {
+          const bool upper = w.l & o;
+          const float keep = upper ? part[r][j + o] : part[r][j], give = upper ? part[r][j] : part[r][j + o];
+          part[r][j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+      sm.out[w.l][w.row[r]] = part[r][0] * p.scale;
     }
     __syncthreads();
 #pragma unroll
@@ -212,29 +237,38 @@ __global__ void __launch_bounds__(kThreads) delta_walk_back_kernel(const __grid_
     __syncthreads();
     if (t >= kTile) next.fetch(p, dyb, p.ds[1], b, h, v0, t - kTile, p.T);
     const int n = (int)min((int64_t)kTile, p.T - t);
-    for (int i = n - 1; i >= 0; --i) {
-      float kk[KE], qq[KE];
-      row_of(kk, sm.k[i], w.l);
-      row_of(qq, sm.q[i], w.l);
-      const float a = sm.gate[i], beta = sm.gate[kTile + i];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float dy = sm.v[i][w.row[r]] * p.scale;
-        float d0 = 0.f, d1 = 0.f;
+    for (int i = kTile - 1; i >= 0; --i) {
+      if (i < n) {
+        float kk[KE], qq[KE];
+        row_of(kk, sm.k[i], w.l);
+        row_of(qq, sm.q[i], w.l);
+        const float a = sm.gate[i], beta = sm.gate[kTile + i];
+        float dv[2];
 #pragma unroll
-        for (int e = 0; e < KE; e += 2) {
-          w.s[r][e] = fmaf(dy, qq[e], w.s[r][e]);
-          w.s[r][e + 1] = fmaf(dy, qq[e + 1], w.s[r][e + 1]);
-          d0 = fmaf(w.s[r][e], kk[e], d0);
-          d1 = fmaf(w.s[r][e + 1], kk[e + 1], d1);
+        for (int r = 0; r < 2; ++r) {
+          const float dy = sm.v[i][w.row[r]] * p.scale;
+          float d0 = 0.f, d1 = 0.f, d2 = 0.f, d3 = 0.f;
+#pragma unroll
+          for (int e = 0; e < KE; e += 4) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w.s[r][e + j] = fmaf(dy, qq[e + j], w.s[r][e + j]);
+            d0 = fmaf(w.s[r][e], kk[e], d0);
+            d1 = fmaf(w.s[r][e + 1], kk[e + 1], d1);
+            d2 = fmaf(w.s[r][e + 2], kk[e + 2], d2);
+            d3 = fmaf(w.s[r][e + 3], kk[e + 3], d3);
+          }
+          const float du = sum8((d0 + d1) + (d2 + d3));
+          dv[r] = beta * du;
+          if (w.l == 0) {
+            sm.err[i][w.row[r]] = du;
+            sm.out[i][w.row[r]] = dv[r];
+          }
         }
-        const float du = sum8(d0 + d1), dv = beta * du;
 #pragma unroll
-        for (int e = 0; e < KE; ++e) w.s[r][e] = a * fmaf(-dv, kk[e], w.s[r][e]);
-        if (w.l == 0) {
-          sm.err[i][w.row[r]] = du;
-          sm.out[i][w.row[r]] = dv;
-        }
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int e = 0; e < KE; ++e) w.s[r][e] = a * fmaf(-dv[r], kk[e], w.s[r][e]);
       }
     }
     __syncthreads();

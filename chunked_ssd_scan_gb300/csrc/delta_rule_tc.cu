@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
 
 // The state before every segment: 16 rows of a sequence a block, a thread a key.
 __global__ void __launch_bounds__(128) delta_carry_kernel(const __grid_constant__ Params p, Segments seg, int tiles) {
-  __shared__ float row[2][16][128];
+  __shared__ __align__(16) float row[2][128][16];   // by keys: four rows a load
   const int seq = blockIdx.x / tiles, v0 = blockIdx.x % tiles * 16, k = threadIdx.x;
   const int64_t KV = p.K * p.V, at = (int64_t)seq * seg.n;
   const bool in = k < p.K;
@@ -626,10 +626,10 @@ __global__ void __launch_bounds__(128) delta_carry_kernel(const __grid_constant_
   for (int r = 0; r < 16; ++r) s[r] = in && v0 + r < p.V ? seg.end[at * KV + (v0 + r) * p.K + k] : 0.f;
   for (int i = 1; i < seg.n; ++i) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      row[i & 1][r][k] = s[r];
+    for (int r = 0; r < 16; ++r)
       if (in && v0 + r < p.V) seg.start[(at + i) * KV + (v0 + r) * p.K + k] = s[r];
-    }
+#pragma unroll
+    for (int r = 0; r < 16; r += 4) *reinterpret_cast<float4*>(&row[i & 1][k][r]) = make_float4(s[r], s[r + 1], s[r + 2], s[r + 3]);
     if (i + 1 == seg.n) break;
     __syncthreads();
 #pragma unroll
@@ -640,9 +640,17 @@ __global__ void __launch_bounds__(128) delta_carry_kernel(const __grid_constant_
 #pragma unroll
       for (int e = 0; e < 32; ++e) f[e] = j + e < p.K ? map[(j + e) * p.K + k] : 0.f;
 #pragma unroll
-      for (int e = 0; e < 32; ++e)
+      for (int e = 0; e < 32; ++e) {
+        if (j + e >= p.K) break;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[r] = fmaf(row[i & 1][r][(j + e) & 127], f[e], s[r]);
+        for (int r = 0; r < 16; r += 4) {
+          const float4 g = *reinterpret_cast<const float4*>(&row[i & 1][j + e][r]);
+          s[r] = fmaf(g.x, f[e], s[r]);
+          s[r + 1] = fmaf(g.y, f[e], s[r + 1]);
+          s[r + 2] = fmaf(g.z, f[e], s[r + 2]);
+          s[r + 3] = fmaf(g.w, f[e], s[r + 3]);
+        }
+      }
     }
   }
 }
