@@ -24,7 +24,10 @@ namespace {
 
 using namespace delta;
 
-constexpr int kTile = 8;      // steps whose rows are in shared memory at once
+// Steps whose rows are in shared memory at once, with the next ones on their way: 16 steps take longer than a load from
+// DRAM; with 256 keys their registers only do for 8.
+template <int KE>
+constexpr int kTileOf = KE > 16 ? 8 : 16;
 constexpr int kRows = 32;     // rows of the state (values) a block walks with
 constexpr int kThreads = 128;
 
@@ -78,8 +81,10 @@ __device__ __forceinline__ void row_of(float (&f)[KE], const float* sm, int l) {
 // Steps [t, t + kTile) of q, k, a slice of v (or dy) and the gates, one tile ahead in registers.
 template <typename T, int KE>
 struct TileLoad {
+  static constexpr int kTile = kTileOf<KE>;
   static constexpr int kKeys = KE * 8, kPer = kTile * kKeys / kThreads;
-  float q[kPer], k[kPer], v[2], gate;
+  static constexpr int kVals = kTile * kRows / kThreads;
+  float q[kPer], k[kPer], v[kVals], gate;
   __device__ __forceinline__ void fetch(const Params& p, const T* vbase, int64_t vstep, int64_t b, int64_t h,
                                         int64_t v0, int64_t t, int64_t end) {
     const int64_t hk = h / (p.H / p.Hk);
@@ -93,11 +98,11 @@ struct TileLoad {
       k[n] = in ? ld_f32(kb + (t + i) * p.ks[1] + c) : 0.f;
     }
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
+    for (int n = 0; n < kVals; ++n) {
       const int at = n * kThreads + threadIdx.x, i = at / kRows, c = at % kRows;
       v[n] = t + i < end && v0 + c < p.V ? ld_f32(vbase + (t + i) * vstep + v0 + c) : 0.f;
     }
-    gate = 0.f;
+    gate = threadIdx.x < kTile ? 1.f : 0.f;   // past the end: a decay of one and no write, so no step needs a branch
     if (threadIdx.x < 2 * kTile) {
       const int64_t at = t + (threadIdx.x & (kTile - 1));
       if (at < end)
@@ -107,6 +112,7 @@ struct TileLoad {
 };
 template <int KE>
 struct Tile {
+  static constexpr int kTile = kTileOf<KE>;
   float q[kTile][KE * 8], k[kTile][KE * 8], v[kTile][kRows], out[kTile][kRows], err[kTile][kRows];
   float gate[2 * kTile];   // decays, betas
   template <typename T>
@@ -118,7 +124,7 @@ struct Tile {
       (&k[0][0])[at] = r.k[n];
     }
 #pragma unroll
-    for (int n = 0; n < 2; ++n) (&v[0][0])[n * kThreads + threadIdx.x] = r.v[n];
+    for (int n = 0; n < TileLoad<T, KE>::kVals; ++n) (&v[0][0])[n * kThreads + threadIdx.x] = r.v[n];
     if (threadIdx.x < 2 * kTile) gate[threadIdx.x] = r.gate;
   }
 };
@@ -126,6 +132,7 @@ struct Tile {
 // Forward.  One chunk a block where the states before the chunks are known (backward: only err is wanted then).
 template <typename T, int KE>
 __global__ void __launch_bounds__(kThreads) delta_walk_kernel(const __grid_constant__ Params p, bool by_chunk) {
+  constexpr int kTile = kTileOf<KE>;
   __shared__ __align__(16) Tile<KE> sm;
   int64_t id = blockIdx.x;
   const int64_t slice = id % p.slices;
@@ -149,63 +156,61 @@ __global__ void __launch_bounds__(kThreads) delta_walk_kernel(const __grid_const
     if (p.states_out && t % kChunk == 0)
       w.store(p.states_out + ((b * p.nch + t / kChunk) * p.H + h) * KV, v0, p.V, p.K);
     const int n = (int)min((int64_t)kTile, end - t);
-    // Steps past the end have k = 0 and a gate of zero; they would clear the state, so the last tile stops before them.
     // The outputs' sums over a row's lanes wait until all steps of the tile are through: on the way from one step to the
     // next lies only the product with k.  (With them in between a step took 660 cycles.)
     float part[2][kTile];
 #pragma unroll
     for (int i = 0; i < kTile; ++i) {
-      part[0][i] = part[1][i] = 0.f;
-      if (i < n) {
-        float kk[KE];
-        row_of(kk, sm.k[i], w.l);
-        const float a = sm.gate[i], beta = sm.gate[kTile + i];
-        float u[2];
+      float kk[KE];
+      row_of(kk, sm.k[i], w.l);
+      const float a = sm.gate[i], beta = sm.gate[kTile + i];
+      float u[2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float d0 = 0.f, d1 = 0.f, d2 = 0.f, d3 = 0.f;
+      for (int r = 0; r < 2; ++r) {
+        float d0 = 0.f, d1 = 0.f, d2 = 0.f, d3 = 0.f;
 #pragma unroll
-          for (int e = 0; e < KE; e += 4) {
-            d0 = fmaf(w.s[r][e], kk[e], d0);
-            d1 = fmaf(w.s[r][e + 1], kk[e + 1], d1);
-            d2 = fmaf(w.s[r][e + 2], kk[e + 2], d2);
-            d3 = fmaf(w.s[r][e + 3], kk[e + 3], d3);
-          }
-          const float err = fmaf(-a, sum8((d0 + d1) + (d2 + d3)), sm.v[i][w.row[r]]);
-          u[r] = beta * err;
-          if (w.l == 0 && p.err) sm.err[i][w.row[r]] = err;
+        for (int e = 0; e < KE; e += 4) {
+          d0 = fmaf(w.s[r][e], kk[e], d0);
+          d1 = fmaf(w.s[r][e + 1], kk[e + 1], d1);
+          d2 = fmaf(w.s[r][e + 2], kk[e + 2], d2);
+          d3 = fmaf(w.s[r][e + 3], kk[e + 3], d3);
         }
-        float qq[KE];
-        row_of(qq, sm.q[i], w.l);
+        const float err = fmaf(-a, sum8((d0 + d1) + (d2 + d3)), sm.v[i][w.row[r]]);
+        u[r] = beta * err;
+        if (w.l == 0 && p.err) sm.err[i][w.row[r]] = err;
+      }
+      float qq[KE];
+      row_of(qq, sm.q[i], w.l);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float o0 = 0.f, o1 = 0.f;
+      for (int r = 0; r < 2; ++r) {
+        float o0 = 0.f, o1 = 0.f;
 #pragma unroll
-          for (int e = 0; e < KE; e += 2) {
-            w.s[r][e] = fmaf(a, w.s[r][e], u[r] * kk[e]);
-            w.s[r][e + 1] = fmaf(a, w.s[r][e + 1], u[r] * kk[e + 1]);
-            o0 = fmaf(w.s[r][e], qq[e], o0);
-            o1 = fmaf(w.s[r][e + 1], qq[e + 1], o1);
-          }
-          part[r][i] = o0 + o1;
+        for (int e = 0; e < KE; e += 2) {
+          w.s[r][e] = fmaf(a, w.s[r][e], u[r] * kk[e]);
+          w.s[r][e + 1] = fmaf(a, w.s[r][e + 1], u[r] * kk[e + 1]);
+          o0 = fmaf(w.s[r][e], qq[e], o0);
+          o1 = fmaf(w.s[r][e + 1], qq[e + 1], o1);
         }
+        part[r][i] = o0 + o1;
       }
     }
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {   // lane l of a row's eight gets the sum of step l
+    for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int o = 4; o; o >>= 1)
+      for (int i0 = 0; i0 < kTile; i0 += 8) {   // lane l of a row's eight gets the sum of step l
 #pragma unroll
-        for (int j = 0; j < o; ++j) {
-          const bool upper = w.l & o;
-          const float keep = upper ? part[r][j + o] : part[r][j], give = upper ? part[r][j] : part[r][j + o];
-          part[r][j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-        }
-      sm.out[w.l][w.row[r]] = part[r][0] * p.scale;
-    }
+        for (int o = 4; o; o >>= 1)
+#pragma unroll
+          for (int j = i0; j < i0 + o; ++j) {
+            const bool upper = w.l & o;
+            const float keep = upper ? part[r][j + o] : part[r][j], give = upper ? part[r][j] : part[r][j + o];
+            part[r][j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+          }
+        sm.out[i0 + w.l][w.row[r]] = part[r][i0] * p.scale;
+      }
     __syncthreads();
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
+    for (int m = 0; m < kTile * kRows / kThreads; ++m) {
       const int at = m * kThreads + threadIdx.x, i = at / kRows, c = at % kRows;
       if (i < n && v0 + c < p.V) {
         const int64_t to = ((b * p.T + t + i) * p.H + h) * p.V + v0 + c;
@@ -220,6 +225,7 @@ __global__ void __launch_bounds__(kThreads) delta_walk_kernel(const __grid_const
 // Backward: G along time, last step first.
 template <typename T, int KE>
 __global__ void __launch_bounds__(kThreads) delta_walk_back_kernel(const __grid_constant__ Params p) {
+  constexpr int kTile = kTileOf<KE>;
   __shared__ __align__(16) Tile<KE> sm;
   int64_t id = blockIdx.x;
   const int64_t slice = id % p.slices;
@@ -239,41 +245,39 @@ __global__ void __launch_bounds__(kThreads) delta_walk_back_kernel(const __grid_
     const int n = (int)min((int64_t)kTile, p.T - t);
 #pragma unroll
     for (int i = kTile - 1; i >= 0; --i) {
-      if (i < n) {
-        float kk[KE], qq[KE];
-        row_of(kk, sm.k[i], w.l);
-        row_of(qq, sm.q[i], w.l);
-        const float a = sm.gate[i], beta = sm.gate[kTile + i];
-        float dv[2];
+      float kk[KE], qq[KE];
+      row_of(kk, sm.k[i], w.l);
+      row_of(qq, sm.q[i], w.l);
+      const float a = sm.gate[i], beta = sm.gate[kTile + i];
+      float dv[2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float dy = sm.v[i][w.row[r]] * p.scale;
-          float d0 = 0.f, d1 = 0.f, d2 = 0.f, d3 = 0.f;
+      for (int r = 0; r < 2; ++r) {
+        const float dy = sm.v[i][w.row[r]] * p.scale;
+        float d0 = 0.f, d1 = 0.f, d2 = 0.f, d3 = 0.f;
 #pragma unroll
-          for (int e = 0; e < KE; e += 4) {
+        for (int e = 0; e < KE; e += 4) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w.s[r][e + j] = fmaf(dy, qq[e + j], w.s[r][e + j]);
-            d0 = fmaf(w.s[r][e], kk[e], d0);
-            d1 = fmaf(w.s[r][e + 1], kk[e + 1], d1);
-            d2 = fmaf(w.s[r][e + 2], kk[e + 2], d2);
-            d3 = fmaf(w.s[r][e + 3], kk[e + 3], d3);
-          }
-          const float du = sum8((d0 + d1) + (d2 + d3));
-          dv[r] = beta * du;
-          if (w.l == 0) {
-            sm.err[i][w.row[r]] = du;
-            sm.out[i][w.row[r]] = dv[r];
-          }
+          for (int j = 0; j < 4; ++j) w.s[r][e + j] = fmaf(dy, qq[e + j], w.s[r][e + j]);
+          d0 = fmaf(w.s[r][e], kk[e], d0);
+          d1 = fmaf(w.s[r][e + 1], kk[e + 1], d1);
+          d2 = fmaf(w.s[r][e + 2], kk[e + 2], d2);
+          d3 = fmaf(w.s[r][e + 3], kk[e + 3], d3);
         }
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int e = 0; e < KE; ++e) w.s[r][e] = a * fmaf(-dv[r], kk[e], w.s[r][e]);
+        const float du = sum8((d0 + d1) + (d2 + d3));
+        dv[r] = beta * du;
+        if (w.l == 0) {
+          sm.err[i][w.row[r]] = du;
+          sm.out[i][w.row[r]] = dv[r];
+        }
       }
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int e = 0; e < KE; ++e) w.s[r][e] = a * fmaf(-dv[r], kk[e], w.s[r][e]);
     }
     __syncthreads();
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
+    for (int m = 0; m < kTile * kRows / kThreads; ++m) {
       const int at = m * kThreads + threadIdx.x, i = at / kRows, c = at % kRows;
       if (i < n && v0 + c < p.V) {
         const int64_t to = ((b * p.T + t + i) * p.H + h) * p.V + v0 + c;
