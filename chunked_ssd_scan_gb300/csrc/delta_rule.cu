@@ -28,7 +28,6 @@ using namespace delta;
 // DRAM; with 256 keys their registers only do for 8.
 template <int KE>
 constexpr int kTileOf = KE > 16 ? 8 : 16;
-constexpr int kRows = 32;     // rows of the state (values) a block walks with
 constexpr int kThreads = 128;
 
 // Where lane l of a row's eight keeps element e of its KE: four neighbours, then 32 further.
@@ -40,26 +39,26 @@ __device__ __forceinline__ float sum8(float v) {
   return v + __shfl_xor_sync(0xffffffffu, v, 4);
 }
 
-// A warp's eight lanes hold a row's K values, two rows each; the rows do not meet, so a block is a slice of V.
-template <int KE>
+// A warp's eight lanes hold a row's K values, R rows each; the rows do not meet, so a block is a slice of 16 R of V.
+template <int KE, int R>
 struct Walk {
-  float s[2][KE];
-  int l, row[2];   // row within the slice
+  float s[R][KE];
+  int l, row[R];   // row within the slice
   __device__ __forceinline__ Walk() {
     l = threadIdx.x & 7;
-    row[0] = threadIdx.x >> 3;
-    row[1] = row[0] + 16;
+#pragma unroll
+    for (int r = 0; r < R; ++r) row[r] = (threadIdx.x >> 3) + 16 * r;
   }
   __device__ __forceinline__ void load(const float* base, int64_t v0, int64_t V, int64_t K) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int e = 0; e < KE; ++e)
         s[r][e] = base && v0 + row[r] < V && key_of(e, l) < K ? base[(v0 + row[r]) * K + key_of(e, l)] : 0.f;
   }
   __device__ __forceinline__ void store(float* base, int64_t v0, int64_t V, int64_t K) const {
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int e = 0; e < KE; ++e)
         if (v0 + row[r] < V && key_of(e, l) < K) base[(v0 + row[r]) * K + key_of(e, l)] = s[r][e];
@@ -79,8 +78,9 @@ __device__ __forceinline__ void row_of(float (&f)[KE], const float* sm, int l) {
 }
 
 // Steps [t, t + kTile) of q, k, a slice of v (or dy) and the gates, one tile ahead in registers.
-template <typename T, int KE>
+template <typename T, int KE, int R>
 struct TileLoad {
+  static constexpr int kRows = 16 * R;
   static constexpr int kTile = kTileOf<KE>;
   static constexpr int kKeys = KE * 8, kPer = kTile * kKeys / kThreads;
   static constexpr int kVals = kTile * kRows / kThreads;
@@ -110,30 +110,31 @@ struct TileLoad {
     }
   }
 };
-template <int KE>
+template <int KE, int R>
 struct Tile {
+  static constexpr int kRows = 16 * R;
   static constexpr int kTile = kTileOf<KE>;
   float q[kTile][KE * 8], k[kTile][KE * 8], v[kTile][kRows], out[kTile][kRows], err[kTile][kRows];
   float gate[2 * kTile];   // decays, betas
   template <typename T>
-  __device__ __forceinline__ void put(const TileLoad<T, KE>& r) {
+  __device__ __forceinline__ void put(const TileLoad<T, KE, R>& r) {
 #pragma unroll
-    for (int n = 0; n < TileLoad<T, KE>::kPer; ++n) {
+    for (int n = 0; n < TileLoad<T, KE, R>::kPer; ++n) {
       const int at = n * kThreads + threadIdx.x;
       (&q[0][0])[at] = r.q[n];
       (&k[0][0])[at] = r.k[n];
     }
 #pragma unroll
-    for (int n = 0; n < TileLoad<T, KE>::kVals; ++n) (&v[0][0])[n * kThreads + threadIdx.x] = r.v[n];
+    for (int n = 0; n < TileLoad<T, KE, R>::kVals; ++n) (&v[0][0])[n * kThreads + threadIdx.x] = r.v[n];
     if (threadIdx.x < 2 * kTile) gate[threadIdx.x] = r.gate;
   }
 };
 
 // Forward.  One chunk a block where the states before the chunks are known (backward: only err is wanted then).
-template <typename T, int KE>
+template <typename T, int KE, int R>
 __global__ void __launch_bounds__(kThreads) delta_walk_kernel(const __grid_constant__ Params p, bool by_chunk) {
-  constexpr int kTile = kTileOf<KE>;
-  __shared__ __align__(16) Tile<KE> sm;
+  constexpr int kTile = kTileOf<KE>, kRows = 16 * R;
+  __shared__ __align__(16) Tile<KE, R> sm;
   int64_t id = blockIdx.x;
   const int64_t slice = id % p.slices;
   id /= p.slices;
@@ -142,11 +143,11 @@ __global__ void __launch_bounds__(kThreads) delta_walk_kernel(const __grid_const
   const int64_t chunk = by_chunk ? id % p.nch : 0, b = by_chunk ? id / p.nch : id;
   const int64_t v0 = slice * kRows, begin = chunk * kChunk, end = by_chunk ? min(begin + kChunk, p.T) : p.T;
   const int64_t KV = p.K * p.V;
-  Walk<KE> w;
+  Walk<KE, R> w;
   w.load(by_chunk ? p.states_in + ((b * p.nch + chunk) * p.H + h) * KV
                   : p.init ? p.init + (b * p.H + h) * KV : nullptr, v0, p.V, p.K);
   const T* vbase = static_cast<const T*>(p.v) + b * p.vs[0] + h * p.vs[2];
-  TileLoad<T, KE> next;
+  TileLoad<T, KE, R> next;
   next.fetch(p, vbase, p.vs[1], b, h, v0, begin, end);
   for (int64_t t = begin; t < end; t += kTile) {
     __syncthreads();
@@ -158,15 +159,15 @@ __global__ void __launch_bounds__(kThreads) delta_walk_kernel(const __grid_const
     const int n = (int)min((int64_t)kTile, end - t);
     // The outputs' sums over a row's lanes wait until all steps of the tile are through: on the way from one step to the
     // next lies only the product with k.  (With them in between a step took 660 cycles.)
-    float part[2][kTile];
+    float part[R][kTile];
 #pragma unroll
     for (int i = 0; i < kTile; ++i) {
       float kk[KE];
       row_of(kk, sm.k[i], w.l);
       const float a = sm.gate[i], beta = sm.gate[kTile + i];
-      float u[2];
+      float u[R];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int r = 0; r < R; ++r) {
         float d0 = 0.f, d1 = 0.f, d2 = 0.f, d3 = 0.f;
 #pragma unroll
         for (int e = 0; e < KE; e += 4) {
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) delta_walk_kernel(const __grid_const
       float qq[KE];
       row_of(qq, sm.q[i], w.l);
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int r = 0; r < R; ++r) {
         float o0 = 0.f, o1 = 0.f;
 #pragma unroll
         for (int e = 0; e < KE; e += 2) {
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(kThreads) delta_walk_kernel(const __grid_const
       }
     }
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int i0 = 0; i0 < kTile; i0 += 8) {   // lane l of a row's eight gets the sum of step l
 #pragma unroll
@@ -223,18 +224,18 @@ __global__ void __launch_bounds__(kThreads) delta_walk_kernel(const __grid_const
 }
 
 // Backward: G along time, last step first.
-template <typename T, int KE>
+template <typename T, int KE, int R>
 __global__ void __launch_bounds__(kThreads) delta_walk_back_kernel(const __grid_constant__ Params p) {
-  constexpr int kTile = kTileOf<KE>;
-  __shared__ __align__(16) Tile<KE> sm;
+  constexpr int kTile = kTileOf<KE>, kRows = 16 * R;
+  __shared__ __align__(16) Tile<KE, R> sm;
   int64_t id = blockIdx.x;
   const int64_t slice = id % p.slices;
   id /= p.slices;
   const int64_t h = id % p.H, b = id / p.H, v0 = slice * kRows, KV = p.K * p.V;
-  Walk<KE> w;
+  Walk<KE, R> w;
   w.load(p.dfinal ? p.dfinal + (b * p.H + h) * KV : nullptr, v0, p.V, p.K);
   const T* dyb = static_cast<const T*>(p.dy) + b * p.ds[0] + h * p.ds[2];
-  TileLoad<T, KE> next;
+  TileLoad<T, KE, R> next;
   const int64_t first = (p.T - 1) / kTile * kTile;
   next.fetch(p, dyb, p.ds[1], b, h, v0, first, p.T);
   for (int64_t t = first; t >= 0; t -= kTile) {
@@ -249,9 +250,9 @@ __global__ void __launch_bounds__(kThreads) delta_walk_back_kernel(const __grid_
       row_of(kk, sm.k[i], w.l);
       row_of(qq, sm.q[i], w.l);
       const float a = sm.gate[i], beta = sm.gate[kTile + i];
-      float dv[2];
+      float dv[R];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int r = 0; r < R; ++r) {
         const float dy = sm.v[i][w.row[r]] * p.scale;
         float d0 = 0.f, d1 = 0.f, d2 = 0.f, d3 = 0.f;
 #pragma unroll
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__(kThreads) delta_walk_back_kernel(const __grid_
         }
       }
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
+      for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int e = 0; e < KE; ++e) w.s[r][e] = a * fmaf(-dv[r], kk[e], w.s[r][e]);
     }
@@ -644,27 +645,51 @@ Params make_params(const gated_delta_rule_shape* s) {
     p.bs[a] = s->beta_stride[a];
   }
   p.scale = s->scale;
-  p.slices = (p.V + kRows - 1) / kRows;
   return p;
+}
+
+// Blocks of 16 rows while these fit the SMs in a round or so (a step is then shorter: 3 x 777 x 6 heads of 60 x 100 f32
+// RAG1 us, with 32 rows 159), else of 32 (a step's loads of k and q serve twice as many).
+constexpr int64_t kFewBlocks = 2 * 152;
+
+template <typename T, int KE>
+cudaError_t launch_walk_as(Params p, bool by_chunk, cudaStream_t st) {
+  const int64_t walks = p.batch * (by_chunk ? p.nch : 1) * p.H;
+  p.slices = (p.V + 15) / 16;
+  if (walks * p.slices <= kFewBlocks) {
+    delta_walk_kernel<T, KE, 1><<<(unsigned)(walks * p.slices), kThreads, 0, st>>>(p, by_chunk);
+  } else {
+    p.slices = (p.V + 31) / 32;
+    delta_walk_kernel<T, KE, 2><<<(unsigned)(walks * p.slices), kThreads, 0, st>>>(p, by_chunk);
+  }
+  return cudaGetLastError();
+}
+template <typename T, int KE>
+cudaError_t launch_walk_back_as(Params p, cudaStream_t st) {
+  const int64_t walks = p.batch * p.H;
+  p.slices = (p.V + 15) / 16;
+  if (walks * p.slices <= kFewBlocks) {
+    delta_walk_back_kernel<T, KE, 1><<<(unsigned)(walks * p.slices), kThreads, 0, st>>>(p);
+  } else {
+    p.slices = (p.V + 31) / 32;
+    delta_walk_back_kernel<T, KE, 2><<<(unsigned)(walks * p.slices), kThreads, 0, st>>>(p);
+  }
+  return cudaGetLastError();
 }
 
 // Keys a lane holds: 8, 16 or 32 of up to 64, 128 or 256.
 template <typename T>
 cudaError_t launch_walk(const Params& p, bool by_chunk, cudaStream_t st) {
-  const unsigned grid = (unsigned)(p.batch * (by_chunk ? p.nch : 1) * p.H * p.slices);
-  if (p.K <= 64) delta_walk_kernel<T, 8><<<grid, kThreads, 0, st>>>(p, by_chunk);
-  else if (p.K <= 128) delta_walk_kernel<T, 16><<<grid, kThreads, 0, st>>>(p, by_chunk);
-  else delta_walk_kernel<T, 32><<<grid, kThreads, 0, st>>>(p, by_chunk);
-  return cudaGetLastError();
+  if (p.K <= 64) return launch_walk_as<T, 8>(p, by_chunk, st);
+  if (p.K <= 128) return launch_walk_as<T, 16>(p, by_chunk, st);
+  return launch_walk_as<T, 32>(p, by_chunk, st);
 }
 
 template <typename T>
 cudaError_t launch_backward(const Params& p, cudaStream_t st) {
-  const unsigned grid = (unsigned)(p.batch * p.H * p.slices);
-  if (p.K <= 64) delta_walk_back_kernel<T, 8><<<grid, kThreads, 0, st>>>(p);
-  else if (p.K <= 128) delta_walk_back_kernel<T, 16><<<grid, kThreads, 0, st>>>(p);
-  else delta_walk_back_kernel<T, 32><<<grid, kThreads, 0, st>>>(p);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = p.K <= 64    ? launch_walk_back_as<T, 8>(p, st)
+                  : p.K <= 128 ? launch_walk_back_as<T, 16>(p, st)
+                               : launch_walk_back_as<T, 32>(p, st);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(delta_chunk_grad_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(GradSmem));
   if (e != cudaSuccess) return e;
