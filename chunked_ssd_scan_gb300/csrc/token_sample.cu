@@ -105,10 +105,10 @@ __device__ __forceinline__ void for_tokens(const T* row, int begin, int end, int
 
 struct SampleSmem {
   uint64_t part[kWarps];
-  uint32_t count[kBins];
-  uint64_t mass[kBins];
+  uint32_t count[kBins], low[kBins], high[kBins];   // of a bin: tokens, sum of weights
   uint32_t list_key[kList];
   int32_t list_id[kList];
+  uint64_t list_w[kList];
   uint64_t out[4];
   int32_t listed;
 };
@@ -145,11 +145,14 @@ __device__ __forceinline__ int pick_warp(SampleSmem& sm, uint64_t mine, uint64_t
   return at;
 }
 
-// What a row keeps: tokens whose key is above `key`, and those of that key up to index `last`.
+// What a row keeps: tokens whose key is above `key`, and those of that key up to index `last`; of these the ones with a
+// weight of at least `least` (min_p).
 struct Cut {
   uint32_t key;
   int32_t last;
+  uint64_t least;
   __device__ __forceinline__ bool keeps(uint32_t k, int i) const { return k > key || (k == key && i <= last); }
+  __device__ __forceinline__ uint64_t of(uint64_t w) const { return w >= least ? w : 0; }
 };
 
 __device__ __forceinline__ int bin_of(const Weight& w, float inv, float x) {
@@ -158,70 +161,101 @@ __device__ __forceinline__ int bin_of(const Weight& w, float inv, float x) {
 }
 
 // The first token, in falling order, at which the running count (kMass: the running sum of weights) of what `have` keeps
-// reaches `want` >= 1; all of `have` where it never does.  On return *sum is the weights' sum up to it.
+// reaches `want` >= 1; all of `have` where it never does.  With kMass *sum is the weights' sum up to it on return.
+// (A count takes no account of min_p: what that leaves is a beginning of the same order.)
 template <bool kMass, typename T>
 __device__ Cut find_cut(SampleSmem& sm, const T* row, int V, const Weight& w, float inv, const Cut& have, uint64_t want,
                         uint64_t* sum) {
   const int tid = threadIdx.x, lane = tid & 31;
   __syncthreads();
   sm.count[tid] = 0;
-  sm.mass[tid] = 0;
+  sm.low[tid] = sm.high[tid] = 0;
   if (tid == 0) sm.listed = 0;
   __syncthreads();
   for_tokens(row, 0, V, tid, kThreads, [&](int i, float x) {
     if (x == kNegInf || !have.keeps(key_of(x), i)) return;
     const int b = bin_of(w, inv, x);
-    const uint64_t m = w(x);
-    atomicAdd(&sm.count[b], 1u);
-    if (m) atomicAdd(reinterpret_cast<unsigned long long*>(&sm.mass[b]), (unsigned long long)m);
+    if constexpr (kMass) {
+      const uint64_t m = have.of(w(x));
+      if (m) {
+        // in two halves (a 64-bit addition in shared memory is a loop): the lower one's carry goes with the upper
+        const uint32_t lo = (uint32_t)m, old = atomicAdd(&sm.low[b], lo), up = (uint32_t)(m >> 32) + (old + lo < lo);
+        if (up) atomicAdd(&sm.high[b], up);
+        atomicAdd(&sm.count[b], 1u);
+      }
+    } else {
+      atomicAdd(&sm.count[b], 1u);
+    }
   });
   __syncthreads();
   // the bin in which it happens: sums over 32 bins by warp, then within
   uint64_t before;
-  const uint64_t c0 = sm.count[tid], m0 = sm.mass[tid], mine = kMass ? m0 : c0;
+  const uint64_t mine = kMass ? (uint64_t)sm.high[tid] << 32 | sm.low[tid] : sm.count[tid];
   const int warp = pick_warp(sm, mine, want - 1, &before);
-  const uint64_t all = block_sum(sm, m0);
   if ((tid >> 5) == warp) {
-    uint64_t upto = mine, mass = m0;
+    uint64_t upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t v = __shfl_up_sync(0xffffffffu, upto, o), u = __shfl_up_sync(0xffffffffu, mass, o);
-      if (lane >= o) {
-        upto += v;
-        mass += u;
-      }
+      const uint64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
     }
     const uint32_t past = __ballot_sync(0xffffffffu, before + upto >= want);
     const int at = past ? __ffs(past) - 1 : 31;
     if (lane == at) {
       sm.out[0] = past ? (uint64_t)tid : kBins;
       sm.out[1] = want - (before + upto - mine);   // still wanted within the bin
-      sm.out[2] = mass - m0;                       // this warp's bins before it
+      sm.out[2] = before + upto - mine;
     }
   }
   __syncthreads();
   const int bin = (int)sm.out[0];
   if (bin == kBins) {
-    *sum = all;
+    if (kMass) *sum = block_sum(sm, mine);
     return have;
   }
-  uint64_t rest = sm.out[1];
-  uint64_t base = block_sum(sm, tid < bin ? m0 : 0);
-  // the bin's tokens: in shared memory if they fit
+  const uint64_t rest = sm.out[1], base = sm.out[2];
   const uint32_t n = sm.count[bin];
-  const bool fits = n <= kList;
-  uint32_t lo = 0xffffffffu, hi = 0;
-  for_tokens(row, 0, V, tid, kThreads, [&](int i, float x) {
-    if (x == kNegInf || bin_of(w, inv, x) != bin) return;
-    const uint32_t k = key_of(x);
-    if (!have.keeps(k, i)) return;
-    lo = min(lo, k);
-    hi = max(hi, k);
-    if (fits) {
+  auto in_bin = [&](int i, float x, uint32_t& k) {
+    if (x == kNegInf || bin_of(w, inv, x) != bin) return false;
+    k = key_of(x);
+    return have.keeps(k, i) && (!kMass || have.of(w(x)) != 0);
+  };
+  if (n <= kList) {   // every one of the bin's tokens counts those before it
+    for_tokens(row, 0, V, tid, kThreads, [&](int i, float x) {
+      uint32_t k;
+      if (!in_bin(i, x, k)) return;
       const int at = atomicAdd(&sm.listed, 1);
       sm.list_key[at] = k;
       sm.list_id[at] = i;
+      if (kMass) sm.list_w[at] = w(x);
+    });
+    __syncthreads();
+    if (tid < (int)n) {
+      const uint32_t k = sm.list_key[tid];
+      const int id = sm.list_id[tid];
+      const uint64_t own = kMass ? sm.list_w[tid] : 1;
+      uint64_t above = 0;
+      for (int j = 0; j < (int)n; ++j) {
+        const uint32_t kj = sm.list_key[j];
+        if (kj > k || (kj == k && sm.list_id[j] < id)) above += kMass ? sm.list_w[j] : 1;
+      }
+      if (above < rest && above + own >= rest) {
+        sm.out[0] = k;
+        sm.out[1] = (uint64_t)(uint32_t)id;
+        sm.out[3] = base + above + own;
+      }
     }
+    __syncthreads();
+    if (kMass) *sum = sm.out[3];
+    return {(uint32_t)sm.out[0], (int32_t)(uint32_t)sm.out[1], have.least};
+  }
+  // more than fit (many equal logits): by bisection of their keys, a pass over the row a step
+  uint32_t lo = 0xffffffffu, hi = 0;
+  for_tokens(row, 0, V, tid, kThreads, [&](int i, float x) {
+    uint32_t k;
+    if (!in_bin(i, x, k)) return;
+    lo = min(lo, k);
+    hi = max(hi, k);
   });
   lo = __reduce_min_sync(0xffffffffu, lo);
   hi = __reduce_max_sync(0xffffffffu, hi);
@@ -232,57 +266,32 @@ __device__ Cut find_cut(SampleSmem& sm, const T* row, int V, const Weight& w, fl
   lo = __reduce_min_sync(0xffffffffu, (uint32_t)pair);
   hi = __reduce_max_sync(0xffffffffu, (uint32_t)(pair >> 32));
   auto value_of = [](uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); };
-  auto of_bin = [&](auto&& f) {   // f(key, index) over the bin's tokens
-    if (fits) {
-      if (tid < (int)n) f(sm.list_key[tid], sm.list_id[tid]);
-    } else {
-      for_tokens(row, 0, V, tid, kThreads, [&](int i, float x) {
-        if (x == kNegInf || bin_of(w, inv, x) != bin) return;
-        const uint32_t k = key_of(x);
-        if (have.keeps(k, i)) f(k, i);
-      });
-    }
+  auto summed = [&](auto&& f) {   // the sum of f(key, index) over the bin's tokens
+    uint64_t s = 0;
+    for_tokens(row, 0, V, tid, kThreads, [&](int i, float x) {
+      uint32_t k;
+      if (in_bin(i, x, k)) s += f(k, i);
+    });
+    return block_sum(sm, s);
   };
   // the largest key with count (sum) of keys >= it at least `rest`
   while (lo < hi) {
     const uint32_t mid = lo + (hi - lo) / 2 + 1;
-    uint64_t s = 0;
-    of_bin([&](uint32_t k, int) {
-      if (k >= mid) s += kMass ? w(value_of(k)) : 1;
-    });
-    s = block_sum(sm, s);
-    if (s >= rest) lo = mid;
+    if (summed([&](uint32_t k, int) { return k >= mid ? kMass ? w(value_of(k)) : 1 : 0; }) >= rest) lo = mid;
     else hi = mid - 1;
   }
-  uint64_t above = 0, mass = 0, ties = 0;
-  of_bin([&](uint32_t k, int) {
-    if (k > lo) {
-      above += 1;
-      mass += w(value_of(k));
-    }
-    if (k == lo) ties += 1;
-  });
-  above = block_sum(sm, above);
-  mass = block_sum(sm, mass);
-  ties = block_sum(sm, ties);
-  const uint64_t each = w(value_of(lo));
-  uint64_t need = rest - (kMass ? mass : above);   // of the equal ones, >= 1
-  if (kMass) need = each ? (need + each - 1) / each : ties;
-  need = min(need, ties);
-  *sum = base + mass + need * each;
-  if (need == ties) return {lo, lo == have.key ? have.last : V};
+  const uint64_t above = summed([&](uint32_t k, int) { return k > lo ? kMass ? w(value_of(k)) : 1 : 0; });
+  const uint64_t ties = summed([&](uint32_t k, int) { return k == lo ? 1ull : 0ull; });
+  const uint64_t each = kMass ? w(value_of(lo)) : 1;
+  const uint64_t need = min((rest - above + each - 1) / each, ties);   // of the equal ones, >= 1
+  if (kMass) *sum = base + above + need * each;
   int from = 0, to = V - 1;   // the smallest index with `need` of the equal ones up to it
   while (from < to) {
     const int mid = from + (to - from) / 2;
-    uint64_t s = 0;
-    of_bin([&](uint32_t k, int i) {
-      if (k == lo && i <= mid) s += 1;
-    });
-    s = block_sum(sm, s);
-    if (s >= need) to = mid;
+    if (summed([&](uint32_t k, int i) { return k == lo && i <= mid ? 1ull : 0ull; }) >= need) to = mid;
     else from = mid + 1;
   }
-  return {lo, from};
+  return {lo, from, have.least};
 }
 
 __device__ __forceinline__ uint64_t fixed64(float v) {   // v in [0, 1) as v 2^64
@@ -332,28 +341,25 @@ __global__ void __launch_bounds__(kThreads) token_sample_kernel(const __grid_con
       }
       continue;
     }
-    const double c = 1.4426950408889634 / (double)fmaxf(temp, 1e-30f);
-    w.ch = (float)c;
-    w.cl = (float)(c - (double)w.ch);
+    // log2(e) / temperature in two floats: the quotient, and what its product with the temperature leaves
+    const float tt = fmaxf(temp, 1e-30f);
+    w.ch = 1.44269502f / tt;
+    w.cl = (fmaf(-w.ch, tt, 1.44269502f) + 1.92596299e-8f) / tt;
     w.shift = p.shift;
-    Cut cut = {0, V};
-    if (min_p > 0.f) {   // exp((x - most) / temp) >= min_p as a bound on x, rounded up to fp32
-      const double least = min_p >= 1.f ? (double)w.most : (double)w.most + (double)temp * log((double)min_p);
-      cut.key = key_of(isinf(w.most) ? w.most : fminf(w.most, __double2float_ru(least)));
+    Cut cut = {0, V, 1};
+    if (min_p > 0.f) {   // a bound on the weights, rounded up
+      const uint64_t one = 1ull << w.shift, f = min_p < 1.f ? fixed64(min_p) : 0;
+      const uint64_t least = __umul64hi(f, one) + (f * one ? 1 : 0);
+      cut.least = min_p < 1.f ? (least ? least : 1) : one;
     }
     uint64_t total = 0;
     bool summed = false;
-    const float inv = (float)kBins / 43.5f / fmaxf(temp, 1e-30f);   // weights end at 2^-62.5 = e^-43.3
-    if (top_k > 0 && top_k < V) {
-      cut = find_cut<false>(sm, row, V, w, inv, cut, (uint64_t)top_k, &total);
-      summed = true;
-    }
+    const float inv = (float)kBins / 43.5f / tt;   // weights end at 2^-62.5 = e^-43.3
+    if (top_k > 0 && top_k < V) cut = find_cut<false>(sm, row, V, w, inv, cut, (uint64_t)top_k, nullptr);
     if (by_sum) {
-      if (!summed) {
-        uint64_t s = 0;
-        for_tokens(row, 0, V, tid, kThreads, [&](int i, float x) { s += cut.keeps(key_of(x), i) ? w(x) : 0; });
-        total = block_sum(sm, s);
-      }
+      uint64_t s = 0;
+      for_tokens(row, 0, V, tid, kThreads, [&](int i, float x) { s += cut.keeps(key_of(x), i) ? cut.of(w(x)) : 0; });
+      total = block_sum(sm, s);
       const uint64_t f = fixed64(fmaxf(top_p, 0.f));
       const uint64_t want = __umul64hi(f, total) + (f * total ? 1 : 0);   // p total, rounded up
       cut = find_cut<true>(sm, row, V, w, inv, cut, want ? want : 1, &total);
@@ -366,7 +372,7 @@ __global__ void __launch_bounds__(kThreads) token_sample_kernel(const __grid_con
       const int len = ((end - begin + kWarps - 1) / kWarps + 7) / 8 * 8;
       const int b0 = min(end, begin + warp * len), b1 = min(end, b0 + len);
       uint64_t s = 0;
-      for_tokens(row, b0, b1, lane, 32, [&](int i, float x) { s += cut.keeps(key_of(x), i) ? w(x) : 0; });
+      for_tokens(row, b0, b1, lane, 32, [&](int i, float x) { s += cut.keeps(key_of(x), i) ? cut.of(w(x)) : 0; });
       if (level == 0) {
         if (!summed) total = block_sum(sm, s);
         const float u = __ldg(p.u + r);
@@ -379,12 +385,11 @@ __global__ void __launch_bounds__(kThreads) token_sample_kernel(const __grid_con
     }
     if (warp == 0) {
       int found = -1;
-      uint64_t mass = 0;
       for (int i0 = begin; i0 < end && found < 0; i0 += 32) {
         const int i = i0 + lane;
         float x = i < end ? ld_f32(row + i) : kNegInf;
         if (x != x) x = kNegInf;
-        const uint64_t own = i < end && cut.keeps(key_of(x), i) ? w(x) : 0;
+        const uint64_t own = i < end && cut.keeps(key_of(x), i) ? cut.of(w(x)) : 0;
         uint64_t upto = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -392,18 +397,16 @@ __global__ void __launch_bounds__(kThreads) token_sample_kernel(const __grid_con
           if (lane >= o) upto += v;
         }
         const uint32_t past = __ballot_sync(0xffffffffu, upto > target);
-        if (past) {
-          found = i0 + __ffs(past) - 1;
-          mass = __shfl_sync(0xffffffffu, own, __ffs(past) - 1);
-        }
+        if (past) found = i0 + __ffs(past) - 1;
         target -= __shfl_sync(0xffffffffu, upto, 31);
       }
       if (lane == 0) {
         p.ids[r] = found;
         if (p.logprob) {
-          float x = found >= 0 ? ld_f32(row + found) : w.most;
-          const double z = x == w.most ? 0.0 : ((double)x - (double)w.most) / (double)fmaxf(temp, 1e-30f);
-          p.logprob[r] = (float)(z - log((double)total) + (double)w.shift * 0.6931471805599453);
+          const float x = found >= 0 ? ld_f32(row + found) : w.most;
+          const float z = x == w.most ? 0.f : (x - w.most) / tt;
+          // the sum is at least the largest weight: its logarithm by that of its 24 leading bits
+          p.logprob[r] = z - logf((float)total * __uint_as_float((uint32_t)(127 - w.shift) << 23));
         }
       }
     }
