@@ -1,11 +1,13 @@
 // Drawing of tokens (declaration in include/ssdscan.h): temperature, top-k, min-p, top-p and the inverse of the running
-// sum at a given random number, one block a row.
+// sum at a given random number, a block a row, or up to eight (a cluster) where there are few rows.
 // A choice hangs on sums over the whole vocabulary, next to which the border between two tokens is at times 1e-6 wide:
 // fp32 sums would draw another token in one row of a few hundred, and in another order another one.  So weights are
 // fixed-point numbers, 2^s for the largest logit with V 2^s <= 2^62, and their sums are exact in any order.  A weight is
 // 2^-t with t = (largest - logit) log2(e) / temperature carried as two floats (fp64 would take 44 us for one addition per
-// value of 512 x 50000), its fraction as 32 bits, and a polynomial in 32-bit integers (a fit of degree 8; it is off by
-// at most 3 units of 2^-31).
+// value of 512 x 50000): 256 values of 2^-j/256 as 32-bit integers, made by a polynomial (a fit of degree 8, off by at most
+// 3 units of 2^-31), and what is left of the exponent, below 1/512, in fp32.  (A polynomial in integers for every weight,
+// with its conversions, took three times as long.)
+#include <cooperative_groups.h>
 #include <math.h>
 #include <string.h>
 
@@ -13,6 +15,8 @@
 
 namespace ssd {
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kBins = 1024;      // of the logits below the largest, over the range in which weights are not zero
@@ -30,33 +34,39 @@ struct SampleParams {
   float temperature_all, top_p_all, min_p_all;
 };
 
+// 2^31 2^-f for a fraction of 32 bits.
+__device__ __forceinline__ uint32_t exp2_fraction(uint32_t f) {
+  uint32_t m = 0x7ddu;
+  m = 0x7a43u - __umulhi(f, m);
+  m = 0x50690u - __umulhi(f, m);
+  m = 0x2badc5u - __umulhi(f, m);
+  m = 0x13b299cu - __umulhi(f, m);
+  m = 0x71ac1ffu - __umulhi(f, m);
+  m = 0x1ebfbdfau - __umulhi(f, m);
+  m = 0x58b90bfcu - __umulhi(f, m);
+  return 0x80000000u - __umulhi(f, m);
+}
+
 // The weight of a logit.
 struct Weight {
+  const uint2* table;   // 2^31 2^-j/256 as an integer and as a float
   float most, ch, cl;   // largest logit; log2(e) / temperature in two parts
   int shift;
-  __device__ __forceinline__ uint64_t operator()(float x) const {
-    if (x == most) return 1ull << shift;
+  __device__ __forceinline__ uint64_t operator()(float x) const {   // without a branch
     const float d = most - x;
     const float ph = d * ch;
-    if (!(ph < 62.5f)) return 0;   // also an infinite largest logit, and NaN of -inf at an infinite temperature
     const float back = d - most, dl = (most - (d - back)) - (x + back);   // what d's rounding left
     const float pl = fmaf(d, ch, -ph) + fmaf(d, cl, dl * ch);
-    const float whole = truncf(ph);
-    // fraction in units of 2^-32, the small part added as an integer
-    int64_t t = (int64_t)(((uint64_t)(uint32_t)whole << 32) + __float2uint_rz((ph - whole) * 4294967296.f));
-    t += __float2ll_rn(pl * 4294967296.f);
-    t = t < 0 ? 0 : t;
-    const uint32_t f = (uint32_t)t, n = (uint32_t)(t >> 32);
-    uint32_t m = 0x7ddu;
-    m = 0x7a43u - __umulhi(f, m);
-    m = 0x50690u - __umulhi(f, m);
-    m = 0x2badc5u - __umulhi(f, m);
-    m = 0x13b299cu - __umulhi(f, m);
-    m = 0x71ac1ffu - __umulhi(f, m);
-    m = 0x1ebfbdfau - __umulhi(f, m);
-    m = 0x58b90bfcu - __umulhi(f, m);
-    m = 0x80000000u - __umulhi(f, m);
-    return n > 62 ? 0 : ((uint64_t)m << (shift - 31)) >> n;
+    // the nearest 256th, by an addition that leaves its number in the lowest bits
+    const float at = fmaf(ph, 256.f, 12582912.f);
+    const int k = __float_as_int(at) - 0x4b400000;
+    const float a = -0.693147181f * (fmaf(at - 12582912.f, -1.f / 256.f, ph) + pl);
+    const float g = fmaf(a * a, fmaf(a, 1.f / 6.f, 0.5f), a);   // e^a - 1, |a| < 0.0014
+    const uint2 t = table[k & 255];
+    const uint32_t m = t.x + (uint32_t)(__float_as_int(fmaf(__uint_as_float(t.y), g, 12582912.f)) - 0x4b400000);
+    const uint64_t w = ((uint64_t)m << (shift - 31)) >> ((k >> 8) & 63);
+    // nothing far below, beneath an infinite largest logit, or of -inf at an infinite temperature (NaN)
+    return x == most ? 1ull << shift : ph < 62.5f ? w : 0;
   }
 };
 
@@ -66,8 +76,10 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// f(index, logit) for the tokens [begin, end) of a row, spread over `threads` of which this is `t`.  NaN is -inf.
-template <typename T, typename F>
+// f(index, logit) for the tokens [begin, end) of a row, spread over `threads` of which this is `t`.  NaN is -inf.  U vectors
+// are on their way at once; one where f is long (its code is there W U times: with four of eight values, 1400
+// instructions a pass, fetching them took most of the time).
+template <int U, typename T, typename F>
 __device__ __forceinline__ void for_tokens(const T* row, int begin, int end, int t, int threads, const F& f) {
   constexpr int W = 16 / (int)sizeof(T);
   auto one = [&](int i, float x) { f(i, x != x ? kNegInf : x); };
@@ -76,41 +88,59 @@ __device__ __forceinline__ void for_tokens(const T* row, int begin, int end, int
   for (int i = begin + t; i < begin + lead; i += threads) one(i, ld_f32(row + i));
   const int start = begin + lead, nvec = (end - start) / W;
   int v = t;
-  for (; v + 3 * threads < nvec; v += 4 * threads) {
-    typename Pack<T, W>::Raw r[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) r[k] = Pack<T, W>::raw(row + start + (int64_t)(v + k * threads) * W);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float2 x[W / 2];
-      Pack<T, W>::unpack(r[k], x);
-#pragma unroll
-      for (int j = 0; j < W / 2; ++j) {
-        one(start + (v + k * threads) * W + 2 * j, x[j].x);
-        one(start + (v + k * threads) * W + 2 * j + 1, x[j].y);
-      }
-    }
-  }
-  for (; v < nvec; v += threads) {
+  auto vector = [&](const typename Pack<T, W>::Raw& r, int at) {
     float2 x[W / 2];
-    Pack<T, W>::unpack(Pack<T, W>::raw(row + start + (int64_t)v * W), x);
+    Pack<T, W>::unpack(r, x);
 #pragma unroll
     for (int j = 0; j < W / 2; ++j) {
-      one(start + v * W + 2 * j, x[j].x);
-      one(start + v * W + 2 * j + 1, x[j].y);
+      one(start + at * W + 2 * j, x[j].x);
+      one(start + at * W + 2 * j + 1, x[j].y);
+    }
+  };
+  if constexpr (U > 1) {
+    for (; v + (U - 1) * threads < nvec; v += U * threads) {
+      typename Pack<T, W>::Raw r[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) r[k] = Pack<T, W>::raw(row + start + (int64_t)(v + k * threads) * W);
+#pragma unroll
+      for (int k = 0; k < U; ++k) vector(r[k], v + k * threads);
     }
   }
+  for (; v < nvec; v += threads) vector(Pack<T, W>::raw(row + start + (int64_t)v * W), v);
   for (int i = start + nvec * W + t; i < end; i += threads) one(i, ld_f32(row + i));
 }
 
 struct SampleSmem {
+  uint2 table[256];
   uint64_t part[kWarps];
+  uint64_t of_block[2][8];
   uint32_t count[kBins], low[kBins], high[kBins];   // of a bin: tokens, sum of weights
-  uint32_t list_key[kList];
-  int32_t list_id[kList];
-  uint64_t list_w[kList];
+  uint64_t list[kList], list_w[kList];   // (key, falling index) of a bin's tokens, and their weights
   uint64_t out[4];
   int32_t listed;
+};
+
+// The blocks of a row.  Each has a slice of the vocabulary; sums and choices are the same in all of them.
+template <bool kMany>
+struct Row {
+  SampleSmem& sm;
+  int rank, blocks;
+  int turn;   // of of_block: a block may be a reduction ahead of another's reading
+  __device__ __forceinline__ void sync() const {
+    if constexpr (kMany) cg::this_cluster().sync();
+    else __syncthreads();
+  }
+  __device__ __forceinline__ SampleSmem& of(int r) const {
+    if constexpr (kMany) return *cg::this_cluster().map_shared_rank(&sm, r);
+    else return sm;
+  }
+  // Every block's value to every block.
+  __device__ __forceinline__ const uint64_t* exchange(uint64_t mine) {
+    turn ^= 1;
+    if (threadIdx.x < blocks) of(threadIdx.x).of_block[turn][rank] = mine;
+    sync();
+    return sm.of_block[turn];
+  }
 };
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
@@ -124,6 +154,16 @@ __device__ __forceinline__ uint64_t block_sum(SampleSmem& sm, uint64_t v) {
   if ((threadIdx.x & 31) == 0) sm.part[threadIdx.x >> 5] = v;
   __syncthreads();
   return warp_sum(sm.part[threadIdx.x & 31]);
+}
+template <bool kMany>
+__device__ __forceinline__ uint64_t row_sum(Row<kMany>& row, uint64_t v) {
+  v = block_sum(row.sm, v);
+  if constexpr (kMany) {
+    const uint64_t* all = row.exchange(v);
+    v = 0;
+    for (int r = 0; r < row.blocks; ++r) v += all[r];
+  }
+  return v;
 }
 // Number of the first of 32 warps' sums whose running sum exceeds `target`, and the sum before it.
 __device__ __forceinline__ int pick_warp(SampleSmem& sm, uint64_t mine, uint64_t target, uint64_t* before) {
@@ -163,16 +203,17 @@ __device__ __forceinline__ int bin_of(const Weight& w, float inv, float x) {
 // The first token, in falling order, at which the running count (kMass: the running sum of weights) of what `have` keeps
 // reaches `want` >= 1; all of `have` where it never does.  With kMass *sum is the weights' sum up to it on return.
 // (A count takes no account of min_p: what that leaves is a beginning of the same order.)
-template <bool kMass, typename T>
-__device__ Cut find_cut(SampleSmem& sm, const T* row, int V, const Weight& w, float inv, const Cut& have, uint64_t want,
-                        uint64_t* sum) {
+template <bool kMass, bool kMany, typename T>
+__device__ Cut find_cut(Row<kMany>& all, const T* row, int begin, int end, int V, const Weight& w, float inv,
+                        const Cut& have, uint64_t want, uint64_t* sum) {
+  SampleSmem& sm = all.sm;
   const int tid = threadIdx.x, lane = tid & 31;
   __syncthreads();
   sm.count[tid] = 0;
   sm.low[tid] = sm.high[tid] = 0;
   if (tid == 0) sm.listed = 0;
   __syncthreads();
-  for_tokens(row, 0, V, tid, kThreads, [&](int i, float x) {
+  for_tokens<1>(row, begin, end, tid, kThreads, [&](int i, float x) {
     if (x == kNegInf || !have.keeps(key_of(x), i)) return;
     const int b = bin_of(w, inv, x);
     if constexpr (kMass) {
@@ -187,10 +228,16 @@ __device__ Cut find_cut(SampleSmem& sm, const T* row, int V, const Weight& w, fl
       atomicAdd(&sm.count[b], 1u);
     }
   });
-  __syncthreads();
+  all.sync();
   // the bin in which it happens: sums over 32 bins by warp, then within
-  uint64_t before;
-  const uint64_t mine = kMass ? (uint64_t)sm.high[tid] << 32 | sm.low[tid] : sm.count[tid];
+  uint64_t before, mine = 0;
+  uint32_t tokens = 0;
+  for (int r = 0; r < all.blocks; ++r) {
+    const SampleSmem& o = all.of(r);
+    const uint32_t c = o.count[tid];
+    tokens += c;
+    mine += kMass ? (uint64_t)o.high[tid] << 32 | o.low[tid] : c;
+  }
   const int warp = pick_warp(sm, mine, want - 1, &before);
   if ((tid >> 5) == warp) {
     uint64_t upto = mine;
@@ -205,53 +252,54 @@ __device__ Cut find_cut(SampleSmem& sm, const T* row, int V, const Weight& w, fl
       sm.out[0] = past ? (uint64_t)tid : kBins;
       sm.out[1] = want - (before + upto - mine);   // still wanted within the bin
       sm.out[2] = before + upto - mine;
+      sm.out[3] = tokens;
     }
   }
   __syncthreads();
   const int bin = (int)sm.out[0];
   if (bin == kBins) {
-    if (kMass) *sum = block_sum(sm, mine);
+    if (kMass) *sum = block_sum(sm, mine);   // bins of the whole row
+    all.sync();   // the others may still be reading this block's bins
     return have;
   }
   const uint64_t rest = sm.out[1], base = sm.out[2];
-  const uint32_t n = sm.count[bin];
+  const uint32_t n = (uint32_t)sm.out[3];
   auto in_bin = [&](int i, float x, uint32_t& k) {
     if (x == kNegInf || bin_of(w, inv, x) != bin) return false;
     k = key_of(x);
     return have.keeps(k, i) && (!kMass || have.of(w(x)) != 0);
   };
-  if (n <= kList) {   // every one of the bin's tokens counts those before it
-    for_tokens(row, 0, V, tid, kThreads, [&](int i, float x) {
+  if (n <= kList) {   // every one of the bin's tokens, in the first block, counts those before it
+    SampleSmem& to = all.of(0);
+    for_tokens<1>(row, begin, end, tid, kThreads, [&](int i, float x) {
       uint32_t k;
       if (!in_bin(i, x, k)) return;
-      const int at = atomicAdd(&sm.listed, 1);
-      sm.list_key[at] = k;
-      sm.list_id[at] = i;
-      if (kMass) sm.list_w[at] = w(x);
+      const int at = atomicAdd(&to.listed, 1);
+      to.list[at] = (uint64_t)k << 32 | (uint32_t)~i;
+      to.list_w[at] = kMass ? w(x) : 1;
     });
-    __syncthreads();
-    if (tid < (int)n) {
-      const uint32_t k = sm.list_key[tid];
-      const int id = sm.list_id[tid];
-      const uint64_t own = kMass ? sm.list_w[tid] : 1;
-      uint64_t above = 0;
-      for (int j = 0; j < (int)n; ++j) {
-        const uint32_t kj = sm.list_key[j];
-        if (kj > k || (kj == k && sm.list_id[j] < id)) above += kMass ? sm.list_w[j] : 1;
-      }
-      if (above < rest && above + own >= rest) {
-        sm.out[0] = k;
-        sm.out[1] = (uint64_t)(uint32_t)id;
-        sm.out[3] = base + above + own;
+    all.sync();
+    if (all.rank == 0) {   // a warp a token
+      for (int e = tid >> 5; e < (int)n; e += kWarps) {
+        const uint64_t mine = sm.list[e], own = sm.list_w[e];
+        uint64_t above = 0;
+        for (int j = lane; j < (int)n; j += 32) above += sm.list[j] > mine ? sm.list_w[j] : 0;
+        above = warp_sum(above);
+        if (above < rest && above + own >= rest && lane < all.blocks) {
+          SampleSmem& o = all.of(lane);
+          o.out[0] = mine >> 32;
+          o.out[1] = (uint32_t)~(uint32_t)mine;
+          o.out[3] = base + above + own;
+        }
       }
     }
-    __syncthreads();
+    all.sync();
     if (kMass) *sum = sm.out[3];
     return {(uint32_t)sm.out[0], (int32_t)(uint32_t)sm.out[1], have.least};
   }
   // more than fit (many equal logits): by bisection of their keys, a pass over the row a step
   uint32_t lo = 0xffffffffu, hi = 0;
-  for_tokens(row, 0, V, tid, kThreads, [&](int i, float x) {
+  for_tokens<1>(row, begin, end, tid, kThreads, [&](int i, float x) {
     uint32_t k;
     if (!in_bin(i, x, k)) return;
     lo = min(lo, k);
@@ -262,17 +310,24 @@ __device__ Cut find_cut(SampleSmem& sm, const T* row, int V, const Weight& w, fl
   __syncthreads();
   if (lane == 0) sm.part[tid >> 5] = (uint64_t)hi << 32 | lo;
   __syncthreads();
-  const uint64_t pair = sm.part[lane];
+  uint64_t pair = sm.part[lane];
   lo = __reduce_min_sync(0xffffffffu, (uint32_t)pair);
   hi = __reduce_max_sync(0xffffffffu, (uint32_t)(pair >> 32));
+  if constexpr (kMany) {
+    const uint64_t* pairs = all.exchange((uint64_t)hi << 32 | lo);
+    for (int r = 0; r < all.blocks; ++r) {
+      lo = min(lo, (uint32_t)pairs[r]);
+      hi = max(hi, (uint32_t)(pairs[r] >> 32));
+    }
+  }
   auto value_of = [](uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); };
   auto summed = [&](auto&& f) {   // the sum of f(key, index) over the bin's tokens
     uint64_t s = 0;
-    for_tokens(row, 0, V, tid, kThreads, [&](int i, float x) {
+    for_tokens<1>(row, begin, end, tid, kThreads, [&](int i, float x) {
       uint32_t k;
       if (in_bin(i, x, k)) s += f(k, i);
     });
-    return block_sum(sm, s);
+    return row_sum(all, s);
   };
   // the largest key with count (sum) of keys >= it at least `rest`
   while (lo < hi) {
@@ -298,11 +353,23 @@ __device__ __forceinline__ uint64_t fixed64(float v) {   // v in [0, 1) as v 2^6
   return __float2ull_rz(v * 18446744073709551616.f);
 }
 
-template <typename T>
+template <typename T, bool kMany>
 __global__ void __launch_bounds__(kThreads) token_sample_kernel(const __grid_constant__ SampleParams p) {
   __shared__ SampleSmem sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, V = p.V;
-  for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
+  Row<kMany> all = {sm, 0, 1, 0};
+  if constexpr (kMany) {
+    all.rank = (int)cg::this_cluster().block_rank();
+    all.blocks = (int)cg::this_cluster().num_blocks();
+  }
+  // this block's slice, in whole vectors
+  const int slice = ((V + all.blocks - 1) / all.blocks + 7) / 8 * 8, begin = min(V, all.rank * slice), end = min(V, begin + slice);
+  if (tid < 256) {
+    const uint32_t m = exp2_fraction((uint32_t)tid << 24);
+    sm.table[tid] = make_uint2(m, __float_as_uint((float)m));
+  }
+  all.sync();   // every block of the row has begun
+  for (int64_t r = blockIdx.x / all.blocks; r < p.rows; r += gridDim.x / all.blocks) {
     const T* row = static_cast<const T*>(p.logits) + r * p.stride;
     float temp = p.temperature ? __ldg(p.temperature + r) : p.temperature_all;
     const float top_p = p.top_p ? __ldg(p.top_p + r) : p.top_p_all;
@@ -313,29 +380,29 @@ __global__ void __launch_bounds__(kThreads) token_sample_kernel(const __grid_con
     if (!(min_p > 0.f)) min_p = 0.f;
     // the largest logit and its first index
     uint64_t best = 0;
-    for_tokens(row, 0, V, tid, kThreads, [&](int i, float x) {
+    for_tokens<4>(row, begin, end, tid, kThreads, [&](int i, float x) {
       const uint64_t k = (uint64_t)key_of(x) << 32 | (uint32_t)~i;
       best = k > best ? k : best;
     });
+    auto larger = [](uint64_t a, uint64_t b) { return a > b ? a : b; };
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const uint64_t v = __shfl_xor_sync(0xffffffffu, best, o);
-      best = v > best ? v : best;
-    }
+    for (int o = 16; o; o >>= 1) best = larger(best, __shfl_xor_sync(0xffffffffu, best, o));
     __syncthreads();
     if (lane == 0) sm.part[warp] = best;
     __syncthreads();
     best = sm.part[lane];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const uint64_t v = __shfl_xor_sync(0xffffffffu, best, o);
-      best = v > best ? v : best;
+    for (int o = 16; o; o >>= 1) best = larger(best, __shfl_xor_sync(0xffffffffu, best, o));
+    if constexpr (kMany) {
+      const uint64_t* of = all.exchange(best);
+      for (int b = 0; b < all.blocks; ++b) best = larger(best, of[b]);
     }
     const uint32_t top_key = (uint32_t)(best >> 32);
     Weight w;
+    w.table = sm.table;
     w.most = __uint_as_float(top_key & 0x80000000u ? top_key & 0x7fffffffu : ~top_key);
     if (w.most == kNegInf || temp == 0.f) {
-      if (tid == 0) {
+      if (tid == 0 && all.rank == 0) {
         p.ids[r] = w.most == kNegInf ? -1 : (int64_t)(uint32_t)~(uint32_t)best;
         if (p.logprob) p.logprob[r] = w.most == kNegInf ? NAN : 0.f;
       }
@@ -352,54 +419,66 @@ __global__ void __launch_bounds__(kThreads) token_sample_kernel(const __grid_con
       const uint64_t least = __umul64hi(f, one) + (f * one ? 1 : 0);
       cut.least = min_p < 1.f ? (least ? least : 1) : one;
     }
+    auto kept = [&](int i, float x) -> uint64_t { return cut.keeps(key_of(x), i) ? cut.of(w(x)) : 0; };
     uint64_t total = 0;
     bool summed = false;
     const float inv = (float)kBins / 43.5f / tt;   // weights end at 2^-62.5 = e^-43.3
-    if (top_k > 0 && top_k < V) cut = find_cut<false>(sm, row, V, w, inv, cut, (uint64_t)top_k, nullptr);
+    if (top_k > 0 && top_k < V)
+      cut = find_cut<false>(all, row, begin, end, V, w, inv, cut, (uint64_t)top_k, nullptr);
     if (by_sum) {
       uint64_t s = 0;
-      for_tokens(row, 0, V, tid, kThreads, [&](int i, float x) { s += cut.keeps(key_of(x), i) ? cut.of(w(x)) : 0; });
-      total = block_sum(sm, s);
+      for_tokens<1>(row, begin, end, tid, kThreads, [&](int i, float x) { s += kept(i, x); });
+      total = row_sum(all, s);
       const uint64_t f = fixed64(fmaxf(top_p, 0.f));
       const uint64_t want = __umul64hi(f, total) + (f * total ? 1 : 0);   // p total, rounded up
-      cut = find_cut<true>(sm, row, V, w, inv, cut, want ? want : 1, &total);
+      cut = find_cut<true>(all, row, begin, end, V, w, inv, cut, want ? want : 1, &total);
       summed = true;
     }
-    // the draw: sums of 32 parts of the row by warp, of 32 parts of the chosen one, then token by token
-    int begin = 0, end = V;
-    uint64_t target = 0, before;
-    for (int level = 0; level < 2; ++level) {
-      const int len = ((end - begin + kWarps - 1) / kWarps + 7) / 8 * 8;
-      const int b0 = min(end, begin + warp * len), b1 = min(end, b0 + len);
-      uint64_t s = 0;
-      for_tokens(row, b0, b1, lane, 32, [&](int i, float x) { s += cut.keeps(key_of(x), i) ? cut.of(w(x)) : 0; });
-      if (level == 0) {
-        if (!summed) total = block_sum(sm, s);
-        const float u = __ldg(p.u + r);
-        target = u >= 1.f ? total - 1 : u > 0.f ? __umul64hi(fixed64(u), total) : 0;
-      }
-      const int at = pick_warp(sm, s, target, &before);
-      target -= before;
-      end = min(end, begin + (at + 1) * len);
-      begin = min(end, begin + at * len);
+    // the draw: sums of the blocks, of 32 parts of the slice by warp, then the chosen part by the whole block
+    const int len = ((end - begin + kWarps - 1) / kWarps + 7) / 8 * 8;
+    uint64_t s = 0, mine = 0, ahead = 0, before;
+    {
+      const int from = min(end, begin + warp * len), to = min(end, from + len);
+      for_tokens<1>(row, from, to, lane, 32, [&](int i, float x) { s += kept(i, x); });
     }
-    if (warp == 0) {
-      int found = -1;
-      for (int i0 = begin; i0 < end && found < 0; i0 += 32) {
-        const int i = i0 + lane;
-        float x = i < end ? ld_f32(row + i) : kNegInf;
-        if (x != x) x = kNegInf;
-        const uint64_t own = i < end && cut.keeps(key_of(x), i) ? cut.of(w(x)) : 0;
-        uint64_t upto = own;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-          if (lane >= o) upto += v;
+    if (kMany || !summed) {
+      mine = block_sum(sm, s);
+      total = mine;
+      if constexpr (kMany) {
+        const uint64_t* of = all.exchange(mine);
+        total = 0;
+        for (int b = 0; b < all.blocks; ++b) {
+          if (b == all.rank) ahead = total;
+          total += of[b];
         }
-        const uint32_t past = __ballot_sync(0xffffffffu, upto > target);
-        if (past) found = i0 + __ffs(past) - 1;
-        target -= __shfl_sync(0xffffffffu, upto, 31);
       }
+    }
+    const float u = __ldg(p.u + r);
+    uint64_t target = u >= 1.f ? total - 1 : u > 0.f ? __umul64hi(fixed64(u), total) : 0;
+    if (kMany && (target < ahead || target >= ahead + mine)) continue;   // another block's
+    target -= ahead;
+    const int part = pick_warp(sm, s, target, &before), b0 = min(end, begin + part * len), b1 = min(end, b0 + len);
+    target -= before;
+    for (int i0 = b0; i0 < b1; i0 += kThreads) {   // a token a thread
+      const int i = i0 + tid;
+      float x = i < b1 ? ld_f32(row + i) : kNegInf;
+      if (x != x) x = kNegInf;
+      const uint64_t own = i < b1 ? kept(i, x) : 0;
+      const int of = pick_warp(sm, own, target, &before);
+      const uint64_t through = block_sum(sm, own);
+      if (target >= through && i0 + kThreads < b1) {
+        target -= through;
+        continue;
+      }
+      if (warp != of) break;
+      uint64_t upto = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, before + upto > target);
+      const int found = past ? i0 + warp * 32 + __ffs(past) - 1 : -1;
       if (lane == 0) {
         p.ids[r] = found;
         if (p.logprob) {
@@ -409,8 +488,32 @@ __global__ void __launch_bounds__(kThreads) token_sample_kernel(const __grid_con
           p.logprob[r] = z - logf((float)total * __uint_as_float((uint32_t)(127 - w.shift) << 23));
         }
       }
+      break;
     }
   }
+  all.sync();   // no block ends while another may read or write its shared memory
+}
+
+template <typename T>
+cudaError_t launch_sample(const SampleParams& p, cudaStream_t st) {
+  // as many blocks a row as leave one block an SM
+  unsigned blocks = 1;
+  while (blocks < 8 && p.rows * (blocks * 2) <= 152) blocks *= 2;
+  if (blocks == 1) {
+    token_sample_kernel<T, false><<<(unsigned)(p.rows < (1 << 20) ? p.rows : 1 << 20), kThreads, 0, st>>>(p);
+    return cudaGetLastError();
+  }
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = blocks;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.rows * blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, token_sample_kernel<T, true>, p);
 }
 
 }  // namespace
@@ -450,9 +553,7 @@ extern "C" ssd_status token_sample(const token_sample_shape* shape, const void* 
   int bits = 0;
   while ((int64_t)1 << bits < shape->vocab) ++bits;
   p.shift = 62 - bits;
-  const unsigned grid = (unsigned)(shape->rows < (1 << 20) ? shape->rows : 1 << 20);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (shape->io_dtype == SSD_BF16) token_sample_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(p);
-  else token_sample_kernel<float><<<grid, kThreads, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+  const cudaError_t err = shape->io_dtype == SSD_BF16 ? launch_sample<__nv_bfloat16>(p, st) : launch_sample<float>(p, st);
+  return err == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
