@@ -20,6 +20,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kBins = 1024;      // of the logits below the largest, over the range in which weights are not zero
+constexpr int kTail = 384;       // the bin of weights of about 2^-23 of the largest
 constexpr int kList = 1024;      // tokens of one bin that are searched in shared memory
 constexpr float kNegInf = -INFINITY;
 
@@ -45,6 +46,12 @@ __device__ __forceinline__ uint32_t exp2_fraction(uint32_t f) {
   m = 0x1ebfbdfau - __umulhi(f, m);
   m = 0x58b90bfcu - __umulhi(f, m);
   return 0x80000000u - __umulhi(f, m);
+}
+
+__device__ __forceinline__ float exp2f_fast(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 // The weight of a logit.
@@ -200,9 +207,11 @@ __device__ __forceinline__ int bin_of(const Weight& w, float inv, float x) {
   return x == w.most ? 0 : d < (float)(kBins - 1) ? (int)d : kBins - 1;   // NaN (of infinities): the last
 }
 
-// The first token, in falling order, at which the running count (kMass: the running sum of weights) of what `have` keeps
-// reaches `want` >= 1; all of `have` where it never does.  With kMass *sum is the weights' sum up to it on return.
-// (A count takes no account of min_p: what that leaves is a beginning of the same order.)
+// The first token, in falling order, at which the running count of what `have` keeps reaches `want` >= 1 (kMass: the running
+// sum of weights the share `want` 2^-64 of their sum); all of `have` where it never does.  With kMass *sum is the weights'
+// sum up to it on return.  (A count takes no account of min_p: what that leaves is a beginning of the same order.)
+// Most tokens weigh next to nothing: from kTail on their weights are summed in registers, and only if the cut should lie
+// there, which takes a very flat row, they enter the bins in a second pass.
 template <bool kMass, bool kMany, typename T>
 __device__ Cut find_cut(Row<kMany>& all, const T* row, int begin, int end, int V, const Weight& w, float inv,
                         const Cut& have, uint64_t want, uint64_t* sum) {
@@ -213,21 +222,37 @@ __device__ Cut find_cut(Row<kMany>& all, const T* row, int begin, int end, int V
   sm.low[tid] = sm.high[tid] = 0;
   if (tid == 0) sm.listed = 0;
   __syncthreads();
+  uint64_t tail = 0;
+  auto enter = [&](int b, uint64_t m) {
+    // in two halves (a 64-bit addition in shared memory is a loop): the lower one's carry goes with the upper
+    const uint32_t lo = (uint32_t)m, old = atomicAdd(&sm.low[b], lo), up = (uint32_t)(m >> 32) + (old + lo < lo);
+    if (up) atomicAdd(&sm.high[b], up);
+    atomicAdd(&sm.count[b], 1u);
+  };
   for_tokens<1>(row, begin, end, tid, kThreads, [&](int i, float x) {
     if (x == kNegInf || !have.keeps(key_of(x), i)) return;
     const int b = bin_of(w, inv, x);
     if constexpr (kMass) {
       const uint64_t m = have.of(w(x));
-      if (m) {
-        // in two halves (a 64-bit addition in shared memory is a loop): the lower one's carry goes with the upper
-        const uint32_t lo = (uint32_t)m, old = atomicAdd(&sm.low[b], lo), up = (uint32_t)(m >> 32) + (old + lo < lo);
-        if (up) atomicAdd(&sm.high[b], up);
-        atomicAdd(&sm.count[b], 1u);
-      }
+      if (b >= kTail) tail += m;
+      else if (m) enter(b, m);
     } else {
       atomicAdd(&sm.count[b], 1u);
     }
   });
+  if constexpr (kMass) {
+    tail = row_sum(all, tail);
+    const uint64_t head = row_sum(all, (uint64_t)sm.high[tid] << 32 | sm.low[tid]);
+    want = __umul64hi(want, head + tail) + (want * (head + tail) ? 1 : 0);   // the share, rounded up
+    want = want ? want : 1;
+    if (want > head)
+      for_tokens<1>(row, begin, end, tid, kThreads, [&](int i, float x) {
+        if (x == kNegInf || !have.keeps(key_of(x), i)) return;
+        const int b = bin_of(w, inv, x);
+        const uint64_t m = b >= kTail ? have.of(w(x)) : 0;
+        if (m) enter(b, m);
+      });
+  }
   all.sync();
   // the bin in which it happens: sums over 32 bins by warp, then within
   uint64_t before, mine = 0;
@@ -426,21 +451,94 @@ __global__ void __launch_bounds__(kThreads) token_sample_kernel(const __grid_con
     if (top_k > 0 && top_k < V)
       cut = find_cut<false>(all, row, begin, end, V, w, inv, cut, (uint64_t)top_k, nullptr);
     if (by_sum) {
-      uint64_t s = 0;
-      for_tokens<1>(row, begin, end, tid, kThreads, [&](int i, float x) { s += kept(i, x); });
-      total = row_sum(all, s);
-      const uint64_t f = fixed64(fmaxf(top_p, 0.f));
-      const uint64_t want = __umul64hi(f, total) + (f * total ? 1 : 0);   // p total, rounded up
-      cut = find_cut<true>(all, row, begin, end, V, w, inv, cut, want ? want : 1, &total);
+      cut = find_cut<true>(all, row, begin, end, V, w, inv, cut, fixed64(fmaxf(top_p, 0.f)), &total);
       summed = true;
     }
-    // the draw: sums of the blocks, of 32 parts of the slice by warp, then the chosen part by the whole block
+    // the draw: sums of the blocks, of 32 parts of the slice by warp, then the chosen part by the whole block.  Where no
+    // order was needed, the sums are first taken of fp32 weights, whose error is known: 2^-22 by the special function; three
+    // roundings of an exponent e make 2.1 e 2^-24, and the mean of e over the weights is at most log2 V = 20; 2^-24 for
+    // each of a thread's additions.  Only where the number drawn is as near as that to a border between two tokens, a row
+    // in a hundred or so, exact sums follow.
     const int len = ((end - begin + kWarps - 1) / kWarps + 7) / 8 * 8;
+    const int from = min(end, begin + warp * len), to = min(end, from + len);
+    const float u = __ldg(p.u + r);
+    const uint64_t share = u >= 1.f ? ~0ull : u > 0.f ? fixed64(u) : 0;
+    auto last_part = [&](int b0, int b1, uint64_t target, uint64_t total, uint64_t slack) {
+      // a token a thread; whether one was found `slack` away from its borders
+      bool clear = false;
+      for (int i0 = b0; i0 < b1; i0 += kThreads) {
+        const int i = i0 + tid;
+        float x = i < b1 ? ld_f32(row + i) : kNegInf;
+        if (x != x) x = kNegInf;
+        const uint64_t own = i < b1 ? kept(i, x) : 0;
+        uint64_t before;
+        const int of = pick_warp(sm, own, target, &before);
+        const uint64_t through = block_sum(sm, own);
+        if (target >= through && i0 + kThreads < b1) {
+          if (target - through < slack) return false;
+          target -= through;
+          continue;
+        }
+        uint64_t upto = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += v;
+        }
+        const uint64_t here = before + upto;
+        const uint32_t past = __ballot_sync(0xffffffffu, here > target);
+        const bool mine = warp == of && past && lane == __ffs(past) - 1;
+        clear = __syncthreads_or(mine && here - target > slack && target - (here - own) >= slack);
+        if (mine && clear) {
+          p.ids[r] = i;
+          if (p.logprob) {
+            const float z = x == w.most ? 0.f : (x - w.most) / tt;
+            // the sum is at least the largest weight: its logarithm by that of its 24 leading bits
+            p.logprob[r] = z - logf((float)total * __uint_as_float((uint32_t)(127 - w.shift) << 23));
+          }
+        }
+        break;
+      }
+      return clear;
+    };
     uint64_t s = 0, mine = 0, ahead = 0, before;
-    {
-      const int from = min(end, begin + warp * len), to = min(end, from + len);
-      for_tokens<1>(row, from, to, lane, 32, [&](int i, float x) { s += kept(i, x); });
+    if (!summed && cut.key == 0 && cut.last == V && cut.least == 1 && w.ch > 0.f) {   // (not at an infinite temperature)
+      float f0 = 0.f, f1 = 0.f;
+      for_tokens<4>(row, from, to, lane, 32, [&](int i, float x) {
+        const float e = exp2f_fast((x - w.most) * w.ch);
+        if (i & 1) f1 += x == w.most ? 1.f : e;
+        else f0 += x == w.most ? 1.f : e;
+      });
+      const float one = __uint_as_float((uint32_t)(127 + w.shift) << 23);
+      s = __float2ull_rn((f0 + f1) * one);
+      mine = block_sum(sm, s);
+      total = mine;
+      if constexpr (kMany) {
+        const uint64_t* of = all.exchange(mine);
+        total = 0;
+        for (int b = 0; b < all.blocks; ++b) {
+          if (b == all.rank) ahead = total;
+          total += of[b];
+        }
+      }
+      const uint64_t slack = (total >> 24) * (uint64_t)(2 * (len / 64 + 52));   // in the sum before and in the target
+      uint64_t target = __umul64hi(share, total);
+      bool clear = true;
+      if (!kMany || (target >= ahead && target < ahead + mine)) {
+        target -= ahead;
+        const int part = pick_warp(sm, s, target, &before), b0 = min(end, begin + part * len), b1 = min(end, b0 + len);
+        clear = last_part(b0, b1, target - before, total, slack);
+      }
+      bool all_clear = clear;
+      if constexpr (kMany) {
+        const uint64_t* of = all.exchange(clear);
+        for (int b = 0; b < all.blocks; ++b) all_clear = all_clear && of[b];
+      }
+      if (all_clear) continue;
+      ahead = 0;
+      s = 0;
     }
+    for_tokens<1>(row, from, to, lane, 32, [&](int i, float x) { s += kept(i, x); });
     if (kMany || !summed) {
       mine = block_sum(sm, s);
       total = mine;
@@ -453,43 +551,11 @@ __global__ void __launch_bounds__(kThreads) token_sample_kernel(const __grid_con
         }
       }
     }
-    const float u = __ldg(p.u + r);
-    uint64_t target = u >= 1.f ? total - 1 : u > 0.f ? __umul64hi(fixed64(u), total) : 0;
+    uint64_t target = u >= 1.f ? total - 1 : __umul64hi(share, total);
     if (kMany && (target < ahead || target >= ahead + mine)) continue;   // another block's
     target -= ahead;
     const int part = pick_warp(sm, s, target, &before), b0 = min(end, begin + part * len), b1 = min(end, b0 + len);
-    target -= before;
-    for (int i0 = b0; i0 < b1; i0 += kThreads) {   // a token a thread
-      const int i = i0 + tid;
-      float x = i < b1 ? ld_f32(row + i) : kNegInf;
-      if (x != x) x = kNegInf;
-      const uint64_t own = i < b1 ? kept(i, x) : 0;
-      const int of = pick_warp(sm, own, target, &before);
-      const uint64_t through = block_sum(sm, own);
-      if (target >= through && i0 + kThreads < b1) {
-        target -= through;
-        continue;
-      }
-      if (warp != of) break;
-      uint64_t upto = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
-      }
-      const uint32_t past = __ballot_sync(0xffffffffu, before + upto > target);
-      const int found = past ? i0 + warp * 32 + __ffs(past) - 1 : -1;
-      if (lane == 0) {
-        p.ids[r] = found;
-        if (p.logprob) {
-          const float x = found >= 0 ? ld_f32(row + found) : w.most;
-          const float z = x == w.most ? 0.f : (x - w.most) / tt;
-          // the sum is at least the largest weight: its logarithm by that of its 24 leading bits
-          p.logprob[r] = z - logf((float)total * __uint_as_float((uint32_t)(127 - w.shift) << 23));
-        }
-      }
-      break;
-    }
+    last_part(b0, b1, target - before, total, 0);
   }
   all.sync();   // no block ends while another may read or write its shared memory
 }

@@ -210,3 +210,21 @@ def test_refusals_of_the_binding():
         pkg.token_sample(x[0], u)
     with pytest.raises(ValueError):
         pkg.token_sample(x.t(), u)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [40, 3001, 50000])
+def test_numbers_at_and_beside_the_borders(V):
+    """Random numbers that lie on a border between two tokens, as near as fp32 comes, and flat rows, whose borders lie
+    everywhere: the draw is the exact one."""
+    g = torch.Generator().manual_seed(9)
+    n = 24
+    x = torch.randn(n, V, generator=g) * torch.linspace(0, 4, n)[:, None]
+    shares = torch.softmax(x.double(), 1).cumsum(1)
+    at = torch.randint(0, V, (n,), generator=g)
+    u = shares[torch.arange(n), at].float().clamp(max=1 - 2.0 ** -24)
+    up = torch.nextafter(u, torch.ones(())).clamp(max=1 - 2.0 ** -24)
+    for uu in (u, up, torch.nextafter(u, torch.zeros(()))):
+        for rows in (n, 1):   # a block a row, and several
+            d = x[:rows].cuda(), uu[:rows].cuda()
+            compare(*d, *pkg.token_sample(*d))
