@@ -18,6 +18,7 @@
 
 #include "delta_tc.cuh"
 #include "launch.h"
+#include "pack.cuh"
 
 namespace ssd {
 namespace {
@@ -517,10 +518,22 @@ __global__ void __launch_bounds__(128) delta_step_kernel(const __grid_constant__
       }
     }
 #pragma unroll
-  for (int e = 0; e < KE; ++e) {
+  for (int e = 0; e < KE; e += 4) {
     const int c = key_of(e, l);
-    k[e] = c < p.K ? ld_f32(kp + c) : 0.f;
-    q[e] = c < p.K ? ld_f32(qp + c) : 0.f;
+    if constexpr (kWide) {
+      using K4 = Pack<T, 4>;
+      float2 a[2], b[2];
+      K4::unpack(c < p.K ? K4::raw(kp + c) : K4::none(), a);
+      K4::unpack(c < p.K ? K4::raw(qp + c) : K4::none(), b);
+      k[e] = a[0].x, k[e + 1] = a[0].y, k[e + 2] = a[1].x, k[e + 3] = a[1].y;
+      q[e] = b[0].x, q[e + 1] = b[0].y, q[e + 2] = b[1].x, q[e + 3] = b[1].y;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        k[e + j] = c + j < p.K ? ld_f32(kp + c + j) : 0.f;
+        q[e + j] = c + j < p.K ? ld_f32(qp + c + j) : 0.f;
+      }
+    }
   }
 #pragma unroll
   for (int r = 0; r < N; ++r)
@@ -711,7 +724,9 @@ cudaError_t launch_step_as(Params p, bool wide, cudaStream_t st) {
 }
 template <typename T>
 cudaError_t launch_step(const Params& p, cudaStream_t st) {
-  const bool wide = p.K % 4 == 0 && !misaligned(p.init, 16) && !misaligned(p.final_state, 16);
+  const uint64_t keys = reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.k) |
+                        (uint64_t)(p.qs[0] | p.qs[2] | p.ks[0] | p.ks[2]) * sizeof(T);
+  const bool wide = p.K % 4 == 0 && !misaligned(p.init, 16) && !misaligned(p.final_state, 16) && keys % (4 * sizeof(T)) == 0;
   if (p.K <= 64) return launch_step_as<T, 8, 2>(p, wide, st);
   if (p.K <= 128) return launch_step_as<T, 16, 2>(p, wide, st);
   return launch_step_as<T, 32, 1>(p, wide, st);

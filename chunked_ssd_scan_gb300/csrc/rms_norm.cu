@@ -21,6 +21,8 @@ namespace {
 constexpr float kMost = 448.f;
 constexpr int kBlock = RMS_NORM_BLOCK;
 constexpr int kWideThreads = 512;
+constexpr int kRowThreads = 512;   // of a block whose rows stay in registers at most; one vector a thread is held to 64
+                                   // registers all the same (16384 x 2048 bf16 backward 51 us, with what it likes 56)
 
 struct NormParams {
   const void *x, *res, *dy;     // backward: x is h, res is dresidual
@@ -87,7 +89,7 @@ __device__ __forceinline__ float scale_of(float most) {
 
 // Rows whose vectors fit the registers: N_ vectors of V values a thread.
 template <typename T, int V, int N_, int Q>
-__global__ void __launch_bounds__(1024) rms_forward_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(N_ == 1 ? 1024 : kRowThreads) rms_forward_kernel(const __grid_constant__ NormParams p) {
   using K = Pack<T, V>;
   __shared__ RowReduce sm;
   const int tpr = p.tpr, rows = blockDim.x / tpr, sub = threadIdx.x / tpr, t = threadIdx.x % tpr;
@@ -240,7 +242,7 @@ __global__ void __launch_bounds__(kWideThreads) rms_forward_wide_kernel(const __
 }
 
 template <typename T, int V, int N_>
-__global__ void __launch_bounds__(1024) rms_backward_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(N_ == 1 ? 1024 : kRowThreads) rms_backward_kernel(const __grid_constant__ NormParams p) {
   using K = Pack<T, V>;
   __shared__ RowReduce sm;
   const int tpr = p.tpr, rows = blockDim.x / tpr, sub = threadIdx.x / tpr, t = threadIdx.x % tpr;
@@ -360,7 +362,13 @@ __global__ void __launch_bounds__(1024) rms_join_kernel(const float* partial, fl
   const int part = threadIdx.x >> 5;
   float s = 0.f;
   if (c < C)
-    for (int64_t r = part; r < rows; r += 32) s += partial[r * C + c];
+    for (int64_t r0 = part; r0 < rows; r0 += 32 * 8) {   // eight on their way at once
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = r0 + 32 * e < rows ? partial[(r0 + 32 * e) * C + c] : 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += f[e];
+    }
   sm[part][threadIdx.x & 31] = s;
   __syncthreads();
   s = warp_sum(sm[threadIdx.x & 31][part]);
@@ -383,7 +391,9 @@ ssd_status check_shape(const rms_norm_shape* s, bool back) {
 }
 
 // Vectors of the widest size that every row starts on and C divides, threads a row and vectors a thread; 0 vectors:
-// a row does not fit the registers.
+// a row does not fit the registers.  At most 256 threads a row where more vectors a thread avoid more (us, forward and
+// backward of bf16 rows: 10007 x 2560 by 160 threads 43 / 45, by 320 45 / 56; 16384 x 4096 by 256 90 / 83, by 512 88 / 120;
+// 4000 x 8192 by 256 45, by 512 49), and no fewer than one vector needs (16384 x 2048 by 256 46 / 52, by 128 47 / 51).
 struct Form {
   int v, n, tpr, rows;
 };
@@ -398,8 +408,7 @@ Form form_of(uint64_t bits, size_t e, int64_t C, int most_n, bool block_scales) 
   const int64_t nvec = C / f.v;
   for (int n = 1; n <= most_n; n *= 2) {
     const int64_t tpr = ((nvec + n - 1) / n + 31) / 32 * 32;
-    if (tpr > 512 && n < most_n) continue;
-    if (tpr > 1024) break;
+    if (tpr > (n < most_n ? kRowThreads / 2 : kRowThreads)) continue;
     f.n = n;
     f.tpr = (int)tpr;
     break;

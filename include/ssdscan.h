@@ -559,10 +559,11 @@ size_t gated_delta_rule_workspace_bytes(const gated_delta_rule_shape* shape, int
  * beta [b,T,H] f32 strided; init_state (NULL = zeros) and final_state (NULL = not written)
  * [b,H,V,K] f32.  states: NULL, or f32 [b, ceil(T / GATED_DELTA_RULE_CHUNK), H, V, K] that receives
  * the state before steps 0, 64, 128, ... for gated_delta_rule_backward.  y may be NULL.
- * g below -200 is a decay of zero, as in fp32.  States and sums are fp32.  With bf16 inputs whose K
- * and V are multiples of 8 and whose rows start on 16-byte boundaries, sequences longer than a few
- * steps run on the tensor cores, where what is computed on the way (the state, the writes, the inverse
- * of a chunk's triangular system) enters a product as two bf16 terms, 16 bits of mantissa.
+ * g below -200 is a decay of zero, as in fp32.  States and sums are fp32.  bf16 inputs with K <= 128, K
+ * and V multiples of 8, rows on 16-byte boundaries and 32 steps or more run on the tensor cores, where
+ * what is computed on the way (the state, the writes, the inverse of a chunk's triangular system)
+ * enters a product as two bf16 terms, 16 bits of mantissa: states are off by some 4e-6 of their size.
+ * There a NaN or an infinity may reach the outputs of the steps before it in its chunk of 64 too.
  * Asynchronous on `stream`; INVALID_ARG / UNSUPPORTED / WORKSPACE leave every output untouched.
  */
 ssd_status gated_delta_rule_forward(const gated_delta_rule_shape* shape, const void* q,
@@ -662,8 +663,8 @@ typedef struct token_sample_shape {
  * which the running sum of the kept weights exceeds u times their sum.  temperature 0 takes the largest
  * logit (the lowest index of equal ones).  ids [n] int64; logprob [n] f32 (may be NULL): the logarithm
  * of the drawn token's share.  NaN counts as -inf; +inf weighs 1 and all else nothing; a row of only
- * -inf draws -1, with logprob NaN.  Weights are fixed-point numbers whose sums do not depend on an
- * order: 2^-31 of a weight, 2^-42 of the largest.
+ * -inf draws -1, with logprob NaN.  A choice is made by weights that are fixed-point numbers (off by
+ * a few 2^-31 of a weight, and by less than 2^-41 of the largest), whose sums do not depend on an order.
  * temperature, top_p, min_p [n] f32 and top_k [n] int32, each NULL or contiguous; values outside their
  * range (a negative or NaN temperature, a NaN) act as 1, 1, 0 and 0.
  */
