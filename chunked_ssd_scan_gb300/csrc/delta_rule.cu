@@ -610,7 +610,7 @@ struct Layout {
 };
 // Whether strides and pointers may let the tensor-core kernels take a call of this shape.
 bool tc_shape(const gated_delta_rule_shape* s) {
-  return s->io_dtype == SSD_BF16 && s->key_dim % 8 == 0 && s->key_dim <= 128 && s->value_dim % 8 == 0 && s->seqlen >= kChunk / 2;
+  return s->io_dtype == SSD_BF16 && s->key_dim % 8 == 0 && s->key_dim <= 128 && s->value_dim % 8 == 0;
 }
 int key_blocks(int64_t K) { return (int)((K + 63) / 64); }
 Layout layout(const gated_delta_rule_shape* s, bool back) {
@@ -662,7 +662,7 @@ Params make_params(const gated_delta_rule_shape* s) {
 }
 
 // Blocks of 16 rows while these fit the SMs in a round or so (a step is then shorter: 3 x 777 x 6 heads of 60 x 100 f32
-// RAG1 us, with 32 rows 159), else of 32 (a step's loads of k and q serve twice as many).
+// 128 us, with 32 rows 159), else of 32 (a step's loads of k and q serve twice as many).
 constexpr int64_t kFewBlocks = 2 * 152;
 
 template <typename T, int KE>

@@ -11,6 +11,9 @@
 // with an input take two passes, between two computed ones three (lo lo is left out, 2^-18).  One term would leave
 // states and outputs off by 3e-3.  States are kept in fp32 registers and products added to them there: the tensor
 // core's own accumulation truncates, which over a long memory would show.
+// Measured: 8 x 4096 x 16 heads of 128 x 128 with their states, 345 us; the chunk kernel takes 110 us of it, the walk 214
+// to 232, 3.4 us a chunk; with 16 sequences alone on the machine a chunk takes 2.3.  The chunk kernel is bound by no unit
+// (8 x 1024: issue slots 44 %, shared memory 49 %, DRAM 33 %) but by barriers and latencies.
 #include <cudaTypedefs.h>
 #include <string.h>
 
@@ -147,7 +150,8 @@ __device__ __forceinline__ void store_split_row(uint8_t* hi, uint8_t* lo, int ro
 }
 
 // Two tiles on their way from shared memory in one copy, read when this returns.  (Rows of 128 bytes straight from the
-// registers, a lane a row, kept the memory pipe at 60 % with 20 % of instructions: 118 us instead of PREPUS.)
+// registers, a lane a row, kept the memory pipe at 60 % with 20 % of instructions: 118 us instead of 110 for
+// 8 x 4096 x 16 heads.)
 __device__ __forceinline__ void send_tiles(uint8_t* to, const void* from) {
   fence_proxy_async_smem();
   __syncthreads();
@@ -431,15 +435,15 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       }
       mma_commit_elect(&bar.u_full);
       if constexpr (kY) {   // S Q^T, while U is turned into operands
-      if (c > 0 && !wait_bar(&bar.o_free, (c - 1) & 1, abort, p.hdr, 16)) break;
-      tc_fence_after();
+        if (c > 0 && !wait_bar(&bar.o_free, (c - 1) & 1, abort, p.hdr, 16)) break;
+        tc_fence_after();
 #pragma unroll
-      for (int ks = 0; ks < KB * 4; ++ks) {
-        const uint32_t at = q_lo + (((ks >> 2) * kTileBytes + (ks & 3) * 32) >> 4);
-        mma_ts_we(tmem + kColO, tmem + kColS + ks * 8, at, kDHi, id_k, ks > 0);
-        mma_ts_we(tmem + kColO, tmem + kColS + Kp / 2 + ks * 8, at, kDHi, id_k, 1);
-      }
-      mma_commit_elect(&bar.o1_full);
+        for (int ks = 0; ks < KB * 4; ++ks) {
+          const uint32_t at = q_lo + (((ks >> 2) * kTileBytes + (ks & 3) * 32) >> 4);
+          mma_ts_we(tmem + kColO, tmem + kColS + ks * 8, at, kDHi, id_k, ks > 0);
+          mma_ts_we(tmem + kColO, tmem + kColS + Kp / 2 + ks * 8, at, kDHi, id_k, 1);
+        }
+        mma_commit_elect(&bar.o1_full);
       }
       // (E U)^T K
       if (!wait_bar(&bar.w_ready, par, abort, p.hdr, 17)) break;
@@ -452,17 +456,17 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       }
       mma_commit_elect(&bar.d_full);
       if constexpr (kY) {   // y = scale D S Q^T + U P^T
-      if (!wait_bar(&bar.u_ready, par, abort, p.hdr, 18)) break;
-      if (!wait_bar(&bar.o_scaled, par, abort, p.hdr, 19)) break;
-      tc_fence_after();
+        if (!wait_bar(&bar.u_ready, par, abort, p.hdr, 18)) break;
+        if (!wait_bar(&bar.o_scaled, par, abort, p.hdr, 19)) break;
+        tc_fence_after();
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        const uint32_t a = tmem + kColU + ks * 16;
-        mma_ts_we(tmem + kColO, a, p_lo + ks * 2, kDHi, id_k, 1);
-        mma_ts_we(tmem + kColO, a, p_lo + kLo + ks * 2, kDHi, id_k, 1);
-        mma_ts_we(tmem + kColO, a + 8, p_lo + ks * 2, kDHi, id_k, 1);
-      }
-      mma_commit_elect(&bar.o2_full);
+        for (int ks = 0; ks < 4; ++ks) {
+          const uint32_t a = tmem + kColU + ks * 16;
+          mma_ts_we(tmem + kColO, a, p_lo + ks * 2, kDHi, id_k, 1);
+          mma_ts_we(tmem + kColO, a, p_lo + kLo + ks * 2, kDHi, id_k, 1);
+          mma_ts_we(tmem + kColO, a + 8, p_lo + ks * 2, kDHi, id_k, 1);
+        }
+        mma_commit_elect(&bar.o2_full);
       }
       mma_commit_elect(&bar.empty[s]);
     }
@@ -479,8 +483,23 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     const float* init = identity ? nullptr : part_of == 0 ? (p.init ? p.init + seq * KV : nullptr)
                         : seg.pre ? nullptr : seg.start + seg_at * KV;
     float S[KQ];
+    // By vectors, each chosen where it is loaded.  (Us for 8 x 4096, 1 x 32768 and 16 x 64 steps of 16 heads of 128 x 128:
+    // 345, 513, 35; value by value 354, 536, 56; zeros first and loads over them 335, 551, 37.)
 #pragma unroll
-    for (int k = 0; k < KQ; ++k) S[k] = init && live && k0 + k < p.K ? init[at + k] : identity && row == k0 + k ? 1.f : 0.f;
+    for (int k = 0; k < KQ; k += 4) {
+      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (init && live && k0 + k < p.K) {
+        if ((reinterpret_cast<uintptr_t>(init) & 15) == 0) f = *reinterpret_cast<const float4*>(init + at + k);
+        else f = make_float4(init[at + k], init[at + k + 1], init[at + k + 2], init[at + k + 3]);
+      } else if (identity) {
+        const int one = row - k0 - k;
+        f = make_float4(one == 0, one == 1, one == 2, one == 3);
+      }
+      S[k] = f.x;
+      S[k + 1] = f.y;
+      S[k + 2] = f.z;
+      S[k + 3] = f.w;
+    }
     const bool keep = p.states_out && !seg.pre;
     int cell = (b * all_chunks + first) * (int)p.H + h;
     for (int c = 0; c < nch; ++c, cell += (int)p.H) {
@@ -611,14 +630,12 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.o_free);
-      {
-        fence_proxy_async_smem();
-        named_barrier(1, 128);
-        if (warp == kStateWarps && lane == 0) {
-          tma_store_4d(&m.y, sm.y, v0, (first + c) * kChunk, h, b);
-          if (v0 + 64 < p.V) tma_store_4d(&m.y, sm.y + kTileBytes, v0 + 64, (first + c) * kChunk, h, b);
-          bulk_commit_group();
-        }
+      fence_proxy_async_smem();
+      named_barrier(1, 128);
+      if (warp == kStateWarps && lane == 0) {
+        tma_store_4d(&m.y, sm.y, v0, (first + c) * kChunk, h, b);
+        if (v0 + 64 < p.V) tma_store_4d(&m.y, sm.y + kTileBytes, v0 + 64, (first + c) * kChunk, h, b);
+        bulk_commit_group();
       }
     }
     if (warp == kStateWarps && lane == 0) bulk_wait_group<0>();
@@ -631,51 +648,67 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
   }
 }
 
-// The state before every segment: 16 rows of a sequence a block, a thread a key.
-__global__ void __launch_bounds__(128) delta_carry_kernel(const __grid_constant__ Params p, Segments seg, int tiles) {
-  __shared__ __align__(16) float row[2][128][16];   // by keys: four rows a load
-  const int seq = blockIdx.x / tiles, v0 = blockIdx.x % tiles * 16, k = threadIdx.x;
+// The state before every segment: 16 rows of a sequence a block.  A thread has a key of four rows, and of the product with
+// a segment's map the sum over 32 keys for all 16; the map's values, which do not wait for the rows, are loaded a segment
+// ahead.  (128 threads, each with all keys: 10 us a segment instead of 3.)
+constexpr int kCarryThreads = 512, kCarryRows = 16;
+struct CarrySmem {
+  float row[128][kCarryRows];       // by keys: four rows a load
+  float part[4][kCarryRows][128];
+};
+
+__global__ void __launch_bounds__(kCarryThreads) delta_carry_kernel(const __grid_constant__ Params p, Segments seg, int tiles) {
+  __shared__ __align__(16) CarrySmem sm;
+  const int seq = blockIdx.x / tiles, v0 = blockIdx.x % tiles * kCarryRows, k = threadIdx.x & 127, part = threadIdx.x >> 7;
   const int64_t KV = p.K * p.V, at = (int64_t)seq * seg.n;
   const bool in = k < p.K;
-  float s[16];
+  float s[4], f[32];
+  auto own = [&](const float* base, int64_t i, int r) { return base + (at + i) * KV + (v0 + part * 4 + r) * p.K + k; };
+  auto fetch = [&](int i) {   // the map of segment i
+    const float* map = seg.map + (at + i) * p.K * p.K + k;
 #pragma unroll
-  for (int r = 0; r < 16; ++r) s[r] = in && v0 + r < p.V ? seg.end[at * KV + (v0 + r) * p.K + k] : 0.f;
+    for (int e = 0; e < 32; ++e) f[e] = in && part * 32 + e < p.K && i + 1 < seg.n ? map[(part * 32 + e) * p.K] : 0.f;
+  };
+  fetch(1);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) s[r] = in && v0 + part * 4 + r < p.V ? *own(seg.end, 0, r) : 0.f;
   for (int i = 1; i < seg.n; ++i) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r)
-      if (in && v0 + r < p.V) seg.start[(at + i) * KV + (v0 + r) * p.K + k] = s[r];
-#pragma unroll
-    for (int r = 0; r < 16; r += 4) *reinterpret_cast<float4*>(&row[i & 1][k][r]) = make_float4(s[r], s[r + 1], s[r + 2], s[r + 3]);
+    for (int r = 0; r < 4; ++r)
+      if (in && v0 + part * 4 + r < p.V) *const_cast<float*>(own(seg.start, i, r)) = s[r];
     if (i + 1 == seg.n) break;
+    *reinterpret_cast<float4*>(&sm.row[k][part * 4]) = make_float4(s[0], s[1], s[2], s[3]);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) s[r] = in && v0 + part * 4 + r < p.V ? *own(seg.end, i, r) : 0.f;
+    __syncthreads();
+    float sum[kCarryRows] = {};
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+#pragma unroll
+      for (int r = 0; r < kCarryRows; r += 4) {
+        const float4 g = *reinterpret_cast<const float4*>(&sm.row[part * 32 + e][r]);
+        sum[r] = fmaf(g.x, f[e], sum[r]);
+        sum[r + 1] = fmaf(g.y, f[e], sum[r + 1]);
+        sum[r + 2] = fmaf(g.z, f[e], sum[r + 2]);
+        sum[r + 3] = fmaf(g.w, f[e], sum[r + 3]);
+      }
+    fetch(i + 1);
+#pragma unroll
+    for (int r = 0; r < kCarryRows; ++r) sm.part[part][r][k] = sum[r];
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < 16; ++r) s[r] = in && v0 + r < p.V ? seg.end[(at + i) * KV + (v0 + r) * p.K + k] : 0.f;
-    const float* map = seg.map + (at + i) * p.K * p.K;
-    for (int j = 0; in && j < p.K; j += 32) {
-      float f[32];   // on their way at once
+    for (int r = 0; r < 4; ++r)
 #pragma unroll
-      for (int e = 0; e < 32; ++e) f[e] = j + e < p.K ? map[(j + e) * p.K + k] : 0.f;
-#pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        if (j + e >= p.K) break;
-#pragma unroll
-        for (int r = 0; r < 16; r += 4) {
-          const float4 g = *reinterpret_cast<const float4*>(&row[i & 1][j + e][r]);
-          s[r] = fmaf(g.x, f[e], s[r]);
-          s[r + 1] = fmaf(g.y, f[e], s[r + 1]);
-          s[r + 2] = fmaf(g.z, f[e], s[r + 2]);
-          s[r + 3] = fmaf(g.w, f[e], s[r + 3]);
-        }
-      }
-    }
+      for (int q = 0; q < 4; ++q) s[r] += sm.part[q][part * 4 + r][k];
   }
 }
 
 // ------------------------------------------------------------------------------------------------ host
 constexpr int kSms = 152, kMostSegments = 16;
 
-// Segments of a sequence, by what the passes take: a chunk 2.25 us with outputs, 1.9 us without, blocks in rounds of one
-// an SM, a segment's carry 4 us.  (1 x 32768 x 16 heads: LONG1 us in one segment, LONGN us in SEGN.)
+// Segments of a sequence, by what the passes take: a chunk 2.5 us with outputs, 2.3 us without (2.4 and 2.2 measured at
+// 86 chunks), blocks in rounds of one an SM, a segment's carry 3 us.  (1 x 32768 x 16 heads: 1261 us in one segment, 513
+// us in six.)
 int segments_for(int64_t batch, int64_t nch, int64_t H, int64_t V) {
   const int64_t vtiles = (V + 127) / 128, seqs = batch * H;
   int best = 1;
@@ -684,8 +717,8 @@ int segments_for(int64_t batch, int64_t nch, int64_t H, int64_t V) {
     const int64_t len = (nch + n - 1) / n;
     if ((n - 1) * len >= nch) continue;   // the last one would be empty
     auto rounds = [](int64_t blocks) { return (double)((blocks + kSms - 1) / kSms); };
-    double us = rounds(seqs * vtiles * n) * len * 2.25;
-    if (n > 1) us += rounds(seqs * ((n - 1) * vtiles + n - 2)) * len * 1.9 + 4.0 * n + 10;
+    double us = rounds(seqs * vtiles * n) * len * 2.5;
+    if (n > 1) us += rounds(seqs * ((n - 1) * vtiles + n - 2)) * len * 2.3 + 3.0 * n + 15;
     if (n == 1 || us < 0.9 * least) {
       best = n;
       least = us;
@@ -742,8 +775,8 @@ cudaError_t chain_as(const Params& p, const TcMaps& m, const TcBuffers& buf, flo
     cudaError_t e = walk_as<KB, false>(p, m, buf, seg, st);
     if (e != cudaSuccess) return e;
     seg.pre = 0;
-    const int tiles = (int)((p.V + 15) / 16);
-    delta_carry_kernel<<<(unsigned)(p.batch * p.H * tiles), 128, 0, st>>>(p, seg, tiles);
+    const int tiles = (int)((p.V + kCarryRows - 1) / kCarryRows);
+    delta_carry_kernel<<<(unsigned)(p.batch * p.H * tiles), kCarryThreads, 0, st>>>(p, seg, tiles);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -802,9 +835,16 @@ size_t tc_bytes(int64_t batch, int64_t nch, int64_t H, int64_t V, int64_t K, boo
          segment_bytes(batch, nch, H, V, K);
 }
 
+// Forward, few sequences whose rows the walk on the CUDA cores has on the machine at once: from as many steps on as
+// make up for two launches (us, walk and tensor cores: 16 heads of 128 x 128, 64 steps 21 and 23, 72 steps 25 and 25, 128
+// steps 37 and 25; 16 of 64 x 64, 64 steps 17 and 17, 128 steps 29 and 19).  Many: from a quarter of a chunk on (256 of
+// 128 x 128, 8 steps 39 and 37, 16 steps 39 and 37, 24 steps 62 and 37).  Backward: always (16 of 128 x 128, 8 steps 56
+// and 36, 128 steps 111 and 39).
 bool tc_takes(const Params& p, bool backward) {
   const int64_t most = INT32_MAX / 2;
-  if (p.K % 8 != 0 || p.K > 128 || p.V % 8 != 0 || p.T > most || p.batch > most || p.T < kChunk / 2) return false;
+  if (p.K % 8 != 0 || p.K > 128 || p.V % 8 != 0 || p.T > most || p.batch > most) return false;
+  const bool few = p.batch * p.H * ((p.V + 15) / 16) <= 2 * kSms;
+  if (!backward && p.T < (few ? 72 : kChunk / 4)) return false;
   if (p.batch * p.nch * p.H >= most) return false;
   if (!rows_fit(p.q, p.qs, p.batch, p.T, p.Hk) || !rows_fit(p.k, p.ks, p.batch, p.T, p.Hk) ||
       !rows_fit(p.v, p.vs, p.batch, p.T, p.H))

@@ -201,7 +201,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     const int64_t at = (((int64_t)b * p.H + h) * p.V + row) * p.K + k0;
     float G[KQ];
 #pragma unroll
-    for (int k = 0; k < KQ; ++k) G[k] = p.dfinal && live && k0 + k < p.K ? p.dfinal[at + k] : 0.f;
+    for (int k = 0; k < KQ; ++k) G[k] = 0.f;
+    if (p.dfinal && live) load_row(G, p.dfinal + at, p.K - k0);
     int cell = (b * nch + nch - 1) * (int)p.H + h;
     for (int n = 0; n < nch; ++n, cell -= (int)p.H) {
       const int s = n & 1;
@@ -346,9 +347,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
 // A block an SM, which goes from chunk to chunk (of a key head; the heads that share the keys one after the other).  What
 // the next head reads is loaded as soon as its place in shared memory is free: dY and dR once the products with them are
 // through, the state, as it is in memory, into G's place, V, T, Q and K at the end.  (A block a chunk, loading when it
-// begins: 415 us instead of GRADUS for 4 x 4096 x 16 heads.)
+// begins: 415 us instead of 364 for 4 x 4096 x 16 heads.)
 // ---------------------------------------------------------------------------------------------------------------------
-constexpr int kGradThreads = 512;   // 16 columns of TMEM a warp (32 and 256 threads: 473 us instead of GRADUS, latency)
+constexpr int kGradThreads = 512;   // 16 columns of TMEM a warp (with 32 and 256 threads 473 us instead of 434: latency)
 // TMEM: X and -D X, then [dY; dR hi] with U's first term; U, then with its second; S^T dY^T; S^T dR^T; G^T U^T; K^T Bm^T;
 // [Q; K] K^T, then K^T N'^T; dR lo U^T, then Q^T Bm + K^T diag(beta) N'.  Operands that follow each other in shared
 // memory enter one product of 128 columns: with 64 the reading of the operands (6 KB for 32 cycles' work) bounds it.

@@ -105,6 +105,24 @@ __device__ __forceinline__ void store8(float* p, const float* v, bool wide) {
   }
 }
 
+// N values of a row, zeros behind its end; rows are multiples of eight values.
+template <int N>
+__device__ __forceinline__ void load_row(float (&v)[N], const float* p, int64_t left) {
+  const bool wide = (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+#pragma unroll
+  for (int k = 0; k < N; k += 4) {
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (k < left) {
+      if (wide) f = *reinterpret_cast<const float4*>(p + k);
+      else f = make_float4(p[k], p[k + 1], p[k + 2], p[k + 3]);
+    }
+    v[k] = f.x;
+    v[k + 1] = f.y;
+    v[k + 2] = f.z;
+    v[k + 3] = f.w;
+  }
+}
+
 __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -129,7 +147,7 @@ __device__ __forceinline__ void store_terms(uint32_t at, const float (&v)[16]) {
 }
 
 // The walks' 16 state warps, four to each quarter of the lanes: a thread has a value's quarter of the keys, and 16 steps
-// of a chunk.  (Eight warps with halves: 2.44 us a chunk instead of CHUNKUS; what they do between two products is a
+// of a chunk.  (Eight warps with halves: 2.44 us a chunk instead of 2.24; what they do between two products is a
 // chain of latencies.)
 constexpr int kStateWarps = 16, kWalkThreads = 22 * 32;   // and four at the output, one for products, one for loads
 

@@ -362,13 +362,7 @@ __global__ void __launch_bounds__(1024) rms_join_kernel(const float* partial, fl
   const int part = threadIdx.x >> 5;
   float s = 0.f;
   if (c < C)
-    for (int64_t r0 = part; r0 < rows; r0 += 32 * 8) {   // eight on their way at once
-      float f[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = r0 + 32 * e < rows ? partial[(r0 + 32 * e) * C + c] : 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s += f[e];
-    }
+    for (int64_t r = part; r < rows; r += 32) s += partial[r * C + c];
   sm[part][threadIdx.x & 31] = s;
   __syncthreads();
   s = warp_sum(sm[threadIdx.x & 31][part]);

@@ -560,7 +560,7 @@ size_t gated_delta_rule_workspace_bytes(const gated_delta_rule_shape* shape, int
  * [b,H,V,K] f32.  states: NULL, or f32 [b, ceil(T / GATED_DELTA_RULE_CHUNK), H, V, K] that receives
  * the state before steps 0, 64, 128, ... for gated_delta_rule_backward.  y may be NULL.
  * g below -200 is a decay of zero, as in fp32.  States and sums are fp32.  bf16 inputs with K <= 128, K
- * and V multiples of 8, rows on 16-byte boundaries and 32 steps or more run on the tensor cores, where
+ * and V multiples of 8, rows on 16-byte boundaries and not too few steps run on the tensor cores, where
  * what is computed on the way (the state, the writes, the inverse of a chunk's triangular system)
  * enters a product as two bf16 terms, 16 bits of mantissa: states are off by some 4e-6 of their size.
  * There a NaN or an infinity may reach the outputs of the steps before it in its chunk of 64 too.

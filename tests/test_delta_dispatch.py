@@ -20,6 +20,33 @@ def test_segments(shape):
     td.check_forward(td.run_forward(d, "bf16"), d, "bf16")
 
 
+# many short sequences: half a chunk, around its end, no room for them on the CUDA cores at once
+@pytest.mark.parametrize("shape", [(40, 32, 2, 2, 64, 64), (24, 65, 4, 4, 128, 128), (30, 64, 2, 4, 72, 40),
+                                   (11, 100, 1, 4, 8, 136), (300, 33, 1, 2, 16, 8), (50, 17, 1, 2, 64, 64)], ids=str)
+def test_many_short_sequences(shape):
+    d = td.inputs(*shape, "bf16", seed=38, dev="cuda")
+    td.check_forward(td.run_forward(d, "bf16"), d, "bf16")
+    td.check_backward(td.run_backward(d, "bf16", None), d, "bf16")
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 1, 1, 8, 8), (2, 5, 1, 3, 128, 128), (1, 31, 2, 2, 64, 40)], ids=str)
+def test_gradients_of_a_few_steps(shape):
+    d = td.inputs(*shape, "bf16", seed=39, dev="cuda")
+    td.check_backward(td.run_backward(d, "bf16", None), d, "bf16")
+
+
+def test_states_that_are_not_on_a_16_byte_border():
+    d = td.inputs(2, 700, 1, 2, 64, 64, "bf16", seed=40, dev="cuda")
+    off = {}
+    for k in ("init", "dfinal"):
+        off[k] = torch.zeros(d[k].numel() + 1, device="cuda")[1:].view(d[k].shape)
+        off[k].copy_(d[k])
+    a = pkg.gated_delta_rule_forward(*td.args(d), init_state=d["init"])
+    b = pkg.gated_delta_rule_forward(*td.args(d), init_state=off["init"])
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    td.check_backward(pkg.gated_delta_rule_backward(*td.args(d), d["dy"], init_state=off["init"], dfinal=off["dfinal"]), d, "bf16")
+
+
 @pytest.mark.parametrize("shape", [(1, 1300, 1, 2, 128, 128), (2, 200, 2, 4, 64, 96)], ids=str)
 def test_states_known_or_formed_anew_give_the_same_gradients(shape):
     d = td.inputs(*shape, "bf16", seed=32, dev="cuda")
