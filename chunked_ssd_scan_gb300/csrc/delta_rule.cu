@@ -743,6 +743,15 @@ cudaError_t set_rows(float* dst, const float* src, int64_t n, cudaStream_t st) {
 
 using namespace ssd;
 
+namespace ssd {
+namespace {
+bool overlap(const float* a, int64_t n, const float* b, int64_t m) {   // counts of values
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + 4 * (uintptr_t)m && y < x + 4 * (uintptr_t)n;
+}
+}  // namespace
+}  // namespace ssd
+
 extern "C" {
 
 size_t gated_delta_rule_workspace_bytes(const gated_delta_rule_shape* shape, int32_t backward) {
@@ -767,6 +776,10 @@ ssd_status gated_delta_rule_forward(const gated_delta_rule_shape* shape, const v
   if (!workspace || misaligned(workspace, kWsAlign) || workspace_bytes < L.total) return SSD_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   Params p = make_params(shape);
+  // A sequence in segments: the last one's block may have written final_state before the first one's reads init_state.
+  const int64_t state = p.batch * p.H * p.K * p.V;
+  if (overlap(init_state, state, final_state, state) || overlap(init_state, state, states, state * p.nch))
+    return SSD_ERR_INVALID_ARG;
   if (empty) return done(set_rows(final_state, init_state, p.batch * p.H * p.K * p.V, st));
   p.q = q;
   p.k = k;

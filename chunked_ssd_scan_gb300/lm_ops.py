@@ -625,7 +625,8 @@ def gated_delta_rule_forward(q, k, v, g, beta, *, scale: Optional[float] = None,
     head h reads q and k of h // (H / Hk)), g (None: zeros) and beta [b,T,H] f32, init_state
     [b,H,V,K] f32; scale is K^-1/2 unless given.  Returns (y, final_state, states): y [b,T,H,V] in
     q's dtype, final_state f32 and, with ``return_states``, the states [b, ceil(T/64), H, V, K] f32
-    that ``gated_delta_rule_backward`` takes (None where not requested)."""
+    that ``gated_delta_rule_backward`` takes (None where not requested).  final_state and states
+    must not lie over init_state (SSDError)."""
     return GatedDeltaRulePlan(q, k, v, g, beta, scale=scale, init_state=init_state, y=y,
                               final_state=final_state, return_final_state=return_final_state,
                               states=states, return_states=return_states, workspace=workspace,

@@ -558,7 +558,8 @@ size_t gated_delta_rule_workspace_bytes(const gated_delta_rule_shape* shape, int
  * q, k [b,T,Hk,K], v [b,T,H,V] strided, y [b,T,H,V] contiguous, all io_dtype; g (NULL = zeros) and
  * beta [b,T,H] f32 strided; init_state (NULL = zeros) and final_state (NULL = not written)
  * [b,H,V,K] f32.  states: NULL, or f32 [b, ceil(T / GATED_DELTA_RULE_CHUNK), H, V, K] that receives
- * the state before steps 0, 64, 128, ... for gated_delta_rule_backward.  y may be NULL.
+ * the state before steps 0, 64, 128, ... for gated_delta_rule_backward.  y may be NULL.  final_state
+ * and states over init_state are refused (INVALID_ARG).
  * g below -200 is a decay of zero, as in fp32.  States and sums are fp32.  bf16 inputs with K <= 128, K
  * and V multiples of 8, rows on 16-byte boundaries and not too few steps run on the tensor cores, where
  * what is computed on the way (the state, the writes, the inverse of a chunk's triangular system)

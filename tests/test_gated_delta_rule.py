@@ -396,6 +396,17 @@ def test_unsupported_shapes(lib, change):
     assert lib.gated_delta_rule_forward(ctypes.byref(s), *[_VP(A16)] * 9, _VP(A16), 1 << 62, None) == 2
 
 
+@pytest.mark.parametrize("final,states", [(0, None), (4, None), (-4, None), (None, 0), (None, -4)], ids=str)
+def test_states_over_the_initial_state(lib, final, states):
+    # written by one segment's block while another one still reads the state
+    s, far = shape_of(), 1 << 40
+    size = 4 * 2 * 2 * 64 * 64
+    at = lambda off, n: None if off is None else _VP(far + (off if off >= 0 else off - n + 8))   # noqa: E731
+    p = [_VP(A16 * (i + 1)) for i in range(5)]
+    assert lib.gated_delta_rule_forward(ctypes.byref(s), *p, _VP(far), _VP(A16 * 9), at(final, size), at(states, 2 * size),
+                                        _VP(A16), 1 << 40, None) == 1
+
+
 def test_bad_pointers_and_workspaces(lib):
     s = shape_of()
     fwd = lambda p, ws=A16, n=1 << 40: lib.gated_delta_rule_forward(ctypes.byref(s), *p, _VP(ws), n, None)   # noqa: E731
