@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(kThreads) token_sample_kernel(const __grid_con
     // log2(e) / temperature in two floats: the quotient, and what its product with the temperature leaves
     const float tt = fmaxf(temp, 1e-30f);
     w.ch = 1.44269502f / tt;
-    w.cl = (fmaf(-w.ch, tt, 1.44269502f) + 1.92596299e-8f) / tt;
+    w.cl = w.ch > 0.f ? (fmaf(-w.ch, tt, 1.44269502f) + 1.92596299e-8f) / tt : 0.f;   // 0 inf is NaN
     w.shift = p.shift;
     Cut cut = {0, V, 1};
     if (min_p > 0.f) {   // a bound on the weights, rounded up

@@ -228,3 +228,27 @@ def test_numbers_at_and_beside_the_borders(V):
         for rows in (n, 1):   # a block a row, and several
             d = x[:rows].cuda(), uu[:rows].cuda()
             compare(*d, *pkg.token_sample(*d))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [3, 200])   # several blocks a row, and one
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_infinite_temperature(dtype, n):
+    # every logit above -inf weighs the same, however low it is
+    V = 1000
+    logits, u, _ = make(n, V, dtype, 7)
+    logits[:, ::3] = -float("inf")
+    logits[:, 1::7] = torch.finfo(DT[dtype]).min
+    live = torch.isfinite(logits[0].float()).nonzero().flatten().cpu()
+    for t in (float("inf"), torch.full((n,), float("inf"), device="cuda")):
+        for settings in ({}, {"min_p": 0.5}, {"min_p": 1.0}):
+            ids, lp = pkg.token_sample(logits, u, temperature=t, **settings)
+            live_r = [(torch.isfinite(logits[r].float())).nonzero().flatten().cpu() for r in range(n)]
+            want = torch.stack([x[int(float(u[r]) * len(x))] for r, x in enumerate(live_r)])
+            assert torch.equal(ids.cpu(), want)
+            assert torch.allclose(lp.cpu(), torch.full((n,), -float(np.log(len(live)))), rtol=1e-6, atol=0)
+        ids, lp = pkg.token_sample(logits, u, temperature=t, top_k=5)
+        for r in range(n):
+            top = torch.sort(logits[r].float().cpu(), descending=True, stable=True)[1][:5].sort()[0]
+            assert int(ids[r]) == int(top[int(float(u[r]) * 5)])
+        assert torch.allclose(lp.cpu(), torch.full((n,), -float(np.log(5.0))), rtol=1e-6, atol=0)
