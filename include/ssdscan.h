@@ -625,8 +625,11 @@ size_t rms_norm_workspace_bytes(const rms_norm_shape* shape);
  * NULL = not written; may be the buffer of x or of residual if that is contiguous); weight [C] f32
  * (NULL = ones); rstd [N] f32 (may be NULL).  y [N,C] contiguous: io_dtype, or with quantize 8-bit
  * values q and scale f32 [N, 1] or [N, ceil(C / RMS_NORM_BLOCK)]: scale is the largest |y| it covers
- * over 448 (1 where all are zero), q = y / scale rounded to nearest, ties to even.  The norm is taken
- * of the unrounded sum; all arithmetic is fp32.
+ * over 448 (1 where that is zero in fp32), q = y / scale, an fp32 quotient, rounded to nearest, ties to
+ * even (448 where the scale is so small, below 2^-126, that fp32 rounds it down).  The norm is taken of the
+ * unrounded sum; all arithmetic is fp32, so q is that of the fp32 y and scale: next to a border between two
+ * 8-bit values an exact y may lie on the other side.  For the scale of a row the products of h and weight
+ * are formed before rstd: those below 2^-126 keep fewer bits.
  */
 ssd_status rms_norm_forward(const rms_norm_shape* shape, const void* x, const void* residual,
                             const float* weight, void* y, void* h, float* rstd, float* scale,
