@@ -52,6 +52,9 @@ __device__ __forceinline__ void add_pair(float& hi, float& lo, float h, float l)
   lo = rest - (hi - s);
 }
 
+// e^(hi + lo).  (Without lo, up to half a step of hi, a decay between neighbours was off by up to 7.6e-6 at sums near 80.)
+__device__ __forceinline__ float exp_pair(float hi, float lo) { return expf(hi) * (1.f + lo); }
+
 // By one whole warp; lane l holds the steps 2l and 2l + 1.
 __device__ __forceinline__ void chunk_decay_warp(const Params& p, ChunkDecay& c, int64_t b, int64_t t0, int n,
                                                  int64_t h, int lane) {
@@ -72,10 +75,10 @@ __device__ __forceinline__ void chunk_decay_warp(const Params& p, ChunkDecay& c,
   c.lo[i0] = l0;
   c.hi[i1] = hi;
   c.lo[i1] = lo;
-  c.from[i0] = expf(h0);
-  c.from[i1] = expf(hi);
-  c.back[i0] = expf(-h0);
-  c.back[i1] = expf(-hi);
+  c.from[i0] = exp_pair(h0, l0);
+  c.from[i1] = exp_pair(hi, lo);
+  c.back[i0] = exp_pair(-h0, -l0);
+  c.back[i1] = exp_pair(-hi, -lo);
   const bool plain = __all_sync(0xffffffffu, fabsf(h0) <= 80.f && fabsf(hi) <= 80.f);
   if (lane == 0) c.plain = plain;
   c.to[i0] = expf((th - h0) + (tl - l0));

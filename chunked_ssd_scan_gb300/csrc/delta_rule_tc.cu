@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kPrepThreads, 6) delta_chunk_kernel(const __gr
         } else {
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            v[j] = c0 + j <= last ? v[j] * by * __expf((hi - sm.c.hi[c0 + j]) + (lo - sm.c.lo[c0 + j])) : 0.f;
+            v[j] = c0 + j <= last ? v[j] * by * expf((hi - sm.c.hi[c0 + j]) + (lo - sm.c.lo[c0 + j])) : 0.f;
         }
       }
       if (warp < 2) {

@@ -714,7 +714,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       for (int j = 0; j < 16; ++j) {
         const int c = c0 + j;
         const float f = lower ? (x[j] + y[j]) + z[j] : x[j] + y[j];
-        const float decay = plain ? mine_from * sm.c.back[c] : __expf((ch - sm.c.hi[c]) + (cl - sm.c.lo[c]));
+        const float decay = plain ? mine_from * sm.c.back[c] : expf((ch - sm.c.hi[c]) + (cl - sm.c.lo[c]));
         x[j] = c <= last ? f * by * decay : 0.f;
       }
 #pragma unroll
