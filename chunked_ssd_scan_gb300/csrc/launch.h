@@ -10,13 +10,14 @@
 namespace ssd {
 namespace {   // of its own in every library: a process may hold the normal and the checked one
 
-// Blocks of `kernel` that the device holds at once (looked up once per kernel and device; throws nothing).
+// Blocks of `kernel` that the device holds at once (looked up once per kernel, device, number of threads and shared memory;
+// throws nothing).  A caller's grid, and with it the order of its sums, depends on these alone, not on earlier calls.
 cudaError_t resident_blocks(const void* kernel, int threads, int smem, int* out) {
   struct Known {
     const void* kernel;
-    int dev, blocks;
+    int dev, threads, smem, blocks;
   };
-  constexpr int kMost = 256;   // more kernels than a translation unit has; beyond it, looked up every time
+  constexpr int kMost = 1024;   // more kernels and block sizes than a translation unit has; beyond it, looked up every time
   static Known known[kMost];
   static int count = 0;
   static std::atomic_flag busy = ATOMIC_FLAG_INIT;
@@ -26,8 +27,9 @@ cudaError_t resident_blocks(const void* kernel, int threads, int smem, int* out)
   while (busy.test_and_set(std::memory_order_acquire)) {
   }
   int blocks = 0;
-  for (int k = 0; k < count; ++k)
-    if (known[k].kernel == kernel && known[k].dev == dev) blocks = known[k].blocks;
+  for (int k = 0; k < count && blocks == 0; ++k)
+    if (known[k].kernel == kernel && known[k].dev == dev && known[k].threads == threads && known[k].smem == smem)
+      blocks = known[k].blocks;
   if (blocks == 0) {
     int sms = 0, per = 0;
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -36,7 +38,7 @@ cudaError_t resident_blocks(const void* kernel, int threads, int smem, int* out)
     if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem);
     if (e == cudaSuccess) {
       blocks = sms * std::max(per, 1);
-      if (count < kMost) known[count++] = {kernel, dev, blocks};
+      if (count < kMost) known[count++] = {kernel, dev, threads, smem, blocks};
     }
   }
   busy.clear(std::memory_order_release);
