@@ -9,8 +9,10 @@
 //   dq_i = scale (D_i S^T dy_i + sum_j<=i M_ij (dy_i . u_j) k_j)
 //   dk_i = E_i G^T u_i - D_i S^T dv_i + scale sum_j>=i M_ji (dy_j . u_i) q_j
 //          - sum_j<i M_ij (dv_i . u_j) k_j - sum_j>i M_ji (dv_j . u_i) k_j
-//   dg_i = <dS, S> before the chunk - sum_j<i (q_j . dq_j - dv_j . v_j)   (scaling k, q and the state by the decay
-//          shows that the sum over the steps behind i is what g_i's gradient is)
+//   dg_i = D_last <G, S> + sum_{a >= i} D_a (scale q_a . S^T dy_a - k_a . S^T dv_a) + sum_{b < i} E_b k_b . G^T u_b
+//          + sum_{a >= i > b} M_ab (scale (dy_a . u_b) (q_a . k_b) - (dv_a . u_b) (k_a . k_b))
+// that is, every product that the decay of step i is a factor of.  (The shorter <dS, S> before the chunk less the sum of
+// q . dq - dv . v over the steps before i cancels: behind a reset of a state of size 1000 dg was off by 1e-3.)
 #include <string.h>
 
 #include <algorithm>
@@ -292,15 +294,18 @@ __global__ void __launch_bounds__(kThreads) delta_walk_back_kernel(const __grid_
   if (p.dinit) w.store(p.dinit + (b * p.H + h) * KV, v0, p.V, p.K);
 }
 
-// dq, dk and the parts of dg of one chunk and key head, 64 of its keys a block: five products over V in slabs of 16
-// values, then the four of the chunk's steps with each other.
+// dq, dk and the part of dg of one chunk and key head, 64 of its keys a block: five products over V in slabs of 16
+// values, then the four of the chunk's steps with each other.  (A backward call of 4 x 4096 x 16 heads of
+// 128 x 128 f32 takes 5.7 ms; 255 registers, one block an SM.)
 constexpr int kGradThreads = 256, kSlab = 16, kPitch = 68;
 struct GradSmem {
   float dy[kSlab][kPitch], u[kSlab][kPitch], dv[kSlab][kPitch];   // [value][step]
   float s[kSlab][kPitch], g[kSlab][kPitch];                       // [value][key]
   float b[kChunk][kPitch], n[kChunk][kPitch];                     // [step][step]
   float q[kChunk][kPitch], k[kChunk][kPitch];                     // [step][key]
+  float qk[kChunk][kPitch], kk[kChunk][kPitch];                   // [step][step]: products of these keys
   float sum[kGradThreads / 32];
+  float read[kChunk], wrote[kChunk];                              // of dg: what step a reads of S; what step b writes to G
   ChunkDecay c;
 };
 
@@ -312,6 +317,14 @@ __device__ __forceinline__ void outer(float (&acc)[4][4], const float4& x, const
     for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
 }
 __device__ __forceinline__ float4 four(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float dot4(const float4& a, const float4& b, float sum) {
+  return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, sum))));
+}
+__device__ __forceinline__ float sum16(float v) {
+#pragma unroll
+  for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kGradThreads) delta_chunk_grad_kernel(const __grid_constant__ Params p) {
@@ -330,14 +343,39 @@ __global__ void __launch_bounds__(kGradThreads) delta_chunk_grad_kernel(const __
     sm.q[i][c] = in ? ld_f32(static_cast<const T*>(p.q) + b * p.qs[0] + (t0 + i) * p.qs[1] + hk * p.qs[2] + k0 + c) : 0.f;
     sm.k[i][c] = in ? ld_f32(static_cast<const T*>(p.k) + b * p.ks[0] + (t0 + i) * p.ks[1] + hk * p.ks[2] + k0 + c) : 0.f;
   }
+  __syncthreads();
+  {   // columns 16 apart: neighbouring lanes' rows on different banks
+    float qk[4][4] = {}, kk[4][4] = {};
+#pragma unroll 2
+    for (int m = 0; m < 64; m += 4) {
+      float4 col[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) col[j] = four(&sm.k[tx + 16 * j][m]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 q = four(&sm.q[ty * 4 + i][m]), k = four(&sm.k[ty * 4 + i][m]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          qk[i][j] = dot4(q, col[j], qk[i][j]);
+          kk[i][j] = dot4(k, col[j], kk[i][j]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sm.qk[ty * 4 + i][tx + 16 * j] = qk[i][j];
+        sm.kk[ty * 4 + i][tx + 16 * j] = kk[i][j];
+      }
+  }
   float dq[4][4] = {}, dk[4][4] = {};
   for (int64_t h = hk * group; h < (hk + 1) * group; ++h) {
     __syncthreads();
     if (tid < 32) chunk_decay_warp(p, sm.c, b, t0, n, h, tid);
     __syncthreads();
     const float* S = p.states_in + ((b * p.nch + chunk) * p.H + h) * KV;
-    const float* before = p.dstates + ((b * p.nch + chunk) * p.H + h) * KV;
-    const float* G = chunk + 1 < p.nch ? before + p.H * KV : p.dfinal ? p.dfinal + (b * p.H + h) * KV : nullptr;
+    const float* G = chunk + 1 < p.nch ? p.dstates + ((b * p.nch + chunk + 1) * p.H + h) * KV : p.dfinal ? p.dfinal + (b * p.H + h) * KV : nullptr;
     float x1[4][4] = {}, x2[4][4] = {}, x3[4][4] = {}, bb[4][4] = {}, nn[4][4] = {};
     float inner = 0.f;
     for (int64_t v0 = 0; v0 < p.V; v0 += kSlab) {
@@ -356,10 +394,10 @@ __global__ void __launch_bounds__(kGradThreads) delta_chunk_grad_kernel(const __
         const int at = m * kGradThreads + tid, r = at >> 6, c = at & 63;
         const bool in = v0 + r < p.V && k0 + c < p.K;
         const int64_t to = (v0 + r) * p.K + k0 + c;
-        const float s = in ? S[to] : 0.f;
+        const float s = in ? S[to] : 0.f, g = in && G ? G[to] : 0.f;
         sm.s[r][c] = s;
-        sm.g[r][c] = in && G ? G[to] : 0.f;
-        inner = fmaf(s, in ? before[to] : 0.f, inner);
+        sm.g[r][c] = g;
+        inner = fmaf(s, g, inner);
       }
       __syncthreads();
 #pragma unroll 4
@@ -393,12 +431,26 @@ __global__ void __launch_bounds__(kGradThreads) delta_chunk_grad_kernel(const __
     for (int i = 0; i < 4; ++i) {
       const int r = ty * 4 + i;
       const float from = sm.c.from[r], to = sm.c.to[r];
+      float read = 0.f, wrote = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        dqh[i][j] = p.scale * from * x1[i][j];
-        dk[i][j] += to * x2[i][j] - from * x3[i][j];
+        const float q1 = p.scale * from * x1[i][j], wr = to * x2[i][j], r1 = from * x3[i][j];
+        const float q = sm.q[r][tx * 4 + j], k = sm.k[r][tx * 4 + j];
+        dqh[i][j] = q1;
+        dk[i][j] += wr - r1;
+        read += q * q1 - k * r1;
+        wrote = fmaf(k, wr, wrote);
+      }
+      read = sum16(read);
+      wrote = sum16(wrote);
+      if (tx == 0) {
+        sm.read[r] = read;
+        sm.wrote[r] = wrote;
       }
     }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, o);
+    if ((tid & 31) == 0) sm.sum[tid >> 5] = inner;
 #pragma unroll 4
     for (int m = 0; m < kChunk; ++m) {
       const float4 q = four(&sm.q[m][tx * 4]), k = four(&sm.k[m][tx * 4]);
@@ -406,26 +458,51 @@ __global__ void __launch_bounds__(kGradThreads) delta_chunk_grad_kernel(const __
       outer(dk, four(&sm.b[m][ty * 4]), q);
       outer(dk, four(&sm.n[m][ty * 4]), k);
     }
-    // parts of q . dq over these keys, and of <dS, S> before the chunk
-    float* part = p.partial + (((int64_t)blockIdx.y * p.batch * p.nch + b * p.nch + chunk) * p.H + h) * (kChunk + 1);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 q = four(&sm.q[ty * 4 + i][tx * 4]);
-      float d = q.x * dqh[i][0] + q.y * dqh[i][1] + q.z * dqh[i][2] + q.w * dqh[i][3];
-#pragma unroll
-      for (int o = 8; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-      if (tx == 0) part[ty * 4 + i] = d;
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) dq[i][j] += dqh[i][j];
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, o);
-    if ((tid & 31) == 0) sm.sum[tid >> 5] = inner;
     __syncthreads();
-    if (tid == 0) {
+    // dg over these keys.  The pairs a > b, summed along a's row before every step, in b's place (four threads a row), ...
+    const int row = tid >> 2, part = tid & 3;
+    {
+      float w[16], ahead = 0.f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int c = part * 16 + j;
+        w[j] = c < row ? fmaf(sm.b[row][c], sm.qk[row][c], sm.n[row][c] * sm.kk[row][c]) : 0.f;
+        ahead += w[j];
+      }
+      float upto = ahead;
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        const float v = __shfl_up_sync(0xffffffffu, upto, o, 4);
+        if (part >= o) upto += v;
+      }
+      float sum = __shfl_up_sync(0xffffffffu, upto, 1, 4);
+      if (part == 0) sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        sm.b[row][part * 16 + j] = sum;
+        sum += w[j];
+      }
+    }
+    __syncthreads();
+    {   // ... then over the rows from the step on, with what these read and the steps before have written
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int a = part * 16 + j;
+        sum += a >= row ? sm.b[a][row] + sm.read[a] : sm.wrote[a];
+      }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       float all = 0.f;
+#pragma unroll
       for (int w = 0; w < kGradThreads / 32; ++w) all += sm.sum[w];
-      part[kChunk] = all;
+      if (part == 0)
+        p.partial[(((int64_t)blockIdx.y * p.batch * p.nch + b * p.nch + chunk) * p.H + h) * kChunk + row] =
+            fmaf(all, sm.c.from[kChunk - 1], sum);
     }
   }
 #pragma unroll
@@ -444,44 +521,26 @@ __global__ void __launch_bounds__(kGradThreads) delta_chunk_grad_kernel(const __
     }
 }
 
-// dg and dbeta of one chunk and head: a warp takes eight steps' products over V, then the sums along the chunk.
-template <typename T>
+// dbeta of one chunk and head, a warp takes eight steps' products over V, and dg, summed over the blocks of keys.
 __global__ void __launch_bounds__(256) delta_gate_grad_kernel(const __grid_constant__ Params p, int key_blocks) {
-  __shared__ float d[kChunk];
   int64_t id = blockIdx.x;
   const int64_t h = id % p.H;
   id /= p.H;
   const int64_t chunk = id % p.nch, b = id / p.nch, t0 = chunk * kChunk;
   const int n = (int)min((int64_t)kChunk, p.T - t0), lane = threadIdx.x & 31;
-  const int64_t per = p.batch * p.nch * p.H * (kChunk + 1);
-  const float* part = p.partial + blockIdx.x * (int64_t)(kChunk + 1);
   for (int i = threadIdx.x >> 5; i < n; i += 8) {
     const int64_t at = ((b * p.T + t0 + i) * p.H + h) * p.V;
-    const T* v = static_cast<const T*>(p.v) + b * p.vs[0] + (t0 + i) * p.vs[1] + h * p.vs[2];
-    float de = 0.f, dvv = 0.f;
-    for (int64_t c = lane; c < p.V; c += 32) {
-      const float du = p.du[at + c];
-      de = fmaf(du, p.err[at + c], de);
-      dvv = fmaf(du, ld_f32(v + c), dvv);
-    }
+    float de = 0.f;
+    for (int64_t c = lane; c < p.V; c += 32) de = fmaf(p.du[at + c], p.err[at + c], de);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      de += __shfl_xor_sync(0xffffffffu, de, o);
-      dvv += __shfl_xor_sync(0xffffffffu, dvv, o);
-    }
-    if (lane == 0) {
-      const float beta = __ldg(p.beta + b * p.bs[0] + (t0 + i) * p.bs[1] + h);
-      float qdq = 0.f;
-      for (int kb = 0; kb < key_blocks; ++kb) qdq += part[kb * per + i];
-      d[i] = qdq - beta * dvv;
-      p.dbeta[(b * p.T + t0 + i) * p.H + h] = de;
-    }
+    for (int o = 16; o; o >>= 1) de += __shfl_xor_sync(0xffffffffu, de, o);
+    if (lane == 0) p.dbeta[(b * p.T + t0 + i) * p.H + h] = de;
   }
-  __syncthreads();
   if (p.dg && threadIdx.x < n) {
+    const int64_t per = p.batch * p.nch * p.H * kChunk;
+    const float* part = p.partial + blockIdx.x * (int64_t)kChunk + threadIdx.x;
     float sum = 0.f;
-    for (int kb = 0; kb < key_blocks; ++kb) sum += part[kb * per + kChunk];
-    for (int j = 0; j < (int)threadIdx.x; ++j) sum -= d[j];
+    for (int kb = 0; kb < key_blocks; ++kb) sum += part[kb * per];
     p.dg[(b * p.T + t0 + threadIdx.x) * p.H + h] = sum;
   }
 }
@@ -631,7 +690,7 @@ Layout layout(const gated_delta_rule_shape* s, bool back) {
     L.du = take(steps);
     L.states = take(states);
     L.dstates = take(states);
-    L.partial = take((size_t)key_blocks(s->key_dim) * (size_t)s->batch * nch * (size_t)s->heads * (kChunk + 1) * 4);
+    L.partial = take((size_t)key_blocks(s->key_dim) * (size_t)s->batch * nch * (size_t)s->heads * kChunk * 4);
   }
   L.total = at;
   return L;
@@ -710,7 +769,7 @@ cudaError_t launch_backward(const Params& p, cudaStream_t st) {
   delta_chunk_grad_kernel<T><<<cells, kGradThreads, sizeof(GradSmem), st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  delta_gate_grad_kernel<T><<<(unsigned)(p.batch * p.nch * p.H), 256, 0, st>>>(p, key_blocks(p.K));
+  delta_gate_grad_kernel<<<(unsigned)(p.batch * p.nch * p.H), 256, 0, st>>>(p, key_blocks(p.K));
   return cudaGetLastError();
 }
 

@@ -19,7 +19,7 @@ struct Params {
   float *final_state, *states_out, *dg, *dbeta, *dinit;
   float *err, *du;                     // [b,T,H,V]: v - S k of every step; gradient of u
   float* dstates;                      // [b,nch,H,V,K]: gradient of the state before every chunk
-  float* partial;                      // [key blocks][b*nch*H][kChunk + 1]
+  float* partial;                      // [key blocks][b*nch*H][kChunk]: of dg
   int64_t batch, T, Hk, H, K, V, nch;
   int64_t qs[3], ks[3], vs[3], ds[3], gs[2], bs[2];
   int64_t slices;                      // blocks side by side in V

@@ -1,4 +1,5 @@
-"""Gated delta rule: decays between steps that lie far down a chunk's sum of g."""
+"""Gated delta rule: the gradient of the gates behind a reset of a large state, and decays between steps that lie far down
+a chunk's sum of g."""
 import math
 
 import numpy as np
@@ -7,7 +8,28 @@ import torch
 
 import chunked_ssd_scan_gb300 as pkg
 from tests import delta_reference as ref
+from tests import test_gated_delta_rule as td
 from tests.parity_util import to_np
+
+
+# on the CUDA cores: f32, bf16 behind an odd element, and wide heads
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(1, 64, 1, 1, 64, 64), (2, 150, 2, 4, 60, 100), (1, 130, 1, 2, 128, 72),
+                                   (1, 100, 1, 1, 200, 40), (1, 70, 1, 2, 64, 264)], ids=str)
+@pytest.mark.parametrize("dtype,layout", [("f32", "plain"), ("bf16", "odd")])
+@pytest.mark.parametrize("size", [30.0, 1000.0])
+def test_gate_gradient_behind_a_reset(size, dtype, layout, shape):
+    """The initial state is large and cut off at step 8 by a decay of e^-30: what g's gradient is behind that does not
+    depend on it, and is held to the same bound as without it."""
+    d = td.inputs(*shape, dtype, seed=21, layout=layout, dev="cuda")
+    d["init"] = torch.randn(d["init"].shape, generator=torch.Generator().manual_seed(22)).cuda() * size
+    d["g"][:, 8] = -30.0
+    h = td.host(d)
+    want = ref.delta_grad(h["q"], h["k"], h["v"], h["g"], h["beta"], h["dy"], h["init"], None, h["dfinal"])
+    got = td.run_backward(d, dtype, None)
+    # (fp32 of a state that has decayed by e^-30 from 1000: 1e-10)
+    ref.check(to_np(got["dg"])[:, 9:], want["dg"][:, 9:], dtype, "dg behind the reset")
+    ref.check(to_np(got["dg"])[:, :9], want["dg"][:, :9], dtype, "dg up to the reset")
 
 
 @pytest.mark.gpu
