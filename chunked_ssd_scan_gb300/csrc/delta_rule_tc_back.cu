@@ -443,13 +443,25 @@ __device__ __forceinline__ float sum_columns(float (&v)[N]) {
   return v[0];
 }
 
-__device__ __forceinline__ float scan_up(float v, int lane) {   // sum over the lanes up to this one
+// Sums over the lanes before this one, and behind it.  Each adds up its own lanes: the sum of all less the others would leave
+// the rounding of large values (of steps that a reset has cut off) on small ones.
+__device__ __forceinline__ float sum_before(float v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const float u = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += u;
   }
-  return v;
+  v = __shfl_up_sync(0xffffffffu, v, 1);
+  return lane ? v : 0.f;
+}
+__device__ __forceinline__ float sum_behind(float v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float u = __shfl_down_sync(0xffffffffu, v, o);
+    if (lane + o < 32) v += u;
+  }
+  v = __shfl_down_sync(0xffffffffu, v, 1);
+  return lane < 31 ? v : 0.f;
 }
 
 __global__ void __launch_bounds__(kGradThreads, 1)
@@ -857,17 +869,17 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       for (int c = 0; c < 3; ++c) {
         const float* of = sums + 16 * kChunk + c * 128;
         const float p0 = of[2 * lane] + of[64 + 2 * lane], p1 = of[2 * lane + 1] + of[65 + 2 * lane];
-        const float upto = scan_up(p0 + p1, lane), rest = __shfl_sync(0xffffffffu, upto, 31) - upto + p1;
+        const float rest = sum_behind(p0 + p1, lane) + p1;
         if (2 * lane >= 16 * (c + 1)) {
           g[0] += rest + p0;
           g[1] += rest;
         }
       }
       float all = lane < 16 ? sums[24 * kChunk + lane] : 0.f;
-      all = __shfl_sync(0xffffffffu, scan_up(all, lane), 31);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
       // from a step to the chunk's end; the sums before it
-      const float r1 = scan_up(rho[0] + rho[1], lane), after = __shfl_sync(0xffffffffu, r1, 31) - r1;
-      const float before = scan_up(sigma[0] + sigma[1], lane) - sigma[0] - sigma[1];
+      const float after = sum_behind(rho[0] + rho[1], lane), before = sum_before(sigma[0] + sigma[1], lane);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int i = 2 * lane + e;

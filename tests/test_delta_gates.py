@@ -12,11 +12,11 @@ from tests import test_gated_delta_rule as td
 from tests.parity_util import to_np
 
 
-# on the CUDA cores: f32, bf16 behind an odd element, and wide heads
+# the CUDA cores (f32, bf16 behind an odd element, wide heads) and the tensor cores
 @pytest.mark.gpu
 @pytest.mark.parametrize("shape", [(1, 64, 1, 1, 64, 64), (2, 150, 2, 4, 60, 100), (1, 130, 1, 2, 128, 72),
                                    (1, 100, 1, 1, 200, 40), (1, 70, 1, 2, 64, 264)], ids=str)
-@pytest.mark.parametrize("dtype,layout", [("f32", "plain"), ("bf16", "odd")])
+@pytest.mark.parametrize("dtype,layout", [("f32", "plain"), ("bf16", "odd"), ("bf16", "plain")])
 @pytest.mark.parametrize("size", [30.0, 1000.0])
 def test_gate_gradient_behind_a_reset(size, dtype, layout, shape):
     """The initial state is large and cut off at step 8 by a decay of e^-30: what g's gradient is behind that does not
