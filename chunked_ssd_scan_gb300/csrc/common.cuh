@@ -18,7 +18,8 @@ struct WsHeader {
   int32_t pad0;
   int64_t detail;    // kernel-specific detail word of the first latched error
   uint32_t counters[2];  // tickets taken and blocks done of a running kernel; zero between kernels
-  uint32_t reserved[58];
+  uint32_t give_up_site, give_up_warps;  // index-checked build: the wait that runs out at once, in these warps (bits)
+  uint32_t reserved[56];
 };
 static_assert(sizeof(WsHeader) == 256, "workspace header must be 256 bytes");
 

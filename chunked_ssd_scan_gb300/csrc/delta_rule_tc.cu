@@ -46,7 +46,7 @@ struct PrepSmem {
   ChunkDecay c;
   uint64_t loaded, done;
   uint32_t tmem;
-  int abort, keep;
+  int abort;
 };
 
 __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kPrepThreads, 6) delta_chunk_kernel(const __gr
   if (threadIdx.x == 0) {
     mbar_init(&sm.loaded, 1);
     mbar_init(&sm.done, 1);
-    sm.abort = sm.keep = 0;
+    sm.abort = 0;
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -210,8 +210,12 @@ __global__ void __launch_bounds__(kPrepThreads, 6) delta_chunk_kernel(const __gr
     }
     if (ok) mma_commit_elect(&sm.done);   // else every wait for it ends by the abort flag
   }
-  const bool done = wait_bar(&sm.done, 0, &sm.abort, p.hdr, 2);
-  if (!done && ok) sm.keep = 1;   // a product may still write TMEM: it stays allocated
+  // All warps go on, or none: one wait may give up as another one's barrier completes.
+  const bool done = !__syncthreads_or(!wait_bar(&sm.done, 0, &sm.abort, p.hdr, 2));
+  if (!done && warp == 0) {   // what this block has on its way
+    mbar_wait_bounded(&sm.loaded, 0, kDrainNs);
+    if (ok) mbar_wait_bounded(&sm.done, 0, kDrainNs);
+  }
   tc_fence_after();
   const int row = (warp & 1) * 32 + lane;
   const uint32_t mine = tmem + ((uint32_t)(warp * 32) << 16);
@@ -294,7 +298,7 @@ __global__ void __launch_bounds__(kPrepThreads, 6) delta_chunk_kernel(const __gr
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 0 && !sm.keep) tmem_dealloc(tmem, 64);
+  if (warp == 0) tmem_dealloc(tmem, 64);
 }
 
 // ---------------------------------------------------------------------------------------------------------------------

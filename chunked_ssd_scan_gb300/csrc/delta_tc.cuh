@@ -55,9 +55,20 @@ static __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, vo
     }
   }
 }
+// A wait that gave up has set the flag, which ends all others of the block.  Its warp must still meet every barrier that it
+// shares with warps whose waits came through: it goes on without waiting, or all settle it at a barrier.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, WsHeader* hdr, int site) {
+#ifdef SSD_INDEX_CHECKS
+  // How a test comes to what is behind a wait that ran out: the workspace names the site and the warps.
+  if (hdr && hdr->give_up_site == (uint32_t)site && (hdr->give_up_warps >> (threadIdx.x / 32) & 1)) {
+    *abort = 1;
+    latch_error(hdr, SSD_ERR_TIMEOUT, site);
+    return false;
+  }
+#endif
   return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort, hdr, site);
 }
+constexpr uint64_t kDrainNs = 2000000000ull;   // that a block waits at its end for its own copies and products
 
 // v = hi + lo, two bf16 terms with 16 bits of mantissa between them, for a pair of values (the first in the low half).
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
