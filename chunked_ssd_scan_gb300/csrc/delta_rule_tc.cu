@@ -324,7 +324,7 @@ struct ChainSmem {
   uint8_t s[4][128 * 64];   // 128 rows of 16 keys of the state on their way out, for each quarter of the keys
   ChainBars bar;
   uint32_t tmem;
-  int abort, keep;
+  int abort;
 };
 
 // kY: with the outputs; without them Q, P and the products with them are left out.
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
   constexpr int Kp = KB * 64;
   volatile int* abort = &sm.abort;
   if (threadIdx.x == 0) {
-    sm.abort = sm.keep = 0;
+    sm.abort = 0;
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar.full[s], 1);
       mbar_init(&bar.empty[s], 1);
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     bool drained = true;   // nothing may still be written to this block's shared memory when it ends
     for (int s = 0; s < 2; ++s) {
       const int loads = issued > s ? (issued - 1 - s) / 2 + 1 : 0;
-      if (loads > 0) drained &= mbar_wait_bounded(&bar.full[s], (loads - 1) & 1, 2000000000ull);
+      if (loads > 0) drained &= mbar_wait_bounded(&bar.full[s], (loads - 1) & 1, kDrainNs);
     }
     if (!drained && lane == 0) latch_error(p.hdr, SSD_ERR_TIMEOUT, 11);
   } else if (warp == 20) {   // products
@@ -406,9 +406,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       const uint32_t t_lo = sdesc_sw128_lo(smem_u32(st.t), 0), p_lo = sdesc_sw128_lo(smem_u32(st.p), 0);
       if (!wait_bar(&bar.full[s], (c >> 1) & 1, abort, p.hdr, 12)) break;
       // X = S K^T, a quarter of the keys as soon as its terms are there
+      bool ready = true;
 #pragma unroll
       for (int part = 0; part < 4; ++part) {
-        if (!wait_bar(&bar.s_ready[part], par, abort, p.hdr, 13)) break;
+        ready = ready && wait_bar(&bar.s_ready[part], par, abort, p.hdr, 13);
+        if (!ready) break;
         tc_fence_after();
 #pragma unroll
         for (int ks = part * KB; ks < (part + 1) * KB; ++ks) {
@@ -417,7 +419,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
           mma_ts_we(tmem + kColX, tmem + kColS + Kp / 2 + ks * 8, at, kDHi, id_k, 1);
         }
       }
-      if (*abort) break;
+      if (!ready) break;
       mma_commit_elect(&bar.x_full);
       // U = V T^T - (D X) T^T
       if (kY && c > 0 && !wait_bar(&bar.o2_full, (c - 1) & 1, abort, p.hdr, 14)) break;   // U's terms have been read
@@ -475,10 +477,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       mma_commit_elect(&bar.empty[s]);
     }
     mma_commit_elect(&bar.drain);
-    if (!mbar_wait_bounded(&bar.drain, 0, 2000000000ull) && lane == 0) {
-      sm.keep = 1;   // products may still write TMEM: it stays allocated
-      latch_error(p.hdr, SSD_ERR_TIMEOUT, 20);
-    }
+    if (!mbar_wait_bounded(&bar.drain, 0, kDrainNs) && lane == 0) latch_error(p.hdr, SSD_ERR_TIMEOUT, 20);
   } else if (warp < kStateWarps) {   // the state, and the operands on the way to the next one
     constexpr int KQ = Kp / 4;
     const int part = warp >> 2, row = v0 + (warp & 3) * 32 + lane, k0 = part * KQ, j0 = part * 16;
@@ -505,6 +504,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       S[k + 3] = f.w;
     }
     const bool keep = p.states_out && !seg.pre;
+    bool on = true;   // after a wait that gave up, without waiting: the quarter's warps meet at its barrier
     int cell = (b * all_chunks + first) * (int)p.H + h;
     for (int c = 0; c < nch; ++c, cell += (int)p.H) {
       const int s = c & 1;
@@ -516,9 +516,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.s_ready[part]);
       if (keep) send_state(sm.s[part], &m.states, S, part, 0, v0, cell, p.K);
-      if (!wait_bar(&bar.full[s], (c >> 1) & 1, abort, p.hdr, 21)) break;   // the decays
+      on = on && wait_bar(&bar.full[s], (c >> 1) & 1, abort, p.hdr, 21);   // the decays
       const float all = st.from[kChunk - 1];
-      if (!wait_bar(&bar.x_full, par, abort, p.hdr, 22)) break;
+      on = on && wait_bar(&bar.x_full, par, abort, p.hdr, 22);
       tc_fence_after();
       float x[16];
       tmem_ld16(tmem + lanes + kColX + j0, x);
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       if (lane == 0) mbar_arrive(&bar.r_ready);
       if constexpr (KB == 2)
         if (keep) send_state(sm.s[part], &m.states, S, part, KQ / 2, v0, cell, p.K);
-      if (!wait_bar(&bar.u_full, par, abort, p.hdr, 23)) break;
+      on = on && wait_bar(&bar.u_full, par, abort, p.hdr, 23);
       tc_fence_after();
       tmem_ld16(tmem + lanes + kColU + j0, x);
       tmem_ld_wait();
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.u_ready);
       }
-      if (!wait_bar(&bar.d_full, par, abort, p.hdr, 24)) break;
+      on = on && wait_bar(&bar.d_full, par, abort, p.hdr, 24);
       tc_fence_after();
 #pragma unroll
       for (int k = 0; k < KQ; k += 16) {
@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     if ((threadIdx.x & 127) == 0) bulk_wait_group<0>();
     float* end = seg.pre ? (identity ? seg.map + seg_at * p.K * p.K : seg.end + seg_at * KV)
                  : part_of == seg.n - 1 && p.final_state ? p.final_state + seq * KV : nullptr;
-    if (end && live && !*abort) {
+    if (end && live && on) {
       const bool wide = (reinterpret_cast<uintptr_t>(end) & 31) == 0;
 #pragma unroll
       for (int k = 0; k < KQ; k += 8)
@@ -588,12 +588,13 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
   } else if constexpr (kY) {   // y: a thread has a value
     const int v = (warp & 3) * 32 + lane;
     uint8_t* column = sm.y + (v >> 6) * kTileBytes;
+    bool on = true;   // as above
     for (int c = 0; c < nch; ++c) {
       const int s = c & 1;
       const uint32_t par = c & 1;
       const Stage<KB>& st = sm.st[s];
-      if (!wait_bar(&bar.full[s], (c >> 1) & 1, abort, p.hdr, 25)) break;
-      if (!wait_bar(&bar.o1_full, par, abort, p.hdr, 26)) break;
+      on = on && wait_bar(&bar.full[s], (c >> 1) & 1, abort, p.hdr, 25);
+      on = on && wait_bar(&bar.o1_full, par, abort, p.hdr, 26);
       tc_fence_after();
       // 16 columns at a time: with more the kernel's 80 registers spill, and a reload from beyond the L1 stalls the walk
 #pragma unroll 1
@@ -619,7 +620,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       if (lane == 0) mbar_arrive(&bar.o_scaled);
       if (warp == kStateWarps && lane == 0) bulk_wait_group_read<0>();   // the last chunk's rows have left
       named_barrier(1, 128);
-      if (!wait_bar(&bar.o2_full, par, abort, p.hdr, 27)) break;
+      on = on && wait_bar(&bar.o2_full, par, abort, p.hdr, 27);
       tc_fence_after();
 #pragma unroll 1
       for (int j0 = 0; j0 < kChunk; j0 += 16) {
@@ -646,7 +647,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 20 && !sm.keep) {
+  if (warp == 20) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

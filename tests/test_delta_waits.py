@@ -64,3 +64,15 @@ def backward(checked, plans, shape, site, warps):
 def test_chunks(checked, plans, site, warps, shape):
     forward(checked, plans, shape, site, warps)
     backward(checked, plans, shape, site, warps)
+
+
+# in segments, too
+LONG = (1, 1025, 2, 2, 128, 128)
+ONE = [(site, 1 << w) for site in (21, 22, 23, 24) for w in (0, 6, 15)] + [(site, 1 << w) for site in (25, 26, 27) for w in (16, 19)]
+
+
+@pytest.mark.parametrize("shape", [SMALL, LONG], ids=str)
+@pytest.mark.parametrize("site,warps", [(site, ALL) for site in (10, *range(12, 20), *range(21, 28))] + ONE, ids=str)
+def test_walk(checked, plans, site, warps, shape):
+    """All warps of a role, or one of those that share a barrier: the others of its quarter must not wait for it."""
+    forward(checked, plans, shape, site, warps)
