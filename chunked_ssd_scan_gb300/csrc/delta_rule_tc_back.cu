@@ -43,7 +43,7 @@ struct BackSmem {
   uint64_t kdy_full[2], kdy_empty[2], q_full, q_empty, t_full, t_empty, p_full, p_empty;
   uint64_t g_ready[4], y_full, u_ready, r_full, w_ready, r_free, dys_ready, d_full, drain;
   uint32_t tmem;
-  int abort, keep;
+  int abort;
 };
 
 template <int KB>
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
   constexpr int Kp = KB * 64;
   volatile int* abort = &sm.abort;
   if (threadIdx.x == 0) {
-    sm.abort = sm.keep = 0;
+    sm.abort = 0;
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.kdy_full[s], 1);
       mbar_init(&sm.kdy_empty[s], 1);
@@ -114,11 +114,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     bool drained = true;
     for (int s = 0; s < 2; ++s) {
       const int loads = pairs > s ? (pairs - 1 - s) / 2 + 1 : 0;
-      if (loads > 0) drained &= mbar_wait_bounded(&sm.kdy_full[s], (loads - 1) & 1, 2000000000ull);
+      if (loads > 0) drained &= mbar_wait_bounded(&sm.kdy_full[s], (loads - 1) & 1, kDrainNs);
     }
-    if (ps > 0) drained &= mbar_wait_bounded(&sm.p_full, (ps - 1) & 1, 2000000000ull);
-    if (ts > 0) drained &= mbar_wait_bounded(&sm.t_full, (ts - 1) & 1, 2000000000ull);
-    if (qs > 0) drained &= mbar_wait_bounded(&sm.q_full, (qs - 1) & 1, 2000000000ull);
+    if (ps > 0) drained &= mbar_wait_bounded(&sm.p_full, (ps - 1) & 1, kDrainNs);
+    if (ts > 0) drained &= mbar_wait_bounded(&sm.t_full, (ts - 1) & 1, kDrainNs);
+    if (qs > 0) drained &= mbar_wait_bounded(&sm.q_full, (qs - 1) & 1, kDrainNs);
     if (!drained && lane == 0) latch_error(p.hdr, SSD_ERR_TIMEOUT, 44);
   } else if (warp == 20) {   // products
     constexpr uint32_t id_k = idesc_bf16(128, 64, 0, 0), id_p = idesc_bf16(128, 64, 1, 1), id_t = idesc_bf16(128, 64, 0, 1);
@@ -141,9 +141,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       }
       mma_commit_elect(&sm.p_empty);
       // K G^T
+      bool ready = true;
 #pragma unroll
       for (int part = 0; part < 4; ++part) {
-        if (!wait_bar(&sm.g_ready[part], par, abort, p.hdr, 47)) break;
+        ready = ready && wait_bar(&sm.g_ready[part], par, abort, p.hdr, 47);
+        if (!ready) break;
         tc_fence_after();
 #pragma unroll
         for (int ks = part * KB; ks < (part + 1) * KB; ++ks) {
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
           mma_ts_we(tmem + kColU, tmem + kColG + Kp / 2 + ks * 8, at, kDHi, id_k, 1);
         }
       }
-      if (*abort) break;
+      if (!ready) break;
       mma_commit_elect(&sm.y_full);
       // scale (D dY)^T Q, while dU is made
       if (!wait_bar(&sm.q_full, par, abort, p.hdr, 48)) break;
@@ -190,15 +192,13 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       mma_commit_elect(&sm.kdy_empty[s]);
     }
     mma_commit_elect(&sm.drain);
-    if (!mbar_wait_bounded(&sm.drain, 0, 2000000000ull) && lane == 0) {
-      sm.keep = 1;
-      latch_error(p.hdr, SSD_ERR_TIMEOUT, 54);
-    }
+    if (!mbar_wait_bounded(&sm.drain, 0, kDrainNs) && lane == 0) latch_error(p.hdr, SSD_ERR_TIMEOUT, 54);
   } else if (warp < kStateWarps) {   // G
     constexpr int KQ = Kp / 4;
     const int part = warp >> 2, row = (warp & 3) * 32 + lane, k0 = part * KQ, j0 = part * 16;
     const bool live = row < p.V;
     const int64_t at = (((int64_t)b * p.H + h) * p.V + row) * p.K + k0;
+    bool on = true;   // after a wait that gave up, without waiting: the quarter's warps meet at its barrier
     float G[KQ];
 #pragma unroll
     for (int k = 0; k < KQ; ++k) G[k] = 0.f;
@@ -213,9 +213,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.g_ready[part]);
       send_state(sm.s[part], &m.states, G, part, 0, 0, cell, p.K);
-      if (!wait_bar(&sm.kdy_full[s], (n >> 1) & 1, abort, p.hdr, 55)) break;   // the decays
+      on = on && wait_bar(&sm.kdy_full[s], (n >> 1) & 1, abort, p.hdr, 55);   // the decays
       const float all = sm.decays[s][kChunk - 1];
-      if (!wait_bar(&sm.y_full, par, abort, p.hdr, 56)) break;
+      on = on && wait_bar(&sm.y_full, par, abort, p.hdr, 56);
       tc_fence_after();
       float x[16], y[16];
       tmem_ld16(tmem + lanes + kColY + j0, y);
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.u_ready);
       if constexpr (KB == 2) send_state(sm.s[part], &m.states, G, part, KQ / 2, 0, cell, p.K);
-      if (!wait_bar(&sm.r_full, par, abort, p.hdr, 57)) break;
+      on = on && wait_bar(&sm.r_full, par, abort, p.hdr, 57);
       tc_fence_after();
       tmem_ld16(tmem + lanes + kColR + j0, x);
       tmem_ld_wait();
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.w_ready);
-      if (!wait_bar(&sm.d_full, par, abort, p.hdr, 58)) break;
+      on = on && wait_bar(&sm.d_full, par, abort, p.hdr, 58);
       tc_fence_after();
 #pragma unroll
       for (int k = 0; k < KQ; k += 16) {
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       }
     }
     if ((threadIdx.x & 127) == 0) bulk_wait_group<0>();
-    if (p.dinit && live && !*abort) {
+    if (p.dinit && live && on) {
       const bool wide = (reinterpret_cast<uintptr_t>(p.dinit) & 31) == 0;
 #pragma unroll
       for (int k = 0; k < KQ; k += 8)
@@ -283,11 +283,12 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     }
   } else {   // scale D dY in two terms, and dR on its way out
     const int t = threadIdx.x - kStateWarps * 32, v = (warp & 3) * 32 + lane;
+    bool on = true;   // as above
     for (int n = 0; n < nch; ++n) {
       const int s = n & 1, c = nch - 1 - n;
       const uint32_t par = n & 1;
-      if (!wait_bar(&sm.kdy_full[s], (n >> 1) & 1, abort, p.hdr, 59)) break;
-      if (n > 0 && !wait_bar(&sm.d_full, (n - 1) & 1, abort, p.hdr, 60)) break;   // the last terms have been read
+      on = on && wait_bar(&sm.kdy_full[s], (n >> 1) & 1, abort, p.hdr, 59);
+      if (n > 0) on = on && wait_bar(&sm.d_full, (n - 1) & 1, abort, p.hdr, 60);   // the last terms have been read
 #pragma unroll 2
       for (int m8 = 0; m8 < 8; ++m8) {   // 16 bytes of a row
         const int at = m8 * 128 + t, blk = at >> 9, i = (at >> 3) & 63, col = (at & 7) * 8;
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.dys_ready);
-      if (!wait_bar(&sm.r_full, par, abort, p.hdr, 61)) break;
+      on = on && wait_bar(&sm.r_full, par, abort, p.hdr, 61);
       tc_fence_after();
       if (warp == kStateWarps && lane == 0) bulk_wait_group_read<0>();
       named_barrier(1, 128);
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 20 && !sm.keep) {
+  if (warp == 20) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

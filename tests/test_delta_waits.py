@@ -76,3 +76,14 @@ ONE = [(site, 1 << w) for site in (21, 22, 23, 24) for w in (0, 6, 15)] + [(site
 def test_walk(checked, plans, site, warps, shape):
     """All warps of a role, or one of those that share a barrier: the others of its quarter must not wait for it."""
     forward(checked, plans, shape, site, warps)
+
+
+ONE_BACK = ([(site, 1 << w) for site in (55, 56, 57, 58) for w in (0, 6, 15)]
+            + [(site, 1 << w) for site in (59, 60, 61) for w in (16, 19)])
+
+
+@pytest.mark.parametrize("shape", [SMALL, WIDE], ids=str)
+@pytest.mark.parametrize("site,warps", [(site, ALL) for site in (*range(40, 44), *range(45, 54), *range(55, 62))] + ONE_BACK,
+                         ids=str)
+def test_walk_back(checked, plans, site, warps, shape):
+    backward(checked, plans, shape, site, warps)
