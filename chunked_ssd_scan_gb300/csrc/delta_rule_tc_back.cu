@@ -365,9 +365,9 @@ struct GradSmem {
   uint8_t n2[2 * kTileBytes];         // diag(beta) N'
   ChunkDecay c;
   float dot[kChunk];                  // dR . v
-  uint64_t loaded, done, shadow;
+  uint64_t loaded, done, shadow, drain;
   uint32_t tmem;
-  int abort, keep;
+  int abort;
 };
 static_assert(sizeof(GradSmem) <= 232448, "shared memory of a block");
 
@@ -476,7 +476,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     mbar_init(&sm.loaded, 1);
     mbar_init(&sm.done, 1);
     mbar_init(&sm.shadow, 1);
-    sm.abort = sm.keep = 0;
+    mbar_init(&sm.drain, 1);
+    sm.abort = 0;
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -499,7 +500,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   const uint32_t bm_lo = sdesc_sw128_lo(smem_u32(sm.v), 0), n2_lo = sdesc_sw128_lo(smem_u32(sm.n2), 0);
   // of 128 values in blocks of 64: step ks of 16
   auto by64 = [](int ks, uint32_t block) { return (ks >> 2) * (block >> 4) + (ks & 3) * 2; };
-  uint32_t phase = 0, turn = 0;
+  uint32_t phase = 0, turn = 0, announced = 0;   // products waited for; loads waited for, and under way
   // The loads of a head's operands, in three parts (by warp 0); the first announces all.
   struct Item {
     int64_t id, h;   // of chunks and key heads; head
@@ -513,6 +514,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   auto load_gradients = [&](const Item& i) {
     int64_t b, chunk, hk;
     split(i.id, b, chunk, hk);
+    ++announced;
     mbar_arrive_expect_tx_elect(&sm.loaded, (i.h == hk * group ? 14 : 10) * kTileBytes + (uint32_t)(KV * 4));
 #pragma unroll
     for (int vb = 0; vb < 2; ++vb) {
@@ -544,7 +546,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   }
   float dq[16] = {}, dk[16] = {};
   bool ok = true;
-  while (ok && item.id < blocks) {
+  while (item.id < blocks) {
     int64_t b, chunk, hk;
     split(item.id, b, chunk, hk);
     const int64_t h = item.h, cell = cell_of(item), t0 = chunk * kChunk;
@@ -553,7 +555,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     const Item next = last_head ? Item{item.id + gridDim.x, (item.id + gridDim.x) % p.Hk * group} : Item{item.id, h + 1};
     const bool more = next.id < blocks;
     if (warp == 1) chunk_decay_warp(p, sm.c, b, t0, n, h, lane);
-    const bool here = wait_bar(&sm.loaded, turn++ & 1, abort, p.hdr, 70);
+    ok = wait_bar(&sm.loaded, turn++ & 1, abort, p.hdr, 70);
     {
       float4 f[8];   // from where the copy put it, then over it
       read_state(f, reinterpret_cast<const float*>(sm.s), p.V, p.K);
@@ -562,9 +564,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
     fence_proxy_async_smem();
     tc_fence_before();
-    __syncthreads();
+    ok = !__syncthreads_or(!ok);   // all warps go on, or none
     tc_fence_after();
-    if (!here || *abort) break;   // (the same for all: the flag is set before the barrier)
+    if (!ok) break;
     if (warp == 0) {
       // X = S K^T and V T^T
 #pragma unroll
@@ -633,9 +635,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
     if (tid == 0) bulk_wait_group_read<0>();   // dq and dk have left U's place
     tc_fence_before();
-    __syncthreads();
+    ok = !__syncthreads_or(!ok);
     tc_fence_after();
-    if (*abort) break;
+    if (!ok) break;
     if (warp == 0) {
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
@@ -672,9 +674,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
     fence_proxy_async_smem();
     tc_fence_before();
-    __syncthreads();
+    ok = !__syncthreads_or(!ok);
     tc_fence_after();
-    if (*abort) break;
+    if (!ok) break;
     if (warp == 0) {
       // [dY; dR hi] U^T, and (rows 64..127) dR lo U^T
 #pragma unroll
@@ -690,8 +692,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     float inner = 0.f;
     if (ok) inner = stage_state<true>(sm, gs) * sm.c.from[kChunk - 1];
     fence_proxy_async_smem();
-    __syncthreads();
-    if (*abort) break;
+    ok = !__syncthreads_or(!ok);
+    if (!ok) break;
     if (warp == 0) {
       // G^T U^T
 #pragma unroll
@@ -764,9 +766,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
     fence_proxy_async_smem();
     tc_fence_before();
-    __syncthreads();
+    ok = !__syncthreads_or(!ok);
     tc_fence_after();
-    if (*abort) break;
+    if (!ok) break;
     if (warp == 0) {
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
@@ -829,8 +831,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       for (int o = 16; o; o >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, o);
       if (lane == 0) sums[24 * kChunk + warp] = inner;
     }
-    __syncthreads();
-    if (*abort) break;
+    ok = !__syncthreads_or(!ok);
+    if (!ok) break;
     if (warp == 0 && more) load_rest(next);
     if (last_head) {   // dq, dk by steps: through U's place
       uint8_t* to = sm.u[0] + (row >> 6) * kTileBytes;
@@ -895,16 +897,14 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     item = next;
   }
   if (tid == 0) bulk_wait_group<0>();
-  if (*abort) {   // a load or a product may be on its way: wait for it, as long as for any other
-    if (warp == 0) {
-      mma_commit_elect(&sm.done);
-      if (!mbar_wait_bounded(&sm.done, phase & 1, 2000000000ull)) sm.keep = 1;
-      mbar_wait_bounded(&sm.loaded, turn & 1, 2000000000ull);
-    }
+  if (!ok && warp == 0) {   // a load or a product may be on its way
+    mma_commit_elect(&sm.drain);
+    mbar_wait_bounded(&sm.drain, 0, kDrainNs);
+    mbar_wait_bounded(&sm.loaded, (announced - 1) & 1, kDrainNs);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 0 && !sm.keep) {
+  if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

@@ -87,3 +87,9 @@ ONE_BACK = ([(site, 1 << w) for site in (55, 56, 57, 58) for w in (0, 6, 15)]
                          ids=str)
 def test_walk_back(checked, plans, site, warps, shape):
     backward(checked, plans, shape, site, warps)
+
+
+@pytest.mark.parametrize("shape", [SMALL, WIDE], ids=str)
+@pytest.mark.parametrize("site,warps", [(site, w) for site in range(70, 76) for w in (ALL, 1, 1 << 6, 1 << 15)], ids=str)
+def test_gradient(checked, plans, site, warps, shape):
+    backward(checked, plans, shape, site, warps)
