@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) delta_walk_kernel(const __grid_const
           d3 = fmaf(w.s[r][e + 3], kk[e + 3], d3);
         }
         const float err = fmaf(-a, sum8((d0 + d1) + (d2 + d3)), sm.v[i][w.row[r]]);
-        u[r] = beta * err;
+        u[r] = i < n ? beta * err : 0.f;   // past the end a state of infinities would give NaN
         if (w.l == 0 && p.err) sm.err[i][w.row[r]] = err;
       }
       float qq[KE];
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kThreads) delta_walk_back_kernel(const __grid_
           d3 = fmaf(w.s[r][e + 3], kk[e + 3], d3);
         }
         const float du = sum8((d0 + d1) + (d2 + d3));
-        dv[r] = beta * du;
+        dv[r] = i < n ? beta * du : 0.f;
         if (w.l == 0) {
           sm.err[i][w.row[r]] = du;
           sm.out[i][w.row[r]] = dv[r];
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kGradThreads) delta_chunk_grad_kernel(const __
       for (int j = 0; j < 4; ++j) {
         const int r = ty * 4 + i, c = tx * 4 + j;
         const float m = c <= r ? decay_between(sm.c, r, c) : 0.f;
-        sm.b[r][c] = p.scale * m * bb[i][j];
+        sm.b[r][c] = c <= r ? p.scale * m * bb[i][j] : 0.f;   // a bad value of a later step stays out
         if (c <= r) {   // symmetric: both steps' k gradients take it
           const float v = c < r ? -m * nn[i][j] : 0.f;
           sm.n[r][c] = v;

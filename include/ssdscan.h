@@ -564,7 +564,9 @@ size_t gated_delta_rule_workspace_bytes(const gated_delta_rule_shape* shape, int
  * and V multiples of 8, rows on 16-byte boundaries and not too few steps run on the tensor cores, where
  * what is computed on the way (the state, the writes, the inverse of a chunk's triangular system)
  * enters a product as two bf16 terms, 16 bits of mantissa: states are off by some 4e-6 of their size.
- * There a NaN or an infinity may reach the outputs of the steps before it in its chunk of 64 too.
+ * There a NaN or an infinity may reach the outputs of the steps before it in its chunk of 64 too, and an
+ * infinity becomes NaN.  On the CUDA cores an infinite write leaves its row of the state infinite, as the
+ * formula does; an output formed of infinities may be NaN where K is not 64, 128 or 256.
  * Asynchronous on `stream`; INVALID_ARG / UNSUPPORTED / WORKSPACE leave every output untouched.
  */
 ssd_status gated_delta_rule_forward(const gated_delta_rule_shape* shape, const void* q,
@@ -579,7 +581,8 @@ ssd_status gated_delta_rule_forward(const gated_delta_rule_shape* shape, const v
  *   dg (may be NULL), dbeta [b,T,H] f32 contiguous; dinit [b,H,V,K] f32 (may be NULL).
  * dy strided io_dtype, dfinal [b,H,V,K] f32 (NULL = zeros).  states: what the forward kept, or NULL
  * (the call then recomputes them in its workspace).  Sums run in a fixed order: the same bits every
- * run.
+ * run.  A NaN or an infinity may reach all gradients of its head (dq, dk: of its key head) that depend on
+ * it by the formula, and those of its chunk of 64 steps.
  */
 ssd_status gated_delta_rule_backward(const gated_delta_rule_shape* shape, const void* q,
                                      const void* k, const void* v, const float* g,
