@@ -57,12 +57,13 @@ __device__ __forceinline__ float exp2f_fast(float v) {
 // The weight of a logit.
 struct Weight {
   const uint2* table;   // 2^31 2^-j/256 as an integer and as a float
-  float most, ch, cl;   // largest logit; log2(e) / temperature in two parts
+  float half, ch, cl;   // half the largest logit; 2 log2(e) / temperature in two parts
   int shift;
   __device__ __forceinline__ uint64_t operator()(float x) const {   // without a branch
-    const float d = most - x;
+    // half the distance: two finite logits may lie further apart than the largest number
+    const float d = fmaf(x, -0.5f, half);
     const float ph = d * ch;
-    const float back = d - most, dl = (most - (d - back)) - (x + back);   // what d's rounding left
+    const float back = d - half, dl = (half - (d - back)) - fmaf(x, 0.5f, back);   // what d's rounding left
     const float pl = fmaf(d, ch, -ph) + fmaf(d, cl, dl * ch);
     // the nearest 256th, by an addition that leaves its number in the lowest bits
     const float at = fmaf(ph, 256.f, 12582912.f);
@@ -73,7 +74,7 @@ struct Weight {
     const uint32_t m = t.x + (uint32_t)(__float_as_int(fmaf(__uint_as_float(t.y), g, 12582912.f)) - 0x4b400000);
     const uint64_t w = ((uint64_t)m << (shift - 31)) >> ((k >> 8) & 63);
     // nothing far below, beneath an infinite largest logit, or of -inf at an infinite temperature (NaN)
-    return x == most ? 1ull << shift : ph < 62.5f ? w : 0;
+    return d > 0.f ? ph < 62.5f ? w : 0 : 1ull << shift;   // (of two infinite logits d is NaN)
   }
 };
 
@@ -203,8 +204,8 @@ struct Cut {
 };
 
 __device__ __forceinline__ int bin_of(const Weight& w, float inv, float x) {
-  const float d = (w.most - x) * inv;
-  return x == w.most ? 0 : d < (float)(kBins - 1) ? (int)d : kBins - 1;   // NaN (of infinities): the last
+  const float d = fmaf(x, -0.5f, w.half), at = d * inv;
+  return !(d > 0.f) ? 0 : at < (float)(kBins - 1) ? (int)at : kBins - 1;   // NaN (inf 0): the last
 }
 
 // The first token, in falling order, at which the running count of what `have` keeps reaches `want` >= 1 (kMass: the running
@@ -425,18 +426,19 @@ __global__ void __launch_bounds__(kThreads) token_sample_kernel(const __grid_con
     const uint32_t top_key = (uint32_t)(best >> 32);
     Weight w;
     w.table = sm.table;
-    w.most = __uint_as_float(top_key & 0x80000000u ? top_key & 0x7fffffffu : ~top_key);
-    if (w.most == kNegInf || temp == 0.f) {
+    const float most = __uint_as_float(top_key & 0x80000000u ? top_key & 0x7fffffffu : ~top_key);
+    if (most == kNegInf || temp == 0.f) {
       if (tid == 0 && all.rank == 0) {
-        p.ids[r] = w.most == kNegInf ? -1 : (int64_t)(uint32_t)~(uint32_t)best;
-        if (p.logprob) p.logprob[r] = w.most == kNegInf ? NAN : 0.f;
+        p.ids[r] = most == kNegInf ? -1 : (int64_t)(uint32_t)~(uint32_t)best;
+        if (p.logprob) p.logprob[r] = most == kNegInf ? NAN : 0.f;
       }
       continue;
     }
-    // log2(e) / temperature in two floats: the quotient, and what its product with the temperature leaves
+    // 2 log2(e) / temperature in two floats: the quotient, and what its product with the temperature leaves
     const float tt = fmaxf(temp, 1e-30f);
-    w.ch = 1.44269502f / tt;
-    w.cl = w.ch > 0.f ? (fmaf(-w.ch, tt, 1.44269502f) + 1.92596299e-8f) / tt : 0.f;   // 0 inf is NaN
+    w.half = 0.5f * most;
+    w.ch = 2.88539004f / tt;
+    w.cl = w.ch > 0.f ? (fmaf(-w.ch, tt, 2.88539004f) + 3.85192598e-8f) / tt : 0.f;   // 0 inf is NaN
     w.shift = p.shift;
     Cut cut = {0, V, 1};
     if (min_p > 0.f) {   // a bound on the weights, rounded up
@@ -447,7 +449,7 @@ __global__ void __launch_bounds__(kThreads) token_sample_kernel(const __grid_con
     auto kept = [&](int i, float x) -> uint64_t { return cut.keeps(key_of(x), i) ? cut.of(w(x)) : 0; };
     uint64_t total = 0;
     bool summed = false;
-    const float inv = (float)kBins / 43.5f / tt;   // weights end at 2^-62.5 = e^-43.3
+    const float inv = (float)kBins / 43.5f / tt * 2.f;   // of half distances; weights end at 2^-62.5 = e^-43.3
     if (top_k > 0 && top_k < V)
       cut = find_cut<false>(all, row, begin, end, V, w, inv, cut, (uint64_t)top_k, nullptr);
     if (by_sum) {
@@ -492,7 +494,7 @@ __global__ void __launch_bounds__(kThreads) token_sample_kernel(const __grid_con
         if (mine && clear) {
           p.ids[r] = i;
           if (p.logprob) {
-            const float z = x == w.most ? 0.f : (x - w.most) / tt;
+            const float d = fmaf(x, -0.5f, w.half), z = d > 0.f ? -2.f * (d / tt) : 0.f;
             // the sum is at least the largest weight: its logarithm by that of its 24 leading bits
             p.logprob[r] = z - logf((float)total * __uint_as_float((uint32_t)(127 - w.shift) << 23));
           }
@@ -505,9 +507,9 @@ __global__ void __launch_bounds__(kThreads) token_sample_kernel(const __grid_con
     if (!summed && cut.key == 0 && cut.last == V && cut.least == 1 && w.ch > 0.f) {   // (not at an infinite temperature)
       float f0 = 0.f, f1 = 0.f;
       for_tokens<4>(row, from, to, lane, 32, [&](int i, float x) {
-        const float e = exp2f_fast((x - w.most) * w.ch);
-        if (i & 1) f1 += x == w.most ? 1.f : e;
-        else f0 += x == w.most ? 1.f : e;
+        const float d = fmaf(x, 0.5f, -w.half), e = exp2f_fast(d * w.ch);
+        if (i & 1) f1 += d < 0.f ? e : 1.f;
+        else f0 += d < 0.f ? e : 1.f;
       });
       const float one = __uint_as_float((uint32_t)(127 + w.shift) << 23);
       s = __float2ull_rn((f0 + f1) * one);
