@@ -672,27 +672,32 @@ bool tc_shape(const gated_delta_rule_shape* s) {
   return s->io_dtype == SSD_BF16 && s->key_dim % 8 == 0 && s->key_dim <= 128 && s->value_dim % 8 == 0;
 }
 int key_blocks(int64_t K) { return (int)((K + 63) / 64); }
+// A call takes the tensor cores or the walk on the CUDA cores: what only one of them uses lies in the same place.
 Layout layout(const gated_delta_rule_shape* s, bool back) {
   Layout L = {};
   size_t at = sizeof(WsHeader);
   const size_t nch = (size_t)((s->seqlen + kChunk - 1) / kChunk);
-  L.chunks = at;
-  if (tc_shape(s)) at = align_up(at + tc_bytes(s->batch, (int64_t)nch, s->heads, s->value_dim, s->key_dim, back), kWsAlign);
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at = align_up(at + bytes, kWsAlign);
+    return here;
+  };
   if (back) {
-    const size_t steps = (size_t)(s->batch * s->seqlen * s->heads * s->value_dim) * 4;
     const size_t states = (size_t)s->batch * nch * (size_t)(s->heads * s->value_dim * s->key_dim) * 4;
-    auto take = [&](size_t bytes) {
-      const size_t here = at;
-      at = align_up(at + bytes, kWsAlign);
-      return here;
-    };
-    L.err = take(steps);
-    L.du = take(steps);
     L.states = take(states);
     L.dstates = take(states);
-    L.partial = take((size_t)key_blocks(s->key_dim) * (size_t)s->batch * nch * (size_t)s->heads * kChunk * 4);
   }
+  const size_t shared = at;
+  if (tc_shape(s)) L.chunks = take(tc_bytes(s->batch, (int64_t)nch, s->heads, s->value_dim, s->key_dim, back));
   L.total = at;
+  if (back) {
+    at = shared;
+    const size_t steps = (size_t)(s->batch * s->seqlen * s->heads * s->value_dim) * 4;
+    L.err = take(steps);
+    L.du = take(steps);
+    L.partial = take((size_t)key_blocks(s->key_dim) * (size_t)s->batch * nch * (size_t)s->heads * kChunk * 4);
+    L.total = std::max(L.total, at);
+  }
   return L;
 }
 
