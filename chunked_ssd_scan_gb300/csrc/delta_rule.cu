@@ -59,12 +59,18 @@ struct Walk {
       for (int e = 0; e < KE; ++e)
         s[r][e] = base && v0 + row[r] < V && key_of(e, l) < K ? base[(v0 + row[r]) * K + key_of(e, l)] : 0.f;
   }
-  __device__ __forceinline__ void store(float* base, int64_t v0, int64_t V, int64_t K) const {
+  // Over the state `cell` of `cells` in `base`.
+  __device__ __forceinline__ void store(const Params& p, float* base, int64_t cell, int64_t cells, int site, int64_t v0) const {
+    float* to = base + cell * p.K * p.V;
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int e = 0; e < KE; ++e)
-        if (v0 + row[r] < V && key_of(e, l) < K) base[(v0 + row[r]) * K + key_of(e, l)] = s[r][e];
+      for (int e = 0; e < KE; ++e) {
+        const int64_t at = (v0 + row[r]) * p.K + key_of(e, l);
+        if (v0 + row[r] < p.V && key_of(e, l) < p.K &&
+            SSD_INDEX_OK(p.hdr, cell * p.K * p.V + at, cells * p.K * p.V, site))
+          to[at] = s[r][e];
+      }
   }
 };
 
@@ -158,7 +164,7 @@ __global__ void __launch_bounds__(kThreads) delta_walk_kernel(const __grid_const
     __syncthreads();
     if (t + kTile < end) next.fetch(p, vbase, p.vs[1], b, h, v0, t + kTile, end);
     if (p.states_out && t % kChunk == 0)
-      w.store(p.states_out + ((b * p.nch + t / kChunk) * p.H + h) * KV, v0, p.V, p.K);
+      w.store(p, p.states_out, (b * p.nch + t / kChunk) * p.H + h, p.batch * p.nch * p.H, 2004, v0);
     const int n = (int)min((int64_t)kTile, end - t);
     // The outputs' sums over a row's lanes wait until all steps of the tile are through: on the way from one step to the
     // next lies only the product with k.  (With them in between a step took 660 cycles.)
@@ -218,12 +224,13 @@ __global__ void __launch_bounds__(kThreads) delta_walk_kernel(const __grid_const
       const int at = m * kThreads + threadIdx.x, i = at / kRows, c = at % kRows;
       if (i < n && v0 + c < p.V) {
         const int64_t to = ((b * p.T + t + i) * p.H + h) * p.V + v0 + c;
-        if (p.y && SSD_INDEX_OK(p.hdr, to, p.batch * p.T * p.H * p.V, 2001)) st_from_f32(static_cast<T*>(p.y) + to, sm.out[i][c]);
+        if (!SSD_INDEX_OK(p.hdr, to, p.batch * p.T * p.H * p.V, 2001)) continue;
+        if (p.y) st_from_f32(static_cast<T*>(p.y) + to, sm.out[i][c]);
         if (p.err) p.err[to] = sm.err[i][c];
       }
     }
   }
-  if (p.final_state) w.store(p.final_state + (b * p.H + h) * KV, v0, p.V, p.K);
+  if (p.final_state) w.store(p, p.final_state, b * p.H + h, p.batch * p.H, 2005, v0);
 }
 
 // Backward: G along time, last step first.
@@ -285,13 +292,14 @@ __global__ void __launch_bounds__(kThreads) delta_walk_back_kernel(const __grid_
       const int at = m * kThreads + threadIdx.x, i = at / kRows, c = at % kRows;
       if (i < n && v0 + c < p.V) {
         const int64_t to = ((b * p.T + t + i) * p.H + h) * p.V + v0 + c;
+        if (!SSD_INDEX_OK(p.hdr, to, p.batch * p.T * p.H * p.V, 2002)) continue;
         p.du[to] = sm.err[i][c];
-        if (SSD_INDEX_OK(p.hdr, to, p.batch * p.T * p.H * p.V, 2002)) st_from_f32(static_cast<T*>(p.dv) + to, sm.out[i][c]);
+        st_from_f32(static_cast<T*>(p.dv) + to, sm.out[i][c]);
       }
     }
-    if (t % kChunk == 0) w.store(p.dstates + ((b * p.nch + t / kChunk) * p.H + h) * KV, v0, p.V, p.K);
+    if (t % kChunk == 0) w.store(p, p.dstates, (b * p.nch + t / kChunk) * p.H + h, p.batch * p.nch * p.H, 2006, v0);
   }
-  if (p.dinit) w.store(p.dinit + (b * p.H + h) * KV, v0, p.V, p.K);
+  if (p.dinit) w.store(p, p.dinit, b * p.H + h, p.batch * p.H, 2007, v0);
 }
 
 // dq, dk and the part of dg of one chunk and key head, 64 of its keys a block: five products over V in slabs of 16
@@ -500,9 +508,9 @@ __global__ void __launch_bounds__(kGradThreads) delta_chunk_grad_kernel(const __
       float all = 0.f;
 #pragma unroll
       for (int w = 0; w < kGradThreads / 32; ++w) all += sm.sum[w];
-      if (part == 0)
-        p.partial[(((int64_t)blockIdx.y * p.batch * p.nch + b * p.nch + chunk) * p.H + h) * kChunk + row] =
-            fmaf(all, sm.c.from[kChunk - 1], sum);
+      const int64_t to = (((int64_t)blockIdx.y * p.batch * p.nch + b * p.nch + chunk) * p.H + h) * kChunk + row;
+      if (part == 0 && SSD_INDEX_OK(p.hdr, to, gridDim.y * p.batch * p.nch * p.H * kChunk, 2008))
+        p.partial[to] = fmaf(all, sm.c.from[kChunk - 1], sum);
     }
   }
 #pragma unroll
@@ -534,14 +542,16 @@ __global__ void __launch_bounds__(256) delta_gate_grad_kernel(const __grid_const
     for (int64_t c = lane; c < p.V; c += 32) de = fmaf(p.du[at + c], p.err[at + c], de);
 #pragma unroll
     for (int o = 16; o; o >>= 1) de += __shfl_xor_sync(0xffffffffu, de, o);
-    if (lane == 0) p.dbeta[(b * p.T + t0 + i) * p.H + h] = de;
+    const int64_t to = (b * p.T + t0 + i) * p.H + h;
+    if (lane == 0 && SSD_INDEX_OK(p.hdr, to, p.batch * p.T * p.H, 2009)) p.dbeta[to] = de;
   }
   if (p.dg && threadIdx.x < n) {
     const int64_t per = p.batch * p.nch * p.H * kChunk;
     const float* part = p.partial + blockIdx.x * (int64_t)kChunk + threadIdx.x;
     float sum = 0.f;
     for (int kb = 0; kb < key_blocks; ++kb) sum += part[kb * per];
-    p.dg[(b * p.T + t0 + threadIdx.x) * p.H + h] = sum;
+    const int64_t to = (b * p.T + t0 + threadIdx.x) * p.H + h;
+    if (SSD_INDEX_OK(p.hdr, to, p.batch * p.T * p.H, 2010)) p.dg[to] = sum;
   }
 }
 

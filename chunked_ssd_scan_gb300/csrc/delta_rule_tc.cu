@@ -221,6 +221,7 @@ __global__ void __launch_bounds__(kPrepThreads, 6) delta_chunk_kernel(const __gr
   const uint32_t mine = tmem + ((uint32_t)(warp * 32) << 16);
   for (int64_t h = hk * group; done && h < (hk + 1) * group; ++h) {
     const int64_t cell = (b * p.nch + chunk) * p.H + h;
+    if (!SSD_INDEX_OK(p.hdr, cell, p.batch * p.nch * p.H, 2011)) break;
     uint8_t* out = buf.squares + cell * buf.square;
     __syncthreads();
     if (h > hk * group) {
@@ -583,7 +584,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       const bool wide = (reinterpret_cast<uintptr_t>(end) & 31) == 0;
 #pragma unroll
       for (int k = 0; k < KQ; k += 8)
-        if (k0 + k < p.K) store8(end + at + k, S + k, wide);
+        if (k0 + k < p.K &&
+            SSD_INDEX_OK(p.hdr, at + k + 7, identity ? p.K * p.K : KV, 2012) &&
+            SSD_INDEX_OK(p.hdr, seg.pre ? seg_at : seq, p.batch * p.H * (seg.pre ? seg.n : 1), 2013))
+          store8(end + at + k, S + k, wide);
     }
   } else if constexpr (kY) {   // y: a thread has a value
     const int v = (warp & 3) * 32 + lane;
@@ -680,7 +684,9 @@ __global__ void __launch_bounds__(kCarryThreads) delta_carry_kernel(const __grid
   for (int i = 1; i < seg.n; ++i) {
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      if (in && v0 + part * 4 + r < p.V) *const_cast<float*>(own(seg.start, i, r)) = s[r];
+      if (in && v0 + part * 4 + r < p.V &&
+          SSD_INDEX_OK(p.hdr, own(seg.start, i, r) - seg.start, p.batch * p.H * seg.n * KV, 2014))
+        *const_cast<float*>(own(seg.start, i, r)) = s[r];
     if (i + 1 == seg.n) break;
     *reinterpret_cast<float4*>(&sm.row[k][part * 4]) = make_float4(s[0], s[1], s[2], s[3]);
 #pragma unroll

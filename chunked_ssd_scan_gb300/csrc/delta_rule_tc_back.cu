@@ -279,7 +279,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       const bool wide = (reinterpret_cast<uintptr_t>(p.dinit) & 31) == 0;
 #pragma unroll
       for (int k = 0; k < KQ; k += 8)
-        if (k0 + k < p.K) store8(p.dinit + at + k, G + k, wide);
+        if (k0 + k < p.K && SSD_INDEX_OK(p.hdr, at + k + 7, p.batch * p.H * p.V * p.K, 2015))
+          store8(p.dinit + at + k, G + k, wide);
     }
   } else {   // scale D dY in two terms, and dR on its way out
     const int t = threadIdx.x - kStateWarps * 32, v = (warp & 3) * 32 + lane;
@@ -328,9 +329,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       named_barrier(1, 128);
       if (warp == kStateWarps && lane == 0) {
         const int64_t cell = ((int64_t)b * nch + c) * p.H + h;
-        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(buf.writes + cell * 4 * kTileBytes),
-                     "r"(smem_u32(sm.r)), "r"(4 * kTileBytes)
-                     : "memory");
+        if (SSD_INDEX_OK(p.hdr, cell, p.batch * p.nch * p.H, 2016))
+          asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(buf.writes + cell * 4 * kTileBytes),
+                       "r"(smem_u32(sm.r)), "r"(4 * kTileBytes)
+                       : "memory");
         bulk_commit_group();
       }
     }
@@ -606,9 +608,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         pair(hi.y, lo.y, v.y, out[1]);
         pair(hi.z, lo.z, v.z, out[2]);
         pair(hi.w, lo.w, v.w, out[3]);
-        if (i < n && col < p.V)
-          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dv) + ((b * p.T + t0 + i) * p.H + h) * p.V + col) =
-              make_uint4(out[0], out[1], out[2], out[3]);
+        const int64_t to = ((b * p.T + t0 + i) * p.H + h) * p.V + col;
+        if (i < n && col < p.V && SSD_INDEX_OK(p.hdr, to + 7, p.batch * p.T * p.H * p.V, 2017))
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dv) + to) = make_uint4(out[0], out[1], out[2], out[3]);
       }
       dot += __shfl_xor_sync(0xffffffffu, dot, 1);
       dot += __shfl_xor_sync(0xffffffffu, dot, 2);
@@ -887,8 +889,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       for (int e = 0; e < 2; ++e) {
         const int i = 2 * lane + e;
         g[e] += all + after + rho[1] + (e ? 0.f : rho[0]) + before + (e ? sigma[0] : 0.f);
-        if (i < n) {
-          const int64_t at = (b * p.T + t0 + i) * p.H + h;
+        const int64_t at = (b * p.T + t0 + i) * p.H + h;
+        if (i < n && SSD_INDEX_OK(p.hdr, at, p.batch * p.T * p.H, 2018)) {
           p.dbeta[at] = sm.dot[i] - z[e];
           if (p.dg) p.dg[at] = g[e];
         }

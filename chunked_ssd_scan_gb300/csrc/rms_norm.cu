@@ -30,8 +30,10 @@ struct NormParams {
   void *y, *h;                  // backward: y is dx
   float *rstd, *scale, *partial, *dw;
   int64_t N, C, xs, rs, ds, blocks;   // blocks of channels with a scale of their own
+  int64_t part_rows;            // backward: rows that the workspace has for partial sums of dw
   float eps;
   int tpr;                      // threads a row
+  WsHeader* hdr;                // backward
 };
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -320,7 +322,8 @@ __global__ void __launch_bounds__(N_ == 1 ? 1024 : kRowThreads) rms_backward_ker
       for (int k = 0; k < K::P; ++k)
         dx[k] = make_float2(fmaf(rs, fmaf(-xh[n][k].x, mean, q[n][k].x), rr[n][k].x),
                             fmaf(rs, fmaf(-xh[n][k].y, mean, q[n][k].y), rr[n][k].y));
-      if (row < p.N && c < nvec) K::store(static_cast<T*>(p.y) + row * p.C + c * V, dx);
+      if (row < p.N && c < nvec && SSD_INDEX_OK(p.hdr, row * p.C + c * V + V - 1, p.N * p.C, 2101))
+        K::store(static_cast<T*>(p.y) + row * p.C + c * V, dx);
     }
   }
   if (!p.partial) return;
@@ -328,7 +331,7 @@ __global__ void __launch_bounds__(N_ == 1 ? 1024 : kRowThreads) rms_backward_ker
 #pragma unroll
   for (int n = 0; n < N_; ++n) {
     const int64_t c = (int64_t)n * tpr + t;
-    if (c >= nvec) continue;
+    if (c >= nvec || !SSD_INDEX_OK(p.hdr, part - p.partial + c * V + V - 1, p.part_rows * p.C, 2102)) continue;
 #pragma unroll
     for (int k = 0; k < K::P; ++k) {
       part[c * V + 2 * k] = dw[n][k].x;
@@ -352,7 +355,7 @@ __global__ void __launch_bounds__(kWideThreads) rms_backward_wide_kernel(const _
     const float mean = block_sum(s, sm) / (float)p.C;
     for (int64_t c = tid; c < p.C; c += kWideThreads) {
       const float xh = ld_f32(x + c) * rstd, q = ld_f32(dy + c) * weight(c);
-      st_from_f32(static_cast<T*>(p.y) + row * p.C + c, fmaf(rstd, fmaf(-xh, mean, q), res ? ld_f32(res + c) : 0.f));
+      if (SSD_INDEX_OK(p.hdr, row * p.C + c, p.N * p.C, 2103)) st_from_f32(static_cast<T*>(p.y) + row * p.C + c, fmaf(rstd, fmaf(-xh, mean, q), res ? ld_f32(res + c) : 0.f));
     }
   }
 }
@@ -367,11 +370,12 @@ __global__ void __launch_bounds__(128) rms_weight_grad_kernel(const __grid_const
   for (int64_t row = blockIdx.y * per; row < end; ++row)
     s = fmaf(ld_f32(static_cast<const T*>(p.dy) + row * p.ds + c),
              ld_f32(static_cast<const T*>(p.x) + row * p.xs + c) * __ldg(p.rstd_in + row), s);
-  p.partial[blockIdx.y * p.C + c] = s;
+  if (SSD_INDEX_OK(p.hdr, blockIdx.y * p.C + c, p.part_rows * p.C, 2104)) p.partial[blockIdx.y * p.C + c] = s;
 }
 
 // dw from the partial rows, in a fixed order: 32 channels a block, 32 threads a channel.
-__global__ void __launch_bounds__(1024) rms_join_kernel(const float* partial, float* dw, int64_t rows, int64_t C) {
+__global__ void __launch_bounds__(1024) rms_join_kernel(const float* partial, float* dw, int64_t rows, int64_t C,
+                                                        WsHeader* hdr) {
   __shared__ float sm[32][33];
   follow();
   const int64_t c = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
@@ -383,7 +387,7 @@ __global__ void __launch_bounds__(1024) rms_join_kernel(const float* partial, fl
   __syncthreads();
   s = warp_sum(sm[threadIdx.x & 31][part]);
   const int64_t to = (int64_t)blockIdx.x * 32 + part;
-  if ((threadIdx.x & 31) == 0 && to < C) dw[to] = s;
+  if ((threadIdx.x & 31) == 0 && to < C && SSD_INDEX_OK(hdr, to, C, 2105)) dw[to] = s;
 }
 
 // ------------------------------------------------------------------------------------------------ host
@@ -492,11 +496,12 @@ cudaError_t launch_backward(NormParams p, uint64_t bits, cudaStream_t st) {
   }
   if (e != cudaSuccess || !p.dw) return e;
   return launch_next(rms_join_kernel, dim3((unsigned)((p.C + 31) / 32)), 1024, 0, st, (const float*)p.partial, p.dw,
-                     partials, p.C);
+                     partials, p.C, p.hdr);
 }
 
+int64_t partial_rows(const rms_norm_shape* s) { return std::min(std::max<int64_t>(s->rows, 1) + 7, kMaxPartials); }
 size_t workspace_total(const rms_norm_shape* s) {
-  return sizeof(WsHeader) + align_up((size_t)std::min(std::max<int64_t>(s->rows, 1) + 7, kMaxPartials) * (size_t)s->channels * 4, kWsAlign);
+  return sizeof(WsHeader) + align_up((size_t)partial_rows(s) * (size_t)s->channels * 4, kWsAlign);
 }
 
 }  // namespace
@@ -575,6 +580,8 @@ ssd_status rms_norm_backward(const rms_norm_shape* shape, const void* h, const v
   p.res = dresidual;
   p.y = dx;
   p.dw = dweight;
+  p.hdr = static_cast<WsHeader*>(workspace);
+  p.part_rows = partial_rows(shape);
   p.partial = dweight ? reinterpret_cast<float*>(static_cast<char*>(workspace) + sizeof(WsHeader)) : nullptr;
   p.N = shape->rows;
   p.C = shape->channels;
