@@ -807,7 +807,7 @@ cudaError_t launch_step(const Params& p, cudaStream_t st) {
 }
 
 cudaError_t set_rows(float* dst, const float* src, int64_t n, cudaStream_t st) {
-  if (!dst || n == 0 || dst == src) return cudaSuccess;
+  if (!dst || n == 0) return cudaSuccess;
   return src ? cudaMemcpyAsync(dst, src, sizeof(float) * (size_t)n, cudaMemcpyDeviceToDevice, st)
              : cudaMemsetAsync(dst, 0, sizeof(float) * (size_t)n, st);
 }
