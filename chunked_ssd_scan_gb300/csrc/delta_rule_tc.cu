@@ -11,7 +11,7 @@
 // with an input take two passes, between two computed ones three (lo lo is left out, 2^-18).  One term would leave
 // states and outputs off by 3e-3.  States are kept in fp32 registers and products added to them there: the tensor
 // core's own accumulation truncates, which over a long memory would show.
-// Measured: 8 x 4096 x 16 heads of 128 x 128 with their states, 345 us; the chunk kernel takes 110 us of it, the walk 214
+// Measured: 8 x 4096 x 16 heads of 128 x 128 with their states, 346 us; the chunk kernel takes 112 us of it, the walk 204
 // to 232, 3.4 us a chunk; with 16 sequences alone on the machine a chunk takes 2.3.  The chunk kernel is bound by no unit
 // (8 x 1024: issue slots 44 %, shared memory 49 %, DRAM 33 %) but by barriers and latencies.
 #include <cudaTypedefs.h>

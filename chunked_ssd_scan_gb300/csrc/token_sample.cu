@@ -459,8 +459,9 @@ __global__ void __launch_bounds__(kThreads) token_sample_kernel(const __grid_con
     // the draw: sums of the blocks, of 32 parts of the slice by warp, then the chosen part by the whole block.  Where no
     // order was needed, the sums are first taken of fp32 weights, whose error is known: 2^-22 by the special function; three
     // roundings of an exponent e make 2.1 e 2^-24, and the mean of e over the weights is at most log2 V = 20; 2^-24 for
-    // each of a thread's additions.  Only where the number drawn is as near as that to a border between two tokens, a row
-    // in a hundred or so, exact sums follow.
+    // each of a thread's additions.  Only where the number drawn is as near as that to a border between two tokens, exact
+    // sums follow: of 50000 tokens in one block, with 9e-6 of the sum on either side, in a row of ten where a few dozen tokens
+    // are likely (512 rows f32 in 75 us), but in nine of ten where all are about alike (125 us).
     const int len = ((end - begin + kWarps - 1) / kWarps + 7) / 8 * 8;
     const int from = min(end, begin + warp * len), to = min(end, from + len);
     const float u = __ldg(p.u + r);

@@ -563,7 +563,9 @@ size_t gated_delta_rule_workspace_bytes(const gated_delta_rule_shape* shape, int
  * g below -200 is a decay of zero, as in fp32.  States and sums are fp32.  bf16 inputs with K <= 128, K
  * and V multiples of 8, rows on 16-byte boundaries and not too few steps run on the tensor cores, where
  * what is computed on the way (the state, the writes, the inverse of a chunk's triangular system)
- * enters a product as two bf16 terms, 16 bits of mantissa: states are off by some 4e-6 of their size.
+ * enters a product as two bf16 terms, 16 bits of mantissa: states are off by some 5e-6 of their size (by
+ * 5e-7 elsewhere), and where the keys of a chunk are alike and beta is near one, so that its writes all but
+ * cancel, by up to 64 * 2^-18 = 2.4e-4 of the largest |v| (of |dy| and dfinal, in gradients).
  * There a NaN or an infinity may reach the outputs of the steps before it in its chunk of 64 too, and an
  * infinity becomes NaN.  On the CUDA cores an infinite write leaves its row of the state infinite, as the
  * formula does; an output formed of infinities may be NaN where K is not 64, 128 or 256.
